@@ -424,6 +424,174 @@ int shadowkv_sparse_attention_noalloc_status(skv_stream stream);
 int shadowkv_fetch_probe(const void* src, size_t bytes, int64_t n_chunks, int chunk_bytes, uint64_t seed,
                          int reps, int fresh, skv_stream stream, double* gbs_out);
 
+/*
+ * Paged caches: the dense path beside the sparse one.  The pages have no
+ * counterpart to these four calls; they serve what surrounds a decode step --
+ * the projections' outputs that have to be normed and rotated before
+ * shadowkv_decode_step takes them, layers that attend over their whole cache,
+ * and caches that are held to a budget by giving rows up instead of by
+ * offloading them.
+ *
+ * A paged cache is the caller's memory.  Keys and values live in two pools of
+ * n_pages pages of page_size rows (one row: one token's key or value of one KV
+ * head); sequence b owns the pages table[b][0 .. max_pages), and row i of it is
+ * row i % page_size of page table[b][i / page_size].  Only the pages of its
+ * first lens[b] rows are read.  Strides are in elements and free (page-major,
+ * head-major or token-major pools), the head dimension is contiguous.
+ *   dtype      SKV_BF16, SKV_F32, or SKV_FP8 (bf16 keys, e5m2 values)
+ *   head_dim   64 or 128;  page_size a power of two from 8 to 1024
+ *   strides    multiples of 16 bytes; pools 16-byte aligned device memory of the
+ *              current device
+ * A negative length counts as 0 and one above max_pages * page_size as that;
+ * a page id outside [0, n_pages) is not followed (its rows count as absent).
+ * Both set an error word of the device, which shadowkv_paged_status reads.
+ *
+ * Calls enqueue their work on `stream`, allocate nothing, keep nothing for the
+ * next call, and give the same bits for the same inputs.  They can be captured
+ * into graphs.  Calls that overlap on the GPU need workspaces of their own (so
+ * do two graphs that may replay at once); calls that only read a cache may
+ * overlap on it.
+ */
+typedef struct {
+    int32_t dtype;              /* skv_dtype of the cache, of q, k, v and of the outputs (SKV_FP8: those are bf16) */
+    int32_t n_kv_heads;         /* H */
+    int32_t head_dim;           /* d */
+    int32_t page_size;
+    int32_t batch;              /* sequences; 0: nothing is done */
+    int32_t max_pages;          /* entries per sequence in table, >= 1 */
+    int64_t n_pages;            /* pages of the pools */
+    int64_t k_page, k_head, k_row;   /* strides of the key pool, elements */
+    int64_t v_page, v_head, v_row;   /* strides of the value pool, elements */
+    int64_t table_seq;          /* entries between sequences of table, >= max_pages */
+    void* k;                    /* dev */
+    void* v;                    /* dev */
+    const int32_t* table;       /* dev [batch][max_pages] */
+    const int32_t* lens;        /* dev [batch] (not used by shadowkv_qk_norm_rope) */
+} skv_paged_cache;
+
+/*
+ * Norm, rotation and append of the queries and keys of `tokens` tokens in one
+ * pass.  For every head x of q and k
+ *   y = x / sqrt(mean(x^2) + eps) * w     (w NULL: y = x)
+ *   (y_i, y_{i+rd/2}) -> (y_i cos a - y_{i+rd/2} sin a, y_{i+rd/2} cos a + y_i sin a),
+ *   a = position * rope_base^(-2i/rd),  i < rd/2
+ * in fp32 (the angle's turns in 64-bit fixed point), rounded once.  With
+ * rd = head_dim these are the keys and queries shadowkv_decode_step takes;
+ * dimensions from rd on pass through.
+ *
+ * With cache.k set, k and v also become row index[t] of sequence seq[t] of the
+ * cache (v is rounded to e5m2 for SKV_FP8, saturating), and where given
+ * row_position[b][h][row] = position and row_weight[b][h][row] = 0.  lens is
+ * the caller's to advance.  No two tokens of a call may name the same row, nor
+ * two sequences share the page of a row that is written.
+ *
+ * A token with a negative position is padding: nothing of it is read or
+ * written.  One with a negative seq is not appended.  An index or seq beyond
+ * the cache, or a bad page, sets the error word and skips the append.
+ * q_out may be q and k_out may be k (same strides); other overlaps are not
+ * allowed.  tokens == 0 does nothing.
+ */
+typedef struct {
+    skv_paged_cache cache;      /* dtype, n_kv_heads, head_dim always; the rest with cache.k */
+    int32_t tokens;
+    int32_t n_q_heads;          /* any number >= 0, not tied to n_kv_heads */
+    int32_t rotary_dim;         /* rd: a multiple of 16, 16 .. head_dim; 0: head_dim */
+    float eps;                  /* > 0 where a weight is given */
+    double rope_base;           /* > 1 */
+    int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head;   /* strides, elements */
+    int64_t q_out_tok, q_out_head, k_out_tok, k_out_head;
+    const void* q;              /* dev [tokens][n_q_heads][d] */
+    const void* k;              /* dev [tokens][n_kv_heads][d] */
+    const void* v;              /* dev [tokens][n_kv_heads][d]; with a cache only */
+    const void* q_weight;       /* dev [d], dtype of q, or NULL: q is not normed */
+    const void* k_weight;       /* dev [d], or NULL: k is not normed */
+    void* q_out;                /* dev [tokens][n_q_heads][d] */
+    void* k_out;                /* dev [tokens][n_kv_heads][d], or NULL with a cache */
+    const int32_t* positions;   /* dev [tokens] */
+    const int32_t* seq;         /* dev [tokens]; with a cache */
+    const int32_t* index;       /* dev [tokens]; with a cache */
+    int32_t* row_position;      /* dev [batch][n_kv_heads][row_pitch], or NULL */
+    float* row_weight;          /* dev, the same shape, or NULL */
+    int64_t row_pitch;          /* >= max_pages * page_size */
+} skv_qk_norm_rope_args;
+int shadowkv_qk_norm_rope(const skv_qk_norm_rope_args* args, skv_stream stream);
+
+/*
+ * Attention of one new token per sequence over its whole paged cache:
+ *   out = softmax(scale q.K^T).V,  lse = ln sum exp(scale q.k_j)
+ * for the G = n_q_heads / n_kv_heads query heads of every KV head (q-head j
+ * belongs to KV head j / G; G from 1 to 8).  A sequence of no rows gives out = 0 and
+ * lse = -inf; what lies behind a sequence's last row, in its last page or in
+ * its table, is not read.  The token's own key has to be in the cache (and
+ * counted in lens) if it is to attend to itself.
+ *
+ * With weight_out set, the weight every row received is added to the running
+ * sums that shadowkv_paged_evict goes by:
+ *   weight_out[b][h][j] = weight[b][h][j] + sum over the G heads of p_j
+ * for j < lens[b]; rows behind are left as they are.  weight_out may be weight.
+ *
+ * Accumulation, softmax statistics and sums are fp32.  bf16 and e5m2 values
+ * are multiplied by probabilities rounded to bf16 and fp16.
+ */
+typedef struct {
+    skv_paged_cache cache;
+    int32_t n_q_heads;
+    float scale;                /* 0: 1 / sqrt(head_dim) */
+    int64_t q_seq, q_head, out_seq, out_head;   /* strides, elements */
+    const void* q;              /* dev [batch][n_q_heads][d] */
+    void* out;                  /* dev [batch][n_q_heads][d] */
+    float* lse;                 /* dev [batch][n_q_heads], or NULL */
+    const float* weight;        /* dev [batch][n_kv_heads][row_pitch]; with weight_out */
+    float* weight_out;          /* dev, the same shape, or NULL */
+    int64_t row_pitch;          /* >= max_pages * page_size */
+    void* workspace;            /* dev, 16-byte aligned */
+    int64_t workspace_bytes;    /* >= shadowkv_paged_attention_workspace(args) */
+} skv_paged_attention_args;
+int64_t shadowkv_paged_attention_workspace(const skv_paged_attention_args* args);   /* bytes, or SKV_ERR_*; goes by the sizes alone, no CUDA call */
+int shadowkv_paged_attention(const skv_paged_attention_args* args, skv_stream stream);
+
+/*
+ * Brings every (sequence, KV head) of more than `budget` rows down to budget
+ * rows.  Kept are the rows whose position is above last - recent (last: the
+ * largest position of the sequence's rows of that head) or below sink, and of
+ * the rest those with the largest weight; a lower row before a higher one among equal
+ * weights (a NaN weighs more than any number).  The kept rows with row >= budget then move, key, value, position and
+ * weight, into the rows below budget that were given up: the i-th such row, in
+ * ascending order, into the i-th given-up one.  Rows so lose their order, which attention does
+ * not depend on; row_position records where each belongs.  Afterwards
+ * lens_out[b] = min(lens[b], budget) and the pages behind are free.
+ *
+ * position_out, weight_out and lens_out may be position, weight and lens (in
+ * place) or buffers of their own, which then hold the rows below lens_out[b]
+ * (rows behind are left as they are).  The key and value pools are changed in
+ * place; the rows at budget and behind stay as they were.  A sequence that
+ * gives up rows must not share its pages.  A bad page sets the error word, and
+ * the rows in it are not moved.
+ */
+typedef struct {
+    skv_paged_cache cache;
+    int32_t budget;             /* >= 1 */
+    int32_t recent, sink;       /* >= 0, recent + sink <= budget */
+    const float* weight;        /* dev [batch][n_kv_heads][row_pitch] */
+    const int32_t* position;    /* dev, the same shape */
+    float* weight_out;
+    int32_t* position_out;
+    int64_t row_pitch;          /* >= max_pages * page_size */
+    int32_t* lens_out;          /* dev [batch] */
+    void* workspace;            /* dev, 16-byte aligned */
+    int64_t workspace_bytes;    /* >= shadowkv_paged_evict_workspace(args) */
+} skv_paged_evict_args;
+int64_t shadowkv_paged_evict_workspace(const skv_paged_evict_args* args);   /* bytes, or SKV_ERR_* */
+int shadowkv_paged_evict(const skv_paged_evict_args* args, skv_stream stream);
+
+/*
+ * Status of the paged calls made so far on the current device: synchronises
+ * `stream`, reads the error words and clears them.  Returns SKV_OK,
+ * SKV_ERR_DEVICE_BOUNDS (a length, index or page id was out of range; its
+ * access was skipped), or SKV_ERR_CUDA.  Not for use during stream capture.
+ */
+int shadowkv_paged_status(skv_stream stream);
+
 void shadowkv_destroy(skv_layer* layer);   /* frees everything the handle owns; NULL ok */
 const char* shadowkv_strerror(int code);
 int shadowkv_version(void);                 /* major*10000 + minor*100 + patch */

@@ -18,7 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libshadowkv.so")
 
-SOURCES = ["api.cu", "k_score.cu", "k_select.cu", "k_rebuild.cu", "k_gather.cu", "k_attn.cu"]
+SOURCES = ["api.cu", "k_score.cu", "k_select.cu", "k_rebuild.cu", "k_gather.cu", "k_attn.cu",
+           "paged.cu", "k_norm_rope.cu", "k_paged_attn.cu", "k_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", INCLUDE, "-I", CSRC]

@@ -1,0 +1,89 @@
+// Internal types of the paged-cache calls: kernel parameters and launchers.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "shadowkv.h"
+
+namespace skv {
+
+// A paged cache as the kernels see it (strides in elements).
+struct PagedView {
+    void* k; void* v;
+    int64_t k_page, k_head, k_row, v_page, v_head, v_row;
+    const int32_t* table; int64_t table_seq;
+    const int32_t* lens;
+    int64_t n_pages;
+    int batch, H;
+    int lg;        // log2(page_size)
+    int cap;       // max_pages * page_size: rows a sequence can have
+};
+
+struct NormRopeParams {
+    PagedView c;
+    int tokens, nq, rd;
+    int per_cta;              // tokens per CTA
+    float eps;
+    int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head, qo_tok, qo_head, ko_tok, ko_head;
+    const void *q, *k, *v, *qw, *kw;
+    void *qo, *ko;
+    const int32_t *positions, *seq, *index;
+    int32_t* row_position; float* row_weight; int64_t row_pitch;
+    uint64_t turn[64];        // rope_base^(-2i/rd) / (2 pi) in units of 2^-64 turns
+};
+int launch_norm_rope(int dtype, int d, const NormRopeParams& p, cudaStream_t s);
+
+struct PagedAttnParams {
+    PagedView c;
+    int G, n_q;
+    float scale_log2;         // scale * log2(e)
+    int64_t q_seq, q_head, o_seq, o_head;
+    const void* q; void* out; float* lse;
+    float* rec;               // [ncta][2][G][d + 2]: a CTA's shares of its first and last unit
+    // weights: raw products q.k of every row [U][cap][Gp], and (base, 1 / sum) per head [U][G]
+    float* z; float2* stat; int Gp;
+    const float* weight; float* weight_out; int64_t row_pitch;
+};
+int paged_attn_ctas(int dtype, int nsm);     // CTAs that fill nsm SMs
+int launch_paged_attn(int dtype, int d, const PagedAttnParams& p, int ncta, cudaStream_t s);
+
+struct EvictParams {
+    PagedView c;
+    int d, es, es_v;
+    int budget, recent, sink;
+    const float* weight; const int32_t* position;
+    float* weight_out; int32_t* position_out; int64_t row_pitch;
+    int32_t* lens_out;
+    int32_t* to; int32_t* of; int list_cap;   // [U][list_cap] rows given up / rows that move there
+    int32_t* count; int32_t* new_len;         // [U], [batch]
+};
+int launch_evict(const EvictParams& p, int nsm, cudaStream_t s);
+
+// The error words of the three kernel files on the current device.
+cudaError_t norm_rope_err(int** p);
+cudaError_t paged_attn_err(int** p);
+cudaError_t evict_err(int** p);
+
+#ifdef __CUDACC__
+// rows of sequence b, brought into [0, cap]
+__device__ __forceinline__ int rows_of(const PagedView& c, int b, int* err, int where) {
+    int n = __ldg(c.lens + b);
+    if (n < 0 || n > c.cap) {
+        set_err(err, DEV_ERR_BOUNDS, where);
+        n = n < 0 ? 0 : c.cap;
+    }
+    return n;
+}
+// page of row i of sequence b, or -1 (and the error word) if its id is out of range
+__device__ __forceinline__ int page_of(const PagedView& c, int b, int i, int* err, int where) {
+    const int id = __ldg(c.table + b * c.table_seq + (i >> c.lg));
+    if (id < 0 || id >= c.n_pages) {
+        set_err(err, DEV_ERR_BOUNDS, where);
+        return -1;
+    }
+    return id;
+}
+#endif
+
+}  // namespace skv
