@@ -231,79 +231,123 @@ def _stream(s) -> int | None:
 
 
 # ---------------------------------------------------------------- paged caches
+#
+# A decode step makes these calls once per layer, so their host time counts.  What a call's tensors
+# look like -- shapes, strides, types, never addresses -- decides all of its checks and most of its
+# argument struct; both are worked out once per form and kept, and a call fills in the pointers.
 
 def _refuse(where: str, why: str):
     raise ShadowKVError(-1, f"{where}: {why}")
 
 
-def _cache_type(where: str, k, v) -> int:
-    kd, vd = str(k.dtype), str(v.dtype)
-    if kd == vd == "torch.bfloat16":
-        return SKV_BF16
-    if kd == vd == "torch.float32":
-        return SKV_F32
-    if kd == "torch.bfloat16" and vd == "torch.float8_e5m2":
-        return SKV_FP8
-    _refuse(where, f"no cache of {kd} keys and {vd} values")
+def _form(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype)
 
 
 def _pool_fields(where: str, k, v, table, lens, batch: int):
-    """The fields of skv_paged_cache from the tensors: pools [n_pages][H][page_size][d] with any
-    strides over a contiguous head dimension, table int32 [batch][max_pages], lens int32 [batch]."""
-    code = _cache_type(where, k, v)
-    if k.dim() != 4 or k.shape != v.shape or k.stride(3) != 1 or v.stride(3) != 1:
+    """The fields of skv_paged_cache before its pointers, from the forms of the tensors: pools
+    [n_pages][H][page_size][d] with any strides over a contiguous head dimension, table int32
+    [batch][max_pages], lens int32 [batch]."""
+    kd, vd = str(k[2]), str(v[2])
+    code = {("torch.bfloat16", "torch.bfloat16"): SKV_BF16, ("torch.float32", "torch.float32"): SKV_F32,
+            ("torch.bfloat16", "torch.float8_e5m2"): SKV_FP8}.get((kd, vd))
+    if code is None:
+        _refuse(where, f"no cache of {kd} keys and {vd} values")
+    if len(k[0]) != 4 or k[0] != v[0] or k[1][3] != 1 or v[1][3] != 1:
         _refuse(where, "the pools are [n_pages][n_kv_heads][page_size][head_dim], alike, head_dim contiguous")
-    if table.dim() != 2 or table.shape[0] != batch or table.stride(1) != 1 or str(table.dtype) != "torch.int32":
+    if len(table[0]) != 2 or table[0][0] != batch or table[1][1] != 1 or str(table[2]) != "torch.int32":
         _refuse(where, "table is int32 [batch][max_pages]")
-    if lens is not None and (lens.dim() != 1 or lens.shape[0] != batch or not lens.is_contiguous()
-                             or str(lens.dtype) != "torch.int32"):
-        _refuse(where, "lens is int32 [batch]")
-    pages, heads, size, d = k.shape
-    ks, vs = k.stride(), v.stride()
-    return (code, heads, d, size, batch, table.shape[1], pages, ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
-            max(table.stride(0), table.shape[1]), k.data_ptr(), v.data_ptr(), table.data_ptr(),
-            0 if lens is None else lens.data_ptr())
+    if lens is not None:
+        _vector(where, "lens", lens, batch)
+    pages, heads, size, d = k[0]
+    return (code, heads, d, size, batch, table[0][1], pages, *k[1][:3], *v[1][:3], max(table[1][0], table[0][1]))
 
 
 def _rows(where: str, name: str, t, dtype: str, batch: int, heads: int, need: int) -> int:
     """Row pitch of a per-row array [batch][n_kv_heads][>= need]."""
-    if (t.dim() != 3 or t.shape[0] != batch or t.shape[1] != heads or t.shape[2] < need or not t.is_contiguous()
-            or str(t.dtype) != dtype):
+    if (len(t[0]) != 3 or t[0][:2] != (batch, heads) or t[0][2] < need or str(t[2]) != dtype
+            or t[1] != (heads * t[0][2], t[0][2], 1)):
         _refuse(where, f"{name} is {dtype} [batch][n_kv_heads][max_pages * page_size or more], contiguous")
-    return t.shape[2]
+    return t[0][2]
 
 
 def _heads(where: str, name: str, t, dtype, shape):
     """Strides over (token or sequence, head) of a [..][heads][d] tensor, head dimension contiguous."""
-    if t.dim() != 3 or t.shape[1:] != shape[1:] or t.shape[0] != shape[0] or t.stride(2) != 1 or t.dtype != dtype:
+    if t is None or t[0] != shape or t[1][2] != 1 or t[2] != dtype:
         _refuse(where, f"{name} is {dtype} {list(shape)}, head_dim contiguous")
-    st = t.stride()
-    return st[0], st[1]
+    return t[1][:2]
 
 
-def _same_rows(where: str, name: str, t, n: int):
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or str(t.dtype) != "torch.int32":
-        _refuse(where, f"{name} is int32 [{n}], contiguous")
-    return t.data_ptr()
+def _vector(where: str, name: str, t, n: int, dtype: str = "torch.int32"):
+    if t is None or t[0] != (n,) or (n > 1 and t[1] != (1,)) or str(t[2]) != dtype:
+        _refuse(where, f"{name} is {dtype} [{n}], contiguous")
 
 
-@functools.lru_cache(maxsize=256)
-def _space_bytes(name: str, packed: bytes, device: int) -> int:
-    n = getattr(load(), name)(packed)
-    if n < 0:
-        _check(int(n), name)
-    return n
+def _current_stream(device) -> int:
+    import torch
+    try:
+        return torch._C._cuda_getCurrentRawStream(device.index or 0)
+    except AttributeError:   # a build without the short way
+        return torch.cuda.current_stream().cuda_stream
 
 
-def _space(nbytes: int, like, stream):
+def _space(nbytes: int, device, stream):
     """Workspace of one call, from torch's allocator on the call's own stream: calls on several
     streams, or captured into several graphs, each have their own."""
     import torch
-    if stream is None or not like.is_cuda:
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), like.device)
+    if stream is None or device.type != "cuda":
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device)
     with torch.cuda.stream(s):
-        return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _launch(name: str, packed: bytes, device, stream):
+    if stream is None:
+        stream = _current_stream(device) if device.type == "cuda" else 0
+    else:
+        stream = _stream(stream)
+    _check(getattr(load(), name)(packed, stream), name)
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_rope_plan(q, k, positions, q_out, k_out, q_weight, k_weight, v, k_cache, v_cache, table, seq, index, position,
+                    weight, rotary_dim, eps, rope_base):
+    w = "qk_norm_rope"
+    if len(q[0]) != 3 or len(k[0]) != 3 or str(q[2]) not in ("torch.bfloat16", "torch.float32"):
+        _refuse(w, "q is bf16 or fp32 [tokens][n_q_heads][d], k [tokens][n_kv_heads][d]")
+    (n, nq, d), nk, dt = q[0], k[0][1], q[2]
+    qs, ks = _heads(w, "q", q, dt, (n, nq, d)), _heads(w, "k", k, dt, (n, nk, d))
+    qo = _heads(w, "q_out", q_out, dt, (n, nq, d))
+    ko = _heads(w, "k_out", k_out, dt, (n, nk, d)) if k_out is not None else (0, 0)
+    for name, x in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if x is not None:
+            _vector(w, name, x, d, str(dt))
+    _vector(w, "positions", positions, n)
+    vs, pitch = (0, 0), 0
+    if k_cache is not None:
+        if v is None or v_cache is None or table is None:
+            _refuse(w, "an append takes v, k_cache, v_cache, table, seq and index")
+        if len(k_cache[0]) != 4 or k_cache[2] != dt or k_cache[0][1] != nk or k_cache[0][3] != d:
+            _refuse(w, f"k_cache is {dt} [n_pages][{nk}][page_size][{d}]")
+        batch = table[0][0]
+        cache = _pool_fields(w, k_cache, v_cache, table, None, batch)
+        vs = _heads(w, "v", v, dt, (n, nk, d))
+        _vector(w, "seq", seq, n)
+        _vector(w, "index", index, n)
+        need = table[0][1] * k_cache[0][2]
+        if position is not None:
+            pitch = _rows(w, "position", position, "torch.int32", batch, nk, need)
+        if weight is not None:
+            wp = _rows(w, "weight", weight, "torch.float32", batch, nk, need)
+            if position is not None and wp != pitch:
+                _refuse(w, "position and weight have rows of different lengths")
+            pitch = wp
+    else:
+        if any(x is not None for x in (position, weight, v_cache, table, seq, index)):
+            _refuse(w, "v_cache, table, seq, index, position and weight go with k_cache")
+        cache = (SKV_F32 if str(dt) == "torch.float32" else SKV_BF16, nk, d) + (0,) * 11
+    return cache, (n, nq, rotary_dim, eps, rope_base, *qs, *ks, *vs, *qo, *ko), pitch
 
 
 def qk_norm_rope(q, k, positions, q_out, k_out=None, *, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -313,48 +357,49 @@ def qk_norm_rope(q, k, positions, q_out, k_out=None, *, q_weight=None, k_weight=
     k [T][H][d] at int32 positions [T] into q_out and k_out; with k_cache, v_cache and table also
     the append of k and v as row index[t] of sequence seq[t], with row_position and row_weight in
     position and weight [batch][H][rows] where given.  Returns (q_out, k_out)."""
-    w = "qk_norm_rope"
-    if q.dim() != 3 or k.dim() != 3 or str(q.dtype) not in ("torch.bfloat16", "torch.float32"):
-        _refuse(w, "q is bf16 or fp32 [tokens][n_q_heads][d], k [tokens][n_kv_heads][d]")
-    (n, nq, d), nk = q.shape, k.shape[1]
-    dt = q.dtype
-    qs, ks = _heads(w, "q", q, dt, (n, nq, d)), _heads(w, "k", k, dt, (n, nk, d))
-    qo = _heads(w, "q_out", q_out, dt, (n, nq, d))
-    ko = _heads(w, "k_out", k_out, dt, (n, nk, d)) if k_out is not None else (0, 0)
-    for name, x in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if x is not None and (x.shape != (d,) or x.stride(0) != 1 or x.dtype != dt):
-            _refuse(w, f"{name} is {dt} [{d}]")
-    pos = _same_rows(w, "positions", positions, n)
-    if k_cache is not None:
-        if v is None or v_cache is None or table is None or seq is None or index is None:
-            _refuse(w, "an append takes v, k_cache, v_cache, table, seq and index")
-        if k_cache.dim() != 4 or k_cache.dtype != dt or k_cache.shape[1] != nk or k_cache.shape[3] != d:
-            _refuse(w, f"k_cache is {dt} [n_pages][{nk}][page_size][{d}]")
-        batch = table.shape[0]
-        cache = _pool_fields(w, k_cache, v_cache, table, None, batch)
-        vs = _heads(w, "v", v, dt, (n, nk, d))
-        vp, sp, ip = v.data_ptr(), _same_rows(w, "seq", seq, n), _same_rows(w, "index", index, n)
-        need = table.shape[1] * k_cache.shape[2]
-        pitch = _rows(w, "position", position, "torch.int32", batch, nk, need) if position is not None else 0
-        if weight is not None:
-            wp = _rows(w, "weight", weight, "torch.float32", batch, nk, need)
-            if position is not None and wp != pitch:
-                _refuse(w, "position and weight have rows of different lengths")
-            pitch = wp
+    cache, fixed, pitch = _norm_rope_plan(
+        _form(q), _form(k), _form(positions), _form(q_out), _form(k_out), _form(q_weight), _form(k_weight),
+        _form(v) if k_cache is not None else None, _form(k_cache), _form(v_cache), _form(table), _form(seq), _form(index),
+        _form(position), _form(weight), rotary_dim, eps, rope_base)
+    if k_cache is None:
+        pools, more = (0, 0, 0, 0), (0, 0, 0)
     else:
-        if position is not None or weight is not None:
-            _refuse(w, "position and weight go with a cache")
-        if k_out is None:
-            _refuse(w, "k_out is missing")
-        cache = (SKV_F32 if str(dt) == "torch.float32" else SKV_BF16, nk, d) + (0,) * 15
-        vs, vp, sp, ip, pitch = (0, 0), 0, 0, 0, 0
+        pools = (k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), 0)
+        more = (v.data_ptr(), seq.data_ptr(), index.data_ptr())
     packed = _NORM_ROPE.pack(
-        *cache, n, nq, rotary_dim, eps, rope_base, *qs, *ks, *vs, *qo, *ko, q.data_ptr(), k.data_ptr(), vp,
-        0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr(),
-        q_out.data_ptr(), 0 if k_out is None else k_out.data_ptr(), pos, sp, ip,
-        0 if position is None else position.data_ptr(), 0 if weight is None else weight.data_ptr(), pitch)
-    _check(load().shadowkv_qk_norm_rope(packed, _stream(stream)), "shadowkv_qk_norm_rope")
+        *cache, *pools, *fixed, q.data_ptr(), k.data_ptr(), more[0], _ptr(q_weight) or 0, _ptr(k_weight) or 0,
+        q_out.data_ptr(), _ptr(k_out) or 0, positions.data_ptr(), more[1], more[2], _ptr(position) or 0, _ptr(weight) or 0,
+        pitch)
+    _launch("shadowkv_qk_norm_rope", packed, q.device, stream)
     return q_out, k_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_attention_plan(q, k_cache, v_cache, table, lens, out, lse, weight, weight_out, scale):
+    w = "paged_attention"
+    if len(q[0]) != 3:
+        _refuse(w, "q is [batch][n_q_heads][d]")
+    batch, nq, d = q[0]
+    cache = _pool_fields(w, k_cache, v_cache, table, lens, batch)
+    if q[2] != k_cache[2] or cache[2] != d:
+        _refuse(w, f"q is {k_cache[2]} [batch][n_q_heads][{cache[2]}]")
+    qs, os_ = _heads(w, "q", q, q[2], (batch, nq, d)), _heads(w, "out", out, q[2], (batch, nq, d))
+    if lse is not None and (lse[0] != (batch, nq) or lse[1] != (nq, 1) or str(lse[2]) != "torch.float32"):
+        _refuse(w, "lse is fp32 [batch][n_q_heads], contiguous")
+    pitch = 0
+    if weight is not None:
+        need = cache[5] * cache[3]
+        pitch = _rows(w, "weight", weight, "torch.float32", batch, cache[1], need)
+        if _rows(w, "weight_out", weight_out, "torch.float32", batch, cache[1], need) != pitch:
+            _refuse(w, "weight and weight_out have rows of different lengths")
+    elif weight_out is not None:
+        _refuse(w, "weight_out goes with weight")
+    # the workspace's size goes by these fields alone
+    size = _PAGED_ATTN.pack(*cache[:6], *(0,) * 12, nq, scale, *(0,) * 8, 0 if weight is None else 1, 0, 0, 0)
+    nbytes = load().shadowkv_paged_attention_workspace(size)
+    if nbytes < 0:
+        _check(int(nbytes), "shadowkv_paged_attention_workspace")
+    return cache, (nq, scale, *qs, *os_), pitch, nbytes
 
 
 def paged_attention(q, k_cache, v_cache, table, lens, out, lse=None, weight=None, weight_out=None,
@@ -363,35 +408,38 @@ def paged_attention(q, k_cache, v_cache, table, lens, out, lse=None, weight=None
     rows of the paged cache into out (and its log-sum-exp into lse [batch][n_q], fp32).  With
     weight [batch][H][rows] the weight that each row received is added to it, in place or into
     weight_out.  scale 0: 1/sqrt(d).  Returns out."""
-    w = "paged_attention"
-    if q.dim() != 3:
-        _refuse(w, "q is [batch][n_q_heads][d]")
-    batch, nq, d = q.shape
-    cache = _pool_fields(w, k_cache, v_cache, table, lens, batch)
-    nk = cache[1]
-    if q.dtype != k_cache.dtype or cache[2] != d:
-        _refuse(w, f"q is {k_cache.dtype} [batch][n_q_heads][{cache[2]}]")
-    qs, os_ = _heads(w, "q", q, q.dtype, (batch, nq, d)), _heads(w, "out", out, q.dtype, (batch, nq, d))
-    if lse is not None and (lse.shape != (batch, nq) or not lse.is_contiguous() or str(lse.dtype) != "torch.float32"):
-        _refuse(w, "lse is fp32 [batch][n_q_heads]")
-    pitch = 0
-    if weight is not None:
-        weight_out = weight if weight_out is None else weight_out
-        need = cache[5] * cache[3]
-        pitch = _rows(w, "weight", weight, "torch.float32", batch, nk, need)
-        if _rows(w, "weight_out", weight_out, "torch.float32", batch, nk, need) != pitch:
-            _refuse(w, "weight and weight_out have rows of different lengths")
-    elif weight_out is not None:
-        _refuse(w, "weight_out goes with weight")
-    tail = (0 if lse is None else lse.data_ptr(), 0 if weight is None else weight.data_ptr(),
-            0 if weight is None else weight_out.data_ptr(), pitch)
-    # the workspace's size goes by these fields alone
-    size = _PAGED_ATTN.pack(*cache[:6], *(0,) * 12, nq, scale, 0, 0, 0, 0, 0, 0, 0, 0, 0 if weight is None else 1, 0, 0, 0)
-    nbytes = _space_bytes("shadowkv_paged_attention_workspace", size, q.device.index or 0)
-    space = _space(nbytes, q, stream)
-    packed = _PAGED_ATTN.pack(*cache, nq, scale, *qs, *os_, q.data_ptr(), out.data_ptr(), *tail, space.data_ptr(), nbytes)
-    _check(load().shadowkv_paged_attention(packed, _stream(stream)), "shadowkv_paged_attention")
+    if weight is not None and weight_out is None:
+        weight_out = weight
+    cache, fixed, pitch, nbytes = _paged_attention_plan(
+        _form(q), _form(k_cache), _form(v_cache), _form(table), _form(lens), _form(out), _form(lse), _form(weight),
+        _form(weight_out), scale)
+    device = q.device
+    space = _space(nbytes, device, stream)
+    packed = _PAGED_ATTN.pack(
+        *cache, k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), *fixed, q.data_ptr(),
+        out.data_ptr(), _ptr(lse) or 0, _ptr(weight) or 0, _ptr(weight_out) or 0, pitch, space.data_ptr(), nbytes)
+    _launch("shadowkv_paged_attention", packed, device, stream)
     return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_evict_plan(k_cache, v_cache, table, lens, weight, position, lens_out, weight_out, position_out, budget, recent,
+                      sink):
+    w = "paged_evict"
+    batch = table[0][0] if len(table[0]) == 2 else -1
+    cache = _pool_fields(w, k_cache, v_cache, table, lens, batch)
+    need = cache[5] * cache[3]
+    pitch = _rows(w, "weight", weight, "torch.float32", batch, cache[1], need)
+    for name, t, dt in (("position", position, "torch.int32"), ("weight_out", weight_out, "torch.float32"),
+                        ("position_out", position_out, "torch.int32")):
+        if _rows(w, name, t, dt, batch, cache[1], need) != pitch:
+            _refuse(w, f"weight and {name} have rows of different lengths")
+    _vector(w, "lens_out", lens_out, batch)
+    size = _EVICT.pack(*cache[:6], *(0,) * 12, budget, recent, sink, *(0,) * 8)
+    nbytes = load().shadowkv_paged_evict_workspace(size)
+    if nbytes < 0:
+        _check(int(nbytes), "shadowkv_paged_evict_workspace")
+    return cache, (budget, recent, sink), pitch, nbytes
 
 
 def paged_evict(k_cache, v_cache, table, lens, weight, position, budget: int, recent: int = 0, sink: int = 0,
@@ -399,25 +447,19 @@ def paged_evict(k_cache, v_cache, table, lens, weight, position, budget: int, re
     """shadowkv_paged_evict: brings every (sequence, KV head) down to budget rows by the weights
     [batch][H][rows] and int32 positions of its rows.  weight, position and lens are updated in
     place, or into weight_out, position_out and lens_out.  Returns lens_out."""
-    w = "paged_evict"
-    batch = table.shape[0] if table.dim() == 2 else -1
-    cache = _pool_fields(w, k_cache, v_cache, table, lens, batch)
-    nk, need = cache[1], cache[5] * cache[3]
     lens_out = lens if lens_out is None else lens_out
     weight_out = weight if weight_out is None else weight_out
     position_out = position if position_out is None else position_out
-    pitch = _rows(w, "weight", weight, "torch.float32", batch, nk, need)
-    for name, t, dt in (("position", position, "torch.int32"), ("weight_out", weight_out, "torch.float32"),
-                        ("position_out", position_out, "torch.int32")):
-        if _rows(w, name, t, dt, batch, nk, need) != pitch:
-            _refuse(w, f"weight and {name} have rows of different lengths")
-    lp = _same_rows(w, "lens_out", lens_out, batch)
-    size = _EVICT.pack(*cache[:6], *(0,) * 12, budget, recent, sink, 0, 0, 0, 0, 0, 0, 0, 0)
-    nbytes = _space_bytes("shadowkv_paged_evict_workspace", size, lens.device.index or 0)
-    space = _space(nbytes, weight, stream)
-    packed = _EVICT.pack(*cache, budget, recent, sink, weight.data_ptr(), position.data_ptr(), weight_out.data_ptr(),
-                         position_out.data_ptr(), pitch, lp, space.data_ptr(), nbytes)
-    _check(load().shadowkv_paged_evict(packed, _stream(stream)), "shadowkv_paged_evict")
+    cache, fixed, pitch, nbytes = _paged_evict_plan(
+        _form(k_cache), _form(v_cache), _form(table), _form(lens), _form(weight), _form(position), _form(lens_out),
+        _form(weight_out), _form(position_out), budget, recent, sink)
+    device = weight.device
+    space = _space(nbytes, device, stream)
+    packed = _EVICT.pack(
+        *cache, k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), *fixed, weight.data_ptr(),
+        position.data_ptr(), weight_out.data_ptr(), position_out.data_ptr(), pitch, lens_out.data_ptr(), space.data_ptr(),
+        nbytes)
+    _launch("shadowkv_paged_evict", packed, device, stream)
     return lens_out
 
 

@@ -6,11 +6,13 @@
 // below M, so sources and destinations are disjoint, only the rows that have to move are moved, and
 // a unit that is one row over its budget moves at most one row instead of shifting the rest.
 //
-// k_evict_select finds the M-th largest key by a radix search of 11, 11 and 10 bits (integer
+// k_evict_select finds the M-th largest key by a radix search of 11, 5, 11 and 5 bits (integer
 // counts in shared memory, so the order of the atomics does not show) and writes both lists in
-// ascending row order.  A unit belongs to a cluster of 1 to 8 CTAs, each with a contiguous slice
-// of the rows whose keys stay in its shared memory; counts are joined through distributed shared
-// memory.  k_evict_move, a programmatic dependent, copies the rows.
+// ascending row order.  A unit belongs to a cluster of 1 to 8 CTAs, each with a contiguous slice of
+// the rows, each warp with a contiguous part of the slice; counts are joined through distributed
+// shared memory.  The upper halves of a slice's keys stay in shared memory, so the weights are read
+// once and again only for rows whose upper half equals the threshold's.  k_evict_move, a
+// programmatic dependent, copies the rows.
 #include "skv_common.cuh"
 #include "skv_internal.h"
 #include "skv_paged.h"
@@ -19,10 +21,13 @@ namespace skv {
 
 static __device__ int g_err[2];
 
-constexpr int kEvThreads = 1024;
+constexpr int kEvThreads = 512;
 constexpr int kEvWarps = kEvThreads / 32;
+constexpr int kEvStep = 256;                   // rows of a warp's step, eight per lane
+constexpr int kEvGrain = kEvStep * kEvWarps;   // a slice is a multiple of this many rows
 constexpr int kEvBins = 2048;
-constexpr int kEvKeys = 40960;                 // keys of a slice held in shared memory at most (160 KB)
+constexpr int kEvKeys = 11 * kEvGrain;         // rows of a slice held in shared memory at most (88 KB: two CTAs per SM)
+constexpr int kEvHist = 2 * kEvBins + 64;      // counts of the four passes
 
 // weights in the order of unsigned integers: -0 counts as 0, a NaN lies above +inf
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -36,11 +41,35 @@ __device__ __forceinline__ void sync_all(int ranks) {
     else __syncthreads();
 }
 
-__global__ void __launch_bounds__(kEvThreads, 1) k_evict_select(const __grid_constant__ EvictParams p, int ranks,
-                                                              int key_cap) {
-    extern __shared__ __align__(16) uint32_t sm[];
-    int* s_hist = reinterpret_cast<int*>(sm);                // [3][kEvBins]
-    uint32_t* s_key = sm + 3 * kEvBins;                      // [key_cap]
+// eight consecutive 32-bit values from row s on, `fill` from row `end` on
+template <typename T>
+__device__ __forceinline__ void load_rows(const T* p, int s, int end, bool vec, T fill, T (&x)[8]) {
+    if (vec && s + 8 <= end) {
+        const int4 a = __ldg(reinterpret_cast<const int4*>(p + s)), b = __ldg(reinterpret_cast<const int4*>(p + s) + 1);
+        const int v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = *reinterpret_cast<const T*>(&v[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = s + e < end ? __ldg(p + s + e) : fill;
+    }
+}
+
+__device__ __forceinline__ int excl_scan(int x, int lane) {
+    int y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += v;
+    }
+    return y - x;
+}
+
+__global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_constant__ EvictParams p, int ranks,
+                                                                 int key_cap) {
+    extern __shared__ __align__(16) int sm[];
+    int* s_hist = sm;                                                  // [kEvHist]
+    uint16_t* s_key = reinterpret_cast<uint16_t*>(sm + kEvHist);      // [key_cap] upper halves of the keys
     __shared__ int s_scan[kEvWarps], s_bin[3], s_maxes[kEvWarps], s_max;
     __shared__ int s_cnt[4][kEvWarps], s_tot[4];
     __shared__ int s_tie[kEvWarps], s_hole[kEvWarps], s_src[kEvWarps];
@@ -54,9 +83,10 @@ __global__ void __launch_bounds__(kEvThreads, 1) k_evict_select(const __grid_con
     const int64_t base = static_cast<int64_t>(u) * p.row_pitch;
     const float* w_in = p.weight + base;
     const int32_t* p_in = p.position + base;
+    const bool vec = ((reinterpret_cast<uintptr_t>(w_in) | reinterpret_cast<uintptr_t>(p_in)) & 15) == 0;
     const bool copy_w = p.weight_out != p.weight, copy_p = p.position_out != p.position;
-    // slices are whole multiples of 32 rows per warp
-    const int per = (static_cast<int>((static_cast<int64_t>(n) + ranks - 1) / ranks) + kEvThreads - 1) / kEvThreads * 32;
+    const int64_t slice = (static_cast<int64_t>(n) + ranks - 1) / ranks;
+    const int per = static_cast<int>((slice + kEvGrain - 1) / kEvGrain) * kEvStep;        // rows of a warp
     const int64_t lo64 = (static_cast<int64_t>(rank) * kEvWarps + warp) * per;
     const int lo = static_cast<int>(min(lo64, static_cast<int64_t>(n)));
     const int hi = static_cast<int>(min(lo64 + per, static_cast<int64_t>(n)));
@@ -70,16 +100,22 @@ __global__ void __launch_bounds__(kEvThreads, 1) k_evict_select(const __grid_con
         return;
     }
 
-    for (int i = tid; i < 3 * kEvBins; i += kEvThreads) s_hist[i] = 0;
+    for (int i = tid; i < kEvHist; i += kEvThreads) s_hist[i] = 0;
     // ---- the unit's last position
     int last = INT_MIN;
-    for (int i = lo + lane; i < hi; i += 32) last = max(last, __ldg(p_in + i));
+#pragma unroll 4
+    for (int r0 = lo; r0 < hi; r0 += kEvStep) {
+        int pos[8];
+        load_rows<int>(p_in, r0 + 8 * lane, hi, vec, INT_MIN, pos);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) last = max(last, pos[e]);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
     if (lane == 0) s_maxes[warp] = last;
     __syncthreads();
     if (warp == 0) {
-        int x = s_maxes[lane];
+        int x = s_maxes[lane % kEvWarps];
 #pragma unroll
         for (int o = 16; o; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
         if (lane == 0) s_max = x;
@@ -91,62 +127,96 @@ __global__ void __launch_bounds__(kEvThreads, 1) k_evict_select(const __grid_con
     const int64_t safe_from = static_cast<int64_t>(last) - p.recent;
 
     const bool held = per * kEvWarps <= key_cap;
-    uint32_t* my = s_key + warp * per;
-    auto make = [&](int i) -> uint32_t {
-        const int pos = __ldg(p_in + i);
-        return (pos > safe_from || pos < p.sink) ? 0xFFFFFFFFu : weight_key(__ldg(w_in + i));
+    uint16_t* my = s_key + warp * per;
+    auto key_of = [&](float w, int pos) -> uint32_t {
+        return (pos > safe_from || pos < p.sink) ? 0xFFFFFFFFu : weight_key(w);
     };
-    auto key = [&](int i) -> uint32_t { return held ? my[i - lo] : make(i); };
+    auto full = [&](int i) -> uint32_t { return key_of(__ldg(w_in + i), __ldg(p_in + i)); };
+    // upper halves of the lane's eight keys from row s on
+    auto make = [&](int s, uint32_t (&t)[8]) {
+        float w[8];
+        int pos[8];
+        load_rows<float>(w_in, s, hi, vec, 0.f, w);
+        load_rows<int>(p_in, s, hi, vec, 0, pos);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = key_of(w[e], pos[e]) >> 16;
+    };
+    auto upper = [&](int s, uint32_t (&t)[8]) {
+        if (held) {
+            const uint4 v = *reinterpret_cast<const uint4*>(my + (s - lo));
+            t[0] = v.x & 0xFFFF; t[1] = v.x >> 16; t[2] = v.y & 0xFFFF; t[3] = v.y >> 16;
+            t[4] = v.z & 0xFFFF; t[5] = v.z >> 16; t[6] = v.w & 0xFFFF; t[7] = v.w >> 16;
+        } else {
+            make(s, t);
+        }
+    };
 
-    // ---- the M-th largest key, from the top
+    // ---- the M-th largest key, from the top; bits 31..21, 20..16, 15..5, 4..0
     uint32_t prefix = 0, T = 0;
     int need = M, ties = 0;
     bool whole = false;        // every key from T + 1 on stays, no ties
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-        int* hist = s_hist + pass * kEvBins;
-        for (int i = lo + lane; i < hi; i += 32) {
-            uint32_t k;
+    for (int pass = 0; pass < 4; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 16 : pass == 2 ? 5 : 0, bins = (pass & 1) ? 32 : kEvBins;
+        int* hist = s_hist + (pass == 0 ? 0 : pass == 1 ? 2 * kEvBins : pass == 2 ? kEvBins : 2 * kEvBins + 32);
+        for (int r0 = lo; r0 < hi; r0 += kEvStep) {
+            const int s = r0 + 8 * lane;
+            uint32_t t[8];
             if (pass == 0) {
-                k = make(i);
-                if (held) my[i - lo] = k;
+                make(s, t);
+                if (held)
+                    *reinterpret_cast<uint4*>(my + (s - lo)) =
+                        make_uint4(t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, t[6] | t[7] << 16);
             } else {
-                k = key(i);
-                if ((k >> (shift + bits)) != prefix) continue;
+                upper(s, t);
             }
-            atomicAdd(hist + ((k >> shift) & ((1u << bits) - 1)), 1);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (s + e >= hi) continue;
+                if (pass == 0) {
+                    atomicAdd(hist + (t[e] >> 5), 1);
+                } else if (pass == 1) {
+                    if ((t[e] >> 5) == prefix) atomicAdd(hist + (t[e] & 31), 1);
+                } else if (t[e] == (pass == 2 ? prefix : prefix >> 11)) {
+                    const uint32_t k = full(s + e);
+                    if (pass == 2) atomicAdd(hist + ((k >> 5) & (kEvBins - 1)), 1);
+                    else if ((k >> 5) == prefix) atomicAdd(hist + (k & 31), 1);
+                }
+            }
         }
         sync_all(ranks);
-        // bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t
-        int c0 = hist[kEvBins - 1 - 2 * tid], c1 = hist[kEvBins - 2 - 2 * tid];
-        for (int r = 0; r < ranks; ++r)
-            if (r != rank) {
-                c0 += ld_cluster_s32(cluster_addr(hist + kEvBins - 1 - 2 * tid, r));
-                c1 += ld_cluster_s32(cluster_addr(hist + kEvBins - 2 - 2 * tid, r));
-            }
-        int sum = c0 + c1;
+        // counts from the top: thread t holds four bins, the uppermost first
+        int cnt[4] = {0, 0, 0, 0};
+        const int top = bins - 1 - 4 * tid;
+        if (top >= 0) {
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += x;
+            for (int e = 0; e < 4; ++e) cnt[e] = hist[top - e];
+            for (int r = 0; r < ranks; ++r)
+                if (r != rank) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) cnt[e] += ld_cluster_s32(cluster_addr(hist + top - e, r));
+                }
         }
-        if (lane == 31) s_scan[warp] = sum;
+        const int mine = cnt[0] + cnt[1] + cnt[2] + cnt[3];
+        int above = excl_scan(mine, lane);
+        if (lane == 31) s_scan[warp] = above + mine;
         __syncthreads();
-        int before = 0;
-        for (int w = 0; w < warp; ++w) before += s_scan[w];
-        const int above = before + sum - c0 - c1;     // keys in the bins above this thread's two
-        if (above < need && above + c0 + c1 >= need) {
-            const bool first = above + c0 >= need;
-            s_bin[0] = first ? kEvBins - 1 - 2 * tid : kEvBins - 2 - 2 * tid;
-            s_bin[1] = first ? above : above + c0;
-            s_bin[2] = first ? c0 : c1;
+        above += __reduce_add_sync(0xffffffffu, lane < warp ? s_scan[lane % kEvWarps] : 0);
+        if (above < need && above + mine >= need) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (above < need && above + cnt[e] >= need) {
+                    s_bin[0] = top - e;
+                    s_bin[1] = above;
+                    s_bin[2] = cnt[e];
+                }
+                above += cnt[e];
+            }
         }
         __syncthreads();
-        const int bin = s_bin[0], inside = s_bin[2];
+        const int inside = s_bin[2];
         need -= s_bin[1];
-        prefix = (prefix << bits) | static_cast<uint32_t>(bin);
-        __syncthreads();
+        prefix = (prefix << ((pass & 1) ? 5 : 11)) | static_cast<uint32_t>(s_bin[0]);
         if (inside == need && prefix != 0) {          // the whole bin stays
             T = (prefix << shift) - 1;
             whole = true;
@@ -157,19 +227,44 @@ __global__ void __launch_bounds__(kEvThreads, 1) k_evict_select(const __grid_con
         T = prefix;
         ties = need;           // this many rows of key T stay, the lowest ones
     }
+    const uint32_t T16 = T >> 16;
+    const bool upper_alone = whole && (T & 0xFFFFu) == 0xFFFFu;     // no key of upper half T16 stays
+    // which of the lane's eight rows from s on lie above the threshold, and which on it
+    auto grade = [&](int s, uint32_t& gt, uint32_t& tie) {
+        uint32_t t[8];
+        upper(s, t);
+        gt = tie = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (s + e >= hi || t[e] < T16) continue;
+            if (t[e] > T16) {
+                gt |= 1u << e;
+            } else if (!upper_alone) {
+                const uint32_t k = full(s + e);
+                if (k > T) gt |= 1u << e;
+                else if (k == T && !whole) tie |= 1u << e;
+            }
+        }
+    };
+    // of the eight rows from s on: bits of those below x
+    auto bits_below = [](int s, int x) -> uint32_t { return x <= s ? 0u : x - s >= 8 ? 0xFFu : (1u << (x - s)) - 1; };
 
     // ---- rows of each kind per warp: given up and tied below M, kept for sure and tied behind
     int n_low = 0, n_tl = 0, n_gt = 0, n_th = 0;
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-        const int i = i0 + lane;
-        const bool in = i < hi;
-        const uint32_t k = in ? key(i) : 0;
-        const bool tie = in && !whole && k == T, gt = in && k > T;
-        n_low += __popc(__ballot_sync(0xffffffffu, in && i < M && !gt && !tie));
-        n_tl += __popc(__ballot_sync(0xffffffffu, i < M && tie));
-        n_gt += __popc(__ballot_sync(0xffffffffu, i >= M && gt));
-        n_th += __popc(__ballot_sync(0xffffffffu, i >= M && tie));
+    for (int r0 = lo; r0 < hi; r0 += kEvStep) {
+        const int s = r0 + 8 * lane;
+        uint32_t gt, tie;
+        grade(s, gt, tie);
+        const uint32_t in = bits_below(s, hi), low = bits_below(s, M);
+        n_low += __popc(in & low & ~(gt | tie));
+        n_tl += __popc(low & tie);
+        n_gt += __popc(~low & gt);
+        n_th += __popc(~low & tie);
     }
+    n_low = __reduce_add_sync(0xffffffffu, n_low);
+    n_tl = __reduce_add_sync(0xffffffffu, n_tl);
+    n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+    n_th = __reduce_add_sync(0xffffffffu, n_th);
     if (lane == 0) {
         s_cnt[0][warp] = n_low;
         s_cnt[1][warp] = n_tl;
@@ -178,7 +273,7 @@ __global__ void __launch_bounds__(kEvThreads, 1) k_evict_select(const __grid_con
     }
     __syncthreads();
     if (warp < 4) {
-        const int x = warp_sum_i(s_cnt[warp][lane]);
+        const int x = __reduce_add_sync(0xffffffffu, lane < kEvWarps ? s_cnt[warp][lane] : 0);
         if (lane == 0) s_tot[warp] = x;
     }
     sync_all(ranks);
@@ -193,54 +288,62 @@ __global__ void __launch_bounds__(kEvThreads, 1) k_evict_select(const __grid_con
             src0 += g + kh;
             tie0 += tl + th;
         }
-        const int a = s_cnt[0][lane], tl = s_cnt[1][lane], g = s_cnt[2][lane], th = s_cnt[3][lane];
-        auto excl = [&](int x) {
-            int y = x;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, y, o);
-                if (lane >= o) y += v;
-            }
-            return y - x;
-        };
-        const int t0 = tie0 + excl(tl + th);
+        const int w = lane % kEvWarps;
+        const bool own = lane < kEvWarps;
+        const int a = own ? s_cnt[0][w] : 0, tl = own ? s_cnt[1][w] : 0, g = own ? s_cnt[2][w] : 0, th = own ? s_cnt[3][w] : 0;
+        const int t0 = tie0 + excl_scan(tl + th, lane);
         const int left = max(0, ties - t0), kl = min(tl, left), kh = min(th, left - kl);
         const int holes = a + tl - kl, srcs = g + kh;
-        s_tie[lane] = t0;
-        s_hole[lane] = hole0 + excl(holes);
-        const int s0 = src0 + excl(srcs);
-        s_src[lane] = s0;
-        if (rank == ranks - 1 && lane == 31) p.count[u] = s0 + srcs;
+        const int h0 = hole0 + excl_scan(holes, lane), s0 = src0 + excl_scan(srcs, lane);
+        if (own) {
+            s_tie[w] = t0;
+            s_hole[w] = h0;
+            s_src[w] = s0;
+        }
+        if (rank == ranks - 1 && lane == kEvWarps - 1) p.count[u] = s0 + srcs;
     }
     sync_all(ranks);       // and no CTA leaves while another reads its counts
     int tie_at = s_tie[warp], hole_at = s_hole[warp], src_at = s_src[warp];
     int32_t* to = p.to + static_cast<int64_t>(u) * p.list_cap;
     int32_t* of = p.of + static_cast<int64_t>(u) * p.list_cap;
-    const uint32_t below = (1u << lane) - 1;
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-        const int i = i0 + lane;
-        const bool in = i < hi;
-        const uint32_t k = in ? key(i) : 0;
-        const bool tie = in && !whole && k == T;
-        const uint32_t tb = __ballot_sync(0xffffffffu, tie);
-        const bool kept = in && ((k > T) || (tie && tie_at + __popc(tb & below) < ties));
-        tie_at += __popc(tb);
-        const uint32_t hb = __ballot_sync(0xffffffffu, in && i < M && !kept);
-        const uint32_t sb = __ballot_sync(0xffffffffu, i >= M && kept);
-        if (in && i < M && !kept) {
-            const int at = hole_at + __popc(hb & below);
-            if (at < p.list_cap) to[at] = i;
+    for (int r0 = lo; r0 < hi; r0 += kEvStep) {
+        const int s = r0 + 8 * lane;
+        uint32_t kept, tie;
+        grade(s, kept, tie);
+        if (__any_sync(0xffffffffu, tie)) {
+            int t = tie_at + excl_scan(__popc(tie), lane);
+            tie_at += __reduce_add_sync(0xffffffffu, __popc(tie));
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if ((tie >> e) & 1) {
+                    if (t < ties) kept |= 1u << e;
+                    ++t;
+                }
         }
-        if (i >= M && kept) {
-            const int at = src_at + __popc(sb & below);
-            if (at < p.list_cap) of[at] = i;
+        const uint32_t in = bits_below(s, hi), low = bits_below(s, M);
+        const uint32_t hole = in & low & ~kept, src = kept & ~low;
+        if (!__any_sync(0xffffffffu, hole | src | (kept & low))) continue;
+        const int both = __popc(hole) | __popc(src) << 16;       // at most 256 of each
+        const int at = excl_scan(both, lane);
+        const int all = __reduce_add_sync(0xffffffffu, both);
+        int ha = hole_at + (at & 0xFFFF), sa = src_at + (at >> 16);
+        hole_at += all & 0xFFFF;
+        src_at += all >> 16;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if ((hole >> e) & 1) {
+                if (ha < p.list_cap) to[ha] = s + e;
+                ++ha;
+            }
+            if ((src >> e) & 1) {
+                if (sa < p.list_cap) of[sa] = s + e;
+                ++sa;
+            }
+            if ((kept & low) >> e & 1) {
+                if (copy_w) p.weight_out[base + s + e] = w_in[s + e];
+                if (copy_p) p.position_out[base + s + e] = p_in[s + e];
+            }
         }
-        if (i < M && kept) {
-            if (copy_w) p.weight_out[base + i] = w_in[i];
-            if (copy_p) p.position_out[base + i] = p_in[i];
-        }
-        hole_at += __popc(hb);
-        src_at += __popc(sb);
     }
 }
 
@@ -297,15 +400,17 @@ __global__ void __launch_bounds__(kMvThreads) k_evict_move(const __grid_constant
 
 int launch_evict(const EvictParams& p, int nsm, cudaStream_t s) {
     const int U = p.c.batch * p.c.H;
-    // CTAs per unit: as many as keep the device's SMs busy, and no fewer than the keys need to
-    // stay in shared memory; a slice of under 4096 rows does not pay for the cluster's barriers
+    // CTAs per unit: as many as the device holds at once (two per SM), and no fewer than the keys
+    // need to stay in shared memory; a slice of under one grain (4096 rows) would leave warps idle
     int ranks = 1;
-    while (ranks < 8 && p.c.cap / ranks > 4096 && (U * ranks * 2 <= nsm || p.c.cap / ranks > kEvKeys)) ranks *= 2;
+    while (ranks < 8 && p.c.cap > ranks * kEvGrain && (U * ranks <= nsm || p.c.cap / ranks > kEvKeys)) ranks *= 2;
     const int64_t slice = (static_cast<int64_t>(p.c.cap) + ranks - 1) / ranks;
-    const int64_t keys = (slice + kEvThreads - 1) / kEvThreads * kEvThreads;
+    const int64_t keys = (slice + kEvGrain - 1) / kEvGrain * kEvGrain;
     const int key_cap = static_cast<int>(keys < kEvKeys ? keys : kEvKeys);
-    const int smem = (3 * kEvBins + key_cap) * 4;
-    if (cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
+    const int smem = kEvHist * 4 + key_cap * 2;
+    if (cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvHist * 4 + kEvKeys * 2) !=
+        cudaSuccess)
+        return -1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(U) * ranks);
     cfg.blockDim = dim3(kEvThreads);

@@ -534,19 +534,19 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
     const int64_t ctas = gridDim.x, me = blockIdx.x;
     const Place pl = plan(p.c, me, ctas, s_plan);
 
-    // sequences of no rows
-    for (int b = blockIdx.x; b < p.c.batch; b += gridDim.x)
-        if (rows_of(p.c, b, g_err, 711) == 0) {
-            for (int i = tid; i < p.n_q * D; i += kPaThreads) store_out(p, kF32, b, 0, i / D, i % D, 0.f);
-            if (p.lse)
-                for (int i = tid; i < p.n_q; i += kPaThreads) p.lse[static_cast<int64_t>(b) * p.n_q + i] = -CUDART_INF_F;
-        }
-    if (me >= pl.n) return;
-
-    const int64_t w0 = me * pl.total / pl.n, w1 = (me + 1) * pl.total / pl.n;
+    const bool work = me < pl.n;
+    const int64_t w0 = work ? me * pl.total / pl.n : 0, w1 = work ? (me + 1) * pl.total / pl.n : 0;
     int b = pl.b, rows = pl.rows, nb = pl.nb;
-    int h = static_cast<int>((w0 - pl.first) / nb);
+    int h = work ? static_cast<int>((w0 - pl.first) / nb) : 0;
     int64_t unit0 = pl.first + static_cast<int64_t>(h) * nb;     // first block of the unit
+    if (tid == 0) {
+        Joint j{-1, 0, 0, 0};
+        if (work && unit0 < w0 && unit0 + nb <= w1) {
+            const int64_t from = ((unit0 + 1) * pl.n - 1) / pl.total;      // the CTA whose range holds block unit0
+            j = Joint{static_cast<int>(from), b, h, from * pl.total / pl.n == unit0 ? 0 : 1};
+        }
+        p.joint[me] = j;
+    }
     Tile tile;
     for (int64_t cur = w0; cur < w1;) {
         const int blk = static_cast<int>(cur - unit0);
@@ -596,57 +596,124 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
             nb = blocks_of(rows);
         }
     }
+    // sequences of no rows
+    for (int e = blockIdx.x; e < p.c.batch; e += gridDim.x)
+        if (rows_of(p.c, e, g_err, 711) == 0) {
+            for (int i = tid; i < p.n_q * D; i += kPaThreads) store_out(p, kF32, e, 0, i / D, i % D, 0.f);
+            if (p.lse)
+                for (int i = tid; i < p.n_q; i += kPaThreads) p.lse[static_cast<int64_t>(e) * p.n_q + i] = -CUDART_INF_F;
+        }
 }
 
 // Joins the records of the units that lie in more than one CTA's range: CTA (i, g) those of head
-// g of the unit that ends in CTA i's range and began before it.
+// g of the unit that ends in CTA i's range and began before it (p.joint[i] says which, if any).
+// Lanes hold four dimensions each; warps (half-warps where d is 64) take the contributors in turn.
+constexpr int kPaMost = 512;      // contributors at most
+
 template <int D, bool kF32>
-__global__ void __launch_bounds__(kPaThreads) k_paged_merge(const __grid_constant__ PagedAttnParams p, int ctas) {
-    __shared__ PlanSmem s_plan;
-    __shared__ float s_x[kPaThreads], s_l[kPaThreads];
+__global__ void __launch_bounds__(kPaThreads) k_paged_merge(const __grid_constant__ PagedAttnParams p) {
+    constexpr int kLanes = D / 4, kWays = kPaThreads / kLanes;
+    __shared__ float s_f[kPaMost], s_red[kPaWarps], s_sum[kPaWarps];
+    __shared__ __align__(16) float s_x[kWays][D];
     pdl_trigger();
-    const int tid = threadIdx.x, g = blockIdx.y;
-    const int64_t me = blockIdx.x;
-    const Place pl = plan(p.c, me, ctas, s_plan);
     // every CTA waits for the grid before, so that this grid's end stands for both
     pdl_wait();
-    if (me >= pl.n) return;
-    const int64_t w0 = me * pl.total / pl.n, w1 = (me + 1) * pl.total / pl.n;
-    const int h = static_cast<int>((w0 - pl.first) / pl.nb);
-    const int64_t unit0 = pl.first + static_cast<int64_t>(h) * pl.nb;
-    if (unit0 == w0 || unit0 + pl.nb > w1) return;
-    // the CTA whose range holds block unit0
-    const int64_t from = ((unit0 + 1) * pl.n - 1) / pl.total;
-    const bool first_of_range = from * pl.total / pl.n == unit0;
-    constexpr int kWays = kPaThreads / D;      // contributors in turn where d is 64
-    const int dim = tid % D, way = tid / D;
-    auto rec_of = [&](int64_t i) { return p.rec + (i * 2 + (i == from && !first_of_range ? 1 : 0)) * p.G * (D + 2) + g * (D + 2); };
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = blockIdx.y, me = blockIdx.x;
+    const int4 raw = __ldcg(reinterpret_cast<const int4*>(p.joint) + me);
+    const Joint j{raw.x, raw.y, raw.z, raw.w};
+    if (j.from < 0) return;
+    const int n = me - j.from + 1;
+    const int64_t pitch = p.G * (D + 2);
+    // contributor i's record: slot 0, but the unit began inside the first one's range
+    auto rec_of = [&](int i) { return p.rec + (static_cast<int64_t>(j.from + i) * 2 + (i == 0 ? j.slot : 0)) * pitch + g * (D + 2); };
     float m = -CUDART_INF_F;
-    for (int64_t i = from; i <= me; ++i) m = fmaxf(m, __ldcg(rec_of(i) + D));
-    float l = 0.f, x = 0.f;
-    for (int64_t i = from + way; i <= me; i += kWays) {
-        const float* r = rec_of(i);
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(r + D));
+    for (int i = tid; i < n; i += kPaThreads) m = fmaxf(m, __ldcg(rec_of(i) + D));
+    m = warp_max(m);
+    if (lane == 0) s_red[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kPaWarps; ++w) m = fmaxf(m, s_red[w]);
+    float l = 0.f;
+    for (int i = tid; i < n; i += kPaThreads) {
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(rec_of(i) + D));
         const float f = ml.x == -CUDART_INF_F && !(ml.y != ml.y) ? 0.f : exp2_fast(ml.x - m);
+        s_f[i] = f;
         l = fmaf(ml.y, f, l);
-        x = fmaf(__ldcg(r + dim), f, x);
     }
-    if (kWays > 1) {
-        s_x[tid] = x;
-        s_l[tid] = l;
-        __syncthreads();
-        x = l = 0.f;
-        for (int w = 0; w < kWays; ++w) {
-            x += s_x[w * D + dim];
-            l += s_l[w * D + dim];
+    l = warp_sum(l);
+    if (lane == 0) s_sum[warp] = l;
+    __syncthreads();
+    l = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+    const int dim = 4 * (tid % kLanes), way = tid / kLanes;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = way; i < n; i += kWays) {
+        const float* r = rec_of(i) + dim;
+        const float2 a = __ldcg(reinterpret_cast<const float2*>(r)), b = __ldcg(reinterpret_cast<const float2*>(r + 2));
+        const float f = s_f[i];
+        x[0] = fmaf(a.x, f, x[0]);
+        x[1] = fmaf(a.y, f, x[1]);
+        x[2] = fmaf(b.x, f, x[2]);
+        x[3] = fmaf(b.y, f, x[3]);
+    }
+    *reinterpret_cast<float4*>(&s_x[way][dim]) = make_float4(x[0], x[1], x[2], x[3]);
+    __syncthreads();
+    if (tid < D) {
+        float sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWays; ++w) sum += s_x[w][tid];
+        store_out(p, kF32, j.b, j.h, g, tid, l == 0.f ? 0.f : sum / l);
+    }
+    if (tid == 0) {
+        if (p.lse) p.lse[static_cast<int64_t>(j.b) * p.n_q + j.h * p.G + g] = ln_of(m, l);
+        if (p.stat) p.stat[(static_cast<int64_t>(j.b) * p.c.H + j.h) * p.G + g] = make_float2(m, l == 0.f ? 0.f : 1.f / l);
+    }
+}
+
+// Four rows per thread and turn: their products are loaded before any of them is used.
+template <int Gp>
+__device__ __forceinline__ void weigh_rows_of(const PagedAttnParams& p, int64_t u, int first, int end) {
+    const float* z = p.z + u * p.c.cap * Gp;
+    const float* in = p.weight + u * p.row_pitch;
+    float* out = p.weight_out + u * p.row_pitch;
+    float base[Gp], inv[Gp];
+#pragma unroll
+    for (int g = 0; g < Gp; ++g) {
+        const float2 st = g < p.G ? __ldcg(p.stat + u * p.G + g) : make_float2(0.f, 0.f);
+        base[g] = st.x;
+        inv[g] = st.y;
+    }
+    for (int i0 = first + threadIdx.x; i0 < end; i0 += 4 * kPaThreads) {
+        float2 x[4][Gp / 2];
+        float w[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = i0 + r * kPaThreads;
+            if (i >= end) continue;
+            w[r] = in[i];
+#pragma unroll
+            for (int g = 0; g < Gp / 2; ++g) x[r][g] = __ldcg(reinterpret_cast<const float2*>(z + static_cast<int64_t>(i) * Gp) + g);
         }
-        if (way) return;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int i = i0 + r * kPaThreads;
+            if (i >= end) continue;
+            float sum = 0.f;
+#pragma unroll
+            for (int g = 0; g < Gp; ++g) {
+                const float v = g & 1 ? x[r][g / 2].y : x[r][g / 2].x;
+                // an absent row's product is -inf and adds nothing
+                if (g < p.G && v != -CUDART_INF_F) sum += exp2_fast(fmaf(v, p.scale_log2, -base[g])) * inv[g];
+            }
+            out[i] = w[r] + sum;
+        }
     }
-    store_out(p, kF32, pl.b, h, g, dim, l == 0.f ? 0.f : x / l);
-    if (dim == 0) {
-        if (p.lse) p.lse[static_cast<int64_t>(pl.b) * p.n_q + h * p.G + g] = ln_of(m, l);
-        if (p.stat) p.stat[(static_cast<int64_t>(pl.b) * p.c.H + h) * p.G + g] = make_float2(m, l == 0.f ? 0.f : 1.f / l);
-    }
+}
+__device__ __forceinline__ void weigh_rows(const PagedAttnParams& p, int64_t u, int first, int end) {
+    if (p.Gp == 2) weigh_rows_of<2>(p, u, first, end);
+    else if (p.Gp == 4) weigh_rows_of<4>(p, u, first, end);
+    else if (p.Gp == 6) weigh_rows_of<6>(p, u, first, end);
+    else weigh_rows_of<8>(p, u, first, end);
 }
 
 // weight_out = weight + sum over the heads of exp2(z scale - base) / sum, over the same split
@@ -666,18 +733,7 @@ __global__ void __launch_bounds__(kPaThreads) k_paged_weigh(const __grid_constan
         const int first = static_cast<int>(cur - unit0) * kPaBlock;
         const int end = static_cast<int>(min(static_cast<int64_t>(rows), (stop - unit0) * kPaBlock));
         const int64_t u = static_cast<int64_t>(b) * p.c.H + h;
-        const float* z = p.z + u * p.c.cap * p.Gp;
-        const float2* stat = p.stat + u * p.G;
-        for (int i = first + tid; i < end; i += kPaThreads) {
-            float sum = 0.f;
-            for (int g = 0; g < p.G; ++g) {
-                const float2 st = __ldcg(stat + g);
-                const float x = __ldcg(z + static_cast<int64_t>(i) * p.Gp + g);
-                // an absent row's product is -inf and adds nothing
-                if (x != -CUDART_INF_F) sum += exp2_fast(fmaf(x, p.scale_log2, -st.x)) * st.y;
-            }
-            p.weight_out[u * p.row_pitch + i] = p.weight[u * p.row_pitch + i] + sum;
-        }
+        weigh_rows(p, u, first, end);
         cur = stop;
         if (cur >= w1) break;
         unit0 += nb;
@@ -693,14 +749,22 @@ __global__ void __launch_bounds__(kPaThreads) k_paged_weigh(const __grid_constan
 // ------------------------------------------------------------------ launches
 
 constexpr int kOccTC = 3, kOccF32 = 2;     // CTAs per SM
+constexpr int kWeighOcc = 3;               // CTAs of k_paged_weigh per CTA of k_paged_attn
 
 int paged_attn_ctas(int dtype, int nsm) { return nsm * (dtype == SKV_F32 ? kOccF32 : kOccTC); }
 
 template <class Tile, int D, bool kF32, int kOcc>
 static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
-    k_paged_attn<Tile, D, kF32, kOcc><<<ncta, kPaThreads, 0, s>>>(p);
-    if (launch_pdl(k_paged_merge<D, kF32>, dim3(ncta, p.G), dim3(kPaThreads), 0, s, p, ncta) != cudaSuccess) return -1;
-    if (p.weight_out && launch_pdl(k_paged_weigh, dim3(ncta), dim3(kPaThreads), 0, s, p) != cudaSuccess) return -1;
+    // no more CTAs than there can be blocks of rows
+    const int64_t most = static_cast<int64_t>(p.c.batch) * p.c.H * ((p.c.cap + kPaBlock - 1) / kPaBlock);
+    const int n = most < ncta ? static_cast<int>(most) : ncta;
+    k_paged_attn<Tile, D, kF32, kOcc><<<n, kPaThreads, 0, s>>>(p);
+    if (launch_pdl(k_paged_merge<D, kF32>, dim3(n, p.G), dim3(kPaThreads), 0, s, p) != cudaSuccess) return -1;
+    if (p.weight_out) {
+        const int64_t wide = kWeighOcc * static_cast<int64_t>(ncta);
+        const int nw = static_cast<int>(most < wide ? most : wide);
+        if (launch_pdl(k_paged_weigh, dim3(nw), dim3(kPaThreads), 0, s, p) != cudaSuccess) return -1;
+    }
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 template <int D>

@@ -117,7 +117,7 @@ int64_t round16(int64_t n) { return (n + 15) & ~int64_t(15); }
 
 // ------------------------------------------------------------------ attention
 
-struct AttnSpace { int Gp; int64_t rec, stat, z, bytes; };
+struct AttnSpace { int Gp; int64_t joint, rec, stat, z, bytes; };
 
 // host-only part of the checks, and the workspace's layout
 int attn_space(const skv_paged_attention_args* a, AttnSpace* w) {
@@ -129,8 +129,9 @@ int attn_space(const skv_paged_attention_args* a, AttnSpace* w) {
         return SKV_ERR_INVALID;
     const int64_t U = static_cast<int64_t>(c.batch) * c.n_kv_heads, cap = static_cast<int64_t>(c.max_pages) * c.page_size;
     w->Gp = (G + 1) & ~1;
-    w->rec = 0;
-    w->stat = round16(static_cast<int64_t>(paged_attn_ctas(c.dtype, kMaxSms)) * 2 * G * (c.head_dim + 2) * 4);
+    w->joint = 0;
+    w->rec = static_cast<int64_t>(paged_attn_ctas(c.dtype, kMaxSms)) * sizeof(Joint);
+    w->stat = w->rec + round16(static_cast<int64_t>(paged_attn_ctas(c.dtype, kMaxSms)) * 2 * G * (c.head_dim + 2) * 4);
     w->z = w->stat;
     w->bytes = w->stat;
     if (a->weight_out) {
@@ -226,7 +227,7 @@ int shadowkv_qk_norm_rope(const skv_qk_norm_rope_args* a, skv_stream stream) {
     for (int i = 0; i < rd / 2; ++i)
         p.turn[i] = static_cast<uint64_t>(
             std::ldexp(std::pow(a->rope_base, -2.0 * i / rd) / 6.283185307179586476925, 64));
-    return done(launch_norm_rope(c.dtype, c.head_dim, p, stream));
+    return done(launch_norm_rope(c.dtype, c.head_dim, p, dev.nsm, stream));
 }
 
 int64_t shadowkv_paged_attention_workspace(const skv_paged_attention_args* a) {
@@ -263,6 +264,7 @@ int shadowkv_paged_attention(const skv_paged_attention_args* a, skv_stream strea
                                       1.4426950408889634074);
     p.q_seq = a->q_seq; p.q_head = a->q_head; p.o_seq = a->out_seq; p.o_head = a->out_head;
     p.q = a->q; p.out = a->out; p.lse = a->lse;
+    p.joint = reinterpret_cast<Joint*>(ws + w.joint);
     p.rec = reinterpret_cast<float*>(ws + w.rec);
     if (a->weight_out) {
         p.stat = reinterpret_cast<float2*>(ws + w.stat);

@@ -32,7 +32,11 @@ struct NormRopeParams {
     int32_t* row_position; float* row_weight; int64_t row_pitch;
     uint64_t turn[64];        // rope_base^(-2i/rd) / (2 pi) in units of 2^-64 turns
 };
-int launch_norm_rope(int dtype, int d, const NormRopeParams& p, cudaStream_t s);
+int launch_norm_rope(int dtype, int d, const NormRopeParams& p, int nsm, cudaStream_t s);
+
+// A unit whose shares CTA i of the attention completes: its shares lie in the records of CTAs
+// from .. i (slot: which of the first one's two); from < 0: there is none.
+struct Joint { int from, b, h, slot; };
 
 struct PagedAttnParams {
     PagedView c;
@@ -41,6 +45,7 @@ struct PagedAttnParams {
     int64_t q_seq, q_head, o_seq, o_head;
     const void* q; void* out; float* lse;
     float* rec;               // [ncta][2][G][d + 2]: a CTA's shares of its first and last unit
+    Joint* joint;             // [ncta]
     // weights: raw products q.k of every row [U][cap][Gp], and (base, 1 / sum) per head [U][G]
     float* z; float2* stat; int Gp;
     const float* weight; float* weight_out; int64_t row_pitch;

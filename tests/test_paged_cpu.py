@@ -159,8 +159,9 @@ def test_host_pools_are_refused_or_need_a_device(skv):
     """Well-formed calls on CPU tensors: refused as host memory, or no device to run on."""
     c, q = cache(), torch.zeros((2, 4, 128), dtype=torch.bfloat16)
     from sparse_kv_cache_gb300 import _binding as b
-    packed = b._PAGED_ATTN.pack(*b._pool_fields("t", c["k_cache"], c["v_cache"], c["table"], c["lens"], 2), 4, 0.0, 512, 128,
-                                512, 128, q.data_ptr(), q.data_ptr(), 0, 0, 0, 0, q.data_ptr(), 1 << 40)
+    pools = [c[n] for n in ("k_cache", "v_cache", "table", "lens")]
+    packed = b._PAGED_ATTN.pack(*b._pool_fields("t", *(b._form(t) for t in pools), 2), *(t.data_ptr() for t in pools), 4,
+                                0.0, 512, 128, 512, 128, q.data_ptr(), q.data_ptr(), 0, 0, 0, 0, q.data_ptr(), 1 << 40)
     assert skv.load().shadowkv_paged_attention(packed, None) in (-1, -4)
 
 
