@@ -21,8 +21,8 @@ namespace skv {
 
 static __device__ int g_err[2];
 
-constexpr int kNrThreads = 256;
-constexpr int kNrMaxTok = 16;     // tokens per CTA at most
+constexpr int kNrThreads = 128;
+constexpr int kNrMaxTok = 16;     // tokens of a CTA at most
 
 // 16 elements of a row as they lie in memory: 8 at o1, 8 at o2
 template <typename T> struct Raw;
@@ -50,82 +50,101 @@ __device__ __forceinline__ void widen(const Raw<float>& r, float (&a)[8], float 
     z[4] = r.z1.x; z[5] = r.z1.y; z[6] = r.z1.z; z[7] = r.z1.w;
 }
 
-// Which row of the CTA's tokens a lane group holds: head j of token t (q heads, then k, then v).
-struct Row {
-    int t, j;
-    __device__ __forceinline__ void step(int rows, int per_tok) {
-        j += rows;
-        while (j >= per_tok) {
-            j -= per_tok;
-            ++t;
-        }
-    }
-};
+__device__ __forceinline__ void put(__nv_bfloat16* p, int o1, int o2, const Raw<__nv_bfloat16>& r) {
+    *reinterpret_cast<uint4*>(p + o1) = r.a;
+    *reinterpret_cast<uint4*>(p + o2) = r.z;
+}
+__device__ __forceinline__ void put(float* p, int o1, int o2, const Raw<float>& r) {
+    reinterpret_cast<float4*>(p + o1)[0] = r.a0;
+    reinterpret_cast<float4*>(p + o1)[1] = r.a1;
+    reinterpret_cast<float4*>(p + o2)[0] = r.z0;
+    reinterpret_cast<float4*>(p + o2)[1] = r.z1;
+}
 
 template <typename T, int D, bool kE5M2>
-__global__ void __launch_bounds__(kNrThreads) k_norm_rope(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kNrThreads, 6) k_norm_rope(const __grid_constant__ NormRopeParams p) {
     constexpr int kLanes = D / 16;                  // lanes of a row
-    constexpr int kRows = kNrThreads / kLanes;      // rows side by side
-    constexpr int kDeep = sizeof(T) == 2 ? 4 : 2;   // rows of a thread whose loads are in flight at once
+    constexpr int kDeep = sizeof(T) == 2 ? 3 : 2;   // rows of a thread whose loads are in flight at once
     __shared__ __align__(16) float s_cos[kNrMaxTok * D / 2], s_sin[kNrMaxTok * D / 2];
 
+    // p.groups lane groups share a token; group g of it takes the heads g, g + groups, ... of q, and
+    // likewise of k and v together
     const int tid = threadIdx.x, c = tid % kLanes, half = p.rd / 2;
-    const int t0 = blockIdx.x * p.per_cta, nt = min(p.per_cta, p.tokens - t0);
+    const int per_cta = kNrThreads / kLanes / p.groups;
+    const int t0 = blockIdx.x * per_cta, nt = min(per_cta, p.tokens - t0);
+    const int t = tid / kLanes / p.groups, g = tid / kLanes % p.groups;
+    const int64_t tok = t0 + t;
+    const int pos = t < nt ? __ldg(p.positions + tok) : -1;
     const bool cache = p.c.k != nullptr;
-    const int per_tok = p.nq + p.c.H * (cache ? 2 : 1);
+    const int H = p.c.H, n_kv = cache ? 2 * H : H;
+    const int q_slots = (p.nq + p.groups - 1) / p.groups, slots = q_slots + (n_kv + p.groups - 1) / p.groups;
     const bool turns = c < p.rd / 16;
     const int o1 = turns ? 8 * c : p.rd + 16 * (c - p.rd / 16);
     const int o2 = turns ? half + 8 * c : o1 + 8;
+    const T* q = static_cast<const T*>(p.q) + tok * p.q_tok;
+    const T* k = static_cast<const T*>(p.k) + tok * p.k_tok;
+    const T* v = static_cast<const T*>(p.v) + tok * p.v_tok;
 
-    Row at{0, 0};
-    at.step(tid / kLanes, per_tok);
-    bool first = true;
-    // the loop bound is uniform in the CTA, so every lane takes part in the shuffles
-    for (int r0 = 0; r0 < nt * per_tok; r0 += kRows * kDeep) {
+    // where the token's rows go in the cache: asked for early, needed late
+    int seq = -1, row = 0;
+    if (cache && pos >= 0) {
+        seq = __ldg(p.seq + tok);
+        row = __ldg(p.index + tok);
+    }
+    float cs[8], sn[8];
+    int page = -1;
+    for (int s0 = 0; s0 < slots; s0 += kDeep) {       // uniform: every lane takes part in the shuffles
         Raw<T> raw[kDeep];
-        Row rows[kDeep];
-        int pos[kDeep];
 #pragma unroll
         for (int i = 0; i < kDeep; ++i) {
-            rows[i] = at;
-            at.step(kRows, per_tok);
-            pos[i] = rows[i].t < nt ? __ldg(p.positions + t0 + rows[i].t) : -1;
-        }
-#pragma unroll
-        for (int i = 0; i < kDeep; ++i) {
-            const int tok = t0 + rows[i].t, j = rows[i].j;
-            const T* src = j < p.nq ? static_cast<const T*>(p.q) + tok * p.q_tok + j * p.q_head
-                           : j < p.nq + p.c.H ? static_cast<const T*>(p.k) + tok * p.k_tok + (j - p.nq) * p.k_head
-                                              : static_cast<const T*>(p.v) + tok * p.v_tok + (j - p.nq - p.c.H) * p.v_head;
             raw[i] = Raw<T>{};
-            if (pos[i] >= 0) fetch(raw[i], src, o1, o2);
+            const int s = s0 + i;
+            if (s < q_slots) {
+                const int h = s * p.groups + g;
+                if (pos >= 0 && h < p.nq) fetch(raw[i], q + h * p.q_head, o1, o2);
+            } else if (s < slots) {
+                const int h = (s - q_slots) * p.groups + g;
+                if (pos >= 0 && h < n_kv) fetch(raw[i], h < H ? k + h * p.k_head : v + (h - H) * p.v_head, o1, o2);
+            }
         }
-        if (first) {       // the angles, while the first rows are on their way
-            first = false;
+        if (s0 == 0) {     // the angles, while the first rows are on their way
             for (int i = tid; i < nt * half; i += kNrThreads) {
-                const int t = i / half, f = i % half;
-                const uint64_t turned = static_cast<uint64_t>(static_cast<int64_t>(__ldg(p.positions + t0 + t))) * p.turn[f];
-                float sn, cs;
-                sincospif(static_cast<float>(static_cast<int32_t>(turned >> 32)) * 0x1p-31f, &sn, &cs);
-                s_cos[t * (D / 2) + f] = cs;
-                s_sin[t * (D / 2) + f] = sn;
+                const int a = i / half, f = i % half;
+                const uint64_t turned = static_cast<uint64_t>(static_cast<int64_t>(__ldg(p.positions + t0 + a))) * p.turn[f];
+                float y, x;
+                sincospif(static_cast<float>(static_cast<int32_t>(turned >> 32)) * 0x1p-31f, &y, &x);
+                s_cos[a * (D / 2) + f] = x;
+                s_sin[a * (D / 2) + f] = y;
+            }
+            if (seq >= 0) {
+                if (seq >= p.c.batch || row < 0 || row >= p.c.cap) set_err(g_err, DEV_ERR_BOUNDS, 701);
+                else page = page_of(p.c, seq, row, g_err, 702);
             }
             __syncthreads();
+            if (turns) {
+                load8(s_cos + t * (D / 2) + 8 * c, cs);
+                load8(s_sin + t * (D / 2) + 8 * c, sn);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
+            }
         }
 #pragma unroll
         for (int i = 0; i < kDeep; ++i) {
-            const int t = rows[i].t, tok = t0 + t, j = rows[i].j;
-            const bool is_q = j < p.nq, is_k = !is_q && j < p.nq + p.c.H;
+            const int s = s0 + i;
+            if (s >= slots) break;
+            const bool is_q = s < q_slots;
+            const int h = (is_q ? s : s - q_slots) * p.groups + g;
+            const bool is_v = !is_q && h >= H, live = pos >= 0 && h < (is_q ? p.nq : n_kv);
             float a[8], z[8];
             widen(raw[i], a, z);
-            float ss = 0.f;
+            const T* w = static_cast<const T*>(is_q ? p.qw : p.kw);
+            if (w) {       // uniform
+                float ss = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(z[e], z[e], ss));
+                for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(z[e], z[e], ss));
 #pragma unroll
-            for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (pos[i] < 0) continue;
-            const T* w = static_cast<const T*>(is_q ? p.qw : is_k ? p.kw : nullptr);
-            if (w) {
+                for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                 const float rs = rsqrtf(ss * (1.f / D) + p.eps);
                 Raw<T> wr;
                 float wa[8], wz[8];
@@ -137,62 +156,49 @@ __global__ void __launch_bounds__(kNrThreads) k_norm_rope(const __grid_constant_
                     z[e] *= rs * wz[e];
                 }
             }
-            if (turns && (is_q || is_k)) {
-                const float* cs = s_cos + t * (D / 2) + 8 * c;
-                const float* sn = s_sin + t * (D / 2) + 8 * c;
-                float cv[8], sv[8];
-                load8(cs, cv);
-                load8(sn, sv);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float x = a[e], y = z[e];
-                    a[e] = fmaf(x, cv[e], -(y * sv[e]));
-                    z[e] = fmaf(y, cv[e], x * sv[e]);
-                }
+            for (int e = 0; e < 8; ++e) {
+                const float x = a[e], y = z[e];
+                a[e] = fmaf(x, cs[e], -(y * sn[e]));
+                z[e] = fmaf(y, cs[e], x * sn[e]);
             }
+            if (!live) continue;
             if (is_q) {
-                T* dst = static_cast<T*>(p.qo) + tok * p.qo_tok + j * p.qo_head;
+                T* dst = static_cast<T*>(p.qo) + tok * p.qo_tok + h * p.qo_head;
                 store8(dst + o1, a);
                 store8(dst + o2, z);
                 continue;
             }
-            const int h = is_k ? j - p.nq : j - p.nq - p.c.H;
-            if (is_k && p.ko) {
-                T* dst = static_cast<T*>(p.ko) + tok * p.ko_tok + h * p.ko_head;
-                store8(dst + o1, a);
-                store8(dst + o2, z);
-            }
-            if (!cache) continue;
-            const int sq = __ldg(p.seq + tok), row = __ldg(p.index + tok);
-            if (sq < 0) continue;
-            if (sq >= p.c.batch || row < 0 || row >= p.c.cap) {
-                set_err(g_err, DEV_ERR_BOUNDS, 701);
-                continue;
-            }
-            const int page = page_of(p.c, sq, row, g_err, 702);
-            if (page < 0) continue;
             const int off = row & ((1 << p.c.lg) - 1);
-            if (is_k) {
+            if (!is_v) {
+                if (p.ko) {
+                    T* dst = static_cast<T*>(p.ko) + tok * p.ko_tok + h * p.ko_head;
+                    store8(dst + o1, a);
+                    store8(dst + o2, z);
+                }
+                if (page < 0) continue;
                 T* dst = static_cast<T*>(p.c.k) + page * p.c.k_page + h * p.c.k_head + off * p.c.k_row;
                 store8(dst + o1, a);
                 store8(dst + o2, z);
-                const int64_t held = (static_cast<int64_t>(sq) * p.c.H + h) * p.row_pitch + row;
-                if (c == 0 && p.row_position) p.row_position[held] = pos[i];
+                const int64_t held = (static_cast<int64_t>(seq) * H + h) * p.row_pitch + row;
+                if (c == 0 && p.row_position) p.row_position[held] = pos;
                 if (c == 0 && p.row_weight) p.row_weight[held] = 0.f;
-            } else if (kE5M2) {
-                uint8_t* dst = static_cast<uint8_t*>(p.c.v) + page * p.c.v_page + h * p.c.v_head + off * p.c.v_row;
-                uint32_t wd[4] = {0, 0, 0, 0};
+            } else if (page >= 0) {
+                const int64_t at = page * p.c.v_page + (h - H) * p.c.v_head + off * p.c.v_row;
+                if (kE5M2) {
+                    uint8_t* dst = static_cast<uint8_t*>(p.c.v) + at;
+                    widen(raw[i], a, z);
+                    uint32_t wd[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    wd[e / 4] |= static_cast<uint32_t>(from_f<__nv_fp8_e5m2>(a[e]).__x) << (8 * (e % 4));
-                    wd[2 + e / 4] |= static_cast<uint32_t>(from_f<__nv_fp8_e5m2>(z[e]).__x) << (8 * (e % 4));
+                    for (int e = 0; e < 8; ++e) {
+                        wd[e / 4] |= static_cast<uint32_t>(from_f<__nv_fp8_e5m2>(a[e]).__x) << (8 * (e % 4));
+                        wd[2 + e / 4] |= static_cast<uint32_t>(from_f<__nv_fp8_e5m2>(z[e]).__x) << (8 * (e % 4));
+                    }
+                    *reinterpret_cast<uint2*>(dst + o1) = make_uint2(wd[0], wd[1]);
+                    *reinterpret_cast<uint2*>(dst + o2) = make_uint2(wd[2], wd[3]);
+                } else {
+                    put(static_cast<T*>(p.c.v) + at, o1, o2, raw[i]);
                 }
-                *reinterpret_cast<uint2*>(dst + o1) = make_uint2(wd[0], wd[1]);
-                *reinterpret_cast<uint2*>(dst + o2) = make_uint2(wd[2], wd[3]);
-            } else {
-                T* dst = static_cast<T*>(p.c.v) + page * p.c.v_page + h * p.c.v_head + off * p.c.v_row;
-                store8(dst + o1, a);
-                store8(dst + o2, z);
             }
         }
     }
@@ -200,14 +206,21 @@ __global__ void __launch_bounds__(kNrThreads) k_norm_rope(const __grid_constant_
 
 template <typename T, int D, bool kE5M2>
 static int launch_nr(NormRopeParams p, int nsm, cudaStream_t s) {
-    const int per_tok = p.nq + p.c.H * (p.c.k ? 2 : 1);
     constexpr int kRows = kNrThreads / (D / 16);
-    // one token per CTA while that leaves SMs idle (a decode step), else enough for four rows per
-    // lane group, whose loads then overlap
-    int per = 1;
-    if (p.tokens > 4 * nsm) per = (4 * kRows + per_tok / 2) / per_tok;
-    p.per_cta = per < 1 ? 1 : per > kNrMaxTok ? kNrMaxTok : per;
-    const int grid = (p.tokens + p.per_cta - 1) / p.per_cta;
+    const int n_kv = p.c.H * (p.c.k ? 2 : 1);
+    // lane groups per token.  A decode step has few tokens: all of a CTA's groups work on one.  A
+    // prompt takes the number that leaves the fewest groups without a head, and of equals the
+    // smallest from four on (each thread then has more rows of a token whose angles it holds).
+    p.groups = kRows;
+    if (p.tokens > 2 * nsm) {
+        int best = 1 << 30;
+        for (int g = kRows; g >= 1; g /= 2) {
+            if (kRows / g > kNrMaxTok) break;
+            const int spent = ((p.nq + g - 1) / g + (n_kv + g - 1) / g) * g;
+            if (spent < best || (spent == best && g >= 4)) best = spent, p.groups = g;
+        }
+    }
+    const int per = kRows / p.groups, grid = (p.tokens + per - 1) / per;
     k_norm_rope<T, D, kE5M2><<<grid, kNrThreads, 0, s>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

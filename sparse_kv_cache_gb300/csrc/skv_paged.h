@@ -23,7 +23,7 @@ struct PagedView {
 struct NormRopeParams {
     PagedView c;
     int tokens, nq, rd;
-    int per_cta;              // tokens per CTA
+    int groups;               // lane groups per token (set by the launcher)
     float eps;
     int64_t q_tok, q_head, k_tok, k_head, v_tok, v_head, qo_tok, qo_head, ko_tok, ko_head;
     const void *q, *k, *v, *qw, *kw;
