@@ -539,7 +539,7 @@ typedef struct {
     float scale;                /* 0: 1 / sqrt(head_dim) */
     int64_t q_seq, q_head, out_seq, out_head;   /* strides, elements */
     const void* q;              /* dev [batch][n_q_heads][d] */
-    void* out;                  /* dev [batch][n_q_heads][d] */
+    void* out;                  /* dev [batch][n_q_heads][d]; q and out 16-byte aligned, strides of whole 16 bytes */
     float* lse;                 /* dev [batch][n_q_heads], or NULL */
     const float* weight;        /* dev [batch][n_kv_heads][row_pitch]; with weight_out */
     float* weight_out;          /* dev, the same shape, or NULL */

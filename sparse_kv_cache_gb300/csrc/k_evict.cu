@@ -10,9 +10,9 @@
 // counts in shared memory, so the order of the atomics does not show) and writes both lists in
 // ascending row order.  A unit belongs to a cluster of 1 to 8 CTAs, each with a contiguous slice of
 // the rows, each warp with a contiguous part of the slice; counts are joined through distributed
-// shared memory.  The upper halves of a slice's keys stay in shared memory, so the weights are read
-// once and again only for rows whose upper half equals the threshold's.  k_evict_move, a
-// programmatic dependent, copies the rows.
+// shared memory.  The upper halves of a slice's keys stay in shared memory, and the lower ones too
+// where there is room; else the weights are read again for lanes that hold a row whose upper half
+// equals the threshold's.  k_evict_move, a programmatic dependent, copies the rows.
 #include "skv_common.cuh"
 #include "skv_internal.h"
 #include "skv_paged.h"
@@ -66,10 +66,11 @@ __device__ __forceinline__ int excl_scan(int x, int lane) {
 }
 
 __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_constant__ EvictParams p, int ranks,
-                                                                 int key_cap) {
+                                                                 int key_cap, int low_cap) {
     extern __shared__ __align__(16) int sm[];
     int* s_hist = sm;                                                  // [kEvHist]
     uint16_t* s_key = reinterpret_cast<uint16_t*>(sm + kEvHist);      // [key_cap] upper halves of the keys
+    uint16_t* s_low = s_key + key_cap;                                 // [low_cap] lower halves
     __shared__ int s_scan[kEvWarps], s_bin[3], s_maxes[kEvWarps], s_max;
     __shared__ int s_cnt[4][kEvWarps], s_tot[4];
     __shared__ int s_tie[kEvWarps], s_hole[kEvWarps], s_src[kEvWarps];
@@ -126,30 +127,46 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
         if (r != rank) last = max(last, ld_cluster_s32(cluster_addr(&s_max, r)));
     const int64_t safe_from = static_cast<int64_t>(last) - p.recent;
 
-    const bool held = per * kEvWarps <= key_cap;
-    uint16_t* my = s_key + warp * per;
+    const bool held = per * kEvWarps <= key_cap, held_low = per * kEvWarps <= low_cap;
+    uint16_t *my = s_key + warp * per, *my_low = s_low + warp * per;
     auto key_of = [&](float w, int pos) -> uint32_t {
         return (pos > safe_from || pos < p.sink) ? 0xFFFFFFFFu : weight_key(w);
     };
-    auto full = [&](int i) -> uint32_t { return key_of(__ldg(w_in + i), __ldg(p_in + i)); };
-    // upper halves of the lane's eight keys from row s on
+    // the lane's eight keys from row s on
     auto make = [&](int s, uint32_t (&t)[8]) {
         float w[8];
         int pos[8];
         load_rows<float>(w_in, s, hi, vec, 0.f, w);
         load_rows<int>(p_in, s, hi, vec, 0, pos);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] = key_of(w[e], pos[e]) >> 16;
+        for (int e = 0; e < 8; ++e) t[e] = key_of(w[e], pos[e]);
     };
+    auto pick = [](const uint16_t* from, uint32_t (&t)[8]) {
+        const uint4 v = *reinterpret_cast<const uint4*>(from);
+        t[0] = v.x & 0xFFFF; t[1] = v.x >> 16; t[2] = v.y & 0xFFFF; t[3] = v.y >> 16;
+        t[4] = v.z & 0xFFFF; t[5] = v.z >> 16; t[6] = v.w & 0xFFFF; t[7] = v.w >> 16;
+    };
+    // their upper halves, and their lower ones
     auto upper = [&](int s, uint32_t (&t)[8]) {
         if (held) {
-            const uint4 v = *reinterpret_cast<const uint4*>(my + (s - lo));
-            t[0] = v.x & 0xFFFF; t[1] = v.x >> 16; t[2] = v.y & 0xFFFF; t[3] = v.y >> 16;
-            t[4] = v.z & 0xFFFF; t[5] = v.z >> 16; t[6] = v.w & 0xFFFF; t[7] = v.w >> 16;
+            pick(my + (s - lo), t);
         } else {
             make(s, t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] >>= 16;
         }
     };
+    auto lower = [&](int s, uint32_t (&t)[8]) {
+        if (held_low) {
+            pick(my_low + (s - lo), t);
+        } else {
+            make(s, t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] &= 0xFFFF;
+        }
+    };
+    // of the eight rows from s on: bits of those below x
+    auto bits_below = [](int s, int x) -> uint32_t { return x <= s ? 0u : x - s >= 8 ? 0xFFu : (1u << (x - s)) - 1; };
 
     // ---- the M-th largest key, from the top; bits 31..21, 20..16, 15..5, 4..0
     uint32_t prefix = 0, T = 0;
@@ -161,27 +178,38 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
         int* hist = s_hist + (pass == 0 ? 0 : pass == 1 ? 2 * kEvBins : pass == 2 ? kEvBins : 2 * kEvBins + 32);
         for (int r0 = lo; r0 < hi; r0 += kEvStep) {
             const int s = r0 + 8 * lane;
+            const uint32_t in = bits_below(s, hi);
             uint32_t t[8];
             if (pass == 0) {
                 make(s, t);
+                auto pair = [&](int e, int sh) { return ((t[e] >> sh) & 0xFFFF) | ((t[e + 1] >> sh) << 16); };
                 if (held)
-                    *reinterpret_cast<uint4*>(my + (s - lo)) =
-                        make_uint4(t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, t[6] | t[7] << 16);
-            } else {
-                upper(s, t);
+                    *reinterpret_cast<uint4*>(my + (s - lo)) = make_uint4(pair(0, 16), pair(2, 16), pair(4, 16), pair(6, 16));
+                if (held_low)
+                    *reinterpret_cast<uint4*>(my_low + (s - lo)) = make_uint4(pair(0, 0), pair(2, 0), pair(4, 0), pair(6, 0));
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if ((in >> e) & 1) atomicAdd(hist + (t[e] >> 21), 1);
+                continue;
             }
+            upper(s, t);
+            if (pass == 1) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if ((in >> e) & 1 && (t[e] >> 5) == prefix) atomicAdd(hist + (t[e] & 31), 1);
+                continue;
+            }
+            uint32_t same = 0, l[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) same |= (t[e] == (pass == 2 ? prefix : prefix >> 11) ? 1u : 0u) << e;
+            same &= in;
+            if (!same) continue;
+            lower(s, l);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (s + e >= hi) continue;
-                if (pass == 0) {
-                    atomicAdd(hist + (t[e] >> 5), 1);
-                } else if (pass == 1) {
-                    if ((t[e] >> 5) == prefix) atomicAdd(hist + (t[e] & 31), 1);
-                } else if (t[e] == (pass == 2 ? prefix : prefix >> 11)) {
-                    const uint32_t k = full(s + e);
-                    if (pass == 2) atomicAdd(hist + ((k >> 5) & (kEvBins - 1)), 1);
-                    else if ((k >> 5) == prefix) atomicAdd(hist + (k & 31), 1);
-                }
+                if (!((same >> e) & 1)) continue;
+                if (pass == 2) atomicAdd(hist + (l[e] >> 5), 1);
+                else if ((l[e] >> 5) == (prefix & (kEvBins - 1))) atomicAdd(hist + (l[e] & 31), 1);
             }
         }
         sync_all(ranks);
@@ -231,23 +259,26 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
     const bool upper_alone = whole && (T & 0xFFFFu) == 0xFFFFu;     // no key of upper half T16 stays
     // which of the lane's eight rows from s on lie above the threshold, and which on it
     auto grade = [&](int s, uint32_t& gt, uint32_t& tie) {
-        uint32_t t[8];
+        uint32_t t[8], l[8], same = 0;
         upper(s, t);
         gt = tie = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (s + e >= hi || t[e] < T16) continue;
-            if (t[e] > T16) {
-                gt |= 1u << e;
-            } else if (!upper_alone) {
-                const uint32_t k = full(s + e);
-                if (k > T) gt |= 1u << e;
-                else if (k == T && !whole) tie |= 1u << e;
-            }
+            gt |= (t[e] > T16 ? 1u : 0u) << e;
+            same |= (t[e] == T16 ? 1u : 0u) << e;
+        }
+        const uint32_t in = bits_below(s, hi);
+        gt &= in;
+        same &= in;
+        if (!same || upper_alone) return;
+        lower(s, l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (!((same >> e) & 1)) continue;
+            if (l[e] > (T & 0xFFFFu)) gt |= 1u << e;
+            else if (l[e] == (T & 0xFFFFu) && !whole) tie |= 1u << e;
         }
     };
-    // of the eight rows from s on: bits of those below x
-    auto bits_below = [](int s, int x) -> uint32_t { return x <= s ? 0u : x - s >= 8 ? 0xFFu : (1u << (x - s)) - 1; };
 
     // ---- rows of each kind per warp: given up and tied below M, kept for sure and tied behind
     int n_low = 0, n_tl = 0, n_gt = 0, n_th = 0;
@@ -348,7 +379,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
 }
 
 constexpr int kMvThreads = 256;
-constexpr int kMvPairs = 8;        // rows per warp and round
+constexpr int kMvPairs = 4;        // rows per warp and round
 
 __global__ void __launch_bounds__(kMvThreads) k_evict_move(const __grid_constant__ EvictParams p, int parts) {
     pdl_wait();
@@ -407,7 +438,8 @@ int launch_evict(const EvictParams& p, int nsm, cudaStream_t s) {
     const int64_t slice = (static_cast<int64_t>(p.c.cap) + ranks - 1) / ranks;
     const int64_t keys = (slice + kEvGrain - 1) / kEvGrain * kEvGrain;
     const int key_cap = static_cast<int>(keys < kEvKeys ? keys : kEvKeys);
-    const int smem = kEvHist * 4 + key_cap * 2;
+    const int low_cap = 2 * key_cap <= kEvKeys ? key_cap : 0;
+    const int smem = kEvHist * 4 + (key_cap + low_cap) * 2;
     if (cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvHist * 4 + kEvKeys * 2) !=
         cudaSuccess)
         return -1;
@@ -422,7 +454,7 @@ int launch_evict(const EvictParams& p, int nsm, cudaStream_t s) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = ranks > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, k_evict_select, p, ranks, key_cap) != cudaSuccess) return -1;
+    if (cudaLaunchKernelEx(&cfg, k_evict_select, p, ranks, key_cap, low_cap) != cudaSuccess) return -1;
     // CTAs per unit for the rows that move
     const int rows = (kMvThreads / 32) * kMvPairs;
     int64_t parts = (static_cast<int64_t>(p.list_cap) + rows - 1) / rows;

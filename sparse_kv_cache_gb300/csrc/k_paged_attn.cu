@@ -4,21 +4,22 @@
 // pass over the unit's rows with a running base and sum of the softmax.  Each cached byte is read
 // once and takes part in G products per element, 2G flops per byte in bf16, so memory bounds it.
 //
-// Work split.  The rows of all units form one sequence of 64-row blocks; CTA i of n takes the
-// blocks [i T / n, (i + 1) T / n), whatever units they belong to, so every SM gets the same
-// share of any mix of lengths and the host need not know them (a captured graph replays with new
-// lengths).  A unit that lies in one CTA's range is finished there; the shares of the others go
-// to the CTA's two records (its first and its last unit), and k_paged_merge, a programmatic
-// dependent, joins them in order.
+// Work split.  The rows of all units form one sequence of 16-row tiles; CTA i of n takes the tiles
+// [i T / n, (i + 1) T / n), whatever units they belong to, and each of its four warps a quarter of
+// them.  So every SM gets the same share of any mix of lengths, and the host need not know them (a
+// captured graph replays with new lengths).  Warps work on their own, with no barrier between
+// them, and finish the units that lie in their quarter whole.  The other shares are joined twice, each
+// time in order: those of a CTA's warps through shared memory, and those of several CTAs by
+// k_paged_merge, a programmatic dependent, from the CTAs' two records (of their first and last unit).
 //
-// bf16 and e5m2: the four warps of a CTA take 16 rows each at a time, with no shared memory in
-// the loop.  S^T = K.Q^T has the rows in the 16-wide dimension of m16n8k16 and the heads in the
-// 8-wide one, so up to eight heads waste nothing; its operands come straight from 16-byte global
-// loads, because a dot product may take its terms in any order as long as both operands agree.
-// O^T = V^T.P^T takes pairs of rows interleaved by byte permutes, again from 16-byte loads, and
-// P^T is S^T's accumulator passed through movmatrix.  The tensor cores are busy for less than a
-// tenth of the time that the loads take, so the warp-level instruction suffices: tcgen05 would
-// put both operands and the accumulator through shared and tensor memory first.
+// bf16 and e5m2: no shared memory in the loop.  S^T = K.Q^T has the rows in the 16-wide dimension
+// of m16n8k16 and the heads in the 8-wide one, so up to eight heads waste nothing; its operands
+// come straight from 16-byte global loads, because a dot product may take its terms in any order
+// as long as both operands agree.  O^T = V^T.P^T takes pairs of rows interleaved by byte
+// permutes, again from 16-byte loads, and P^T is S^T's accumulator passed through movmatrix.  The
+// tensor cores are busy for less than a tenth of the time that the loads take, so the warp-level
+// instruction suffices: tcgen05 would put both operands and the accumulator through shared and
+// tensor memory first.
 //
 // fp32 takes the same split with products on the CUDA cores: a half-warp per row, four rows'
 // sums joined by a transposing reduction.
@@ -33,10 +34,8 @@ namespace skv {
 static __device__ int g_err[2];
 
 constexpr int kPaThreads = 128;
-constexpr int kPaWarps = kPaThreads / 32;
+static_assert(kPaThreads == 32 * kPaWarps, "");
 constexpr int kPaTile = 16;                       // rows of a warp's step
-constexpr int kPaBlock = kPaTile * kPaWarps;      // rows of a CTA's step
-constexpr int kPaHeads = 8;                       // heads of an accumulator
 constexpr float kPaSlack = 8.f;                   // the base moves when a score passes it by 2^8
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -89,28 +88,32 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 
 
 // ------------------------------------------------------------------ the split of the work
 
-__device__ __forceinline__ int blocks_of(int n) { return (n + kPaBlock - 1) / kPaBlock; }
+__device__ __forceinline__ int tiles_of(int n) { return (n + kPaTile - 1) / kPaTile; }
 
-// Where block x of the launch lies: its sequence, KV head, and block of the unit.
-struct Place {
-    int64_t total;    // blocks of all units
-    int64_t n;        // CTAs that have work
-    int64_t first;    // first block of the sequence in the launch
-    int b, rows, nb;  // sequence, its rows, blocks per unit of it
-};
+// What CTA `me` of `ctas` takes, and where its W parts begin.
+template <int W>
 struct PlanSmem {
     int64_t warp_sum[kPaWarps];
-    int64_t first;
-    int b, rows;
+    int64_t at[W];       // first tile of the sequence that part starts in
+    int b[W], rows[W];   // that sequence and its rows
+};
+template <int W>
+struct Plan {
+    int64_t total, n;    // tiles of all units; CTAs that have work
+    int64_t lo, hi;      // tiles of this CTA (lo == hi: none)
+    __device__ __forceinline__ int64_t start(int64_t i) const { return i * total / n; }
+    __device__ __forceinline__ int64_t holder(int64_t x) const { return ((x + 1) * n - 1) / total; }   // of tile x
+    __device__ __forceinline__ int64_t part(int w) const { return lo + w * (hi - lo) / W; }
 };
 
-// Every thread sums a run of sequences; the thread whose run holds CTA i's first block finds it.
-__device__ __forceinline__ Place plan(const PagedView& c, int64_t i, int64_t ctas, PlanSmem& sm) {
+// Every thread sums a run of sequences; the thread whose run holds a part's first tile finds it.
+template <int W>
+__device__ __forceinline__ Plan<W> make_plan(const PagedView& c, int64_t me, int64_t ctas, PlanSmem<W>& sm) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (c.batch + kPaThreads - 1) / kPaThreads;
     const int s0 = min(tid * per, c.batch), s1 = min(s0 + per, c.batch);
     int64_t mine = 0;
-    for (int s = s0; s < s1; ++s) mine += blocks_of(rows_of(c, s, g_err, 711));
+    for (int s = s0; s < s1; ++s) mine += tiles_of(rows_of(c, s, g_err, 711));
     int64_t run = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -125,57 +128,113 @@ __device__ __forceinline__ Place plan(const PagedView& c, int64_t i, int64_t cta
         if (w < warp) before += sm.warp_sum[w];
         all += sm.warp_sum[w];
     }
-    Place pl;
+    Plan<W> pl;
     pl.total = all * c.H;
     pl.n = min(ctas, pl.total);
-    int64_t at = (before + run - mine) * c.H;
-    if (i < pl.n) {
-        const int64_t x = i * pl.total / pl.n;
-        if (x >= at && x < at + mine * c.H) {
-            for (int s = s0; s < s1; ++s) {
-                const int rows = rows_of(c, s, g_err, 711);
-                const int64_t size = static_cast<int64_t>(blocks_of(rows)) * c.H;
-                if (x < at + size) {
-                    sm.first = at;
-                    sm.b = s;
-                    sm.rows = rows;
-                    break;
-                }
-                at += size;
+    pl.lo = me < pl.n ? pl.start(me) : 0;
+    pl.hi = me < pl.n ? pl.start(me + 1) : 0;
+    const int64_t begin = (before + run - mine) * c.H, stop = begin + mine * c.H;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        const int64_t x = pl.part(w);
+        if (pl.lo == pl.hi || x < begin || x >= stop) continue;
+        int64_t at = begin;
+        for (int s = s0; s < s1; ++s) {
+            const int rows = rows_of(c, s, g_err, 711);
+            const int64_t size = static_cast<int64_t>(tiles_of(rows)) * c.H;
+            if (x < at + size) {
+                sm.at[w] = at;
+                sm.b[w] = s;
+                sm.rows[w] = rows;
+                break;
             }
+            at += size;
         }
     }
     __syncthreads();
-    pl.first = sm.first;
-    pl.b = sm.b;
-    pl.rows = sm.rows;
-    pl.nb = i < pl.n ? blocks_of(pl.rows) : 1;
     return pl;
 }
 
-// The next sequence after b that has rows.
-__device__ __forceinline__ void next_rows(const PagedView& c, int& b, int& rows) {
-    do rows = ++b < c.batch ? rows_of(c, b, g_err, 711) : -1;
-    while (rows == 0);
-}
+// A part's way through the units: its current unit, and the unit's first tile in the launch.
+struct Walk {
+    int b, h, rows, nt;
+    int64_t unit0;
+    __device__ __forceinline__ void enter(int seq, int n, int64_t at, int64_t x) {
+        b = seq;
+        rows = n;
+        nt = tiles_of(n);
+        h = static_cast<int>((x - at) / nt);
+        unit0 = at + static_cast<int64_t>(h) * nt;
+    }
+    // the next unit that has rows; false if there is none (the lengths changed under the call)
+    __device__ __forceinline__ bool next(const PagedView& c) {
+        unit0 += nt;
+        if (++h < c.H) return true;
+        h = 0;
+        const int lane = threadIdx.x & 31;
+        for (int s = b + 1; s < c.batch; s += 32) {
+            const int n = s + lane < c.batch ? rows_of(c, s + lane, g_err, 711) : 0;
+            const uint32_t some = __ballot_sync(0xffffffffu, n > 0);
+            if (!some) continue;
+            const int at = __ffs(some) - 1;
+            b = s + at;
+            rows = __shfl_sync(0xffffffffu, n, at);
+            nt = tiles_of(rows);
+            return true;
+        }
+        return false;
+    }
+};
 
 // ------------------------------------------------------------------ a warp's share of a unit
 
-// What the four warps hand to the join: O [warp][head][d] unnormalised, base and sum per head.
-// Heads lie in two planes by parity with a pitch of d + 2, so that the accumulators' pairs of
-// dimensions go to distinct banks.
-template <int D>
+__device__ __forceinline__ void store_out(const PagedAttnParams& p, bool f32, int b, int h, int g, int dim, float x) {
+    const int64_t at = b * p.o_seq + (h * p.G + g) * p.o_head + dim;
+    if (f32) static_cast<float*>(p.out)[at] = x;
+    else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
+}
+// base + log2(sum) as a natural logarithm; -inf for a unit of no rows
+__device__ __forceinline__ float ln_of(float m, float l) { return l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.693147180559945309f; }
+
+// four consecutive dimensions of a head
+template <bool kF32>
+__device__ __forceinline__ void store4(const PagedAttnParams& p, int b, int h, int g, int dim, const float (&x)[4]) {
+    const int64_t at = b * p.o_seq + (h * p.G + g) * p.o_head + dim;
+    if (kF32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+            make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+}
+
+// What goes with head g of a unit beside its output.
+__device__ __forceinline__ void note(const PagedAttnParams& p, int b, int h, int g, float m, float l) {
+    if (p.lse) p.lse[static_cast<int64_t>(b) * p.n_q + h * p.G + g] = ln_of(m, l);
+    if (p.stat) p.stat[(static_cast<int64_t>(b) * p.c.H + h) * p.G + g] = make_float2(m, l == 0.f ? 0.f : 1.f / l);
+}
+
+// The shares that a CTA's warps leave for the join: two per warp, of its first and its last unit.
+// O is not normalised; heads lie d + 4 apart, so that the lanes' 16-byte writes spread over the banks.
+// b < 0: none; whether it holds the unit's first and last tile, and the CTA's first
+struct ShareOf { int b, h; bool begins, ends, first; };
+struct Run { int b, h, from, last; bool whole, first; };      // consecutive shares of one unit
+template <int D, int G>
 struct JoinSmem {
-    float o[kPaWarps][2][kPaHeads / 2][D + 2];
-    float m[kPaWarps][kPaHeads], l[kPaWarps][kPaHeads];
+    float o[2 * kPaWarps][G][D + 4];
+    float m[2 * kPaWarps][G], l[2 * kPaWarps][G], w[2 * kPaWarps][G];
+    ShareOf of[2 * kPaWarps];
+    Run run[2 * kPaWarps];
+    int runs;
 };
+// weight of a share of base x and sum l against the base m of all
+__device__ __forceinline__ float share_weight(float x, float l, float m) {
+    return x == -CUDART_INF_F && !(l != l) ? 0.f : exp2_fast(x - m);
+}
 
 // Page ids of a warp's coming tiles: lane j holds those of tile j of the current 32.
 struct PageIds {
     int a, b;    // of the tile's first and last eight rows
 };
 
-// tile t of the warp covers rows row0 + t * kPaBlock ..+15 of sequence b
 __device__ __forceinline__ PageIds page_ids(const PagedView& c, int b, int row, int end) {
     PageIds id{-1, -1};
     if (row < end) {
@@ -330,61 +389,77 @@ struct TileTC {
             }
         }
     }
-    // first of the two dimensions of accumulator t that lane group r holds
-    __device__ __forceinline__ static int dim_of(int t, int r) {
-        return kE5M2 ? (D / 8) * r + 2 * t : 64 * (t >> 2) + 8 * r + 2 * (t & 3);
-    }
-    __device__ __forceinline__ void hand_over(JoinSmem<D>& js) {
-        const int warp = threadIdx.x >> 5, r = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
+    // The lane's accumulators are runs of consecutive dimensions (accumulator t holds a pair for
+    // each of two heads): two runs of 8 with bf16 values, one of D / 8 with e5m2 ones.
+    static constexpr int kRun = kE5M2 ? D / 8 : 8;
+    // writes the unit's result, or this share of it for the join
+    __device__ __forceinline__ void finish(const PagedAttnParams& p, int b, int h, bool alone, JoinSmem<D, 8>& js, int slot) {
+        const int r = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, x);
             l1 += __shfl_xor_sync(0xffffffffu, l1, x);
         }
-        if (r == 0) {
-            js.m[warp][2 * c] = m0 - kBaseShift;
-            js.m[warp][2 * c + 1] = m1 - kBaseShift;
-            js.l[warp][2 * c] = l0;
-            js.l[warp][2 * c + 1] = l1;
-        }
 #pragma unroll
-        for (int t = 0; t < D / 16; ++t) {
-            *reinterpret_cast<float2*>(&js.o[warp][0][c][dim_of(t, r)]) = make_float2(o[t][0], o[t][2]);
-            *reinterpret_cast<float2*>(&js.o[warp][1][c][dim_of(t, r)]) = make_float2(o[t][1], o[t][3]);
+        for (int e = 0; e < 2; ++e) {
+            const int g = 2 * c + e;
+            if (g >= p.G) continue;
+            const float m = (e ? m1 : m0) - kBaseShift, l = e ? l1 : l0;
+            const float inv = !alone ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + b * p.o_seq + (h * p.G + g) * p.o_head;
+#pragma unroll
+            for (int t = 0; t < D / 16; t += 4) {
+                const int dim = kE5M2 ? kRun * r + 2 * t : 64 * (t / 4) + 8 * r;
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[2 * i] = o[t + i][e] * inv;
+                    x[2 * i + 1] = o[t + i][2 + e] * inv;
+                }
+                if (alone) store8(out + dim, x);
+                else store8(&js.o[slot][g][dim], x);
+            }
+            if (r == 0) {
+                if (alone) {
+                    note(p, b, h, g, m, l);
+                } else {
+                    js.m[slot][g] = m;
+                    js.l[slot][g] = l;
+                }
+            }
         }
     }
-    // rows [row0, end) of the unit, 16 at row0 + t * kPaBlock
+    // rows [row0, end) of the unit
     __device__ __forceinline__ void share(const PagedAttnParams& p, int b, int h, int row0, int end, float* z) {
         const int lane = threadIdx.x & 31;
-        if (row0 >= end) return;
-        PageIds now = page_ids(p.c, b, row0 + lane * kPaBlock, end), next = now;
+        PageIds now = page_ids(p.c, b, row0 + lane * kPaTile, end), next = now;
         int t = 0;
         Keys k;
         Values v;
         int ida = __shfl_sync(0xffffffffu, now.a, 0), idb = __shfl_sync(0xffffffffu, now.b, 0);
         load_k(p, h, row0, end, ida, idb, k);
         load_v(p, h, row0, end, ida, idb, v);
-        if (row0 + 32 * kPaBlock < end) next = page_ids(p.c, b, row0 + (32 + lane) * kPaBlock, end);
-        for (int row = row0; row < end; row += kPaBlock) {
+        if (row0 + 32 * kPaTile < end) next = page_ids(p.c, b, row0 + (32 + lane) * kPaTile, end);
+        for (int row = row0; row < end; row += kPaTile) {
             float s[4];
             scores(k, s);
             const int was_a = ida, was_b = idb;
-            const bool more = row + kPaBlock < end;
+            const bool more = row + kPaTile < end;
             if (more) {
                 if (++t == 32) {
                     t = 0;
                     now = next;
-                    if (row + 33 * kPaBlock < end) next = page_ids(p.c, b, row + (33 + lane) * kPaBlock, end);
+                    if (row + 33 * kPaTile < end) next = page_ids(p.c, b, row + (33 + lane) * kPaTile, end);
                 }
                 ida = __shfl_sync(0xffffffffu, now.a, t);
                 idb = __shfl_sync(0xffffffffu, now.b, t);
-                load_k(p, h, row + kPaBlock, end, ida, idb, k);
+                load_k(p, h, row + kPaTile, end, ida, idb, k);
             }
             if (z) keep(p, z, row, end, was_a, was_b, s);
             uint32_t b0, b1;
             softmax(p.scale_log2, row, end, was_a, was_b, s, b0, b1);
             values(v, b0, b1);
-            if (more) load_v(p, h, row + kPaBlock, end, ida, idb, v);
+            if (more) load_v(p, h, row + kPaTile, end, ida, idb, v);
         }
     }
 };
@@ -395,15 +470,15 @@ struct TileF32 {
     static constexpr int kV = D / 64;      // float4 of a row per lane
     float o[G][4 * kV];
     float m[G], l[G];
-    const float* sq;                       // [G][D] queries in shared memory
+    const float* sq;                       // [G][D + 4] the warp's queries in shared memory
 
     __device__ __forceinline__ void load_q(const PagedAttnParams& p, int b, int h, float* s_q) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < G * D; i += kPaThreads) {
+        __syncwarp();
+        for (int i = threadIdx.x & 31; i < G * D; i += 32) {
             const int g = i / D;
-            s_q[i] = g < p.G ? __ldg(static_cast<const float*>(p.q) + b * p.q_seq + (h * p.G + g) * p.q_head + i % D) : 0.f;
+            s_q[g * (D + 4) + i % D] = g < p.G ? __ldg(static_cast<const float*>(p.q) + b * p.q_seq + (h * p.G + g) * p.q_head + i % D) : 0.f;
         }
-        __syncthreads();
+        __syncwarp();
         sq = s_q;
     }
     __device__ __forceinline__ void reset() {
@@ -438,10 +513,10 @@ struct TileF32 {
         const float* vb = static_cast<const float*>(p.c.v) + h * p.c.v_head;
         PageIds now{-1, -1};
         int t = 32;
-        for (int row = row0; row < end; row += kPaBlock, ++t) {
+        for (int row = row0; row < end; row += kPaTile, ++t) {
             if (t == 32) {
                 t = 0;
-                now = page_ids(p.c, b, row + lane * kPaBlock, end);
+                now = page_ids(p.c, b, row + lane * kPaTile, end);
             }
             const int ida = __shfl_sync(0xffffffffu, now.a, t), idb = __shfl_sync(0xffffffffu, now.b, t);
             const int id = half ? idb : ida, mine = row + 8 * half;      // this half-warp's eight rows
@@ -457,7 +532,7 @@ struct TileF32 {
                 for (int i = 0; i < 8; ++i) a[i] = 0.f;
 #pragma unroll
                 for (int j = 0; j < kV; ++j) {
-                    const float4 qv = *reinterpret_cast<const float4*>(sq + g * D + 64 * j + 4 * hl);
+                    const float4 qv = *reinterpret_cast<const float4*>(sq + g * (D + 4) + 64 * j + 4 * hl);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         a[i] = fmaf(x[i][4 * j], qv.x, a[i]);
@@ -496,19 +571,31 @@ struct TileF32 {
             }
         }
     }
-    __device__ __forceinline__ void hand_over(JoinSmem<D>& js) {
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, hl = lane & 15;
+    __device__ __forceinline__ void finish(const PagedAttnParams& p, int b, int h, bool alone, JoinSmem<D, G>& js, int slot) {
+        const int lane = threadIdx.x & 31, hl = lane & 15;
+        __syncwarp();      // no lane reads the queries any more
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             const float sum = 0.5f * warp_sum(l[g]);
-            if (lane == 0) {
-                js.m[warp][g] = m[g];
-                js.l[warp][g] = sum;
-            }
+            float x[4 * kV];
 #pragma unroll
-            for (int i = 0; i < 4 * kV; ++i) {
-                const float x = o[g][i] + __shfl_xor_sync(0xffffffffu, o[g][i], 16);
-                if (lane < 16) js.o[warp][g & 1][g >> 1][64 * (i / 4) + 4 * hl + i % 4] = x;
+            for (int i = 0; i < 4 * kV; ++i) x[i] = o[g][i] + __shfl_xor_sync(0xffffffffu, o[g][i], 16);
+            if (g >= p.G) continue;
+            const float inv = !alone ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+            float* dst = alone ? static_cast<float*>(p.out) + b * p.o_seq + (h * p.G + g) * p.o_head : js.o[slot][g];
+            if (lane < 16) {
+#pragma unroll
+                for (int i = 0; i < kV; ++i)
+                    *reinterpret_cast<float4*>(dst + 64 * i + 4 * hl) =
+                        make_float4(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
+            }
+            if (lane == 0) {
+                if (alone) {
+                    note(p, b, h, g, m[g], sum);
+                } else {
+                    js.m[slot][g] = m[g];
+                    js.l[slot][g] = sum;
+                }
             }
         }
     }
@@ -516,86 +603,115 @@ struct TileF32 {
 
 // ------------------------------------------------------------------ the kernels
 
-__device__ __forceinline__ void store_out(const PagedAttnParams& p, bool f32, int b, int h, int g, int dim, float x) {
-    const int64_t at = b * p.o_seq + (h * p.G + g) * p.o_head + dim;
-    if (f32) static_cast<float*>(p.out)[at] = x;
-    else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(x);
-}
-// base + log2(sum) as a natural logarithm; -inf for a unit of no rows
-__device__ __forceinline__ float ln_of(float m, float l) { return l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.693147180559945309f; }
-
-template <class Tile, int D, bool kF32, int kOcc>
-__global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_constant__ PagedAttnParams p) {
-    __shared__ PlanSmem s_plan;
-    __shared__ __align__(16) JoinSmem<D> js;
-    __shared__ __align__(16) float s_q[kF32 ? kPaHeads * D : 4];
-    pdl_trigger();
-    const int tid = threadIdx.x, warp = tid >> 5;
-    const int64_t ctas = gridDim.x, me = blockIdx.x;
-    const Place pl = plan(p.c, me, ctas, s_plan);
-
-    const bool work = me < pl.n;
-    const int64_t w0 = work ? me * pl.total / pl.n : 0, w1 = work ? (me + 1) * pl.total / pl.n : 0;
-    int b = pl.b, rows = pl.rows, nb = pl.nb;
-    int h = work ? static_cast<int>((w0 - pl.first) / nb) : 0;
-    int64_t unit0 = pl.first + static_cast<int64_t>(h) * nb;     // first block of the unit
-    if (tid == 0) {
-        Joint j{-1, 0, 0, 0};
-        if (work && unit0 < w0 && unit0 + nb <= w1) {
-            const int64_t from = ((unit0 + 1) * pl.n - 1) / pl.total;      // the CTA whose range holds block unit0
-            j = Joint{static_cast<int>(from), b, h, from * pl.total / pl.n == unit0 ? 0 : 1};
-        }
-        p.joint[me] = j;
+// Joins the shares of a CTA's warps: each run of shares of one unit, in order, becomes the unit's
+// result or one of the CTA's records.
+template <int D, bool kF32, int G>
+__device__ __forceinline__ void join_shares(const PagedAttnParams& p, JoinSmem<D, G>& js) {
+    constexpr int kShares = 2 * kPaWarps;
+    const int tid = threadIdx.x;
+    if (tid < 32) {            // lane e looks at share e: which run it belongs to, where that ends
+        const ShareOf f = tid < kShares ? js.of[tid] : ShareOf{-1, 0, false, false, false};
+        const uint32_t some = __ballot_sync(0xffffffffu, f.b >= 0);
+        const uint32_t before = some & ((1u << tid) - 1);
+        const int prev = before ? 31 - __clz(before) : 0;
+        const int pb = __shfl_sync(0xffffffffu, f.b, prev), ph = __shfl_sync(0xffffffffu, f.h, prev);
+        const bool starts = f.b >= 0 && !(before && pb == f.b && ph == f.h);
+        const uint32_t heads = __ballot_sync(0xffffffffu, starts);
+        const uint32_t later = heads & ~((2u << tid) - 1);
+        const uint32_t mine = some & ~((1u << tid) - 1) & (later ? (later & -later) - 1 : ~0u);
+        const int last = mine ? 31 - __clz(mine) : 0;
+        const bool ends = __shfl_sync(0xffffffffu, static_cast<int>(f.ends), last);
+        if (starts) js.run[__popc(heads & ((1u << tid) - 1))] = Run{f.b, f.h, tid, last, f.begins && ends, f.first};
+        if (tid == 0) js.runs = __popc(heads);
     }
-    Tile tile;
-    for (int64_t cur = w0; cur < w1;) {
-        const int blk = static_cast<int>(cur - unit0);
-        const int64_t stop = min(w1, unit0 + nb);
-        const int first = blk * kPaBlock, end = static_cast<int>(min(static_cast<int64_t>(rows), (stop - unit0) * kPaBlock));
-        tile.load_q(p, b, h, s_q);
-        tile.reset();
-        const int64_t u = static_cast<int64_t>(b) * p.c.H + h;
-        float* z = p.z ? p.z + u * p.c.cap * p.Gp : nullptr;
-        tile.share(p, b, h, first + warp * kPaTile, end, z);
-        tile.hand_over(js);
-        __syncthreads();
-        // join the warps: thread = dimension (and every other head where d is 64)
-        const bool alone = cur == unit0 && stop == unit0 + nb;
-        float* rec = p.rec + (me * 2 + (cur == w0 ? 0 : 1)) * p.G * (D + 2);
-        for (int g = tid / D; g < p.G; g += kPaThreads / D) {
-            const int dim = tid % D;
-            float m = -CUDART_INF_F;
-#pragma unroll
-            for (int w = 0; w < kPaWarps; ++w) m = fmaxf(m, js.m[w][g]);
-            float l = 0.f, x = 0.f;
-#pragma unroll
-            for (int w = 0; w < kPaWarps; ++w) {
-                const float f = js.m[w][g] == -CUDART_INF_F && !(js.l[w][g] != js.l[w][g]) ? 0.f : exp2_fast(js.m[w][g] - m);
-                l = fmaf(js.l[w][g], f, l);
-                x = fmaf(js.o[w][g & 1][g >> 1][dim], f, x);
+    __syncthreads();
+    const int runs = js.runs;
+    // a share's weight against its run, and the run's base and sum (thread = run, head)
+    if (tid < runs * G && tid % G < p.G) {
+        const Run r = js.run[tid / G];
+        const int g = tid % G;
+        float m = -CUDART_INF_F, l = 0.f;
+        for (int e = r.from; e <= r.last; ++e)
+            if (js.of[e].b >= 0) m = fmaxf(m, js.m[e][g]);
+        for (int e = r.from; e <= r.last; ++e)
+            if (js.of[e].b >= 0) l = fmaf(js.l[e][g], share_weight(js.m[e][g], js.l[e][g], m), l);
+        const float scale = !r.whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        for (int e = r.from; e <= r.last; ++e)
+            js.w[e][g] = js.of[e].b >= 0 ? share_weight(js.m[e][g], js.l[e][g], m) * scale : -1.f;
+        if (r.whole) note(p, r.b, r.h, g, m, l);
+        else p.rec_stat[(static_cast<int64_t>(blockIdx.x) * 2 + (r.first ? 0 : 1)) * p.G + g] = make_float2(m, l);
+    }
+    __syncthreads();
+    for (int i = 0; i < runs; ++i) {
+        const Run r = js.run[i];
+        float* rec = p.rec + (static_cast<int64_t>(blockIdx.x) * 2 + (r.first ? 0 : 1)) * p.G * D;
+        for (int k = tid; k < p.G * (D / 4); k += kPaThreads) {
+            const int g = k / (D / 4), dim = 4 * (k % (D / 4));
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int e = r.from; e <= r.last; ++e) {
+                const float w = js.w[e][g];
+                if (w < 0.f) continue;         // no share
+                const float4 v = *reinterpret_cast<const float4*>(&js.o[e][g][dim]);
+                x[0] = fmaf(v.x, w, x[0]);
+                x[1] = fmaf(v.y, w, x[1]);
+                x[2] = fmaf(v.z, w, x[2]);
+                x[3] = fmaf(v.w, w, x[3]);
             }
-            if (alone) {
-                store_out(p, kF32, b, h, g, dim, l == 0.f ? 0.f : x / l);
-                if (dim == 0) {
-                    if (p.lse) p.lse[static_cast<int64_t>(b) * p.n_q + h * p.G + g] = ln_of(m, l);
-                    if (p.stat) p.stat[u * p.G + g] = make_float2(m, l == 0.f ? 0.f : 1.f / l);
-                }
+            if (!r.whole) {
+                *reinterpret_cast<float4*>(rec + g * D + dim) = make_float4(x[0], x[1], x[2], x[3]);
             } else {
-                rec[g * (D + 2) + dim] = x;
-                if (dim == 0) *reinterpret_cast<float2*>(rec + g * (D + 2) + D) = make_float2(m, l);
+                store4<kF32>(p, r.b, r.h, g, dim, x);
             }
         }
-        __syncthreads();
-        cur = stop;
-        if (cur >= w1) break;
-        unit0 += nb;
-        if (++h == p.c.H) {      // the next sequence that has rows
-            h = 0;
-            next_rows(p.c, b, rows);
-            if (rows < 0) break;     // the lengths changed under the call
-            nb = blocks_of(rows);
+    }
+}
+
+template <class Tile, int D, bool kF32, int G, int kOcc>
+__global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_constant__ PagedAttnParams p) {
+    __shared__ PlanSmem<kPaWarps> s_plan;
+    __shared__ __align__(16) JoinSmem<D, G> js;
+    pdl_trigger();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, me = blockIdx.x;
+    const Plan<kPaWarps> pl = make_plan(p.c, me, gridDim.x, s_plan);
+    const int64_t w0 = pl.part(warp), w1 = pl.part(warp + 1);
+    if (lane == 0) js.of[2 * warp].b = js.of[2 * warp + 1].b = -1;
+    __syncwarp();
+    if (w0 < w1) {
+        Walk at;
+        at.enter(s_plan.b[warp], s_plan.rows[warp], s_plan.at[warp], w0);
+        Tile tile;
+        for (int64_t cur = w0; cur < w1;) {
+            const int64_t stop = min(w1, at.unit0 + at.nt);
+            const int row0 = static_cast<int>(cur - at.unit0) * kPaTile;
+            const int end = static_cast<int>(min(static_cast<int64_t>(at.rows), (stop - at.unit0) * kPaTile));
+            // (fp32 keeps its queries where the warp's last share will go)
+            tile.load_q(p, at.b, at.h, js.o[2 * warp + 1][0]);
+            tile.reset();
+            float* z = p.z ? p.z + (static_cast<int64_t>(at.b) * p.c.H + at.h) * p.c.cap * p.Gp : nullptr;
+            tile.share(p, at.b, at.h, row0, end, z);
+            const bool begins = cur == at.unit0, ends = stop == at.unit0 + at.nt;
+            const int slot = 2 * warp + (cur == w0 ? 0 : 1);
+            tile.finish(p, at.b, at.h, begins && ends, js, slot);
+            if (!(begins && ends) && lane == 0) js.of[slot] = ShareOf{at.b, at.h, begins, ends, cur == pl.lo};
+            cur = stop;
+            if (cur < w1 && !at.next(p.c)) break;
         }
     }
+    // a unit that ends in this CTA and began before it
+    if (tid == 0) {
+        Joint joint{-1, 0, 0, 0};
+        if (pl.lo < pl.hi) {
+            Walk at;
+            at.enter(s_plan.b[0], s_plan.rows[0], s_plan.at[0], pl.lo);
+            if (at.unit0 < pl.lo && at.unit0 + at.nt <= pl.hi) {
+                const int64_t from = pl.holder(at.unit0);
+                joint = Joint{static_cast<int>(from), at.b, at.h, pl.start(from) == at.unit0 ? 0 : 1};
+            }
+        }
+        p.joint[me] = joint;
+    }
+    __syncthreads();
+    join_shares<D, kF32, G>(p, js);
     // sequences of no rows
     for (int e = blockIdx.x; e < p.c.batch; e += gridDim.x)
         if (rows_of(p.c, e, g_err, 711) == 0) {
@@ -605,72 +721,145 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
         }
 }
 
-// Joins the records of the units that lie in more than one CTA's range: CTA (i, g) those of head
-// g of the unit that ends in CTA i's range and began before it (p.joint[i] says which, if any).
-// Lanes hold four dimensions each; warps (half-warps where d is 64) take the contributors in turn.
-constexpr int kPaMost = 512;      // contributors at most
+// Joins the records of the units that lie in more than one CTA's range: row i of the grid those of
+// the unit that ends in CTA i's range and began before it (p.joint says which, if any).  The grid's
+// y dimension deals the heads out.
+constexpr int kPaMost = 512;      // shares of a unit at most
+constexpr int kPaFew = 8;         // shares that a thread joins by itself
 
+// Few shares: a thread holds four dimensions of one head, and forms the weights for itself.
 template <int D, bool kF32>
-__global__ void __launch_bounds__(kPaThreads) k_paged_merge(const __grid_constant__ PagedAttnParams p) {
-    constexpr int kLanes = D / 4, kWays = kPaThreads / kLanes;
-    __shared__ float s_f[kPaMost], s_red[kPaWarps], s_sum[kPaWarps];
-    __shared__ __align__(16) float s_x[kWays][D];
-    pdl_trigger();
-    // every CTA waits for the grid before, so that this grid's end stands for both
-    pdl_wait();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = blockIdx.y, me = blockIdx.x;
-    const int4 raw = __ldcg(reinterpret_cast<const int4*>(p.joint) + me);
-    const Joint j{raw.x, raw.y, raw.z, raw.w};
-    if (j.from < 0) return;
-    const int n = me - j.from + 1;
-    const int64_t pitch = p.G * (D + 2);
-    // contributor i's record: slot 0, but the unit began inside the first one's range
-    auto rec_of = [&](int i) { return p.rec + (static_cast<int64_t>(j.from + i) * 2 + (i == 0 ? j.slot : 0)) * pitch + g * (D + 2); };
+__device__ __forceinline__ void merge_few(const PagedAttnParams& p, const Joint& j, int n) {
+    for (int k = threadIdx.x + blockIdx.y * kPaThreads; k < p.G * (D / 4); k += gridDim.y * kPaThreads) {
+        const int g = k / (D / 4), dim = 4 * (k % (D / 4));
+        float2 ml[kPaFew];
+        float4 v[kPaFew];
+#pragma unroll
+        for (int i = 0; i < kPaFew; ++i) {
+            ml[i] = make_float2(-CUDART_INF_F, 0.f);
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < n) {
+                const int64_t rec = (static_cast<int64_t>(j.from + i) * 2 + (i == 0 ? j.slot : 0)) * p.G + g;
+                ml[i] = __ldcg(p.rec_stat + rec);
+                v[i] = __ldcg(reinterpret_cast<const float4*>(p.rec + rec * D + dim));
+            }
+        }
+        float m = -CUDART_INF_F, l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kPaFew; ++i) m = fmaxf(m, ml[i].x);
+#pragma unroll
+        for (int i = 0; i < kPaFew; ++i) {
+            if (i >= n) break;
+            const float f = share_weight(ml[i].x, ml[i].y, m);
+            l = fmaf(ml[i].y, f, l);
+            x[0] = fmaf(v[i].x, f, x[0]);
+            x[1] = fmaf(v[i].y, f, x[1]);
+            x[2] = fmaf(v[i].z, f, x[2]);
+            x[3] = fmaf(v[i].w, f, x[3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = l == 0.f ? 0.f : x[e] / l;
+        store4<kF32>(p, j.b, j.h, g, dim, x);
+        if (dim == 0) note(p, j.b, j.h, g, m, l);
+    }
+}
+
+// More: the CTA forms the weights of one head, lanes hold four dimensions, and warps (half-warps
+// where d is 64) take the shares in turn.
+template <int D>
+struct MergeSmem {
+    float f[kPaMost], red[kPaWarps], sum[kPaWarps];
+    __align__(16) float x[kPaThreads / (D / 4)][D];
+};
+template <int D, bool kF32>
+__device__ __forceinline__ void merge_many(const PagedAttnParams& p, const Joint& j, int n, int g, MergeSmem<D>& sm) {
+    constexpr int kLanes = D / 4, kWays = kPaThreads / kLanes, kEach = kPaMost / kPaThreads;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // share i: slot 0, but the unit began inside the first CTA's range
+    auto rec_of = [&](int i) -> int64_t {
+        return (static_cast<int64_t>(j.from + i) * 2 + (i == 0 ? j.slot : 0)) * p.G + g;
+    };
+    float2 ml[kEach];
     float m = -CUDART_INF_F;
-    for (int i = tid; i < n; i += kPaThreads) m = fmaxf(m, __ldcg(rec_of(i) + D));
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int i = tid + e * kPaThreads;
+        ml[e] = i < n ? __ldcg(p.rec_stat + rec_of(i)) : make_float2(-CUDART_INF_F, 0.f);
+        m = fmaxf(m, ml[e].x);
+    }
+    // the first shares are on their way while the weights form
+    constexpr int kAhead = 4;
+    const int dim = 4 * (tid % kLanes), way = tid / kLanes;
+    auto fetch = [&](int i) {
+        return i < n ? __ldcg(reinterpret_cast<const float4*>(p.rec + rec_of(i) * D + dim)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    float4 a[kAhead];
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) a[e] = fetch(way + e * kWays);
     m = warp_max(m);
-    if (lane == 0) s_red[warp] = m;
+    if (lane == 0) sm.red[warp] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kPaWarps; ++w) m = fmaxf(m, s_red[w]);
+    for (int w = 0; w < kPaWarps; ++w) m = fmaxf(m, sm.red[w]);
     float l = 0.f;
-    for (int i = tid; i < n; i += kPaThreads) {
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(rec_of(i) + D));
-        const float f = ml.x == -CUDART_INF_F && !(ml.y != ml.y) ? 0.f : exp2_fast(ml.x - m);
-        s_f[i] = f;
-        l = fmaf(ml.y, f, l);
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int i = tid + e * kPaThreads;
+        const float f = share_weight(ml[e].x, ml[e].y, m);
+        if (i < n) sm.f[i] = f;
+        l = fmaf(ml[e].y, f, l);
     }
     l = warp_sum(l);
-    if (lane == 0) s_sum[warp] = l;
+    if (lane == 0) sm.sum[warp] = l;
     __syncthreads();
-    l = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
-    const int dim = 4 * (tid % kLanes), way = tid / kLanes;
+    l = sm.sum[0] + sm.sum[1] + sm.sum[2] + sm.sum[3];
     float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int i = way; i < n; i += kWays) {
-        const float* r = rec_of(i) + dim;
-        const float2 a = __ldcg(reinterpret_cast<const float2*>(r)), b = __ldcg(reinterpret_cast<const float2*>(r + 2));
-        const float f = s_f[i];
-        x[0] = fmaf(a.x, f, x[0]);
-        x[1] = fmaf(a.y, f, x[1]);
-        x[2] = fmaf(b.x, f, x[2]);
-        x[3] = fmaf(b.y, f, x[3]);
+    for (int i = way; i < n; i += kAhead * kWays) {
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) {
+            if (i + e * kWays >= n) break;
+            const float f = sm.f[i + e * kWays];
+            x[0] = fmaf(a[e].x, f, x[0]);
+            x[1] = fmaf(a[e].y, f, x[1]);
+            x[2] = fmaf(a[e].z, f, x[2]);
+            x[3] = fmaf(a[e].w, f, x[3]);
+        }
+#pragma unroll
+        for (int e = 0; e < kAhead; ++e) a[e] = fetch(i + (kAhead + e) * kWays);
     }
-    *reinterpret_cast<float4*>(&s_x[way][dim]) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(&sm.x[way][dim]) = make_float4(x[0], x[1], x[2], x[3]);
     __syncthreads();
     if (tid < D) {
         float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWays; ++w) sum += s_x[w][tid];
+        for (int w = 0; w < kWays; ++w) sum += sm.x[w][tid];
         store_out(p, kF32, j.b, j.h, g, tid, l == 0.f ? 0.f : sum / l);
     }
-    if (tid == 0) {
-        if (p.lse) p.lse[static_cast<int64_t>(j.b) * p.n_q + j.h * p.G + g] = ln_of(m, l);
-        if (p.stat) p.stat[(static_cast<int64_t>(j.b) * p.c.H + j.h) * p.G + g] = make_float2(m, l == 0.f ? 0.f : 1.f / l);
-    }
+    if (tid == 0) note(p, j.b, j.h, g, m, l);
+    __syncthreads();
 }
 
-// Four rows per thread and turn: their products are loaded before any of them is used.
+template <int D, bool kF32>
+__global__ void __launch_bounds__(kPaThreads) k_paged_merge(const __grid_constant__ PagedAttnParams p) {
+    __shared__ MergeSmem<D> sm;
+    pdl_trigger();
+    // every CTA waits for the grid before, so that this grid's end stands for both
+    pdl_wait();
+    const int me = blockIdx.x;
+    const int4 raw = __ldcg(reinterpret_cast<const int4*>(p.joint) + me);
+    const Joint j{raw.x, raw.y, raw.z, raw.w};
+    if (j.from < 0) return;
+    const int n = me - j.from + 1;
+    if (n <= kPaFew) {
+        merge_few<D, kF32>(p, j, n);
+        return;
+    }
+    for (int g = blockIdx.y; g < p.G; g += gridDim.y) merge_many<D, kF32>(p, j, n, g, sm);
+}
+
+// Two rows per thread and turn: their products are loaded before any of them is used.
+constexpr int kTurn = 2;
+
 template <int Gp>
 __device__ __forceinline__ void weigh_rows_of(const PagedAttnParams& p, int64_t u, int first, int end) {
     const float* z = p.z + u * p.c.cap * Gp;
@@ -683,11 +872,11 @@ __device__ __forceinline__ void weigh_rows_of(const PagedAttnParams& p, int64_t 
         base[g] = st.x;
         inv[g] = st.y;
     }
-    for (int i0 = first + threadIdx.x; i0 < end; i0 += 4 * kPaThreads) {
-        float2 x[4][Gp / 2];
-        float w[4];
+    for (int i0 = first + threadIdx.x; i0 < end; i0 += kTurn * kPaThreads) {
+        float2 x[kTurn][Gp / 2];
+        float w[kTurn];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < kTurn; ++r) {
             const int i = i0 + r * kPaThreads;
             if (i >= end) continue;
             w[r] = in[i];
@@ -695,7 +884,7 @@ __device__ __forceinline__ void weigh_rows_of(const PagedAttnParams& p, int64_t 
             for (int g = 0; g < Gp / 2; ++g) x[r][g] = __ldcg(reinterpret_cast<const float2*>(z + static_cast<int64_t>(i) * Gp) + g);
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < kTurn; ++r) {
             const int i = i0 + r * kPaThreads;
             if (i >= end) continue;
             float sum = 0.f;
@@ -717,32 +906,20 @@ __device__ __forceinline__ void weigh_rows(const PagedAttnParams& p, int64_t u, 
 }
 
 // weight_out = weight + sum over the heads of exp2(z scale - base) / sum, over the same split
-__global__ void __launch_bounds__(kPaThreads) k_paged_weigh(const __grid_constant__ PagedAttnParams p) {
-    __shared__ PlanSmem s_plan;
-    const int tid = threadIdx.x;
-    const int64_t ctas = gridDim.x, me = blockIdx.x;
-    const Place pl = plan(p.c, me, ctas, s_plan);
+__global__ void __launch_bounds__(kPaThreads, 8) k_paged_weigh(const __grid_constant__ PagedAttnParams p) {
+    __shared__ PlanSmem<1> s_plan;
+    const Plan<1> pl = make_plan(p.c, blockIdx.x, gridDim.x, s_plan);
     pdl_wait();
-    if (me >= pl.n) return;
-    const int64_t w0 = me * pl.total / pl.n, w1 = (me + 1) * pl.total / pl.n;
-    int b = pl.b, rows = pl.rows, nb = pl.nb;
-    int h = static_cast<int>((w0 - pl.first) / nb);
-    int64_t unit0 = pl.first + static_cast<int64_t>(h) * nb;
-    for (int64_t cur = w0; cur < w1;) {
-        const int64_t stop = min(w1, unit0 + nb);
-        const int first = static_cast<int>(cur - unit0) * kPaBlock;
-        const int end = static_cast<int>(min(static_cast<int64_t>(rows), (stop - unit0) * kPaBlock));
-        const int64_t u = static_cast<int64_t>(b) * p.c.H + h;
-        weigh_rows(p, u, first, end);
+    if (pl.lo == pl.hi) return;
+    int64_t cur = pl.lo;
+    Walk at;
+    at.enter(s_plan.b[0], s_plan.rows[0], s_plan.at[0], cur);
+    while (cur < pl.hi) {
+        const int64_t stop = min(pl.hi, at.unit0 + at.nt);
+        weigh_rows(p, static_cast<int64_t>(at.b) * p.c.H + at.h, static_cast<int>(cur - at.unit0) * kPaTile,
+                   static_cast<int>(min(static_cast<int64_t>(at.rows), (stop - at.unit0) * kPaTile)));
         cur = stop;
-        if (cur >= w1) break;
-        unit0 += nb;
-        if (++h == p.c.H) {
-            h = 0;
-            next_rows(p.c, b, rows);
-            if (rows < 0) break;     // the lengths changed under the call
-            nb = blocks_of(rows);
-        }
+        if (cur < pl.hi && !at.next(p.c)) break;
     }
 }
 
@@ -753,13 +930,16 @@ constexpr int kWeighOcc = 3;               // CTAs of k_paged_weigh per CTA of k
 
 int paged_attn_ctas(int dtype, int nsm) { return nsm * (dtype == SKV_F32 ? kOccF32 : kOccTC); }
 
-template <class Tile, int D, bool kF32, int kOcc>
+template <class Tile, int D, bool kF32, int G, int kOcc>
 static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
-    // no more CTAs than there can be blocks of rows
-    const int64_t most = static_cast<int64_t>(p.c.batch) * p.c.H * ((p.c.cap + kPaBlock - 1) / kPaBlock);
+    // no more CTAs than there can be tiles for their warps
+    const int64_t tiles = static_cast<int64_t>(p.c.batch) * p.c.H * ((p.c.cap + kPaTile - 1) / kPaTile);
+    const int64_t most = (tiles + kPaWarps - 1) / kPaWarps;
     const int n = most < ncta ? static_cast<int>(most) : ncta;
-    k_paged_attn<Tile, D, kF32, kOcc><<<n, kPaThreads, 0, s>>>(p);
-    if (launch_pdl(k_paged_merge<D, kF32>, dim3(n, p.G), dim3(kPaThreads), 0, s, p) != cudaSuccess) return -1;
+    k_paged_attn<Tile, D, kF32, G, kOcc><<<n, kPaThreads, 0, s>>>(p);
+    // a CTA per head where units are few and so have many shares; one for all heads where they are many
+    const int heads = p.c.batch * static_cast<int64_t>(p.c.H) * 4 >= n ? 1 : p.G;
+    if (launch_pdl(k_paged_merge<D, kF32>, dim3(n, heads), dim3(kPaThreads), 0, s, p) != cudaSuccess) return -1;
     if (p.weight_out) {
         const int64_t wide = kWeighOcc * static_cast<int64_t>(ncta);
         const int nw = static_cast<int>(most < wide ? most : wide);
@@ -769,19 +949,19 @@ static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
 }
 template <int D>
 static int launch_f32(const PagedAttnParams& p, int ncta, cudaStream_t s) {
-    if (p.G <= 1) return launch_pa<TileF32<D, 1>, D, true, kOccF32>(p, ncta, s);
-    if (p.G <= 2) return launch_pa<TileF32<D, 2>, D, true, kOccF32>(p, ncta, s);
-    if (p.G <= 4) return launch_pa<TileF32<D, 4>, D, true, kOccF32>(p, ncta, s);
-    return launch_pa<TileF32<D, 8>, D, true, kOccF32>(p, ncta, s);
+    if (p.G <= 1) return launch_pa<TileF32<D, 1>, D, true, 1, kOccF32>(p, ncta, s);
+    if (p.G <= 2) return launch_pa<TileF32<D, 2>, D, true, 2, kOccF32>(p, ncta, s);
+    if (p.G <= 4) return launch_pa<TileF32<D, 4>, D, true, 4, kOccF32>(p, ncta, s);
+    return launch_pa<TileF32<D, 8>, D, true, 8, kOccF32>(p, ncta, s);
 }
 
 int launch_paged_attn(int dtype, int d, const PagedAttnParams& p, int ncta, cudaStream_t s) {
     if (dtype == SKV_F32) return d == 64 ? launch_f32<64>(p, ncta, s) : launch_f32<128>(p, ncta, s);
     if (dtype == SKV_FP8)
-        return d == 64 ? launch_pa<TileTC<64, true>, 64, false, kOccTC>(p, ncta, s)
-                       : launch_pa<TileTC<128, true>, 128, false, kOccTC>(p, ncta, s);
-    return d == 64 ? launch_pa<TileTC<64, false>, 64, false, kOccTC>(p, ncta, s)
-                   : launch_pa<TileTC<128, false>, 128, false, kOccTC>(p, ncta, s);
+        return d == 64 ? launch_pa<TileTC<64, true>, 64, false, 8, kOccTC>(p, ncta, s)
+                       : launch_pa<TileTC<128, true>, 128, false, 8, kOccTC>(p, ncta, s);
+    return d == 64 ? launch_pa<TileTC<64, false>, 64, false, 8, kOccTC>(p, ncta, s)
+                   : launch_pa<TileTC<128, false>, 128, false, 8, kOccTC>(p, ncta, s);
 }
 
 cudaError_t paged_attn_err(int** e) { return cudaGetSymbolAddress(reinterpret_cast<void**>(e), g_err); }

@@ -117,7 +117,7 @@ int64_t round16(int64_t n) { return (n + 15) & ~int64_t(15); }
 
 // ------------------------------------------------------------------ attention
 
-struct AttnSpace { int Gp; int64_t joint, rec, stat, z, bytes; };
+struct AttnSpace { int Gp; int64_t joint, rec, rec_stat, stat, z, bytes; };
 
 // host-only part of the checks, and the workspace's layout
 int attn_space(const skv_paged_attention_args* a, AttnSpace* w) {
@@ -129,9 +129,11 @@ int attn_space(const skv_paged_attention_args* a, AttnSpace* w) {
         return SKV_ERR_INVALID;
     const int64_t U = static_cast<int64_t>(c.batch) * c.n_kv_heads, cap = static_cast<int64_t>(c.max_pages) * c.page_size;
     w->Gp = (G + 1) & ~1;
+    const int64_t ctas = paged_attn_ctas(c.dtype, kMaxSms);
     w->joint = 0;
-    w->rec = static_cast<int64_t>(paged_attn_ctas(c.dtype, kMaxSms)) * sizeof(Joint);
-    w->stat = w->rec + round16(static_cast<int64_t>(paged_attn_ctas(c.dtype, kMaxSms)) * 2 * G * (c.head_dim + 2) * 4);
+    w->rec = ctas * static_cast<int64_t>(sizeof(Joint));
+    w->rec_stat = w->rec + ctas * 2 * G * c.head_dim * 4;
+    w->stat = w->rec_stat + round16(ctas * 2 * G * 8);
     w->z = w->stat;
     w->bytes = w->stat;
     if (a->weight_out) {
@@ -247,6 +249,7 @@ int shadowkv_paged_attention(const skv_paged_attention_args* a, skv_stream strea
     const int es = key_bytes(c.dtype), G = a->n_q_heads / c.n_kv_heads;
     if (!c.lens || !a->q || !a->out || !a->workspace || !aligned16(a->q) || !aligned16(a->workspace)) return SKV_ERR_INVALID;
     if (!good_stride(a->q_seq, es) || !good_stride(a->q_head, es)) return SKV_ERR_INVALID;
+    if (!aligned16(a->out) || !good_stride(a->out_seq, es) || !good_stride(a->out_head, es)) return SKV_ERR_INVALID;
     if (!spread(a->out_seq, c.batch, c.head_dim) || !spread(a->out_head, a->n_q_heads, c.head_dim)) return SKV_ERR_INVALID;
     if (a->workspace_bytes < w.bytes) return SKV_ERR_INVALID;
     if ((a->weight != nullptr) != (a->weight_out != nullptr)) return SKV_ERR_INVALID;
@@ -266,6 +269,7 @@ int shadowkv_paged_attention(const skv_paged_attention_args* a, skv_stream strea
     p.q = a->q; p.out = a->out; p.lse = a->lse;
     p.joint = reinterpret_cast<Joint*>(ws + w.joint);
     p.rec = reinterpret_cast<float*>(ws + w.rec);
+    p.rec_stat = reinterpret_cast<float2*>(ws + w.rec_stat);
     if (a->weight_out) {
         p.stat = reinterpret_cast<float2*>(ws + w.stat);
         p.z = reinterpret_cast<float*>(ws + w.z);

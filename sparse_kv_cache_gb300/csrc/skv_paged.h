@@ -34,7 +34,7 @@ struct NormRopeParams {
 };
 int launch_norm_rope(int dtype, int d, const NormRopeParams& p, int nsm, cudaStream_t s);
 
-// A unit whose shares CTA i of the attention completes: its shares lie in the records of CTAs
+// A unit whose shares CTA i of the attention completes: they lie in the records of CTAs
 // from .. i (slot: which of the first one's two); from < 0: there is none.
 struct Joint { int from, b, h, slot; };
 
@@ -44,12 +44,14 @@ struct PagedAttnParams {
     float scale_log2;         // scale * log2(e)
     int64_t q_seq, q_head, o_seq, o_head;
     const void* q; void* out; float* lse;
-    float* rec;               // [ncta][2][G][d + 2]: a CTA's shares of its first and last unit
+    float* rec;               // [ncta][2][G][d]: a CTA's shares of its first and last unit, unnormalised
+    float2* rec_stat;         // [ncta][2][G]: their bases and sums
     Joint* joint;             // [ncta]
     // weights: raw products q.k of every row [U][cap][Gp], and (base, 1 / sum) per head [U][G]
     float* z; float2* stat; int Gp;
     const float* weight; float* weight_out; int64_t row_pitch;
 };
+constexpr int kPaWarps = 4;                  // warps of a CTA of the attention
 int paged_attn_ctas(int dtype, int nsm);     // CTAs that fill nsm SMs
 int launch_paged_attn(int dtype, int d, const PagedAttnParams& p, int ncta, cudaStream_t s);
 
