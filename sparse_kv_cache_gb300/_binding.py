@@ -283,31 +283,41 @@ def _vector(where: str, name: str, t, n: int, dtype: str = "torch.int32"):
         _refuse(where, f"{name} is {dtype} [{n}], contiguous")
 
 
-def _current_stream(device) -> int:
+def _raw_stream(device, stream) -> int:
+    """The handle of a call's stream: the given one, or torch's current one."""
+    if stream is not None:
+        return _stream(stream)
+    if device.type != "cuda":
+        return 0
     import torch
     try:
-        return torch._C._cuda_getCurrentRawStream(device.index or 0)
+        return torch._C._cuda_getCurrentRawStream(device.index)
     except AttributeError:   # a build without the short way
         return torch.cuda.current_stream().cuda_stream
 
 
-def _space(nbytes: int, device, stream):
-    """Workspace of one call, from torch's allocator on the call's own stream: calls on several
-    streams, or captured into several graphs, each have their own."""
+_KEPT_BYTES = 8 << 20
+_kept_spaces: dict = {}      # (device, stream) -> workspace of that stream's calls
+
+
+def _space(nbytes: int, device, stream, raw: int):
+    """Workspace of one call.  Calls on torch's current stream run one after the other and share one
+    per stream; a captured call, one on a stream that was handed in, and one that needs much have
+    their own from torch's allocator, on the call's stream -- so neither streams nor graphs that
+    run side by side ever share one."""
     import torch
-    if stream is None or device.type != "cuda":
+    if device.type != "cuda":
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream), device)
+    if stream is None:
+        if nbytes > _KEPT_BYTES or torch.cuda.is_current_stream_capturing():
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        t = _kept_spaces.get((device.index, raw))
+        if t is None or t.numel() < nbytes:
+            t = _kept_spaces[device.index, raw] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return t
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw, device)
     with torch.cuda.stream(s):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-
-
-def _launch(name: str, packed: bytes, device, stream):
-    if stream is None:
-        stream = _current_stream(device) if device.type == "cuda" else 0
-    else:
-        stream = _stream(stream)
-    _check(getattr(load(), name)(packed, stream), name)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -370,7 +380,7 @@ def qk_norm_rope(q, k, positions, q_out, k_out=None, *, q_weight=None, k_weight=
         *cache, *pools, *fixed, q.data_ptr(), k.data_ptr(), more[0], _ptr(q_weight) or 0, _ptr(k_weight) or 0,
         q_out.data_ptr(), _ptr(k_out) or 0, positions.data_ptr(), more[1], more[2], _ptr(position) or 0, _ptr(weight) or 0,
         pitch)
-    _launch("shadowkv_qk_norm_rope", packed, q.device, stream)
+    _check(load().shadowkv_qk_norm_rope(packed, _raw_stream(q.device, stream)), "shadowkv_qk_norm_rope")
     return q_out, k_out
 
 
@@ -414,11 +424,12 @@ def paged_attention(q, k_cache, v_cache, table, lens, out, lse=None, weight=None
         _form(q), _form(k_cache), _form(v_cache), _form(table), _form(lens), _form(out), _form(lse), _form(weight),
         _form(weight_out), scale)
     device = q.device
-    space = _space(nbytes, device, stream)
+    raw = _raw_stream(device, stream)
+    space = _space(nbytes, device, stream, raw)
     packed = _PAGED_ATTN.pack(
         *cache, k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), *fixed, q.data_ptr(),
         out.data_ptr(), _ptr(lse) or 0, _ptr(weight) or 0, _ptr(weight_out) or 0, pitch, space.data_ptr(), nbytes)
-    _launch("shadowkv_paged_attention", packed, device, stream)
+    _check(load().shadowkv_paged_attention(packed, raw), "shadowkv_paged_attention")
     return out
 
 
@@ -454,12 +465,13 @@ def paged_evict(k_cache, v_cache, table, lens, weight, position, budget: int, re
         _form(k_cache), _form(v_cache), _form(table), _form(lens), _form(weight), _form(position), _form(lens_out),
         _form(weight_out), _form(position_out), budget, recent, sink)
     device = weight.device
-    space = _space(nbytes, device, stream)
+    raw = _raw_stream(device, stream)
+    space = _space(nbytes, device, stream, raw)
     packed = _EVICT.pack(
         *cache, k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), *fixed, weight.data_ptr(),
         position.data_ptr(), weight_out.data_ptr(), position_out.data_ptr(), pitch, lens_out.data_ptr(), space.data_ptr(),
         nbytes)
-    _launch("shadowkv_paged_evict", packed, device, stream)
+    _check(load().shadowkv_paged_evict(packed, raw), "shadowkv_paged_evict")
     return lens_out
 
 
