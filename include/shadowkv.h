@@ -572,11 +572,11 @@ typedef struct {
     skv_paged_cache cache;
     int32_t budget;             /* >= 1 */
     int32_t recent, sink;       /* >= 0, recent + sink <= budget */
-    const float* weight;        /* dev [batch][n_kv_heads][row_pitch] */
-    const int32_t* position;    /* dev, the same shape */
+    const float* weight;        /* dev [batch][n_kv_heads][row_pitch]; this and the next three 16-byte aligned */
+    const int32_t* position;    /* dev, the same shape; >= 0 */
     float* weight_out;
     int32_t* position_out;
-    int64_t row_pitch;          /* >= max_pages * page_size */
+    int64_t row_pitch;          /* >= max_pages * page_size, a multiple of 4 */
     int32_t* lens_out;          /* dev [batch] */
     void* workspace;            /* dev, 16-byte aligned */
     int64_t workspace_bytes;    /* >= shadowkv_paged_evict_workspace(args) */

@@ -12,7 +12,9 @@
 // the rows, each warp with a contiguous part of the slice; counts are joined through distributed
 // shared memory.  The upper halves of a slice's keys stay in shared memory, and the lower ones too
 // where there is room; else the weights are read again for lanes that hold a row whose upper half
-// equals the threshold's.  k_evict_move, a programmatic dependent, copies the rows.
+// equals the threshold's.  Once the 11 uppermost bits of the threshold are known, a warp whose rows
+// all lie behind the budget keeps a list of those that can still stay -- of a long prompt a few in
+// a hundred -- and goes on with that.  k_evict_move, a programmatic dependent, copies the rows.
 #include "skv_common.cuh"
 #include "skv_internal.h"
 #include "skv_paged.h"
@@ -36,23 +38,61 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
+__device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr) {
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ void sync_all(int ranks) {
     if (ranks > 1) cluster_sync_all();
     else __syncthreads();
 }
 
-// eight consecutive 32-bit values from row s on, `fill` from row `end` on
-template <typename T>
-__device__ __forceinline__ void load_rows(const T* p, int s, int end, bool vec, T fill, T (&x)[8]) {
-    if (vec && s + 8 <= end) {
-        const int4 a = __ldg(reinterpret_cast<const int4*>(p + s)), b = __ldg(reinterpret_cast<const int4*>(p + s) + 1);
-        const int v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = *reinterpret_cast<const T*>(&v[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = s + e < end ? __ldg(p + s + e) : fill;
+// Eight consecutive weights and positions from row s on.  s is a multiple of 8 below the unit's
+// rows, and a sequence's room is one too, so rows that are read beyond its last lie in its room.
+struct Rows8 { float4 w0, w1; int4 p0, p1; };
+__device__ __forceinline__ void load_rows(const float* w, const int32_t* p, int s, Rows8& r) {
+    r.w0 = __ldg(reinterpret_cast<const float4*>(w + s));
+    r.w1 = __ldg(reinterpret_cast<const float4*>(w + s) + 1);
+    r.p0 = __ldg(reinterpret_cast<const int4*>(p + s));
+    r.p1 = __ldg(reinterpret_cast<const int4*>(p + s) + 1);
+}
+// Their keys: the largest for a protected row.
+struct Protect {
+    int from, sink;    // positions above from are recent, those below sink are first ones
+    __device__ __forceinline__ uint32_t key(float w, int pos) const {
+        return (pos > from || pos < sink) ? 0xFFFFFFFFu : weight_key(w);
     }
+};
+__device__ __forceinline__ void keys_of(const Protect& pr, const Rows8& r, uint32_t (&t)[8]) {
+    t[0] = pr.key(r.w0.x, r.p0.x); t[1] = pr.key(r.w0.y, r.p0.y); t[2] = pr.key(r.w0.z, r.p0.z); t[3] = pr.key(r.w0.w, r.p0.w);
+    t[4] = pr.key(r.w1.x, r.p1.x); t[5] = pr.key(r.w1.y, r.p1.y); t[6] = pr.key(r.w1.z, r.p1.z); t[7] = pr.key(r.w1.w, r.p1.w);
+}
+// eight upper (sh 16) or lower (sh 0) halves of keys in 16 bytes
+__device__ __forceinline__ uint4 halves(const uint32_t (&t)[8], int sh) {
+    auto pair = [&](int e) { return ((t[e] >> sh) & 0xFFFF) | ((t[e + 1] >> sh) << 16); };
+    return make_uint4(pair(0), pair(2), pair(4), pair(6));
+}
+// the same from the weights, where the keys are not held (kept out of line: seldom called)
+__device__ __noinline__ uint4 remade(const float* w, const int32_t* p, int s, Protect pr, int sh) {
+    Rows8 r;
+    load_rows(w, p, s, r);
+    uint32_t t[8];
+    keys_of(pr, r, t);
+    return halves(t, sh);
+}
+// bits of the halves that f holds for
+template <typename F>
+__device__ __forceinline__ uint32_t mark(const uint4& v, F f) {
+    return (f(v.x & 0xFFFF) ? 1u : 0u) | (f(v.x >> 16) ? 2u : 0u) | (f(v.y & 0xFFFF) ? 4u : 0u) | (f(v.y >> 16) ? 8u : 0u) |
+           (f(v.z & 0xFFFF) ? 16u : 0u) | (f(v.z >> 16) ? 32u : 0u) | (f(v.w & 0xFFFF) ? 64u : 0u) | (f(v.w >> 16) ? 128u : 0u);
+}
+__device__ __forceinline__ uint32_t half_of(const uint4& v, int e) {
+    const uint32_t x = e < 4 ? (e < 2 ? v.x : v.y) : (e < 6 ? v.z : v.w);
+    return (e & 1) ? x >> 16 : x & 0xFFFF;
 }
 
 __device__ __forceinline__ int excl_scan(int x, int lane) {
@@ -84,7 +124,6 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
     const int64_t base = static_cast<int64_t>(u) * p.row_pitch;
     const float* w_in = p.weight + base;
     const int32_t* p_in = p.position + base;
-    const bool vec = ((reinterpret_cast<uintptr_t>(w_in) | reinterpret_cast<uintptr_t>(p_in)) & 15) == 0;
     const bool copy_w = p.weight_out != p.weight, copy_p = p.position_out != p.position;
     const int64_t slice = (static_cast<int64_t>(n) + ranks - 1) / ranks;
     const int per = static_cast<int>((slice + kEvGrain - 1) / kEvGrain) * kEvStep;        // rows of a warp
@@ -104,12 +143,30 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
     for (int i = tid; i < kEvHist; i += kEvThreads) s_hist[i] = 0;
     // ---- the unit's last position
     int last = INT_MIN;
-#pragma unroll 4
-    for (int r0 = lo; r0 < hi; r0 += kEvStep) {
-        int pos[8];
-        load_rows<int>(p_in, r0 + 8 * lane, hi, vec, INT_MIN, pos);
+    constexpr int kDeep = 4;       // steps whose loads are in flight together
+    for (int r0 = lo; r0 < hi; r0 += kDeep * kEvStep) {
+        int4 pos[kDeep][2];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) last = max(last, pos[e]);
+        for (int k = 0; k < kDeep; ++k) {
+            const int s = r0 + k * kEvStep + 8 * lane;
+            pos[k][0] = pos[k][1] = make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);
+            if (s < hi) {
+                pos[k][0] = __ldg(reinterpret_cast<const int4*>(p_in + s));
+                pos[k][1] = __ldg(reinterpret_cast<const int4*>(p_in + s) + 1);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            const int left = hi - (r0 + k * kEvStep + 8 * lane);      // of the lane's eight rows, those below hi
+            const int4 a = pos[k][0], b = pos[k][1];
+            if (left >= 8) {
+                last = max(last, max(max(max(a.x, a.y), max(a.z, a.w)), max(max(b.x, b.y), max(b.z, b.w))));
+            } else {
+                const int v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int e = 0; e < 7; ++e) last = e < left ? max(last, v[e]) : last;
+            }
+        }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
@@ -125,91 +182,66 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
     last = s_max;
     for (int r = 0; r < ranks; ++r)
         if (r != rank) last = max(last, ld_cluster_s32(cluster_addr(&s_max, r)));
-    const int64_t safe_from = static_cast<int64_t>(last) - p.recent;
+    const Protect pr{static_cast<int>(max(static_cast<int64_t>(last) - p.recent, static_cast<int64_t>(-1))), p.sink};
 
     const bool held = per * kEvWarps <= key_cap, held_low = per * kEvWarps <= low_cap;
     uint16_t *my = s_key + warp * per, *my_low = s_low + warp * per;
-    auto key_of = [&](float w, int pos) -> uint32_t {
-        return (pos > safe_from || pos < p.sink) ? 0xFFFFFFFFu : weight_key(w);
-    };
-    // the lane's eight keys from row s on
-    auto make = [&](int s, uint32_t (&t)[8]) {
-        float w[8];
-        int pos[8];
-        load_rows<float>(w_in, s, hi, vec, 0.f, w);
-        load_rows<int>(p_in, s, hi, vec, 0, pos);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) t[e] = key_of(w[e], pos[e]);
-    };
-    auto pick = [](const uint16_t* from, uint32_t (&t)[8]) {
-        const uint4 v = *reinterpret_cast<const uint4*>(from);
-        t[0] = v.x & 0xFFFF; t[1] = v.x >> 16; t[2] = v.y & 0xFFFF; t[3] = v.y >> 16;
-        t[4] = v.z & 0xFFFF; t[5] = v.z >> 16; t[6] = v.w & 0xFFFF; t[7] = v.w >> 16;
-    };
-    // their upper halves, and their lower ones
-    auto upper = [&](int s, uint32_t (&t)[8]) {
-        if (held) {
-            pick(my + (s - lo), t);
-        } else {
-            make(s, t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] >>= 16;
-        }
-    };
-    auto lower = [&](int s, uint32_t (&t)[8]) {
-        if (held_low) {
-            pick(my_low + (s - lo), t);
-        } else {
-            make(s, t);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) t[e] &= 0xFFFF;
-        }
-    };
+    // halves of the lane's eight keys from row s on
+    auto upper = [&](int s) { return held ? *reinterpret_cast<const uint4*>(my + (s - lo)) : remade(w_in, p_in, s, pr, 16); };
+    auto lower = [&](int s) { return held_low ? *reinterpret_cast<const uint4*>(my_low + (s - lo)) : remade(w_in, p_in, s, pr, 0); };
     // of the eight rows from s on: bits of those below x
     auto bits_below = [](int s, int x) -> uint32_t { return x <= s ? 0u : x - s >= 8 ? 0xFFu : (1u << (x - s)) - 1; };
+
+    // the warp's list, where it has one: offsets of its rows from lo, and their keys
+    int listed = -1;
+    uint32_t* my_list = nullptr;
 
     // ---- the M-th largest key, from the top; bits 31..21, 20..16, 15..5, 4..0
     uint32_t prefix = 0, T = 0;
     int need = M, ties = 0;
     bool whole = false;        // every key from T + 1 on stays, no ties
+    {
+        Rows8 r, next;
+        if (lo + 8 * lane < hi) load_rows(w_in, p_in, lo + 8 * lane, r);
+        for (int r0 = lo; r0 < hi; r0 += kEvStep) {
+            const int s = r0 + 8 * lane;
+            if (s + kEvStep < hi) load_rows(w_in, p_in, s + kEvStep, next);       // the next step's, early
+            if (s < hi) {
+                const uint32_t in = bits_below(s, hi);
+                uint32_t t[8];
+                keys_of(pr, r, t);
+                if (held) *reinterpret_cast<uint4*>(my + (s - lo)) = halves(t, 16);
+                if (held_low) *reinterpret_cast<uint4*>(my_low + (s - lo)) = halves(t, 0);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if ((in >> e) & 1) atomicAdd(s_hist + (t[e] >> 21), 1);
+            }
+            r = next;
+        }
+    }
 #pragma unroll 1
     for (int pass = 0; pass < 4; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 16 : pass == 2 ? 5 : 0, bins = (pass & 1) ? 32 : kEvBins;
         int* hist = s_hist + (pass == 0 ? 0 : pass == 1 ? 2 * kEvBins : pass == 2 ? kEvBins : 2 * kEvBins + 32);
-        for (int r0 = lo; r0 < hi; r0 += kEvStep) {
-            const int s = r0 + 8 * lane;
-            const uint32_t in = bits_below(s, hi);
-            uint32_t t[8];
-            if (pass == 0) {
-                make(s, t);
-                auto pair = [&](int e, int sh) { return ((t[e] >> sh) & 0xFFFF) | ((t[e + 1] >> sh) << 16); };
-                if (held)
-                    *reinterpret_cast<uint4*>(my + (s - lo)) = make_uint4(pair(0, 16), pair(2, 16), pair(4, 16), pair(6, 16));
-                if (held_low)
-                    *reinterpret_cast<uint4*>(my_low + (s - lo)) = make_uint4(pair(0, 0), pair(2, 0), pair(4, 0), pair(6, 0));
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if ((in >> e) & 1) atomicAdd(hist + (t[e] >> 21), 1);
-                continue;
+        if (pass > 0 && listed >= 0) {
+            for (int e = lane; e < listed; e += 32) {
+                const uint32_t k = my_list[e];
+                if ((k >> (shift + ((pass & 1) ? 5 : 11))) == prefix) atomicAdd(hist + ((k >> shift) & (bins - 1)), 1);
             }
-            upper(s, t);
-            if (pass == 1) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if ((in >> e) & 1 && (t[e] >> 5) == prefix) atomicAdd(hist + (t[e] & 31), 1);
-                continue;
-            }
-            uint32_t same = 0, l[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) same |= (t[e] == (pass == 2 ? prefix : prefix >> 11) ? 1u : 0u) << e;
-            same &= in;
-            if (!same) continue;
-            lower(s, l);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (!((same >> e) & 1)) continue;
-                if (pass == 2) atomicAdd(hist + (l[e] >> 5), 1);
-                else if ((l[e] >> 5) == (prefix & (kEvBins - 1))) atomicAdd(hist + (l[e] & 31), 1);
+        } else if (pass > 0) {
+#pragma unroll 1
+            for (int s = lo + 8 * lane; s < hi; s += kEvStep) {
+                const uint4 up = upper(s);
+                uint32_t same = bits_below(s, hi);
+                if (pass == 1) same &= mark(up, [&](uint32_t t) { return (t >> 5) == prefix; });
+                else same &= mark(up, [&](uint32_t t) { return t == (pass == 2 ? prefix : prefix >> 11); });
+                if (!same) continue;
+                const uint4 low = pass == 1 ? up : lower(s);
+                for (; same; same &= same - 1) {
+                    const uint32_t l = half_of(low, __ffs(same) - 1);
+                    if (pass == 2) atomicAdd(hist + (l >> 5), 1);
+                    else if (pass == 1 || (l >> 5) == (prefix & (kEvBins - 1))) atomicAdd(hist + (l & 31), 1);
+                }
             }
         }
         sync_all(ranks);
@@ -217,12 +249,12 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
         int cnt[4] = {0, 0, 0, 0};
         const int top = bins - 1 - 4 * tid;
         if (top >= 0) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) cnt[e] = hist[top - e];
+            const int4 own = *reinterpret_cast<const int4*>(hist + top - 3);
+            cnt[0] = own.w, cnt[1] = own.z, cnt[2] = own.y, cnt[3] = own.x;
             for (int r = 0; r < ranks; ++r)
                 if (r != rank) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) cnt[e] += ld_cluster_s32(cluster_addr(hist + top - e, r));
+                    const int4 v = ld_cluster_v4(cluster_addr(hist + top - 3, r));
+                    cnt[0] += v.w, cnt[1] += v.z, cnt[2] += v.y, cnt[3] += v.x;
                 }
         }
         const int mine = cnt[0] + cnt[1] + cnt[2] + cnt[3];
@@ -245,6 +277,40 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
         const int inside = s_bin[2];
         need -= s_bin[1];
         prefix = (prefix << ((pass & 1) ? 5 : 11)) | static_cast<uint32_t>(s_bin[0]);
+        // Of the unit's rows, M - need + inside have uppermost bits that reach the threshold's.  Where
+        // those are few, a warp behind the budget lists its own: an offset of two bytes where their keys
+        // were, and a key of four, in the two bytes that each of its rows has.
+        if (pass == 0 && held && lo >= M && hi > lo && 4 * static_cast<int64_t>(M - need + inside) <= n) {
+            listed = 0;
+            bool room = true;
+#pragma unroll 1
+            for (int r0 = lo; r0 < hi && room; r0 += kEvStep) {       // offsets go where keys were read already
+                const int s = r0 + 8 * lane;
+                uint32_t some = 0;
+                if (s < hi) some = mark(upper(s), [&](uint32_t t) { return (t >> 5) >= prefix; }) & bits_below(s, hi);
+                int at = excl_scan(__popc(some), lane);
+                const int all = __shfl_sync(0xffffffffu, at + __popc(some), 31);
+                at += listed;
+                listed += all;
+                room = 3 * listed <= per;
+                __syncwarp();
+                for (; some && room; some &= some - 1) my[at++] = static_cast<uint16_t>(s + __ffs(some) - 1 - lo);
+                __syncwarp();
+            }
+            if (room) {
+                my_list = reinterpret_cast<uint32_t*>(my + per) - listed;
+                for (int e = lane; e < listed; e += 32) {
+                    const int row = lo + my[e];
+                    my_list[e] = pr.key(__ldg(w_in + row), __ldg(p_in + row));
+                }
+            } else {            // they crowd in this warp's rows: its keys again
+                listed = -1;
+#pragma unroll 1
+                for (int s = lo + 8 * lane; s < hi; s += kEvStep)
+                    *reinterpret_cast<uint4*>(my + (s - lo)) = remade(w_in, p_in, s, pr, 16);
+            }
+            __syncwarp();
+        }
         if (inside == need && prefix != 0) {          // the whole bin stays
             T = (prefix << shift) - 1;
             whole = true;
@@ -259,127 +325,157 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
     const bool upper_alone = whole && (T & 0xFFFFu) == 0xFFFFu;     // no key of upper half T16 stays
     // which of the lane's eight rows from s on lie above the threshold, and which on it
     auto grade = [&](int s, uint32_t& gt, uint32_t& tie) {
-        uint32_t t[8], l[8], same = 0;
-        upper(s, t);
         gt = tie = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            gt |= (t[e] > T16 ? 1u : 0u) << e;
-            same |= (t[e] == T16 ? 1u : 0u) << e;
-        }
-        const uint32_t in = bits_below(s, hi);
-        gt &= in;
-        same &= in;
+        if (s >= hi) return;
+        const uint4 up = upper(s);
+        const uint32_t in = bits_below(s, hi), t16 = T16, t0 = T & 0xFFFFu;
+        gt = in & mark(up, [&](uint32_t t) { return t > t16; });
+        uint32_t same = in & mark(up, [&](uint32_t t) { return t == t16; });
         if (!same || upper_alone) return;
-        lower(s, l);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (!((same >> e) & 1)) continue;
-            if (l[e] > (T & 0xFFFFu)) gt |= 1u << e;
-            else if (l[e] == (T & 0xFFFFu) && !whole) tie |= 1u << e;
+        const uint4 low = lower(s);
+        for (; same; same &= same - 1) {
+            const int e = __ffs(same) - 1;
+            const uint32_t l = half_of(low, e);
+            if (l > t0) gt |= 1u << e;
+            else if (l == t0 && !whole) tie |= 1u << e;
         }
     };
 
-    // ---- rows of each kind per warp: given up and tied below M, kept for sure and tied behind
-    int n_low = 0, n_tl = 0, n_gt = 0, n_th = 0;
-    for (int r0 = lo; r0 < hi; r0 += kEvStep) {
-        const int s = r0 + 8 * lane;
-        uint32_t gt, tie;
-        grade(s, gt, tie);
-        const uint32_t in = bits_below(s, hi), low = bits_below(s, M);
-        n_low += __popc(in & low & ~(gt | tie));
-        n_tl += __popc(low & tie);
-        n_gt += __popc(~low & gt);
-        n_th += __popc(~low & tie);
-    }
-    n_low = __reduce_add_sync(0xffffffffu, n_low);
-    n_tl = __reduce_add_sync(0xffffffffu, n_tl);
-    n_gt = __reduce_add_sync(0xffffffffu, n_gt);
-    n_th = __reduce_add_sync(0xffffffffu, n_th);
-    if (lane == 0) {
-        s_cnt[0][warp] = n_low;
-        s_cnt[1][warp] = n_tl;
-        s_cnt[2][warp] = n_gt;
-        s_cnt[3][warp] = n_th;
-    }
-    __syncthreads();
-    if (warp < 4) {
-        const int x = __reduce_add_sync(0xffffffffu, lane < kEvWarps ? s_cnt[warp][lane] : 0);
-        if (lane == 0) s_tot[warp] = x;
-    }
-    sync_all(ranks);
-    if (warp == 0) {
-        // what lies in the slices before this one (rows below M come first in every slice)
-        int tie0 = 0, hole0 = 0, src0 = 0;
-        for (int r = 0; r < rank; ++r) {
-            const int a = ld_cluster_s32(cluster_addr(&s_tot[0], r)), tl = ld_cluster_s32(cluster_addr(&s_tot[1], r));
-            const int g = ld_cluster_s32(cluster_addr(&s_tot[2], r)), th = ld_cluster_s32(cluster_addr(&s_tot[3], r));
-            const int left = max(0, ties - tie0), kl = min(tl, left), kh = min(th, left - kl);
-            hole0 += a + tl - kl;
-            src0 += g + kh;
-            tie0 += tl + th;
-        }
-        const int w = lane % kEvWarps;
-        const bool own = lane < kEvWarps;
-        const int a = own ? s_cnt[0][w] : 0, tl = own ? s_cnt[1][w] : 0, g = own ? s_cnt[2][w] : 0, th = own ? s_cnt[3][w] : 0;
-        const int t0 = tie0 + excl_scan(tl + th, lane);
-        const int left = max(0, ties - t0), kl = min(tl, left), kh = min(th, left - kl);
-        const int holes = a + tl - kl, srcs = g + kh;
-        const int h0 = hole0 + excl_scan(holes, lane), s0 = src0 + excl_scan(srcs, lane);
-        if (own) {
-            s_tie[w] = t0;
-            s_hole[w] = h0;
-            s_src[w] = s0;
-        }
-        if (rank == ranks - 1 && lane == kEvWarps - 1) p.count[u] = s0 + srcs;
-    }
-    sync_all(ranks);       // and no CTA leaves while another reads its counts
-    int tie_at = s_tie[warp], hole_at = s_hole[warp], src_at = s_src[warp];
+    // ---- twice over the rows: count those of each kind per warp (given up and tied below M, kept for
+    // sure and tied behind), and once it is known where each warp's begin in the lists, write them
+    int n_low = 0, n_tl = 0, n_gt = 0, n_th = 0, tie_at = 0, hole_at = 0, src_at = 0;
     int32_t* to = p.to + static_cast<int64_t>(u) * p.list_cap;
     int32_t* of = p.of + static_cast<int64_t>(u) * p.list_cap;
-    for (int r0 = lo; r0 < hi; r0 += kEvStep) {
-        const int s = r0 + 8 * lane;
-        uint32_t kept, tie;
-        grade(s, kept, tie);
-        if (__any_sync(0xffffffffu, tie)) {
-            int t = tie_at + excl_scan(__popc(tie), lane);
-            tie_at += __reduce_add_sync(0xffffffffu, __popc(tie));
+#pragma unroll 1
+    for (int turn = 0; turn < 2; ++turn) {
+        for (int e0 = 0; e0 < listed; e0 += 32) {
+            const bool in = e0 + lane < listed;
+            const uint32_t k = in ? my_list[e0 + lane] : 0, below = (1u << lane) - 1;
+            const bool tie = in && !whole && k == T;
+            const uint32_t tb = __ballot_sync(0xffffffffu, tie);
+            if (turn == 0) {
+                n_gt += in && k > T ? 1 : 0;
+                n_th += tie ? 1 : 0;
+                continue;
+            }
+            const bool kept = in && (k > T || (tie && tie_at + __popc(tb & below) < ties));
+            const uint32_t kb = __ballot_sync(0xffffffffu, kept);
+            const int at = src_at + __popc(kb & below);
+            if (kept && at < p.list_cap) of[at] = lo + my[e0 + lane];
+            tie_at += __popc(tb);
+            src_at += __popc(kb);
+        }
+#pragma unroll 1
+        for (int r0 = listed < 0 ? lo : hi; r0 < hi; r0 += kEvStep) {
+            const int s = r0 + 8 * lane;
+            uint32_t kept, tie;
+            grade(s, kept, tie);
+            const uint32_t in = bits_below(s, hi), low = bits_below(s, M);
+            if (turn == 0) {
+                n_low += __popc(in & low & ~(kept | tie));
+                n_tl += __popc(low & tie);
+                n_gt += __popc(~low & kept);
+                n_th += __popc(~low & tie);
+                continue;
+            }
+            if (__any_sync(0xffffffffu, tie)) {
+                int t = tie_at + excl_scan(__popc(tie), lane);
+                tie_at += __reduce_add_sync(0xffffffffu, __popc(tie));
+                for (; tie; tie &= tie - 1, ++t)
+                    if (t < ties) kept |= tie & (0 - tie);
+            }
+            uint32_t hole = in & low & ~kept, src = kept & ~low;
+            const uint32_t stay = kept & low;
+            if (__any_sync(0xffffffffu, hole | src)) {
+                const int both = __popc(hole) | __popc(src) << 16;       // at most 256 of each
+                const int at = excl_scan(both, lane);
+                const int all = __reduce_add_sync(0xffffffffu, both);
+                int ha = hole_at + (at & 0xFFFF), sa = src_at + (at >> 16);
+                hole_at += all & 0xFFFF;
+                src_at += all >> 16;
+                for (; hole; hole &= hole - 1, ++ha)
+                    if (ha < p.list_cap) to[ha] = s + __ffs(hole) - 1;
+                for (; src; src &= src - 1, ++sa)
+                    if (sa < p.list_cap) of[sa] = s + __ffs(src) - 1;
+            }
+            if (stay && (copy_w || copy_p)) {
+                Rows8 r;
+                load_rows(w_in, p_in, s, r);
+                if (stay == 0xFFu) {
+                    if (copy_w) {
+                        float4* out = reinterpret_cast<float4*>(p.weight_out + base + s);
+                        out[0] = r.w0;
+                        out[1] = r.w1;
+                    }
+                    if (copy_p) {
+                        int4* out = reinterpret_cast<int4*>(p.position_out + base + s);
+                        out[0] = r.p0;
+                        out[1] = r.p1;
+                    }
+                } else {
+                    const float w[8] = {r.w0.x, r.w0.y, r.w0.z, r.w0.w, r.w1.x, r.w1.y, r.w1.z, r.w1.w};
+                    const int q[8] = {r.p0.x, r.p0.y, r.p0.z, r.p0.w, r.p1.x, r.p1.y, r.p1.z, r.p1.w};
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if ((tie >> e) & 1) {
-                    if (t < ties) kept |= 1u << e;
-                    ++t;
+                    for (int e = 0; e < 8; ++e) {
+                        if (!((stay >> e) & 1)) continue;
+                        if (copy_w) p.weight_out[base + s + e] = w[e];
+                        if (copy_p) p.position_out[base + s + e] = q[e];
+                    }
                 }
-        }
-        const uint32_t in = bits_below(s, hi), low = bits_below(s, M);
-        const uint32_t hole = in & low & ~kept, src = kept & ~low;
-        if (!__any_sync(0xffffffffu, hole | src | (kept & low))) continue;
-        const int both = __popc(hole) | __popc(src) << 16;       // at most 256 of each
-        const int at = excl_scan(both, lane);
-        const int all = __reduce_add_sync(0xffffffffu, both);
-        int ha = hole_at + (at & 0xFFFF), sa = src_at + (at >> 16);
-        hole_at += all & 0xFFFF;
-        src_at += all >> 16;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if ((hole >> e) & 1) {
-                if (ha < p.list_cap) to[ha] = s + e;
-                ++ha;
-            }
-            if ((src >> e) & 1) {
-                if (sa < p.list_cap) of[sa] = s + e;
-                ++sa;
-            }
-            if ((kept & low) >> e & 1) {
-                if (copy_w) p.weight_out[base + s + e] = w_in[s + e];
-                if (copy_p) p.position_out[base + s + e] = p_in[s + e];
             }
         }
+        if (turn == 1) break;
+        n_low = __reduce_add_sync(0xffffffffu, n_low);
+        n_tl = __reduce_add_sync(0xffffffffu, n_tl);
+        n_gt = __reduce_add_sync(0xffffffffu, n_gt);
+        n_th = __reduce_add_sync(0xffffffffu, n_th);
+        if (lane == 0) {
+            s_cnt[0][warp] = n_low;
+            s_cnt[1][warp] = n_tl;
+            s_cnt[2][warp] = n_gt;
+            s_cnt[3][warp] = n_th;
+        }
+        __syncthreads();
+        if (warp < 4) {
+            const int x = __reduce_add_sync(0xffffffffu, lane < kEvWarps ? s_cnt[warp][lane] : 0);
+            if (lane == 0) s_tot[warp] = x;
+        }
+        sync_all(ranks);
+        if (warp == 0) {
+            // what lies in the slices before this one (rows below M come first in every slice)
+            int tie0 = 0, hole0 = 0, src0 = 0;
+            for (int r = 0; r < rank; ++r) {
+                const int a = ld_cluster_s32(cluster_addr(&s_tot[0], r)), tl = ld_cluster_s32(cluster_addr(&s_tot[1], r));
+                const int g = ld_cluster_s32(cluster_addr(&s_tot[2], r)), th = ld_cluster_s32(cluster_addr(&s_tot[3], r));
+                const int left = max(0, ties - tie0), kl = min(tl, left), kh = min(th, left - kl);
+                hole0 += a + tl - kl;
+                src0 += g + kh;
+                tie0 += tl + th;
+            }
+            const int w = lane % kEvWarps;
+            const bool own = lane < kEvWarps;
+            const int a = own ? s_cnt[0][w] : 0, tl = own ? s_cnt[1][w] : 0, g = own ? s_cnt[2][w] : 0, th = own ? s_cnt[3][w] : 0;
+            const int t0 = tie0 + excl_scan(tl + th, lane);
+            const int left = max(0, ties - t0), kl = min(tl, left), kh = min(th, left - kl);
+            const int holes = a + tl - kl, srcs = g + kh;
+            const int h0 = hole0 + excl_scan(holes, lane), s0 = src0 + excl_scan(srcs, lane);
+            if (own) {
+                s_tie[w] = t0;
+                s_hole[w] = h0;
+                s_src[w] = s0;
+            }
+            if (rank == ranks - 1 && lane == kEvWarps - 1) p.count[u] = s0 + srcs;
+        }
+        sync_all(ranks);       // and no CTA leaves while another reads its counts
+        tie_at = s_tie[warp];
+        hole_at = s_hole[warp];
+        src_at = s_src[warp];
     }
 }
 
-constexpr int kMvThreads = 256;
-constexpr int kMvPairs = 4;        // rows per warp and round
+constexpr int kMvThreads = 128;
+constexpr int kMvRows = 32;        // rows of a warp's turn: a lane looks each up
+constexpr int kMvDeep = 8;         // of them, rows whose words are in flight together
 
 __global__ void __launch_bounds__(kMvThreads) k_evict_move(const __grid_constant__ EvictParams p, int parts) {
     pdl_wait();
@@ -390,40 +486,43 @@ __global__ void __launch_bounds__(kMvThreads) k_evict_move(const __grid_constant
     const int64_t base = static_cast<int64_t>(u) * p.row_pitch;
     const int32_t* to = p.to + static_cast<int64_t>(u) * p.list_cap;
     const int32_t* of = p.of + static_cast<int64_t>(u) * p.list_cap;
-    const int step = parts * (kMvThreads / 32) * kMvPairs;
-    const int kw = p.d * p.es / 16, vw = p.d * p.es_v / 16, mask = (1 << p.c.lg) - 1;
+    const int step = parts * (kMvThreads / 32) * kMvRows;
+    const int kw = p.d * p.es / 16, words = kw + p.d * p.es_v / 16, mask = (1 << p.c.lg) - 1;
     uint8_t* kp = static_cast<uint8_t*>(p.c.k) + h * p.c.k_head * p.es;
     uint8_t* vp = static_cast<uint8_t*>(p.c.v) + h * p.c.v_head * p.es_v;
-    for (int i0 = (part * (kMvThreads / 32) + (threadIdx.x >> 5)) * kMvPairs; i0 < cnt; i0 += step) {
-        // lane j < kMvPairs looks pair j up
-        int64_t kd = -1, ks = 0, vd = 0, vs = 0;
-        if (lane < kMvPairs && i0 + lane < cnt) {
-            const int d = to[i0 + lane], s = of[i0 + lane];
-            const int pd = page_of(p.c, b, d, g_err, 722), ps = page_of(p.c, b, s, g_err, 723);
+    for (int i0 = (part * (kMvThreads / 32) + (threadIdx.x >> 5)) * kMvRows; i0 < cnt; i0 += step) {
+        int pd = -1, ps = -1, d = 0, s = 0;
+        if (i0 + lane < cnt) {
+            d = to[i0 + lane];
+            s = of[i0 + lane];
+            pd = page_of(p.c, b, d, g_err, 722);
+            ps = page_of(p.c, b, s, g_err, 723);
             p.weight_out[base + d] = p.weight[base + s];
             p.position_out[base + d] = p.position[base + s];
-            if (pd >= 0 && ps >= 0) {
-                kd = (pd * p.c.k_page + (d & mask) * p.c.k_row) * p.es;
-                ks = (ps * p.c.k_page + (s & mask) * p.c.k_row) * p.es;
-                vd = (pd * p.c.v_page + (d & mask) * p.c.v_row) * p.es_v;
-                vs = (ps * p.c.v_page + (s & mask) * p.c.v_row) * p.es_v;
-            }
+            if (ps < 0) pd = -1;
+            d &= mask;
+            s &= mask;
         }
-        // 16-byte words of the key and value rows, lane-strided
-        for (int w = lane; w < ((kw + vw + 31) & ~31); w += 32) {
-            uint4 x[kMvPairs];
+        const int rows = min(kMvRows, cnt - i0);
+        for (int w = lane; w < ((words + 31) & ~31); w += 32) {      // 16-byte words of a key row and its value row
+            const bool key = w < kw;
+            uint8_t* pool = (key ? kp : vp) + (key ? w : w - kw) * 16;
+            const int64_t page = (key ? p.c.k_page : p.c.v_page) * (key ? p.es : p.es_v);
+            const int64_t row = (key ? p.c.k_row : p.c.v_row) * (key ? p.es : p.es_v);
+            for (int j0 = 0; j0 < rows; j0 += kMvDeep) {
+                uint4 x[kMvDeep];
+                int64_t dst[kMvDeep];
 #pragma unroll
-            for (int j = 0; j < kMvPairs; ++j) {
-                const int64_t d = __shfl_sync(0xffffffffu, kd, j), s = __shfl_sync(0xffffffffu, ks, j);
-                const int64_t sv = __shfl_sync(0xffffffffu, vs, j);
-                if (d >= 0 && w < kw + vw)
-                    x[j] = __ldg(reinterpret_cast<const uint4*>(w < kw ? kp + s : vp + sv) + (w < kw ? w : w - kw));
-            }
+                for (int j = 0; j < kMvDeep; ++j) {
+                    const int at = (j0 + j) & 31;
+                    const int to_page = __shfl_sync(0xffffffffu, pd, at), of_page = __shfl_sync(0xffffffffu, ps, at);
+                    const int to_row = __shfl_sync(0xffffffffu, d, at), of_row = __shfl_sync(0xffffffffu, s, at);
+                    dst[j] = to_page >= 0 && w < words ? to_page * page + to_row * row : -1;
+                    if (dst[j] >= 0) x[j] = __ldg(reinterpret_cast<const uint4*>(pool + of_page * page + of_row * row));
+                }
 #pragma unroll
-            for (int j = 0; j < kMvPairs; ++j) {
-                const int64_t d = __shfl_sync(0xffffffffu, kd, j), dv = __shfl_sync(0xffffffffu, vd, j);
-                if (d >= 0 && w < kw + vw)
-                    *(reinterpret_cast<uint4*>(w < kw ? kp + d : vp + dv) + (w < kw ? w : w - kw)) = x[j];
+                for (int j = 0; j < kMvDeep; ++j)
+                    if (dst[j] >= 0) *reinterpret_cast<uint4*>(pool + dst[j]) = x[j];
             }
         }
     }
@@ -456,7 +555,7 @@ int launch_evict(const EvictParams& p, int nsm, cudaStream_t s) {
     cfg.numAttrs = ranks > 1 ? 1 : 0;
     if (cudaLaunchKernelEx(&cfg, k_evict_select, p, ranks, key_cap, low_cap) != cudaSuccess) return -1;
     // CTAs per unit for the rows that move
-    const int rows = (kMvThreads / 32) * kMvPairs;
+    const int rows = (kMvThreads / 32) * kMvRows;
     int64_t parts = (static_cast<int64_t>(p.list_cap) + rows - 1) / rows;
     const int64_t most = (16 * nsm + U - 1) / U;
     if (parts > most) parts = most;

@@ -296,7 +296,10 @@ int shadowkv_paged_evict(const skv_paged_evict_args* a, skv_stream stream) {
     if (int rc = check_cache(c, true)) return rc;
     if (!c.lens || !a->weight || !a->position || !a->weight_out || !a->position_out || !a->lens_out || !a->workspace)
         return SKV_ERR_INVALID;
-    if (a->row_pitch < static_cast<int64_t>(c.max_pages) * c.page_size) return SKV_ERR_INVALID;
+    if (a->row_pitch < static_cast<int64_t>(c.max_pages) * c.page_size || a->row_pitch % 4) return SKV_ERR_INVALID;
+    for (const void* q : {static_cast<const void*>(a->weight), static_cast<const void*>(a->position),
+                          static_cast<const void*>(a->weight_out), static_cast<const void*>(a->position_out)})
+        if (!aligned16(q)) return SKV_ERR_INVALID;
     if (!aligned16(a->workspace) || a->workspace_bytes < w.bytes) return SKV_ERR_INVALID;
     Device dev;
     if (int rc = device(&dev)) return rc;

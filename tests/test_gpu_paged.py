@@ -507,6 +507,21 @@ def test_eviction_of_slices_beyond_shared_memory():
     assert torch.equal(k.view(-1, 64)[:budget], pool.view(-1, 64)[rows]) and torch.equal(k, v) and int(l_out) == budget
 
 
+@pytest.mark.parametrize("where", ["front", "behind", "spread"])
+def test_eviction_where_the_heavy_rows_crowd(where):
+    """A small budget out of a long sequence, with the rows that can stay in one place: within the
+    budget's own rows, in one warp's rows behind it, or everywhere; near-equal weights, so that
+    most of the search happens in the lower bits."""
+    n, budget = 20000, 700
+    c = Paged("bf16", [n, 15], 1, 64, 64, seed=40)
+    g = torch.Generator().manual_seed(41)
+    weight = torch.rand((2, 1, c.rows), generator=g) * 1e-3
+    at = {"front": torch.arange(0, 900), "behind": torch.arange(9000, 9900), "spread": torch.randperm(n, generator=g)[:900]}[where]
+    weight[0, 0, at] = 1.0 + torch.randint(0, 200, (900,), generator=g) * 2.0 ** -20
+    position = torch.arange(c.rows, dtype=torch.int32).expand(2, 1, -1).contiguous()
+    run_evict(c, weight.cuda(), position.cuda(), budget, 0, 0, False)
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
