@@ -485,8 +485,7 @@ typedef struct {
  * the caller's to advance.  No two tokens of a call may name the same row, nor
  * two sequences share the page of a row that is written.
  *
- * A token with a negative position is padding: nothing of it is read or
- * written.  One with a negative seq is not appended.  An index or seq beyond
+ * A token with a negative position is padding: nothing of it is written.  One with a negative seq is not appended.  An index or seq beyond
  * the cache, or a bad page, sets the error word and skips the append.
  * q_out may be q and k_out may be k (same strides); other overlaps are not
  * allowed.  tokens == 0 does nothing.

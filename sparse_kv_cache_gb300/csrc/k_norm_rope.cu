@@ -22,6 +22,7 @@ namespace skv {
 static __device__ int g_err[2];
 
 constexpr int kNrThreads = 128;
+constexpr int kNrOcc = 6;         // CTAs per SM
 constexpr int kNrMaxTok = 16;     // tokens of a CTA at most
 
 // 16 elements of a row as they lie in memory: 8 at o1, 8 at o2
@@ -62,7 +63,7 @@ __device__ __forceinline__ void put(float* p, int o1, int o2, const Raw<float>& 
 }
 
 template <typename T, int D, bool kE5M2>
-__global__ void __launch_bounds__(kNrThreads, 6) k_norm_rope(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kNrThreads, kNrOcc) k_norm_rope(const __grid_constant__ NormRopeParams p) {
     constexpr int kLanes = D / 16;                  // lanes of a row
     constexpr int kDeep = sizeof(T) == 2 ? 3 : 2;   // rows of a thread whose loads are in flight at once
     __shared__ __align__(16) float s_cos[kNrMaxTok * D / 2], s_sin[kNrMaxTok * D / 2];
@@ -94,6 +95,7 @@ __global__ void __launch_bounds__(kNrThreads, 6) k_norm_rope(const __grid_consta
     float cs[8], sn[8];
     int page = -1;
     for (int s0 = 0; s0 < slots; s0 += kDeep) {       // uniform: every lane takes part in the shuffles
+        // (asked for before the position is known: a padding token's rows are there to be read too)
         Raw<T> raw[kDeep];
 #pragma unroll
         for (int i = 0; i < kDeep; ++i) {
@@ -101,10 +103,10 @@ __global__ void __launch_bounds__(kNrThreads, 6) k_norm_rope(const __grid_consta
             const int s = s0 + i;
             if (s < q_slots) {
                 const int h = s * p.groups + g;
-                if (pos >= 0 && h < p.nq) fetch(raw[i], q + h * p.q_head, o1, o2);
+                if (t < nt && h < p.nq) fetch(raw[i], q + h * p.q_head, o1, o2);
             } else if (s < slots) {
                 const int h = (s - q_slots) * p.groups + g;
-                if (pos >= 0 && h < n_kv) fetch(raw[i], h < H ? k + h * p.k_head : v + (h - H) * p.v_head, o1, o2);
+                if (t < nt && h < n_kv) fetch(raw[i], h < H ? k + h * p.k_head : v + (h - H) * p.v_head, o1, o2);
             }
         }
         if (s0 == 0) {     // the angles, while the first rows are on their way
@@ -210,14 +212,18 @@ static int launch_nr(NormRopeParams p, int nsm, cudaStream_t s) {
     const int n_kv = p.c.H * (p.c.k ? 2 : 1);
     // lane groups per token.  A decode step has few tokens: all of a CTA's groups work on one.  A
     // prompt takes the number that leaves the fewest groups without a head, and of equals the
-    // smallest from four on (each thread then has more rows of a token whose angles it holds).
+    // smallest from four on (each thread then has more rows of a token whose angles it holds: 32K
+    // tokens of 32 + 2 x 8 heads in 141 us against 143 with two and 151 with eight), or from two on
+    // where four would make less than two waves of CTAs (5K tokens of 16 + 2 x 2 heads: 14.7 us
+    // against 16.2).
     p.groups = kRows;
     if (p.tokens > 2 * nsm) {
+        const int least = p.tokens / (kRows / 4) <= 2 * kNrOcc * nsm ? 2 : 4;
         int best = 1 << 30;
         for (int g = kRows; g >= 1; g /= 2) {
             if (kRows / g > kNrMaxTok) break;
             const int spent = ((p.nq + g - 1) / g + (n_kv + g - 1) / g) * g;
-            if (spent < best || (spent == best && g >= 4)) best = spent, p.groups = g;
+            if (spent < best || (spent == best && g >= least)) best = spent, p.groups = g;
         }
     }
     const int per = kRows / p.groups, grid = (p.tokens + per - 1) / per;
