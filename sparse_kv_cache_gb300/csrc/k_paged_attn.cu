@@ -79,6 +79,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ float4 ld_cluster_v4f(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -721,6 +729,88 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
         }
 }
 
+// Short sequences of few units, where the latency of a step counts: a cluster of CTAs per unit, whose
+// warps share its rows evenly.  No search for the place, no records and no second kernel: each CTA
+// joins its warps' shares, and the cluster joins the CTAs' through distributed shared memory.
+template <class Tile, int D, bool kF32, int G, int kOcc>
+__global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid_constant__ PagedAttnParams p, int ranks) {
+    __shared__ __align__(16) JoinSmem<D, G> js;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int u = blockIdx.x / ranks, rank = ranks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int b = u / p.c.H, h = u % p.c.H;
+    const int rows = rows_of(p.c, b, g_err, 711);
+    const int nt = tiles_of(rows), parts = ranks * kPaWarps, part = rank * kPaWarps + warp;
+    const int t0 = static_cast<int>(static_cast<int64_t>(nt) * part / parts);
+    const int t1 = static_cast<int>(static_cast<int64_t>(nt) * (part + 1) / parts);
+    Tile tile;
+    tile.load_q(p, b, h, js.o[2 * warp + 1][0]);
+    tile.reset();
+    if (t0 < t1) tile.share(p, b, h, t0 * kPaTile, min(rows, t1 * kPaTile), nullptr);
+    tile.finish(p, b, h, false, js, 2 * warp);
+    __syncthreads();
+    // the CTA's share, in slot 1: of the four warps' in order
+    if (tid < G && tid < p.G) {
+        float m = -CUDART_INF_F, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kPaWarps; ++w) m = fmaxf(m, js.m[2 * w][tid]);
+#pragma unroll
+        for (int w = 0; w < kPaWarps; ++w) {
+            const float f = share_weight(js.m[2 * w][tid], js.l[2 * w][tid], m);
+            js.w[w][tid] = f;
+            l = fmaf(js.l[2 * w][tid], f, l);
+        }
+        js.m[1][tid] = m;
+        js.l[1][tid] = l;
+    }
+    __syncthreads();
+    for (int k = tid; k < p.G * (D / 4); k += kPaThreads) {
+        const int g = k / (D / 4), dim = 4 * (k % (D / 4));
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kPaWarps; ++w) {
+            const float f = js.w[w][g];
+            const float4 v = *reinterpret_cast<const float4*>(&js.o[2 * w][g][dim]);
+            x[0] = fmaf(v.x, f, x[0]);
+            x[1] = fmaf(v.y, f, x[1]);
+            x[2] = fmaf(v.z, f, x[2]);
+            x[3] = fmaf(v.w, f, x[3]);
+        }
+        *reinterpret_cast<float4*>(&js.o[1][g][dim]) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+    if (ranks > 1) cluster_sync_all();
+    else __syncthreads();
+    // every CTA of the cluster writes a part of the result
+    for (int k = tid * ranks + rank; k < p.G * (D / 4); k += kPaThreads * ranks) {
+        const int g = k / (D / 4), dim = 4 * (k % (D / 4));
+        float m = -CUDART_INF_F, l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < ranks; ++r) m = fmaxf(m, ranks > 1 ? ld_cluster_f32(cluster_addr(&js.m[1][g], r)) : js.m[1][g]);
+        for (int r = 0; r < ranks; ++r) {
+            float rm, rl;
+            float4 v;
+            if (ranks > 1) {
+                rm = ld_cluster_f32(cluster_addr(&js.m[1][g], r));
+                rl = ld_cluster_f32(cluster_addr(&js.l[1][g], r));
+                v = ld_cluster_v4f(cluster_addr(&js.o[1][g][dim], r));
+            } else {
+                rm = js.m[1][g];
+                rl = js.l[1][g];
+                v = *reinterpret_cast<const float4*>(&js.o[1][g][dim]);
+            }
+            const float f = share_weight(rm, rl, m);
+            l = fmaf(rl, f, l);
+            x[0] = fmaf(v.x, f, x[0]);
+            x[1] = fmaf(v.y, f, x[1]);
+            x[2] = fmaf(v.z, f, x[2]);
+            x[3] = fmaf(v.w, f, x[3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = l == 0.f ? 0.f : x[e] / l;
+        store4<kF32>(p, b, h, g, dim, x);
+        if (dim == 0) note(p, b, h, g, m, l);
+    }
+    if (ranks > 1) cluster_sync_all();       // no CTA leaves while another reads its share
+}
+
 // Joins the records of the units that lie in more than one CTA's range: row i of the grid those of
 // the unit that ends in CTA i's range and began before it (p.joint says which, if any).  The grid's
 // y dimension deals the heads out.
@@ -930,8 +1020,37 @@ constexpr int kWeighOcc = 3;               // CTAs of k_paged_weigh per CTA of k
 
 int paged_attn_ctas(int dtype, int nsm) { return nsm * (dtype == SKV_F32 ? kOccF32 : kOccTC); }
 
+// CTAs of a unit's cluster, or 0: the general form.  The cluster form serves a step whose units leave
+// SMs idle and whose longest possible sequence takes a warp no more than kClusterTiles tiles.
+constexpr int kClusterTiles = 8;
+static int cluster_ranks(const PagedAttnParams& p, int ncta) {
+    if (p.weight_out) return 0;
+    const int64_t U = static_cast<int64_t>(p.c.batch) * p.c.H, tiles = (p.c.cap + kPaTile - 1) / kPaTile;
+    int ranks = 1;
+    while (ranks < 16 && tiles > ranks * kPaWarps && 2 * U * ranks <= ncta) ranks *= 2;
+    return U * ranks <= ncta && tiles <= static_cast<int64_t>(ranks) * kPaWarps * kClusterTiles ? ranks : 0;
+}
+
+template <class Tile, int D, bool kF32, int G, int kOcc>
+static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
+    auto kernel = k_paged_cluster<Tile, D, kF32, G, kOcc>;
+    if (ranks > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return -1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.c.batch) * p.c.H * ranks);
+    cfg.blockDim = dim3(kPaThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ranks > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, p, ranks) == cudaSuccess ? 0 : -1;
+}
+
 template <class Tile, int D, bool kF32, int G, int kOcc>
 static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
+    if (const int ranks = cluster_ranks(p, ncta)) return launch_cluster<Tile, D, kF32, G, kOcc>(p, ranks, s);
     // no more CTAs than there can be tiles for their warps
     const int64_t tiles = static_cast<int64_t>(p.c.batch) * p.c.H * ((p.c.cap + kPaTile - 1) / kPaTile);
     const int64_t most = (tiles + kPaWarps - 1) / kPaWarps;

@@ -77,6 +77,9 @@ def queries(c, G, seed=1, scale=1.0):
     ("bf16", 8, 2, 128, 8, "hnd", [63, 64, 65, 0, 127, 128, 129]),
     ("bf16", 3, 3, 128, 32, "nhd", [1000, 0, 0, 5, 333]),
     ("bf16", 7, 1, 64, 1024, "hnd", [2049, 1023]),
+    ("bf16", 8, 1, 128, 16, "hnd", [8190]),
+    ("f32", 3, 2, 128, 16, "hnd", [6000, 0, 17]),
+    ("fp8", 4, 1, 128, 16, "hnd", [2000] * 30 + [0, 3]),
     ("bf16", 2, 2, 128, 64, "nhd", [40000, 1, 0, 700]),        # one sequence over most of the CTAs
     ("bf16", 5, 8, 128, 16, "hnd", [300] * 40 + [0] * 200),    # several units per CTA, idle sequences behind
     ("bf16", 4, 1, 64, 16, "hnd", [0] * 150 + [77] + [0] * 150 + [3000]),
@@ -92,6 +95,11 @@ def queries(c, G, seed=1, scale=1.0):
 def test_attention_matches_float64(kind, G, heads, d, ps, layout, lens):
     c = Paged(kind, lens, heads, d, ps, layout, seed=len(lens) + G)
     q = queries(c, G)
+    # a table with room for far longer sequences: steps of few short ones are then split another way
+    wide = torch.cat([c.table, torch.full((len(lens), 16384 // ps), -1, dtype=torch.int32, device="cuda")], 1)
+    out, lse = torch.full_like(q, float("nan")), torch.full(q.shape[:2], float("nan"), device="cuda")
+    skv.paged_attention(q, c.k, c.v, wide, c.lens, out, lse)
+    check_all(c, q, out, lse)
     for weigh in (False, True):
         out = torch.full_like(q, float("nan"))
         lse = torch.full(q.shape[:2], float("nan"), device="cuda")
