@@ -519,17 +519,22 @@ struct TileF32 {
         const int lane = threadIdx.x & 31, hl = lane & 15, half = lane >> 4, mask = (1 << p.c.lg) - 1;
         const float* kb = static_cast<const float*>(p.c.k) + h * p.c.k_head;
         const float* vb = static_cast<const float*>(p.c.v) + h * p.c.v_head;
-        PageIds now{-1, -1};
-        int t = 32;
-        for (int row = row0; row < end; row += kPaTile, ++t) {
-            if (t == 32) {
-                t = 0;
-                now = page_ids(p.c, b, row + lane * kPaTile, end);
-            }
-            const int ida = __shfl_sync(0xffffffffu, now.a, t), idb = __shfl_sync(0xffffffffu, now.b, t);
-            const int id = half ? idb : ida, mine = row + 8 * half;      // this half-warp's eight rows
-            float x[8][4 * kV];
-            load(kb, p.c.k_page, p.c.k_row, mask, mine, end, id, x);
+        // the keys of the next tile and the values of this one are on their way during the scores, where
+        // registers allow it (all but eight heads of 128 dimensions)
+        constexpr bool kAhead = G * kV < 16;
+        PageIds now = page_ids(p.c, b, row0 + lane * kPaTile, end);
+        int t = 0;
+        auto id_of = [&](int at) {
+            const int ida = __shfl_sync(0xffffffffu, now.a, at), idb = __shfl_sync(0xffffffffu, now.b, at);
+            return half ? idb : ida;
+        };
+        int id = id_of(0);
+        float x[8][4 * kV], v[8][4 * kV];
+        if (kAhead) load(kb, p.c.k_page, p.c.k_row, mask, row0 + 8 * half, end, id, x);
+        for (int row = row0; row < end; row += kPaTile) {
+            const int mine = row + 8 * half;      // this half-warp's eight rows
+            if (kAhead) load(vb, p.c.v_page, p.c.v_row, mask, mine, end, id, v);
+            else load(kb, p.c.k_page, p.c.k_row, mask, mine, end, id, x);
             const bool in = id >= 0 && mine + (hl >> 1) < end;
             float s[G];
             bool up = false;
@@ -554,7 +559,15 @@ struct TileF32 {
                     z[static_cast<int64_t>(mine + (hl >> 1)) * p.Gp + g] = in ? s[g] : -CUDART_INF_F;
                 up = up || (in && s[g] * p.scale_log2 > m[g] + kPaSlack);
             }
-            load(vb, p.c.v_page, p.c.v_row, mask, mine, end, id, x);
+            if (!kAhead) load(vb, p.c.v_page, p.c.v_row, mask, mine, end, id, v);
+            if (row + kPaTile < end) {
+                if (++t == 32) {
+                    t = 0;
+                    now = page_ids(p.c, b, row + (1 + lane) * kPaTile, end);
+                }
+                id = id_of(t);
+                if (kAhead) load(kb, p.c.k_page, p.c.k_row, mask, mine + kPaTile, end, id, x);
+            }
             if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
@@ -574,7 +587,7 @@ struct TileF32 {
                 for (int i = 0; i < 8; ++i) {
                     const float w = __shfl_sync(0xffffffffu, pr, 16 * half + 2 * i);
 #pragma unroll
-                    for (int j = 0; j < 4 * kV; ++j) o[g][j] = fmaf(w, x[i][j], o[g][j]);
+                    for (int j = 0; j < 4 * kV; ++j) o[g][j] = fmaf(w, v[i][j], o[g][j]);
                 }
             }
         }
