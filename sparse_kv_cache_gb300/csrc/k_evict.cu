@@ -28,7 +28,7 @@ constexpr int kEvWarps = kEvThreads / 32;
 constexpr int kEvStep = 256;                   // rows of a warp's step, eight per lane
 constexpr int kEvGrain = kEvStep * kEvWarps;   // a slice is a multiple of this many rows
 constexpr int kEvBins = 2048;
-constexpr int kEvKeys = 11 * kEvGrain;         // rows of a slice held in shared memory at most (88 KB: two CTAs per SM)
+constexpr int kEvKeys = 11 * kEvGrain;         // halves of keys held in shared memory at most (88 KB: two CTAs per SM)
 constexpr int kEvHist = 2 * kEvBins + 64;      // counts of the four passes
 
 // weights in the order of unsigned integers: -0 counts as 0, a NaN lies above +inf
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
         if (r != rank) last = max(last, ld_cluster_s32(cluster_addr(&s_max, r)));
     const Protect pr{static_cast<int>(max(static_cast<int64_t>(last) - p.recent, static_cast<int64_t>(-1))), p.sink};
 
-    const bool held = per * kEvWarps <= key_cap, held_low = per * kEvWarps <= low_cap;
+    const bool held = per * kEvWarps <= key_cap, held_low = (warp + 1) * per <= low_cap;
     uint16_t *my = s_key + warp * per, *my_low = s_low + warp * per;
     // halves of the lane's eight keys from row s on
     auto upper = [&](int s) { return held ? *reinterpret_cast<const uint4*>(my + (s - lo)) : remade(w_in, p_in, s, pr, 16); };
@@ -537,7 +537,8 @@ int launch_evict(const EvictParams& p, int nsm, cudaStream_t s) {
     const int64_t slice = (static_cast<int64_t>(p.c.cap) + ranks - 1) / ranks;
     const int64_t keys = (slice + kEvGrain - 1) / kEvGrain * kEvGrain;
     const int key_cap = static_cast<int>(keys < kEvKeys ? keys : kEvKeys);
-    const int low_cap = 2 * key_cap <= kEvKeys ? key_cap : 0;
+    // what is left of a half SM's shared memory goes to the first warps' lower halves
+    const int left = kEvKeys - key_cap, low_cap = key_cap < left ? key_cap : left;
     const int smem = kEvHist * 4 + (key_cap + low_cap) * 2;
     if (cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvHist * 4 + kEvKeys * 2) !=
         cudaSuccess)
