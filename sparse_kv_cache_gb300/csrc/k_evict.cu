@@ -29,6 +29,7 @@ constexpr int kEvStep = 256;                   // rows of a warp's step, eight p
 constexpr int kEvGrain = kEvStep * kEvWarps;   // a slice is a multiple of this many rows
 constexpr int kEvBins = 2048;
 constexpr int kEvKeys = 11 * kEvGrain;         // halves of keys held in shared memory at most (88 KB: two CTAs per SM)
+static_assert(kEvBins == 4 * kEvThreads && kEvWarps <= 32, "the search reads four bins per thread");
 constexpr int kEvHist = 2 * kEvBins + 64;      // counts of the four passes
 
 // weights in the order of unsigned integers: -0 counts as 0, a NaN lies above +inf
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
 
 constexpr int kMvThreads = 128;
 constexpr int kMvRows = 32;        // rows of a warp's turn: a lane looks each up
-constexpr int kMvDeep = 8;         // of them, rows whose words are in flight together
+constexpr int kMvDeep = 4;         // of them, rows whose words are in flight together
 
 __global__ void __launch_bounds__(kMvThreads) k_evict_move(const __grid_constant__ EvictParams p, int parts) {
     pdl_wait();
@@ -495,13 +496,17 @@ __global__ void __launch_bounds__(kMvThreads) k_evict_move(const __grid_constant
         if (i0 + lane < cnt) {
             d = to[i0 + lane];
             s = of[i0 + lane];
-            pd = page_of(p.c, b, d, g_err, 722);
-            ps = page_of(p.c, b, s, g_err, 723);
-            p.weight_out[base + d] = p.weight[base + s];
-            p.position_out[base + d] = p.position[base + s];
-            if (ps < 0) pd = -1;
-            d &= mask;
-            s &= mask;
+            if (d < 0 || d >= p.c.cap || s < 0 || s >= p.c.cap) {     // the lengths changed under the call
+                set_err(g_err, DEV_ERR_BOUNDS, 724);
+            } else {
+                pd = page_of(p.c, b, d, g_err, 722);
+                ps = page_of(p.c, b, s, g_err, 723);
+                p.weight_out[base + d] = p.weight[base + s];
+                p.position_out[base + d] = p.position[base + s];
+                if (ps < 0) pd = -1;
+                d &= mask;
+                s &= mask;
+            }
         }
         const int rows = min(kMvRows, cnt - i0);
         for (int w = lane; w < ((words + 31) & ~31); w += 32) {      // 16-byte words of a key row and its value row
@@ -537,8 +542,9 @@ int launch_evict(const EvictParams& p, int nsm, cudaStream_t s) {
     const int64_t slice = (static_cast<int64_t>(p.c.cap) + ranks - 1) / ranks;
     const int64_t keys = (slice + kEvGrain - 1) / kEvGrain * kEvGrain;
     const int key_cap = static_cast<int>(keys < kEvKeys ? keys : kEvKeys);
-    // what is left of a half SM's shared memory goes to the first warps' lower halves
-    const int left = kEvKeys - key_cap, low_cap = key_cap < left ? key_cap : left;
+    // the lower halves only where a slice is short: what they take of shared memory is taken from L1
+    // (128K rows: 68 us with the upper halves alone, 79 with some of the lower ones)
+    const int low_cap = 2 * key_cap <= kEvKeys ? key_cap : 0;
     const int smem = kEvHist * 4 + (key_cap + low_cap) * 2;
     if (cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvHist * 4 + kEvKeys * 2) !=
         cudaSuccess)
