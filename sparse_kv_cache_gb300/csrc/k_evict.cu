@@ -116,12 +116,12 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
     __shared__ int s_cnt[4][kEvWarps], s_tot[4];
     __shared__ int s_tie[kEvWarps], s_hole[kEvWarps], s_src[kEvWarps];
 
+    begin_call();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int u = blockIdx.x / ranks, rank = ranks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int b = u / p.c.H;
     const int n = rows_of(p.c, b, g_err, 721);
     const int M = p.budget;
-    pdl_trigger();
     const int64_t base = static_cast<int64_t>(u) * p.row_pitch;
     const float* w_in = p.weight + base;
     const int32_t* p_in = p.position + base;
@@ -549,18 +549,9 @@ int launch_evict(const EvictParams& p, int nsm, cudaStream_t s) {
     if (cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvHist * 4 + kEvKeys * 2) !=
         cudaSuccess)
         return -1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(U) * ranks);
-    cfg.blockDim = dim3(kEvThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ranks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = ranks > 1 ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, k_evict_select, p, ranks, key_cap, low_cap) != cudaSuccess) return -1;
+    if (launch_first(k_evict_select, static_cast<unsigned>(U) * ranks, kEvThreads, smem, ranks, s, p, ranks, key_cap,
+                     low_cap) != cudaSuccess)
+        return -1;
     // CTAs per unit for the rows that move
     const int rows = (kMvThreads / 32) * kMvRows;
     int64_t parts = (static_cast<int64_t>(p.list_cap) + rows - 1) / rows;

@@ -68,6 +68,7 @@ __global__ void __launch_bounds__(kNrThreads, kNrOcc) k_norm_rope(const __grid_c
     constexpr int kDeep = sizeof(T) == 2 ? 3 : 2;   // rows of a thread whose loads are in flight at once
     __shared__ __align__(16) float s_cos[kNrMaxTok * D / 2], s_sin[kNrMaxTok * D / 2];
 
+    begin_call();
     // p.groups lane groups share a token; group g of it takes the heads g, g + groups, ... of q, and
     // likewise of k and v together
     const int tid = threadIdx.x, c = tid % kLanes, half = p.rd / 2;
@@ -227,8 +228,7 @@ static int launch_nr(NormRopeParams p, int nsm, cudaStream_t s) {
         }
     }
     const int per = kRows / p.groups, grid = (p.tokens + per - 1) / per;
-    k_norm_rope<T, D, kE5M2><<<grid, kNrThreads, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    return launch_first(k_norm_rope<T, D, kE5M2>, grid, kNrThreads, 0, 1, s, p) == cudaSuccess ? 0 : -1;
 }
 
 int launch_norm_rope(int dtype, int d, const NormRopeParams& p, int nsm, cudaStream_t s) {

@@ -96,9 +96,10 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 
 
 // ------------------------------------------------------------------ the split of the work
 
-__device__ __forceinline__ int tiles_of(int n) { return (n + kPaTile - 1) / kPaTile; }
+template <int R = kPaTile>
+__device__ __forceinline__ int tiles_of(int n) { return (n + R - 1) / R; }
 
-// What CTA `me` of `ctas` takes, and where its W parts begin.  A part has kPaLeast tiles at least, or
+// What CTA `me` of `ctas` takes of the tiles of R rows, and where its W parts begin.  A part has `least` tiles, or
 // joining the shares would take longer than forming them (one unit of 32K rows: 17.4 us with four,
 // 19.2 with two, 23.2 with one).
 constexpr int kPaLeast = 4;
@@ -119,13 +120,13 @@ struct Plan {
 };
 
 // Every thread sums a run of sequences; the thread whose run holds a part's first tile finds it.
-template <int W>
+template <int W, int R, int kLeast>
 __device__ __forceinline__ Plan<W> make_plan(const PagedView& c, int64_t me, int64_t ctas, PlanSmem<W>& sm) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (c.batch + kPaThreads - 1) / kPaThreads;
     const int s0 = min(tid * per, c.batch), s1 = min(s0 + per, c.batch);
     int64_t mine = 0;
-    for (int s = s0; s < s1; ++s) mine += tiles_of(rows_of(c, s, g_err, 711));
+    for (int s = s0; s < s1; ++s) mine += tiles_of<R>(rows_of(c, s, g_err, 711));
     int64_t run = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -142,7 +143,7 @@ __device__ __forceinline__ Plan<W> make_plan(const PagedView& c, int64_t me, int
     }
     Plan<W> pl;
     pl.total = all * c.H;
-    pl.n = min(ctas, (pl.total + kPaLeast * W - 1) / (kPaLeast * W));
+    pl.n = min(ctas, (pl.total + kLeast * W - 1) / (kLeast * W));
     pl.lo = me < pl.n ? pl.start(me) : 0;
     pl.hi = me < pl.n ? pl.start(me + 1) : 0;
     const int64_t begin = (before + run - mine) * c.H, stop = begin + mine * c.H;
@@ -153,7 +154,7 @@ __device__ __forceinline__ Plan<W> make_plan(const PagedView& c, int64_t me, int
         int64_t at = begin;
         for (int s = s0; s < s1; ++s) {
             const int rows = rows_of(c, s, g_err, 711);
-            const int64_t size = static_cast<int64_t>(tiles_of(rows)) * c.H;
+            const int64_t size = static_cast<int64_t>(tiles_of<R>(rows)) * c.H;
             if (x < at + size) {
                 sm.at[w] = at;
                 sm.b[w] = s;
@@ -168,13 +169,14 @@ __device__ __forceinline__ Plan<W> make_plan(const PagedView& c, int64_t me, int
 }
 
 // A part's way through the units: its current unit, and the unit's first tile in the launch.
+template <int R>
 struct Walk {
     int b, h, rows, nt;
     int64_t unit0;
     __device__ __forceinline__ void enter(int seq, int n, int64_t at, int64_t x) {
         b = seq;
         rows = n;
-        nt = tiles_of(n);
+        nt = tiles_of<R>(n);
         h = static_cast<int>((x - at) / nt);
         unit0 = at + static_cast<int64_t>(h) * nt;
     }
@@ -191,7 +193,7 @@ struct Walk {
             const int at = __ffs(some) - 1;
             b = s + at;
             rows = __shfl_sync(0xffffffffu, n, at);
-            nt = tiles_of(rows);
+            nt = tiles_of<R>(rows);
             return true;
         }
         return false;
@@ -695,14 +697,14 @@ template <class Tile, int D, bool kF32, int G, int kOcc>
 __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_constant__ PagedAttnParams p) {
     __shared__ PlanSmem<kPaWarps> s_plan;
     __shared__ __align__(16) JoinSmem<D, G> js;
-    pdl_trigger();
+    begin_call();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, me = blockIdx.x;
-    const Plan<kPaWarps> pl = make_plan(p.c, me, gridDim.x, s_plan);
+    const Plan<kPaWarps> pl = make_plan<kPaWarps, kPaTile, kPaLeast>(p.c, me, gridDim.x, s_plan);
     const int64_t w0 = pl.part(warp), w1 = pl.part(warp + 1);
     if (lane == 0) js.of[2 * warp].b = js.of[2 * warp + 1].b = -1;
     __syncwarp();
     if (w0 < w1) {
-        Walk at;
+        Walk<kPaTile> at;
         at.enter(s_plan.b[warp], s_plan.rows[warp], s_plan.at[warp], w0);
         Tile tile;
         for (int64_t cur = w0; cur < w1;) {
@@ -726,7 +728,7 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
     if (tid == 0) {
         Joint joint{-1, 0, 0, 0};
         if (pl.lo < pl.hi) {
-            Walk at;
+            Walk<kPaTile> at;
             at.enter(s_plan.b[0], s_plan.rows[0], s_plan.at[0], pl.lo);
             if (at.unit0 < pl.lo && at.unit0 + at.nt <= pl.hi) {
                 const int64_t from = pl.holder(at.unit0);
@@ -752,7 +754,8 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
 template <class Tile, int D, bool kF32, int G, int kOcc>
 __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid_constant__ PagedAttnParams p, int ranks) {
     __shared__ __align__(16) JoinSmem<D, G> js;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    begin_call();
+    const int tid = threadIdx.x, warp = tid >> 5;
     const int u = blockIdx.x / ranks, rank = ranks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int b = u / p.c.H, h = u % p.c.H;
     const int rows = rows_of(p.c, b, g_err, 711);
@@ -949,9 +952,11 @@ __device__ __forceinline__ void merge_many(const PagedAttnParams& p, const Joint
 template <int D, bool kF32>
 __global__ void __launch_bounds__(kPaThreads) k_paged_merge(const __grid_constant__ PagedAttnParams p) {
     __shared__ MergeSmem<D> sm;
-    pdl_trigger();
-    // every CTA waits for the grid before, so that this grid's end stands for both
+    // every CTA waits for the grid before, so that this grid's end stands for both; what comes after is
+    // let in then (let in before, the next call's CTAs held the registers that this grid's wanted: 47 us
+    // against 34 for 192 short sequences)
     pdl_wait();
+    pdl_trigger();
     const int me = blockIdx.x;
     const int4 raw = __ldcg(reinterpret_cast<const int4*>(p.joint) + me);
     const Joint j{raw.x, raw.y, raw.z, raw.w};
@@ -964,11 +969,12 @@ __global__ void __launch_bounds__(kPaThreads) k_paged_merge(const __grid_constan
     for (int g = blockIdx.y; g < p.G; g += gridDim.y) merge_many<D, kF32>(p, j, n, g, sm);
 }
 
-// Two rows per thread and turn: their products are loaded before any of them is used.
-constexpr int kTurn = 2;
+// Rows per thread and turn, whose products are loaded before any of them is used: four, or two of
+// more than four heads.
+constexpr int kWeighRows = 1024;      // rows of a CTA's step: eight per thread
 
 template <int Gp>
-__device__ __forceinline__ void weigh_rows_of(const PagedAttnParams& p, int64_t u, int first, int end) {
+__device__ __forceinline__ void weigh_rows(const PagedAttnParams& p, int64_t u, int first, int end) {
     const float* z = p.z + u * p.c.cap * Gp;
     const float* in = p.weight + u * p.row_pitch;
     float* out = p.weight_out + u * p.row_pitch;
@@ -979,6 +985,7 @@ __device__ __forceinline__ void weigh_rows_of(const PagedAttnParams& p, int64_t 
         base[g] = st.x;
         inv[g] = st.y;
     }
+    constexpr int kTurn = Gp <= 4 ? 4 : 2;
     for (int i0 = first + threadIdx.x; i0 < end; i0 += kTurn * kPaThreads) {
         float2 x[kTurn][Gp / 2];
         float w[kTurn];
@@ -1005,35 +1012,28 @@ __device__ __forceinline__ void weigh_rows_of(const PagedAttnParams& p, int64_t 
         }
     }
 }
-__device__ __forceinline__ void weigh_rows(const PagedAttnParams& p, int64_t u, int first, int end) {
-    if (p.Gp == 2) weigh_rows_of<2>(p, u, first, end);
-    else if (p.Gp == 4) weigh_rows_of<4>(p, u, first, end);
-    else if (p.Gp == 6) weigh_rows_of<6>(p, u, first, end);
-    else weigh_rows_of<8>(p, u, first, end);
-}
-
 // weight_out = weight + sum over the heads of exp2(z scale - base) / sum, over the same split
-__global__ void __launch_bounds__(kPaThreads, 8) k_paged_weigh(const __grid_constant__ PagedAttnParams p) {
+constexpr int kWeighOcc = 8;          // CTAs per SM
+template <int Gp>
+__global__ void __launch_bounds__(kPaThreads, kWeighOcc) k_paged_weigh(const __grid_constant__ PagedAttnParams p) {
     __shared__ PlanSmem<1> s_plan;
-    const Plan<1> pl = make_plan(p.c, blockIdx.x, gridDim.x, s_plan);
+    // the lengths were there before the call began; the rest comes from the grids before
+    const Plan<1> pl = make_plan<1, kWeighRows, 1>(p.c, blockIdx.x, gridDim.x, s_plan);
     pdl_wait();
     if (pl.lo == pl.hi) return;
     int64_t cur = pl.lo;
-    Walk at;
+    Walk<kWeighRows> at;
     at.enter(s_plan.b[0], s_plan.rows[0], s_plan.at[0], cur);
     while (cur < pl.hi) {
-        const int64_t stop = min(pl.hi, at.unit0 + at.nt);
-        weigh_rows(p, static_cast<int64_t>(at.b) * p.c.H + at.h, static_cast<int>(cur - at.unit0) * kPaTile,
-                   static_cast<int>(min(static_cast<int64_t>(at.rows), (stop - at.unit0) * kPaTile)));
-        cur = stop;
-        if (cur < pl.hi && !at.next(p.c)) break;
+        const int first = static_cast<int>(cur - at.unit0) * kWeighRows;
+        weigh_rows<Gp>(p, static_cast<int64_t>(at.b) * p.c.H + at.h, first, min(at.rows, first + kWeighRows));
+        if (++cur == at.unit0 + at.nt && cur < pl.hi && !at.next(p.c)) break;
     }
 }
 
 // ------------------------------------------------------------------ launches
 
 constexpr int kOccTC = 3, kOccF32 = 2;     // CTAs per SM
-constexpr int kWeighOcc = 3;               // CTAs of k_paged_weigh per CTA of k_paged_attn
 
 int paged_attn_ctas(int dtype, int nsm) { return nsm * (dtype == SKV_F32 ? kOccF32 : kOccTC); }
 
@@ -1052,17 +1052,10 @@ template <class Tile, int D, bool kF32, int G, int kOcc>
 static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
     auto kernel = k_paged_cluster<Tile, D, kF32, G, kOcc>;
     if (ranks > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return -1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.c.batch) * p.c.H * ranks);
-    cfg.blockDim = dim3(kPaThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ranks;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = ranks > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, p, ranks) == cudaSuccess ? 0 : -1;
+    return launch_first(kernel, static_cast<unsigned>(p.c.batch) * p.c.H * ranks, kPaThreads, 0, ranks, s, p, ranks) ==
+                   cudaSuccess
+               ? 0
+               : -1;
 }
 
 template <class Tile, int D, bool kF32, int G, int kOcc>
@@ -1072,14 +1065,16 @@ static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
     const int64_t tiles = static_cast<int64_t>(p.c.batch) * p.c.H * ((p.c.cap + kPaTile - 1) / kPaTile);
     const int64_t most = (tiles + kPaLeast * kPaWarps - 1) / (kPaLeast * kPaWarps);
     const int n = most < ncta ? static_cast<int>(most) : ncta;
-    k_paged_attn<Tile, D, kF32, G, kOcc><<<n, kPaThreads, 0, s>>>(p);
+    if (launch_first(k_paged_attn<Tile, D, kF32, G, kOcc>, n, kPaThreads, 0, 1, s, p) != cudaSuccess) return -1;
     // a CTA per head where units are few and so have many shares; one for all heads where they are many
     const int heads = p.c.batch * static_cast<int64_t>(p.c.H) * 4 >= n ? 1 : p.G;
     if (launch_pdl(k_paged_merge<D, kF32>, dim3(n, heads), dim3(kPaThreads), 0, s, p) != cudaSuccess) return -1;
     if (p.weight_out) {
-        const int64_t wide = kWeighOcc * static_cast<int64_t>(ncta);
-        const int nw = static_cast<int>(most < wide ? most : wide);
-        if (launch_pdl(k_paged_weigh, dim3(nw), dim3(kPaThreads), 0, s, p) != cudaSuccess) return -1;
+        const int64_t blocks = static_cast<int64_t>(p.c.batch) * p.c.H * ((p.c.cap + kWeighRows - 1) / kWeighRows);
+        const int64_t wide = static_cast<int64_t>(kWeighOcc) * (ncta / kOcc);
+        const int nw = static_cast<int>(blocks < wide ? blocks : wide);
+        auto weigh = p.Gp == 2 ? k_paged_weigh<2> : p.Gp == 4 ? k_paged_weigh<4> : p.Gp == 6 ? k_paged_weigh<6> : k_paged_weigh<8>;
+        if (launch_pdl(weigh, dim3(nw), dim3(kPaThreads), 0, s, p) != cudaSuccess) return -1;
     }
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

@@ -73,9 +73,36 @@ cudaError_t paged_attn_err(int** p);
 cudaError_t evict_err(int** p);
 
 #ifdef __CUDACC__
+// A kernel of a call's beginning: a programmatic dependent of whatever is before it in the stream,
+// so that its CTAs are in place when that ends (it waits for that before it touches memory), as one
+// grid or as clusters of `ranks` CTAs.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_first(void (*k)(KArgs...), unsigned grid, int block, size_t smem, int ranks, cudaStream_t s,
+                                Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ranks > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k, static_cast<Args&&>(args)...);
+}
+// Its first lines: the kernels after it may be brought in once it knows that those before it are done.
+__device__ __forceinline__ void begin_call() {
+    pdl_wait();
+    pdl_trigger();
+}
+
 // rows of sequence b, brought into [0, cap]
 __device__ __forceinline__ int rows_of(const PagedView& c, int b, int* err, int where) {
-    int n = __ldg(c.lens + b);
+    int n = __ldcg(c.lens + b);
     if (n < 0 || n > c.cap) {
         set_err(err, DEV_ERR_BOUNDS, where);
         n = n < 0 ? 0 : c.cap;
