@@ -83,6 +83,7 @@ def queries(c, G, seed=1, scale=1.0):
     ("bf16", 2, 2, 128, 64, "nhd", [40000, 1, 0, 700]),        # one sequence over most of the CTAs
     ("bf16", 5, 8, 128, 16, "hnd", [300] * 40 + [0] * 200),    # several units per CTA, idle sequences behind
     ("bf16", 4, 1, 64, 16, "hnd", [0] * 150 + [77] + [0] * 150 + [3000]),
+    ("bf16", 1, 1, 64, 8, "hnd", [(i * 7919) % 41 for i in range(1000)]),      # eight sequences per thread of the search
     ("fp8", 4, 2, 128, 16, "hnd", [1, 0, 500, 64]),
     ("fp8", 8, 1, 64, 8, "nhd", [1300, 7]),
     ("fp8", 1, 4, 128, 256, "nhd", [20000]),
@@ -336,6 +337,72 @@ def test_captured_calls_replay_with_new_lengths():
         c.krows, c.vrows = keep
     # one per query head, sequence with rows and replay
     assert float(w.sum()) == pytest.approx(8 * (2 + 1 + 2), rel=1e-3)
+
+
+def test_calls_of_two_host_threads():
+    import threading
+    c = Paged("bf16", [3000, 100], 2, 128, 16, seed=23)
+    qs = [queries(c, 4, 24 + i) for i in range(2)]
+    want = [skv.paged_attention(x, c.k, c.v, c.table, c.lens, torch.empty_like(x)).clone() for x in qs]
+    torch.cuda.synchronize()
+    got, failed = [[], []], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got[i] = [skv.paged_attention(qs[i], c.k, c.v, c.table, c.lens, torch.empty_like(qs[i])) for _ in range(50)]
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001 (reported by the test)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for i in range(2):
+        assert len(got[i]) == 50 and all(torch.equal(o, want[i]) for o in got[i])
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Every call captured before any was made: nothing needs a set-up outside the capture."""
+    code = """
+import torch, sparse_kv_cache_gb300 as skv
+torch.manual_seed(0)
+dev = "cuda"
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev)
+k, v = (torch.randn(40, 2, 16, 64, device=dev).bfloat16() for _ in range(2))
+table = torch.arange(40, dtype=torch.int32, device=dev).view(1, 40)
+q = torch.randn(1, 8, 64, device=dev).bfloat16(); qr = torch.empty_like(q); out = torch.empty_like(q)
+kn = torch.randn(1, 2, 64, device=dev).bfloat16()
+w = torch.rand(1, 2, 640, device=dev); pos = torch.arange(640, dtype=torch.int32, device=dev).expand(1, 2, 640).contiguous()
+lens, at, zero = i32(601), i32(600), i32(0)
+saved = [t.clone() for t in (k, v, w, pos, lens)]
+def step():
+    skv.qk_norm_rope(q, kn, at, qr, v=kn, k_cache=k, v_cache=v, table=table, seq=zero, index=at, position=pos, weight=w)
+    skv.paged_attention(qr, k, v, table, lens, out, weight=w)
+    skv.paged_evict(k, v, table, lens, w, pos, 512, 16, 4)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+first = [t.clone() for t in (out, k, v, w, pos, lens)]
+for t, s in zip((k, v, w, pos, lens), saved): t.copy_(s)
+step()
+torch.cuda.synchronize()
+assert int(lens) == 512 and all(torch.equal(a, b) for a, b in zip(first, (out, k, v, w, pos, lens)))
+assert skv.paged_status() == 0
+print("same")
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=200)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
 
 
 # ------------------------------------------------------------------ norm, rotation, append

@@ -56,6 +56,11 @@ def cache(batch=2, heads=2, d=128, ps=16, pages=8, width=4, kind=torch.bfloat16,
                 lens=torch.zeros(batch, dtype=torch.int32))
 
 
+def off(t):
+    """A copy of t that begins one element behind a 16-byte boundary."""
+    return torch.zeros(t.numel() + 8, dtype=t.dtype)[1:t.numel() + 1].view(t.shape)
+
+
 def refused(skv, call):
     with pytest.raises(skv.ShadowKVError) as e:
         call()
@@ -92,6 +97,7 @@ def test_attention_refuses_tensors_of_other_shapes(skv):
                 dict(out=out[:1].expand(2, -1, -1)),                                   # one row for two results
                 dict(q=torch.zeros((2, 4, 256), dtype=torch.bfloat16)[..., ::2]),
                 dict(q=torch.zeros(2 * 4 * 129, dtype=torch.bfloat16).as_strided((2, 4, 128), (516, 129, 1))),
+                dict(q=off(q)), dict(out=off(q)),                                      # 2 bytes off a 16-byte boundary
                 dict(scale=math.inf), dict(scale=math.nan)):
         refused(skv, lambda: go(**bad))
 
@@ -110,6 +116,7 @@ def test_norm_refuses(skv):
                 dict(rope_base=1.0), dict(rope_base=math.inf), dict(position=rows.int()), dict(weight=rows),
                 dict(at, index=None), dict(at, v=None), dict(at, table=None), dict(at, seq=pos[:1]),
                 dict(at, weight=rows[..., :60]), dict(at, weight=rows, position=torch.zeros(2, 2, 80).int()),
+                dict(q=off(q)), dict(k_out=off(k)), dict(k_weight=off(x(128))),
                 dict(at, k_cache=c["k_cache"][:, :1]), dict(at, k_cache=c["k_cache"].float()),
                 dict(at, k_cache=c["k_cache"][:1].expand(8, -1, -1, -1)),              # pages that are one
                 dict(q_out=q[:1].expand(3, -1, -1))):
@@ -122,6 +129,8 @@ def test_evict_refuses(skv):
     go = lambda **kw: skv.paged_evict(**{**c, **dict(weight=rows, position=rows.int(), budget=8, stream=0), **kw})  # noqa: E731
     for bad in (dict(budget=0), dict(budget=-1), dict(recent=-1), dict(sink=-1), dict(recent=5, sink=4),
                 dict(weight=rows.double()), dict(position=rows), dict(weight=rows[:, :1]), dict(position=rows[..., :63].int()),
+                dict(weight=torch.zeros(2, 2, 66), position=torch.zeros(2, 2, 66).int()),     # rows 8 bytes off
+                dict(weight=off(rows)), dict(weight_out=off(rows)), dict(position_out=off(rows.int())),
                 dict(weight_out=torch.zeros(2, 2, 65)), dict(lens_out=torch.zeros(3, dtype=torch.int32)),
                 dict(lens_out=torch.zeros(2)), dict(table=c["table"][0]),
                 dict(k_cache=c["k_cache"][:, :1].expand(-1, 2, -1, -1))):
