@@ -6,15 +6,17 @@
 // below M, so sources and destinations are disjoint, only the rows that have to move are moved, and
 // a unit that is one row over its budget moves at most one row instead of shifting the rest.
 //
-// k_evict_select finds the M-th largest key by a radix search of 11, 5, 11 and 5 bits (integer
-// counts in shared memory, so the order of the atomics does not show) and writes both lists in
-// ascending row order.  A unit belongs to a cluster of 1 to 8 CTAs, each with a contiguous slice of
-// the rows, each warp with a contiguous part of the slice; counts are joined through distributed
-// shared memory.  The upper halves of a slice's keys stay in shared memory, and the lower ones too
-// where there is room; else the weights are read again for lanes that hold a row whose upper half
-// equals the threshold's.  Once the 11 uppermost bits of the threshold are known, a warp whose rows
-// all lie behind the budget keeps a list of those that can still stay -- of a long prompt a few in
-// a hundred -- and goes on with that.  k_evict_move, a programmatic dependent, copies the rows.
+// k_evict finds the M-th largest key by a radix search of 11, 5, 11 and 5 bits (integer counts in
+// shared memory, so the order of the atomics does not show) and writes both lists in ascending row
+// order.  A unit belongs to a cluster of 1 to 8 CTAs, each with a contiguous slice of the rows, each
+// warp with a contiguous part of the slice; counts are joined through distributed shared memory.  The
+// upper halves of a slice's keys stay in shared memory, and the lower ones too where there is room;
+// else the weights are read again for lanes that hold a row whose upper half equals the threshold's.
+// Once the 11 uppermost bits of the threshold are known, a warp whose rows all lie behind the budget
+// keeps a list of those that can still stay -- of a long prompt a few in a hundred -- and goes on with
+// that.  Where only a few rows of a unit can move (decode steps), its cluster moves them itself; else
+// k_evict_move, a programmatic dependent, does with all of the device (154K rows of 64 long units:
+// 63 us in all against 68).
 #include "skv_common.cuh"
 #include "skv_internal.h"
 #include "skv_paged.h"
@@ -30,6 +32,9 @@ constexpr int kEvGrain = kEvStep * kEvWarps;   // a slice is a multiple of this 
 constexpr int kEvBins = 2048;
 constexpr int kEvKeys = 11 * kEvGrain;         // halves of keys held in shared memory at most (88 KB: two CTAs per SM)
 static_assert(kEvBins == 4 * kEvThreads && kEvWarps <= 32, "the search reads four bins per thread");
+// Rows of a unit that its own cluster moves, at most.  Of 2048 rows + 256, 64 units take 14.6 us with one
+// kernel and 15.9 with two, + 512 19.1 and 20.5 (8 units: 16.1 and 15.3), + 952 29.4 and 24.0.
+constexpr int kEvFew = 512;
 constexpr int kEvHist = 2 * kEvBins + 64;      // counts of the four passes
 
 // weights in the order of unsigned integers: -0 counts as 0, a NaN lies above +inf
@@ -106,7 +111,63 @@ __device__ __forceinline__ int excl_scan(int x, int lane) {
     return y - x;
 }
 
-__global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_constant__ EvictParams p, int ranks,
+// Moves the unit's listed rows of which this is warp `warp` of `warps`: a lane of the warp looks each up,
+// then their 16-byte words, four rows' at a time in flight (eight: 68 us, two: 65, against 63).
+__device__ __forceinline__ void move_rows(const EvictParams& p, int u, int moves, int warp, int warps) {
+    constexpr int kTurn = 32, kFlight = 4;
+    const int lane = threadIdx.x & 31, b = u / p.c.H, h = u % p.c.H;
+    const int64_t base = static_cast<int64_t>(u) * p.row_pitch;
+    const int32_t* to = p.to + static_cast<int64_t>(u) * p.list_cap;
+    const int32_t* of = p.of + static_cast<int64_t>(u) * p.list_cap;
+    const int kw = p.d * p.es / 16, words = kw + p.d * p.es_v / 16, mask = (1 << p.c.lg) - 1;
+    uint8_t* kp = static_cast<uint8_t*>(p.c.k) + h * p.c.k_head * p.es;
+    uint8_t* vp = static_cast<uint8_t*>(p.c.v) + h * p.c.v_head * p.es_v;
+#pragma unroll 1
+    for (int i0 = warp * kTurn; i0 < moves; i0 += warps * kTurn) {
+        int pd = -1, ps = -1, d = 0, s = 0;
+        if (i0 + lane < moves) {
+            d = __ldcg(to + i0 + lane);
+            s = __ldcg(of + i0 + lane);
+            if (d < 0 || d >= p.c.cap || s < 0 || s >= p.c.cap) {     // the lengths changed under the call
+                set_err(g_err, DEV_ERR_BOUNDS, 724);
+            } else {
+                pd = page_of(p.c, b, d, g_err, 722);
+                ps = page_of(p.c, b, s, g_err, 723);
+                p.weight_out[base + d] = __ldg(p.weight + base + s);
+                p.position_out[base + d] = __ldg(p.position + base + s);
+                if (ps < 0) pd = -1;
+                d &= mask;
+                s &= mask;
+            }
+        }
+        const int rows = min(kTurn, moves - i0);
+#pragma unroll 1
+        for (int w = lane; w < ((words + 31) & ~31); w += 32) {      // words of a key row and its value row
+            const bool key = w < kw;
+            uint8_t* pool = (key ? kp : vp) + (key ? w : w - kw) * 16;
+            const int64_t page = (key ? p.c.k_page : p.c.v_page) * (key ? p.es : p.es_v);
+            const int64_t row = (key ? p.c.k_row : p.c.v_row) * (key ? p.es : p.es_v);
+#pragma unroll 1
+            for (int j0 = 0; j0 < rows; j0 += kFlight) {
+                uint4 x[kFlight];
+                int64_t dst[kFlight];
+#pragma unroll
+                for (int j = 0; j < kFlight; ++j) {
+                    const int to_page = __shfl_sync(0xffffffffu, pd, j0 + j), of_page = __shfl_sync(0xffffffffu, ps, j0 + j);
+                    const int to_row = __shfl_sync(0xffffffffu, d, j0 + j), of_row = __shfl_sync(0xffffffffu, s, j0 + j);
+                    dst[j] = to_page >= 0 && w < words ? to_page * page + to_row * row : -1;
+                    if (dst[j] >= 0) x[j] = __ldg(reinterpret_cast<const uint4*>(pool + of_page * page + of_row * row));
+                }
+#pragma unroll
+                for (int j = 0; j < kFlight; ++j)
+                    if (dst[j] >= 0) *reinterpret_cast<uint4*>(pool + dst[j]) = x[j];
+            }
+        }
+    }
+}
+
+template <bool kMove>
+__global__ void __launch_bounds__(kEvThreads, 2) k_evict(const __grid_constant__ EvictParams p, int ranks,
                                                                  int key_cap, int low_cap) {
     extern __shared__ __align__(16) int sm[];
     int* s_hist = sm;                                                  // [kEvHist]
@@ -114,7 +175,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
     uint16_t* s_low = s_key + key_cap;                                 // [low_cap] lower halves
     __shared__ int s_scan[kEvWarps], s_bin[3], s_maxes[kEvWarps], s_max;
     __shared__ int s_cnt[4][kEvWarps], s_tot[4];
-    __shared__ int s_tie[kEvWarps], s_hole[kEvWarps], s_src[kEvWarps];
+    __shared__ int s_tie[kEvWarps], s_hole[kEvWarps], s_src[kEvWarps], s_moves;
 
     begin_call();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -131,9 +192,10 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
     const int64_t lo64 = (static_cast<int64_t>(rank) * kEvWarps + warp) * per;
     const int lo = static_cast<int>(min(lo64, static_cast<int64_t>(n)));
     const int hi = static_cast<int>(min(lo64 + per, static_cast<int64_t>(n)));
-    if (rank == 0 && tid == 0 && u % p.c.H == 0) p.new_len[b] = min(n, M);
+    // (the other heads' CTAs may not have read a length that is to be updated in place: it goes by new_len)
+    if (rank == 0 && tid == 0 && u % p.c.H == 0) (p.lens_out == p.c.lens ? p.new_len : p.lens_out)[b] = min(n, M);
     if (n <= M) {      // the whole cluster: nothing is given up
-        if (rank == 0 && tid == 0) p.count[u] = 0;
+        if (!kMove && rank == 0 && tid == 0) p.count[u] = 0;
         for (int i = lo + lane; i < hi; i += 32) {
             if (copy_w) p.weight_out[base + i] = w_in[i];
             if (copy_p) p.position_out[base + i] = p_in[i];
@@ -443,16 +505,19 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
         }
         sync_all(ranks);
         if (warp == 0) {
-            // what lies in the slices before this one (rows below M come first in every slice)
-            int tie0 = 0, hole0 = 0, src0 = 0;
-            for (int r = 0; r < rank; ++r) {
-                const int a = ld_cluster_s32(cluster_addr(&s_tot[0], r)), tl = ld_cluster_s32(cluster_addr(&s_tot[1], r));
-                const int g = ld_cluster_s32(cluster_addr(&s_tot[2], r)), th = ld_cluster_s32(cluster_addr(&s_tot[3], r));
-                const int left = max(0, ties - tie0), kl = min(tl, left), kh = min(th, left - kl);
-                hole0 += a + tl - kl;
-                src0 += g + kh;
-                tie0 += tl + th;
+            // what lies in the slices before this one, and in all (rows below M come first in every slice)
+            int tie0 = 0, hole0 = 0, src0 = 0, tie_sum = 0, hole_sum = 0, src_sum = 0;
+            for (int r = 0; r < ranks; ++r) {
+                if (r == rank) tie0 = tie_sum, hole0 = hole_sum, src0 = src_sum;
+                int v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = r == rank ? s_tot[e] : ld_cluster_s32(cluster_addr(&s_tot[e], r));
+                const int left = max(0, ties - tie_sum), kl = min(v[1], left), kh = min(v[3], left - kl);
+                hole_sum += v[0] + v[1] - kl;
+                src_sum += v[2] + kh;
+                tie_sum += v[1] + v[3];
             }
+            if (lane == 0) s_moves = min(min(hole_sum, src_sum), p.list_cap);
             const int w = lane % kEvWarps;
             const bool own = lane < kEvWarps;
             const int a = own ? s_cnt[0][w] : 0, tl = own ? s_cnt[1][w] : 0, g = own ? s_cnt[2][w] : 0, th = own ? s_cnt[3][w] : 0;
@@ -465,72 +530,33 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict_select(const __grid_con
                 s_hole[w] = h0;
                 s_src[w] = s0;
             }
-            if (rank == ranks - 1 && lane == kEvWarps - 1) p.count[u] = s0 + srcs;
         }
-        sync_all(ranks);       // and no CTA leaves while another reads its counts
+        sync_all(ranks);       // nor does a CTA leave while another reads its counts
         tie_at = s_tie[warp];
         hole_at = s_hole[warp];
         src_at = s_src[warp];
     }
+
+    if (kMove) {
+        sync_all(ranks);       // the lists are whole
+        move_rows(p, u, s_moves, rank * kEvWarps + warp, ranks * kEvWarps);
+    } else if (rank == 0 && tid == 0) {
+        p.count[u] = s_moves;
+    }
 }
 
 constexpr int kMvThreads = 128;
-constexpr int kMvRows = 32;        // rows of a warp's turn: a lane looks each up
-constexpr int kMvDeep = 4;         // of them, rows whose words are in flight together
-
 __global__ void __launch_bounds__(kMvThreads) k_evict_move(const __grid_constant__ EvictParams p, int parts) {
     pdl_wait();
-    const int u = blockIdx.x / parts, part = blockIdx.x % parts, b = u / p.c.H, h = u % p.c.H;
-    const int lane = threadIdx.x & 31;
-    if (h == 0 && part == 0 && threadIdx.x == 0) p.lens_out[b] = p.new_len[b];
-    const int cnt = min(p.count[u], p.list_cap);
-    const int64_t base = static_cast<int64_t>(u) * p.row_pitch;
-    const int32_t* to = p.to + static_cast<int64_t>(u) * p.list_cap;
-    const int32_t* of = p.of + static_cast<int64_t>(u) * p.list_cap;
-    const int step = parts * (kMvThreads / 32) * kMvRows;
-    const int kw = p.d * p.es / 16, words = kw + p.d * p.es_v / 16, mask = (1 << p.c.lg) - 1;
-    uint8_t* kp = static_cast<uint8_t*>(p.c.k) + h * p.c.k_head * p.es;
-    uint8_t* vp = static_cast<uint8_t*>(p.c.v) + h * p.c.v_head * p.es_v;
-    for (int i0 = (part * (kMvThreads / 32) + (threadIdx.x >> 5)) * kMvRows; i0 < cnt; i0 += step) {
-        int pd = -1, ps = -1, d = 0, s = 0;
-        if (i0 + lane < cnt) {
-            d = to[i0 + lane];
-            s = of[i0 + lane];
-            if (d < 0 || d >= p.c.cap || s < 0 || s >= p.c.cap) {     // the lengths changed under the call
-                set_err(g_err, DEV_ERR_BOUNDS, 724);
-            } else {
-                pd = page_of(p.c, b, d, g_err, 722);
-                ps = page_of(p.c, b, s, g_err, 723);
-                p.weight_out[base + d] = p.weight[base + s];
-                p.position_out[base + d] = p.position[base + s];
-                if (ps < 0) pd = -1;
-                d &= mask;
-                s &= mask;
-            }
-        }
-        const int rows = min(kMvRows, cnt - i0);
-        for (int w = lane; w < ((words + 31) & ~31); w += 32) {      // 16-byte words of a key row and its value row
-            const bool key = w < kw;
-            uint8_t* pool = (key ? kp : vp) + (key ? w : w - kw) * 16;
-            const int64_t page = (key ? p.c.k_page : p.c.v_page) * (key ? p.es : p.es_v);
-            const int64_t row = (key ? p.c.k_row : p.c.v_row) * (key ? p.es : p.es_v);
-            for (int j0 = 0; j0 < rows; j0 += kMvDeep) {
-                uint4 x[kMvDeep];
-                int64_t dst[kMvDeep];
-#pragma unroll
-                for (int j = 0; j < kMvDeep; ++j) {
-                    const int at = (j0 + j) & 31;
-                    const int to_page = __shfl_sync(0xffffffffu, pd, at), of_page = __shfl_sync(0xffffffffu, ps, at);
-                    const int to_row = __shfl_sync(0xffffffffu, d, at), of_row = __shfl_sync(0xffffffffu, s, at);
-                    dst[j] = to_page >= 0 && w < words ? to_page * page + to_row * row : -1;
-                    if (dst[j] >= 0) x[j] = __ldg(reinterpret_cast<const uint4*>(pool + of_page * page + of_row * row));
-                }
-#pragma unroll
-                for (int j = 0; j < kMvDeep; ++j)
-                    if (dst[j] >= 0) *reinterpret_cast<uint4*>(pool + dst[j]) = x[j];
-            }
-        }
-    }
+    const int u = blockIdx.x / parts, part = blockIdx.x % parts;
+    if (p.lens_out == p.c.lens && u % p.c.H == 0 && part == 0 && threadIdx.x == 0) p.lens_out[u / p.c.H] = p.new_len[u / p.c.H];
+    move_rows(p, u, min(p.count[u], p.list_cap), part * (kMvThreads / 32) + (threadIdx.x >> 5), parts * (kMvThreads / 32));
+}
+
+__global__ void k_evict_lens(const __grid_constant__ EvictParams p) {
+    pdl_wait();
+    const int b = blockIdx.x * blockDim.x + threadIdx.x;
+    if (b < p.c.batch) p.lens_out[b] = __ldcg(p.new_len + b);
 }
 
 int launch_evict(const EvictParams& p, int nsm, cudaStream_t s) {
@@ -546,21 +572,24 @@ int launch_evict(const EvictParams& p, int nsm, cudaStream_t s) {
     // (128K rows: 68 us with the upper halves alone, 79 with some of the lower ones)
     const int low_cap = 2 * key_cap <= kEvKeys ? key_cap : 0;
     const int smem = kEvHist * 4 + (key_cap + low_cap) * 2;
-    if (cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvHist * 4 + kEvKeys * 2) !=
-        cudaSuccess)
+    const bool few = p.list_cap <= kEvFew;
+    auto kernel = few ? k_evict<true> : k_evict<false>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvHist * 4 + kEvKeys * 2) != cudaSuccess ||
+        launch_first(kernel, static_cast<unsigned>(U) * ranks, kEvThreads, smem, ranks, s, p, ranks, key_cap, low_cap) !=
+            cudaSuccess)
         return -1;
-    if (launch_first(k_evict_select, static_cast<unsigned>(U) * ranks, kEvThreads, smem, ranks, s, p, ranks, key_cap,
-                     low_cap) != cudaSuccess)
-        return -1;
-    // CTAs per unit for the rows that move
-    const int rows = (kMvThreads / 32) * kMvRows;
-    int64_t parts = (static_cast<int64_t>(p.list_cap) + rows - 1) / rows;
-    const int64_t most = (16 * nsm + U - 1) / U;
-    if (parts > most) parts = most;
-    if (launch_pdl(k_evict_move, dim3(static_cast<unsigned>(parts * U)), dim3(kMvThreads), 0, s, p,
-                   static_cast<int>(parts)) != cudaSuccess)
-        return -1;
-    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+    cudaError_t e = cudaSuccess;
+    if (!few) {
+        // CTAs per unit for the rows that move
+        const int rows = kMvThreads;
+        int64_t parts = (static_cast<int64_t>(p.list_cap) + rows - 1) / rows;
+        const int64_t most = (16 * nsm + U - 1) / U;
+        if (parts > most) parts = most;
+        e = launch_pdl(k_evict_move, dim3(static_cast<unsigned>(parts * U)), dim3(kMvThreads), 0, s, p, static_cast<int>(parts));
+    } else if (p.lens_out == p.c.lens) {
+        e = launch_pdl(k_evict_lens, dim3((p.c.batch + 127) / 128), dim3(128), 0, s, p);
+    }
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
 cudaError_t evict_err(int** e) { return cudaGetSymbolAddress(reinterpret_cast<void**>(e), g_err); }

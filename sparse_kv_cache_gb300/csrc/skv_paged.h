@@ -63,7 +63,8 @@ struct EvictParams {
     float* weight_out; int32_t* position_out; int64_t row_pitch;
     int32_t* lens_out;
     int32_t* to; int32_t* of; int list_cap;   // [U][list_cap] rows given up / rows that move there
-    int32_t* count; int32_t* new_len;         // [U], [batch]
+    int32_t* count;           // [U]: entries of the lists
+    int32_t* new_len;         // [batch]: lengths that are updated in place
 };
 int launch_evict(const EvictParams& p, int nsm, cudaStream_t s);
 
