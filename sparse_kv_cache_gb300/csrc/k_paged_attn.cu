@@ -258,6 +258,59 @@ __device__ __forceinline__ PageIds page_ids(const PagedView& c, int b, int row, 
     return id;
 }
 
+// A warp's rows of one unit: rows [row, end) of head h of sequence b, and the page ids of the first 32
+// tiles.
+struct Piece {
+    int b, h, row, end;
+    PageIds ids;
+    __device__ __forceinline__ void ask(const PagedView& c) { ids = page_ids(c, b, row + (threadIdx.x & 31) * kPaTile, end); }
+};
+// The pieces of a warp's tiles, one after the other: all but the first begin with their unit's first
+// tile, all but the last end with its last.  The lengths of 32 sequences are held by the lanes, so
+// that going on to the next takes no load.
+struct Pieces {
+    int b, h, left, base, lens;
+    bool begins, ends;      // whether the first piece does, and the last one
+    __device__ __forceinline__ void fetch(const PagedView& c) {
+        const int s = base + (threadIdx.x & 31);
+        lens = s < c.batch ? rows_of(c, s, g_err, 711) : 0;
+    }
+    // the first: tiles from x on, `tiles` of them, x in the sequence `seq` whose first tile is `at`
+    __device__ __forceinline__ Piece first(const PagedView& c, int seq, int rows, int64_t at, int64_t x, int64_t tiles) {
+        const int nt = tiles_of(rows);
+        const int skip = static_cast<int>((x - at) % nt), take = static_cast<int>(min(tiles, static_cast<int64_t>(nt - skip)));
+        b = base = seq;
+        h = static_cast<int>((x - at) / nt);
+        left = static_cast<int>(tiles - take);
+        begins = skip == 0;
+        ends = skip + take == nt;
+        if (left > 0) fetch(c);
+        Piece q{b, h, skip * kPaTile, min(rows, (skip + take) * kPaTile), {-1, -1}};
+        q.ask(c);
+        return q;
+    }
+    __device__ __forceinline__ bool next(const PagedView& c, Piece& q) {
+        if (left <= 0) return false;
+        if (++h == c.H) {
+            h = 0;
+            uint32_t some = __ballot_sync(0xffffffffu, lens > 0) & ~((2u << (b - base)) - 1);
+            while (!some) {
+                base += 32;
+                if (base >= c.batch) return false;      // the lengths changed under the call
+                fetch(c);
+                some = __ballot_sync(0xffffffffu, lens > 0);
+            }
+            b = base + __ffs(some) - 1;
+        }
+        const int rows = __shfl_sync(0xffffffffu, lens, b - base), nt = tiles_of(rows), take = min(left, nt);
+        left -= take;
+        ends = take == nt;
+        q = Piece{b, h, 0, min(rows, take * kPaTile), {-1, -1}};
+        q.ask(c);
+        return true;
+    }
+};
+
 template <int D, bool kE5M2>
 struct TileTC {
     static constexpr int kKV = D / 32;                     // 16-byte words of a key row per lane
@@ -267,7 +320,7 @@ struct TileTC {
     float o[D / 16][4];
     float m0, m1, l0, l1;                                  // heads 2c and 2c + 1
 
-    __device__ __forceinline__ void load_q(const PagedAttnParams& p, int b, int h, float*) {
+    __device__ __forceinline__ void load_q(const PagedAttnParams& p, int b, int h) {
         const int g = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + b * p.q_seq + (h * p.G + g) * p.q_head + c * 8;
 #pragma unroll
@@ -443,37 +496,62 @@ struct TileTC {
             }
         }
     }
-    // rows [row0, end) of the unit
-    __device__ __forceinline__ void share(const PagedAttnParams& p, int b, int h, int row0, int end, float* z) {
+    // The pieces from `cur` on, as one stream of tiles: the first loads of the next piece are on their
+    // way before this one is done with.  next(piece) gives the following one; done(piece, whether there is
+    // another) hands over.
+    template <bool kKeep, class Next, class Done>
+    __device__ __forceinline__ void stream(const PagedAttnParams& p, Piece cur, float*, Next next, Done done) {
         const int lane = threadIdx.x & 31;
-        PageIds now = page_ids(p.c, b, row0 + lane * kPaTile, end), next = now;
+        Piece then;
+        bool more = next(then);
+        PageIds ids = cur.ids, later = ids;
+        if (cur.row + 32 * kPaTile < cur.end) later = page_ids(p.c, cur.b, cur.row + (32 + lane) * kPaTile, cur.end);
         int t = 0;
         Keys k;
         Values v;
-        int ida = __shfl_sync(0xffffffffu, now.a, 0), idb = __shfl_sync(0xffffffffu, now.b, 0);
-        load_k(p, h, row0, end, ida, idb, k);
-        load_v(p, h, row0, end, ida, idb, v);
-        if (row0 + 32 * kPaTile < end) next = page_ids(p.c, b, row0 + (32 + lane) * kPaTile, end);
-        for (int row = row0; row < end; row += kPaTile) {
+        int ida = __shfl_sync(0xffffffffu, ids.a, 0), idb = __shfl_sync(0xffffffffu, ids.b, 0);
+        load_q(p, cur.b, cur.h);
+        load_k(p, cur.h, cur.row, cur.end, ida, idb, k);
+        load_v(p, cur.h, cur.row, cur.end, ida, idb, v);
+        reset();
+        for (;;) {
             float s[4];
             scores(k, s);
-            const int was_a = ida, was_b = idb;
-            const bool more = row + kPaTile < end;
-            if (more) {
+            const int was_a = ida, was_b = idb, row = cur.row;
+            const bool last = row + kPaTile >= cur.end;
+            if (!last) {
                 if (++t == 32) {
                     t = 0;
-                    now = next;
-                    if (row + 33 * kPaTile < end) next = page_ids(p.c, b, row + (33 + lane) * kPaTile, end);
+                    ids = later;
+                    if (row + 33 * kPaTile < cur.end) later = page_ids(p.c, cur.b, row + (33 + lane) * kPaTile, cur.end);
                 }
-                ida = __shfl_sync(0xffffffffu, now.a, t);
-                idb = __shfl_sync(0xffffffffu, now.b, t);
-                load_k(p, h, row + kPaTile, end, ida, idb, k);
+                ida = __shfl_sync(0xffffffffu, ids.a, t);
+                idb = __shfl_sync(0xffffffffu, ids.b, t);
+                load_k(p, cur.h, row + kPaTile, cur.end, ida, idb, k);
+            } else if (more) {
+                ida = __shfl_sync(0xffffffffu, then.ids.a, 0);
+                idb = __shfl_sync(0xffffffffu, then.ids.b, 0);
+                load_q(p, then.b, then.h);
+                load_k(p, then.h, 0, then.end, ida, idb, k);
             }
-            if (z) keep(p, z, row, end, was_a, was_b, s);
+            if (kKeep) keep(p, p.z + (static_cast<int64_t>(cur.b) * p.c.H + cur.h) * p.c.cap * p.Gp, row, cur.end, was_a, was_b, s);
             uint32_t b0, b1;
-            softmax(p.scale_log2, row, end, was_a, was_b, s, b0, b1);
+            softmax(p.scale_log2, row, cur.end, was_a, was_b, s, b0, b1);
             values(v, b0, b1);
-            if (more) load_v(p, h, row + kPaTile, end, ida, idb, v);
+            if (!last) {
+                load_v(p, cur.h, row + kPaTile, cur.end, ida, idb, v);
+                cur.row = row + kPaTile;
+                continue;
+            }
+            if (more) load_v(p, then.h, 0, then.end, ida, idb, v);
+            done(cur, more);
+            if (!more) break;
+            reset();
+            cur = then;
+            ids = cur.ids;
+            t = 0;
+            if (cur.row + 32 * kPaTile < cur.end) later = page_ids(p.c, cur.b, cur.row + (32 + lane) * kPaTile, cur.end);
+            more = next(then);
         }
     }
 };
@@ -521,14 +599,17 @@ struct TileF32 {
             }
         }
     }
-    __device__ __forceinline__ void share(const PagedAttnParams& p, int b, int h, int row0, int end, float* z) {
+    template <bool kKeep>
+    __device__ __forceinline__ void share(const PagedAttnParams& p, const Piece& piece) {
+        float* z = kKeep ? p.z + (static_cast<int64_t>(piece.b) * p.c.H + piece.h) * p.c.cap * p.Gp : nullptr;
+        const int b = piece.b, h = piece.h, row0 = piece.row, end = piece.end;
         const int lane = threadIdx.x & 31, hl = lane & 15, half = lane >> 4, mask = (1 << p.c.lg) - 1;
         const float* kb = static_cast<const float*>(p.c.k) + h * p.c.k_head;
         const float* vb = static_cast<const float*>(p.c.v) + h * p.c.v_head;
         // the keys of the next tile and the values of this one are on their way during the scores, where
         // registers allow it (all but eight heads of 128 dimensions)
         constexpr bool kAhead = G * kV < 16;
-        PageIds now = page_ids(p.c, b, row0 + lane * kPaTile, end);
+        PageIds now = piece.ids;
         int t = 0;
         auto id_of = [&](int at) {
             const int ida = __shfl_sync(0xffffffffu, now.a, at), idb = __shfl_sync(0xffffffffu, now.b, at);
@@ -561,7 +642,7 @@ struct TileF32 {
                     }
                 }
                 s[g] = transpose_reduce8(a, hl);
-                if (z && (hl & 1) == 0 && mine + (hl >> 1) < end && g < p.G)
+                if (kKeep && (hl & 1) == 0 && mine + (hl >> 1) < end && g < p.G)
                     z[static_cast<int64_t>(mine + (hl >> 1)) * p.Gp + g] = in ? s[g] : -CUDART_INF_F;
                 up = up || (in && s[g] * p.scale_log2 > m[g] + kPaSlack);
             }
@@ -596,6 +677,18 @@ struct TileF32 {
                     for (int j = 0; j < 4 * kV; ++j) o[g][j] = fmaf(w, v[i][j], o[g][j]);
                 }
             }
+        }
+    }
+    template <bool kKeep, class Next, class Done>
+    __device__ __forceinline__ void stream(const PagedAttnParams& p, Piece cur, float* s_q, Next next, Done done) {
+        for (bool more = true; more;) {
+            load_q(p, cur.b, cur.h, s_q);
+            reset();
+            share<kKeep>(p, cur);
+            Piece then = cur;
+            more = next(then);
+            done(cur, more);
+            cur = then;
         }
     }
     __device__ __forceinline__ void finish(const PagedAttnParams& p, int b, int h, bool alone, JoinSmem<D, G>& js, int slot) {
@@ -693,7 +786,7 @@ __device__ __forceinline__ void join_shares(const PagedAttnParams& p, JoinSmem<D
     }
 }
 
-template <class Tile, int D, bool kF32, int G, int kOcc>
+template <class Tile, int D, bool kF32, int G, int kOcc, bool kKeep>
 __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_constant__ PagedAttnParams p) {
     __shared__ PlanSmem<kPaWarps> s_plan;
     __shared__ __align__(16) JoinSmem<D, G> js;
@@ -704,25 +797,19 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
     if (lane == 0) js.of[2 * warp].b = js.of[2 * warp + 1].b = -1;
     __syncwarp();
     if (w0 < w1) {
-        Walk<kPaTile> at;
-        at.enter(s_plan.b[warp], s_plan.rows[warp], s_plan.at[warp], w0);
+        Pieces pieces;
+        const Piece head = pieces.first(p.c, s_plan.b[warp], s_plan.rows[warp], s_plan.at[warp], w0, w1 - w0);
         Tile tile;
-        for (int64_t cur = w0; cur < w1;) {
-            const int64_t stop = min(w1, at.unit0 + at.nt);
-            const int row0 = static_cast<int>(cur - at.unit0) * kPaTile;
-            const int end = static_cast<int>(min(static_cast<int64_t>(at.rows), (stop - at.unit0) * kPaTile));
-            // (fp32 keeps its queries where the warp's last share will go)
-            tile.load_q(p, at.b, at.h, js.o[2 * warp + 1][0]);
-            tile.reset();
-            float* z = p.z ? p.z + (static_cast<int64_t>(at.b) * p.c.H + at.h) * p.c.cap * p.Gp : nullptr;
-            tile.share(p, at.b, at.h, row0, end, z);
-            const bool begins = cur == at.unit0, ends = stop == at.unit0 + at.nt;
-            const int slot = 2 * warp + (cur == w0 ? 0 : 1);
-            tile.finish(p, at.b, at.h, begins && ends, js, slot);
-            if (!(begins && ends) && lane == 0) js.of[slot] = ShareOf{at.b, at.h, begins, ends, cur == pl.lo};
-            cur = stop;
-            if (cur < w1 && !at.next(p.c)) break;
-        }
+        bool first = true;
+        // (fp32 keeps its queries where the warp's last share will go)
+        tile.template stream<kKeep>(p, head, js.o[2 * warp + 1][0], [&](Piece& q) { return pieces.next(p.c, q); },
+                    [&](const Piece& q, bool more) {
+                        const int slot = 2 * warp + (first ? 0 : 1);
+                        const bool begins = !first || pieces.begins, ends = more || pieces.ends;
+                        tile.finish(p, q.b, q.h, begins && ends, js, slot);
+                        if (!(begins && ends) && lane == 0) js.of[slot] = ShareOf{q.b, q.h, begins, ends, first && w0 == pl.lo};
+                        first = false;
+                    });
     }
     // a unit that ends in this CTA and began before it
     if (tid == 0) {
@@ -763,10 +850,15 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid
     const int t0 = static_cast<int>(static_cast<int64_t>(nt) * part / parts);
     const int t1 = static_cast<int>(static_cast<int64_t>(nt) * (part + 1) / parts);
     Tile tile;
-    tile.load_q(p, b, h, js.o[2 * warp + 1][0]);
-    tile.reset();
-    if (t0 < t1) tile.share(p, b, h, t0 * kPaTile, min(rows, t1 * kPaTile), nullptr);
-    tile.finish(p, b, h, false, js, 2 * warp);
+    auto hand_over = [&](const Piece&, bool) { tile.finish(p, b, h, false, js, 2 * warp); };
+    Piece piece{b, h, t0 * kPaTile, min(rows, t1 * kPaTile), {-1, -1}};
+    if (t0 < t1) {
+        piece.ask(p.c);
+        tile.template stream<false>(p, piece, js.o[2 * warp + 1][0], [](Piece&) { return false; }, hand_over);
+    } else {
+        tile.reset();
+        hand_over(piece, false);
+    }
     __syncthreads();
     // the CTA's share, in slot 1: of the four warps' in order
     if (tid < G && tid < p.G) {
@@ -1065,7 +1157,8 @@ static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
     const int64_t tiles = static_cast<int64_t>(p.c.batch) * p.c.H * ((p.c.cap + kPaTile - 1) / kPaTile);
     const int64_t most = (tiles + kPaLeast * kPaWarps - 1) / (kPaLeast * kPaWarps);
     const int n = most < ncta ? static_cast<int>(most) : ncta;
-    if (launch_first(k_paged_attn<Tile, D, kF32, G, kOcc>, n, kPaThreads, 0, 1, s, p) != cudaSuccess) return -1;
+    auto kernel = p.weight_out ? k_paged_attn<Tile, D, kF32, G, kOcc, true> : k_paged_attn<Tile, D, kF32, G, kOcc, false>;
+    if (launch_first(kernel, n, kPaThreads, 0, 1, s, p) != cudaSuccess) return -1;
     // a CTA per head where units are few and so have many shares; one for all heads where they are many
     const int heads = p.c.batch * static_cast<int64_t>(p.c.H) * 4 >= n ? 1 : p.G;
     if (launch_pdl(k_paged_merge<D, kF32>, dim3(n, heads), dim3(kPaThreads), 0, s, p) != cudaSuccess) return -1;
