@@ -25,16 +25,16 @@ namespace skv {
 
 static __device__ int g_err[2];
 
-constexpr int kEvThreads = 512;
-constexpr int kEvWarps = kEvThreads / 32;
+constexpr int kEvWide = 512, kEvNarrow = 128;  // threads of a CTA: two per SM, or eight
 constexpr int kEvStep = 256;                   // rows of a warp's step, eight per lane
-constexpr int kEvGrain = kEvStep * kEvWarps;   // a slice is a multiple of this many rows
 constexpr int kEvBins = 2048;
-constexpr int kEvKeys = 11 * kEvGrain;         // halves of keys held in shared memory at most (88 KB: two CTAs per SM)
-static_assert(kEvBins == 4 * kEvThreads && kEvWarps <= 32, "the search reads four bins per thread");
+constexpr int grain_of(int threads) { return kEvStep * (threads / 32); }     // a slice is a multiple of this many rows
+constexpr int kEvKeys = 11 * grain_of(kEvWide);   // halves of keys held in shared memory at most (88 KB: two CTAs per SM)
+
 // Rows of a unit that its own cluster moves, at most.  Of 2048 rows + 256, 64 units take 14.6 us with one
 // kernel and 15.9 with two, + 512 19.1 and 20.5 (8 units: 16.1 and 15.3), + 952 29.4 and 24.0.
 constexpr int kEvFew = 512;
+constexpr int kEvShort = 4096;                 // room of a sequence that narrow CTAs serve, at most
 constexpr int kEvHist = 2 * kEvBins + 64;      // counts of the four passes
 
 // weights in the order of unsigned integers: -0 counts as 0, a NaN lies above +inf
@@ -166,16 +166,18 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, int u, int moves
     }
 }
 
-template <bool kMove>
-__global__ void __launch_bounds__(kEvThreads, 2) k_evict(const __grid_constant__ EvictParams p, int ranks,
+template <int kThreads, bool kMove>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_evict(const __grid_constant__ EvictParams p, int ranks,
                                                                  int key_cap, int low_cap) {
+    constexpr int kWarps = kThreads / 32, kGrain = grain_of(kThreads), kEach = kEvBins / kThreads;     // bins per thread
+    static_assert(kEach * kThreads == kEvBins && kEach % 4 == 0 && kWarps >= 4 && kWarps <= 32, "");
     extern __shared__ __align__(16) int sm[];
     int* s_hist = sm;                                                  // [kEvHist]
     uint16_t* s_key = reinterpret_cast<uint16_t*>(sm + kEvHist);      // [key_cap] upper halves of the keys
     uint16_t* s_low = s_key + key_cap;                                 // [low_cap] lower halves
-    __shared__ int s_scan[kEvWarps], s_bin[3], s_maxes[kEvWarps], s_max;
-    __shared__ int s_cnt[4][kEvWarps], s_tot[4];
-    __shared__ int s_tie[kEvWarps], s_hole[kEvWarps], s_src[kEvWarps], s_moves;
+    __shared__ int s_scan[kWarps], s_bin[3], s_maxes[kWarps], s_max;
+    __shared__ int s_cnt[4][kWarps], s_tot[4];
+    __shared__ int s_tie[kWarps], s_hole[kWarps], s_src[kWarps], s_moves;
 
     begin_call();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -188,8 +190,8 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict(const __grid_constant__
     const int32_t* p_in = p.position + base;
     const bool copy_w = p.weight_out != p.weight, copy_p = p.position_out != p.position;
     const int64_t slice = (static_cast<int64_t>(n) + ranks - 1) / ranks;
-    const int per = static_cast<int>((slice + kEvGrain - 1) / kEvGrain) * kEvStep;        // rows of a warp
-    const int64_t lo64 = (static_cast<int64_t>(rank) * kEvWarps + warp) * per;
+    const int per = static_cast<int>((slice + kGrain - 1) / kGrain) * kEvStep;        // rows of a warp
+    const int64_t lo64 = (static_cast<int64_t>(rank) * kWarps + warp) * per;
     const int lo = static_cast<int>(min(lo64, static_cast<int64_t>(n)));
     const int hi = static_cast<int>(min(lo64 + per, static_cast<int64_t>(n)));
     // (the other heads' CTAs may not have read a length that is to be updated in place: it goes by new_len)
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict(const __grid_constant__
         return;
     }
 
-    for (int i = tid; i < kEvHist; i += kEvThreads) s_hist[i] = 0;
+    for (int i = tid; i < kEvHist; i += kThreads) s_hist[i] = 0;
     // ---- the unit's last position
     int last = INT_MIN;
     constexpr int kDeep = 4;       // steps whose loads are in flight together
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict(const __grid_constant__
     if (lane == 0) s_maxes[warp] = last;
     __syncthreads();
     if (warp == 0) {
-        int x = s_maxes[lane % kEvWarps];
+        int x = s_maxes[lane % kWarps];
 #pragma unroll
         for (int o = 16; o; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
         if (lane == 0) s_max = x;
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict(const __grid_constant__
         if (r != rank) last = max(last, ld_cluster_s32(cluster_addr(&s_max, r)));
     const Protect pr{static_cast<int>(max(static_cast<int64_t>(last) - p.recent, static_cast<int64_t>(-1))), p.sink};
 
-    const bool held = per * kEvWarps <= key_cap, held_low = (warp + 1) * per <= low_cap;
+    const bool held = per * kWarps <= key_cap, held_low = (warp + 1) * per <= low_cap;
     uint16_t *my = s_key + warp * per, *my_low = s_low + warp * per;
     // halves of the lane's eight keys from row s on
     auto upper = [&](int s) { return held ? *reinterpret_cast<const uint4*>(my + (s - lo)) : remade(w_in, p_in, s, pr, 16); };
@@ -308,26 +310,31 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict(const __grid_constant__
             }
         }
         sync_all(ranks);
-        // counts from the top: thread t holds four bins, the uppermost first
-        int cnt[4] = {0, 0, 0, 0};
-        const int top = bins - 1 - 4 * tid;
+        // counts from the top: thread t holds kEach bins, the uppermost first
+        int cnt[kEach], mine = 0;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) cnt[e] = 0;
+        const int top = bins - 1 - kEach * tid;
         if (top >= 0) {
-            const int4 own = *reinterpret_cast<const int4*>(hist + top - 3);
-            cnt[0] = own.w, cnt[1] = own.z, cnt[2] = own.y, cnt[3] = own.x;
-            for (int r = 0; r < ranks; ++r)
-                if (r != rank) {
-                    const int4 v = ld_cluster_v4(cluster_addr(hist + top - 3, r));
-                    cnt[0] += v.w, cnt[1] += v.z, cnt[2] += v.y, cnt[3] += v.x;
-                }
+#pragma unroll
+            for (int e = 0; e < kEach; e += 4) {
+                const int4 own = *reinterpret_cast<const int4*>(hist + top - 3 - e);
+                cnt[e] = own.w, cnt[e + 1] = own.z, cnt[e + 2] = own.y, cnt[e + 3] = own.x;
+                for (int r = 0; r < ranks; ++r)
+                    if (r != rank) {
+                        const int4 v = ld_cluster_v4(cluster_addr(hist + top - 3 - e, r));
+                        cnt[e] += v.w, cnt[e + 1] += v.z, cnt[e + 2] += v.y, cnt[e + 3] += v.x;
+                    }
+                mine += cnt[e] + cnt[e + 1] + cnt[e + 2] + cnt[e + 3];
+            }
         }
-        const int mine = cnt[0] + cnt[1] + cnt[2] + cnt[3];
         int above = excl_scan(mine, lane);
         if (lane == 31) s_scan[warp] = above + mine;
         __syncthreads();
-        above += __reduce_add_sync(0xffffffffu, lane < warp ? s_scan[lane % kEvWarps] : 0);
+        above += __reduce_add_sync(0xffffffffu, lane < warp ? s_scan[lane % kWarps] : 0);
         if (above < need && above + mine >= need) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < kEach; ++e) {
                 if (above < need && above + cnt[e] >= need) {
                     s_bin[0] = top - e;
                     s_bin[1] = above;
@@ -500,7 +507,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict(const __grid_constant__
         }
         __syncthreads();
         if (warp < 4) {
-            const int x = __reduce_add_sync(0xffffffffu, lane < kEvWarps ? s_cnt[warp][lane] : 0);
+            const int x = __reduce_add_sync(0xffffffffu, lane < kWarps ? s_cnt[warp][lane] : 0);
             if (lane == 0) s_tot[warp] = x;
         }
         sync_all(ranks);
@@ -518,8 +525,8 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict(const __grid_constant__
                 tie_sum += v[1] + v[3];
             }
             if (lane == 0) s_moves = min(min(hole_sum, src_sum), p.list_cap);
-            const int w = lane % kEvWarps;
-            const bool own = lane < kEvWarps;
+            const int w = lane % kWarps;
+            const bool own = lane < kWarps;
             const int a = own ? s_cnt[0][w] : 0, tl = own ? s_cnt[1][w] : 0, g = own ? s_cnt[2][w] : 0, th = own ? s_cnt[3][w] : 0;
             const int t0 = tie0 + excl_scan(tl + th, lane);
             const int left = max(0, ties - t0), kl = min(tl, left), kh = min(th, left - kl);
@@ -539,7 +546,7 @@ __global__ void __launch_bounds__(kEvThreads, 2) k_evict(const __grid_constant__
 
     if (kMove) {
         sync_all(ranks);       // the lists are whole
-        move_rows(p, u, s_moves, rank * kEvWarps + warp, ranks * kEvWarps);
+        move_rows(p, u, s_moves, rank * kWarps + warp, ranks * kWarps);
     } else if (rank == 0 && tid == 0) {
         p.count[u] = s_moves;
     }
@@ -561,21 +568,25 @@ __global__ void k_evict_lens(const __grid_constant__ EvictParams p) {
 
 int launch_evict(const EvictParams& p, int nsm, cudaStream_t s) {
     const int U = p.c.batch * p.c.H;
-    // CTAs per unit: as many as the device holds at once (two per SM), and no fewer than the keys
-    // need to stay in shared memory; a slice of under one grain (4096 rows) would leave warps idle
+    // Many short units of which few rows can move go to narrow CTAs, of which an SM holds eight (2048 units
+    // of 501 rows, one of them given up: 29.4 us against 79.9; of 2049 rows: 55.0 against 98.0; but 66.6
+    // against 61.1 for 320 units of 3000 rows with 952 given up).  The others go to as many CTAs as the
+    // device holds at once (two per SM), and no fewer than the keys need to stay in shared memory.  A
+    // slice of under one grain would leave warps idle.
+    const bool few = p.list_cap <= kEvFew, narrow = few && U > 2 * nsm && p.c.cap <= kEvShort;
+    const int threads = narrow ? kEvNarrow : kEvWide, grain = grain_of(threads);
     int ranks = 1;
-    while (ranks < 8 && p.c.cap > ranks * kEvGrain && (U * ranks <= nsm || p.c.cap / ranks > kEvKeys)) ranks *= 2;
+    while (!narrow && ranks < 8 && p.c.cap > ranks * grain && (U * ranks <= nsm || p.c.cap / ranks > kEvKeys)) ranks *= 2;
     const int64_t slice = (static_cast<int64_t>(p.c.cap) + ranks - 1) / ranks;
-    const int64_t keys = (slice + kEvGrain - 1) / kEvGrain * kEvGrain;
+    const int64_t keys = (slice + grain - 1) / grain * grain;
     const int key_cap = static_cast<int>(keys < kEvKeys ? keys : kEvKeys);
     // the lower halves only where a slice is short: what they take of shared memory is taken from L1
     // (128K rows: 68 us with the upper halves alone, 79 with some of the lower ones)
     const int low_cap = 2 * key_cap <= kEvKeys ? key_cap : 0;
     const int smem = kEvHist * 4 + (key_cap + low_cap) * 2;
-    const bool few = p.list_cap <= kEvFew;
-    auto kernel = few ? k_evict<true> : k_evict<false>;
+    auto kernel = narrow ? k_evict<kEvNarrow, true> : few ? k_evict<kEvWide, true> : k_evict<kEvWide, false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvHist * 4 + kEvKeys * 2) != cudaSuccess ||
-        launch_first(kernel, static_cast<unsigned>(U) * ranks, kEvThreads, smem, ranks, s, p, ranks, key_cap, low_cap) !=
+        launch_first(kernel, static_cast<unsigned>(U) * ranks, threads, smem, ranks, s, p, ranks, key_cap, low_cap) !=
             cudaSuccess)
         return -1;
     cudaError_t e = cudaSuccess;

@@ -541,6 +541,8 @@ def run_evict(c, weight, position, budget, recent, sink, in_place):
     ("bf16", [10000, 9], 1, 64, 64, "hnd", 2464, 32, 4, "ties"),      # two CTAs per unit
     ("bf16", [40000], 2, 64, 64, "hnd", 1000, 32, 4, "ties"),         # eight
     ("bf16", [70000, 65000], 1, 64, 1024, "nhd", 66000, 9, 2, "plain"),
+    ("bf16", [(i * 53) % 300 for i in range(50)], 7, 64, 16, "hnd", 90, 8, 2, "ties"),      # many short units
+    ("fp8", [3000 - i for i in range(80)], 4, 64, 32, "nhd", 1200, 30, 2, "wild"),          # many units, many rows that move
 ])
 def test_eviction_matches(kind, lens, heads, d, ps, layout, budget, recent, sink, flavour, in_place):
     c = Paged(kind, lens, heads, d, ps, layout, seed=budget)
