@@ -23,7 +23,7 @@ static __device__ int g_err[2];
 
 constexpr int kNrThreads = 128;
 constexpr int kNrOcc = 6;         // CTAs per SM
-constexpr int kNrMaxTok = 16;     // tokens of a CTA at most
+constexpr int max_tokens(int d) { return 2048 / d; }     // of a CTA, for their angles' 8 KB of shared memory
 
 // 16 elements of a row as they lie in memory: 8 at o1, 8 at o2
 template <typename T> struct Raw;
@@ -66,7 +66,7 @@ template <typename T, int D, bool kE5M2>
 __global__ void __launch_bounds__(kNrThreads, kNrOcc) k_norm_rope(const __grid_constant__ NormRopeParams p) {
     constexpr int kLanes = D / 16;                  // lanes of a row
     constexpr int kDeep = sizeof(T) == 2 ? 3 : 2;   // rows of a thread whose loads are in flight at once
-    __shared__ __align__(16) float s_cos[kNrMaxTok * D / 2], s_sin[kNrMaxTok * D / 2];
+    __shared__ __align__(16) float s_cos[max_tokens(D) * D / 2], s_sin[max_tokens(D) * D / 2];
 
     begin_call();
     // p.groups lane groups share a token; group g of it takes the heads g, g + groups, ... of q, and
@@ -211,21 +211,16 @@ template <typename T, int D, bool kE5M2>
 static int launch_nr(NormRopeParams p, int nsm, cudaStream_t s) {
     constexpr int kRows = kNrThreads / (D / 16);
     const int n_kv = p.c.H * (p.c.k ? 2 : 1);
-    // lane groups per token.  A decode step has few tokens: all of a CTA's groups work on one.  A
-    // prompt takes the number that leaves the fewest groups without a head, and of equals the
-    // smallest from four on (each thread then has more rows of a token whose angles it holds: 32K
-    // tokens of 32 + 2 x 8 heads in 141 us against 143 with two and 151 with eight), or from two on
-    // where four would make less than two waves of CTAs (5K tokens of 16 + 2 x 2 heads: 14.7 us
-    // against 16.2).
+    // Lane groups per token: all of a CTA's, or fewer as long as that leaves four CTAs per SM.  Then the
+    // number that leaves the fewest groups without a head, and of equals the largest whose threads
+    // have ten rows of a token (whose angles they hold), or the smallest (32K tokens of 32 + 2 x 8
+    // heads, four groups: 141 us, two 143, eight 151; 5K tokens of 16 + 2 x 2 heads, two groups: 14.7 us,
+    // four 16.2).
+    auto slots_of = [&](int g) { return (p.nq + g - 1) / g + (n_kv + g - 1) / g; };
     p.groups = kRows;
-    if (p.tokens > 2 * nsm) {
-        const int least = p.tokens / (kRows / 4) <= 2 * kNrOcc * nsm ? 2 : 4;
-        int best = 1 << 30;
-        for (int g = kRows; g >= 1; g /= 2) {
-            if (kRows / g > kNrMaxTok) break;
-            const int spent = ((p.nq + g - 1) / g + (n_kv + g - 1) / g) * g;
-            if (spent < best || (spent == best && g >= least)) best = spent, p.groups = g;
-        }
+    for (int g = kRows / 2; g >= 1 && kRows / g <= max_tokens(D) && p.tokens / (kRows / g) >= 4 * nsm; g /= 2) {
+        const int spent = slots_of(g) * g, had = slots_of(p.groups) * p.groups;
+        if (spent < had || (spent == had && slots_of(p.groups) < 10)) p.groups = g;
     }
     const int per = kRows / p.groups, grid = (p.tokens + per - 1) / per;
     return launch_first(k_norm_rope<T, D, kE5M2>, grid, kNrThreads, 0, 1, s, p) == cudaSuccess ? 0 : -1;

@@ -101,7 +101,7 @@ __device__ __forceinline__ int tiles_of(int n) { return (n + R - 1) / R; }
 
 // What CTA `me` of `ctas` takes of the tiles of R rows, and where its W parts begin.  A part has `least` tiles, or
 // joining the shares would take longer than forming them (one unit of 32K rows: 17.4 us with four,
-// 19.2 with two, 23.2 with one).
+// 19.2 with two, 23.2 with one).  The tiles of fp32 take longer, and so may come one by one.
 constexpr int kPaLeast = 4;
 
 template <int W>
@@ -311,6 +311,26 @@ struct Pieces {
     }
 };
 
+// Where the products q.k of a tile's rows are kept for the weights, [row][Gp]: nowhere, in the
+// workspace, or in the warp's part of shared memory.
+struct KeepNone {
+    static constexpr bool on = false;
+    __device__ __forceinline__ float* operator()(int, int, int) const { return nullptr; }
+};
+struct KeepGlobal {
+    static constexpr bool on = true;
+    const PagedAttnParams& p;
+    __device__ __forceinline__ float* operator()(int b, int h, int row) const {
+        return p.z + ((static_cast<int64_t>(b) * p.c.H + h) * p.c.cap + row) * p.Gp;
+    }
+};
+struct KeepShared {
+    static constexpr bool on = true;
+    float* z;
+    int row0, Gp;
+    __device__ __forceinline__ float* operator()(int, int, int row) const { return z + (row - row0) * Gp; }
+};
+
 template <int D, bool kE5M2>
 struct TileTC {
     static constexpr int kKV = D / 32;                     // 16-byte words of a key row per lane
@@ -377,16 +397,16 @@ struct TileTC {
             mma_bf16(s, k.a[j].z, k.b[j].z, k.a[j].w, k.b[j].w, q[j].z, q[j].w);
         }
     }
-    // raw products kept for the weights: z [row][Gp]
+    // raw products kept for the weights, z [row][Gp] from the tile's first row on
     __device__ __forceinline__ void keep(const PagedAttnParams& p, float* z, int row, int end, int ida, int idb,
                                          const float (&s)[4]) {
         const int r = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
         if (2 * c >= p.G) return;
         if (row + r < end)
-            *reinterpret_cast<float2*>(z + static_cast<int64_t>(row + r) * p.Gp + 2 * c) =
+            *reinterpret_cast<float2*>(z + r * p.Gp + 2 * c) =
                 ida >= 0 ? make_float2(s[0], s[1]) : make_float2(-CUDART_INF_F, -CUDART_INF_F);
         if (row + 8 + r < end)
-            *reinterpret_cast<float2*>(z + static_cast<int64_t>(row + 8 + r) * p.Gp + 2 * c) =
+            *reinterpret_cast<float2*>(z + (8 + r) * p.Gp + 2 * c) =
                 idb >= 0 ? make_float2(s[2], s[3]) : make_float2(-CUDART_INF_F, -CUDART_INF_F);
     }
     // probabilities against the running base; returns P^T as the second product's operand
@@ -499,8 +519,8 @@ struct TileTC {
     // The pieces from `cur` on, as one stream of tiles: the first loads of the next piece are on their
     // way before this one is done with.  next(piece) gives the following one; done(piece, whether there is
     // another) hands over.
-    template <bool kKeep, class Next, class Done>
-    __device__ __forceinline__ void stream(const PagedAttnParams& p, Piece cur, float*, Next next, Done done) {
+    template <class Keep, class Next, class Done>
+    __device__ __forceinline__ void stream(const PagedAttnParams& p, Piece cur, float*, Keep z, Next next, Done done) {
         const int lane = threadIdx.x & 31;
         Piece then;
         bool more = next(then);
@@ -534,7 +554,7 @@ struct TileTC {
                 load_q(p, then.b, then.h);
                 load_k(p, then.h, 0, then.end, ida, idb, k);
             }
-            if (kKeep) keep(p, p.z + (static_cast<int64_t>(cur.b) * p.c.H + cur.h) * p.c.cap * p.Gp, row, cur.end, was_a, was_b, s);
+            if (Keep::on) keep(p, z(cur.b, cur.h, row), row, cur.end, was_a, was_b, s);
             uint32_t b0, b1;
             softmax(p.scale_log2, row, cur.end, was_a, was_b, s, b0, b1);
             values(v, b0, b1);
@@ -599,9 +619,8 @@ struct TileF32 {
             }
         }
     }
-    template <bool kKeep>
-    __device__ __forceinline__ void share(const PagedAttnParams& p, const Piece& piece) {
-        float* z = kKeep ? p.z + (static_cast<int64_t>(piece.b) * p.c.H + piece.h) * p.c.cap * p.Gp : nullptr;
+    template <class Keep>
+    __device__ __forceinline__ void share(const PagedAttnParams& p, const Piece& piece, const Keep& z) {
         const int b = piece.b, h = piece.h, row0 = piece.row, end = piece.end;
         const int lane = threadIdx.x & 31, hl = lane & 15, half = lane >> 4, mask = (1 << p.c.lg) - 1;
         const float* kb = static_cast<const float*>(p.c.k) + h * p.c.k_head;
@@ -642,8 +661,8 @@ struct TileF32 {
                     }
                 }
                 s[g] = transpose_reduce8(a, hl);
-                if (kKeep && (hl & 1) == 0 && mine + (hl >> 1) < end && g < p.G)
-                    z[static_cast<int64_t>(mine + (hl >> 1)) * p.Gp + g] = in ? s[g] : -CUDART_INF_F;
+                if (Keep::on && (hl & 1) == 0 && mine + (hl >> 1) < end && g < p.G)
+                    z(b, h, mine + (hl >> 1))[g] = in ? s[g] : -CUDART_INF_F;
                 up = up || (in && s[g] * p.scale_log2 > m[g] + kPaSlack);
             }
             if (!kAhead) load(vb, p.c.v_page, p.c.v_row, mask, mine, end, id, v);
@@ -679,12 +698,12 @@ struct TileF32 {
             }
         }
     }
-    template <bool kKeep, class Next, class Done>
-    __device__ __forceinline__ void stream(const PagedAttnParams& p, Piece cur, float* s_q, Next next, Done done) {
+    template <class Keep, class Next, class Done>
+    __device__ __forceinline__ void stream(const PagedAttnParams& p, Piece cur, float* s_q, Keep z, Next next, Done done) {
         for (bool more = true; more;) {
             load_q(p, cur.b, cur.h, s_q);
             reset();
-            share<kKeep>(p, cur);
+            share(p, cur, z);
             Piece then = cur;
             more = next(then);
             done(cur, more);
@@ -792,7 +811,7 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
     __shared__ __align__(16) JoinSmem<D, G> js;
     begin_call();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, me = blockIdx.x;
-    const Plan<kPaWarps> pl = make_plan<kPaWarps, kPaTile, kPaLeast>(p.c, me, gridDim.x, s_plan);
+    const Plan<kPaWarps> pl = make_plan<kPaWarps, kPaTile, kF32 ? 1 : kPaLeast>(p.c, me, gridDim.x, s_plan);
     const int64_t w0 = pl.part(warp), w1 = pl.part(warp + 1);
     if (lane == 0) js.of[2 * warp].b = js.of[2 * warp + 1].b = -1;
     __syncwarp();
@@ -802,14 +821,17 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
         Tile tile;
         bool first = true;
         // (fp32 keeps its queries where the warp's last share will go)
-        tile.template stream<kKeep>(p, head, js.o[2 * warp + 1][0], [&](Piece& q) { return pieces.next(p.c, q); },
-                    [&](const Piece& q, bool more) {
-                        const int slot = 2 * warp + (first ? 0 : 1);
-                        const bool begins = !first || pieces.begins, ends = more || pieces.ends;
-                        tile.finish(p, q.b, q.h, begins && ends, js, slot);
-                        if (!(begins && ends) && lane == 0) js.of[slot] = ShareOf{q.b, q.h, begins, ends, first && w0 == pl.lo};
-                        first = false;
-                    });
+        auto next = [&](Piece& q) { return pieces.next(p.c, q); };
+        auto done = [&](const Piece& q, bool more) {
+            const int slot = 2 * warp + (first ? 0 : 1);
+            const bool begins = !first || pieces.begins, ends = more || pieces.ends;
+            tile.finish(p, q.b, q.h, begins && ends, js, slot);
+            if (!(begins && ends) && lane == 0) js.of[slot] = ShareOf{q.b, q.h, begins, ends, first && w0 == pl.lo};
+            first = false;
+        };
+        float* queries = js.o[2 * warp + 1][0];
+        if constexpr (kKeep) tile.stream(p, head, queries, KeepGlobal{p}, next, done);
+        else tile.stream(p, head, queries, KeepNone{}, next, done);
     }
     // a unit that ends in this CTA and began before it
     if (tid == 0) {
@@ -837,24 +859,32 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
 
 // Short sequences of few units, where the latency of a step counts: a cluster of CTAs per unit, whose
 // warps share its rows evenly.  No search for the place, no records and no second kernel: each CTA
-// joins its warps' shares, and the cluster joins the CTAs' through distributed shared memory.
-template <class Tile, int D, bool kF32, int G, int kOcc>
+// joins its warps' shares, and the cluster joins the CTAs' through distributed shared memory.  The
+// products for the weights stay in shared memory until the sums are known.
+constexpr int kClusterTiles = 8;      // tiles of a warp at most
+template <class Tile, int D, bool kF32, int G, int kOcc, bool kKeep>
 __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid_constant__ PagedAttnParams p, int ranks) {
+    extern __shared__ __align__(16) float s_z[];        // [warps][kClusterTiles * kPaTile][Gp]
     __shared__ __align__(16) JoinSmem<D, G> js;
     begin_call();
-    const int tid = threadIdx.x, warp = tid >> 5;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int u = blockIdx.x / ranks, rank = ranks > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int b = u / p.c.H, h = u % p.c.H;
     const int rows = rows_of(p.c, b, g_err, 711);
     const int nt = tiles_of(rows), parts = ranks * kPaWarps, part = rank * kPaWarps + warp;
     const int t0 = static_cast<int>(static_cast<int64_t>(nt) * part / parts);
     const int t1 = static_cast<int>(static_cast<int64_t>(nt) * (part + 1) / parts);
+    float* my_z = s_z + warp * kClusterTiles * kPaTile * (kKeep ? p.Gp : 0);
     Tile tile;
     auto hand_over = [&](const Piece&, bool) { tile.finish(p, b, h, false, js, 2 * warp); };
-    Piece piece{b, h, t0 * kPaTile, min(rows, t1 * kPaTile), {-1, -1}};
+    const int piece_row = t0 * kPaTile, piece_end = t0 < t1 ? min(rows, t1 * kPaTile) : piece_row;
+    Piece piece{b, h, piece_row, piece_end, {-1, -1}};
     if (t0 < t1) {
         piece.ask(p.c);
-        tile.template stream<false>(p, piece, js.o[2 * warp + 1][0], [](Piece&) { return false; }, hand_over);
+        float* queries = js.o[2 * warp + 1][0];
+        auto none = [](Piece&) { return false; };
+        if constexpr (kKeep) tile.stream(p, piece, queries, KeepShared{my_z, piece.row, p.Gp}, none, hand_over);
+        else tile.stream(p, piece, queries, KeepNone{}, none, hand_over);
     } else {
         tile.reset();
         hand_over(piece, false);
@@ -919,6 +949,32 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid
         for (int e = 0; e < 4; ++e) x[e] = l == 0.f ? 0.f : x[e] / l;
         store4<kF32>(p, b, h, g, dim, x);
         if (dim == 0) note(p, b, h, g, m, l);
+    }
+    if (kKeep) {
+        // the unit's base and 1 / sum per head, then the weights of the warp's own rows
+        __shared__ float2 s_stat[G];
+        if (tid < G && tid < p.G) {
+            float m = -CUDART_INF_F, l = 0.f;
+            for (int r = 0; r < ranks; ++r) m = fmaxf(m, ranks > 1 ? ld_cluster_f32(cluster_addr(&js.m[1][tid], r)) : js.m[1][tid]);
+            for (int r = 0; r < ranks; ++r) {
+                const float rm = ranks > 1 ? ld_cluster_f32(cluster_addr(&js.m[1][tid], r)) : js.m[1][tid];
+                const float rl = ranks > 1 ? ld_cluster_f32(cluster_addr(&js.l[1][tid], r)) : js.l[1][tid];
+                l = fmaf(rl, share_weight(rm, rl, m), l);
+            }
+            s_stat[tid] = make_float2(m, l == 0.f ? 0.f : 1.f / l);
+        }
+        __syncthreads();
+        const float* in = p.weight + u * p.row_pitch;
+        float* out = p.weight_out + u * p.row_pitch;
+        for (int i = piece_row + lane; i < piece_end; i += 32) {
+            float sum = 0.f;
+            for (int g = 0; g < p.G; ++g) {
+                const float x = my_z[(i - piece_row) * p.Gp + g];
+                // an absent row's product is -inf and adds nothing
+                if (x != -CUDART_INF_F) sum += exp2_fast(fmaf(x, p.scale_log2, -s_stat[g].x)) * s_stat[g].y;
+            }
+            out[i] = in[i] + sum;
+        }
     }
     if (ranks > 1) cluster_sync_all();       // no CTA leaves while another reads its share
 }
@@ -1131,9 +1187,7 @@ int paged_attn_ctas(int dtype, int nsm) { return nsm * (dtype == SKV_F32 ? kOccF
 
 // CTAs of a unit's cluster, or 0: the general form.  The cluster form serves a step whose units leave
 // SMs idle and whose longest possible sequence takes a warp no more than kClusterTiles tiles.
-constexpr int kClusterTiles = 8;
 static int cluster_ranks(const PagedAttnParams& p, int ncta) {
-    if (p.weight_out) return 0;
     const int64_t U = static_cast<int64_t>(p.c.batch) * p.c.H, tiles = (p.c.cap + kPaTile - 1) / kPaTile;
     int ranks = 1;
     while (ranks < 16 && tiles > ranks * kPaWarps && 2 * U * ranks <= ncta) ranks *= 2;
@@ -1142,9 +1196,11 @@ static int cluster_ranks(const PagedAttnParams& p, int ncta) {
 
 template <class Tile, int D, bool kF32, int G, int kOcc>
 static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
-    auto kernel = k_paged_cluster<Tile, D, kF32, G, kOcc>;
+    auto kernel = p.weight_out ? k_paged_cluster<Tile, D, kF32, G, kOcc, true> : k_paged_cluster<Tile, D, kF32, G, kOcc, false>;
+    const int smem = p.weight_out ? kPaWarps * kClusterTiles * kPaTile * p.Gp * 4 : 0;
     if (ranks > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return -1;
-    return launch_first(kernel, static_cast<unsigned>(p.c.batch) * p.c.H * ranks, kPaThreads, 0, ranks, s, p, ranks) ==
+    if (smem && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
+    return launch_first(kernel, static_cast<unsigned>(p.c.batch) * p.c.H * ranks, kPaThreads, smem, ranks, s, p, ranks) ==
                    cudaSuccess
                ? 0
                : -1;
@@ -1155,7 +1211,8 @@ static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
     if (const int ranks = cluster_ranks(p, ncta)) return launch_cluster<Tile, D, kF32, G, kOcc>(p, ranks, s);
     // no more CTAs than there can be tiles for their warps
     const int64_t tiles = static_cast<int64_t>(p.c.batch) * p.c.H * ((p.c.cap + kPaTile - 1) / kPaTile);
-    const int64_t most = (tiles + kPaLeast * kPaWarps - 1) / (kPaLeast * kPaWarps);
+    constexpr int kMin = (kF32 ? 1 : kPaLeast) * kPaWarps;
+    const int64_t most = (tiles + kMin - 1) / kMin;
     const int n = most < ncta ? static_cast<int>(most) : ncta;
     auto kernel = p.weight_out ? k_paged_attn<Tile, D, kF32, G, kOcc, true> : k_paged_attn<Tile, D, kF32, G, kOcc, false>;
     if (launch_first(kernel, n, kPaThreads, 0, 1, s, p) != cudaSuccess) return -1;

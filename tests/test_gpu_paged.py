@@ -98,22 +98,20 @@ def test_attention_matches_float64(kind, G, heads, d, ps, layout, lens):
     q = queries(c, G)
     # a table with room for far longer sequences: steps of few short ones are then split another way
     wide = torch.cat([c.table, torch.full((len(lens), 16384 // ps), -1, dtype=torch.int32, device="cuda")], 1)
-    out, lse = torch.full_like(q, float("nan")), torch.full(q.shape[:2], float("nan"), device="cuda")
-    skv.paged_attention(q, c.k, c.v, wide, c.lens, out, lse)
-    check_all(c, q, out, lse)
-    for weigh in (False, True):
-        out = torch.full_like(q, float("nan"))
-        lse = torch.full(q.shape[:2], float("nan"), device="cuda")
-        if weigh:
-            weight = torch.rand((len(lens), heads, c.rows), device="cuda")
-            held = torch.full_like(weight, -7.0)
-            skv.paged_attention(q, c.k, c.v, c.table, c.lens, out, lse, weight, held)
-            check_all(c, q, out, lse, None, weight, held)
-            for b, n in enumerate(lens):
-                assert (held[b, :, n:] == -7.0).all()                   # rows behind are left as they were
-        else:
-            skv.paged_attention(q, c.k, c.v, c.table, c.lens, out, lse)
-            check_all(c, q, out, lse)
+    for table in (c.table, wide):
+        for weigh in (False, True):
+            out = torch.full_like(q, float("nan"))
+            lse = torch.full(q.shape[:2], float("nan"), device="cuda")
+            if weigh:
+                weight = torch.rand((len(lens), heads, table.shape[1] * ps), device="cuda")
+                held = torch.full_like(weight, -7.0)
+                skv.paged_attention(q, c.k, c.v, table, c.lens, out, lse, weight, held)
+                check_all(c, q, out, lse, None, weight, held)
+                for b, n in enumerate(lens):
+                    assert (held[b, :, n:] == -7.0).all()               # rows behind are left as they were
+            else:
+                skv.paged_attention(q, c.k, c.v, table, c.lens, out, lse)
+                check_all(c, q, out, lse)
     assert skv.paged_status() == 0
 
 
