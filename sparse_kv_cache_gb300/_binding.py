@@ -244,6 +244,11 @@ def _form(t):
     return None if t is None else (t.shape, t.stride(), t.dtype)
 
 
+def _steps(t, n: int):
+    """The first n strides, 0 where a dimension is never stepped through."""
+    return tuple(0 if size == 1 else step for size, step in zip(t[0][:n], t[1]))
+
+
 def _pool_fields(where: str, k, v, table, lens, batch: int):
     """The fields of skv_paged_cache before its pointers, from the forms of the tensors: pools
     [n_pages][H][page_size][d] with any strides over a contiguous head dimension, table int32
@@ -260,7 +265,8 @@ def _pool_fields(where: str, k, v, table, lens, batch: int):
     if lens is not None:
         _vector(where, "lens", lens, batch)
     pages, heads, size, d = k[0]
-    return (code, heads, d, size, batch, table[0][1], pages, *k[1][:3], *v[1][:3], max(table[1][0], table[0][1]))
+    return (code, heads, d, size, batch, table[0][1], pages, *_steps(k, 3), *_steps(v, 3),
+            table[1][0] if batch > 1 else table[0][1])
 
 
 def _rows(where: str, name: str, t, dtype: str, batch: int, heads: int, need: int) -> int:
@@ -275,7 +281,7 @@ def _heads(where: str, name: str, t, dtype, shape):
     """Strides over (token or sequence, head) of a [..][heads][d] tensor, head dimension contiguous."""
     if t is None or t[0] != shape or t[1][2] != 1 or t[2] != dtype:
         _refuse(where, f"{name} is {dtype} {list(shape)}, head_dim contiguous")
-    return t[1][:2]
+    return _steps(t, 2)
 
 
 def _vector(where: str, name: str, t, n: int, dtype: str = "torch.int32"):

@@ -198,6 +198,16 @@ def test_strided_queries_and_results():
     assert wide[..., :16].isnan().all() and wide[..., 144:].isnan().all()
 
 
+def test_strides_of_dimensions_that_are_not_stepped_through():
+    """One sequence, one KV head: their strides may be anything, a row of 129 elements too."""
+    c = Paged("bf16", [30], 1, 64, 16, seed=44)
+    odd = lambda t: t.as_strided(t.shape, (t.stride(0), 129, t.stride(2), 1))  # noqa: E731
+    q = torch.randn((1, 1, 64), device="cuda").to(torch.bfloat16).as_strided((1, 1, 64), (77, 33, 1))
+    out = torch.empty_like(q)
+    skv.paged_attention(q, odd(c.k), odd(c.v), c.table[:, :2].as_strided((1, 2), (5, 1)), c.lens, out)
+    check_all(c, q, out, None)
+
+
 def test_pages_of_two_sequences_may_be_the_same():
     c = Paged("bf16", [48, 48], 2, 128, 16, seed=11)
     c.table[1] = c.table[0]

@@ -90,6 +90,7 @@ def test_attention_refuses_tensors_of_other_shapes(skv):
     go = lambda **kw: skv.paged_attention(**{**dict(q=q, out=out, stream=0), **c, **kw})  # noqa: E731
     for bad in (dict(q=q[:1]), dict(q=q.float()), dict(out=out[:, :2]), dict(out=out.float()), dict(q=q[..., :64]),
                 dict(lens=c["lens"].long()), dict(table=c["table"].long()), dict(table=c["table"][:1]),
+                dict(table=c["table"][:1].expand(2, -1)), dict(table=c["table"].t().contiguous().t()),
                 dict(lse=torch.zeros(2, 4, dtype=torch.float64)), dict(lse=torch.zeros(2, 2)),
                 dict(weight=torch.zeros(2, 2, 63)), dict(weight=torch.zeros(2, 2, 64, dtype=torch.float64)),
                 dict(weight_out=torch.zeros(2, 2, 64)),
