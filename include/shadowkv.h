@@ -529,8 +529,9 @@ int shadowkv_qk_norm_rope(const skv_qk_norm_rope_args* args, skv_stream stream);
  *   weight_out[b][h][j] = weight[b][h][j] + sum over the G heads of p_j
  * for j < lens[b]; rows behind are left as they are.  weight_out may be weight.
  *
- * Accumulation, softmax statistics and sums are fp32.  bf16 and e5m2 values
- * are multiplied by probabilities rounded to bf16 and fp16.
+ * Accumulation, softmax statistics and sums are fp32.  bf16 values are
+ * multiplied by probabilities in two bf16 terms (16 bits), e5m2 ones by
+ * probabilities in fp16.
  */
 typedef struct {
     skv_paged_cache cache;

@@ -7,7 +7,7 @@ Tolerances, derived from the arithmetic (u = finfo.eps / 2 of the output type):
   it passes through) in all, and one rounding: u |y|.
 * attention: a score is an fp32 sum of d products, off by at most delta = d 2^-24 scale sum|q_i k_i|
   (any order); every probability then by 2 delta relatively (itself and the sum), and by u_p where it is
-  rounded for the product with the values (bf16 2^-8, fp16 2^-11, fp32 0).  exp2 and the fp32 sums
+  rounded for the product with the values (two bf16 terms 2^-16, fp16 2^-11, fp32 0).  exp2 and the fp32 sums
   add less than 2^-16.  So |out - ref| <= (2 delta + u_p + 2^-16) sum p|v| + u |ref|; an fp16
   probability below the smallest normal one is off by 2^-25 against a top of 2^7 at least: 2^-32 sum|v|.
 * lse: delta + 2^-16 + 2^-22 |lse|.   weights: G heads of p (2 delta + 2^-16), one fp32 sum.
@@ -26,7 +26,7 @@ from tests.paged_harness import KINDS, Paged, f64
 pytestmark = pytest.mark.gpu
 
 U = {"bf16": 2.0 ** -8, "fp8": 2.0 ** -8, "f32": 2.0 ** -24}
-UP = {"bf16": 2.0 ** -8, "fp8": 2.0 ** -11, "f32": 0.0}
+UP = {"bf16": 2.0 ** -16, "fp8": 2.0 ** -11, "f32": 0.0}
 
 
 def check_attention(kind, q, got, lse, krows, vrows, scale, weight=None, weight_out=None):
