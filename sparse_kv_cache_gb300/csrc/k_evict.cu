@@ -17,6 +17,10 @@
 // that.  Where only a few rows of a unit can move (decode steps), its cluster moves them itself; else
 // k_evict_move, a programmatic dependent, does with all of the device (154K rows of 64 long units:
 // 63 us in all against 68).
+//
+// Measured back to back, 8 KV heads, d = 128, bf16: 8 ragged sequences of up to 128K rows down to 2464,
+// 154K rows moved, 64 us -- 38 for the search, bound by the latency of its phases, 27 for the moves,
+// 5.9 TB/s; 64 units of 2081 rows down to 2080 12 us, all of it latency.
 #include "skv_common.cuh"
 #include "skv_internal.h"
 #include "skv_paged.h"
