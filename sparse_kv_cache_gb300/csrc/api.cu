@@ -48,7 +48,7 @@ using namespace skv;
 
 namespace {
 
-constexpr int kVersion = 1 * 10000 + 0 * 100 + 0;
+constexpr int kVersion = 1 * 10000 + 1 * 100 + 0;
 
 // ------------------------------------------------------------------ fault injection
 // SHADOWKV_FAULT=oom[:N] makes the N-th device allocation of a pre-filling
