@@ -10,6 +10,7 @@ import ctypes
 import functools
 import os
 import struct
+import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libshadowkv.so")
@@ -303,27 +304,51 @@ def _raw_stream(device, stream) -> int:
 
 
 _KEPT_BYTES = 8 << 20
-_kept_spaces: dict = {}      # (device, stream) -> workspace of that stream's calls
 
 
-def _space(nbytes: int, device, stream, raw: int):
-    """Workspace of one call.  Calls on torch's current stream run one after the other and share one
-    per stream; a captured call, one on a stream that was handed in, and one that needs much have
-    their own from torch's allocator, on the call's stream -- so neither streams nor graphs that
-    run side by side ever share one."""
+class _Space:
+    """A workspace, at the address `at`.  Its lock is held while a call is put into the stream, or the
+    kernels of two host threads' calls could come there alternately, with one workspace for both."""
+    __slots__ = ("lock", "mem", "at", "size")
+
+    def __init__(self):
+        self.lock, self.mem, self.at, self.size = threading.RLock(), None, 0, 0
+
+    def grow(self, nbytes: int, device):
+        import torch
+        self.mem = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.at, self.size = self.mem.data_ptr(), nbytes
+
+
+_kept_spaces: dict = {}      # (device, stream) -> _Space of that stream's calls
+
+
+def _space(nbytes: int, device, stream, raw: int) -> _Space:
+    """Workspace of one call, its lock taken: the caller releases it.  Calls on torch's current stream
+    run one after the other and share one per stream; a captured call, one on a stream that was
+    handed in, and one that needs much have their own from torch's allocator, on the call's stream --
+    so neither streams nor graphs that run side by side ever share one."""
     import torch
-    if device.type != "cuda":
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is None:
-        if nbytes > _KEPT_BYTES or torch.cuda.is_current_stream_capturing():
-            return torch.empty(nbytes, dtype=torch.uint8, device=device)
-        t = _kept_spaces.get((device.index, raw))
-        if t is None or t.numel() < nbytes:
-            t = _kept_spaces[device.index, raw] = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        return t
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw, device)
-    with torch.cuda.stream(s):
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is None and device.type == "cuda" and nbytes <= _KEPT_BYTES and not torch.cuda.is_current_stream_capturing():
+        space = _kept_spaces.get((device.index, raw))
+        if space is None:
+            space = _kept_spaces.setdefault((device.index, raw), _Space())
+        space.lock.acquire()
+        try:
+            if space.size < nbytes:
+                space.grow(nbytes, device)
+        except BaseException:
+            space.lock.release()
+            raise
+        return space
+    space = _Space()
+    if stream is None or device.type != "cuda":
+        space.grow(nbytes, device)
+    else:
+        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(raw, device)):
+            space.grow(nbytes, device)
+    space.lock.acquire()
+    return space
 
 
 @functools.lru_cache(maxsize=1024)
@@ -432,10 +457,13 @@ def paged_attention(q, k_cache, v_cache, table, lens, out, lse=None, weight=None
     device = q.device
     raw = _raw_stream(device, stream)
     space = _space(nbytes, device, stream, raw)
-    packed = _PAGED_ATTN.pack(
-        *cache, k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), *fixed, q.data_ptr(),
-        out.data_ptr(), _ptr(lse) or 0, _ptr(weight) or 0, _ptr(weight_out) or 0, pitch, space.data_ptr(), nbytes)
-    _check(load().shadowkv_paged_attention(packed, raw), "shadowkv_paged_attention")
+    try:
+        packed = _PAGED_ATTN.pack(
+            *cache, k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), *fixed, q.data_ptr(),
+            out.data_ptr(), _ptr(lse) or 0, _ptr(weight) or 0, _ptr(weight_out) or 0, pitch, space.at, nbytes)
+        _check(load().shadowkv_paged_attention(packed, raw), "shadowkv_paged_attention")
+    finally:
+        space.lock.release()
     return out
 
 
@@ -473,11 +501,13 @@ def paged_evict(k_cache, v_cache, table, lens, weight, position, budget: int, re
     device = weight.device
     raw = _raw_stream(device, stream)
     space = _space(nbytes, device, stream, raw)
-    packed = _EVICT.pack(
-        *cache, k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), *fixed, weight.data_ptr(),
-        position.data_ptr(), weight_out.data_ptr(), position_out.data_ptr(), pitch, lens_out.data_ptr(), space.data_ptr(),
-        nbytes)
-    _check(load().shadowkv_paged_evict(packed, raw), "shadowkv_paged_evict")
+    try:
+        packed = _EVICT.pack(
+            *cache, k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), *fixed, weight.data_ptr(),
+            position.data_ptr(), weight_out.data_ptr(), position_out.data_ptr(), pitch, lens_out.data_ptr(), space.at, nbytes)
+        _check(load().shadowkv_paged_evict(packed, raw), "shadowkv_paged_evict")
+    finally:
+        space.lock.release()
     return lens_out
 
 

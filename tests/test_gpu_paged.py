@@ -373,6 +373,35 @@ def test_calls_of_two_host_threads():
         assert len(got[i]) == 50 and all(torch.equal(o, want[i]) for o in got[i])
 
 
+def test_calls_of_two_host_threads_on_one_stream():
+    """Each call is several kernels around one workspace; the threads' kernels must not alternate."""
+    import threading
+    c = Paged("bf16", [30000, 9000], 2, 128, 16, seed=27)
+    qs = [queries(c, 4, 28 + i) for i in range(3)]
+    ws = [torch.zeros((2, 2, c.rows), device="cuda") for _ in qs]
+    want = [(skv.paged_attention(x, c.k, c.v, c.table, c.lens, torch.empty_like(x), weight=w).clone(), w.clone())
+            for x, w in zip(qs, ws)]
+    got, failed = [[] for _ in qs], []
+
+    def work(i):
+        try:
+            for _ in range(40):
+                w = torch.zeros_like(ws[i])
+                got[i].append((skv.paged_attention(qs[i], c.k, c.v, c.table, c.lens, torch.empty_like(qs[i]), weight=w), w))
+        except Exception as e:  # noqa: BLE001 (reported by the test)
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(qs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for mine, (out, w) in zip(got, want):
+        assert len(mine) == 40 and all(torch.equal(o, out) and torch.equal(x, w) for o, x in mine)
+
+
 def test_first_calls_of_a_process_inside_a_capture():
     """Every call captured before any was made: nothing needs a set-up outside the capture."""
     code = """
