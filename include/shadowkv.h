@@ -441,7 +441,7 @@ int shadowkv_fetch_probe(const void* src, size_t bytes, int64_t n_chunks, int ch
  *   dtype      SKV_BF16, SKV_F32, or SKV_FP8 (bf16 keys, e5m2 values)
  *   head_dim   64 or 128;  page_size a power of two from 8 to 1024
  *   strides    multiples of 16 bytes; pools 16-byte aligned device memory of the
- *              current device
+ *              current device; rows of pools and outputs that are written do not overlap
  * A negative length counts as 0 and one above max_pages * page_size as that;
  * a page id outside [0, n_pages) is not followed (its rows count as absent).
  * Both set an error word of the device, which shadowkv_paged_status reads.
@@ -449,7 +449,8 @@ int shadowkv_fetch_probe(const void* src, size_t bytes, int64_t n_chunks, int ch
  * Calls enqueue their work on `stream`, allocate nothing, keep nothing for the
  * next call, and give the same bits for the same inputs.  They can be captured
  * into graphs.  Calls that overlap on the GPU need workspaces of their own (so
- * do two graphs that may replay at once); calls that only read a cache may
+ * do two graphs that may replay at once, and the calls of host threads that
+ * enqueue on one stream side by side); calls that only read a cache may
  * overlap on it.
  */
 typedef struct {
@@ -485,8 +486,9 @@ typedef struct {
  * the caller's to advance.  No two tokens of a call may name the same row, nor
  * two sequences share the page of a row that is written.
  *
- * A token with a negative position is padding: nothing of it is written.  One with a negative seq is not appended.  An index or seq beyond
- * the cache, or a bad page, sets the error word and skips the append.
+ * A token with a negative position is padding: nothing of it is written.  One
+ * with a negative seq is not appended.  An index or seq beyond the cache, or a
+ * bad page, sets the error word and skips the append.
  * q_out may be q and k_out may be k (same strides); other overlaps are not
  * allowed.  tokens == 0 does nothing.
  */

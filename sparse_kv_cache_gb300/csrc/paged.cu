@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
 
@@ -24,6 +25,8 @@ struct Range {
 
 // rows of a sequence above this are refused: row arithmetic in the kernels is 32-bit
 constexpr int64_t kMaxRows = int64_t(1) << 30;
+// units (KV heads of sequences): with it, sizes in bytes stay below 2^60
+constexpr int64_t kMaxUnits = int64_t(1) << 24;
 // SMs that the attention's records have room for (a GB300 has 152)
 constexpr int kMaxSms = 160;
 
@@ -49,8 +52,24 @@ bool good_type(const skv_paged_cache& c) {
 
 // a stride of whole 16-byte words
 bool good_stride(int64_t s, int bytes) { return s >= 0 && s * bytes % 16 == 0; }
-// rows of a written pool must not overlap: each dimension that is stepped through moves by a row at least
-bool spread(int64_t s, int64_t n, int d) { return n <= 1 || s >= d; }
+// Rows of d elements that are written must not overlap: every dimension that is stepped through (n steps
+// of s) moves past all that the shorter steps reach.
+struct Dim { int64_t n, s; };
+template <int N>
+bool apart(Dim (&x)[N], int64_t d) {
+    std::sort(x, x + N, [](const Dim& a, const Dim& b) { return a.s < b.s; });
+    int64_t reach = d;       // elements from the first row's first to the last one's last
+    for (const Dim& e : x) {
+        if (e.n <= 1) continue;
+        if (e.s < reach || e.s > (INT64_MAX - reach) / e.n) return false;
+        reach += (e.n - 1) * e.s;
+    }
+    return true;
+}
+bool apart(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t d) {
+    Dim x[] = {{n0, s0}, {n1, s1}};
+    return apart(x, d);
+}
 
 // what the host can tell without the device
 int check_cache(const skv_paged_cache& c, bool written) {
@@ -58,17 +77,16 @@ int check_cache(const skv_paged_cache& c, bool written) {
     if (c.page_size < 8 || c.page_size > 1024 || (c.page_size & (c.page_size - 1))) return SKV_ERR_INVALID;
     if (c.max_pages < 1 || c.n_pages < 1 || c.n_pages > INT32_MAX || c.table_seq < c.max_pages) return SKV_ERR_INVALID;
     if (static_cast<int64_t>(c.max_pages) * c.page_size > kMaxRows) return SKV_ERR_INVALID;
-    if (static_cast<int64_t>(c.batch) * c.n_kv_heads > (1 << 24)) return SKV_ERR_INVALID;
+    if (static_cast<int64_t>(c.batch) * c.n_kv_heads > kMaxUnits) return SKV_ERR_INVALID;
     const int es = key_bytes(c.dtype), ev = value_bytes(c.dtype);
     for (int64_t s : {c.k_page, c.k_head, c.k_row})
         if (!good_stride(s, es)) return SKV_ERR_INVALID;
     for (int64_t s : {c.v_page, c.v_head, c.v_row})
         if (!good_stride(s, ev)) return SKV_ERR_INVALID;
     if (written) {
-        const int64_t n[3] = {c.n_pages, c.n_kv_heads, c.page_size};
-        const int64_t k[3] = {c.k_page, c.k_head, c.k_row}, v[3] = {c.v_page, c.v_head, c.v_row};
-        for (int i = 0; i < 3; ++i)
-            if (!spread(k[i], n[i], c.head_dim) || !spread(v[i], n[i], c.head_dim)) return SKV_ERR_INVALID;
+        Dim k[] = {{c.n_pages, c.k_page}, {c.n_kv_heads, c.k_head}, {c.page_size, c.k_row}};
+        Dim v[] = {{c.n_pages, c.v_page}, {c.n_kv_heads, c.v_head}, {c.page_size, c.v_row}};
+        if (!apart(k, c.head_dim) || !apart(v, c.head_dim)) return SKV_ERR_INVALID;
     }
     if (!c.k || !c.v || !c.table || !aligned16(c.k) || !aligned16(c.v)) return SKV_ERR_INVALID;
     return SKV_OK;
@@ -128,6 +146,7 @@ int attn_space(const skv_paged_attention_args* a, AttnSpace* w) {
     if (c.max_pages < 1 || c.page_size < 1 || static_cast<int64_t>(c.max_pages) * c.page_size > kMaxRows)
         return SKV_ERR_INVALID;
     const int64_t U = static_cast<int64_t>(c.batch) * c.n_kv_heads, cap = static_cast<int64_t>(c.max_pages) * c.page_size;
+    if (U > kMaxUnits) return SKV_ERR_INVALID;
     w->Gp = (G + 1) & ~1;
     const int64_t ctas = paged_attn_ctas(c.dtype, kMaxSms);
     w->joint = 0;
@@ -155,6 +174,7 @@ int evict_space(const skv_paged_evict_args* a, EvictSpace* w) {
     if (c.max_pages < 1 || c.page_size < 1 || static_cast<int64_t>(c.max_pages) * c.page_size > kMaxRows)
         return SKV_ERR_INVALID;
     const int64_t U = static_cast<int64_t>(c.batch) * c.n_kv_heads, cap = static_cast<int64_t>(c.max_pages) * c.page_size;
+    if (U > kMaxUnits) return SKV_ERR_INVALID;
     // rows that can move: no more than the budget, no more than lie behind it
     const int64_t behind = cap > a->budget ? cap - a->budget : 0;
     w->list_cap = static_cast<int>(behind < a->budget ? behind : a->budget);
@@ -203,8 +223,7 @@ int shadowkv_qk_norm_rope(const skv_qk_norm_rope_args* a, skv_stream stream) {
     for (const auto& x : t) {
         if (!x.need) continue;
         if (!x.p || !aligned16(x.p) || !good_stride(x.tok, es) || !good_stride(x.head, es)) return SKV_ERR_INVALID;
-        if (x.written && (!spread(x.tok, a->tokens, c.head_dim) || !spread(x.head, x.heads, c.head_dim)))
-            return SKV_ERR_INVALID;
+        if (x.written && !apart(a->tokens, x.tok, x.heads, x.head, c.head_dim)) return SKV_ERR_INVALID;
     }
     Device dev;
     if (int rc = device(&dev)) return rc;
@@ -250,7 +269,7 @@ int shadowkv_paged_attention(const skv_paged_attention_args* a, skv_stream strea
     if (!c.lens || !a->q || !a->out || !a->workspace || !aligned16(a->q) || !aligned16(a->workspace)) return SKV_ERR_INVALID;
     if (!good_stride(a->q_seq, es) || !good_stride(a->q_head, es)) return SKV_ERR_INVALID;
     if (!aligned16(a->out) || !good_stride(a->out_seq, es) || !good_stride(a->out_head, es)) return SKV_ERR_INVALID;
-    if (!spread(a->out_seq, c.batch, c.head_dim) || !spread(a->out_head, a->n_q_heads, c.head_dim)) return SKV_ERR_INVALID;
+    if (!apart(c.batch, a->out_seq, a->n_q_heads, a->out_head, c.head_dim)) return SKV_ERR_INVALID;
     if (a->workspace_bytes < w.bytes) return SKV_ERR_INVALID;
     if ((a->weight != nullptr) != (a->weight_out != nullptr)) return SKV_ERR_INVALID;
     if (a->weight && a->row_pitch < static_cast<int64_t>(c.max_pages) * c.page_size) return SKV_ERR_INVALID;

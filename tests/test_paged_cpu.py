@@ -155,6 +155,77 @@ def test_c_entries_refuse_null_and_host_only_mistakes(skv):
         assert lib.shadowkv_paged_evict(packed, None) == -1
 
 
+@pytest.mark.parametrize("size,stride,good", [
+    ((8, 2, 16), (4096, 2048, 128), True), ((8, 2, 16), (4096, 128, 256), True), ((8, 2, 16), (2048, 16384, 128), True),
+    ((8, 2, 16), (8192, 2048, 128), True),       # with room between pages
+    ((8, 1, 16), (2048, 0, 128), True),          # one head: its stride is not stepped through
+    ((8, 2, 16), (2048, 2048, 128), False),      # a page's second head is the next page's first
+    ((8, 2, 16), (4096, 1920, 128), False),      # heads share a row
+    ((8, 2, 16), (4096, 128, 128), False), ((8, 2, 16), (4088, 2048, 128), False), ((8, 2, 16), (4096, 2048, 120), False),
+    ((8, 2, 16), (1 << 60, 2048, 128), False)])  # beyond what 64 bits hold
+def test_written_pools_whose_rows_overlap_are_refused(skv, size, stride, good):
+    from sparse_kv_cache_gb300 import _binding as b
+    (pages, heads, ps), host = size, torch.zeros(64)
+    at = host.data_ptr() + 15 & ~15
+    dev = skv.load().shadowkv_paged_status(None) == 0
+    for k, v in ((stride, (4096, 2048, 128)), ((4096, 2048, 128), stride)):
+        packed = b._EVICT.pack(1, heads, 128, ps, 1, 4, pages, *k, *v, 4, at, at, at, at, 8, 0, 0, at, at, at, at, 64, at, at,
+                               1 << 40)
+        # good ones get as far as the look at the device (or at the memory, which is the host's)
+        assert skv.load().shadowkv_paged_evict(packed, None) == (-1 if dev or not good else -4)
+
+
+def test_outputs_whose_rows_overlap_are_refused(skv):
+    x = torch.zeros(1 << 12, dtype=torch.bfloat16)
+    k, pos = torch.zeros((3, 2, 128), dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int32)
+    for strides in ((256, 128, 1), (128, 256, 1), (128, 128, 1)):     # four heads of three tokens
+        q_out = x.as_strided((3, 4, 128), strides)
+        refused(skv, lambda: skv.qk_norm_rope(torch.zeros((3, 4, 128), dtype=x.dtype), k, pos, q_out, k.clone(), stream=0))
+        c = cache(batch=3)
+        refused(skv, lambda: skv.paged_attention(torch.zeros((3, 4, 128), dtype=x.dtype), **c, out=q_out, stream=0))
+
+
+def test_workspaces_of_too_many_units_are_refused(skv):
+    from sparse_kv_cache_gb300 import _binding as b
+    c = (1, 1 << 16, 128, 1024, (1 << 31) - 1, 1 << 20, *(0,) * 12)
+    assert skv.load().shadowkv_paged_attention_workspace(b._PAGED_ATTN.pack(*c, 1 << 16, 0.0, *(0,) * 8, 64, 0, 0, 0)) == -1
+    assert skv.load().shadowkv_paged_evict_workspace(b._EVICT.pack(*c, 8, *(0,) * 10)) == -1
+    c = (1, 1 << 16, 128, 1024, 1 << 8, 1 << 20, *(0,) * 12)          # the most that there may be
+    assert skv.load().shadowkv_paged_attention_workspace(
+        b._PAGED_ATTN.pack(*c, 1 << 19, 0.0, *(0,) * 8, 64, 0, 0, 0)) > 1 << 59
+    assert skv.load().shadowkv_paged_evict_workspace(b._EVICT.pack(*c, 1 << 29, *(0,) * 10)) > 1 << 56
+
+
+def test_host_threads_do_not_share_a_workspace_in_the_middle_of_a_call(skv, monkeypatch):
+    """Threads that call on one stream: while one is enqueueing, the workspace is its own."""
+    import threading
+    import time
+    from sparse_kv_cache_gb300 import _binding as b
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    real = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: real(*a, **kw))
+    monkeypatch.setattr(b, "_kept_spaces", {})
+    busy, clashes, done = set(), [], []
+
+    def work(raw):
+        for n in (100, 5000, 200):
+            space = b._space(n, torch.device("cuda", 0), None, raw)
+            if space.at in busy or space.size < n:
+                clashes.append((raw, n))
+            busy.add(space.at)
+            time.sleep(0.002)
+            busy.discard(space.at)
+            done.append(raw)
+            space.lock.release()
+
+    threads = [threading.Thread(target=work, args=(raw,)) for raw in (0, 0, 0, 7)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not clashes and len(done) == 12
+
+
 def test_empty_calls_do_nothing(skv):
     q = torch.zeros((0, 4, 128), dtype=torch.bfloat16)
     k = torch.zeros((0, 2, 128), dtype=torch.bfloat16)
