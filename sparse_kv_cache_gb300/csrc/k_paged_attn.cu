@@ -27,8 +27,8 @@
 // Measured back to back (8 KV heads of 4 query heads, d = 128, each row's bytes once over the time;
 // a copy runs at 6.7 TB/s): 8 x 128K rows in bf16 605 us, 7.1 TB/s; 4 x 32K rows 88 us, 6.1 TB/s; 8
 // ragged sequences of up to 64K rows with e5m2 values 138 us, 6.3 TB/s; 192 of 0 to 611 rows (4 KV
-// heads of 8) 32 us, 3.8 TB/s, of which the search for a CTA's place, the joins and the launches
-// take some 13; one sequence of 1013 rows 6.4 us, all of it latency.
+// heads of 8) 30.6 us, 4.0 TB/s, a CTA per unit whose start and end are latency; 4096 of 0 to 30 rows (2
+// of 4) 30.5 us against 11.6 of their bytes; one sequence of 1013 rows 6.4 us, all of it latency.
 #include <math_constants.h>
 
 #include "skv_common.cuh"
@@ -125,14 +125,33 @@ struct Plan {
     __device__ __forceinline__ int64_t part(int w) const { return lo + w * (hi - lo) / W; }
 };
 
-// Every thread sums a run of sequences; the thread whose run holds a part's first tile finds it.
+// Each warp takes a quarter of the sequences, 32 at a time, and its lane j keeps the sum of the j-th run of
+// them; the warp whose runs hold a part's first tile looks through that run.  A part whose sequence is not
+// found (the lengths changed under the call) has no rows.
 template <int W, int R, int kLeast>
 __device__ __forceinline__ Plan<W> make_plan(const PagedView& c, int64_t me, int64_t ctas, PlanSmem<W>& sm) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (c.batch + kPaThreads - 1) / kPaThreads;
-    const int s0 = min(tid * per, c.batch), s1 = min(s0 + per, c.batch);
+    const int steps = (c.batch + 32 * kPaWarps - 1) / (32 * kPaWarps), run_steps = (steps + 31) / 32;
+    const int s0 = warp * steps * 32 + lane;
+    constexpr int kDeep = 4;       // steps whose loads are in flight together
     int64_t mine = 0;
-    for (int s = s0; s < s1; ++s) mine += tiles_of<R>(rows_of(c, s, g_err, 711));
+    int first = 0;
+    for (int j0 = 0; j0 < steps; j0 += kDeep) {
+        int n[kDeep];
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            const int s = s0 + 32 * (j0 + k);
+            n[k] = j0 + k < steps && s < c.batch ? __ldcg(c.lens + s) : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kDeep; ++k) {
+            n[k] = rows_in(c, n[k], g_err, 711);
+            const uint32_t sum = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(tiles_of<R>(n[k])));
+            if (lane == (j0 + k) / run_steps) mine += sum;
+        }
+        if (j0 == 0) first = n[0];
+    }
+    if (tid < W) sm.rows[tid] = 0;
     int64_t run = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -153,21 +172,37 @@ __device__ __forceinline__ Plan<W> make_plan(const PagedView& c, int64_t me, int
     pl.lo = me < pl.n ? pl.start(me) : 0;
     pl.hi = me < pl.n ? pl.start(me + 1) : 0;
     const int64_t begin = (before + run - mine) * c.H, stop = begin + mine * c.H;
+    int held = 0, rows = first;                // the warp's step whose lengths the lanes have
 #pragma unroll
     for (int w = 0; w < W; ++w) {
         const int64_t x = pl.part(w);
-        if (pl.lo == pl.hi || x < begin || x >= stop) continue;
-        int64_t at = begin;
-        for (int s = s0; s < s1; ++s) {
-            const int rows = rows_of(c, s, g_err, 711);
-            const int64_t size = static_cast<int64_t>(tiles_of<R>(rows)) * c.H;
-            if (x < at + size) {
-                sm.at[w] = at;
-                sm.b[w] = s;
-                sm.rows[w] = rows;
+        const uint32_t who = __ballot_sync(0xffffffffu, pl.lo < pl.hi && x >= begin && x < stop);
+        if (!who) continue;
+        const int owner = __ffs(who) - 1;
+        int64_t at = __shfl_sync(0xffffffffu, begin, owner);
+        for (int j = owner * run_steps; j < steps; ++j) {
+            const int s = s0 + 32 * j;
+            if (j != held) {
+                rows = s < c.batch ? rows_of(c, s, g_err, 711) : 0;
+                held = j;
+            }
+            const uint32_t size = tiles_of<R>(rows);
+            uint32_t upto = size;              // (32 sequences have 2^31 tiles at most)
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            const int64_t end = at + static_cast<int64_t>(upto) * c.H, from = end - static_cast<int64_t>(size) * c.H;
+            if (__any_sync(0xffffffffu, x < end)) {
+                if (x >= from && x < end) {
+                    sm.at[w] = from;
+                    sm.b[w] = s;
+                    sm.rows[w] = rows;
+                }
                 break;
             }
-            at += size;
+            at = __shfl_sync(0xffffffffu, end, 31);
         }
     }
     __syncthreads();
@@ -828,7 +863,7 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
     const int64_t w0 = pl.part(warp), w1 = pl.part(warp + 1);
     if (lane == 0) js.of[2 * warp].b = js.of[2 * warp + 1].b = -1;
     __syncwarp();
-    if (w0 < w1) {
+    if (w0 < w1 && s_plan.rows[warp] > 0) {
         Pieces pieces;
         const Piece head = pieces.first(p.c, s_plan.b[warp], s_plan.rows[warp], s_plan.at[warp], w0, w1 - w0);
         Tile tile;
@@ -849,7 +884,7 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
     // a unit that ends in this CTA and began before it
     if (tid == 0) {
         Joint joint{-1, 0, 0, 0};
-        if (pl.lo < pl.hi) {
+        if (pl.lo < pl.hi && s_plan.rows[0] > 0) {
             Walk<kPaTile> at;
             at.enter(s_plan.b[0], s_plan.rows[0], s_plan.at[0], pl.lo);
             if (at.unit0 < pl.lo && at.unit0 + at.nt <= pl.hi) {
@@ -870,15 +905,19 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
         }
 }
 
-// Short sequences of few units, where the latency of a step counts (one sequence of 1013 rows: 6.4 us
-// against 9.6 in the general form, four of 4096 rows 16.5 against 20.4): a cluster of CTAs per unit, whose
-// warps share its rows evenly.  No search for the place, no records and no second kernel: each CTA
-// joins its warps' shares, and the cluster joins the CTAs' through distributed shared memory.  The
+// Short sequences, where the latency of a step counts (one sequence of 1013 rows: 6.4 us against 9.6 in the
+// general form, four of 4096 rows 16.5 against 20.4): a cluster of CTAs per unit, or one CTA where units are
+// many, whose warps share its rows evenly.  No search for the place, no records and no second kernel:
+// each CTA joins its warps' shares, and the cluster joins the CTAs' through distributed shared memory.  The
 // products for the weights stay in shared memory until the sums are known.
-constexpr int kClusterTiles = 8;      // tiles of a warp at most
+// Tiles of a warp of a unit's longest possible sequence:
+__host__ __device__ __forceinline__ int cluster_tiles(int cap, int ranks) {
+    const int parts = ranks * kPaWarps;
+    return ((cap + kPaTile - 1) / kPaTile + parts - 1) / parts;
+}
 template <class Tile, int D, bool kF32, int G, int kOcc, bool kKeep>
 __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid_constant__ PagedAttnParams p, int ranks) {
-    extern __shared__ __align__(16) float s_z[];        // [warps][kClusterTiles * kPaTile][Gp]
+    extern __shared__ __align__(16) float s_z[];        // [warps][rows of a warp at most][Gp]
     __shared__ __align__(16) JoinSmem<D, G> js;
     begin_call();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -888,7 +927,7 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid
     const int nt = tiles_of(rows), parts = ranks * kPaWarps, part = rank * kPaWarps + warp;
     const int t0 = static_cast<int>(static_cast<int64_t>(nt) * part / parts);
     const int t1 = static_cast<int>(static_cast<int64_t>(nt) * (part + 1) / parts);
-    float* my_z = s_z + warp * kClusterTiles * kPaTile * (kKeep ? p.Gp : 0);
+    float* my_z = s_z + warp * cluster_tiles(p.c.cap, ranks) * kPaTile * (kKeep ? p.Gp : 0);
     Tile tile;
     auto hand_over = [&](const Piece&, bool) { tile.finish(p, b, h, false, js, 2 * warp); };
     const int piece_row = t0 * kPaTile, piece_end = t0 < t1 ? min(rows, t1 * kPaTile) : piece_row;
@@ -1183,7 +1222,7 @@ __global__ void __launch_bounds__(kPaThreads, kWeighOcc) k_paged_weigh(const __g
     // the lengths were there before the call began; the rest comes from the grids before
     const Plan<1> pl = make_plan<1, kWeighRows, 1>(p.c, blockIdx.x, gridDim.x, s_plan);
     pdl_wait();
-    if (pl.lo == pl.hi) return;
+    if (pl.lo == pl.hi || s_plan.rows[0] == 0) return;
     int64_t cur = pl.lo;
     Walk<kWeighRows> at;
     at.enter(s_plan.b[0], s_plan.rows[0], s_plan.at[0], cur);
@@ -1202,18 +1241,26 @@ int paged_attn_ctas(int dtype, int nsm) { return nsm * (dtype == SKV_F32 ? kOccF
 
 // CTAs of a unit's cluster, or 0: the general form.  The cluster form serves a step whose units leave
 // SMs idle and whose longest possible sequence takes a warp no more than kClusterTiles tiles (with twice
-// as many, 8 units of 16K rows took 25.0 us against the general form's 21.0).
-static int cluster_ranks(const PagedAttnParams& p, int ncta) {
+// as many, 8 units of 16K rows took 25.0 us against the general form's 21.0, 64 ragged ones of 4000 rows
+// 25.0 against 21.1), and one whose units, a CTA each, are up to three times as many as the CTAs that the
+// device holds (fp32: twice), with at most kUnitTiles tiles for a warp.  (Ragged bf16 units of up to 250
+// rows: 460 of them 9.6 us against 18.0, 1368 23.6 against 25.6, 2000 32.1 against 31.6.  Of up to 611 rows:
+// 300 16.8 against 18.5, 768 28.6 against 29.6; of 1000 300 24.7 against 22.6.  Units of one length lose
+// where a few are left over: 460 of 750 rows 41.6 against 36.5, 912 57.4 against 59.8.  fp32, 600 ragged
+// ones of 250 rows 27.0 against 33.5; 912 of exactly 250 54.4 against 44.7.)
+constexpr int kClusterTiles = 8, kUnitTiles = 12;
+static int cluster_ranks(const PagedAttnParams& p, int ncta, bool f32) {
     const int64_t U = static_cast<int64_t>(p.c.batch) * p.c.H, tiles = (p.c.cap + kPaTile - 1) / kPaTile;
     int ranks = 1;
     while (ranks < 16 && tiles > ranks * kPaWarps && 2 * U * ranks <= ncta) ranks *= 2;
-    return U * ranks <= ncta && tiles <= static_cast<int64_t>(ranks) * kPaWarps * kClusterTiles ? ranks : 0;
+    if (ranks == 1) return U <= (f32 ? 2 : 3) * static_cast<int64_t>(ncta) && cluster_tiles(p.c.cap, 1) <= kUnitTiles ? 1 : 0;
+    return cluster_tiles(p.c.cap, ranks) <= kClusterTiles ? ranks : 0;
 }
 
 template <class Tile, int D, bool kF32, int G, int kOcc>
 static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
     auto kernel = p.weight_out ? k_paged_cluster<Tile, D, kF32, G, kOcc, true> : k_paged_cluster<Tile, D, kF32, G, kOcc, false>;
-    const int smem = p.weight_out ? kPaWarps * kClusterTiles * kPaTile * p.Gp * 4 : 0;
+    const int smem = p.weight_out ? kPaWarps * cluster_tiles(p.c.cap, ranks) * kPaTile * p.Gp * 4 : 0;
     if (ranks > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return -1;
     if (smem && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
     return launch_first(kernel, static_cast<unsigned>(p.c.batch) * p.c.H * ranks, kPaThreads, smem, ranks, s, p, ranks) ==
@@ -1224,7 +1271,7 @@ static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
 
 template <class Tile, int D, bool kF32, int G, int kOcc>
 static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
-    if (const int ranks = cluster_ranks(p, ncta)) return launch_cluster<Tile, D, kF32, G, kOcc>(p, ranks, s);
+    if (const int ranks = cluster_ranks(p, ncta, kF32)) return launch_cluster<Tile, D, kF32, G, kOcc>(p, ranks, s);
     // no more CTAs than there can be tiles for their warps
     const int64_t tiles = static_cast<int64_t>(p.c.batch) * p.c.H * ((p.c.cap + kPaTile - 1) / kPaTile);
     constexpr int kMin = (kF32 ? 1 : kPaLeast) * kPaWarps;

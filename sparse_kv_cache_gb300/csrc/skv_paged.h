@@ -101,14 +101,16 @@ __device__ __forceinline__ void begin_call() {
     pdl_trigger();
 }
 
-// rows of sequence b, brought into [0, cap]
-__device__ __forceinline__ int rows_of(const PagedView& c, int b, int* err, int where) {
-    int n = __ldcg(c.lens + b);
+// a length brought into [0, cap], and that of sequence b
+__device__ __forceinline__ int rows_in(const PagedView& c, int n, int* err, int where) {
     if (n < 0 || n > c.cap) {
         set_err(err, DEV_ERR_BOUNDS, where);
         n = n < 0 ? 0 : c.cap;
     }
     return n;
+}
+__device__ __forceinline__ int rows_of(const PagedView& c, int b, int* err, int where) {
+    return rows_in(c, __ldcg(c.lens + b), err, where);
 }
 // page of row i of sequence b, or -1 (and the error word) if its id is out of range
 __device__ __forceinline__ int page_of(const PagedView& c, int b, int i, int* err, int where) {

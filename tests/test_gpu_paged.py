@@ -84,6 +84,10 @@ def queries(c, G, seed=1, scale=1.0):
     ("bf16", 5, 8, 128, 16, "hnd", [300] * 40 + [0] * 200),    # several units per CTA, idle sequences behind
     ("bf16", 4, 1, 64, 16, "hnd", [0] * 150 + [77] + [0] * 150 + [3000]),
     ("bf16", 1, 1, 64, 8, "hnd", [(i * 7919) % 41 for i in range(1000)]),      # eight sequences per thread of the search
+    ("bf16", 2, 1, 64, 16, "nhd", [(i * 31) % 23 for i in range(5000)]),       # runs of more than 32 sequences
+    ("fp8", 1, 2, 64, 16, "hnd", [0] * 4500 + [900] + [0] * 200 + [5] * 100 + [0] * 30),
+    ("bf16", 8, 4, 128, 16, "hnd", [(i * 97) % 700 for i in range(150)]),      # more units than CTAs are held at once
+    ("f32", 4, 2, 64, 8, "hnd", [(i * 97) % 200 for i in range(200)]),
     ("fp8", 4, 2, 128, 16, "hnd", [1, 0, 500, 64]),
     ("fp8", 8, 1, 64, 8, "nhd", [1300, 7]),
     ("fp8", 1, 4, 128, 256, "nhd", [20000]),
