@@ -19,7 +19,7 @@
 // 63 us in all against 68).
 //
 // Measured back to back, 8 KV heads, d = 128, bf16: 8 ragged sequences of up to 128K rows down to 2464,
-// 154K rows moved, 64 us -- 38 for the search, bound by the latency of its phases, 27 for the moves,
+// 154K rows moved, 62 us -- 36 for the search, bound by the latency of its phases, 27 for the moves,
 // 5.9 TB/s; 64 units of 2081 rows down to 2080 12 us, all of it latency.
 #include "skv_common.cuh"
 #include "skv_internal.h"
@@ -93,6 +93,19 @@ __device__ __noinline__ uint4 remade(const float* w, const int32_t* p, int s, Pr
     uint32_t t[8];
     keys_of(pr, r, t);
     return halves(t, sh);
+}
+// the first `count` of eight elements
+template <typename T4, typename T>
+__device__ __forceinline__ void copy_below(T* out, const T4& a, const T4& b, int count) {
+    if (count >= 8) {
+        reinterpret_cast<T4*>(out)[0] = a;
+        reinterpret_cast<T4*>(out)[1] = b;
+    } else if (count > 0) {
+        const T x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (e < count) out[e] = x[e];
+    }
 }
 // bits of the halves that f holds for
 template <typename F>
@@ -269,24 +282,27 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_evict(const __gri
     uint32_t prefix = 0, T = 0;
     int need = M, ties = 0;
     bool whole = false;        // every key from T + 1 on stays, no ties
-    {
-        Rows8 r, next;
-        if (lo + 8 * lane < hi) load_rows(w_in, p_in, lo + 8 * lane, r);
-        for (int r0 = lo; r0 < hi; r0 += kEvStep) {
-            const int s = r0 + 8 * lane;
-            if (s + kEvStep < hi) load_rows(w_in, p_in, s + kEvStep, next);       // the next step's, early
-            if (s < hi) {
-                const uint32_t in = bits_below(s, hi);
-                uint32_t t[8];
-                keys_of(pr, r, t);
-                if (held) *reinterpret_cast<uint4*>(my + (s - lo)) = halves(t, 16);
-                if (held_low) *reinterpret_cast<uint4*>(my_low + (s - lo)) = halves(t, 0);
+    Rows8 r;
+    if (lo + 8 * lane < hi) load_rows(w_in, p_in, lo + 8 * lane, r);
+    for (int r0 = lo; r0 < hi; r0 += kEvStep) {
+        const int s = r0 + 8 * lane;
+        Rows8 next;
+        if (s + kEvStep < hi) load_rows(w_in, p_in, s + kEvStep, next);       // the next step's, early
+        if (s < hi) {
+            const uint32_t in = bits_below(s, hi);
+            uint32_t t[8];
+            keys_of(pr, r, t);
+            if (held) *reinterpret_cast<uint4*>(my + (s - lo)) = halves(t, 16);
+            if (held_low) *reinterpret_cast<uint4*>(my_low + (s - lo)) = halves(t, 0);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if ((in >> e) & 1) atomicAdd(s_hist + (t[e] >> 21), 1);
-            }
-            r = next;
+            for (int e = 0; e < 8; ++e)
+                if ((in >> e) & 1) atomicAdd(s_hist + (t[e] >> 21), 1);
+            // the rows below the budget go to buffers of their own now; those given up are written over by
+            // the rows that move there
+            if (copy_w) copy_below<float4>(p.weight_out + base + s, r.w0, r.w1, M - s);
+            if (copy_p) copy_below<int4>(p.position_out + base + s, r.p0, r.p1, M - s);
         }
+        r = next;
     }
 #pragma unroll 1
     for (int pass = 0; pass < 4; ++pass) {
@@ -459,7 +475,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_evict(const __gri
                     if (t < ties) kept |= tie & (0 - tie);
             }
             uint32_t hole = in & low & ~kept, src = kept & ~low;
-            const uint32_t stay = kept & low;
             if (__any_sync(0xffffffffu, hole | src)) {
                 const int both = __popc(hole) | __popc(src) << 16;       // at most 256 of each
                 const int at = excl_scan(both, lane);
@@ -467,35 +482,13 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_evict(const __gri
                 int ha = hole_at + (at & 0xFFFF), sa = src_at + (at >> 16);
                 hole_at += all & 0xFFFF;
                 src_at += all >> 16;
-                for (; hole; hole &= hole - 1, ++ha)
-                    if (ha < p.list_cap) to[ha] = s + __ffs(hole) - 1;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int at_e = ha + __popc(hole & ((1u << e) - 1));
+                    if (((hole >> e) & 1) && at_e < p.list_cap) to[at_e] = s + e;
+                }
                 for (; src; src &= src - 1, ++sa)
                     if (sa < p.list_cap) of[sa] = s + __ffs(src) - 1;
-            }
-            if (stay && (copy_w || copy_p)) {
-                Rows8 r;
-                load_rows(w_in, p_in, s, r);
-                if (stay == 0xFFu) {
-                    if (copy_w) {
-                        float4* out = reinterpret_cast<float4*>(p.weight_out + base + s);
-                        out[0] = r.w0;
-                        out[1] = r.w1;
-                    }
-                    if (copy_p) {
-                        int4* out = reinterpret_cast<int4*>(p.position_out + base + s);
-                        out[0] = r.p0;
-                        out[1] = r.p1;
-                    }
-                } else {
-                    const float w[8] = {r.w0.x, r.w0.y, r.w0.z, r.w0.w, r.w1.x, r.w1.y, r.w1.z, r.w1.w};
-                    const int q[8] = {r.p0.x, r.p0.y, r.p0.z, r.p0.w, r.p1.x, r.p1.y, r.p1.z, r.p1.w};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        if (!((stay >> e) & 1)) continue;
-                        if (copy_w) p.weight_out[base + s + e] = w[e];
-                        if (copy_p) p.position_out[base + s + e] = q[e];
-                    }
-                }
             }
         }
         if (turn == 1) break;
