@@ -14,8 +14,8 @@
 // the top by themselves, so the reduction is exact for every int32 position; the 32 leading bits
 // of the remaining turn, as a fraction of pi, go to sincospi (error below 2^-23 of a half turn).
 //
-// Measured back to back: 32K tokens of 32 + 2 x 8 heads, d = 128, 141 us, 6.2 TB/s of a copy's 6.7;
-// 5105 tokens of 16 + 2 x 2 heads with e5m2 values 15.7 us (51 MB: latency of two waves of CTAs); a
+// Measured back to back: 32K tokens of 32 + 2 x 8 heads, d = 128, 140 us, 6.2 TB/s of a copy's 6.7;
+// 5105 tokens of 16 + 2 x 2 heads with e5m2 values 14.2 us (51 MB: latency of one wave of CTAs); a
 // decode step of 8 tokens 3.4 us.
 #include "skv_common.cuh"
 #include "skv_internal.h"
@@ -26,7 +26,6 @@ namespace skv {
 static __device__ int g_err[2];
 
 constexpr int kNrThreads = 128;
-constexpr int kNrOcc = 6;         // CTAs per SM
 constexpr int max_tokens(int d) { return 2048 / d; }     // of a CTA, for their angles' 8 KB of shared memory
 
 // 16 elements of a row as they lie in memory: 8 at o1, 8 at o2
@@ -66,8 +65,8 @@ __device__ __forceinline__ void put(float* p, int o1, int o2, const Raw<float>& 
     reinterpret_cast<float4*>(p + o2)[1] = r.z1;
 }
 
-template <typename T, int D, bool kE5M2>
-__global__ void __launch_bounds__(kNrThreads, kNrOcc) k_norm_rope(const __grid_constant__ NormRopeParams p) {
+template <typename T, int D, bool kE5M2, int kOcc>      // kOcc: CTAs per SM
+__global__ void __launch_bounds__(kNrThreads, kOcc) k_norm_rope(const __grid_constant__ NormRopeParams p) {
     constexpr int kLanes = D / 16;                  // lanes of a row
     constexpr int kDeep = sizeof(T) == 2 ? 3 : 2;   // rows of a thread whose loads are in flight at once
     __shared__ __align__(16) float s_cos[max_tokens(D) * D / 2], s_sin[max_tokens(D) * D / 2];
@@ -227,7 +226,13 @@ static int launch_nr(NormRopeParams p, int nsm, cudaStream_t s) {
         if (spent < had || (spent == had && slots_of(p.groups) < 10)) p.groups = g;
     }
     const int per = kRows / p.groups, grid = (p.tokens + per - 1) / per;
-    return launch_first(k_norm_rope<T, D, kE5M2>, grid, kNrThreads, 0, 1, s, p) == cudaSuccess ? 0 : -1;
+    // Five CTAs per SM have the registers to keep their rows' loads in flight, seven take fewer waves: a wave
+    // of seven takes 1.2 times as long as one of five (fp32: 1.45).  5105 tokens of 16 + 2 x 2 heads 14.2
+    // us with five, 19.7 with seven; 32K of 32 + 2 x 8 150 and 140, 4096 26.7 and 22.3, 3000 16.7 and 20.1.
+    const int w5 = (grid + 5 * nsm - 1) / (5 * nsm), w7 = (grid + 7 * nsm - 1) / (7 * nsm);
+    const bool seven = sizeof(T) == 2 ? 6 * w7 < 5 * w5 : 3 * w7 < 2 * w5;
+    auto kernel = seven ? k_norm_rope<T, D, kE5M2, 7> : k_norm_rope<T, D, kE5M2, 5>;
+    return launch_first(kernel, grid, kNrThreads, 0, 1, s, p) == cudaSuccess ? 0 : -1;
 }
 
 int launch_norm_rope(int dtype, int d, const NormRopeParams& p, int nsm, cudaStream_t s) {

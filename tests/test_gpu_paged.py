@@ -518,6 +518,35 @@ def test_norm_rope_append(kind, n, nq, nk, d, rd, ps, layout, norms):
     assert torch.equal(rows, want_p) and torch.equal(sums, want_s)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
+def test_norm_rope_of_a_prompt(kind, d):
+    """As many tokens as take the form with more CTAs per SM."""
+    n, nq, nk, ps = 1003, 2, 1, 16
+    c = Paged(kind, [0], nk, d, ps, seed=31, cap=n)
+    g = torch.Generator().manual_seed(32)
+    wide = KINDS[kind][0]
+    q, k, v = ((torch.randn((n, h, d), generator=g) * 2).to(wide).cuda() for h in (nq, nk, nk))
+    w = (1 + torch.rand(d, generator=g)).to(wide).cuda()
+    pos = torch.arange(70000, 70000 + n, dtype=torch.int32)
+    pos[500] = -1
+    index = torch.randperm(n, generator=g).to(torch.int32)
+    q_out, k_out = (torch.full_like(x, 77.0) for x in (q, k))
+    skv.qk_norm_rope(q, k, pos.cuda(), q_out, k_out, q_weight=w, k_weight=w, eps=1e-5, rope_base=10000.0, rotary_dim=d - 32,
+                     v=v, k_cache=c.k, v_cache=c.v, table=c.table, seq=torch.zeros(n, dtype=torch.int32, device="cuda"),
+                     index=index.cuda())
+    assert skv.paged_status() == 0
+    live = [t for t in range(n) if t != 500]
+    for x, out in ((q, q_out), (k, k_out)):
+        assert (out[500] == 77).all()
+        check_norm(x[live], w, pos[live], out[live], kind, 10000.0, d - 32, 1e-5)
+    at = index.long()[live].cuda()
+    page, off = c.table[0].long()[at // ps], at % ps
+    assert torch.equal(c.k[page, :, off], k_out[live])
+    raw = lambda x: x.contiguous().view(torch.uint8)  # noqa: E731
+    assert torch.equal(raw(c.v[page, :, off] if kind != "fp8" else c.v.view(torch.uint8)[page, :, off]), raw(v[live].to(c.v.dtype)))
+
+
 def test_norm_rope_in_place_and_without_a_cache():
     for kind in ("bf16", "f32"):
         x = torch.randn((300, 12, 128), device="cuda").to(KINDS[kind][0])
