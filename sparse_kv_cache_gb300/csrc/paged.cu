@@ -245,9 +245,15 @@ int shadowkv_qk_norm_rope(const skv_qk_norm_rope_args* a, skv_stream stream) {
     p.q = a->q; p.k = a->k; p.v = a->v; p.qw = a->q_weight; p.kw = a->k_weight; p.qo = a->q_out; p.ko = a->k_out;
     p.positions = a->positions; p.seq = a->seq; p.index = a->index;
     p.row_position = a->row_position; p.row_weight = a->row_weight; p.row_pitch = a->row_pitch;
+    // rope_base^(-2i/rd) from the powers of i's bits: six calls of pow, not 64, and off by at most a few
+    // units of 2^-53 (64 calls were 1.5 us of the host's 4.4)
+    double power[64] = {1.0};
+    for (int bit = 1; bit < rd / 2; bit *= 2) {
+        const double f = std::pow(a->rope_base, -2.0 * bit / rd);
+        for (int i = bit; i < 2 * bit && i < rd / 2; ++i) power[i] = power[i - bit] * f;
+    }
     for (int i = 0; i < rd / 2; ++i)
-        p.turn[i] = static_cast<uint64_t>(
-            std::ldexp(std::pow(a->rope_base, -2.0 * i / rd) / 6.283185307179586476925, 64));
+        p.turn[i] = static_cast<uint64_t>(power[i] * (18446744073709551616.0 / 6.283185307179586476925));
     return done(launch_norm_rope(c.dtype, c.head_dim, p, dev.nsm, stream));
 }
 
