@@ -31,6 +31,8 @@
 // of 4) 30.5 us against 11.6 of their bytes; one sequence of 1013 rows 6.4 us, all of it latency.
 #include <math_constants.h>
 
+#include <atomic>
+
 #include "skv_common.cuh"
 #include "skv_internal.h"
 #include "skv_paged.h"
@@ -1239,30 +1241,69 @@ constexpr int kOccTC = 3, kOccF32 = 2;     // CTAs per SM
 
 int paged_attn_ctas(int dtype, int nsm) { return nsm * (dtype == SKV_F32 ? kOccF32 : kOccTC); }
 
-// CTAs of a unit's cluster, or 0: the general form.  The cluster form serves a step whose units leave
-// SMs idle and whose longest possible sequence takes a warp no more than kClusterTiles tiles (with twice
-// as many, 8 units of 16K rows took 25.0 us against the general form's 21.0, 64 ragged ones of 4000 rows
-// 25.0 against 21.1), and one whose units, a CTA each, are up to three times as many as the CTAs that the
-// device holds (fp32: twice), with at most kUnitTiles tiles for a warp.  (Ragged bf16 units of up to 250
-// rows: 460 of them 9.6 us against 18.0, 1368 23.6 against 25.6, 2000 32.1 against 31.6.  Of up to 611 rows:
-// 300 16.8 against 18.5, 768 28.6 against 29.6; of 1000 300 24.7 against 22.6.  Units of one length lose
-// where a few are left over: 460 of 750 rows 41.6 against 36.5, 912 57.4 against 59.8.  fp32, 600 ragged
-// ones of 250 rows 27.0 against 33.5; 912 of exactly 250 54.4 against 44.7.)
+// Clusters of `ranks` CTAs that the device holds at once, asked for once per kernel: those of four and
+// more do not fill every GPC (of 152 SMs with three CTAs each 110 of four, 51 of eight, 21 of 16).
 constexpr int kClusterTiles = 8, kUnitTiles = 12;
-static int cluster_ranks(const PagedAttnParams& p, int ncta, bool f32) {
+// shared memory of a cluster form's kernel: all of a kind are allowed the most, whatever one takes (calls of
+// several host threads would set each other's limit)
+constexpr int z_bytes(int tiles, int Gp) { return kPaWarps * tiles * kPaTile * Gp * 4; }
+template <class Kernel>
+static bool allow(Kernel kernel, int ranks, int smem) {
+    return (ranks <= 8 || cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) &&
+           (!smem || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, z_bytes(kUnitTiles, 8)) == cudaSuccess);
+}
+template <class Tile, int D, bool kF32, int G, int kOcc, bool kKeep>
+static int clusters_held(int ranks) {
+    static std::atomic<int> known[17];
+    int n = known[ranks].load(std::memory_order_relaxed) - 1;
+    if (n >= 0) return n;
+    auto kernel = k_paged_cluster<Tile, D, kF32, G, kOcc, kKeep>;
+    const int smem = kKeep ? z_bytes(kClusterTiles, 8) : 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ranks);
+    cfg.blockDim = dim3(kPaThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ranks;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (!allow(kernel, ranks, smem) || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    known[ranks].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+// CTAs of a unit's cluster, or 0: the general form.  The cluster form serves a step whose units leave
+// SMs idle, whose clusters all run at once and whose longest possible sequence takes a warp no more than
+// kClusterTiles tiles (with twice as many, 8 units of 16K rows took 25.0 us against the general form's
+// 21.0, 64 ragged ones of 4000 rows 25.0 against 21.1; with two clusters left over, 112 of 2000 rows took
+// 32.3 against 26.9, ragged 18.0 against 20.5, where 108 take 21.2 against 26.5), and one whose units,
+// a CTA each, are up to three times as many as the CTAs that the device holds (fp32: twice), with at most
+// kUnitTiles tiles for a warp.  (Ragged bf16 units of up to 250 rows: 460 of them 9.6 us against 18.0, 1368
+// 23.6 against 25.6, 2000 32.1 against 31.6.  Of up to 611 rows: 300 16.8 against 18.5, 768 28.6 against
+// 29.6; of 1000 300 24.7 against 22.6.  Units of one length lose where a few are left over: 460 of 750
+// rows 41.6 against 36.5, 912 57.4 against 59.8.  fp32, 600 ragged ones of 250 rows 27.0 against 33.5; 912
+// of exactly 250 54.4 against 44.7.)
+template <class Tile, int D, bool kF32, int G, int kOcc, bool kKeep>
+static int cluster_ranks(const PagedAttnParams& p, int ncta) {
     const int64_t U = static_cast<int64_t>(p.c.batch) * p.c.H, tiles = (p.c.cap + kPaTile - 1) / kPaTile;
     int ranks = 1;
-    while (ranks < 16 && tiles > ranks * kPaWarps && 2 * U * ranks <= ncta) ranks *= 2;
-    if (ranks == 1) return U <= (f32 ? 2 : 3) * static_cast<int64_t>(ncta) && cluster_tiles(p.c.cap, 1) <= kUnitTiles ? 1 : 0;
+    while (ranks < 16 && tiles > ranks * kPaWarps && 2 * U * ranks <= ncta &&
+           U <= clusters_held<Tile, D, kF32, G, kOcc, kKeep>(2 * ranks))
+        ranks *= 2;
+    if (ranks == 1) return U <= (kF32 ? 2 : 3) * static_cast<int64_t>(ncta) && cluster_tiles(p.c.cap, 1) <= kUnitTiles ? 1 : 0;
     return cluster_tiles(p.c.cap, ranks) <= kClusterTiles ? ranks : 0;
 }
 
-template <class Tile, int D, bool kF32, int G, int kOcc>
+template <class Tile, int D, bool kF32, int G, int kOcc, bool kKeep>
 static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
-    auto kernel = p.weight_out ? k_paged_cluster<Tile, D, kF32, G, kOcc, true> : k_paged_cluster<Tile, D, kF32, G, kOcc, false>;
-    const int smem = p.weight_out ? kPaWarps * cluster_tiles(p.c.cap, ranks) * kPaTile * p.Gp * 4 : 0;
-    if (ranks > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return -1;
-    if (smem && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
+    auto kernel = k_paged_cluster<Tile, D, kF32, G, kOcc, kKeep>;
+    const int smem = kKeep ? z_bytes(cluster_tiles(p.c.cap, ranks), p.Gp) : 0;
+    if (!allow(kernel, ranks, smem)) return -1;
     return launch_first(kernel, static_cast<unsigned>(p.c.batch) * p.c.H * ranks, kPaThreads, smem, ranks, s, p, ranks) ==
                    cudaSuccess
                ? 0
@@ -1271,7 +1312,12 @@ static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
 
 template <class Tile, int D, bool kF32, int G, int kOcc>
 static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
-    if (const int ranks = cluster_ranks(p, ncta, kF32)) return launch_cluster<Tile, D, kF32, G, kOcc>(p, ranks, s);
+    if (p.weight_out) {
+        if (const int ranks = cluster_ranks<Tile, D, kF32, G, kOcc, true>(p, ncta))
+            return launch_cluster<Tile, D, kF32, G, kOcc, true>(p, ranks, s);
+    } else if (const int ranks = cluster_ranks<Tile, D, kF32, G, kOcc, false>(p, ncta)) {
+        return launch_cluster<Tile, D, kF32, G, kOcc, false>(p, ranks, s);
+    }
     // no more CTAs than there can be tiles for their warps
     const int64_t tiles = static_cast<int64_t>(p.c.batch) * p.c.H * ((p.c.cap + kPaTile - 1) / kPaTile);
     constexpr int kMin = (kF32 ? 1 : kPaLeast) * kPaWarps;
