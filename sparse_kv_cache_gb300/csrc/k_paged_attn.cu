@@ -1237,9 +1237,13 @@ __global__ void __launch_bounds__(kPaThreads, kWeighOcc) k_paged_weigh(const __g
 
 // ------------------------------------------------------------------ launches
 
-constexpr int kOccTC = 3, kOccF32 = 2;     // CTAs per SM
+// CTAs per SM.  fp32 of 64 dimensions has the registers for three in the general form (4 x 16K rows of 8 x 4
+// heads 51 us against 57, of 8 x 8 72 against 80; of 128 dimensions and 8 x 4 heads 105 against 87), short
+// sequences take two all the same (three of 4099 rows of 2 x 8 heads 14.6 against 15.7).
+constexpr int kOccTC = 3, kOccF32 = 2;
+constexpr int occ_of(bool f32, int d) { return f32 && d == 128 ? kOccF32 : kOccTC; }
 
-int paged_attn_ctas(int dtype, int nsm) { return nsm * (dtype == SKV_F32 ? kOccF32 : kOccTC); }
+int paged_attn_ctas(int dtype, int d, int nsm) { return nsm * occ_of(dtype == SKV_F32, d); }
 
 // Clusters of `ranks` CTAs that the device holds at once, asked for once per kernel: those of four and
 // more do not fill every GPC (of 152 SMs with three CTAs each 110 of four, 51 of eight, 21 of 16).
@@ -1310,13 +1314,15 @@ static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
                : -1;
 }
 
-template <class Tile, int D, bool kF32, int G, int kOcc>
+template <class Tile, int D, bool kF32, int G>
 static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
+    constexpr int kOcc = occ_of(kF32, D), kOccShort = kF32 ? kOccF32 : kOccTC;
+    const int held = ncta / kOcc * kOccShort;
     if (p.weight_out) {
-        if (const int ranks = cluster_ranks<Tile, D, kF32, G, kOcc, true>(p, ncta))
-            return launch_cluster<Tile, D, kF32, G, kOcc, true>(p, ranks, s);
-    } else if (const int ranks = cluster_ranks<Tile, D, kF32, G, kOcc, false>(p, ncta)) {
-        return launch_cluster<Tile, D, kF32, G, kOcc, false>(p, ranks, s);
+        if (const int ranks = cluster_ranks<Tile, D, kF32, G, kOccShort, true>(p, held))
+            return launch_cluster<Tile, D, kF32, G, kOccShort, true>(p, ranks, s);
+    } else if (const int ranks = cluster_ranks<Tile, D, kF32, G, kOccShort, false>(p, held)) {
+        return launch_cluster<Tile, D, kF32, G, kOccShort, false>(p, ranks, s);
     }
     // no more CTAs than there can be tiles for their warps
     const int64_t tiles = static_cast<int64_t>(p.c.batch) * p.c.H * ((p.c.cap + kPaTile - 1) / kPaTile);
@@ -1339,19 +1345,19 @@ static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
 }
 template <int D>
 static int launch_f32(const PagedAttnParams& p, int ncta, cudaStream_t s) {
-    if (p.G <= 1) return launch_pa<TileF32<D, 1>, D, true, 1, kOccF32>(p, ncta, s);
-    if (p.G <= 2) return launch_pa<TileF32<D, 2>, D, true, 2, kOccF32>(p, ncta, s);
-    if (p.G <= 4) return launch_pa<TileF32<D, 4>, D, true, 4, kOccF32>(p, ncta, s);
-    return launch_pa<TileF32<D, 8>, D, true, 8, kOccF32>(p, ncta, s);
+    if (p.G <= 1) return launch_pa<TileF32<D, 1>, D, true, 1>(p, ncta, s);
+    if (p.G <= 2) return launch_pa<TileF32<D, 2>, D, true, 2>(p, ncta, s);
+    if (p.G <= 4) return launch_pa<TileF32<D, 4>, D, true, 4>(p, ncta, s);
+    return launch_pa<TileF32<D, 8>, D, true, 8>(p, ncta, s);
 }
 
 int launch_paged_attn(int dtype, int d, const PagedAttnParams& p, int ncta, cudaStream_t s) {
     if (dtype == SKV_F32) return d == 64 ? launch_f32<64>(p, ncta, s) : launch_f32<128>(p, ncta, s);
     if (dtype == SKV_FP8)
-        return d == 64 ? launch_pa<TileTC<64, true>, 64, false, 8, kOccTC>(p, ncta, s)
-                       : launch_pa<TileTC<128, true>, 128, false, 8, kOccTC>(p, ncta, s);
-    return d == 64 ? launch_pa<TileTC<64, false>, 64, false, 8, kOccTC>(p, ncta, s)
-                   : launch_pa<TileTC<128, false>, 128, false, 8, kOccTC>(p, ncta, s);
+        return d == 64 ? launch_pa<TileTC<64, true>, 64, false, 8>(p, ncta, s)
+                       : launch_pa<TileTC<128, true>, 128, false, 8>(p, ncta, s);
+    return d == 64 ? launch_pa<TileTC<64, false>, 64, false, 8>(p, ncta, s)
+                   : launch_pa<TileTC<128, false>, 128, false, 8>(p, ncta, s);
 }
 
 cudaError_t paged_attn_err(int** e) { return cudaGetSymbolAddress(reinterpret_cast<void**>(e), g_err); }

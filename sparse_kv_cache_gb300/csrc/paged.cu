@@ -148,7 +148,7 @@ int attn_space(const skv_paged_attention_args* a, AttnSpace* w) {
     const int64_t U = static_cast<int64_t>(c.batch) * c.n_kv_heads, cap = static_cast<int64_t>(c.max_pages) * c.page_size;
     if (U > kMaxUnits) return SKV_ERR_INVALID;
     w->Gp = (G + 1) & ~1;
-    const int64_t ctas = paged_attn_ctas(c.dtype, kMaxSms);
+    const int64_t ctas = paged_attn_ctas(c.dtype, c.head_dim, kMaxSms);
     w->joint = 0;
     w->rec = ctas * static_cast<int64_t>(sizeof(Joint));
     w->rec_stat = w->rec + ctas * 2 * G * c.head_dim * 4;
@@ -302,7 +302,7 @@ int shadowkv_paged_attention(const skv_paged_attention_args* a, skv_stream strea
         p.weight = a->weight; p.weight_out = a->weight_out; p.row_pitch = a->row_pitch;
     }
     return done(launch_paged_attn(c.dtype, c.head_dim, p,
-                                  paged_attn_ctas(c.dtype, dev.nsm < kMaxSms ? dev.nsm : kMaxSms), stream));
+                                  paged_attn_ctas(c.dtype, c.head_dim, dev.nsm < kMaxSms ? dev.nsm : kMaxSms), stream));
 }
 
 int64_t shadowkv_paged_evict_workspace(const skv_paged_evict_args* a) {

@@ -52,7 +52,7 @@ struct PagedAttnParams {
     const float* weight; float* weight_out; int64_t row_pitch;
 };
 constexpr int kPaWarps = 4;                  // warps of a CTA of the attention
-int paged_attn_ctas(int dtype, int nsm);     // CTAs that fill nsm SMs
+int paged_attn_ctas(int dtype, int d, int nsm);     // CTAs that fill nsm SMs
 int launch_paged_attn(int dtype, int d, const PagedAttnParams& p, int ncta, cudaStream_t s);
 
 struct EvictParams {
