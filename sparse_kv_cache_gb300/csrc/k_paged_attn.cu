@@ -1037,7 +1037,7 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid
 // Joins the records of the units that lie in more than one CTA's range: row i of the grid those of
 // the unit that ends in CTA i's range and began before it (p.joint says which, if any).  The grid's
 // y dimension deals the heads out.
-constexpr int kPaMost = 512;      // shares of a unit at most
+constexpr int kPaMost = 640;      // shares of a unit at most (CTAs of the attention)
 constexpr int kPaFew = 8;         // shares that a thread joins by itself
 
 // Few shares: a thread holds four dimensions of one head, and forms the weights for itself.
@@ -1237,24 +1237,25 @@ __global__ void __launch_bounds__(kPaThreads, kWeighOcc) k_paged_weigh(const __g
 
 // ------------------------------------------------------------------ launches
 
-// CTAs per SM.  fp32 of 64 dimensions has the registers for three in the general form (4 x 16K rows of 8 x 4
-// heads 51 us against 57, of 8 x 8 72 against 80; of 128 dimensions and 8 x 4 heads 105 against 87), short
-// sequences take two all the same (three of 4099 rows of 2 x 8 heads 14.6 against 15.7).
-constexpr int kOccTC = 3, kOccF32 = 2;
-constexpr int occ_of(bool f32, int d) { return f32 && d == 128 ? kOccF32 : kOccTC; }
+// CTAs per SM, by the registers that 128 and 64 dimensions need.  (64 dimensions: 64 ragged units of up to
+// 64K rows with e5m2 values 78 us with four, 89 with three; 32 of 16K rows in bf16 31.7 and 32.7; fp32, 32
+// of 16K rows of four heads 51 with three, 57 with two, of eight 72 and 80; 128 dimensions and four heads
+// 105 and 87.)  Short sequences in fp32 take two all the same (three of 4099 rows of 2 x 8 heads, 64
+// dimensions, 14.6 us against 15.7).
+constexpr int occ_of(bool f32, int d) { return (f32 ? 2 : 3) + (d == 64 ? 1 : 0); }
 
 int paged_attn_ctas(int dtype, int d, int nsm) { return nsm * occ_of(dtype == SKV_F32, d); }
 
 // Clusters of `ranks` CTAs that the device holds at once, asked for once per kernel: those of four and
 // more do not fill every GPC (of 152 SMs with three CTAs each 110 of four, 51 of eight, 21 of 16).
-constexpr int kClusterTiles = 8, kUnitTiles = 12;
+constexpr int kClusterTiles = 8, kUnitTiles = 12, kOneWaveTiles = 16;
 // shared memory of a cluster form's kernel: all of a kind are allowed the most, whatever one takes (calls of
 // several host threads would set each other's limit)
 constexpr int z_bytes(int tiles, int Gp) { return kPaWarps * tiles * kPaTile * Gp * 4; }
 template <class Kernel>
 static bool allow(Kernel kernel, int ranks, int smem) {
     return (ranks <= 8 || cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) &&
-           (!smem || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, z_bytes(kUnitTiles, 8)) == cudaSuccess);
+           (!smem || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, z_bytes(kOneWaveTiles, 8)) == cudaSuccess);
 }
 template <class Tile, int D, bool kF32, int G, int kOcc, bool kKeep>
 static int clusters_held(int ranks) {
@@ -1287,9 +1288,10 @@ static int clusters_held(int ranks) {
 // 21.0, 64 ragged ones of 4000 rows 25.0 against 21.1; with two clusters left over, 112 of 2000 rows took
 // 32.3 against 26.9, ragged 18.0 against 20.5, where 108 take 21.2 against 26.5), and one whose units,
 // a CTA each, are up to three times as many as the CTAs that the device holds (fp32: twice), with at most
-// kUnitTiles tiles for a warp.  (Ragged bf16 units of up to 250 rows: 460 of them 9.6 us against 18.0, 1368
-// 23.6 against 25.6, 2000 32.1 against 31.6.  Of up to 611 rows: 300 16.8 against 18.5, 768 28.6 against
-// 29.6; of 1000 300 24.7 against 22.6.  Units of one length lose where a few are left over: 460 of 750
+// kUnitTiles tiles for a warp, or kOneWaveTiles where they fill the device once.  (Ragged bf16 units of up
+// to 250 rows: 460 of them 9.6 us against 18.0, 1368 23.6 against 25.6, 2000 32.1 against 31.6.  Of up to
+// 611 rows: 300 16.8 against 18.5, 768 28.6 against 29.6; of 1000 300 24.7 against 22.6, 452 27.1 against
+// 28.2, and 37.7 against 44.7 of 1000 each.  Units of one length lose where a few are left over: 460 of 750
 // rows 41.6 against 36.5, 912 57.4 against 59.8.  fp32, 600 ragged ones of 250 rows 27.0 against 33.5; 912
 // of exactly 250 54.4 against 44.7.)
 template <class Tile, int D, bool kF32, int G, int kOcc, bool kKeep>
@@ -1299,7 +1301,10 @@ static int cluster_ranks(const PagedAttnParams& p, int ncta) {
     while (ranks < 16 && tiles > ranks * kPaWarps && 2 * U * ranks <= ncta &&
            U <= clusters_held<Tile, D, kF32, G, kOcc, kKeep>(2 * ranks))
         ranks *= 2;
-    if (ranks == 1) return U <= (kF32 ? 2 : 3) * static_cast<int64_t>(ncta) && cluster_tiles(p.c.cap, 1) <= kUnitTiles ? 1 : 0;
+    if (ranks == 1) {
+        const int tiles_most = U <= ncta && 4 * U >= 3 * static_cast<int64_t>(ncta) ? kOneWaveTiles : kUnitTiles;
+        return U <= (kF32 ? 2 : 3) * static_cast<int64_t>(ncta) && cluster_tiles(p.c.cap, 1) <= tiles_most ? 1 : 0;
+    }
     return cluster_tiles(p.c.cap, ranks) <= kClusterTiles ? ranks : 0;
 }
 
@@ -1316,7 +1321,7 @@ static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
 
 template <class Tile, int D, bool kF32, int G>
 static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
-    constexpr int kOcc = occ_of(kF32, D), kOccShort = kF32 ? kOccF32 : kOccTC;
+    constexpr int kOcc = occ_of(kF32, D), kOccShort = kF32 ? 2 : kOcc;
     const int held = ncta / kOcc * kOccShort;
     if (p.weight_out) {
         if (const int ranks = cluster_ranks<Tile, D, kF32, G, kOccShort, true>(p, held))
