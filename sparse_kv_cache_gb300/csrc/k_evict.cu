@@ -583,7 +583,7 @@ int launch_evict(const EvictParams& p, int nsm, cudaStream_t s) {
     const int smem = kEvHist * 4 + (key_cap + low_cap) * 2;
     auto kernel = narrow ? k_evict<kEvNarrow, true> : few ? k_evict<kEvWide, true> : k_evict<kEvWide, false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvHist * 4 + kEvKeys * 2) != cudaSuccess ||
-        launch_first(kernel, static_cast<unsigned>(U) * ranks, threads, smem, ranks, s, p, ranks, key_cap, low_cap) !=
+        launch_first(kernel, static_cast<unsigned>(U) * ranks, threads, smem, ranks, 0, s, p, ranks, key_cap, low_cap) !=
             cudaSuccess)
         return -1;
     cudaError_t e = cudaSuccess;

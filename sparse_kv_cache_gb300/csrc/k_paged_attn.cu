@@ -1313,7 +1313,7 @@ static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
     auto kernel = k_paged_cluster<Tile, D, kF32, G, kOcc, kKeep>;
     const int smem = kKeep ? z_bytes(cluster_tiles(p.c.cap, ranks), p.Gp) : 0;
     if (!allow(kernel, ranks, smem)) return -1;
-    return launch_first(kernel, static_cast<unsigned>(p.c.batch) * p.c.H * ranks, kPaThreads, smem, ranks, s, p, ranks) ==
+    return launch_first(kernel, static_cast<unsigned>(p.c.batch) * p.c.H * ranks, kPaThreads, smem, ranks, kCarve, s, p, ranks) ==
                    cudaSuccess
                ? 0
                : -1;
@@ -1335,16 +1335,16 @@ static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
     const int64_t most = (tiles + kMin - 1) / kMin;
     const int n = most < ncta ? static_cast<int>(most) : ncta;
     auto kernel = p.weight_out ? k_paged_attn<Tile, D, kF32, G, kOcc, true> : k_paged_attn<Tile, D, kF32, G, kOcc, false>;
-    if (launch_first(kernel, n, kPaThreads, 0, 1, s, p) != cudaSuccess) return -1;
+    if (launch_first(kernel, n, kPaThreads, 0, 1, kCarve, s, p) != cudaSuccess) return -1;
     // a CTA per head where units are few and so have many shares; one for all heads where they are many
     const int heads = p.c.batch * static_cast<int64_t>(p.c.H) * 4 >= n ? 1 : p.G;
-    if (launch_pdl(k_paged_merge<D, kF32>, dim3(n, heads), dim3(kPaThreads), 0, s, p) != cudaSuccess) return -1;
+    if (launch_first(k_paged_merge<D, kF32>, dim3(n, heads), kPaThreads, 0, 1, kCarve, s, p) != cudaSuccess) return -1;
     if (p.weight_out) {
         const int64_t blocks = static_cast<int64_t>(p.c.batch) * p.c.H * ((p.c.cap + kWeighRows - 1) / kWeighRows);
         const int64_t wide = static_cast<int64_t>(kWeighOcc) * (ncta / kOcc);
         const int nw = static_cast<int>(blocks < wide ? blocks : wide);
         auto weigh = p.Gp == 2 ? k_paged_weigh<2> : p.Gp == 4 ? k_paged_weigh<4> : p.Gp == 6 ? k_paged_weigh<6> : k_paged_weigh<8>;
-        if (launch_pdl(weigh, dim3(nw), dim3(kPaThreads), 0, s, p) != cudaSuccess) return -1;
+        if (launch_first(weigh, nw, kPaThreads, 0, 1, kCarve, s, p) != cudaSuccess) return -1;
     }
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
