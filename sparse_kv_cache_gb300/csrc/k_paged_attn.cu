@@ -287,6 +287,13 @@ __device__ __forceinline__ float share_weight(float x, float l, float m) {
     return x == -CUDART_INF_F && !(l != l) ? 0.f : exp2_fast(x - m);
 }
 
+// A running sum of thousands of terms loses more by its roundings (the tensor cores cut off what does
+// not fit) than its terms are off by.  So every 32 tiles a warp adds its sums to ones held in shared
+// memory, in the place of its last share, and begins again at zero; what is held goes by the base that
+// it was formed with.  (One warp over 128K rows of values 1, then -1: off by 1.7e-4 without, where all other
+// roundings may make 7e-5.  8 x 128K rows take 0.2 % longer for it.)
+struct HoldNone { __device__ __forceinline__ void operator()() const {} };     // a warp of few tiles
+
 // Page ids of a warp's coming tiles: lane j holds those of tile j of the current 32.
 struct PageIds {
     int a, b;    // of the tile's first and last eight rows
@@ -382,6 +389,7 @@ struct TileTC {
     uint4 q[kKV];
     float o[D / 16][4];
     float m0, m1, l0, l1;                                  // heads 2c and 2c + 1
+    bool held;                                             // whether the unit has held sums
 
     __device__ __forceinline__ void load_q(const PagedAttnParams& p, int b, int h) {
         const int g = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
@@ -395,6 +403,7 @@ struct TileTC {
         for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         m0 = m1 = -CUDART_INF_F;
         l0 = l1 = 0.f;
+        held = false;
     }
     struct Keys { uint4 a[kKV], b[kKV]; };                 // row r and row r + 8
     struct Values { uint4 v[4][kVV]; };                    // rows 2c, 2c + 1, 2c + 8, 2c + 9
@@ -529,9 +538,70 @@ struct TileTC {
     // The lane's accumulators are runs of consecutive dimensions (accumulator t holds a pair for
     // each of two heads): two runs of 8 with bf16 values, one of D / 8 with e5m2 ones.
     static constexpr int kRun = kE5M2 ? D / 8 : 8;
-    // writes the unit's result, or this share of it for the join
-    __device__ __forceinline__ void finish(const PagedAttnParams& p, int b, int h, bool alone, JoinSmem<D, 8>& js, int slot) {
+    __device__ __forceinline__ static int dim_of(int r, int t) { return kE5M2 ? kRun * r + 2 * t : 64 * (t / 4) + 8 * r; }
+    // adds what is held in a slot to the sums
+    __device__ __forceinline__ void take(const JoinSmem<D, 8>& js, int slot) {
         const int r = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float l = js.l[slot][2 * c + e], w = share_weight(js.m[slot][2 * c + e], l, e ? m1 : m0);
+            if (r == 0) (e ? l1 : l0) = fmaf(l, w, e ? l1 : l0);
+#pragma unroll
+            for (int t = 0; t < D / 16; t += 4) {
+                float x[8];
+                load8(&js.o[slot][2 * c + e][dim_of(r, t)], x);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[t + i][e] = fmaf(x[2 * i], w, o[t + i][e]);
+                    o[t + i][2 + e] = fmaf(x[2 * i + 1], w, o[t + i][2 + e]);
+                }
+            }
+        }
+        __syncwarp();      // the slot may be written again
+    }
+    // adds the sums to what is held and begins again at zero
+    __device__ __forceinline__ void hold(JoinSmem<D, 8>& js, int slot) {
+        const int r = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int g = 2 * c + e;
+            float l = e ? l1 : l0, w = 0.f;
+            if (held) {
+                w = share_weight(js.m[slot][g], js.l[slot][g], e ? m1 : m0);
+                l = fmaf(js.l[slot][g], w, l);
+            }
+            __syncwarp();
+            if (r == 0) {
+                js.m[slot][g] = e ? m1 : m0;
+                js.l[slot][g] = l;
+            }
+#pragma unroll
+            for (int t = 0; t < D / 16; t += 4) {
+                float x[8] = {};
+                if (held) load8(&js.o[slot][g][dim_of(r, t)], x);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[2 * i] = fmaf(x[2 * i], w, o[t + i][e]);
+                    x[2 * i + 1] = fmaf(x[2 * i + 1], w, o[t + i][2 + e]);
+                    o[t + i][e] = o[t + i][2 + e] = 0.f;
+                }
+                store8(&js.o[slot][g][dim_of(r, t)], x);
+            }
+        }
+        l0 = l1 = 0.f;
+        held = true;
+        __syncwarp();
+    }
+    // writes the unit's result, or this share of it for the join
+    __device__ __forceinline__ void finish(const PagedAttnParams& p, int b, int h, bool alone, JoinSmem<D, 8>& js, int slot,
+                                           int from) {
+        const int r = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
+        if (held) take(js, from);
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, x);
@@ -546,7 +616,7 @@ struct TileTC {
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + b * p.o_seq + (h * p.G + g) * p.o_head;
 #pragma unroll
             for (int t = 0; t < D / 16; t += 4) {
-                const int dim = kE5M2 ? kRun * r + 2 * t : 64 * (t / 4) + 8 * r;
+                const int dim = dim_of(r, t);
                 float x[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -568,9 +638,10 @@ struct TileTC {
     }
     // The pieces from `cur` on, as one stream of tiles: the first loads of the next piece are on their
     // way before this one is done with.  next(piece) gives the following one; done(piece, whether there is
-    // another) hands over.
-    template <class Keep, class Next, class Done>
-    __device__ __forceinline__ void stream(const PagedAttnParams& p, Piece cur, float*, Keep z, Next next, Done done) {
+    // another) hands over; put_by() holds the sums.
+    template <class Keep, class Hold, class Next, class Done>
+    __device__ __forceinline__ void stream(const PagedAttnParams& p, Piece cur, float*, Keep z, Hold put_by, Next next,
+                                           Done done) {
         const int lane = threadIdx.x & 31;
         Piece then;
         bool more = next(then);
@@ -609,6 +680,7 @@ struct TileTC {
             softmax(p.scale_log2, row, cur.end, was_a, was_b, s, b0, b1, r0, r1);
             values(v, b0, b1, r0, r1);
             if (!last) {
+                if (t == 0) put_by();
                 load_v(p, cur.h, row + kPaTile, cur.end, ida, idb, v);
                 cur.row = row + kPaTile;
                 continue;
@@ -632,6 +704,7 @@ struct TileF32 {
     static constexpr int kV = D / 64;      // float4 of a row per lane
     float o[G][4 * kV];
     float m[G], l[G];
+    bool held;                             // whether the unit has held sums
     const float* sq;                       // [G][D + 4] the warp's queries in shared memory
 
     __device__ __forceinline__ void load_q(const PagedAttnParams& p, int b, int h, float* s_q) {
@@ -651,6 +724,7 @@ struct TileF32 {
 #pragma unroll
             for (int i = 0; i < 4 * kV; ++i) o[g][i] = 0.f;
         }
+        held = false;
     }
     __device__ __forceinline__ void load(const float* base, int64_t page, int64_t pitch, int mask, int row, int end, int id,
                                          float (&x)[8][4 * kV]) {
@@ -669,8 +743,8 @@ struct TileF32 {
             }
         }
     }
-    template <class Keep>
-    __device__ __forceinline__ void share(const PagedAttnParams& p, const Piece& piece, const Keep& z) {
+    template <class Keep, class Hold>
+    __device__ __forceinline__ void share(const PagedAttnParams& p, const Piece& piece, const Keep& z, Hold put_by) {
         const int b = piece.b, h = piece.h, row0 = piece.row, end = piece.end;
         const int lane = threadIdx.x & 31, hl = lane & 15, half = lane >> 4, mask = (1 << p.c.lg) - 1;
         const float* kb = static_cast<const float*>(p.c.k) + h * p.c.k_head;
@@ -746,23 +820,78 @@ struct TileF32 {
                     for (int j = 0; j < 4 * kV; ++j) o[g][j] = fmaf(w, v[i][j], o[g][j]);
                 }
             }
+            if (t == 0 && row + kPaTile < end) put_by();
         }
     }
-    template <class Keep, class Next, class Done>
-    __device__ __forceinline__ void stream(const PagedAttnParams& p, Piece cur, float* s_q, Keep z, Next next, Done done) {
+    template <class Keep, class Hold, class Next, class Done>
+    __device__ __forceinline__ void stream(const PagedAttnParams& p, Piece cur, float* s_q, Keep z, Hold put_by, Next next,
+                                           Done done) {
         for (bool more = true; more;) {
             load_q(p, cur.b, cur.h, s_q);
             reset();
-            share(p, cur, z);
+            share(p, cur, z, put_by);
             Piece then = cur;
             more = next(then);
             done(cur, more);
             cur = then;
         }
     }
-    __device__ __forceinline__ void finish(const PagedAttnParams& p, int b, int h, bool alone, JoinSmem<D, G>& js, int slot) {
+    // adds what is held in a slot to the sums: the first half-warp's, and every lane's half of the rows' sum
+    __device__ __forceinline__ void take(const JoinSmem<D, G>& js, int slot) {
+        const int lane = threadIdx.x & 31, hl = lane & 15;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const float w = share_weight(js.m[slot][g], js.l[slot][g], m[g]);
+            if (lane == 0) l[g] = fmaf(2.f * js.l[slot][g], w, l[g]);
+            if (lane >= 16) continue;
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const float4 x = *reinterpret_cast<const float4*>(&js.o[slot][g][64 * i + 4 * hl]);
+                o[g][4 * i] = fmaf(x.x, w, o[g][4 * i]);
+                o[g][4 * i + 1] = fmaf(x.y, w, o[g][4 * i + 1]);
+                o[g][4 * i + 2] = fmaf(x.z, w, o[g][4 * i + 2]);
+                o[g][4 * i + 3] = fmaf(x.w, w, o[g][4 * i + 3]);
+            }
+        }
+        __syncwarp();      // the slot may be written again
+    }
+    // the sums of both half-warps, of head g into a slot
+    __device__ __forceinline__ void put(JoinSmem<D, G>& js, int slot, int g, float sum, const float (&x)[4 * kV]) const {
+        const int lane = threadIdx.x & 31, hl = lane & 15;
+        if (lane < 16) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i)
+                *reinterpret_cast<float4*>(&js.o[slot][g][64 * i + 4 * hl]) =
+                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        }
+        if (lane == 0) {
+            js.m[slot][g] = m[g];
+            js.l[slot][g] = sum;
+        }
+    }
+    // holds the sums so far and begins again at zero
+    __device__ __forceinline__ void hold(JoinSmem<D, G>& js, int slot) {
+        if (held) take(js, slot);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float x[4 * kV];
+            const float sum = 0.5f * warp_sum(l[g]);
+#pragma unroll
+            for (int i = 0; i < 4 * kV; ++i) {
+                x[i] = o[g][i] + __shfl_xor_sync(0xffffffffu, o[g][i], 16);
+                o[g][i] = 0.f;
+            }
+            put(js, slot, g, sum, x);
+            l[g] = 0.f;
+        }
+        held = true;
+        __syncwarp();
+    }
+    __device__ __forceinline__ void finish(const PagedAttnParams& p, int b, int h, bool alone, JoinSmem<D, G>& js, int slot,
+                                           int from) {
         const int lane = threadIdx.x & 31, hl = lane & 15;
         __syncwarp();      // no lane reads the queries any more
+        if (held) take(js, from);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
             const float sum = 0.5f * warp_sum(l[g]);
@@ -770,22 +899,19 @@ struct TileF32 {
 #pragma unroll
             for (int i = 0; i < 4 * kV; ++i) x[i] = o[g][i] + __shfl_xor_sync(0xffffffffu, o[g][i], 16);
             if (g >= p.G) continue;
-            const float inv = !alone ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-            float* dst = alone ? static_cast<float*>(p.out) + b * p.o_seq + (h * p.G + g) * p.o_head : js.o[slot][g];
+            if (!alone) {
+                put(js, slot, g, sum, x);
+                continue;
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            float* dst = static_cast<float*>(p.out) + b * p.o_seq + (h * p.G + g) * p.o_head;
             if (lane < 16) {
 #pragma unroll
                 for (int i = 0; i < kV; ++i)
                     *reinterpret_cast<float4*>(dst + 64 * i + 4 * hl) =
                         make_float4(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
             }
-            if (lane == 0) {
-                if (alone) {
-                    note(p, b, h, g, m[g], sum);
-                } else {
-                    js.m[slot][g] = m[g];
-                    js.l[slot][g] = sum;
-                }
-            }
+            if (lane == 0) note(p, b, h, g, m[g], sum);
         }
     }
 };
@@ -857,6 +983,7 @@ __device__ __forceinline__ void join_shares(const PagedAttnParams& p, JoinSmem<D
 
 template <class Tile, int D, bool kF32, int G, int kOcc, bool kKeep>
 __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_constant__ PagedAttnParams p) {
+    extern __shared__ __align__(16) float s_q[];       // fp32: [warps][G][D + 4] their queries
     __shared__ PlanSmem<kPaWarps> s_plan;
     __shared__ __align__(16) JoinSmem<D, G> js;
     begin_call();
@@ -870,18 +997,18 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
         const Piece head = pieces.first(p.c, s_plan.b[warp], s_plan.rows[warp], s_plan.at[warp], w0, w1 - w0);
         Tile tile;
         bool first = true;
-        // (fp32 keeps its queries where the warp's last share will go)
+        auto put_by = [&] { tile.hold(js, 2 * warp + 1); };
         auto next = [&](Piece& q) { return pieces.next(p.c, q); };
         auto done = [&](const Piece& q, bool more) {
             const int slot = 2 * warp + (first ? 0 : 1);
             const bool begins = !first || pieces.begins, ends = more || pieces.ends;
-            tile.finish(p, q.b, q.h, begins && ends, js, slot);
+            tile.finish(p, q.b, q.h, begins && ends, js, slot, 2 * warp + 1);
             if (!(begins && ends) && lane == 0) js.of[slot] = ShareOf{q.b, q.h, begins, ends, first && w0 == pl.lo};
             first = false;
         };
-        float* queries = js.o[2 * warp + 1][0];
-        if constexpr (kKeep) tile.stream(p, head, queries, KeepGlobal{p}, next, done);
-        else tile.stream(p, head, queries, KeepNone{}, next, done);
+        float* queries = s_q + warp * G * (D + 4);
+        if constexpr (kKeep) tile.stream(p, head, queries, KeepGlobal{p}, put_by, next, done);
+        else tile.stream(p, head, queries, KeepNone{}, put_by, next, done);
     }
     // a unit that ends in this CTA and began before it
     if (tid == 0) {
@@ -931,15 +1058,16 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid
     const int t1 = static_cast<int>(static_cast<int64_t>(nt) * (part + 1) / parts);
     float* my_z = s_z + warp * cluster_tiles(p.c.cap, ranks) * kPaTile * (kKeep ? p.Gp : 0);
     Tile tile;
-    auto hand_over = [&](const Piece&, bool) { tile.finish(p, b, h, false, js, 2 * warp); };
+    auto hand_over = [&](const Piece&, bool) { tile.finish(p, b, h, false, js, 2 * warp, 0); };
     const int piece_row = t0 * kPaTile, piece_end = t0 < t1 ? min(rows, t1 * kPaTile) : piece_row;
     Piece piece{b, h, piece_row, piece_end, {-1, -1}};
     if (t0 < t1) {
         piece.ask(p.c);
         float* queries = js.o[2 * warp + 1][0];
         auto none = [](Piece&) { return false; };
-        if constexpr (kKeep) tile.stream(p, piece, queries, KeepShared{my_z, piece.row, p.Gp}, none, hand_over);
-        else tile.stream(p, piece, queries, KeepNone{}, none, hand_over);
+        // (at most kOneWaveTiles tiles: none of them fills a row of page ids)
+        if constexpr (kKeep) tile.stream(p, piece, queries, KeepShared{my_z, piece.row, p.Gp}, HoldNone{}, none, hand_over);
+        else tile.stream(p, piece, queries, KeepNone{}, HoldNone{}, none, hand_over);
     } else {
         tile.reset();
         hand_over(piece, false);
@@ -1335,7 +1463,11 @@ static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
     const int64_t most = (tiles + kMin - 1) / kMin;
     const int n = most < ncta ? static_cast<int>(most) : ncta;
     auto kernel = p.weight_out ? k_paged_attn<Tile, D, kF32, G, kOcc, true> : k_paged_attn<Tile, D, kF32, G, kOcc, false>;
-    if (launch_first(kernel, n, kPaThreads, 0, 1, kCarve, s, p) != cudaSuccess) return -1;
+    const int smem = kF32 ? kPaWarps * G * (D + 4) * 4 : 0;
+    // (eight heads of 128 dimensions take more than a kernel has without asking)
+    if (kF32 && G * D >= 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return -1;
+    if (launch_first(kernel, n, kPaThreads, smem, 1, kCarve, s, p) != cudaSuccess) return -1;
     // a CTA per head where units are few and so have many shares; one for all heads where they are many
     const int heads = p.c.batch * static_cast<int64_t>(p.c.H) * 4 >= n ? 1 : p.G;
     if (launch_first(k_paged_merge<D, kF32>, dim3(n, heads), kPaThreads, 0, 1, kCarve, s, p) != cudaSuccess) return -1;
