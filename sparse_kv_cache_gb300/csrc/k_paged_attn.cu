@@ -95,6 +95,10 @@ __device__ __forceinline__ float4 ld_cluster_v4f(uint32_t addr) {
                  : "memory");
     return v;
 }
+// the upper halves of two floats
+__device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -502,13 +506,16 @@ struct TileTC {
         l1 += x1 + x3;
         // The values' type for the tensor cores: fp16 (off by 2^-11 at most), or bf16 as the sum of two
         // terms (2^-16; one term alone, 2^-8, moved the result as much as its own rounding, and two cost
-        // 0.4 % of 8 x 128K rows' time and 1 % of 192 short sequences').  The sums keep the fp32 ones.
+        // 0.4 % of 8 x 128K rows' time and 1 % of 192 short sequences').  Both terms are above zero where the
+        // probability is, or an infinite value would meet a zero or a negative term and give NaN: the first is
+        // cut off a little below it, not rounded.  The sums keep the fp32 ones.
         if (kE5M2) {
             const __half2 lo = __floats2half2_rn(x0, x1), hi = __floats2half2_rn(x2, x3);
             b0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
             b1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi));
         } else {
-            const uint32_t h0 = pack_bf16x2(x0, x1), h1 = pack_bf16x2(x2, x3);
+            constexpr float kBelow = 1.f - 0x1p-20f;
+            const uint32_t h0 = cut_bf16x2(x0 * kBelow, x1 * kBelow), h1 = cut_bf16x2(x2 * kBelow, x3 * kBelow);
             b0 = transpose8x8(h0);
             b1 = transpose8x8(h1);
             r0 = transpose8x8(pack_bf16x2(x0 - bf16lo(h0), x1 - bf16hi(h0)));

@@ -8,10 +8,16 @@ import torch
 
 import sparse_kv_cache_gb300 as skv
 from oracle import paged_ref as ref
-from tests.paged_harness import KINDS, f64
-from tests.test_gpu_paged import U, UP
+from tests.paged_harness import KINDS, Paged, f64
+from tests.test_gpu_paged import U, UP, check_all, queries
 
 pytestmark = pytest.mark.gpu
+
+
+def wider(table, rows, ps):
+    """The table with room for `rows` rows more of every sequence."""
+    more = torch.full((table.shape[0], rows // ps), -1, dtype=torch.int32, device=table.device)
+    return torch.cat([table, more], 1)
 
 
 # ------------------------------------------------------------------ long sums
@@ -51,3 +57,37 @@ def test_one_warp_walks_a_long_unit(kind, d, units, flavour):
         bad = np.abs(got_lse[i::4] - want_lse)
         assert (bad <= delta + 2.0 ** -16 + 2.0 ** -22 * np.abs(want_lse)).all(), f"lse off by {bad.max():.3g}"
     assert skv.paged_status() == 0
+
+
+# ------------------------------------------------------------------ infinite and large values
+
+def put_value(c, b, row, dim, x):
+    page, off = int(c.table[b, row // c.ps]), row % c.ps
+    if c.kind == "fp8":
+        c.v.view(torch.uint8)[page, :, off, dim] = {math.inf: 0x7C, -math.inf: 0xFC}[x]
+    else:
+        c.v[page, :, off, dim] = x
+
+
+@pytest.mark.parametrize("headroom", [0, 16384])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
+def test_infinite_values_in_rows_that_count(kind, headroom):
+    """sum p_j v_j with v_j infinite and p_j > 0 is that infinity, whatever p_j; with both, NaN."""
+    lens = [1, 40, 3000, 700]
+    c = Paged(kind, lens, 2, 64, 16, seed=51)
+    q = queries(c, 4, 52, 0.5)
+    for b, n in enumerate(lens):
+        for dim, rows, x in ((1, [0], math.inf), (2, [n - 1], -math.inf), (3, [n // 2, n // 3], math.inf)):
+            for r in rows:
+                put_value(c, b, r, dim, x)
+        if n > 1:
+            put_value(c, b, 0, 4, math.inf), put_value(c, b, n - 1, 4, -math.inf)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    skv.paged_attention(q, c.k, c.v, wider(c.table, headroom, 16), c.lens, out, lse)
+    assert (out[..., 1] == math.inf).all() and (out[..., 2] == -math.inf).all() and (out[..., 3] == math.inf).all()
+    assert out[1:, :, 4].isnan().all()
+    # the other dimensions are what they are without
+    out[..., 1:5] = 0
+    for b in range(len(lens)):
+        c.vrows[b][..., 1:5] = 0
+    check_all(c, q, out, lse)
