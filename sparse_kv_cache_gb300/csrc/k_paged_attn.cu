@@ -45,6 +45,10 @@ constexpr int kPaThreads = 128;
 static_assert(kPaThreads == 32 * kPaWarps, "");
 constexpr int kPaTile = 16;                       // rows of a warp's step
 constexpr float kPaSlack = 8.f;                   // the base moves when a score passes it by 2^8
+// Probabilities before they are normalised are held 2^38 lower: those of 2^30 rows, 2^8 over their base
+// each, add up to 1 at most, so no sum of values passes the largest value, which may be the type's.  (Rows
+// 2^-88 below the top fall out at 2^-126; products of values below 2^-80 lose bits there.)
+constexpr float kPaDown = 38.f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -389,7 +393,8 @@ template <int D, bool kE5M2>
 struct TileTC {
     static constexpr int kKV = D / 32;                     // 16-byte words of a key row per lane
     static constexpr int kVV = kE5M2 ? 1 : D / 64;         // words of a value row per lane
-    static constexpr float kBaseShift = kE5M2 ? 7.f : 0.f; // keeps small fp16 probabilities normal: p <= 2^15
+    // fp16 probabilities: up to 2^15, the more of the small ones are normal (2^30 e5m2 values fit into a sum)
+    static constexpr float kBaseShift = kE5M2 ? 7.f : -kPaDown;
     uint4 q[kKV];
     float o[D / 16][4];
     float m0, m1, l0, l1;                                  // heads 2c and 2c + 1
@@ -818,7 +823,7 @@ struct TileF32 {
             }
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                const float pr = in ? exp2_fast(fmaf(s[g], p.scale_log2, m[g] == -CUDART_INF_F ? 0.f : -m[g])) : 0.f;
+                const float pr = in ? exp2_fast(fmaf(s[g], p.scale_log2, m[g] == -CUDART_INF_F ? 0.f : -m[g] - kPaDown)) : 0.f;
                 l[g] += pr;                     // every row is held by two lanes: halved at the end
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -863,7 +868,8 @@ struct TileF32 {
         __syncwarp();      // the slot may be written again
     }
     // the sums of both half-warps, of head g into a slot
-    __device__ __forceinline__ void put(JoinSmem<D, G>& js, int slot, int g, float sum, const float (&x)[4 * kV]) const {
+    __device__ __forceinline__ void put(JoinSmem<D, G>& js, int slot, int g, float base, float sum,
+                                        const float (&x)[4 * kV]) const {
         const int lane = threadIdx.x & 31, hl = lane & 15;
         if (lane < 16) {
 #pragma unroll
@@ -872,7 +878,7 @@ struct TileF32 {
                     make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
         }
         if (lane == 0) {
-            js.m[slot][g] = m[g];
+            js.m[slot][g] = base;
             js.l[slot][g] = sum;
         }
     }
@@ -888,7 +894,7 @@ struct TileF32 {
                 x[i] = o[g][i] + __shfl_xor_sync(0xffffffffu, o[g][i], 16);
                 o[g][i] = 0.f;
             }
-            put(js, slot, g, sum, x);
+            put(js, slot, g, m[g], sum, x);
             l[g] = 0.f;
         }
         held = true;
@@ -907,7 +913,7 @@ struct TileF32 {
             for (int i = 0; i < 4 * kV; ++i) x[i] = o[g][i] + __shfl_xor_sync(0xffffffffu, o[g][i], 16);
             if (g >= p.G) continue;
             if (!alone) {
-                put(js, slot, g, sum, x);
+                put(js, slot, g, m[g] + kPaDown, sum, x);
                 continue;
             }
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -918,7 +924,7 @@ struct TileF32 {
                     *reinterpret_cast<float4*>(dst + 64 * i + 4 * hl) =
                         make_float4(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
             }
-            if (lane == 0) note(p, b, h, g, m[g], sum);
+            if (lane == 0) note(p, b, h, g, m[g] + kPaDown, sum);
         }
     }
 };

@@ -91,3 +91,29 @@ def test_infinite_values_in_rows_that_count(kind, headroom):
     for b in range(len(lens)):
         c.vrows[b][..., 1:5] = 0
     check_all(c, q, out, lse)
+
+
+@pytest.mark.parametrize("headroom", [0, 16384])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_values_near_the_types_largest(kind, headroom):
+    """The result lies between the values, so it is finite where they are: whatever the sums are before
+    they are normalised.  Scores climb by less than the step at which a running base moves, and many rows
+    share the weight."""
+    lens = [5, 900, 20000]
+    c = Paged(kind, lens, 1, 64, 16, seed=53)
+    most = torch.finfo(KINDS[kind][0]).max
+    for b, n in enumerate(lens):
+        c.vrows[b][:, :, 0], c.vrows[b][:, :, 1] = 0.99 * most, -0.99 * most
+        c.vrows[b][:, :, 2] = (torch.rand((1, n), generator=torch.Generator().manual_seed(n)) * most).to(c.v.dtype)
+        c.krows[b].zero_()
+        c.krows[b][:, 16:, 0] = 5.0                            # 2^7 above the first rows''
+        for p in range(-(-n // 16)):
+            hi = min(16, n - 16 * p)
+            for pool, rows in ((c.k, c.krows), (c.v, c.vrows)):
+                pool[int(c.table[b, p]), 0, :hi] = rows[b][0, 16 * p:16 * p + hi].cuda()
+    q = torch.zeros((3, 2, 64), device="cuda").to(KINDS[kind][0])
+    q[..., 0] = 1.0
+    out, lse = torch.empty_like(q), torch.empty((3, 2), device="cuda")
+    skv.paged_attention(q, c.k, c.v, wider(c.table, headroom, 16), c.lens, out, lse, scale=7 * math.log(2) / 5)
+    assert out.isfinite().all()
+    check_all(c, q, out, lse, 7 * math.log(2) / 5)
