@@ -369,6 +369,9 @@ struct Pieces {
     }
 };
 
+// The product that scores -infinity: what is kept for an absent row, which adds no weight.
+__device__ __forceinline__ float no_product(const PagedAttnParams& p) { return copysignf(CUDART_INF_F, -p.scale_log2); }
+
 // Where the products q.k of a tile's rows are kept for the weights, [row][Gp]: nowhere, in the
 // workspace, or in the warp's part of shared memory.
 struct KeepNone {
@@ -463,12 +466,13 @@ struct TileTC {
                                          const float (&s)[4]) {
         const int r = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
         if (2 * c >= p.G) return;
+        const float none = no_product(p);
         if (row + r < end)
             *reinterpret_cast<float2*>(z + r * p.Gp + 2 * c) =
-                ida >= 0 ? make_float2(s[0], s[1]) : make_float2(-CUDART_INF_F, -CUDART_INF_F);
+                ida >= 0 ? make_float2(s[0], s[1]) : make_float2(none, none);
         if (row + 8 + r < end)
             *reinterpret_cast<float2*>(z + (8 + r) * p.Gp + 2 * c) =
-                idb >= 0 ? make_float2(s[2], s[3]) : make_float2(-CUDART_INF_F, -CUDART_INF_F);
+                idb >= 0 ? make_float2(s[2], s[3]) : make_float2(none, none);
     }
     // probabilities against the running base; returns P^T as the second product's operand, b, and what
     // its rounding to bf16 left, r
@@ -798,7 +802,7 @@ struct TileF32 {
                 }
                 s[g] = transpose_reduce8(a, hl);
                 if (Keep::on && (hl & 1) == 0 && mine + (hl >> 1) < end && g < p.G)
-                    z(b, h, mine + (hl >> 1))[g] = in ? s[g] : -CUDART_INF_F;
+                    z(b, h, mine + (hl >> 1))[g] = in ? s[g] : no_product(p);
                 up = up || (in && s[g] * p.scale_log2 > m[g] + kPaSlack);
             }
             if (!kAhead) load(vb, p.c.v_page, p.c.v_row, mask, mine, end, id, v);
@@ -1162,12 +1166,12 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid
         __syncthreads();
         const float* in = p.weight + u * p.row_pitch;
         float* out = p.weight_out + u * p.row_pitch;
+        const float none = no_product(p);
         for (int i = piece_row + lane; i < piece_end; i += 32) {
             float sum = 0.f;
             for (int g = 0; g < p.G; ++g) {
                 const float x = my_z[(i - piece_row) * p.Gp + g];
-                // an absent row's product is -inf and adds nothing
-                if (x != -CUDART_INF_F) sum += exp2_fast(fmaf(x, p.scale_log2, -s_stat[g].x)) * s_stat[g].y;
+                if (x != none) sum += exp2_fast(fmaf(x, p.scale_log2, -s_stat[g].x)) * s_stat[g].y;
             }
             out[i] = in[i] + sum;
         }
@@ -1322,6 +1326,7 @@ __device__ __forceinline__ void weigh_rows(const PagedAttnParams& p, int64_t u, 
     const float* z = p.z + u * p.c.cap * Gp;
     const float* in = p.weight + u * p.row_pitch;
     float* out = p.weight_out + u * p.row_pitch;
+    const float none = no_product(p);
     float base[Gp], inv[Gp];
 #pragma unroll
     for (int g = 0; g < Gp; ++g) {
@@ -1349,8 +1354,7 @@ __device__ __forceinline__ void weigh_rows(const PagedAttnParams& p, int64_t u, 
 #pragma unroll
             for (int g = 0; g < Gp; ++g) {
                 const float v = g & 1 ? x[r][g / 2].y : x[r][g / 2].x;
-                // an absent row's product is -inf and adds nothing
-                if (g < p.G && v != -CUDART_INF_F) sum += exp2_fast(fmaf(v, p.scale_log2, -base[g])) * inv[g];
+                if (g < p.G && v != none) sum += exp2_fast(fmaf(v, p.scale_log2, -base[g])) * inv[g];
             }
             out[i] = w[r] + sum;
         }

@@ -9,7 +9,7 @@ import torch
 import sparse_kv_cache_gb300 as skv
 from oracle import paged_ref as ref
 from tests.paged_harness import KINDS, Paged, f64
-from tests.test_gpu_paged import U, UP, check_all, queries
+from tests.test_gpu_paged import U, UP, check_all, check_attention, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +117,21 @@ def test_values_near_the_types_largest(kind, headroom):
     skv.paged_attention(q, c.k, c.v, wider(c.table, headroom, 16), c.lens, out, lse, scale=7 * math.log(2) / 5)
     assert out.isfinite().all()
     check_all(c, q, out, lse, 7 * math.log(2) / 5)
+
+
+@pytest.mark.parametrize("headroom", [0, 16384])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_rows_that_a_negative_scale_brings_to_minus_infinity(kind, headroom):
+    """Keys of +infinity under a negative scale score -infinity: such rows weigh nothing, one or all."""
+    c = Paged(kind, [70, 50], 1, 64, 16, seed=54)
+    q = queries(c, 2, 55).abs() + 0.5
+    c.k[c.table[0, :5].long()] = math.inf
+    c.k[int(c.table[1, 1]), 0, 3] = math.inf
+    w = torch.rand((2, 1, c.rows + headroom), device="cuda")
+    out, lse, got = torch.full_like(q, 9.0), torch.zeros((2, 2), device="cuda"), torch.zeros_like(w)
+    skv.paged_attention(q, c.k, c.v, wider(c.table, headroom, 16), c.lens, out, lse, w, got, scale=-0.125)
+    assert (out[0] == 0).all() and (lse[0] == -math.inf).all() and torch.equal(got[0, :, :70], w[0, :, :70])
+    live = np.arange(50) != 19
+    check_attention(kind, f64(q[1]), f64(out[1]), f64(lse[1]), f64(c.krows[1][0])[live], f64(c.vrows[1][0])[live], -0.125,
+                    f64(w[1, 0, :50])[live], f64(got[1, 0, :50])[live])
+    assert got[1, 0, 19] == w[1, 0, 19]
