@@ -571,8 +571,9 @@ int shadowkv_paged_attention(const skv_paged_attention_args* args, skv_stream st
  * place) or buffers of their own, which then hold the rows below lens_out[b]
  * (rows behind are left as they are).  The key and value pools are changed in
  * place; the rows at budget and behind stay as they were.  A sequence that
- * gives up rows must not share its pages.  A bad page sets the error word, and
- * the rows in it are not moved.
+ * gives up rows must not share its pages.  A bad page sets the error word; a
+ * row that would move out of or into one does not, and its place keeps the key,
+ * value, weight and position of the row that was given up there.
  */
 typedef struct {
     skv_paged_cache cache;

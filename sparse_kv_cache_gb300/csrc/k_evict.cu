@@ -150,9 +150,12 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, int u, int moves
             } else {
                 pd = page_of(p.c, b, d, g_err, 722);
                 ps = page_of(p.c, b, s, g_err, 723);
-                p.weight_out[base + d] = __ldg(p.weight + base + s);
-                p.position_out[base + d] = __ldg(p.position + base + s);
-                if (ps < 0) pd = -1;
+                if (pd >= 0 && ps >= 0) {
+                    p.weight_out[base + d] = __ldg(p.weight + base + s);
+                    p.position_out[base + d] = __ldg(p.position + base + s);
+                } else {       // the place keeps the row that was given up there
+                    pd = -1;
+                }
                 d &= mask;
                 s &= mask;
             }

@@ -135,3 +135,41 @@ def test_rows_that_a_negative_scale_brings_to_minus_infinity(kind, headroom):
     check_attention(kind, f64(q[1]), f64(out[1]), f64(lse[1]), f64(c.krows[1][0])[live], f64(c.vrows[1][0])[live], -0.125,
                     f64(w[1, 0, :50])[live], f64(got[1, 0, :50])[live])
     assert got[1, 0, 19] == w[1, 0, 19]
+
+
+# ------------------------------------------------------------------ bad pages in an eviction
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("budget,n", [(32, 64), (700, 1500)])          # moved by the search's own CTAs, by a second kernel
+def test_a_row_that_cannot_move_leaves_the_place_as_it_was(budget, n, in_place):
+    """A kept row in a bad page, or one whose new place is in one: key, value, weight and position of the
+    place all stay those of the row that was given up there."""
+    c = Paged("bf16", [n, n], 2, 64, 16, seed=58)
+    g = torch.Generator().manual_seed(59)
+    weight = torch.rand((2, 2, c.rows), generator=g).cuda()
+    position = torch.stack([torch.randperm(c.rows, generator=g) for _ in range(4)]).view(2, 2, -1).to(torch.int32).cuda()
+    good = c.table.clone()
+    c.table[0, -1], c.table[1, 1] = c.k.shape[0] + 3, -2          # the last page; a page below the budget
+    want_k, want_v, want_w, want_p = (x.clone().cpu() for x in (c.k, c.v, weight, position))
+    if not in_place:
+        want_w[:, :, budget:], want_p[:, :, budget:] = -3, -3
+    t, stuck = good.cpu(), 0
+    for b in range(2):
+        for h in range(2):
+            kept = ref.kept_rows(f64(weight[b, h, :n]), position[b, h, :n].cpu().numpy(), budget, 0, 0)
+            for to, of in ref.moves(kept, budget):
+                if of // 16 == c.table.shape[1] - 1 if b == 0 else to // 16 == 1:
+                    stuck += 1
+                    continue
+                want_w[b, h, to], want_p[b, h, to] = weight[b, h, of].cpu(), position[b, h, of].cpu()
+                for pool in (want_k, want_v):
+                    pool[int(t[b, to // 16]), h, to % 16] = pool[int(t[b, of // 16]), h, of % 16]
+    assert stuck > 4
+    outs = {} if in_place else dict(weight_out=torch.full_like(weight, -3), position_out=torch.full_like(position, -3),
+                                    lens_out=torch.empty_like(c.lens))
+    skv.paged_evict(c.k, c.v, c.table, c.lens, weight, position, budget, **outs)
+    assert skv.paged_status() == -5
+    assert torch.equal(c.k.cpu().view(torch.int16), want_k.view(torch.int16))
+    assert torch.equal(c.v.cpu().view(torch.int16), want_v.view(torch.int16))
+    assert torch.equal(outs.get("weight_out", weight).cpu(), want_w)
+    assert torch.equal(outs.get("position_out", position).cpu(), want_p)
