@@ -65,10 +65,10 @@ __device__ __forceinline__ void sync_all(int ranks) {
 // rows, and a sequence's room is one too, so rows that are read beyond its last lie in its room.
 struct Rows8 { float4 w0, w1; int4 p0, p1; };
 __device__ __forceinline__ void load_rows(const float* w, const int32_t* p, int s, Rows8& r) {
-    r.w0 = __ldg(reinterpret_cast<const float4*>(w + s));
-    r.w1 = __ldg(reinterpret_cast<const float4*>(w + s) + 1);
-    r.p0 = __ldg(reinterpret_cast<const int4*>(p + s));
-    r.p1 = __ldg(reinterpret_cast<const int4*>(p + s) + 1);
+    r.w0 = reinterpret_cast<const float4*>(w + s)[0];
+    r.w1 = reinterpret_cast<const float4*>(w + s)[1];
+    r.p0 = reinterpret_cast<const int4*>(p + s)[0];
+    r.p1 = reinterpret_cast<const int4*>(p + s)[1];
 }
 // Their keys: the largest for a protected row.
 struct Protect {
@@ -151,8 +151,8 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, int u, int moves
                 pd = page_of(p.c, b, d, g_err, 722);
                 ps = page_of(p.c, b, s, g_err, 723);
                 if (pd >= 0 && ps >= 0) {
-                    p.weight_out[base + d] = __ldg(p.weight + base + s);
-                    p.position_out[base + d] = __ldg(p.position + base + s);
+                    p.weight_out[base + d] = p.weight[base + s];
+                    p.position_out[base + d] = p.position[base + s];
                 } else {       // the place keeps the row that was given up there
                     pd = -1;
                 }
@@ -176,7 +176,7 @@ __device__ __forceinline__ void move_rows(const EvictParams& p, int u, int moves
                     const int to_page = __shfl_sync(0xffffffffu, pd, j0 + j), of_page = __shfl_sync(0xffffffffu, ps, j0 + j);
                     const int to_row = __shfl_sync(0xffffffffu, d, j0 + j), of_row = __shfl_sync(0xffffffffu, s, j0 + j);
                     dst[j] = to_page >= 0 && w < words ? to_page * page + to_row * row : -1;
-                    if (dst[j] >= 0) x[j] = __ldg(reinterpret_cast<const uint4*>(pool + of_page * page + of_row * row));
+                    if (dst[j] >= 0) x[j] = *reinterpret_cast<const uint4*>(pool + of_page * page + of_row * row);
                 }
 #pragma unroll
                 for (int j = 0; j < kFlight; ++j)
@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_evict(const __gri
             const int s = r0 + k * kEvStep + 8 * lane;
             pos[k][0] = pos[k][1] = make_int4(INT_MIN, INT_MIN, INT_MIN, INT_MIN);
             if (s < hi) {
-                pos[k][0] = __ldg(reinterpret_cast<const int4*>(p_in + s));
-                pos[k][1] = __ldg(reinterpret_cast<const int4*>(p_in + s) + 1);
+                pos[k][0] = reinterpret_cast<const int4*>(p_in + s)[0];
+                pos[k][1] = reinterpret_cast<const int4*>(p_in + s)[1];
             }
         }
 #pragma unroll
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) k_evict(const __gri
                 my_list = reinterpret_cast<uint32_t*>(my + per) - listed;
                 for (int e = lane; e < listed; e += 32) {
                     const int row = lo + my[e];
-                    my_list[e] = pr.key(__ldg(w_in + row), __ldg(p_in + row));
+                    my_list[e] = pr.key(w_in[row], p_in[row]);
                 }
             } else {            // they crowd in this warp's rows: its keys again
                 listed = -1;

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kNrThreads, kOcc) k_norm_rope(const __grid_con
     const int t0 = blockIdx.x * per_cta, nt = min(per_cta, p.tokens - t0);
     const int t = tid / kLanes / p.groups, g = tid / kLanes % p.groups;
     const int64_t tok = t0 + t;
-    const int pos = t < nt ? __ldg(p.positions + tok) : -1;
+    const int pos = t < nt ? p.positions[tok] : -1;
     const bool cache = p.c.k != nullptr;
     const int H = p.c.H, n_kv = cache ? 2 * H : H;
     const int q_slots = (p.nq + p.groups - 1) / p.groups, slots = q_slots + (n_kv + p.groups - 1) / p.groups;
@@ -93,8 +93,8 @@ __global__ void __launch_bounds__(kNrThreads, kOcc) k_norm_rope(const __grid_con
     // where the token's rows go in the cache: asked for early, needed late
     int seq = -1, row = 0;
     if (cache && pos >= 0) {
-        seq = __ldg(p.seq + tok);
-        row = __ldg(p.index + tok);
+        seq = p.seq[tok];
+        row = p.index[tok];
     }
     float cs[8], sn[8];
     int page = -1;
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(kNrThreads, kOcc) k_norm_rope(const __grid_con
         if (s0 == 0) {     // the angles, while the first rows are on their way
             for (int i = tid; i < nt * half; i += kNrThreads) {
                 const int a = i / half, f = i % half;
-                const uint64_t turned = static_cast<uint64_t>(static_cast<int64_t>(__ldg(p.positions + t0 + a))) * p.turn[f];
+                const uint64_t turned = static_cast<uint64_t>(static_cast<int64_t>(p.positions[t0 + a])) * p.turn[f];
                 float y, x;
                 sincospif(static_cast<float>(static_cast<int32_t>(turned >> 32)) * 0x1p-31f, &y, &x);
                 s_cos[a * (D / 2) + f] = x;

@@ -61,7 +61,7 @@ __device__ __forceinline__ uint4 ld_stream(const void* p, bool in) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
         "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        "@p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
         : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
         : "l"(p), "r"(static_cast<int>(in)));
     return v;
@@ -70,7 +70,7 @@ __device__ __forceinline__ uint2 ld_stream8(const void* p, bool in) {
     uint2 v;
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n\t}"
+        "@p ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];\n\t}"
         : "=&r"(v.x), "=&r"(v.y)
         : "l"(p), "r"(static_cast<int>(in)));
     return v;
@@ -408,7 +408,7 @@ struct TileTC {
         const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + b * p.q_seq + (h * p.G + g) * p.q_head + c * 8;
 #pragma unroll
         for (int j = 0; j < kKV; ++j)
-            q[j] = g < p.G ? __ldg(reinterpret_cast<const uint4*>(src + 32 * j)) : make_uint4(0, 0, 0, 0);
+            q[j] = g < p.G ? *reinterpret_cast<const uint4*>(src + 32 * j) : make_uint4(0, 0, 0, 0);
     }
     __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -727,7 +727,7 @@ struct TileF32 {
         __syncwarp();
         for (int i = threadIdx.x & 31; i < G * D; i += 32) {
             const int g = i / D;
-            s_q[g * (D + 4) + i % D] = g < p.G ? __ldg(static_cast<const float*>(p.q) + b * p.q_seq + (h * p.G + g) * p.q_head + i % D) : 0.f;
+            s_q[g * (D + 4) + i % D] = g < p.G ? static_cast<const float*>(p.q)[b * p.q_seq + (h * p.G + g) * p.q_head + i % D] : 0.f;
         }
         __syncwarp();
         sq = s_q;

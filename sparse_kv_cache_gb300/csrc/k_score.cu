@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(320, 1) k_score_f8(const __grid_constant__ CUt
 // with max|q| * 2^s < 2^14), then x = q * 2^s gives t1 = e5m2(x), t2 = e5m2(x - t1),
 // t3 = e5m2(x - t1 - t2) into rows jt*G + g of qt[u], and qinv[u][g] = 2^-s.
 template <int G>
-__global__ void __launch_bounds__(32 * G) k_qsplit(const __nv_bfloat16* __restrict__ q, uint8_t* __restrict__ qt,
+__global__ void __launch_bounds__(32 * G) k_qsplit(const __nv_bfloat16* q, uint8_t* __restrict__ qt,
                                                    float* __restrict__ qinv) {
     pdl_wait();
     pdl_trigger();

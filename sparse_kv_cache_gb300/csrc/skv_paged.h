@@ -108,6 +108,8 @@ inline cudaError_t launch_first(void (*k)(KArgs...), dim3 grid, int block, size_
     return cudaLaunchKernelEx(&cfg, k, static_cast<Args&&>(args)...);
 }
 // Its first lines: the kernels after it may be brought in once it knows that those before it are done.
+// So a kernel is on the device while those before it write, and reads what they wrote by coherent loads only:
+// the non-coherent ones are for what nothing writes as long as their kernel runs.
 __device__ __forceinline__ void begin_call() {
     pdl_wait();
     pdl_trigger();
@@ -126,7 +128,7 @@ __device__ __forceinline__ int rows_of(const PagedView& c, int b, int* err, int 
 }
 // page of row i of sequence b, or -1 (and the error word) if its id is out of range
 __device__ __forceinline__ int page_of(const PagedView& c, int b, int i, int* err, int where) {
-    const int id = __ldg(c.table + b * c.table_seq + (i >> c.lg));
+    const int id = c.table[b * c.table_seq + (i >> c.lg)];
     if (id < 0 || id >= c.n_pages) {
         set_err(err, DEV_ERR_BOUNDS, where);
         return -1;
