@@ -592,10 +592,12 @@ int64_t shadowkv_paged_evict_workspace(const skv_paged_evict_args* args);   /* b
 int shadowkv_paged_evict(const skv_paged_evict_args* args, skv_stream stream);
 
 /*
- * Status of the paged calls made so far on the current device: synchronises
- * `stream`, reads the error words and clears them.  Returns SKV_OK,
- * SKV_ERR_DEVICE_BOUNDS (a length, index or page id was out of range; its
- * access was skipped), or SKV_ERR_CUDA.  Not for use during stream capture.
+ * Status of the paged calls on the current device, of all streams: waits for
+ * `stream`, then takes the error words and clears them in one step.  A call that
+ * still runs on another stream is in it as far as it has come; what it sets
+ * later is in the next status.  Returns SKV_OK, SKV_ERR_DEVICE_BOUNDS (a length,
+ * index or page id was out of range; its access was skipped), or SKV_ERR_CUDA.
+ * Not for use during stream capture.
  */
 int shadowkv_paged_status(skv_stream stream);
 

@@ -512,7 +512,8 @@ def paged_evict(k_cache, v_cache, table, lens, weight, position, budget: int, re
 
 
 def paged_status(stream=None) -> int:
-    """shadowkv_paged_status: the kept status of the paged calls' kernels, cleared on read."""
+    """shadowkv_paged_status: waits for the stream, then the kept status of the paged calls' kernels of
+    all streams as far as they have come, cleared on read."""
     return load().shadowkv_paged_status(_stream(stream))
 
 

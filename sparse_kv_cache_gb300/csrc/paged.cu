@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <mutex>
 
 #include "skv_common.cuh"
 #include "skv_internal.h"
@@ -187,6 +188,17 @@ int evict_space(const skv_paged_evict_args* a, EvictSpace* w) {
     return SKV_OK;
 }
 
+// ------------------------------------------------------------------ status
+
+// The error words are shared by all streams: reading and clearing is one step, so that nothing another
+// stream's kernel sets in between is lost.
+__device__ int g_taken;
+std::mutex g_taking;       // g_taken is one call's at a time
+__global__ void k_take_status(int* a, int* b, int* c) {
+    const int x = atomicExch(a, 0), y = atomicExch(b, 0), z = atomicExch(c, 0);
+    g_taken = x ? x : y ? y : z;
+}
+
 }  // namespace
 
 extern "C" {
@@ -350,22 +362,21 @@ int shadowkv_paged_evict(const skv_paged_evict_args* a, skv_stream stream) {
 }
 
 int shadowkv_paged_status(skv_stream stream) {
-    int code = SKV_OK;
-    if (cudaStreamSynchronize(stream) != cudaSuccess) {
+    std::lock_guard<std::mutex> mine(g_taking);
+    int *norm = nullptr, *attn = nullptr, *evict = nullptr, taken = 0;
+    if (cudaStreamSynchronize(stream) != cudaSuccess || norm_rope_err(&norm) != cudaSuccess ||
+        paged_attn_err(&attn) != cudaSuccess || evict_err(&evict) != cudaSuccess) {
         cudaGetLastError();
         return SKV_ERR_CUDA;
     }
-    for (auto word : {norm_rope_err, paged_attn_err, evict_err}) {
-        int* w = nullptr;
-        int e[2] = {0, 0};
-        if (word(&w) != cudaSuccess || cudaMemcpyAsync(e, w, sizeof(e), cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
-            cudaMemsetAsync(w, 0, sizeof(e), stream) != cudaSuccess || cudaStreamSynchronize(stream) != cudaSuccess) {
-            cudaGetLastError();
-            return SKV_ERR_CUDA;
-        }
-        if (e[0] != 0) code = SKV_ERR_DEVICE_BOUNDS;
+    k_take_status<<<1, 1, 0, stream>>>(norm, attn, evict);
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyFromSymbolAsync(&taken, g_taken, sizeof(taken), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+        cudaStreamSynchronize(stream) != cudaSuccess) {
+        cudaGetLastError();
+        return SKV_ERR_CUDA;
     }
-    return code;
+    return taken ? SKV_ERR_DEVICE_BOUNDS : SKV_OK;
 }
 
 }  // extern "C"

@@ -173,3 +173,27 @@ def test_a_row_that_cannot_move_leaves_the_place_as_it_was(budget, n, in_place):
     assert torch.equal(c.v.cpu().view(torch.int16), want_v.view(torch.int16))
     assert torch.equal(outs.get("weight_out", weight).cpu(), want_w)
     assert torch.equal(outs.get("position_out", position).cpu(), want_p)
+
+
+# ------------------------------------------------------------------ errors of several streams
+
+def test_no_error_is_lost_between_streams():
+    """Bad calls on one stream while another's status is read all the time: every one is reported."""
+    c = Paged("bf16", [64], 1, 64, 16, seed=60)
+    q, bad = queries(c, 1), c.table.clone()
+    bad[0, 2] = -1
+    out = torch.empty_like(q)
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+    skv.paged_attention(q, c.k, c.v, bad, c.lens, out)
+    assert skv.paged_status() == -5
+    for i in range(3000):
+        seen, done = 0, torch.cuda.Event()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(2000 + i * 7919 % 160000)        # up to 80 us: a status takes 50
+            skv.paged_attention(q, c.k, c.v, bad, c.lens, out, stream=side)
+            done.record()
+        over = False
+        while not over:
+            over = done.query()          # (asked before the status is: what is done then has to be in it)
+            seen += skv.paged_status(main) != 0
+        assert seen, f"call {i} was not reported"
