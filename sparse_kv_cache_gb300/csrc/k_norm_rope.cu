@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kNrThreads, kOcc) k_norm_rope(const __grid_con
         seq = p.seq[tok];
         row = p.index[tok];
     }
-    float cs[8], sn[8];
+    float cs[8] = {}, sn[8] = {};
     int page = -1;
     for (int s0 = 0; s0 < slots; s0 += kDeep) {       // uniform: every lane takes part in the shuffles
         // (asked for before the position is known: a padding token's rows are there to be read too)
@@ -130,9 +130,6 @@ __global__ void __launch_bounds__(kNrThreads, kOcc) k_norm_rope(const __grid_con
             if (turns) {
                 load8(s_cos + t * (D / 2) + 8 * c, cs);
                 load8(s_sin + t * (D / 2) + 8 * c, sn);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) cs[e] = 1.f, sn[e] = 0.f;
             }
         }
 #pragma unroll
@@ -162,11 +159,13 @@ __global__ void __launch_bounds__(kNrThreads, kOcc) k_norm_rope(const __grid_con
                     z[e] *= rs * wz[e];
                 }
             }
+            if (turns) {     // (a turn by nothing would not do: an infinite partner times a sine of 0 is NaN)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = a[e], y = z[e];
-                a[e] = fmaf(x, cs[e], -(y * sn[e]));
-                z[e] = fmaf(y, cs[e], x * sn[e]);
+                for (int e = 0; e < 8; ++e) {
+                    const float x = a[e], y = z[e];
+                    a[e] = fmaf(x, cs[e], -(y * sn[e]));
+                    z[e] = fmaf(y, cs[e], x * sn[e]);
+                }
             }
             if (!live) continue;
             if (is_q) {

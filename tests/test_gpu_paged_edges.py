@@ -9,7 +9,7 @@ import torch
 import sparse_kv_cache_gb300 as skv
 from oracle import paged_ref as ref
 from tests.paged_harness import KINDS, Paged, f64
-from tests.test_gpu_paged import U, UP, check_all, check_attention, queries
+from tests.test_gpu_paged import U, UP, check_all, check_attention, check_norm, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -197,3 +197,28 @@ def test_no_error_is_lost_between_streams():
             over = done.query()          # (asked before the status is: what is done then has to be in it)
             seen += skv.paged_status(main) != 0
         assert seen, f"call {i} was not reported"
+
+
+# ------------------------------------------------------------------ dimensions that are not turned
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
+def test_dimensions_beyond_the_rotation_pass_through(kind):
+    """Bit for bit where there is no norm, whatever their neighbours hold."""
+    wide, g = KINDS[kind][0], torch.Generator().manual_seed(61)
+    x = torch.randn((40, 3, 128), generator=g)
+    pick = torch.rand(x.shape, generator=g)
+    for lo, v in ((0.0, math.inf), (0.1, -math.inf), (0.2, 0.0), (0.3, -0.0), (0.4, 3e38)):
+        x[(pick > lo) & (pick < lo + 0.1)] = v
+    x[..., :64] = torch.randn((40, 3, 64), generator=g)
+    x = x.to(wide).cuda()
+    pos = torch.randint(0, 1 << 20, (40,), generator=g).to(torch.int32).cuda()
+    c = Paged(kind, [0], 3, 128, 16, seed=62, cap=48)
+    q_out, k_out = torch.empty_like(x), torch.empty_like(x)
+    at = torch.arange(40, dtype=torch.int32, device="cuda")
+    skv.qk_norm_rope(x, x, pos, q_out, k_out, rotary_dim=64, v=x, k_cache=c.k, v_cache=c.v, table=c.table,
+                     seq=torch.zeros_like(at), index=at)
+    bits = lambda t: t[..., 64:].contiguous().view(torch.uint8)  # noqa: E731
+    held = c.k[c.table[0, at.long() // 16].long(), :, at.long() % 16]
+    for out in (q_out, k_out, held):
+        assert torch.equal(bits(out), bits(x))
+    check_norm(x[..., :64], None, pos.cpu(), q_out[..., :64], kind, 500000.0, 64, 1e-6)
