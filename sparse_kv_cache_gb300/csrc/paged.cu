@@ -93,6 +93,13 @@ int check_cache(const skv_paged_cache& c, bool written) {
     return SKV_OK;
 }
 
+// every one of the pointers, where set, begins at an element of four bytes
+int check_words(std::initializer_list<const void*> ptrs) {
+    for (const void* p : ptrs)
+        if (reinterpret_cast<uintptr_t>(p) & 3) return SKV_ERR_INVALID;
+    return SKV_OK;
+}
+
 // every one of the pointers that is set has to be device memory of the current device
 int check_memory(std::initializer_list<const void*> ptrs, int dev) {
     for (const void* p : ptrs)
@@ -237,6 +244,9 @@ int shadowkv_qk_norm_rope(const skv_qk_norm_rope_args* a, skv_stream stream) {
         if (!x.p || !aligned16(x.p) || !good_stride(x.tok, es) || !good_stride(x.head, es)) return SKV_ERR_INVALID;
         if (x.written && !apart(a->tokens, x.tok, x.heads, x.head, c.head_dim)) return SKV_ERR_INVALID;
     }
+    if (int rc = check_words({a->positions})) return rc;
+    if (cache)
+        if (int rc = check_words({c.table, a->seq, a->index, a->row_position, a->row_weight})) return rc;
     Device dev;
     if (int rc = device(&dev)) return rc;
     if (int rc = check_memory({a->positions, a->k, a->n_q_heads ? a->q : nullptr, a->n_q_heads ? a->q_out : nullptr, a->k_out,
@@ -291,6 +301,7 @@ int shadowkv_paged_attention(const skv_paged_attention_args* a, skv_stream strea
     if (a->workspace_bytes < w.bytes) return SKV_ERR_INVALID;
     if ((a->weight != nullptr) != (a->weight_out != nullptr)) return SKV_ERR_INVALID;
     if (a->weight && a->row_pitch < static_cast<int64_t>(c.max_pages) * c.page_size) return SKV_ERR_INVALID;
+    if (int rc = check_words({c.table, c.lens, a->lse, a->weight, a->weight_out})) return rc;
     Device dev;
     if (int rc = device(&dev)) return rc;
     if (int rc = check_memory({c.k, c.v, c.table, c.lens, a->q, a->out, a->lse, a->weight, a->weight_out, a->workspace}, dev.id))
@@ -338,6 +349,7 @@ int shadowkv_paged_evict(const skv_paged_evict_args* a, skv_stream stream) {
                           static_cast<const void*>(a->weight_out), static_cast<const void*>(a->position_out)})
         if (!aligned16(q)) return SKV_ERR_INVALID;
     if (!aligned16(a->workspace) || a->workspace_bytes < w.bytes) return SKV_ERR_INVALID;
+    if (int rc = check_words({c.table, c.lens, a->lens_out})) return rc;
     Device dev;
     if (int rc = device(&dev)) return rc;
     if (int rc = check_memory({c.k, c.v, c.table, c.lens, a->weight, a->position, a->weight_out, a->position_out, a->lens_out,
