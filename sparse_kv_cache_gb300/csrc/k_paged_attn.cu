@@ -1402,6 +1402,13 @@ static bool allow(Kernel kernel, int ranks, int smem) {
     return (ranks <= 8 || cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) &&
            (!smem || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, z_bytes(kOneWaveTiles, 8)) == cudaSuccess);
 }
+// shared memory of an SM that holds kOcc CTAs of a cluster form's kernel, and the split to ask for
+template <int D, int G, int kOcc>
+constexpr int shared_bytes(int smem) { return kOcc * (static_cast<int>(sizeof(JoinSmem<D, G>) + G * sizeof(float2)) + 1024 + smem); }
+constexpr int carve_of(int bytes) {
+    const int percent = (bytes * 100 + kSmShared - 1) / kSmShared;
+    return percent < kCarve ? kCarve : percent > 100 ? 100 : percent;
+}
 template <class Tile, int D, bool kF32, int G, int kOcc, bool kKeep>
 static int clusters_held(int ranks) {
     static std::atomic<int> known[17];
@@ -1413,12 +1420,14 @@ static int clusters_held(int ranks) {
     cfg.gridDim = dim3(ranks);
     cfg.blockDim = dim3(kPaThreads);
     cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = ranks;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+    attr[1].val.sharedMemCarveout = carve_of(shared_bytes<D, G, kOcc>(smem));
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     if (!allow(kernel, ranks, smem) || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
         cudaGetLastError();
         return 0;
@@ -1439,6 +1448,11 @@ static int clusters_held(int ranks) {
 // 28.2, and 37.7 against 44.7 of 1000 each.  Units of one length lose where a few are left over: 460 of 750
 // rows 41.6 against 36.5, 912 57.4 against 59.8.  fp32, 600 ragged ones of 250 rows 27.0 against 33.5; 912
 // of exactly 250 54.4 against 44.7.)
+// The products that are kept for the weights take shared memory, and with it an SM's L1 through which the
+// loads go: a unit has a CTA only where that leaves kLeastL1 of it.  (452 units with eight heads of 128
+// dimensions, weighed, in CTAs against the general form: of 600 rows, 181 KB an SM, 29.4 us against 43.3; of
+// 1000, 206 KB, 57.4 against 60.9, but 440 ragged ones 47.3 against 38.9.)
+constexpr int kLeastL1 = 32 << 10;
 template <class Tile, int D, bool kF32, int G, int kOcc, bool kKeep>
 static int cluster_ranks(const PagedAttnParams& p, int ncta) {
     const int64_t U = static_cast<int64_t>(p.c.batch) * p.c.H, tiles = (p.c.cap + kPaTile - 1) / kPaTile;
@@ -1448,7 +1462,9 @@ static int cluster_ranks(const PagedAttnParams& p, int ncta) {
         ranks *= 2;
     if (ranks == 1) {
         const int tiles_most = U <= ncta && 4 * U >= 3 * static_cast<int64_t>(ncta) ? kOneWaveTiles : kUnitTiles;
-        return U <= (kF32 ? 2 : 3) * static_cast<int64_t>(ncta) && cluster_tiles(p.c.cap, 1) <= tiles_most ? 1 : 0;
+        const int mine = cluster_tiles(p.c.cap, 1);
+        if (U > (kF32 ? 2 : 3) * static_cast<int64_t>(ncta) || mine > tiles_most) return 0;
+        return !kKeep || shared_bytes<D, G, kOcc>(z_bytes(mine, p.Gp)) <= kSmShared - kLeastL1 ? 1 : 0;
     }
     return cluster_tiles(p.c.cap, ranks) <= kClusterTiles ? ranks : 0;
 }
@@ -1458,7 +1474,8 @@ static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
     auto kernel = k_paged_cluster<Tile, D, kF32, G, kOcc, kKeep>;
     const int smem = kKeep ? z_bytes(cluster_tiles(p.c.cap, ranks), p.Gp) : 0;
     if (!allow(kernel, ranks, smem)) return -1;
-    return launch_first(kernel, static_cast<unsigned>(p.c.batch) * p.c.H * ranks, kPaThreads, smem, ranks, kCarve, s, p, ranks) ==
+    const int carve = carve_of(shared_bytes<D, G, kOcc>(smem));
+    return launch_first(kernel, static_cast<unsigned>(p.c.batch) * p.c.H * ranks, kPaThreads, smem, ranks, carve, s, p, ranks) ==
                    cudaSuccess
                ? 0
                : -1;

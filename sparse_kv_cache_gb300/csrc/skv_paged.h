@@ -81,7 +81,8 @@ cudaError_t evict_err(int** p);
 // that follow each other ask for the same one, or the later one finds room for fewer CTAs than it needs and
 // runs in two waves (the attention after its merge kernel, 300 units of 1000 rows with e5m2 values: 36 us
 // against 28).
-constexpr int kCarve = 58;        // 132 KB: three CTAs of the attention
+constexpr int kCarve = 58;        // room for three CTAs of the attention
+constexpr int kSmShared = 228 << 10;      // all that can be shared memory
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_first(void (*k)(KArgs...), dim3 grid, int block, size_t smem, int ranks, int carve, cudaStream_t s,
                                 Args&&... args) {

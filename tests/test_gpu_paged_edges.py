@@ -137,6 +137,24 @@ def test_rows_that_a_negative_scale_brings_to_minus_infinity(kind, headroom):
     assert got[1, 0, 19] == w[1, 0, 19]
 
 
+# ------------------------------------------------------------------ a CTA per unit with its products kept
+
+@pytest.mark.parametrize("kind,G,d", [("bf16", 4, 128), ("bf16", 6, 128), ("bf16", 8, 128), ("fp8", 8, 128), ("bf16", 7, 64),
+                                      ("f32", 8, 128), ("f32", 4, 64)])
+def test_weights_of_as_many_units_as_fill_the_device(kind, G, d):
+    """Rooms of 769 to 1024 rows, just as many units as CTAs: the most that a warp keeps in shared memory."""
+    per = {"f32": 2}.get(kind, 3 if d == 128 else 4)
+    units = torch.cuda.get_device_properties(0).multi_processor_count * per - 4
+    c = Paged(kind, [1024 - (i * 37) % 300 for i in range(units // 4)], 4, d, 16, seed=56)
+    q = queries(c, G, 57)
+    w = torch.rand((units // 4, 4, c.rows), device="cuda")
+    out, lse, got = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda"), torch.full_like(w, -7.0)
+    skv.paged_attention(q, c.k, c.v, c.table, c.lens, out, lse, w, got)
+    check_all(c, q, out, lse, None, w, got)
+    for b, n in enumerate(c.n):
+        assert (got[b, :, n:] == -7.0).all()
+
+
 # ------------------------------------------------------------------ bad pages in an eviction
 
 @pytest.mark.parametrize("in_place", [False, True])
