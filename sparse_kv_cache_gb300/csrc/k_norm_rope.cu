@@ -220,13 +220,15 @@ static int launch_nr(NormRopeParams p, int nsm, cudaStream_t s) {
     // four 16.2).
     auto slots_of = [&](int g) { return (p.nq + g - 1) / g + (n_kv + g - 1) / g; };
     p.groups = kRows;
-    for (int g = kRows / 2; g >= 1 && kRows / g <= max_tokens(D) && p.tokens / (kRows / g) >= 4 * nsm; g /= 2) {
+    static_assert(kRows <= max_tokens(D), "a CTA has the angles' room for a token per lane group");
+    for (int g = kRows / 2; g >= 1 && p.tokens / (kRows / g) >= 4 * nsm; g /= 2) {
         const int spent = slots_of(g) * g, had = slots_of(p.groups) * p.groups;
         if (spent < had || (spent == had && slots_of(p.groups) < 10)) p.groups = g;
     }
-    const int per = kRows / p.groups, grid = (p.tokens + per - 1) / per;
-    // Five CTAs per SM have the registers to keep their rows' loads in flight, seven take fewer waves: a wave
-    // of seven takes 1.2 times as long as one of five (fp32: 1.45).  5105 tokens of 16 + 2 x 2 heads 14.2
+    const int per = kRows / p.groups, grid = (p.tokens - 1) / per + 1;
+    // Five CTAs per SM have the registers to keep their rows' loads in flight, seven take fewer waves (and spill
+    // 8 bytes in bf16, 48 with e5m2 values, 56 in fp32): a wave of seven takes 1.2 times as long as one of five
+    // (fp32: 1.45).  5105 tokens of 16 + 2 x 2 heads 14.2
     // us with five, 19.7 with seven; 32K of 32 + 2 x 8 150 and 140, 4096 26.7 and 22.3, 3000 16.7 and 20.1.
     const int w5 = (grid + 5 * nsm - 1) / (5 * nsm), w7 = (grid + 7 * nsm - 1) / (7 * nsm);
     const bool seven = sizeof(T) == 2 ? 6 * w7 < 5 * w5 : 3 * w7 < 2 * w5;
