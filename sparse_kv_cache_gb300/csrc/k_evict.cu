@@ -29,14 +29,15 @@ namespace skv {
 
 static __device__ int g_err[2];
 
-constexpr int kEvWide = 512, kEvNarrow = 128;  // threads of a CTA: two per SM, or eight
+constexpr int kEvWide = 512, kEvNarrow = 128;  // threads of a CTA: two per SM, or eight (six where they hold 4096 keys)
 constexpr int kEvStep = 256;                   // rows of a warp's step, eight per lane
 constexpr int kEvBins = 2048;
 constexpr int grain_of(int threads) { return kEvStep * (threads / 32); }     // a slice is a multiple of this many rows
 constexpr int kEvKeys = 11 * grain_of(kEvWide);   // halves of keys held in shared memory at most (88 KB: two CTAs per SM)
 
 // Rows of a unit that its own cluster moves, at most.  Of 2048 rows + 256, 64 units take 14.6 us with one
-// kernel and 15.9 with two, + 512 19.1 and 20.5 (8 units: 16.1 and 15.3), + 952 29.4 and 24.0.
+// kernel and 15.9 with two, + 512 19.1 and 20.5, + 952 29.4 and 24.0; 8 units, whose clusters leave most of the
+// device idle, lose 0.8 us at + 512 (16.1 and 15.3).
 constexpr int kEvFew = 512;
 constexpr int kEvShort = 4096;                 // room of a sequence that narrow CTAs serve, at most
 constexpr int kEvHist = 2 * kEvBins + 64;      // counts of the four passes
@@ -568,9 +569,10 @@ __global__ void k_evict_lens(const __grid_constant__ EvictParams p) {
 
 int launch_evict(const EvictParams& p, int nsm, cudaStream_t s) {
     const int U = p.c.batch * p.c.H;
-    // Many short units of which few rows can move go to narrow CTAs, of which an SM holds eight (2048 units
-    // of 501 rows, one of them given up: 29.4 us against 79.9; of 2049 rows: 55.0 against 98.0; but 66.6
-    // against 61.1 for 320 units of 3000 rows with 952 given up).  The others go to as many CTAs as the
+    // Many short units of which few rows can move go to narrow CTAs, of which an SM holds eight, or as their
+    // keys take 25 to 33 KB in rooms of 2048 to 4096 rows, eight to six (2048 units of 501 rows, one of them
+    // given up: 29.4 us against 79.9; of 2049 rows: 55.0 against 98.0; but 66.6 against 61.1 for 320 units of
+    // 3000 rows with 952 given up).  The others go to as many CTAs as the
     // device holds at once (two per SM), and no fewer than the keys need to stay in shared memory.  A
     // slice of under one grain would leave warps idle.
     const bool few = p.list_cap <= kEvFew, narrow = few && U > 2 * nsm && p.c.cap <= kEvShort;

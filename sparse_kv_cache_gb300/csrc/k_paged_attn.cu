@@ -115,9 +115,10 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int i) { return i == 0 
 template <int R = kPaTile>
 __device__ __forceinline__ int tiles_of(int n) { return (n + R - 1) / R; }
 
-// What CTA `me` of `ctas` takes of the tiles of R rows, and where its W parts begin.  A part has `least` tiles, or
-// joining the shares would take longer than forming them (one unit of 32K rows: 17.4 us with four,
-// 19.2 with two, 23.2 with one).  The tiles of fp32 take longer, and so may come one by one.
+// What CTA `me` of `ctas` takes of the tiles of R rows, and where its W parts begin.  Little work goes to the
+// fewest CTAs whose parts average no more than kPaLeast tiles (so that beyond one CTA's they average more
+// than half of it): with less, joining the shares takes longer than forming them (one unit of 32K rows: 17.4
+// us with four, 19.2 with two, 23.2 with one).  The tiles of fp32 take longer, and so may come one by one.
 constexpr int kPaLeast = 4;
 
 template <int W>
