@@ -15,8 +15,8 @@
 // of the remaining turn, as a fraction of pi, go to sincospi (error below 2^-23 of a half turn).
 //
 // Measured back to back: 32K tokens of 32 + 2 x 8 heads, d = 128, 140 us, 6.2 TB/s of a copy's 6.7;
-// 5105 tokens of 16 + 2 x 2 heads with e5m2 values 14.2 us (51 MB: latency of one wave of CTAs); a
-// decode step of 8 tokens 3.4 us.
+// 5105 tokens of 16 + 2 x 2 heads with e5m2 values 14.5 us (51 MB: latency of one wave of CTAs, four rounds of
+// loads one after the other in each); a decode step of 8 tokens 3.2 us.
 #include "skv_common.cuh"
 #include "skv_internal.h"
 #include "skv_paged.h"

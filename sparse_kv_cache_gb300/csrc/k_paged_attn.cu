@@ -25,10 +25,11 @@
 // joined by a transposing reduction.
 //
 // Measured back to back (8 KV heads of 4 query heads, d = 128, each row's bytes once over the time;
-// a copy runs at 6.7 TB/s): 8 x 128K rows in bf16 605 us, 7.1 TB/s; 4 x 32K rows 88 us, 6.1 TB/s; 8
-// ragged sequences of up to 64K rows with e5m2 values 138 us, 6.3 TB/s; 192 of 0 to 611 rows (4 KV
-// heads of 8) 30.6 us, 4.0 TB/s, a CTA per unit whose start and end are latency; 4096 of 0 to 30 rows (2
-// of 4) 30.5 us against 11.6 of their bytes; one sequence of 1013 rows 6.4 us, all of it latency.
+// a copy runs at 6.7 TB/s): 8 x 128K rows in bf16 600 to 609 us by box, 7.1 TB/s; 4 x 32K rows 88.7 us, 6.1
+// TB/s; 8 ragged sequences of up to 64K rows with e5m2 values 139 us, 6.2 TB/s; 192 of 0 to 611 rows (4
+// KV heads of 8) 30.6 us, 4.0 TB/s, a CTA per unit whose start and end are latency; 4096 of 0 to 30 rows (2
+// of 4) 31.0 us against 11.6 of their bytes; one sequence of 1013 rows 6.4 us, all of it latency (13 in a
+// table for 128K rows, by whose width the form is chosen).
 #include <math_constants.h>
 
 #include <atomic>
