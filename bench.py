@@ -30,11 +30,11 @@ from workload import ALL, LLAMA_128K, Workload  # noqa: E402
 # DRAM traffic of one scorer launch from ncu captures (dram__bytes_read.sum +
 # dram__bytes_write.sum), valid only while the scorer source is the one that was profiled;
 # per unit, scaled to a launch by its units.  bf16: k_score_tc at 128K b4 (32 units),
-# 133.89 + 4.35 MB; fp8: k_score_f8 at 128K b8 (64 units), 133.94 + 5.40 MB.
-SCORE_TRAFFIC_SHA256 = "6b81a89c450e7c0b18c603f24db0192aae24ae37004b7445e69bd0cdc73c951f"
+# 133.88 + 4.22 MB; fp8: k_score_f8 at 128K b8 (64 units), 133.97 + 4.09 MB.
+SCORE_TRAFFIC_SHA256 = "19e5e6b49f6a8f1303ed5763a47022a7c883de527ce6f60722f16506871d4856"
 SCORE_TRAFFIC = {
-    "bf16": {"seq_len": 131072, "bytes_per_unit": (133885696 + 4347136) / 32},
-    "fp8": {"seq_len": 131072, "bytes_per_unit": (133939712 + 5395456) / 64},
+    "bf16": {"seq_len": 131072, "bytes_per_unit": (133884928 + 4224768) / 32},
+    "fp8": {"seq_len": 131072, "bytes_per_unit": (133968640 + 4085248) / 64},
 }
 
 METRIC = "sparse decode-attention tokens/s and HBM GB/s (% of 8 TB/s) at 128K, 1×GB300"
