@@ -46,10 +46,11 @@ constexpr int kPaThreads = 128;
 static_assert(kPaThreads == 32 * kPaWarps, "");
 constexpr int kPaTile = 16;                       // rows of a warp's step
 constexpr float kPaSlack = 8.f;                   // the base moves when a score passes it by 2^8
-// Probabilities before they are normalised are held 2^38 lower: those of 2^30 rows, 2^8 over their base
-// each, add up to 1 at most, so no sum of values passes the largest value, which may be the type's.  (Rows
-// 2^-88 below the top fall out at 2^-126; products of values below 2^-80 lose bits there.)
-constexpr float kPaDown = 38.f;
+// Values are multiplied by 2^-38 of a probability that is not normalised yet: those of 2^30 rows, 2^8 over
+// their base each, add up to 1 at most, so no sum of values passes the largest value, which may be the
+// type's.  (Rows 2^-88 below the top fall out at 2^-126; products of values below 2^-80 lose bits there.  In the
+// exponent the 38 would cost all probabilities 2^-20 of themselves.)
+constexpr float kPaDown = 0x1p-38f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -399,7 +400,8 @@ struct TileTC {
     static constexpr int kKV = D / 32;                     // 16-byte words of a key row per lane
     static constexpr int kVV = kE5M2 ? 1 : D / 64;         // words of a value row per lane
     // fp16 probabilities: up to 2^15, the more of the small ones are normal (2^30 e5m2 values fit into a sum)
-    static constexpr float kBaseShift = kE5M2 ? 7.f : -kPaDown;
+    static constexpr float kBaseShift = kE5M2 ? 7.f : 0.f;
+    static constexpr float kDown = kE5M2 ? 1.f : kPaDown;
     uint4 q[kKV];
     float o[D / 16][4];
     float m0, m1, l0, l1;                                  // heads 2c and 2c + 1
@@ -525,12 +527,12 @@ struct TileTC {
             b0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
             b1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi));
         } else {
-            constexpr float kBelow = 1.f - 0x1p-20f;
+            constexpr float kBelow = kDown * (1.f - 0x1p-20f);
             const uint32_t h0 = cut_bf16x2(x0 * kBelow, x1 * kBelow), h1 = cut_bf16x2(x2 * kBelow, x3 * kBelow);
             b0 = transpose8x8(h0);
             b1 = transpose8x8(h1);
-            r0 = transpose8x8(pack_bf16x2(x0 - bf16lo(h0), x1 - bf16hi(h0)));
-            r1 = transpose8x8(pack_bf16x2(x2 - bf16lo(h1), x3 - bf16hi(h1)));
+            r0 = transpose8x8(pack_bf16x2(fmaf(x0, kDown, -bf16lo(h0)), fmaf(x1, kDown, -bf16hi(h0))));
+            r1 = transpose8x8(pack_bf16x2(fmaf(x2, kDown, -bf16lo(h1)), fmaf(x3, kDown, -bf16hi(h1))));
         }
     }
     __device__ __forceinline__ void values(const Values& v, uint32_t b0, uint32_t b1, uint32_t r0, uint32_t r1) {
@@ -630,7 +632,7 @@ struct TileTC {
             const int g = 2 * c + e;
             if (g >= p.G) continue;
             const float m = (e ? m1 : m0) - kBaseShift, l = e ? l1 : l0;
-            const float inv = !alone ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            const float inv = !alone ? 1.f : l == 0.f ? 0.f : 1.f / (l * kDown);
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + b * p.o_seq + (h * p.G + g) * p.o_head;
 #pragma unroll
             for (int t = 0; t < D / 16; t += 4) {
@@ -720,6 +722,7 @@ struct TileTC {
 template <int D, int G>
 struct TileF32 {
     static constexpr int kV = D / 64;      // float4 of a row per lane
+    static constexpr float kDown = kPaDown;
     float o[G][4 * kV];
     float m[G], l[G];
     bool held;                             // whether the unit has held sums
@@ -829,11 +832,12 @@ struct TileF32 {
             }
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                const float pr = in ? exp2_fast(fmaf(s[g], p.scale_log2, m[g] == -CUDART_INF_F ? 0.f : -m[g] - kPaDown)) : 0.f;
+                const float pr = in ? exp2_fast(fmaf(s[g], p.scale_log2, m[g] == -CUDART_INF_F ? 0.f : -m[g])) : 0.f;
+                const float down = pr * kDown;
                 l[g] += pr;                     // every row is held by two lanes: halved at the end
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float w = __shfl_sync(0xffffffffu, pr, 16 * half + 2 * i);
+                    const float w = __shfl_sync(0xffffffffu, down, 16 * half + 2 * i);
 #pragma unroll
                     for (int j = 0; j < 4 * kV; ++j) o[g][j] = fmaf(w, v[i][j], o[g][j]);
                 }
@@ -874,8 +878,7 @@ struct TileF32 {
         __syncwarp();      // the slot may be written again
     }
     // the sums of both half-warps, of head g into a slot
-    __device__ __forceinline__ void put(JoinSmem<D, G>& js, int slot, int g, float base, float sum,
-                                        const float (&x)[4 * kV]) const {
+    __device__ __forceinline__ void put(JoinSmem<D, G>& js, int slot, int g, float sum, const float (&x)[4 * kV]) const {
         const int lane = threadIdx.x & 31, hl = lane & 15;
         if (lane < 16) {
 #pragma unroll
@@ -884,7 +887,7 @@ struct TileF32 {
                     make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
         }
         if (lane == 0) {
-            js.m[slot][g] = base;
+            js.m[slot][g] = m[g];
             js.l[slot][g] = sum;
         }
     }
@@ -900,7 +903,7 @@ struct TileF32 {
                 x[i] = o[g][i] + __shfl_xor_sync(0xffffffffu, o[g][i], 16);
                 o[g][i] = 0.f;
             }
-            put(js, slot, g, m[g], sum, x);
+            put(js, slot, g, sum, x);
             l[g] = 0.f;
         }
         held = true;
@@ -919,10 +922,10 @@ struct TileF32 {
             for (int i = 0; i < 4 * kV; ++i) x[i] = o[g][i] + __shfl_xor_sync(0xffffffffu, o[g][i], 16);
             if (g >= p.G) continue;
             if (!alone) {
-                put(js, slot, g, m[g] + kPaDown, sum, x);
+                put(js, slot, g, sum, x);
                 continue;
             }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float inv = sum == 0.f ? 0.f : 1.f / (sum * kDown);
             float* dst = static_cast<float*>(p.out) + b * p.o_seq + (h * p.G + g) * p.o_head;
             if (lane < 16) {
 #pragma unroll
@@ -930,7 +933,7 @@ struct TileF32 {
                     *reinterpret_cast<float4*>(dst + 64 * i + 4 * hl) =
                         make_float4(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
             }
-            if (lane == 0) note(p, b, h, g, m[g] + kPaDown, sum);
+            if (lane == 0) note(p, b, h, g, m[g], sum);
         }
     }
 };
@@ -969,7 +972,7 @@ __device__ __forceinline__ void join_shares(const PagedAttnParams& p, JoinSmem<D
             if (js.of[e].b >= 0) m = fmaxf(m, js.m[e][g]);
         for (int e = r.from; e <= r.last; ++e)
             if (js.of[e].b >= 0) l = fmaf(js.l[e][g], share_weight(js.m[e][g], js.l[e][g], m), l);
-        const float scale = !r.whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        const float scale = !r.whole ? 1.f : l == 0.f ? 0.f : 1.f / (l * p.down);
         for (int e = r.from; e <= r.last; ++e)
             js.w[e][g] = js.of[e].b >= 0 ? share_weight(js.m[e][g], js.l[e][g], m) * scale : -1.f;
         if (r.whole) note(p, r.b, r.h, g, m, l);
@@ -1148,7 +1151,7 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid
             x[3] = fmaf(v.w, f, x[3]);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = l == 0.f ? 0.f : x[e] / l;
+        for (int e = 0; e < 4; ++e) x[e] = l == 0.f ? 0.f : x[e] / (l * p.down);
         store4<kF32>(p, b, h, g, dim, x);
         if (dim == 0) note(p, b, h, g, m, l);
     }
@@ -1218,7 +1221,7 @@ __device__ __forceinline__ void merge_few(const PagedAttnParams& p, const Joint&
             x[3] = fmaf(v[i].w, f, x[3]);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = l == 0.f ? 0.f : x[e] / l;
+        for (int e = 0; e < 4; ++e) x[e] = l == 0.f ? 0.f : x[e] / (l * p.down);
         store4<kF32>(p, j.b, j.h, g, dim, x);
         if (dim == 0) note(p, j.b, j.h, g, m, l);
     }
@@ -1293,7 +1296,7 @@ __device__ __forceinline__ void merge_many(const PagedAttnParams& p, const Joint
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWays; ++w) sum += sm.x[w][tid];
-        store_out(p, kF32, j.b, j.h, g, tid, l == 0.f ? 0.f : sum / l);
+        store_out(p, kF32, j.b, j.h, g, tid, l == 0.f ? 0.f : sum / (l * p.down));
     }
     if (tid == 0) note(p, j.b, j.h, g, m, l);
     __syncthreads();
@@ -1484,7 +1487,8 @@ static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
 }
 
 template <class Tile, int D, bool kF32, int G>
-static int launch_pa(const PagedAttnParams& p, int ncta, cudaStream_t s) {
+static int launch_pa(PagedAttnParams p, int ncta, cudaStream_t s) {
+    p.down = Tile::kDown;
     constexpr int kOcc = occ_of(kF32, D), kOccShort = kF32 ? 2 : kOcc;
     const int held = ncta / kOcc * kOccShort;
     if (p.weight_out) {

@@ -59,6 +59,23 @@ def test_one_warp_walks_a_long_unit(kind, d, units, flavour):
     assert skv.paged_status() == 0
 
 
+@pytest.mark.parametrize("headroom", [0, 16384])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "f32"])
+def test_log_sum_exp_near_zero(kind, headroom):
+    """Of one row it is the row's score, where the base lies: the rest is exp2 of a difference near 0 (off by
+    2^-22 at most), its logarithm, and roundings of the result.  With e5m2 values the base lies 7 lower: two
+    roundings of numbers near 7, 2^-22 each, and a logarithm near 7, 2^-21."""
+    c = Paged(kind, [1] * 300, 1, 64, 16, seed=63)
+    q = queries(c, 4, 64, 0.02)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    skv.paged_attention(q, c.k, c.v, wider(c.table, headroom, 16), c.lens, out, lse)
+    for b in range(300):
+        z = f64(q[b]) @ f64(c.krows[b][0, 0]) / 8
+        delta = 64 * 2.0 ** -24 / 8 * (np.abs(f64(q[b])) @ np.abs(f64(c.krows[b][0, 0])))
+        tol = delta + 2.0 ** -21 + (2.0 ** -20 if kind == "fp8" else 0)
+        assert (np.abs(f64(lse[b]) - z) <= tol).all(), np.abs(f64(lse[b]) - z).max()
+
+
 # ------------------------------------------------------------------ infinite and large values
 
 def put_value(c, b, row, dim, x):
