@@ -546,10 +546,10 @@ int shadowkv_qk_norm_rope(const skv_qk_norm_rope_args* args, skv_stream stream);
  * Accumulation, softmax statistics and sums are fp32.  bf16 values are
  * multiplied by probabilities in two bf16 terms (16 bits), e5m2 ones by
  * probabilities in fp16.  Values may be as large as their type's largest; the
- * products of those below 2^-80 lose bits.  An infinite value gives that
- * infinity, one of each sign or a NaN gives NaN.  A row 2^-75 below the heaviest
- * (e5m2: 2^-32) weighs nothing, and an infinity there gives NaN.  Rows that
- * score -infinity count as absent.
+ * products of those below 2^-118 times the table's rows lose bits.  An infinite
+ * value gives that infinity, one of each sign or a NaN gives NaN.  A row 2^-75
+ * below the heaviest (e5m2: 2^-32) may weigh nothing, and an infinity there give
+ * NaN.  Rows that score -infinity count as absent.
  */
 typedef struct {
     skv_paged_cache cache;

@@ -46,11 +46,10 @@ constexpr int kPaThreads = 128;
 static_assert(kPaThreads == 32 * kPaWarps, "");
 constexpr int kPaTile = 16;                       // rows of a warp's step
 constexpr float kPaSlack = 8.f;                   // the base moves when a score passes it by 2^8
-// Values are multiplied by 2^-38 of a probability that is not normalised yet: those of 2^30 rows, 2^8 over
-// their base each, add up to 1 at most, so no sum of values passes the largest value, which may be the
-// type's.  (Rows 2^-88 below the top fall out at 2^-126; products of values below 2^-80 lose bits there.  In the
-// exponent the 38 would cost all probabilities 2^-20 of themselves.)
-constexpr float kPaDown = 0x1p-38f;
+// Values are multiplied by p.down of a probability that is not normalised yet, 2^-8 over the rows that a
+// sequence has room for: with the slack they then add up to 1 at most, so no sum of values passes the
+// largest value, which may be the type's.  (Of a table for 128K rows, 2^-25: products of values below 2^-101
+// lose bits at fp32's smallest.  In the exponent it would cost all probabilities 2^-20 of themselves.)
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -401,7 +400,7 @@ struct TileTC {
     static constexpr int kVV = kE5M2 ? 1 : D / 64;         // words of a value row per lane
     // fp16 probabilities: up to 2^15, the more of the small ones are normal (2^30 e5m2 values fit into a sum)
     static constexpr float kBaseShift = kE5M2 ? 7.f : 0.f;
-    static constexpr float kDown = kE5M2 ? 1.f : kPaDown;
+    static constexpr bool kLow = !kE5M2;                   // whether p.down is in the sums of values
     uint4 q[kKV];
     float o[D / 16][4];
     float m0, m1, l0, l1;                                  // heads 2c and 2c + 1
@@ -480,8 +479,8 @@ struct TileTC {
     }
     // probabilities against the running base; returns P^T as the second product's operand, b, and what
     // its rounding to bf16 left, r
-    __device__ __forceinline__ void softmax(float scale, int row, int end, int ida, int idb, const float (&s)[4], uint32_t& b0,
-                                            uint32_t& b1, uint32_t& r0, uint32_t& r1) {
+    __device__ __forceinline__ void softmax(float scale, int row, int end, int ida, int idb, const float (&s)[4], float down,
+                                            uint32_t& b0, uint32_t& b1, uint32_t& r0, uint32_t& r1) {
         const int r = (threadIdx.x & 31) >> 2;
         // scores in powers of two, -inf for an absent row (whatever the sign of the scale)
         const bool ia = ida >= 0 && row + r < end, ib = idb >= 0 && row + 8 + r < end;
@@ -527,12 +526,12 @@ struct TileTC {
             b0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
             b1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi));
         } else {
-            constexpr float kBelow = kDown * (1.f - 0x1p-20f);
-            const uint32_t h0 = cut_bf16x2(x0 * kBelow, x1 * kBelow), h1 = cut_bf16x2(x2 * kBelow, x3 * kBelow);
+            const float below = down * (1.f - 0x1p-20f);
+            const uint32_t h0 = cut_bf16x2(x0 * below, x1 * below), h1 = cut_bf16x2(x2 * below, x3 * below);
             b0 = transpose8x8(h0);
             b1 = transpose8x8(h1);
-            r0 = transpose8x8(pack_bf16x2(fmaf(x0, kDown, -bf16lo(h0)), fmaf(x1, kDown, -bf16hi(h0))));
-            r1 = transpose8x8(pack_bf16x2(fmaf(x2, kDown, -bf16lo(h1)), fmaf(x3, kDown, -bf16hi(h1))));
+            r0 = transpose8x8(pack_bf16x2(fmaf(x0, down, -bf16lo(h0)), fmaf(x1, down, -bf16hi(h0))));
+            r1 = transpose8x8(pack_bf16x2(fmaf(x2, down, -bf16lo(h1)), fmaf(x3, down, -bf16hi(h1))));
         }
     }
     __device__ __forceinline__ void values(const Values& v, uint32_t b0, uint32_t b1, uint32_t r0, uint32_t r1) {
@@ -632,7 +631,7 @@ struct TileTC {
             const int g = 2 * c + e;
             if (g >= p.G) continue;
             const float m = (e ? m1 : m0) - kBaseShift, l = e ? l1 : l0;
-            const float inv = !alone ? 1.f : l == 0.f ? 0.f : 1.f / (l * kDown);
+            const float inv = !alone ? 1.f : l == 0.f ? 0.f : 1.f / (l * p.down);
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + b * p.o_seq + (h * p.G + g) * p.o_head;
 #pragma unroll
             for (int t = 0; t < D / 16; t += 4) {
@@ -697,7 +696,7 @@ struct TileTC {
             }
             if (Keep::on) keep(p, z(cur.b, cur.h, row), row, cur.end, was_a, was_b, s);
             uint32_t b0, b1, r0 = 0, r1 = 0;
-            softmax(p.scale_log2, row, cur.end, was_a, was_b, s, b0, b1, r0, r1);
+            softmax(p.scale_log2, row, cur.end, was_a, was_b, s, p.down, b0, b1, r0, r1);
             values(v, b0, b1, r0, r1);
             if (!last) {
                 if (t == 0) put_by();
@@ -722,7 +721,7 @@ struct TileTC {
 template <int D, int G>
 struct TileF32 {
     static constexpr int kV = D / 64;      // float4 of a row per lane
-    static constexpr float kDown = kPaDown;
+    static constexpr bool kLow = true;     // whether p.down is in the sums of values
     float o[G][4 * kV];
     float m[G], l[G];
     bool held;                             // whether the unit has held sums
@@ -833,7 +832,7 @@ struct TileF32 {
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 const float pr = in ? exp2_fast(fmaf(s[g], p.scale_log2, m[g] == -CUDART_INF_F ? 0.f : -m[g])) : 0.f;
-                const float down = pr * kDown;
+                const float down = pr * p.down;
                 l[g] += pr;                     // every row is held by two lanes: halved at the end
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -925,7 +924,7 @@ struct TileF32 {
                 put(js, slot, g, sum, x);
                 continue;
             }
-            const float inv = sum == 0.f ? 0.f : 1.f / (sum * kDown);
+            const float inv = sum == 0.f ? 0.f : 1.f / (sum * p.down);
             float* dst = static_cast<float*>(p.out) + b * p.o_seq + (h * p.G + g) * p.o_head;
             if (lane < 16) {
 #pragma unroll
@@ -1488,7 +1487,9 @@ static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
 
 template <class Tile, int D, bool kF32, int G>
 static int launch_pa(PagedAttnParams p, int ncta, cudaStream_t s) {
-    p.down = Tile::kDown;
+    int bits = static_cast<int>(kPaSlack);
+    while (Tile::kLow && p.c.cap > 1 << (bits - static_cast<int>(kPaSlack))) ++bits;
+    p.down = Tile::kLow ? 1.f / static_cast<float>(int64_t(1) << bits) : 1.f;
     constexpr int kOcc = occ_of(kF32, D), kOccShort = kF32 ? 2 : kOcc;
     const int held = ncta / kOcc * kOccShort;
     if (p.weight_out) {

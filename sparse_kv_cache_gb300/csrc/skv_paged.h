@@ -42,7 +42,7 @@ struct PagedAttnParams {
     PagedView c;
     int G, n_q;
     float scale_log2;         // scale * log2(e)
-    float down;               // sums of values are lower by this than those of probabilities (set by the launcher)
+    float down;               // values are weighed by this much of a probability (set by the launcher)
     int64_t q_seq, q_head, o_seq, o_head;
     const void* q; void* out; float* lse;
     float* rec;               // [ncta][2][G][d]: a CTA's shares of its first and last unit, unnormalised

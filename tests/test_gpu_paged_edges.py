@@ -136,6 +136,21 @@ def test_values_near_the_types_largest(kind, headroom):
     check_all(c, q, out, lse, 7 * math.log(2) / 5)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_small_values_keep_their_bits(kind):
+    """Values near 2^-104 in a table for 16K rows: their products with 2^-22 of a probability lie near fp32's
+    smallest normal number, 2^-126, and below it down to 2^-149: 2^-23 of that."""
+    c = Paged(kind, [3000, 40], 1, 64, 16, seed=65)
+    for b in range(2):
+        c.vrows[b] = c.vrows[b] * 2.0 ** -104
+    c.v = (c.v.float() * 2.0 ** -104).to(c.v.dtype)
+    q = queries(c, 4, 66, 0.3)
+    out = torch.empty_like(q)
+    skv.paged_attention(q, c.k, c.v, wider(c.table, 13376, 16), c.lens, out)
+    for b, n in enumerate(c.n):           # scaled up, with the tolerances of ordinary values
+        check_attention(kind, f64(q[b]), f64(out[b]) * 2.0 ** 104, None, f64(c.krows[b][0]), f64(c.vrows[b][0]) * 2.0 ** 104, 0.125)
+
+
 @pytest.mark.parametrize("headroom", [0, 16384])
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_rows_that_a_negative_scale_brings_to_minus_infinity(kind, headroom):
