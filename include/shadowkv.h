@@ -55,7 +55,8 @@ typedef struct CUstream_st* skv_stream;
  * q, k_new, v_new, the keys and out stay bf16.  Scores stay bf16-exact (the
  * query is split into three e5m2 terms for the 8-bit tensor-core product).
  */
-typedef enum { SKV_F32 = 0, SKV_BF16 = 1, SKV_FP8 = 2 } skv_dtype;
+/* SKV_E4M3: a paged cache of e4m3 codes with block scales (skv_block_scales); for the paged calls that name it */
+typedef enum { SKV_F32 = 0, SKV_BF16 = 1, SKV_FP8 = 2, SKV_E4M3 = 3 } skv_dtype;
 typedef enum { SKV_V_HBM = 0, SKV_V_HOST = 1 } skv_vplace;
 
 /*
@@ -426,7 +427,7 @@ int shadowkv_fetch_probe(const void* src, size_t bytes, int64_t n_chunks, int ch
 
 /*
  * Paged caches: the dense path beside the sparse one.  The pages have no
- * counterpart to these four calls; they serve what surrounds a decode step --
+ * counterpart to these calls; they serve what surrounds a decode step --
  * the projections' outputs that have to be normed and rotated before
  * shadowkv_decode_step takes them, layers that attend over their whole cache,
  * and caches that are held to a budget by giving rows up instead of by
@@ -438,7 +439,7 @@ int shadowkv_fetch_probe(const void* src, size_t bytes, int64_t n_chunks, int ch
  * row i % page_size of page table[b][i / page_size].  Only the pages of its
  * first lens[b] rows are read.  Strides are in elements and free (page-major,
  * head-major or token-major pools), the head dimension is contiguous.
- *   dtype      SKV_BF16, SKV_F32, or SKV_FP8 (bf16 keys, e5m2 values)
+ *   dtype      SKV_BF16, SKV_F32, or SKV_FP8 (bf16 keys, e5m2 values); SKV_E4M3 where a call says so
  *   head_dim   64 or 128;  page_size a power of two from 8 to 1024
  *   strides    multiples of 16 bytes; pools 16-byte aligned device memory of the
  *              current device; rows of pools and outputs that are written do not overlap
@@ -606,6 +607,83 @@ typedef struct {
 } skv_paged_evict_args;
 int64_t shadowkv_paged_evict_workspace(const skv_paged_evict_args* args);   /* bytes, or SKV_ERR_* */
 int shadowkv_paged_evict(const skv_paged_evict_args* args, skv_stream stream);
+
+/*
+ * The same for one new token per sequence over a part of its rows, and over caches of 8-bit codes.
+ *
+ * With window > 0 the token sees its sequence's last `window` rows and its first `sink` ones: row j < lens[b] with
+ * j >= lens[b] - window or j < sink, by the place in the cache (a cache that has lost rows in an eviction has no
+ * such order).  window 0: all rows, whatever sink is.  Groups of eight rows of which none is seen are not looked
+ * at, neither the rows nor their page ids: a server may give the pages between back.
+ *
+ * A cache of dtype SKV_E4M3 holds codes of four significant bits, keys and values alike, and their scales beside
+ * the pools: a value is code * scale[page][head][row % page_size / block].  q and out are bf16.  The
+ * scales are powers of two as shadowkv_paged_quantise writes them; any positive ones do here.  A code of NaN
+ * in a row that is seen gives NaN.  Scores are formed from fp16 queries, a power of two per head apart (what is below
+ * 2^-39 of a head's largest element is lost), probabilities take their value's scale and are rounded to fp16:
+ * a row whose probability times scale is 2^-32 below the unit's heaviest may weigh nothing.  Everything else is
+ * as above.
+ *
+ * attn.weight and attn.weight_out go with whole caches of the other types (window 0), where this call is
+ * shadowkv_paged_attention; anywhere else they are refused.
+ */
+typedef struct {
+    float* k;                   /* dev [n_pages][n_kv_heads][page_size / block] */
+    float* v;                   /* dev, the same shape */
+    int32_t block;              /* rows of a scale: a power of two from 8 to 128, at most page_size */
+    int32_t reserved;           /* 0 */
+} skv_block_scales;
+typedef struct {
+    skv_paged_attention_args attn;
+    skv_block_scales scales;    /* with SKV_E4M3; otherwise zeros */
+    int32_t window;             /* >= 0 */
+    int32_t sink;               /* >= 0 */
+} skv_paged_attention_ext_args;
+int64_t shadowkv_paged_attention_ext_workspace(const skv_paged_attention_ext_args* args);   /* bytes, or SKV_ERR_* */
+int shadowkv_paged_attention_ext(const skv_paged_attention_ext_args* args, skv_stream stream);
+
+/*
+ * Writes new rows of a cache of dtype SKV_E4M3.  Tokens start[b] .. start[b+1] of k and v (bf16 or fp32) become rows
+ * lens[b] on of sequence b; lens is the caller's to advance.  For every block (scales.block rows of a page, from the
+ * page's first) and head, of keys and of values:
+ *   scale = 2^e, the smallest e >= -100 with |x| <= 448 * 2^e for the finite x among the block's new rows
+ * and, where the block holds rows of the sequence already, the larger of that and the scale it has;
+ * held codes are then rounded to the new one (between powers of two only what falls below 2^-9 of it is lost).
+ *   code = x / scale, to the nearest, ties to even; NaN for a NaN and for an infinity
+ * start does not fall, start[0] >= 0, start[batch] <= tokens; a sequence for which it does, or whose rows
+ * would pass its table, sets the error word, and what is out of range is not written.  A bad page sets it too and
+ * its rows are left out.  A sequence that is written to does not share its last page.
+ */
+typedef struct {
+    skv_paged_cache cache;      /* dtype SKV_E4M3; lens: rows held before the call */
+    skv_block_scales scales;
+    int32_t tokens;             /* 0: nothing is done */
+    int32_t dtype;              /* SKV_BF16 or SKV_F32: of k and v */
+    int64_t k_tok, k_head, v_tok, v_head;   /* strides, elements, of whole 16 bytes */
+    const void* k;              /* dev [tokens][n_kv_heads][d], 16-byte aligned */
+    const void* v;
+    const int32_t* start;       /* dev [batch + 1] */
+} skv_paged_quantise_args;
+int shadowkv_paged_quantise(const skv_paged_quantise_args* args, skv_stream stream);
+
+/*
+ * Reads rows of a cache of dtype SKV_E4M3 back: tokens start[b] .. start[b+1] of k and v (bf16 or fp32) become
+ * rows first[b] on of sequence b, code * scale in fp32, rounded once.  Rows from lens[b] on and tokens of no
+ * sequence are left as they are, and so are the rows of a bad page, which sets the error word, and the
+ * tokens of a sequence whose start or first is out of range, which does too.
+ */
+typedef struct {
+    skv_paged_cache cache;      /* dtype SKV_E4M3 */
+    skv_block_scales scales;
+    int32_t tokens;             /* 0: nothing is done */
+    int32_t dtype;              /* SKV_BF16 or SKV_F32: of k and v */
+    int64_t k_tok, k_head, v_tok, v_head;   /* strides, elements, of whole 16 bytes; rows do not overlap */
+    void* k;                    /* dev [tokens][n_kv_heads][d], 16-byte aligned, written */
+    void* v;
+    const int32_t* start;       /* dev [batch + 1], does not fall */
+    const int32_t* first;       /* dev [batch], >= 0 */
+} skv_paged_dequantise_args;
+int shadowkv_paged_dequantise(const skv_paged_dequantise_args* args, skv_stream stream);
 
 /*
  * Status of the paged calls on the current device, of all streams: waits for

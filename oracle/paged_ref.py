@@ -53,3 +53,35 @@ def moves(kept: np.ndarray, budget: int) -> list[tuple[int, int]]:
     of = [i for i in range(budget, len(kept)) if kept[i]]
     assert len(to) == len(of)
     return list(zip(to, of))
+
+
+def e4m3(x: np.ndarray) -> np.ndarray:
+    """The nearest e4m3 numbers (3 mantissa bits, normal from 2^-6, steps of 2^-9 below), ties to even, of |x| <= 448."""
+    grid = np.exp2(np.maximum(np.floor(np.log2(np.maximum(np.abs(x), 1e-300))), -6.0) - 3.0)
+    return np.rint(x / grid) * grid
+
+
+def block_scale(x: np.ndarray) -> float:
+    """The smallest 2^e, e >= -100, with |x| <= 448 * 2^e for the finite x."""
+    most = np.abs(x[np.isfinite(x)]).max(initial=0.0)
+    e = -100
+    while most > 448.0 * 2.0 ** e:
+        e += 1
+    return 2.0 ** e
+
+
+def append_block(held: np.ndarray, scale: float, new: np.ndarray):
+    """A block [rows][d] of codes that holds `held` at `scale` after rows `new` joined it: (codes, scale)."""
+    size = block_scale(new)
+    if len(held):
+        size = max(size, scale)
+        held = e4m3(held * (scale / size)) if size != scale else held
+    with np.errstate(invalid="ignore"):
+        codes = np.where(np.isfinite(new), e4m3(np.where(np.isfinite(new), new, 0.0) / size), np.nan)
+    return np.concatenate([held.reshape(-1, new.shape[1]), codes]), size
+
+
+def seen_rows(row: int, window: int, sink: int) -> np.ndarray:
+    """The rows that the token at `row` sees: itself and those before it, of them (window > 0) the last `window` and
+    the first `sink`."""
+    return np.array([j for j in range(row + 1) if window == 0 or j < sink or j > row - window], dtype=int)

@@ -15,7 +15,7 @@ import threading
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libshadowkv.so")
 
-SKV_F32, SKV_BF16, SKV_FP8 = 0, 1, 2
+SKV_F32, SKV_BF16, SKV_FP8, SKV_E4M3 = 0, 1, 2, 3
 DTYPE_CODES = {"f32": SKV_F32, "bf16": SKV_BF16, "fp8": SKV_FP8}
 SKV_V_HBM, SKV_V_HOST = 0, 1
 HOST_KINDS = {"pinned": 0, "huge": 1}   # SKV_HOST_PINNED, SKV_HOST_HUGE
@@ -37,7 +37,9 @@ EXPORTED = ("shadowkv_validate_config", "shadowkv_prefill_index", "shadowkv_pref
             "shadowkv_sparse_attention_noalloc", "shadowkv_sparse_attention_noalloc_status",
             "shadowkv_fetch_probe",
             "shadowkv_qk_norm_rope", "shadowkv_paged_attention", "shadowkv_paged_attention_workspace",
-            "shadowkv_paged_evict", "shadowkv_paged_evict_workspace", "shadowkv_paged_status")
+            "shadowkv_paged_evict", "shadowkv_paged_evict_workspace", "shadowkv_paged_status",
+            "shadowkv_paged_attention_ext", "shadowkv_paged_attention_ext_workspace",
+            "shadowkv_paged_quantise", "shadowkv_paged_dequantise")
 
 # C layouts of the paged calls' argument structs (native sizes and alignment, as the header declares
 # them).  They are packed in one go: a decode step calls these once per layer, where filling a
@@ -46,6 +48,10 @@ _CACHE = "6i q 6q q 4P"                                  # skv_paged_cache
 _NORM_ROPE = struct.Struct(_CACHE + " 3i f d 10q 7P 3P 2P q")
 _PAGED_ATTN = struct.Struct(_CACHE + " i f 4q 5P q P q")
 _EVICT = struct.Struct(_CACHE + " 3i 4P q 2P q")
+_SCALES = "2P 2i"                                        # skv_block_scales
+_PAGED_ATTN_EXT = struct.Struct(_CACHE + " i f 4q 5P q P q " + _SCALES + " 2i")
+_QUANTISE = struct.Struct(_CACHE + " " + _SCALES + " 2i 4q 3P")
+_DEQUANTISE = struct.Struct(_CACHE + " " + _SCALES + " 2i 4q 4P")
 
 
 class SkvConfig(ctypes.Structure):
@@ -136,10 +142,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
                                          ctypes.POINTER(ctypes.c_double)]
     lib.shadowkv_fetch_probe.restype = i32
     lib.shadowkv_sparse_attention_noalloc_status.restype = i32
-    for name in ("shadowkv_qk_norm_rope", "shadowkv_paged_attention", "shadowkv_paged_evict"):
+    for name in ("shadowkv_qk_norm_rope", "shadowkv_paged_attention", "shadowkv_paged_evict", "shadowkv_paged_attention_ext",
+                 "shadowkv_paged_quantise", "shadowkv_paged_dequantise"):
         getattr(lib, name).argtypes = [ctypes.c_char_p, vp]
         getattr(lib, name).restype = i32
-    for name in ("shadowkv_paged_attention_workspace", "shadowkv_paged_evict_workspace"):
+    for name in ("shadowkv_paged_attention_workspace", "shadowkv_paged_evict_workspace", "shadowkv_paged_attention_ext_workspace"):
         getattr(lib, name).argtypes = [ctypes.c_char_p]
         getattr(lib, name).restype = i64
     lib.shadowkv_paged_status.argtypes = [vp]
@@ -250,12 +257,12 @@ def _steps(t, n: int):
     return tuple(0 if size == 1 else step for size, step in zip(t[0][:n], t[1]))
 
 
-def _pool_fields(where: str, k, v, table, lens, batch: int):
+def _pool_fields(where: str, k, v, table, lens, batch: int, codes: bool = False):
     """The fields of skv_paged_cache before its pointers, from the forms of the tensors: pools
     [n_pages][H][page_size][d] with any strides over a contiguous head dimension, table int32
-    [batch][max_pages], lens int32 [batch]."""
+    [batch][max_pages], lens int32 [batch].  codes: e4m3 pools, with scales of their own."""
     kd, vd = str(k[2]), str(v[2])
-    code = {("torch.bfloat16", "torch.bfloat16"): SKV_BF16, ("torch.float32", "torch.float32"): SKV_F32,
+    code = SKV_E4M3 if codes and kd == vd == "torch.float8_e4m3fn" else None if codes else {("torch.bfloat16", "torch.bfloat16"): SKV_BF16, ("torch.float32", "torch.float32"): SKV_F32,
             ("torch.bfloat16", "torch.float8_e5m2"): SKV_FP8}.get((kd, vd))
     if code is None:
         _refuse(where, f"no cache of {kd} keys and {vd} values")
@@ -268,6 +275,19 @@ def _pool_fields(where: str, k, v, table, lens, batch: int):
     pages, heads, size, d = k[0]
     return (code, heads, d, size, batch, table[0][1], pages, *_steps(k, 3), *_steps(v, 3),
             table[1][0] if batch > 1 else table[0][1])
+
+
+def _scale_block(where: str, k_scale, v_scale, k) -> int:
+    """Rows of a scale, from the forms of the scales [n_pages][H][page_size / block] and of a pool."""
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is None or len(t[0]) != 3 or t[0][:2] != k[0][:2] or str(t[2]) != "torch.float32" or t[0] != k_scale[0]:
+            _refuse(where, f"{name} is fp32 [n_pages][n_kv_heads][page_size / block], contiguous")
+        blocks = t[0][2]
+        if _steps(t, 3) != tuple(0 if n == 1 else s for n, s in zip(t[0], (t[0][1] * blocks, blocks, 1))):
+            _refuse(where, f"{name} is contiguous")
+    if blocks < 1 or k[0][2] % blocks:
+        _refuse(where, "a page is whole blocks")
+    return k[0][2] // blocks
 
 
 def _rows(where: str, name: str, t, dtype: str, batch: int, heads: int, need: int) -> int:
@@ -416,14 +436,21 @@ def qk_norm_rope(q, k, positions, q_out, k_out=None, *, q_weight=None, k_weight=
 
 
 @functools.lru_cache(maxsize=1024)
-def _paged_attention_plan(q, k_cache, v_cache, table, lens, out, lse, weight, weight_out, scale):
+def _paged_attention_plan(q, k_cache, v_cache, table, lens, out, lse, weight, weight_out, scale, k_scale, v_scale, window, sink):
     w = "paged_attention"
     if len(q[0]) != 3:
         _refuse(w, "q is [batch][n_q_heads][d]")
     batch, nq, d = q[0]
-    cache = _pool_fields(w, k_cache, v_cache, table, lens, batch)
-    if q[2] != k_cache[2] or cache[2] != d:
-        _refuse(w, f"q is {k_cache[2]} [batch][n_q_heads][{cache[2]}]")
+    codes = k_scale is not None or v_scale is not None
+    cache = _pool_fields(w, k_cache, v_cache, table, lens, batch, codes)
+    block = _scale_block(w, k_scale, v_scale, k_cache) if codes else 0
+    wide = "torch.bfloat16" if codes else str(k_cache[2])
+    if str(q[2]) != wide or cache[2] != d:
+        _refuse(w, f"q is {wide} [batch][n_q_heads][{cache[2]}]")
+    if not (isinstance(window, int) and isinstance(sink, int) and 0 <= window < 1 << 31 and 0 <= sink < 1 << 31):
+        _refuse(w, "window and sink are numbers of rows")
+    if weight is not None and (codes or window):
+        _refuse(w, "weights go with whole caches of bf16, fp32 or e5m2")
     qs, os_ = _heads(w, "q", q, q[2], (batch, nq, d)), _heads(w, "out", out, q[2], (batch, nq, d))
     if lse is not None and (lse[0] != (batch, nq) or lse[1] != (nq, 1) or str(lse[2]) != "torch.float32"):
         _refuse(w, "lse is fp32 [batch][n_q_heads], contiguous")
@@ -437,31 +464,41 @@ def _paged_attention_plan(q, k_cache, v_cache, table, lens, out, lse, weight, we
         _refuse(w, "weight_out goes with weight")
     # the workspace's size goes by these fields alone
     size = _PAGED_ATTN.pack(*cache[:6], *(0,) * 12, nq, scale, *(0,) * 8, 0 if weight is None else 1, 0, 0, 0)
-    nbytes = load().shadowkv_paged_attention_workspace(size)
+    if codes:
+        nbytes = load().shadowkv_paged_attention_ext_workspace(size + struct.pack(_SCALES + " 2i", 0, 0, block, 0, window, sink))
+    else:
+        nbytes = load().shadowkv_paged_attention_workspace(size)
     if nbytes < 0:
         _check(int(nbytes), "shadowkv_paged_attention_workspace")
-    return cache, (nq, scale, *qs, *os_), pitch, nbytes
+    return cache, (nq, scale, *qs, *os_), pitch, nbytes, block
 
 
 def paged_attention(q, k_cache, v_cache, table, lens, out, lse=None, weight=None, weight_out=None,
-                    scale: float = 0.0, stream=None):
+                    scale: float = 0.0, stream=None, k_scale=None, v_scale=None, window: int = 0, sink: int = 0):
     """shadowkv_paged_attention: attention of q [batch][n_q][d] over each sequence's first lens[b]
     rows of the paged cache into out (and its log-sum-exp into lse [batch][n_q], fp32).  With
     weight [batch][H][rows] the weight that each row received is added to it, in place or into
-    weight_out.  scale 0: 1/sqrt(d).  Returns out."""
+    weight_out.  scale 0: 1/sqrt(d).  Returns out.
+
+    shadowkv_paged_attention_ext: window > 0 leaves each sequence's last window rows and its first sink
+    ones; k_scale and v_scale, fp32 [n_pages][H][page_size / block], are the block scales of e4m3 pools
+    (q and out bf16)."""
     if weight is not None and weight_out is None:
         weight_out = weight
-    cache, fixed, pitch, nbytes = _paged_attention_plan(
+    cache, fixed, pitch, nbytes, block = _paged_attention_plan(
         _form(q), _form(k_cache), _form(v_cache), _form(table), _form(lens), _form(out), _form(lse), _form(weight),
-        _form(weight_out), scale)
+        _form(weight_out), scale, _form(k_scale), _form(v_scale), window, sink)
     device = q.device
     raw = _raw_stream(device, stream)
     space = _space(nbytes, device, stream, raw)
     try:
-        packed = _PAGED_ATTN.pack(
-            *cache, k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), *fixed, q.data_ptr(),
-            out.data_ptr(), _ptr(lse) or 0, _ptr(weight) or 0, _ptr(weight_out) or 0, pitch, space.at, nbytes)
-        _check(load().shadowkv_paged_attention(packed, raw), "shadowkv_paged_attention")
+        args = (*cache, k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), *fixed, q.data_ptr(),
+                out.data_ptr(), _ptr(lse) or 0, _ptr(weight) or 0, _ptr(weight_out) or 0, pitch, space.at, nbytes)
+        if block or window:
+            packed = _PAGED_ATTN_EXT.pack(*args, _ptr(k_scale) or 0, _ptr(v_scale) or 0, block, 0, window, sink)
+            _check(load().shadowkv_paged_attention_ext(packed, raw), "shadowkv_paged_attention_ext")
+        else:
+            _check(load().shadowkv_paged_attention(_PAGED_ATTN.pack(*args), raw), "shadowkv_paged_attention")
     finally:
         space.lock.release()
     return out
@@ -509,6 +546,46 @@ def paged_evict(k_cache, v_cache, table, lens, weight, position, budget: int, re
     finally:
         space.lock.release()
     return lens_out
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_codes_plan(w, k, v, k_cache, v_cache, k_scale, v_scale, table, lens, start, first):
+    if len(k[0]) != 3 or str(k[2]) not in ("torch.bfloat16", "torch.float32") or len(table[0]) != 2:
+        _refuse(w, "k and v are bf16 or fp32 [tokens][n_kv_heads][d], table int32 [batch][max_pages]")
+    batch, n = table[0][0], k[0][0]
+    cache = _pool_fields(w, k_cache, v_cache, table, lens, batch, True)
+    block = _scale_block(w, k_scale, v_scale, k_cache)
+    shape = (n, cache[1], cache[2])
+    ks, vs = _heads(w, "k", k, k[2], shape), _heads(w, "v", v, k[2], shape)
+    _vector(w, "start", start, batch + 1)
+    if first is not None:
+        _vector(w, "first", first, batch)
+    return cache, block, (n, SKV_F32 if str(k[2]) == "torch.float32" else SKV_BF16, *ks, *vs)
+
+
+def paged_quantise(k, v, k_cache, v_cache, k_scale, v_scale, table, lens, start, stream=None):
+    """shadowkv_paged_quantise: tokens start[b] .. start[b+1] of k and v [T][H][d] (bf16 or fp32) become rows
+    lens[b] on of sequence b, e4m3 codes in the pools and a power of two per block of rows and head in
+    k_scale and v_scale, fp32 [n_pages][H][page_size / block].  start is int32 [batch + 1]."""
+    cache, block, fixed = _paged_codes_plan("paged_quantise", _form(k), _form(v), _form(k_cache), _form(v_cache), _form(k_scale),
+                                            _form(v_scale), _form(table), _form(lens), _form(start), None)
+    packed = _QUANTISE.pack(*cache, k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), k_scale.data_ptr(),
+                            v_scale.data_ptr(), block, 0, *fixed, k.data_ptr(), v.data_ptr(), start.data_ptr())
+    _check(load().shadowkv_paged_quantise(packed, _raw_stream(k.device, stream)), "shadowkv_paged_quantise")
+
+
+def paged_dequantise(k_cache, v_cache, k_scale, v_scale, table, lens, first, start, k_out, v_out, stream=None):
+    """shadowkv_paged_dequantise: rows first[b] on of sequence b, as far as it has them, into tokens
+    start[b] .. start[b+1] of k_out and v_out [T][H][d] (bf16 or fp32).  Returns (k_out, v_out)."""
+    if first is None:
+        _refuse("paged_dequantise", "first is int32 [batch]")
+    cache, block, fixed = _paged_codes_plan("paged_dequantise", _form(k_out), _form(v_out), _form(k_cache), _form(v_cache),
+                                            _form(k_scale), _form(v_scale), _form(table), _form(lens), _form(start), _form(first))
+    packed = _DEQUANTISE.pack(*cache, k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(),
+                              k_scale.data_ptr(), v_scale.data_ptr(), block, 0, *fixed, k_out.data_ptr(), v_out.data_ptr(),
+                              start.data_ptr(), first.data_ptr())
+    _check(load().shadowkv_paged_dequantise(packed, _raw_stream(k_out.device, stream)), "shadowkv_paged_dequantise")
+    return k_out, v_out
 
 
 def paged_status(stream=None) -> int:

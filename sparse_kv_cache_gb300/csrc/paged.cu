@@ -43,12 +43,16 @@ bool on_device(const void* p, int dev) {
     return (a.type == cudaMemoryTypeDevice && a.device == dev) || a.type == cudaMemoryTypeManaged;
 }
 
-int key_bytes(int dtype) { return dtype == SKV_F32 ? 4 : 2; }
-int value_bytes(int dtype) { return dtype == SKV_F32 ? 4 : dtype == SKV_FP8 ? 1 : 2; }
+int wide_bytes(int dtype) { return dtype == SKV_F32 ? 4 : 2; }         // q and outputs
+int key_bytes(int dtype) { return dtype == SKV_E4M3 ? 1 : wide_bytes(dtype); }
+int value_bytes(int dtype) { return dtype == SKV_F32 ? 4 : dtype == SKV_BF16 ? 2 : 1; }
 
-bool good_type(const skv_paged_cache& c) {
-    return (c.dtype == SKV_F32 || c.dtype == SKV_BF16 || c.dtype == SKV_FP8) && c.n_kv_heads >= 1 &&
-           c.n_kv_heads <= (1 << 16) && (c.head_dim == 64 || c.head_dim == 128);
+// the types that a call takes: those of all calls, one more, or that one alone
+enum Types { kPlain, kAll, kCodes };
+bool good_type(const skv_paged_cache& c, Types types = kPlain) {
+    const bool plain = c.dtype == SKV_F32 || c.dtype == SKV_BF16 || c.dtype == SKV_FP8, codes = c.dtype == SKV_E4M3;
+    return ((plain && types != kCodes) || (codes && types != kPlain)) && c.n_kv_heads >= 1 && c.n_kv_heads <= (1 << 16) &&
+           (c.head_dim == 64 || c.head_dim == 128);
 }
 
 // a stride of whole 16-byte words
@@ -73,8 +77,8 @@ bool apart(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t d) {
 }
 
 // what the host can tell without the device
-int check_cache(const skv_paged_cache& c, bool written) {
-    if (!good_type(c)) return SKV_ERR_INVALID;
+int check_cache(const skv_paged_cache& c, bool written, Types types = kPlain) {
+    if (!good_type(c, types)) return SKV_ERR_INVALID;
     if (c.page_size < 8 || c.page_size > 1024 || (c.page_size & (c.page_size - 1))) return SKV_ERR_INVALID;
     if (c.max_pages < 1 || c.n_pages < 1 || c.n_pages > INT32_MAX || c.table_seq < c.max_pages) return SKV_ERR_INVALID;
     if (static_cast<int64_t>(c.max_pages) * c.page_size > kMaxRows) return SKV_ERR_INVALID;
@@ -107,6 +111,18 @@ int check_memory(std::initializer_list<const void*> ptrs, int dev) {
     return SKV_OK;
 }
 
+// scales of a cache that check_cache has seen
+int check_scales(const skv_paged_cache& c, const skv_block_scales& s) {
+    if (s.block < 8 || s.block > 128 || s.block > c.page_size || (s.block & (s.block - 1)) || s.reserved) return SKV_ERR_INVALID;
+    if (!s.k || !s.v) return SKV_ERR_INVALID;
+    return check_words({s.k, s.v});
+}
+int log2_of(int x) {
+    int lg = 0;
+    while ((1 << lg) < x) ++lg;
+    return lg;
+}
+
 PagedView view(const skv_paged_cache& c) {
     PagedView v{};
     v.k = c.k; v.v = c.v;
@@ -116,7 +132,7 @@ PagedView view(const skv_paged_cache& c) {
     v.lens = c.lens;
     v.n_pages = c.n_pages;
     v.batch = c.batch; v.H = c.n_kv_heads;
-    while ((1 << v.lg) < c.page_size) ++v.lg;
+    v.lg = log2_of(c.page_size);
     v.cap = c.max_pages * c.page_size;
     return v;
 }
@@ -146,9 +162,9 @@ int64_t round16(int64_t n) { return (n + 15) & ~int64_t(15); }
 struct AttnSpace { int Gp; int64_t joint, rec, rec_stat, stat, z, bytes; };
 
 // host-only part of the checks, and the workspace's layout
-int attn_space(const skv_paged_attention_args* a, AttnSpace* w) {
+int attn_space(const skv_paged_attention_args* a, AttnSpace* w, Types types = kPlain) {
     const skv_paged_cache& c = a->cache;
-    if (!good_type(c) || c.batch < 0 || a->n_q_heads < 1 || a->n_q_heads % c.n_kv_heads) return SKV_ERR_INVALID;
+    if (!good_type(c, types) || c.batch < 0 || a->n_q_heads < 1 || a->n_q_heads % c.n_kv_heads) return SKV_ERR_INVALID;
     const int G = a->n_q_heads / c.n_kv_heads;
     if (G > 8 || !std::isfinite(a->scale)) return SKV_ERR_INVALID;
     if (c.max_pages < 1 || c.page_size < 1 || static_cast<int64_t>(c.max_pages) * c.page_size > kMaxRows)
@@ -201,10 +217,20 @@ int evict_space(const skv_paged_evict_args* a, EvictSpace* w) {
 // stream's kernel sets in between is lost.
 __device__ int g_taken;
 std::mutex g_taking;       // g_taken is one call's at a time
-__global__ void k_take_status(int* a, int* b, int* c) {
-    const int x = atomicExch(a, 0), y = atomicExch(b, 0), z = atomicExch(c, 0);
-    g_taken = x ? x : y ? y : z;
+struct ErrorWords { int* at[5]; };
+__global__ void k_take_status(ErrorWords words) {
+    int taken = 0;
+    for (int* word : words.at) {
+        const int x = atomicExch(word, 0);
+        if (!taken) taken = x;
+    }
+    g_taken = taken;
 }
+
+// what attention takes of the rows: all of them, or the last `window` and the first `sink`
+struct Part { const skv_block_scales* scales; int window, sink; };
+
+int attend(const skv_paged_attention_args* a, const Part* part, const char* name, skv_stream stream);
 
 }  // namespace
 
@@ -287,13 +313,23 @@ int64_t shadowkv_paged_attention_workspace(const skv_paged_attention_args* a) {
 }
 
 int shadowkv_paged_attention(const skv_paged_attention_args* a, skv_stream stream) {
-    if (!a) return SKV_ERR_INVALID;
+    return a ? attend(a, nullptr, "shadowkv_paged_attention", stream) : SKV_ERR_INVALID;
+}
+
+}  // extern "C"
+
+namespace {
+int attend(const skv_paged_attention_args* a, const Part* part, const char* name, skv_stream stream) {
     const skv_paged_cache& c = a->cache;
+    const Types types = part ? kAll : kPlain;
     AttnSpace w;
-    if (int rc = attn_space(a, &w)) return rc;
+    if (int rc = attn_space(a, &w, types)) return rc;
     if (c.batch == 0) return SKV_OK;
-    if (int rc = check_cache(c, false)) return rc;
-    const int es = key_bytes(c.dtype), G = a->n_q_heads / c.n_kv_heads;
+    if (int rc = check_cache(c, false, types)) return rc;
+    const bool codes = c.dtype == SKV_E4M3;
+    if (codes)
+        if (int rc = check_scales(c, *part->scales)) return rc;
+    const int es = wide_bytes(c.dtype), G = a->n_q_heads / c.n_kv_heads;
     if (!c.lens || !a->q || !a->out || !a->workspace || !aligned16(a->q) || !aligned16(a->workspace)) return SKV_ERR_INVALID;
     if (!good_stride(a->q_seq, es) || !good_stride(a->q_head, es)) return SKV_ERR_INVALID;
     if (!aligned16(a->out) || !good_stride(a->out_seq, es) || !good_stride(a->out_head, es)) return SKV_ERR_INVALID;
@@ -306,10 +342,25 @@ int shadowkv_paged_attention(const skv_paged_attention_args* a, skv_stream strea
     if (int rc = device(&dev)) return rc;
     if (int rc = check_memory({c.k, c.v, c.table, c.lens, a->q, a->out, a->lse, a->weight, a->weight_out, a->workspace}, dev.id))
         return rc;
-    Range range("shadowkv_paged_attention");
+    if (codes)
+        if (int rc = check_memory({part->scales->k, part->scales->v}, dev.id)) return rc;
+    Range range(name);
     uint8_t* ws = static_cast<uint8_t*>(a->workspace);
     PagedAttnParams p{};
     p.c = view(c);
+    p.span = p.c.cap;
+    if (part) {
+        // a window of more rows than there can be shows them all
+        p.c.window = part->window ? std::min<int64_t>(part->window, kMaxRows) : static_cast<int>(kMaxRows);
+        p.c.sink = part->window ? std::min<int64_t>(part->sink, kMaxRows) : 0;
+        p.c.s16 = (p.c.sink + 15) & ~15;
+        p.span = static_cast<int>(std::min<int64_t>(p.c.cap, static_cast<int64_t>(p.c.window) + 15 + p.c.s16));
+        if (codes) {
+            p.ks = part->scales->k;
+            p.vs = part->scales->v;
+            p.lgb = log2_of(part->scales->block);
+        }
+    }
     p.G = G; p.n_q = a->n_q_heads;
     p.scale_log2 = static_cast<float>((a->scale != 0.f ? static_cast<double>(a->scale) : 1.0 / std::sqrt(double(c.head_dim))) *
                                       1.4426950408889634074);
@@ -324,8 +375,84 @@ int shadowkv_paged_attention(const skv_paged_attention_args* a, skv_stream strea
         p.Gp = w.Gp;
         p.weight = a->weight; p.weight_out = a->weight_out; p.row_pitch = a->row_pitch;
     }
-    return done(launch_paged_attn(c.dtype, c.head_dim, p,
-                                  paged_attn_ctas(c.dtype, c.head_dim, dev.nsm < kMaxSms ? dev.nsm : kMaxSms), stream));
+    const int ctas = paged_attn_ctas(c.dtype, c.head_dim, dev.nsm < kMaxSms ? dev.nsm : kMaxSms);
+    return done((part ? launch_paged_span : launch_paged_attn)(c.dtype, c.head_dim, p, ctas, stream));
+}
+}  // namespace
+
+extern "C" {
+
+int64_t shadowkv_paged_attention_ext_workspace(const skv_paged_attention_ext_args* a) {
+    if (!a || a->window < 0 || a->sink < 0) return SKV_ERR_INVALID;
+    if (a->attn.weight_out && (a->window || a->attn.cache.dtype == SKV_E4M3)) return SKV_ERR_INVALID;
+    AttnSpace w;
+    const int rc = attn_space(&a->attn, &w, kAll);
+    return rc ? rc : w.bytes;
+}
+
+int shadowkv_paged_attention_ext(const skv_paged_attention_ext_args* a, skv_stream stream) {
+    if (!a || a->window < 0 || a->sink < 0) return SKV_ERR_INVALID;
+    const bool codes = a->attn.cache.dtype == SKV_E4M3;
+    if (!codes && (a->scales.k || a->scales.v || a->scales.block || a->scales.reserved)) return SKV_ERR_INVALID;
+    if (!codes && !a->window) return shadowkv_paged_attention(&a->attn, stream);
+    if (a->attn.weight || a->attn.weight_out) return SKV_ERR_INVALID;
+    const Part part{&a->scales, a->window, a->sink};
+    return attend(&a->attn, &part, "shadowkv_paged_attention_ext", stream);
+}
+
+int shadowkv_paged_quantise(const skv_paged_quantise_args* a, skv_stream stream) {
+    if (!a) return SKV_ERR_INVALID;
+    const skv_paged_cache& c = a->cache;
+    if (!good_type(c, kCodes) || c.batch < 0 || a->tokens < 0 || (a->dtype != SKV_BF16 && a->dtype != SKV_F32)) return SKV_ERR_INVALID;
+    if (c.batch == 0 || a->tokens == 0) return SKV_OK;
+    if (int rc = check_cache(c, true, kCodes)) return rc;
+    if (int rc = check_scales(c, a->scales)) return rc;
+    const int es = wide_bytes(a->dtype);
+    if (!a->k || !a->v || !a->start || !c.lens || !aligned16(a->k) || !aligned16(a->v)) return SKV_ERR_INVALID;
+    for (int64_t s : {a->k_tok, a->k_head, a->v_tok, a->v_head})
+        if (!good_stride(s, es)) return SKV_ERR_INVALID;
+    if (int rc = check_words({c.table, c.lens, a->start})) return rc;
+    Device dev;
+    if (int rc = device(&dev)) return rc;
+    if (int rc = check_memory({c.k, c.v, c.table, c.lens, a->scales.k, a->scales.v, a->k, a->v, a->start}, dev.id)) return rc;
+    Range range("shadowkv_paged_quantise");
+    QuantParams p{};
+    p.c = view(c);
+    p.lgb = log2_of(a->scales.block);
+    p.tokens = a->tokens;
+    p.slots = quantise_slots(a->tokens, c.batch, p.lgb);
+    p.k_tok = a->k_tok; p.k_head = a->k_head; p.v_tok = a->v_tok; p.v_head = a->v_head;
+    p.k = a->k; p.v = a->v; p.k_scale = a->scales.k; p.v_scale = a->scales.v; p.start = a->start;
+    return done(launch_quantise(a->dtype, c.head_dim, p, stream));
+}
+
+int shadowkv_paged_dequantise(const skv_paged_dequantise_args* a, skv_stream stream) {
+    if (!a) return SKV_ERR_INVALID;
+    const skv_paged_cache& c = a->cache;
+    if (!good_type(c, kCodes) || c.batch < 0 || a->tokens < 0 || (a->dtype != SKV_BF16 && a->dtype != SKV_F32)) return SKV_ERR_INVALID;
+    if (c.batch == 0 || a->tokens == 0) return SKV_OK;
+    if (int rc = check_cache(c, false, kCodes)) return rc;
+    if (int rc = check_scales(c, a->scales)) return rc;
+    const int es = wide_bytes(a->dtype);
+    if (!a->k || !a->v || !a->start || !a->first || !c.lens || !aligned16(a->k) || !aligned16(a->v)) return SKV_ERR_INVALID;
+    for (int64_t s : {a->k_tok, a->k_head, a->v_tok, a->v_head})
+        if (!good_stride(s, es)) return SKV_ERR_INVALID;
+    if (!apart(a->tokens, a->k_tok, c.n_kv_heads, a->k_head, c.head_dim) ||
+        !apart(a->tokens, a->v_tok, c.n_kv_heads, a->v_head, c.head_dim))
+        return SKV_ERR_INVALID;
+    if (int rc = check_words({c.table, c.lens, a->start, a->first})) return rc;
+    Device dev;
+    if (int rc = device(&dev)) return rc;
+    if (int rc = check_memory({c.k, c.v, c.table, c.lens, a->scales.k, a->scales.v, a->k, a->v, a->start, a->first}, dev.id))
+        return rc;
+    Range range("shadowkv_paged_dequantise");
+    DequantParams p{};
+    p.c = view(c);
+    p.lgb = log2_of(a->scales.block);
+    p.tokens = a->tokens;
+    p.k_tok = a->k_tok; p.k_head = a->k_head; p.v_tok = a->v_tok; p.v_head = a->v_head;
+    p.k = a->k; p.v = a->v; p.k_scale = a->scales.k; p.v_scale = a->scales.v; p.start = a->start; p.first = a->first;
+    return done(launch_dequantise(a->dtype, c.head_dim, p, stream));
 }
 
 int64_t shadowkv_paged_evict_workspace(const skv_paged_evict_args* a) {
@@ -375,13 +502,15 @@ int shadowkv_paged_evict(const skv_paged_evict_args* a, skv_stream stream) {
 
 int shadowkv_paged_status(skv_stream stream) {
     std::lock_guard<std::mutex> mine(g_taking);
-    int *norm = nullptr, *attn = nullptr, *evict = nullptr, taken = 0;
-    if (cudaStreamSynchronize(stream) != cudaSuccess || norm_rope_err(&norm) != cudaSuccess ||
-        paged_attn_err(&attn) != cudaSuccess || evict_err(&evict) != cudaSuccess) {
+    ErrorWords words;
+    int taken = 0;
+    if (cudaStreamSynchronize(stream) != cudaSuccess || norm_rope_err(&words.at[0]) != cudaSuccess ||
+        paged_attn_err(&words.at[1]) != cudaSuccess || evict_err(&words.at[2]) != cudaSuccess ||
+        paged_span_err(&words.at[3]) != cudaSuccess || quantise_err(&words.at[4]) != cudaSuccess) {
         cudaGetLastError();
         return SKV_ERR_CUDA;
     }
-    k_take_status<<<1, 1, 0, stream>>>(norm, attn, evict);
+    k_take_status<<<1, 1, 0, stream>>>(words);
     if (cudaGetLastError() != cudaSuccess ||
         cudaMemcpyFromSymbolAsync(&taken, g_taken, sizeof(taken), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
         cudaStreamSynchronize(stream) != cudaSuccess) {

@@ -18,6 +18,7 @@ struct PagedView {
     int batch, H;
     int lg;        // log2(page_size)
     int cap;       // max_pages * page_size: rows a sequence can have
+    int window, sink, s16;      // attention over a part of the rows: last, first, those in whole tiles of 16
 };
 
 struct NormRopeParams {
@@ -51,10 +52,35 @@ struct PagedAttnParams {
     // weights: raw products q.k of every row [U][cap][Gp], and (base, 1 / sum) per head [U][G]
     float* z; float2* stat; int Gp;
     const float* weight; float* weight_out; int64_t row_pitch;
+    int span;                 // rows that a sequence can show at most
+    const float *ks, *vs; int lgb;      // e4m3: scales [n_pages][H][page_size >> lgb]
 };
 constexpr int kPaWarps = 4;                  // warps of a CTA of the attention
 int paged_attn_ctas(int dtype, int d, int nsm);     // CTAs that fill nsm SMs
 int launch_paged_attn(int dtype, int d, const PagedAttnParams& p, int ncta, cudaStream_t s);
+int launch_paged_span(int dtype, int d, const PagedAttnParams& p, int ncta, cudaStream_t s);
+
+struct QuantParams {
+    PagedView c;
+    int lgb, tokens;          // log2(rows of a block)
+    int64_t slots;            // places for blocks: quantise_slots()
+    int64_t k_tok, k_head, v_tok, v_head;
+    const void *k, *v;
+    float *k_scale, *v_scale;
+    const int32_t* start;
+};
+int64_t quantise_slots(int tokens, int batch, int lgb);
+int launch_quantise(int dtype, int d, const QuantParams& p, cudaStream_t s);
+
+struct DequantParams {
+    PagedView c;
+    int lgb, tokens;
+    int64_t k_tok, k_head, v_tok, v_head;
+    void *k, *v;
+    const float *k_scale, *v_scale;
+    const int32_t *start, *first;
+};
+int launch_dequantise(int dtype, int d, const DequantParams& p, cudaStream_t s);
 
 struct EvictParams {
     PagedView c;
@@ -69,10 +95,12 @@ struct EvictParams {
 };
 int launch_evict(const EvictParams& p, int nsm, cudaStream_t s);
 
-// The error words of the three kernel files on the current device.
+// The error words of the kernel files on the current device.
 cudaError_t norm_rope_err(int** p);
 cudaError_t paged_attn_err(int** p);
 cudaError_t evict_err(int** p);
+cudaError_t paged_span_err(int** p);
+cudaError_t quantise_err(int** p);
 
 #ifdef __CUDACC__
 // A kernel of a call's beginning: a programmatic dependent of whatever is before it in the stream,
@@ -127,6 +155,20 @@ __device__ __forceinline__ int rows_in(const PagedView& c, int n, int* err, int 
 }
 __device__ __forceinline__ int rows_of(const PagedView& c, int b, int* err, int where) {
     return rows_in(c, __ldcg(c.lens + b), err, where);
+}
+// The last sequence b whose key(start[b], b) is at most x, by the whole warp: 0 if there is none (keys do not
+// fall; where they do, whatever comes out is a sequence).
+template <class Key>
+__device__ __forceinline__ int find_sequence(const int32_t* start, int batch, int64_t x, Key key) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = batch;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+        const bool in = i < hi && (lane == 0 || key(__ldcg(start + i), i) <= x);
+        lo += (31 - __clz(__ballot_sync(0xffffffffu, in))) * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
 }
 // page of row i of sequence b, or -1 (and the error word) if its id is out of range
 __device__ __forceinline__ int page_of(const PagedView& c, int b, int i, int* err, int where) {
