@@ -686,11 +686,49 @@ typedef struct {
 int shadowkv_paged_dequantise(const skv_paged_dequantise_args* args, skv_stream stream);
 
 /*
+ * Attention of many new tokens per sequence: prompts, chunks of prompts, drafted tokens.  Tokens start[b] ..
+ * start[b+1] of q are the last rows of sequence b, whose keys and values are in the cache already and counted in
+ * lens[b]; token start[b+1] - 1 is row lens[b] - 1.  Token of row r sees row j <= r where window is 0, and
+ * otherwise where j > r - window or j < sink besides.  out and lse as for one token; a token that sees nothing (there
+ * are more tokens than rows, or its pages are bad) has out = 0 and lse = -inf.
+ *
+ * dtype SKV_BF16 (others: SKV_ERR_UNSUPPORTED; a cache of codes is read back by shadowkv_paged_dequantise into rows
+ * that make pages).  Strides of q and of the pools are above zero where there is more than one
+ * to step through, and below 2^40 bytes.  Whole pages are read, also behind a sequence's last row; what is in
+ * a row that a token does not see has no part in its result, whatever it is.  Pages of which no row is
+ * seen are not looked at.  start does not fall, start[0] >= 0, start[batch] <= tokens: the tokens of a sequence
+ * for which it does are left out and set the error word.  Tokens of no sequence are left as they are.
+ *
+ * Scores, sums and softmax statistics are fp32; probabilities are rounded to bf16 (2^-8 at most), and what is
+ * 2^-88 below a row's heaviest may weigh nothing (an infinite value there gives NaN).  Sums of values
+ * are cut off to fp32 at every 16 rows.  Keys that score -infinity count as absent.  Where a kernel's bounded wait ran
+ * out (shadowkv_paged_status: SKV_ERR_TIMEOUT) results are NaN.
+ */
+typedef struct {
+    skv_paged_cache cache;      /* dtype SKV_BF16; lens: with the new tokens' rows */
+    int32_t n_q_heads;
+    float scale;                /* 0: 1 / sqrt(head_dim) */
+    int32_t window, sink;       /* >= 0 */
+    int32_t tokens;             /* 0: nothing is done */
+    int32_t reserved;           /* 0 */
+    int64_t q_tok, q_head, out_tok, out_head;   /* strides, elements, of whole 16 bytes */
+    const void* q;              /* dev [tokens][n_q_heads][d], 16-byte aligned */
+    void* out;                  /* dev [tokens][n_q_heads][d], 16-byte aligned */
+    float* lse;                 /* dev [tokens][n_q_heads], or NULL */
+    const int32_t* start;       /* dev [batch + 1] */
+    void* workspace;            /* dev, 16-byte aligned; may be NULL where no bytes are asked for */
+    int64_t workspace_bytes;    /* >= shadowkv_paged_prompt_attention_workspace(args) */
+} skv_paged_prompt_args;
+int64_t shadowkv_paged_prompt_attention_workspace(const skv_paged_prompt_args* args);   /* bytes, or SKV_ERR_*; no CUDA call */
+int shadowkv_paged_prompt_attention(const skv_paged_prompt_args* args, skv_stream stream);
+
+/*
  * Status of the paged calls on the current device, of all streams: waits for
  * `stream`, then takes the error words and clears them in one step.  A call that
  * still runs on another stream is in it as far as it has come; what it sets
  * later is in the next status.  Returns SKV_OK, SKV_ERR_DEVICE_BOUNDS (a length,
- * index or page id was out of range; its access was skipped), or SKV_ERR_CUDA.
+ * index or page id was out of range; its access was skipped), SKV_ERR_TIMEOUT (a bounded wait inside a
+ * kernel ran out), or SKV_ERR_CUDA.
  * Not for use during stream capture.
  */
 int shadowkv_paged_status(skv_stream stream);

@@ -39,7 +39,8 @@ EXPORTED = ("shadowkv_validate_config", "shadowkv_prefill_index", "shadowkv_pref
             "shadowkv_qk_norm_rope", "shadowkv_paged_attention", "shadowkv_paged_attention_workspace",
             "shadowkv_paged_evict", "shadowkv_paged_evict_workspace", "shadowkv_paged_status",
             "shadowkv_paged_attention_ext", "shadowkv_paged_attention_ext_workspace",
-            "shadowkv_paged_quantise", "shadowkv_paged_dequantise")
+            "shadowkv_paged_quantise", "shadowkv_paged_dequantise",
+            "shadowkv_paged_prompt_attention", "shadowkv_paged_prompt_attention_workspace")
 
 # C layouts of the paged calls' argument structs (native sizes and alignment, as the header declares
 # them).  They are packed in one go: a decode step calls these once per layer, where filling a
@@ -51,6 +52,7 @@ _EVICT = struct.Struct(_CACHE + " 3i 4P q 2P q")
 _SCALES = "2P 2i"                                        # skv_block_scales
 _PAGED_ATTN_EXT = struct.Struct(_CACHE + " i f 4q 5P q P q " + _SCALES + " 2i")
 _QUANTISE = struct.Struct(_CACHE + " " + _SCALES + " 2i 4q 3P")
+_PROMPT = struct.Struct(_CACHE + " i f 4i 4q 5P q")
 _DEQUANTISE = struct.Struct(_CACHE + " " + _SCALES + " 2i 4q 4P")
 
 
@@ -143,10 +145,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.shadowkv_fetch_probe.restype = i32
     lib.shadowkv_sparse_attention_noalloc_status.restype = i32
     for name in ("shadowkv_qk_norm_rope", "shadowkv_paged_attention", "shadowkv_paged_evict", "shadowkv_paged_attention_ext",
-                 "shadowkv_paged_quantise", "shadowkv_paged_dequantise"):
+                 "shadowkv_paged_quantise", "shadowkv_paged_dequantise", "shadowkv_paged_prompt_attention"):
         getattr(lib, name).argtypes = [ctypes.c_char_p, vp]
         getattr(lib, name).restype = i32
-    for name in ("shadowkv_paged_attention_workspace", "shadowkv_paged_evict_workspace", "shadowkv_paged_attention_ext_workspace"):
+    for name in ("shadowkv_paged_attention_workspace", "shadowkv_paged_evict_workspace", "shadowkv_paged_attention_ext_workspace",
+                 "shadowkv_paged_prompt_attention_workspace"):
         getattr(lib, name).argtypes = [ctypes.c_char_p]
         getattr(lib, name).restype = i64
     lib.shadowkv_paged_status.argtypes = [vp]
@@ -501,6 +504,51 @@ def paged_attention(q, k_cache, v_cache, table, lens, out, lse=None, weight=None
             _check(load().shadowkv_paged_attention(_PAGED_ATTN.pack(*args), raw), "shadowkv_paged_attention")
     finally:
         space.lock.release()
+    return out
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_prompt_plan(q, k_cache, v_cache, table, lens, start, out, lse, scale, window, sink):
+    w = "paged_prompt_attention"
+    if len(q[0]) != 3 or len(table[0]) != 2:
+        _refuse(w, "q is [tokens][n_q_heads][d], table int32 [batch][max_pages]")
+    n, nq, d = q[0]
+    batch = table[0][0]
+    cache = _pool_fields(w, k_cache, v_cache, table, lens, batch)
+    if q[2] != k_cache[2] or cache[2] != d:
+        _refuse(w, f"q is {k_cache[2]} [tokens][n_q_heads][{cache[2]}]")
+    qs, os_ = _heads(w, "q", q, q[2], (n, nq, d)), _heads(w, "out", out, q[2], (n, nq, d))
+    _vector(w, "start", start, batch + 1)
+    if lse is not None and (lse[0] != (n, nq) or lse[1] != (nq, 1) or str(lse[2]) != "torch.float32"):
+        _refuse(w, "lse is fp32 [tokens][n_q_heads], contiguous")
+    if not (isinstance(window, int) and isinstance(sink, int) and 0 <= window < 1 << 31 and 0 <= sink < 1 << 31):
+        _refuse(w, "window and sink are numbers of rows")
+    fixed = (nq, scale, window, sink, n, 0, *qs, *os_)
+    nbytes = load().shadowkv_paged_prompt_attention_workspace(_PROMPT.pack(*cache, *(0,) * 4, *fixed, *(0,) * 6))
+    if nbytes < 0:
+        _check(int(nbytes), "shadowkv_paged_prompt_attention_workspace")
+    return cache, fixed, nbytes
+
+
+def paged_prompt_attention(q, k_cache, v_cache, table, lens, start, out, lse=None, scale: float = 0.0, window: int = 0,
+                           sink: int = 0, stream=None):
+    """shadowkv_paged_prompt_attention: causal attention of q [T][n_q][d] (bf16), tokens start[b] .. start[b+1] being the
+    last rows of the lens[b] that sequence b has in the paged cache, into out (and the log-sum-exp into lse
+    [T][n_q], fp32); with window > 0 each token sees the window rows up to its own and the first sink ones.
+    start is int32 [batch + 1].  scale 0: 1/sqrt(d).  Returns out."""
+    cache, fixed, nbytes = _paged_prompt_plan(_form(q), _form(k_cache), _form(v_cache), _form(table), _form(lens), _form(start),
+                                              _form(out), _form(lse), scale, window, sink)
+    device = q.device
+    raw = _raw_stream(device, stream)
+    space = _space(nbytes, device, stream, raw) if nbytes else None
+    try:
+        packed = _PROMPT.pack(
+            *cache, k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(), *fixed, q.data_ptr(), out.data_ptr(),
+            _ptr(lse) or 0, start.data_ptr(), space.at if space else 0, nbytes)
+        _check(load().shadowkv_paged_prompt_attention(packed, raw), "shadowkv_paged_prompt_attention")
+    finally:
+        if space:
+            space.lock.release()
     return out
 
 

@@ -1,0 +1,663 @@
+// Attention of many new tokens per sequence over its paged cache (shadowkv_paged_prompt_attention): bf16, causal, whole
+// or through a window with first rows.
+//
+// out = softmax(scale q.K^T).V, row r seeing rows j <= r with (window) j > r - window or j < sink.  4 d flops
+// for every (token, query head, row seen): the fifth-generation tensor cores bound it where tokens are many, memory
+// where they are few.
+//
+// A CTA takes 256 query rows of one KV head -- 2 x tq tokens times its G query heads, two halves of 128 rows with an
+// accumulator each -- and walks the tiles of 128 rows that any of them sees.  Both halves use each tile of keys
+// and values: with one half the L2 would have to deliver 64 bytes per clock to every SM, more than it has.
+//   warp 8       page ids, TMA of queries, keys and values (pages are boxes of a tensor map)
+//   warp 9       S = Q.K^T (both operands in shared memory), O += P.V (P in tensor memory, V as it lies in the
+//                pages: its dimension is the one along the rows of a page, so the operand is MN-major)
+//   warps 0-7    a thread per query row: scores from tensor memory into registers, softmax, P back
+//   warps 10, 11 values of tiles at an edge: rows that no query sees become zeros, and whether an element that is
+//                not finite is among the others, which must not meet a probability of zero
+// While one half's warps form its probabilities, the tensor cores have the other half's two products.
+//
+// The tensor memory holds S of both halves and O of both, 512 columns; P takes the place of its S.  A half's
+// products are issued in the order P(j).V, Q.K(j+1): they execute in that order, so what says that the second
+// is done says it of the first too, and a thread that has the scores of tile j + 1 may rescale O.
+//
+// Probabilities are rounded to bf16 once, off by 2^-9 of each on average: as far as the result's own rounding moves it
+// (two terms would double the second product).  They are 2^-8 over the table's rows of a probability that is not
+// normalised, in the exponent, so that no sum of values passes the type's largest; O and the sums of
+// probabilities, in fp32, take the same factor, and it cancels.
+#include <math_constants.h>
+
+#include <algorithm>
+
+#include "skv_common.cuh"
+#include "skv_internal.h"
+#include "skv_paged.h"
+
+namespace skv {
+
+static __device__ int g_err[2];
+
+constexpr int kPrTile = 128;                   // rows of a tile of keys
+constexpr int kPrHalf = 128;                   // query rows of an accumulator
+constexpr int kPrThreads = 384;
+constexpr float kPrSlack = 8.f;                // the base moves when a score passes it by 2^8
+constexpr int kPrStages = 2;                   // tiles of keys, and of values, on their way or in use
+// registers of a thread: 384 x 168 at launch; the eight warps with a row per thread take 208, the others 88
+constexpr int kPrRegsMore = 208, kPrRegsLess = 88;
+static_assert(256 * kPrRegsMore + 128 * kPrRegsLess <= kPrThreads * 168, "");
+
+__device__ __forceinline__ float pr_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// A wait that ends after about a second, or once another of the CTA's has; false then.
+__device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*dead) return false;
+        if (globaltimer() - t0 > kWaitLimitNs) {
+            *dead = 1;
+            set_err(g_err, DEV_ERR_TIMEOUT, 911);
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem], A 128 x 16 bf16 packed in pairs
+__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// An operand that is stored along its M or N dimension, 128-byte swizzle: rows of 64 elements, one per k, in
+// groups of eight (1024 bytes apart); the next 64 elements lie `next` bytes away.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t next) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(next >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    d |= static_cast<uint64_t>(2) << 61;
+    return d;
+}
+constexpr uint32_t kBIsMN = 1u << 16;          // instruction descriptor: B is stored along N
+
+#define PR_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
+#define PR_W8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
+// Columns of this thread's lane, there when the function returns (the wait is in the same statement, so that nothing
+// that uses them can come before it).
+__device__ __forceinline__ void tmem_get32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        : PR_R8(r, 0), PR_R8(r, 8), PR_R8(r, 16), PR_R8(r, 24)
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_get128(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,"
+        "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
+        "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,"
+        "%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
+        "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : PR_R8(r, 0), PR_R8(r, 8), PR_R8(r, 16), PR_R8(r, 24), PR_R8(r, 32), PR_R8(r, 40), PR_R8(r, 48), PR_R8(r, 56),
+          PR_R8(r, 64), PR_R8(r, 72), PR_R8(r, 80), PR_R8(r, 88), PR_R8(r, 96), PR_R8(r, 104), PR_R8(r, 112), PR_R8(r, 120)
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t tmem_get1(uint32_t taddr) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(r) : "r"(taddr) : "memory");
+    return r;
+}
+__device__ __forceinline__ void tmem_put32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::PR_W8(r, 0), PR_W8(r, 8), PR_W8(r, 16), PR_W8(r, 24),
+        "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ------------------------------------------------------------------ what a CTA does
+
+// The unit of a CTA: tokens `tok` .. of the call, at rows row0 .. of sequence b; its tiles are positions
+// lo .. hi of the list [0, ts), [tw, ..) of tiles.
+struct PrUnit {
+    int b, h, split, tok, ntok, row0, ts, tw, lo, hi;
+    __device__ __forceinline__ int tile(int pos) const { return pos < ts ? pos : tw + (pos - ts); }
+};
+// Rows that the tokens first .. last of a sequence see.
+struct PrSees {
+    int first, last, window, sink;      // window 0: all up to one's own
+    // whether some of them sees one of the rows a .. z, and whether all of them see all those rows
+    __device__ __forceinline__ bool any(int a, int z) const {
+        return a <= last && (window == 0 || a < sink || z > first - window);
+    }
+    __device__ __forceinline__ bool all(int a, int z) const {
+        return z <= first && (window == 0 || a > last - window || z < sink);
+    }
+};
+__device__ __forceinline__ PrSees sees(const PromptParams& p, const PrUnit& u, int half) {
+    const int from = half * p.tq, to = min(u.ntok, from + p.tq);       // tokens of the unit: half 2 is both
+    return half == 2 ? PrSees{u.row0, u.row0 + u.ntok - 1, p.c.window, p.c.sink}
+                     : PrSees{u.row0 + from, u.row0 + to - 1, p.c.window, p.c.sink};
+}
+// whether a tile has a row that not all of the unit's tokens see
+__device__ __forceinline__ bool at_edge(const PrSees& both, int tile) { return !both.all(tile * kPrTile, tile * kPrTile + kPrTile - 1); }
+
+// By one warp: which unit a block has; ntok 0 if none.
+__device__ __forceinline__ PrUnit find_unit(const PromptParams& p, int64_t block) {
+    const int t2 = 2 * p.tq;
+    PrUnit u{};
+    u.split = static_cast<int>(block % p.nsplit);
+    block /= p.nsplit;
+    u.h = static_cast<int>(block % p.c.H);
+    // the last tokens of a sequence see most: their units start first
+    const int64_t slot = p.slots - 1 - block / p.c.H;
+    u.b = find_sequence(p.start, p.c.batch, slot, [&](int s, int i) { return static_cast<int64_t>(s / t2) + i; });
+    const int t0 = __ldcg(p.start + u.b), t1 = __ldcg(p.start + u.b + 1);
+    const int len = rows_of(p.c, u.b, g_err, 912);
+    if (t0 < 0 || t1 < t0 || t1 > p.tokens) {
+        set_err(g_err, DEV_ERR_BOUNDS, 913);
+        return u;
+    }
+    const int64_t skip = (slot - (static_cast<int64_t>(t0 / t2) + u.b)) * t2;
+    if (skip < 0 || skip >= t1 - t0) return u;
+    u.tok = t0 + static_cast<int>(skip);
+    u.ntok = min(t2, t1 - u.tok);
+    u.row0 = len - (t1 - u.tok);
+    // tiles: those of the first rows, then from the first token's window to the last token
+    const int last = u.row0 + u.ntok - 1;
+    if (last >= 0) {
+        const int upto = last / kPrTile;
+        u.tw = p.c.window ? max(0, u.row0 - p.c.window + 1) / kPrTile : 0;
+        u.ts = p.c.window ? min(u.tw, (p.c.sink + kPrTile - 1) / kPrTile) : 0;
+        const int64_t n = u.ts + upto - u.tw + 1;
+        u.lo = static_cast<int>(n * u.split / p.nsplit);
+        u.hi = static_cast<int>(n * (u.split + 1) / p.nsplit);
+    }
+    return u;
+}
+
+template <int D>
+struct PrSmem {
+    static constexpr int kParts = D / 64;                            // 64 dimensions of 128 rows: 16 KB
+    static constexpr int kTileBytes = kParts * 16384;
+    static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kPrStages * kTileBytes, kBytes = kV + kPrStages * kTileBytes;
+};
+struct PrShared {
+    uint64_t q_full, k_full[kPrStages], k_empty[kPrStages], v_full[kPrStages], v_ok[kPrStages], v_empty[kPrStages];
+    uint64_t s_full[2], p_full[2], o_full[2];
+    PrUnit unit;
+    uint32_t tmem;
+    int dead;
+    int absent[4];             // per tile (mod 4): groups of eight rows whose page is out of range or not looked at
+    int wild[kPrStages][2];    // a tile at an edge has values that are not finite (what each of the two warps found)
+    uint64_t given_up;         // the products that were under way
+    __device__ __forceinline__ bool is_wild(int s) const {
+        const volatile int* w = wild[s];
+        return (w[0] | w[1]) != 0;
+    }
+};
+
+// ------------------------------------------------------------------ the roles
+
+template <int D>
+__device__ void pr_load(const PromptParams& p, const CUtensorMap* mq, const CUtensorMap* mk, const CUtensorMap* mv, PrShared& sh,
+                        uint8_t* base) {
+    using L = PrSmem<D>;
+    const PrUnit u = sh.unit;
+    const PrSees both = sees(p, u, 2);
+    const int lane = threadIdx.x & 31;
+    const int box = min(kPrTile, 1 << p.c.lg), boxes = kPrTile / box, mask = (1 << p.c.lg) - 1;
+    const uint32_t at = smem_u32(base);
+    // rows that kernels before this one wrote, to be read by the copy engine
+    asm volatile("fence.proxy.async;" ::: "memory");
+    const int halves = u.ntok > p.tq ? 2 : 1, j = lane % boxes, part = lane / boxes;
+    if (u.lo >= u.hi) return;
+    if (lane == 0) {
+        mbar_arrive_expect_tx(&sh.q_full, halves * L::kParts * p.tq * p.G * 128);
+        for (int x = 0; x < halves; ++x)
+            for (int i = 0; i < L::kParts; ++i)
+                tma_load_3d(at + L::kQ + x * L::kTileBytes + i * 16384, mq, i * 64, u.h * p.G, u.tok + x * p.tq, &sh.q_full);
+    }
+    int keys = 0, vals = 0;                        // tiles that are on their way or there
+    for (int pos = u.lo; pos < u.hi; ++pos) {
+        const int n = pos - u.lo, s = n % kPrStages, row = u.tile(pos) * kPrTile;
+        const uint32_t parity = (n / kPrStages + 1) & 1;
+        int page = -1;
+        if (lane < boxes && both.any(row + lane * box, row + lane * box + box - 1)) page = page_of(p.c, u.b, row + lane * box, g_err, 914);
+        const uint32_t gone = __ballot_sync(0xffffffffu, page < 0);
+        // (a page beyond the pool is read as zeros)
+        const int z = __shfl_sync(0xffffffffu, page < 0 ? static_cast<int>(p.c.n_pages) : page, j);
+        const int in_page = (row + j * box) & mask;
+        const uint32_t to = at + s * L::kTileBytes + part * 16384 + j * box * 128;
+        if (!__all_sync(0xffffffffu, pr_wait(&sh.k_empty[s], parity, &sh.dead))) break;
+        if (lane == 0) {
+            int absent = 0;
+            for (int i = 0; i < 16; ++i) absent |= (gone >> (i * 8 / box) & 1) << i;
+            sh.absent[n & 3] = absent;
+            mbar_arrive_expect_tx(&sh.k_full[s], L::kTileBytes);
+        }
+        __syncwarp();
+        if (part < L::kParts) tma_load_4d(to + L::kK, mk, part * 64, in_page, u.h, z, &sh.k_full[s]);
+        keys = n + 1;
+        if (!__all_sync(0xffffffffu, pr_wait(&sh.v_empty[s], parity, &sh.dead))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&sh.v_full[s], L::kTileBytes);
+        __syncwarp();
+        if (part < L::kParts) tma_load_4d(to + L::kV, mv, part * 64, in_page, u.h, z, &sh.v_full[s]);
+        vals = n + 1;
+    }
+    if (*const_cast<volatile int*>(&sh.dead)) {
+        // given up: no copy may be on its way when the CTA ends
+        mbar_wait(&sh.q_full, 0);
+        for (int n = max(0, keys - kPrStages); n < keys; ++n) mbar_wait(&sh.k_full[n % kPrStages], (n / kPrStages) & 1);
+        for (int n = max(0, vals - kPrStages); n < vals; ++n) mbar_wait(&sh.v_full[n % kPrStages], (n / kPrStages) & 1);
+    }
+}
+
+template <int D>
+__device__ bool pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) {
+    using L = PrSmem<D>;
+    const PrUnit u = sh.unit;
+    const PrSees both = sees(p, u, 2);
+    const uint32_t at = smem_u32(base), tmem = sh.tmem;
+    const int halves = u.ntok > p.tq ? 2 : 1, tiles = u.hi - u.lo;
+    if (tiles <= 0) return true;
+    constexpr uint32_t qk = idesc_bf16_f32(kPrHalf, kPrTile), pv = idesc_bf16_f32(kPrHalf, D) | kBIsMN;
+    auto scores = [&](int x, int n) {
+        const uint32_t q = at + L::kQ + x * L::kTileBytes, k = at + L::kK + (n % kPrStages) * L::kTileBytes;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            tc_mma_bf16(tmem + x * 128, smem_desc_sw128(q + (i / 4) * 16384 + (i % 4) * 32),
+                        smem_desc_sw128(k + (i / 4) * 16384 + (i % 4) * 32), qk, i > 0);
+        tc_commit(&sh.s_full[x]);
+    };
+    auto values = [&](int x, int n) {
+        const uint32_t v = at + L::kV + (n % kPrStages) * L::kTileBytes;
+#pragma unroll
+        for (int i = 0; i < kPrTile / 16; ++i)
+            tc_mma_bf16_ts(tmem + 256 + x * 128, tmem + x * 128 + i * 8, smem_desc_mn(v + i * 2048, 16384), pv, n > 0 || i > 0);
+    };
+    if (!pr_wait(&sh.q_full, 0, &sh.dead) || !pr_wait(&sh.k_full[0], 0, &sh.dead)) return false;
+    for (int x = 0; x < halves; ++x) scores(x, 0);
+    tc_commit(&sh.k_empty[0]);
+    for (int n = 0; n < tiles; ++n) {
+        const int s = n % kPrStages, next = (n + 1) % kPrStages;
+        if (!pr_wait(&sh.v_ok[s], (n / kPrStages) & 1, &sh.dead)) return false;
+        const bool wild = at_edge(both, u.tile(u.lo + n)) && sh.is_wild(s);
+        for (int x = 0; x < halves; ++x) {
+            if (!pr_wait(&sh.p_full[x], n & 1, &sh.dead)) return false;
+            tc_fence_after();
+            if (!wild) values(x, n);       // otherwise the row's threads have done it
+            if (x == halves - 1) tc_commit(&sh.v_empty[s]);
+            if (n + 1 < tiles) {
+                if (x == 0 && !pr_wait(&sh.k_full[next], ((n + 1) / kPrStages) & 1, &sh.dead)) return false;
+                scores(x, n + 1);
+                if (x == halves - 1) tc_commit(&sh.k_empty[next]);
+            } else {
+                tc_commit(&sh.o_full[x]);
+            }
+        }
+    }
+    return true;
+}
+
+template <int D>
+__device__ void pr_look(const PromptParams& p, PrShared& sh, uint8_t* base) {
+    using L = PrSmem<D>;
+    const PrUnit u = sh.unit;
+    const PrSees both = sees(p, u, 2);
+    const int t = threadIdx.x - 320, warp = t >> 5;   // of 64
+    for (int n = 0; n < u.hi - u.lo; ++n) {
+        const int s = n % kPrStages, tile = u.tile(u.lo + n);
+        if (!__all_sync(0xffffffffu, pr_wait(&sh.v_full[s], (n / kPrStages) & 1, &sh.dead))) return;
+        if (at_edge(both, tile)) {
+            uint32_t some = 0;
+            uint8_t* v = base + L::kV + s * L::kTileBytes;
+            for (int part = 0; part < L::kParts; ++part)
+#pragma unroll 4
+                for (int r = t >> 3; r < kPrTile; r += 8) {
+                    uint4* w = reinterpret_cast<uint4*>(v + part * 16384 + r * 128 + (t & 7) * 16);
+                    const int row = tile * kPrTile + r;
+                    if (!both.any(row, row)) {
+                        *w = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    const uint4 x = *w;
+                    // an exponent of ones carries into the bit above it
+                    some |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                            ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+                }
+            const bool found = __any_sync(0xffffffffu, some & 0x80008000u);
+            if ((t & 31) == 0) sh.wild[s][warp] = found;
+            fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if ((t & 31) == 0) mbar_arrive(&sh.v_ok[s]);
+    }
+}
+
+// O of this thread's row += P.V on the CUDA cores, element by element that the row sees: for a tile at an edge with
+// values that are not finite.
+template <int D>
+__device__ __noinline__ void pr_by_hand(uint32_t o_tmem, uint32_t p_tmem, const uint8_t* v, bool first) {
+    for (int d0 = 0; d0 < D; d0 += 32) {
+        uint32_t raw[32];
+        float o[32];
+        if (!first) tmem_get32(o_tmem + d0, raw);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = first ? 0.f : __uint_as_float(raw[i]);
+        for (int j = 0; j < kPrTile; ++j) {
+            const uint32_t two = tmem_get1(p_tmem + j / 2);
+            const float w = j & 1 ? bf16hi(two) : bf16lo(two);
+            const uint8_t* row = v + (d0 / 64) * 16384 + j * 128;
+            if (w != 0.f) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float x[8];
+                    load8(reinterpret_cast<const __nv_bfloat16*>(row + (((d0 / 8 + c) & 7) ^ (j & 7)) * 16), x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[8 * c + i] = fmaf(w, x[i], o[8 * c + i]);
+                }
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) raw[i] = __float_as_uint(o[i]);
+        tmem_put32(o_tmem + d0, raw);
+    }
+    tmem_put_wait();
+}
+
+template <int D>
+__device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
+    using L = PrSmem<D>;
+    const PrUnit u = sh.unit;
+    const int half = threadIdx.x >> 7, r = threadIdx.x & 127;
+    const int tiles = u.hi - u.lo;
+    if (half * p.tq >= u.ntok) return;
+    const PrSees mine = sees(p, u, half), both = sees(p, u, 2);
+    const int t = min(r / p.G, p.tq - 1), token = half * p.tq + t;      // (rows beyond the last token repeat its)
+    const int row = min(u.row0 + token, mine.last);
+    const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;      // 32 lanes of the tensor memory
+    const uint32_t s_at = sh.tmem + lanes + half * 128, o_at = sh.tmem + lanes + 256 + half * 128;
+    const float scale = p.scale_log2;
+    const bool falls = scale < 0.f;
+    const float none = falls ? CUDART_INF_F : -CUDART_INF_F;             // the product that scores -infinity
+    float m = -CUDART_INF_F, l = 0.f;
+    bool good = true;
+    for (int n = 0; n < tiles; ++n) {
+        const int tile = u.tile(u.lo + n), first = tile * kPrTile;
+        good = pr_wait(&sh.s_full[half], n & 1, &sh.dead);
+        if (!__all_sync(0xffffffffu, good)) { good = false; break; }
+        tc_fence_after();
+        uint32_t raw[128];
+        tmem_get128(s_at, raw);
+        const int absent = *const_cast<volatile int*>(&sh.absent[n & 3]);
+        if (absent || !mine.all(first, first + kPrTile - 1)) {
+            const int hi = row - first, lo = mine.window ? hi - mine.window : -1, sink = mine.window ? mine.sink - first : 0;
+#pragma unroll
+            for (int i = 0; i < 128; ++i) {
+                const bool in = i <= hi && (i > lo || i < sink) && !(absent >> (i / 8) & 1);
+                raw[i] = in ? raw[i] : __float_as_uint(none);
+            }
+        }
+        float top[4];
+        if (falls) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top[i] = __uint_as_float(raw[i]);
+#pragma unroll
+            for (int i = 4; i < 128; ++i) top[i & 3] = fminf(top[i & 3], __uint_as_float(raw[i]));
+            top[0] = fminf(fminf(top[0], top[1]), fminf(top[2], top[3])) * scale;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top[i] = __uint_as_float(raw[i]);
+#pragma unroll
+            for (int i = 4; i < 128; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(raw[i]));
+            top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+        }
+        if (__any_sync(0xffffffffu, top[0] > m + kPrSlack)) {
+            const float now = fmaxf(m, top[0]);
+            const float w = m == -CUDART_INF_F ? 0.f : pr_exp2(m - now);
+            m = now;
+            l *= w;
+            if (n > 0) {
+#pragma unroll 1
+                for (int d0 = 0; d0 < D; d0 += 32) {
+                    uint32_t o[32];
+                    tmem_get32(o_at + d0, o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * w);
+                    tmem_put32(o_at + d0, o);
+                }
+            }
+        }
+        const float minus = m == -CUDART_INF_F ? 0.f : -(m + p.down_bits);
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+            const float a = pr_exp2(fmaf(__uint_as_float(raw[2 * i]), scale, minus));
+            const float b = pr_exp2(fmaf(__uint_as_float(raw[2 * i + 1]), scale, minus));
+            sum[(2 * i) & 3] += a;
+            sum[(2 * i + 1) & 3] += b;
+            raw[i] = pack_bf16x2(a, b);
+        }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        tmem_put32(s_at, raw);
+        tmem_put32(s_at + 32, raw + 32);
+        tmem_put_wait();
+        if (at_edge(both, tile)) {
+            const int s = n % kPrStages;
+            good = pr_wait(&sh.v_ok[s], (n / kPrStages) & 1, &sh.dead);
+            if (!__all_sync(0xffffffffu, good)) { good = false; break; }
+            if (sh.is_wild(s)) pr_by_hand<D>(o_at, s_at, base + L::kV + s * L::kTileBytes, n == 0);
+        }
+        tc_fence_before();
+        mbar_arrive(&sh.p_full[half]);
+    }
+    if (good && tiles > 0) {
+        good = pr_wait(&sh.o_full[half], 0, &sh.dead);
+        good = __all_sync(0xffffffffu, good);
+        tc_fence_after();
+    }
+    const bool live = r < p.tq * p.G && token < u.ntok;
+    const int g = r % p.G;
+    const int64_t head = static_cast<int64_t>(u.h) * p.G + g, tok = u.tok + token;
+    const float base2 = m == -CUDART_INF_F ? m : m + p.down_bits;
+    if (p.nsplit > 1) {
+        const int64_t rec = static_cast<int64_t>(blockIdx.x) * 2 * kPrHalf + threadIdx.x;
+        if (live) p.part_stat[rec] = good ? make_float2(base2, l) : make_float2(0.f, CUDART_NAN_F);
+        if (!good || tiles <= 0) return;
+#pragma unroll 1
+        for (int d0 = 0; d0 < D; d0 += 32) {
+            uint32_t o[32];
+            tmem_get32(o_at + d0, o);
+            if (live) {
+                uint4* dst = reinterpret_cast<uint4*>(p.part + rec * D + d0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+        }
+        return;
+    }
+    const float inv = !good ? CUDART_NAN_F : l == 0.f ? 0.f : 1.f / l;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + tok * p.o_tok + head * p.o_head;
+#pragma unroll 1
+    for (int d0 = 0; d0 < D; d0 += 32) {
+        uint32_t o[32];
+        if (good && tiles > 0) {
+            tmem_get32(o_at + d0, o);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0;
+        }
+        if (live) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = l == 0.f && good ? 0.f : __uint_as_float(o[8 * c + i]) * inv;
+                store8(out + d0 + 8 * c, x);
+            }
+        }
+    }
+    if (live && p.lse) p.lse[tok * p.n_q + head] = !good ? CUDART_NAN_F : l == 0.f ? -CUDART_INF_F : (base2 + log2f(l)) * 0.693147180559945309f;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPrThreads, 1) k_prompt_attn(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap mq,
+                                                               const __grid_constant__ CUtensorMap mk,
+                                                               const __grid_constant__ CUtensorMap mv) {
+    extern __shared__ uint8_t s_raw[];
+    __shared__ PrShared sh;
+    uint8_t* base = s_raw + ((1024 - (smem_u32(s_raw) & 1023)) & 1023);
+    begin_call();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == 8) {
+        const PrUnit u = find_unit(p, blockIdx.x);
+        if (lane == 0) {
+            sh.unit = u;
+            sh.dead = 0;
+            mbar_init(&sh.q_full, 1);
+            for (int s = 0; s < kPrStages; ++s) {
+                mbar_init(&sh.k_full[s], 1);
+                mbar_init(&sh.k_empty[s], 1);
+                mbar_init(&sh.v_full[s], 1);
+                mbar_init(&sh.v_ok[s], 2);
+                mbar_init(&sh.v_empty[s], 1);
+            }
+            mbar_init(&sh.given_up, 1);
+            for (int x = 0; x < 2; ++x) {
+                mbar_init(&sh.s_full[x], 1);
+                mbar_init(&sh.p_full[x], kPrHalf);
+                mbar_init(&sh.o_full[x], 1);
+            }
+            fence_mbar_init();
+            prefetch_tensormap(&mq);
+            prefetch_tensormap(&mk);
+            prefetch_tensormap(&mv);
+        }
+    }
+    __syncthreads();
+    if (sh.unit.ntok == 0) return;
+    if (warp == 9) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrRegsMore));
+        pr_softmax<D>(p, sh, base);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrRegsLess));
+        if (warp == 8) pr_load<D>(p, &mq, &mk, &mv, sh, base);
+        else if (warp == 9) {
+            if (lane == 0 && !pr_multiply<D>(p, sh, base)) {
+                tc_commit(&sh.given_up);
+                mbar_wait(&sh.given_up, 0);
+            }
+        } else pr_look<D>(p, sh, base);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(sh.tmem, 512);
+    }
+}
+
+// Joins the parts of the units' rows in their order: a block per unit, a thread per row and four dimensions.
+template <int D>
+__global__ void __launch_bounds__(256) k_prompt_merge(const __grid_constant__ PromptParams p) {
+    __shared__ PrUnit s_unit;
+    pdl_wait();
+    pdl_trigger();
+    if (threadIdx.x < 32) {
+        const PrUnit u = find_unit(p, static_cast<int64_t>(blockIdx.x) * p.nsplit);
+        if (threadIdx.x == 0) s_unit = u;
+    }
+    __syncthreads();
+    const PrUnit u = s_unit;
+    const int rows = u.ntok * p.G;
+    for (int k = threadIdx.x + blockIdx.y * 256; k < rows * (D / 4); k += 256 * gridDim.y) {
+        const int i = k / (D / 4), dim = 4 * (k % (D / 4)), token = i / p.G, g = i % p.G;
+        const int half = token / p.tq, r = (token - half * p.tq) * p.G + g;
+        const int64_t rec = static_cast<int64_t>(blockIdx.x) * p.nsplit * 2 * kPrHalf + half * kPrHalf + r;
+        float m = -CUDART_INF_F, l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int s = 0; s < p.nsplit; ++s) m = fmaxf(m, __ldcg(p.part_stat + rec + s * 2 * kPrHalf).x);
+        for (int s = 0; s < p.nsplit; ++s) {
+            const float2 st = __ldcg(p.part_stat + rec + s * 2 * kPrHalf);
+            if (st.y == 0.f) continue;             // this part sees nothing
+            const float w = st.x == -CUDART_INF_F ? CUDART_NAN_F : pr_exp2(st.x - m);
+            const float4 o = st.y != st.y ? make_float4(st.y, st.y, st.y, st.y)
+                                          : __ldcg(reinterpret_cast<const float4*>(p.part + (rec + s * 2 * kPrHalf) * D + dim));
+            l = fmaf(st.y, w, l);
+            x[0] = fmaf(o.x, w, x[0]);
+            x[1] = fmaf(o.y, w, x[1]);
+            x[2] = fmaf(o.z, w, x[2]);
+            x[3] = fmaf(o.w, w, x[3]);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t head = static_cast<int64_t>(u.h) * p.G + g, tok = u.tok + token;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + tok * p.o_tok + head * p.o_head + dim) =
+            make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+        if (dim == 0 && p.lse) p.lse[tok * p.n_q + head] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.693147180559945309f;
+    }
+}
+
+// ------------------------------------------------------------------ launches
+
+int64_t prompt_slots(int tokens, int batch, int G) { return tokens / (2 * (kPrHalf / G)) + static_cast<int64_t>(batch); }
+
+// Parts of a unit's tiles: as many as fill the SMs once, of two tiles at least.
+int prompt_splits(int64_t units, int64_t tiles, int nsm) {
+    const int64_t most = std::min<int64_t>((tiles + 1) / 2, nsm / std::max<int64_t>(units, 1));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, 32)));
+}
+
+template <int D>
+static int launch_prompt(const PromptParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+    constexpr int smem = PrSmem<D>::kBytes + 1024;
+    if (cudaFuncSetAttribute(k_prompt_attn<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
+    const int64_t units = p.slots * p.c.H;
+    if (units * p.nsplit > INT32_MAX) return -1;
+    if (launch_first(k_prompt_attn<D>, static_cast<unsigned>(units * p.nsplit), kPrThreads, smem, 1, 0, s, p, mq, mk, mv) != cudaSuccess)
+        return -1;
+    if (p.nsplit > 1 && launch_first(k_prompt_merge<D>, dim3(static_cast<unsigned>(units), 4), 256, 0, 1, 0, s, p) != cudaSuccess) return -1;
+    return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+int launch_prompt_attn(int d, const PromptParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+    return d == 64 ? launch_prompt<64>(p, mq, mk, mv, s) : launch_prompt<128>(p, mq, mk, mv, s);
+}
+
+cudaError_t prompt_err(int** e) { return cudaGetSymbolAddress(reinterpret_cast<void**>(e), g_err); }
+
+}  // namespace skv

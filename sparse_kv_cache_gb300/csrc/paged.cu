@@ -211,13 +211,71 @@ int evict_space(const skv_paged_evict_args* a, EvictSpace* w) {
     return SKV_OK;
 }
 
+// ------------------------------------------------------------------ attention of prompts
+
+struct PromptSpace { int64_t slots, tiles, stat, bytes; };
+
+int prompt_space(const skv_paged_prompt_args* a, PromptSpace* w) {
+    const skv_paged_cache& c = a->cache;
+    if (!good_type(c) || c.batch < 0 || a->tokens < 0 || a->reserved || a->n_q_heads < 1 || a->n_q_heads % c.n_kv_heads)
+        return SKV_ERR_INVALID;
+    const int G = a->n_q_heads / c.n_kv_heads;
+    if (G > 8 || !std::isfinite(a->scale) || a->window < 0 || a->sink < 0) return SKV_ERR_INVALID;
+    if (c.max_pages < 1 || c.page_size < 1 || static_cast<int64_t>(c.max_pages) * c.page_size > kMaxRows) return SKV_ERR_INVALID;
+    if (static_cast<int64_t>(c.batch) * c.n_kv_heads > kMaxUnits) return SKV_ERR_INVALID;
+    if (c.dtype != SKV_BF16) return SKV_ERR_UNSUPPORTED;
+    w->slots = prompt_slots(a->tokens, c.batch, G);
+    // tiles of 128 rows that a unit of 256 / G tokens can see
+    const int64_t all = (static_cast<int64_t>(c.max_pages) * c.page_size + 127) / 128;
+    w->tiles = a->window ? std::min<int64_t>(all, (static_cast<int64_t>(a->sink) + 127) / 128 + (static_cast<int64_t>(a->window) + 256) / 128 + 2) : all;
+    const int64_t units = w->slots * c.n_kv_heads;
+    const int n = prompt_splits(units, w->tiles, kMaxSms);
+    const int64_t rows = n > 1 ? units * n * 256 : 0;
+    w->stat = rows * c.head_dim * 4;
+    w->bytes = w->stat + rows * 8;
+    return SKV_OK;
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn find_encode() {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(f);
+}
+// Map of a bf16 tensor [..][d] (sizes and strides in elements, innermost first without d), 64 elements of d to a box
+int tensor_map(CUtensorMap* m, const void* base, int d, std::initializer_list<Dim> dims, std::initializer_list<uint32_t> box) {
+    static const EncodeFn encode = find_encode();
+    if (!encode) return SKV_ERR_CUDA;
+    cuuint64_t size[4] = {static_cast<cuuint64_t>(d)}, step[3];
+    cuuint32_t boxes[4] = {64}, ones[4] = {1, 1, 1, 1};
+    int n = 1;
+    for (const Dim& x : dims) {
+        size[n] = x.n;
+        step[n - 1] = (x.n > 1 ? x.s : d) * 2;           // (a step that is never taken has to be some step)
+        if (step[n - 1] == 0 || step[n - 1] >= cuuint64_t(1) << 40) return SKV_ERR_INVALID;
+        ++n;
+    }
+    std::copy(box.begin(), box.end(), boxes + 1);
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n, const_cast<void*>(base), size, step, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? SKV_OK
+               : SKV_ERR_INVALID;
+}
+
 // ------------------------------------------------------------------ status
 
 // The error words are shared by all streams: reading and clearing is one step, so that nothing another
 // stream's kernel sets in between is lost.
 __device__ int g_taken;
 std::mutex g_taking;       // g_taken is one call's at a time
-struct ErrorWords { int* at[5]; };
+struct ErrorWords { int* at[6]; };
 __global__ void k_take_status(ErrorWords words) {
     int taken = 0;
     for (int* word : words.at) {
@@ -455,6 +513,55 @@ int shadowkv_paged_dequantise(const skv_paged_dequantise_args* a, skv_stream str
     return done(launch_dequantise(a->dtype, c.head_dim, p, stream));
 }
 
+int64_t shadowkv_paged_prompt_attention_workspace(const skv_paged_prompt_args* a) {
+    if (!a) return SKV_ERR_INVALID;
+    PromptSpace w;
+    const int rc = prompt_space(a, &w);
+    return rc ? rc : w.bytes;
+}
+
+int shadowkv_paged_prompt_attention(const skv_paged_prompt_args* a, skv_stream stream) {
+    if (!a) return SKV_ERR_INVALID;
+    const skv_paged_cache& c = a->cache;
+    PromptSpace w;
+    if (int rc = prompt_space(a, &w)) return rc;
+    if (c.batch == 0 || a->tokens == 0) return SKV_OK;
+    if (int rc = check_cache(c, false)) return rc;
+    if (!c.lens || !a->q || !a->out || !a->start || !aligned16(a->q) || !aligned16(a->out)) return SKV_ERR_INVALID;
+    for (int64_t s : {a->q_tok, a->q_head, a->out_tok, a->out_head})
+        if (!good_stride(s, 2)) return SKV_ERR_INVALID;
+    if (!apart(a->tokens, a->out_tok, a->n_q_heads, a->out_head, c.head_dim)) return SKV_ERR_INVALID;
+    if (a->workspace_bytes < w.bytes || (w.bytes && (!a->workspace || !aligned16(a->workspace)))) return SKV_ERR_INVALID;
+    if (int rc = check_words({c.table, c.lens, a->lse, a->start})) return rc;
+    Device dev;
+    if (int rc = device(&dev)) return rc;
+    if (int rc = check_memory({c.k, c.v, c.table, c.lens, a->q, a->out, a->lse, a->start, w.bytes ? a->workspace : nullptr}, dev.id))
+        return rc;
+    const uint32_t G = a->n_q_heads / c.n_kv_heads, tq = 128 / G, box = std::min(c.page_size, 128);
+    CUtensorMap mq, mk, mv;
+    if (int rc = tensor_map(&mq, a->q, c.head_dim, {{a->n_q_heads, a->q_head}, {a->tokens, a->q_tok}}, {G, tq})) return rc;
+    if (int rc = tensor_map(&mk, c.k, c.head_dim, {{c.page_size, c.k_row}, {c.n_kv_heads, c.k_head}, {c.n_pages, c.k_page}}, {box, 1, 1}))
+        return rc;
+    if (int rc = tensor_map(&mv, c.v, c.head_dim, {{c.page_size, c.v_row}, {c.n_kv_heads, c.v_head}, {c.n_pages, c.v_page}}, {box, 1, 1}))
+        return rc;
+    Range range("shadowkv_paged_prompt_attention");
+    PromptParams p{};
+    p.c = view(c);
+    p.c.window = static_cast<int>(std::min<int64_t>(a->window, kMaxRows));
+    p.c.sink = static_cast<int>(std::min<int64_t>(a->sink, kMaxRows));
+    p.G = G; p.n_q = a->n_q_heads; p.tokens = a->tokens; p.tq = tq;
+    p.slots = w.slots;
+    p.nsplit = prompt_splits(w.slots * c.n_kv_heads, w.tiles, dev.nsm < kMaxSms ? dev.nsm : kMaxSms);
+    p.scale_log2 = static_cast<float>((a->scale != 0.f ? static_cast<double>(a->scale) : 1.0 / std::sqrt(double(c.head_dim))) *
+                                      1.4426950408889634074);
+    p.down_bits = static_cast<float>(8 + log2_of(p.c.cap));
+    p.o_tok = a->out_tok; p.o_head = a->out_head;
+    p.start = a->start; p.out = a->out; p.lse = a->lse;
+    p.part = static_cast<float*>(a->workspace);
+    p.part_stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(a->workspace) + w.stat);
+    return done(launch_prompt_attn(c.head_dim, p, mq, mk, mv, stream));
+}
+
 int64_t shadowkv_paged_evict_workspace(const skv_paged_evict_args* a) {
     if (!a) return SKV_ERR_INVALID;
     EvictSpace w;
@@ -506,7 +613,8 @@ int shadowkv_paged_status(skv_stream stream) {
     int taken = 0;
     if (cudaStreamSynchronize(stream) != cudaSuccess || norm_rope_err(&words.at[0]) != cudaSuccess ||
         paged_attn_err(&words.at[1]) != cudaSuccess || evict_err(&words.at[2]) != cudaSuccess ||
-        paged_span_err(&words.at[3]) != cudaSuccess || quantise_err(&words.at[4]) != cudaSuccess) {
+        paged_span_err(&words.at[3]) != cudaSuccess || quantise_err(&words.at[4]) != cudaSuccess ||
+        prompt_err(&words.at[5]) != cudaSuccess) {
         cudaGetLastError();
         return SKV_ERR_CUDA;
     }
@@ -517,7 +625,7 @@ int shadowkv_paged_status(skv_stream stream) {
         cudaGetLastError();
         return SKV_ERR_CUDA;
     }
-    return taken ? SKV_ERR_DEVICE_BOUNDS : SKV_OK;
+    return taken == DEV_ERR_TIMEOUT ? SKV_ERR_TIMEOUT : taken ? SKV_ERR_DEVICE_BOUNDS : SKV_OK;
 }
 
 }  // extern "C"

@@ -1,6 +1,7 @@
 // Internal types of the paged-cache calls: kernel parameters and launchers.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -82,6 +83,23 @@ struct DequantParams {
 };
 int launch_dequantise(int dtype, int d, const DequantParams& p, cudaStream_t s);
 
+struct PromptParams {
+    PagedView c;              // window 0: none
+    int G, n_q, tokens;
+    int tq;                   // tokens of half a unit: 128 / G
+    int nsplit;               // parts of a unit's tiles
+    int64_t slots;            // places for units of 2 tq tokens of a sequence: prompt_slots()
+    float scale_log2, down_bits;
+    int64_t o_tok, o_head;
+    const int32_t* start;
+    void* out; float* lse;
+    float* part;              // [slots * H * nsplit][256][d]: parts of sums, unnormalised
+    float2* part_stat;        // their bases and sums of probabilities
+};
+int64_t prompt_slots(int tokens, int batch, int G);
+int prompt_splits(int64_t units, int64_t tiles, int nsm);
+int launch_prompt_attn(int d, const PromptParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s);
+
 struct EvictParams {
     PagedView c;
     int d, es, es_v;
@@ -101,6 +119,7 @@ cudaError_t paged_attn_err(int** p);
 cudaError_t evict_err(int** p);
 cudaError_t paged_span_err(int** p);
 cudaError_t quantise_err(int** p);
+cudaError_t prompt_err(int** p);
 
 #ifdef __CUDACC__
 // A kernel of a call's beginning: a programmatic dependent of whatever is before it in the stream,

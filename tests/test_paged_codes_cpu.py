@@ -161,3 +161,70 @@ def test_sources_of_the_further_kernels_read_coherently():
     import re
     for name in ("paged_attn.cuh", "k_paged_span.cu", "k_quantise.cu"):
         assert not re.findall(r"\.nc\b|__ldg\b|__restrict__", code_of(name)), name
+
+
+# ------------------------------------------------------------------ prompts
+
+def test_packed_arguments_of_prompts_match_the_header(tmp_path):
+    from sparse_kv_cache_gb300 import _binding as b
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("gcc missing")
+    src, exe = tmp_path / "sizes.c", tmp_path / "sizes"
+    src.write_text('#include "shadowkv.h"\n#include <stdio.h>\n#include <stddef.h>\nint main(){printf("%zu %zu %zu", '
+                   'sizeof(skv_paged_prompt_args), offsetof(skv_paged_prompt_args, q_tok), offsetof(skv_paged_prompt_args, workspace));return 0;}\n')
+    subprocess.run([gcc, "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True).stdout.split()]
+    import struct
+    assert got == [b._PROMPT.size, struct.calcsize(b._CACHE + " i f 4i"), b._PROMPT.size - 16]
+
+
+def test_prompt_attention_refuses(skv):  # noqa: F811
+    c, q = cache(), torch.zeros((5, 4, 128), dtype=torch.bfloat16)
+    start = torch.zeros(3, dtype=torch.int32)
+    go = lambda **kw: skv.paged_prompt_attention(**{**dict(q=q, out=torch.empty_like(q), start=start, stream=0), **c, **kw})  # noqa: E731
+    odd = torch.zeros((5, 3, 128), dtype=torch.bfloat16)
+    many = torch.zeros((5, 18, 128), dtype=torch.bfloat16)
+    for bad in (dict(q=q[:4]), dict(q=q.float()), dict(q=q[0]), dict(out=q[:, :2]), dict(out=q.float()), dict(q=odd, out=odd.clone()),
+                dict(q=many, out=many.clone()), dict(start=start[:2]), dict(start=start.long()), dict(start=None), dict(lens=c["lens"][:1]),
+                dict(table=c["table"].long()), dict(table=c["table"][0]), dict(lse=torch.zeros(5, 2)), dict(window=-1), dict(sink=-1),
+                dict(window=2.5), dict(scale=float("nan")), dict(q=off(q)), dict(out=off(q)), dict(out=q[:1].expand(5, -1, -1)),
+                dict(k_cache=c["k_cache"].to(E4M3), v_cache=c["v_cache"].to(E4M3)), dict(k_cache=c["k_cache"][:, :, :, :64])):
+        refused(skv, lambda: go(**bad))
+
+
+def test_prompt_entry_and_workspace(skv):  # noqa: F811
+    from sparse_kv_cache_gb300 import _binding as b
+    lib, host = skv.load(), torch.zeros(64)
+    at = (host.data_ptr() + 15) & ~15
+    pools = (1, 2, 128, 16, 1, 4, 8, 4096, 2048, 128, 4096, 2048, 128, 4, at, at, at, at)
+    dev = lib.shadowkv_paged_status(None) == 0
+    assert lib.shadowkv_paged_prompt_attention(None, None) == -1 and lib.shadowkv_paged_prompt_attention_workspace(None) == -1
+
+    def args(pools=pools, heads=4, scale=0.0, window=0, sink=0, tokens=9, reserved=0, steps=(512, 128, 512, 128), q=at, out=at, start=at,
+             space=at, nbytes=1 << 40):
+        return b._PROMPT.pack(*pools, heads, scale, window, sink, tokens, reserved, *steps, q, out, 0, start, space, nbytes)
+    call = lambda **kw: lib.shadowkv_paged_prompt_attention(args(**kw), None)  # noqa: E731
+    long = (1, 2, 128, 1024, 1, 4, *pools[6:])
+    good = -1 if dev else -4          # as far as the look at the device, or at the memory, which is the host's
+    assert call() == good and call(nbytes=0, space=0) == good and call(pools=long) == good
+    assert call(tokens=0) == 0 and call(pools=(*pools[:4], 0, *pools[5:])) == 0
+    for x in (dict(heads=3), dict(heads=18), dict(heads=0), dict(window=-1), dict(sink=-1), dict(tokens=-1), dict(reserved=1), dict(q=0),
+              dict(q=at + 8), dict(out=at + 8), dict(start=0), dict(start=at + 2), dict(steps=(512, 124, 512, 128)),
+              dict(steps=(512, 128, 512, 120)), dict(steps=(512, 128, 128, 128)), dict(scale=float("inf")), dict(pools=long, nbytes=0),
+              dict(pools=long, space=0), dict(pools=long, space=at + 8), dict(pools=(*pools[:17], 0)), dict(pools=(*pools[:3], 24, *pools[4:]))):
+        assert call(**x) == -1, x
+    for kind in (0, 2):
+        assert call(pools=(kind, *pools[1:])) == -8
+    # parts take room, one unit per SM and more takes none; the most that there may be does not overflow
+    size = lambda **kw: lib.shadowkv_paged_prompt_attention_workspace(args(**kw))  # noqa: E731
+    wide = (1, 2, 128, 1024, 1, 1 << 20, *pools[6:])
+    assert size() == 0 and 0 < size(pools=wide) <= 160 * 256 * (128 * 4 + 8) and size(pools=wide, tokens=100000) == 0
+    assert size(pools=(1, 1 << 16, 128, 16, 1 << 8, 4, *pools[6:]), heads=1 << 16, tokens=(1 << 31) - 1) == 0
+    assert size(pools=wide, window=(1 << 31) - 1, sink=(1 << 31) - 1) == size(pools=wide)
+
+
+def test_sources_of_prompts_read_coherently():
+    from tests.test_paged_source import code_of
+    import re
+    assert not re.findall(r"\.nc\b|__ldg\b|__restrict__", code_of("k_prompt_attn.cu"))
