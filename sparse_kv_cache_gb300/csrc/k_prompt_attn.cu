@@ -50,21 +50,25 @@ __device__ __forceinline__ float pr_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// A wait that ends after about a second, or once another of the CTA's has; false then.
-__device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, volatile int* dead) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer();
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*dead) return false;
-        if (globaltimer() - t0 > kWaitLimitNs) {
-            *dead = 1;
-            set_err(g_err, DEV_ERR_TIMEOUT, 911);
-            return false;
-        }
-    }
+// A wait that ends after about a second, or once another of the CTA's has; false then.  One statement: with a way out
+// for some threads of a warp alone the compiler keeps what is the warp's in registers of each thread behind it, and
+// a prompt of 32K tokens takes 6.5 ms instead of 6.3.  (The threads of a warp are told the same: a phase that one of
+// them saw end does not come again before all of them went on.)
+__device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, int* dead) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 now, end;\n\t.reg .b32 given_up;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "mov.u64 end, %%globaltimer;\n\tadd.u64 end, end, %4;\n\t"
+        "AGAIN:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "ld.volatile.shared::cta.u32 given_up, [%3];\n\tsetp.ne.u32 q, given_up, 0;\n\t@q bra DONE;\n\t"
+        "mov.u64 now, %%globaltimer;\n\tsetp.lt.u64 q, now, end;\n\t@q bra AGAIN;\n\t"
+        "st.volatile.shared::cta.u32 [%3], 1;\n\t"
+        "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(smem_u32(dead)), "n"(kWaitLimitNs)
+        : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
     asm volatile(
@@ -78,6 +82,12 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
             dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
         : "memory");
+}
+// One thread of the warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t is;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(is));
+    return is != 0;
 }
 // D[tmem] (+)= A[tmem] * B[smem], A 128 x 16 bf16 packed in pairs
 __device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
@@ -101,6 +111,7 @@ __device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t next) 
 constexpr uint32_t kBIsMN = 1u << 16;          // instruction descriptor: B is stored along N
 
 #define PR_R8(v, i) "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3]), "=r"(v[i + 4]), "=r"(v[i + 5]), "=r"(v[i + 6]), "=r"(v[i + 7])
+#define PR_F8(c, v, i) c(v[i]), c(v[i + 1]), c(v[i + 2]), c(v[i + 3]), c(v[i + 4]), c(v[i + 5]), c(v[i + 6]), c(v[i + 7])
 #define PR_W8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), "r"(v[i + 6]), "r"(v[i + 7])
 // Columns of this thread's lane, there when the function returns (the wait is in the same statement, so that nothing
 // that uses them can come before it).
@@ -112,21 +123,32 @@ __device__ __forceinline__ void tmem_get32(uint32_t taddr, uint32_t* r) {
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_get128(uint32_t taddr, uint32_t* r) {
+// The same in steps: asked for, waited for (tmem_ld_wait), and marked as there, before which nothing uses them.
+__device__ __forceinline__ void tmem_ask32(uint32_t taddr, float* r) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,"
-        "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
-        "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,"
-        "%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
-        "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%128];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : PR_R8(r, 0), PR_R8(r, 8), PR_R8(r, 16), PR_R8(r, 24), PR_R8(r, 32), PR_R8(r, 40), PR_R8(r, 48), PR_R8(r, 56),
-          PR_R8(r, 64), PR_R8(r, 72), PR_R8(r, 80), PR_R8(r, 88), PR_R8(r, 96), PR_R8(r, 104), PR_R8(r, 112), PR_R8(r, 120)
-        : "r"(taddr)
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : PR_F8("=f", r, 0), PR_F8("=f", r, 8), PR_F8("=f", r, 16), PR_F8("=f", r, 24)
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_have32(float* r) {
+    asm volatile("" : PR_F8("+f", r, 0), PR_F8("+f", r, 8), PR_F8("+f", r, 16), PR_F8("+f", r, 24));
+}
+// two fp32 products and sums, or sums, in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 __device__ __forceinline__ uint32_t tmem_get1(uint32_t taddr) {
     uint32_t r;
@@ -137,6 +159,12 @@ __device__ __forceinline__ void tmem_put32(uint32_t taddr, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
         "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::PR_W8(r, 0), PR_W8(r, 8), PR_W8(r, 16), PR_W8(r, 24),
+        "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::PR_W8(r, 0), PR_W8(r, 8),
         "r"(taddr)
         : "memory");
 }
@@ -166,8 +194,16 @@ __device__ __forceinline__ PrSees sees(const PromptParams& p, const PrUnit& u, i
     return half == 2 ? PrSees{u.row0, u.row0 + u.ntok - 1, p.c.window, p.c.sink}
                      : PrSees{u.row0 + from, u.row0 + to - 1, p.c.window, p.c.sink};
 }
-// whether a tile has a row that not all of the unit's tokens see
-__device__ __forceinline__ bool at_edge(const PrSees& both, int tile) { return !both.all(tile * kPrTile, tile * kPrTile + kPrTile - 1); }
+// The tiles of which some tokens see all rows: up to `upto`, and of those from `from` on or up to `sink`.
+struct PrWhole {
+    int upto, from, sink;
+    __device__ __forceinline__ bool has(int tile) const { return tile <= upto && (tile >= from || tile <= sink); }
+};
+__device__ __forceinline__ PrWhole whole(const PrSees& s) {
+    // of tile t, rows 128 t .. 128 t + 127: the last is no later than the first token's own, the first within the last
+    // token's window (shifts round down)
+    return PrWhole{(s.first - (kPrTile - 1)) >> 7, s.window ? ((s.last - s.window) >> 7) + 1 : INT32_MIN, (s.sink - kPrTile) >> 7};
+}
 
 // By one warp: which unit a block has; ntok 0 if none.
 __device__ __forceinline__ PrUnit find_unit(const PromptParams& p, int64_t block) {
@@ -213,6 +249,7 @@ struct PrShared {
     uint64_t q_full, k_full[kPrStages], k_empty[kPrStages], v_full[kPrStages], v_ok[kPrStages], v_empty[kPrStages];
     uint64_t s_full[2], p_full[2], o_full[2];
     PrUnit unit;
+    PrWhole whole[3];          // of either half's tokens, and of all
     uint32_t tmem;
     int dead;
     int absent[4];             // per tile (mod 4): groups of eight rows whose page is out of range or not looked at
@@ -256,7 +293,7 @@ __device__ void pr_load(const PromptParams& p, const CUtensorMap* mq, const CUte
         const int z = __shfl_sync(0xffffffffu, page < 0 ? static_cast<int>(p.c.n_pages) : page, j);
         const int in_page = (row + j * box) & mask;
         const uint32_t to = at + s * L::kTileBytes + part * 16384 + j * box * 128;
-        if (!__all_sync(0xffffffffu, pr_wait(&sh.k_empty[s], parity, &sh.dead))) break;
+        if (!pr_wait(&sh.k_empty[s], parity, &sh.dead)) break;
         if (lane == 0) {
             int absent = 0;
             for (int i = 0; i < 16; ++i) absent |= (gone >> (i * 8 / box) & 1) << i;
@@ -266,7 +303,7 @@ __device__ void pr_load(const PromptParams& p, const CUtensorMap* mq, const CUte
         __syncwarp();
         if (part < L::kParts) tma_load_4d(to + L::kK, mk, part * 64, in_page, u.h, z, &sh.k_full[s]);
         keys = n + 1;
-        if (!__all_sync(0xffffffffu, pr_wait(&sh.v_empty[s], parity, &sh.dead))) break;
+        if (!pr_wait(&sh.v_empty[s], parity, &sh.dead)) break;
         if (lane == 0) mbar_arrive_expect_tx(&sh.v_full[s], L::kTileBytes);
         __syncwarp();
         if (part < L::kParts) tma_load_4d(to + L::kV, mv, part * 64, in_page, u.h, z, &sh.v_full[s]);
@@ -284,43 +321,54 @@ template <int D>
 __device__ bool pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) {
     using L = PrSmem<D>;
     const PrUnit u = sh.unit;
-    const PrSees both = sees(p, u, 2);
+    const PrWhole calm = sh.whole[2];
     const uint32_t at = smem_u32(base), tmem = sh.tmem;
     const int halves = u.ntok > p.tq ? 2 : 1, tiles = u.hi - u.lo;
     if (tiles <= 0) return true;
     constexpr uint32_t qk = idesc_bf16_f32(kPrHalf, kPrTile), pv = idesc_bf16_f32(kPrHalf, D) | kBIsMN;
+    // The whole warp comes this way and one thread of it issues: operands that are the warp's stay in uniform
+    // registers (with one thread alone on the path an instruction took 115 clocks to issue, twice its work).
+    const bool mine = elect_one();
+    const uint64_t q_desc = smem_desc_sw128(at + L::kQ), k_desc = smem_desc_sw128(at + L::kK), v_desc = smem_desc_mn(at + L::kV, 16384);
     auto scores = [&](int x, int n) {
-        const uint32_t q = at + L::kQ + x * L::kTileBytes, k = at + L::kK + (n % kPrStages) * L::kTileBytes;
+        const uint64_t q = q_desc + x * (L::kTileBytes >> 4), k = k_desc + (n % kPrStages) * (L::kTileBytes >> 4);
+        if (!mine) return;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-            tc_mma_bf16(tmem + x * 128, smem_desc_sw128(q + (i / 4) * 16384 + (i % 4) * 32),
-                        smem_desc_sw128(k + (i / 4) * 16384 + (i % 4) * 32), qk, i > 0);
+        for (int i = 0; i < D / 16; ++i) {
+            constexpr int kPart = 16384 >> 4, kStep = 32 >> 4;
+            tc_mma_bf16(tmem + x * 128, q + (i / 4) * kPart + (i % 4) * kStep, k + (i / 4) * kPart + (i % 4) * kStep, qk, i > 0);
+        }
         tc_commit(&sh.s_full[x]);
     };
     auto values = [&](int x, int n) {
-        const uint32_t v = at + L::kV + (n % kPrStages) * L::kTileBytes;
+        const uint64_t v = v_desc + (n % kPrStages) * (L::kTileBytes >> 4);
+        if (!mine) return;
 #pragma unroll
         for (int i = 0; i < kPrTile / 16; ++i)
-            tc_mma_bf16_ts(tmem + 256 + x * 128, tmem + x * 128 + i * 8, smem_desc_mn(v + i * 2048, 16384), pv, n > 0 || i > 0);
+            tc_mma_bf16_ts(tmem + 256 + x * 128, tmem + x * 128 + i * 8, v + i * (2048 >> 4), pv, n > 0 || i > 0);
     };
-    if (!pr_wait(&sh.q_full, 0, &sh.dead) || !pr_wait(&sh.k_full[0], 0, &sh.dead)) return false;
+    auto told = [&](uint64_t* bar, uint32_t parity) { return pr_wait(bar, parity, &sh.dead); };
+    auto commit = [&](uint64_t* bar) {
+        if (mine) tc_commit(bar);
+    };
+    if (!told(&sh.q_full, 0) || !told(&sh.k_full[0], 0)) return false;
     for (int x = 0; x < halves; ++x) scores(x, 0);
-    tc_commit(&sh.k_empty[0]);
+    commit(&sh.k_empty[0]);
     for (int n = 0; n < tiles; ++n) {
         const int s = n % kPrStages, next = (n + 1) % kPrStages;
-        if (!pr_wait(&sh.v_ok[s], (n / kPrStages) & 1, &sh.dead)) return false;
-        const bool wild = at_edge(both, u.tile(u.lo + n)) && sh.is_wild(s);
+        if (!told(&sh.v_ok[s], (n / kPrStages) & 1)) return false;
+        const bool wild = !calm.has(u.tile(u.lo + n)) && sh.is_wild(s);
         for (int x = 0; x < halves; ++x) {
-            if (!pr_wait(&sh.p_full[x], n & 1, &sh.dead)) return false;
+            if (!told(&sh.p_full[x], n & 1)) return false;
             tc_fence_after();
             if (!wild) values(x, n);       // otherwise the row's threads have done it
-            if (x == halves - 1) tc_commit(&sh.v_empty[s]);
+            if (x == halves - 1) commit(&sh.v_empty[s]);
             if (n + 1 < tiles) {
-                if (x == 0 && !pr_wait(&sh.k_full[next], ((n + 1) / kPrStages) & 1, &sh.dead)) return false;
+                if (x == 0 && !told(&sh.k_full[next], ((n + 1) / kPrStages) & 1)) return false;
                 scores(x, n + 1);
-                if (x == halves - 1) tc_commit(&sh.k_empty[next]);
+                if (x == halves - 1) commit(&sh.k_empty[next]);
             } else {
-                tc_commit(&sh.o_full[x]);
+                commit(&sh.o_full[x]);
             }
         }
     }
@@ -332,11 +380,12 @@ __device__ void pr_look(const PromptParams& p, PrShared& sh, uint8_t* base) {
     using L = PrSmem<D>;
     const PrUnit u = sh.unit;
     const PrSees both = sees(p, u, 2);
+    const PrWhole calm = sh.whole[2];
     const int t = threadIdx.x - 320, warp = t >> 5;   // of 64
     for (int n = 0; n < u.hi - u.lo; ++n) {
         const int s = n % kPrStages, tile = u.tile(u.lo + n);
-        if (!__all_sync(0xffffffffu, pr_wait(&sh.v_full[s], (n / kPrStages) & 1, &sh.dead))) return;
-        if (at_edge(both, tile)) {
+        if (!pr_wait(&sh.v_full[s], (n / kPrStages) & 1, &sh.dead)) return;
+        if (!calm.has(tile)) {
             uint32_t some = 0;
             uint8_t* v = base + L::kV + s * L::kTileBytes;
             for (int part = 0; part < L::kParts; ++part)
@@ -394,95 +443,127 @@ __device__ __noinline__ void pr_by_hand(uint32_t o_tmem, uint32_t p_tmem, const 
     tmem_put_wait();
 }
 
+// O of this thread's row *= w
+template <int D>
+__device__ __forceinline__ void pr_rescale(uint32_t o_tmem, float w) {
+#pragma unroll 1
+    for (int d0 = 0; d0 < D; d0 += 32) {
+        uint32_t o[32];
+        tmem_get32(o_tmem + d0, o);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * w);
+        tmem_put32(o_tmem + d0, o);
+    }
+}
+
+// the lowest k bits
+__device__ __forceinline__ uint32_t lowest(int k) { return k <= 0 ? 0u : 0xFFFFFFFFu >> (32 - min(k, 32)); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 template <int D>
 __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     using L = PrSmem<D>;
-    const PrUnit u = sh.unit;
+    const PrUnit& u = sh.unit;
     const int half = threadIdx.x >> 7, r = threadIdx.x & 127;
-    const int tiles = u.hi - u.lo;
+    const int lo = u.lo, tiles = u.hi - lo;
+    const int token = half * p.tq + min(r / p.G, p.tq - 1);             // (rows beyond the last token repeat its)
     if (half * p.tq >= u.ntok) return;
-    const PrSees mine = sees(p, u, half), both = sees(p, u, 2);
-    const int t = min(r / p.G, p.tq - 1), token = half * p.tq + t;      // (rows beyond the last token repeat its)
-    const int row = min(u.row0 + token, mine.last);
+    const int row = u.row0 + min(token, u.ntok - 1);
     const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;      // 32 lanes of the tensor memory
-    const uint32_t s_at = sh.tmem + lanes + half * 128, o_at = sh.tmem + lanes + 256 + half * 128;
+    const uint32_t s_at = sh.tmem + lanes + half * 128, o_at = s_at + 256;
     const float scale = p.scale_log2;
     const bool falls = scale < 0.f;
     const float none = falls ? CUDART_INF_F : -CUDART_INF_F;             // the product that scores -infinity
     float m = -CUDART_INF_F, l = 0.f;
     bool good = true;
     for (int n = 0; n < tiles; ++n) {
-        const int tile = u.tile(u.lo + n), first = tile * kPrTile;
+        const int tile = u.tile(lo + n);
         good = pr_wait(&sh.s_full[half], n & 1, &sh.dead);
-        if (!__all_sync(0xffffffffu, good)) { good = false; break; }
+        if (!good) break;
         tc_fence_after();
-        uint32_t raw[128];
-        tmem_get128(s_at, raw);
-        const int absent = *const_cast<volatile int*>(&sh.absent[n & 3]);
-        if (absent || !mine.all(first, first + kPrTile - 1)) {
-            const int hi = row - first, lo = mine.window ? hi - mine.window : -1, sink = mine.window ? mine.sink - first : 0;
+        float x[4][32];
 #pragma unroll
-            for (int i = 0; i < 128; ++i) {
-                const bool in = i <= hi && (i > lo || i < sink) && !(absent >> (i / 8) & 1);
-                raw[i] = in ? raw[i] : __float_as_uint(none);
+        for (int c = 0; c < 4; ++c) tmem_ask32(s_at + 32 * c, x[c]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_have32(x[c]);
+        const int absent = *const_cast<volatile int*>(&sh.absent[n & 3]);
+        if (absent || !sh.whole[half].has(tile)) {
+            // per 32 rows of the tile, those that this thread's token sees
+            const int first = tile * kPrTile, window = p.c.window;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int upto = row - first - 32 * c;
+                uint32_t in = lowest(upto + 1);
+                if (window) in &= ~lowest(upto + 1 - window) | lowest(p.c.sink - first - 32 * c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (absent >> (4 * c + e) & 1) in &= ~(0xFFu << (8 * e));
+                if (__all_sync(0xffffffffu, in == 0xFFFFFFFFu)) continue;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[c][i] = in >> i & 1 ? x[c][i] : none;
             }
         }
-        float top[4];
+        // eight maxima side by side: one after the other each would wait for the last
+        float top[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top[i] = falls ? fminf(x[0][2 * i], x[0][2 * i + 1]) : fmaxf(x[0][2 * i], x[0][2 * i + 1]);
         if (falls) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top[i] = __uint_as_float(raw[i]);
-#pragma unroll
-            for (int i = 4; i < 128; ++i) top[i & 3] = fminf(top[i & 3], __uint_as_float(raw[i]));
-            top[0] = fminf(fminf(top[0], top[1]), fminf(top[2], top[3])) * scale;
+            for (int i = 16; i < 128; i += 2) top[i / 2 & 7] = fminf(top[i / 2 & 7], fminf(x[i / 32][i % 32], x[i / 32][i % 32 + 1]));
+            top[0] = fminf(fminf(fminf(top[0], top[1]), fminf(top[2], top[3])), fminf(fminf(top[4], top[5]), fminf(top[6], top[7]))) * scale;
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top[i] = __uint_as_float(raw[i]);
-#pragma unroll
-            for (int i = 4; i < 128; ++i) top[i & 3] = fmaxf(top[i & 3], __uint_as_float(raw[i]));
-            top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * scale;
+            for (int i = 16; i < 128; i += 2) top[i / 2 & 7] = max3(top[i / 2 & 7], x[i / 32][i % 32], x[i / 32][i % 32 + 1]);
+            top[0] = max3(max3(top[0], top[1], top[2]), max3(top[3], top[4], top[5]), fmaxf(top[6], top[7])) * scale;
         }
         if (__any_sync(0xffffffffu, top[0] > m + kPrSlack)) {
             const float now = fmaxf(m, top[0]);
             const float w = m == -CUDART_INF_F ? 0.f : pr_exp2(m - now);
             m = now;
             l *= w;
-            if (n > 0) {
-#pragma unroll 1
-                for (int d0 = 0; d0 < D; d0 += 32) {
-                    uint32_t o[32];
-                    tmem_get32(o_at + d0, o);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * w);
-                    tmem_put32(o_at + d0, o);
-                }
-            }
+            if (n > 0) pr_rescale<D>(o_at, w);
         }
         const float minus = m == -CUDART_INF_F ? 0.f : -(m + p.down_bits);
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 sum[4] = {make_float2(l, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 scale2 = make_float2(scale, scale), minus2 = make_float2(minus, minus);
 #pragma unroll
-        for (int i = 0; i < 64; ++i) {
-            const float a = pr_exp2(fmaf(__uint_as_float(raw[2 * i]), scale, minus));
-            const float b = pr_exp2(fmaf(__uint_as_float(raw[2 * i + 1]), scale, minus));
-            sum[(2 * i) & 3] += a;
-            sum[(2 * i + 1) & 3] += b;
-            raw[i] = pack_bf16x2(a, b);
+        for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+                const float2 e = fma2(make_float2(x[c][i], x[c][i + 1]), scale2, minus2);
+                x[c][i] = e.x;
+                x[c][i + 1] = e.y;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[c][i] = pr_exp2(x[c][i]);
+            uint32_t two[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                two[i] = pack_bf16x2(x[c][2 * i], x[c][2 * i + 1]);
+                sum[i & 3] = add2(sum[i & 3], make_float2(x[c][2 * i], x[c][2 * i + 1]));
+            }
+            tmem_put16(s_at + 16 * c, two);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        tmem_put32(s_at, raw);
-        tmem_put32(s_at + 32, raw + 32);
+        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l = sum[0].x + sum[0].y;
         tmem_put_wait();
-        if (at_edge(both, tile)) {
+        if (!sh.whole[2].has(tile)) {
             const int s = n % kPrStages;
             good = pr_wait(&sh.v_ok[s], (n / kPrStages) & 1, &sh.dead);
-            if (!__all_sync(0xffffffffu, good)) { good = false; break; }
+            if (!good) break;
             if (sh.is_wild(s)) pr_by_hand<D>(o_at, s_at, base + L::kV + s * L::kTileBytes, n == 0);
         }
         tc_fence_before();
-        mbar_arrive(&sh.p_full[half]);
+        __syncwarp();
+        if ((r & 31) == 0) mbar_arrive(&sh.p_full[half]);
     }
     if (good && tiles > 0) {
         good = pr_wait(&sh.o_full[half], 0, &sh.dead);
-        good = __all_sync(0xffffffffu, good);
         tc_fence_after();
     }
     const bool live = r < p.tq * p.G && token < u.ntok;
@@ -542,6 +623,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_prompt_attn(const __grid_cons
         const PrUnit u = find_unit(p, blockIdx.x);
         if (lane == 0) {
             sh.unit = u;
+            for (int x = 0; x < 3; ++x) sh.whole[x] = whole(sees(p, u, x));
             sh.dead = 0;
             mbar_init(&sh.q_full, 1);
             for (int s = 0; s < kPrStages; ++s) {
@@ -554,7 +636,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_prompt_attn(const __grid_cons
             mbar_init(&sh.given_up, 1);
             for (int x = 0; x < 2; ++x) {
                 mbar_init(&sh.s_full[x], 1);
-                mbar_init(&sh.p_full[x], kPrHalf);
+                mbar_init(&sh.p_full[x], 4);
                 mbar_init(&sh.o_full[x], 1);
             }
             fence_mbar_init();
@@ -579,8 +661,8 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_prompt_attn(const __grid_cons
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrRegsLess));
         if (warp == 8) pr_load<D>(p, &mq, &mk, &mv, sh, base);
         else if (warp == 9) {
-            if (lane == 0 && !pr_multiply<D>(p, sh, base)) {
-                tc_commit(&sh.given_up);
+            if (!pr_multiply<D>(p, sh, base)) {
+                if (elect_one()) tc_commit(&sh.given_up);
                 mbar_wait(&sh.given_up, 0);
             }
         } else pr_look<D>(p, sh, base);
@@ -588,6 +670,7 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_prompt_attn(const __grid_cons
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && sh.dead) set_err(g_err, DEV_ERR_TIMEOUT, 911);
     if (warp == 9) {
         tc_fence_after();
         tmem_dealloc(sh.tmem, 512);
