@@ -4,7 +4,7 @@
 
 namespace skv {
 
-int paged_attn_ctas(int dtype, int d, int nsm) { return nsm * occ_of(dtype == SKV_F32, d); }
+int paged_attn_ctas(int dtype, int d, int nsm) { return nsm * occ_of(dtype, d); }
 
 int launch_paged_attn(int dtype, int d, const PagedAttnParams& p, int ncta, cudaStream_t s) {
     if (dtype == SKV_F32) return d == 64 ? launch_f32<64, false>(p, ncta, s) : launch_f32<128, false>(p, ncta, s);

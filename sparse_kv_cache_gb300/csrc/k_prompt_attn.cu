@@ -50,39 +50,6 @@ __device__ __forceinline__ float pr_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// A wait that ends after about a second, or once another of the CTA's has; false then.  One statement: with a way out
-// for some threads of a warp alone the compiler keeps what is the warp's in registers of each thread behind it, and
-// a prompt of 32K tokens takes 6.5 ms instead of 6.3.  (The threads of a warp are told the same: a phase that one of
-// them saw end does not come again before all of them went on.)
-__device__ __forceinline__ bool pr_wait(uint64_t* bar, uint32_t parity, int* dead) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 now, end;\n\t.reg .b32 given_up;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
-        "mov.u64 end, %%globaltimer;\n\tadd.u64 end, end, %4;\n\t"
-        "AGAIN:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
-        "ld.volatile.shared::cta.u32 given_up, [%3];\n\tsetp.ne.u32 q, given_up, 0;\n\t@q bra DONE;\n\t"
-        "mov.u64 now, %%globaltimer;\n\tsetp.lt.u64 q, now, end;\n\t@q bra AGAIN;\n\t"
-        "st.volatile.shared::cta.u32 [%3], 1;\n\t"
-        "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(smem_u32(dead)), "n"(kWaitLimitNs)
-        : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-            dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-        : "memory");
-}
 // One thread of the warp, always the same.
 __device__ __forceinline__ bool elect_one() {
     uint32_t is;
@@ -293,7 +260,7 @@ __device__ void pr_load(const PromptParams& p, const CUtensorMap* mq, const CUte
         const int z = __shfl_sync(0xffffffffu, page < 0 ? static_cast<int>(p.c.n_pages) : page, j);
         const int in_page = (row + j * box) & mask;
         const uint32_t to = at + s * L::kTileBytes + part * 16384 + j * box * 128;
-        if (!pr_wait(&sh.k_empty[s], parity, &sh.dead)) break;
+        if (!wait_or_give_up(&sh.k_empty[s], parity, &sh.dead)) break;
         if (lane == 0) {
             int absent = 0;
             for (int i = 0; i < 16; ++i) absent |= (gone >> (i * 8 / box) & 1) << i;
@@ -303,7 +270,7 @@ __device__ void pr_load(const PromptParams& p, const CUtensorMap* mq, const CUte
         __syncwarp();
         if (part < L::kParts) tma_load_4d(to + L::kK, mk, part * 64, in_page, u.h, z, &sh.k_full[s]);
         keys = n + 1;
-        if (!pr_wait(&sh.v_empty[s], parity, &sh.dead)) break;
+        if (!wait_or_give_up(&sh.v_empty[s], parity, &sh.dead)) break;
         if (lane == 0) mbar_arrive_expect_tx(&sh.v_full[s], L::kTileBytes);
         __syncwarp();
         if (part < L::kParts) tma_load_4d(to + L::kV, mv, part * 64, in_page, u.h, z, &sh.v_full[s]);
@@ -347,7 +314,7 @@ __device__ bool pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) 
         for (int i = 0; i < kPrTile / 16; ++i)
             tc_mma_bf16_ts(tmem + 256 + x * 128, tmem + x * 128 + i * 8, v + i * (2048 >> 4), pv, n > 0 || i > 0);
     };
-    auto told = [&](uint64_t* bar, uint32_t parity) { return pr_wait(bar, parity, &sh.dead); };
+    auto told = [&](uint64_t* bar, uint32_t parity) { return wait_or_give_up(bar, parity, &sh.dead); };
     auto commit = [&](uint64_t* bar) {
         if (mine) tc_commit(bar);
     };
@@ -384,7 +351,7 @@ __device__ void pr_look(const PromptParams& p, PrShared& sh, uint8_t* base) {
     const int t = threadIdx.x - 320, warp = t >> 5;   // of 64
     for (int n = 0; n < u.hi - u.lo; ++n) {
         const int s = n % kPrStages, tile = u.tile(u.lo + n);
-        if (!pr_wait(&sh.v_full[s], (n / kPrStages) & 1, &sh.dead)) return;
+        if (!wait_or_give_up(&sh.v_full[s], (n / kPrStages) & 1, &sh.dead)) return;
         if (!calm.has(tile)) {
             uint32_t some = 0;
             uint8_t* v = base + L::kV + s * L::kTileBytes;
@@ -482,7 +449,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     bool good = true;
     for (int n = 0; n < tiles; ++n) {
         const int tile = u.tile(lo + n);
-        good = pr_wait(&sh.s_full[half], n & 1, &sh.dead);
+        good = wait_or_give_up(&sh.s_full[half], n & 1, &sh.dead);
         if (!good) break;
         tc_fence_after();
         float x[4][32];
@@ -554,7 +521,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
         tmem_put_wait();
         if (!sh.whole[2].has(tile)) {
             const int s = n % kPrStages;
-            good = pr_wait(&sh.v_ok[s], (n / kPrStages) & 1, &sh.dead);
+            good = wait_or_give_up(&sh.v_ok[s], (n / kPrStages) & 1, &sh.dead);
             if (!good) break;
             if (sh.is_wild(s)) pr_by_hand<D>(o_at, s_at, base + L::kV + s * L::kTileBytes, n == 0);
         }
@@ -563,7 +530,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
         if ((r & 31) == 0) mbar_arrive(&sh.p_full[half]);
     }
     if (good && tiles > 0) {
-        good = pr_wait(&sh.o_full[half], 0, &sh.dead);
+        good = wait_or_give_up(&sh.o_full[half], 0, &sh.dead);
         tc_fence_after();
     }
     const bool live = r < p.tq * p.G && token < u.ntok;

@@ -157,6 +157,46 @@ int done(int rc) {
 
 int64_t round16(int64_t n) { return (n + 15) & ~int64_t(15); }
 
+// ------------------------------------------------------------------ tensor maps
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn find_encode() {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(f);
+}
+// Map of a tensor [..][d] of bf16 or bytes (sizes and strides in elements, innermost first without d), for boxes of
+// `width` elements of d, swizzled by their width of 128 or 64 bytes.  Steps of zero (a dimension that is expanded) and of 2^40
+// bytes and more have no map.
+int tensor_map(CUtensorMap* m, const void* base, int bytes, int d, uint32_t width, std::initializer_list<Dim> dims,
+               std::initializer_list<uint32_t> box) {
+    static const EncodeFn encode = find_encode();
+    if (!encode) return SKV_ERR_CUDA;
+    cuuint64_t size[4] = {static_cast<cuuint64_t>(d)}, step[3];
+    cuuint32_t boxes[4] = {width}, ones[4] = {1, 1, 1, 1};
+    int n = 1;
+    for (const Dim& x : dims) {
+        size[n] = x.n;
+        step[n - 1] = static_cast<cuuint64_t>(x.n > 1 ? x.s : d) * bytes;     // (a step that is never taken has to be some step)
+        if (step[n - 1] == 0 || step[n - 1] >= cuuint64_t(1) << 40) return SKV_ERR_INVALID;
+        ++n;
+    }
+    std::copy(box.begin(), box.end(), boxes + 1);
+    return encode(m, bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, n, const_cast<void*>(base), size,
+                  step, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  width * bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? SKV_OK
+               : SKV_ERR_INVALID;
+}
+
 // ------------------------------------------------------------------ attention
 
 struct AttnSpace { int Gp; int64_t joint, rec, rec_stat, stat, z, bytes; };
@@ -234,39 +274,6 @@ int prompt_space(const skv_paged_prompt_args* a, PromptSpace* w) {
     w->stat = rows * c.head_dim * 4;
     w->bytes = w->stat + rows * 8;
     return SKV_OK;
-}
-
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeFn find_encode() {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess) {
-        cudaGetLastError();
-        return nullptr;
-    }
-    return reinterpret_cast<EncodeFn>(f);
-}
-// Map of a bf16 tensor [..][d] (sizes and strides in elements, innermost first without d), 64 elements of d to a box
-int tensor_map(CUtensorMap* m, const void* base, int d, std::initializer_list<Dim> dims, std::initializer_list<uint32_t> box) {
-    static const EncodeFn encode = find_encode();
-    if (!encode) return SKV_ERR_CUDA;
-    cuuint64_t size[4] = {static_cast<cuuint64_t>(d)}, step[3];
-    cuuint32_t boxes[4] = {64}, ones[4] = {1, 1, 1, 1};
-    int n = 1;
-    for (const Dim& x : dims) {
-        size[n] = x.n;
-        step[n - 1] = (x.n > 1 ? x.s : d) * 2;           // (a step that is never taken has to be some step)
-        if (step[n - 1] == 0 || step[n - 1] >= cuuint64_t(1) << 40) return SKV_ERR_INVALID;
-        ++n;
-    }
-    std::copy(box.begin(), box.end(), boxes + 1);
-    return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n, const_cast<void*>(base), size, step, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? SKV_OK
-               : SKV_ERR_INVALID;
 }
 
 // ------------------------------------------------------------------ status
@@ -404,7 +411,14 @@ int attend(const skv_paged_attention_args* a, const Part* part, const char* name
         if (int rc = check_memory({part->scales->k, part->scales->v}, dev.id)) return rc;
     Range range(name);
     uint8_t* ws = static_cast<uint8_t*>(a->workspace);
-    PagedAttnParams p{};
+    PagedCodesParams p{};
+    if (codes) {
+        const uint32_t d = c.head_dim, box = std::min(c.page_size, 16);
+        if (int rc = tensor_map(&p.mk, c.k, 1, d, d, {{c.page_size, c.k_row}, {c.n_kv_heads, c.k_head}, {c.n_pages, c.k_page}}, {box, 1, 1}))
+            return rc;
+        if (int rc = tensor_map(&p.mv, c.v, 1, d, d, {{c.page_size, c.v_row}, {c.n_kv_heads, c.v_head}, {c.n_pages, c.v_page}}, {box, 1, 1}))
+            return rc;
+    }
     p.c = view(c);
     p.span = p.c.cap;
     if (part) {
@@ -434,6 +448,7 @@ int attend(const skv_paged_attention_args* a, const Part* part, const char* name
         p.weight = a->weight; p.weight_out = a->weight_out; p.row_pitch = a->row_pitch;
     }
     const int ctas = paged_attn_ctas(c.dtype, c.head_dim, dev.nsm < kMaxSms ? dev.nsm : kMaxSms);
+    if (codes) return done(launch_paged_codes(c.head_dim, p, ctas, stream));
     return done((part ? launch_paged_span : launch_paged_attn)(c.dtype, c.head_dim, p, ctas, stream));
 }
 }  // namespace
@@ -539,10 +554,10 @@ int shadowkv_paged_prompt_attention(const skv_paged_prompt_args* a, skv_stream s
         return rc;
     const uint32_t G = a->n_q_heads / c.n_kv_heads, tq = 128 / G, box = std::min(c.page_size, 128);
     CUtensorMap mq, mk, mv;
-    if (int rc = tensor_map(&mq, a->q, c.head_dim, {{a->n_q_heads, a->q_head}, {a->tokens, a->q_tok}}, {G, tq})) return rc;
-    if (int rc = tensor_map(&mk, c.k, c.head_dim, {{c.page_size, c.k_row}, {c.n_kv_heads, c.k_head}, {c.n_pages, c.k_page}}, {box, 1, 1}))
+    if (int rc = tensor_map(&mq, a->q, 2, c.head_dim, 64, {{a->n_q_heads, a->q_head}, {a->tokens, a->q_tok}}, {G, tq})) return rc;
+    if (int rc = tensor_map(&mk, c.k, 2, c.head_dim, 64, {{c.page_size, c.k_row}, {c.n_kv_heads, c.k_head}, {c.n_pages, c.k_page}}, {box, 1, 1}))
         return rc;
-    if (int rc = tensor_map(&mv, c.v, c.head_dim, {{c.page_size, c.v_row}, {c.n_kv_heads, c.v_head}, {c.n_pages, c.v_page}}, {box, 1, 1}))
+    if (int rc = tensor_map(&mv, c.v, 2, c.head_dim, 64, {{c.page_size, c.v_row}, {c.n_kv_heads, c.v_head}, {c.n_pages, c.v_page}}, {box, 1, 1}))
         return rc;
     Range range("shadowkv_paged_prompt_attention");
     PromptParams p{};

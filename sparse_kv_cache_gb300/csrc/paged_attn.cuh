@@ -102,10 +102,34 @@ __device__ __forceinline__ float4 ld_cluster_v4f(uint32_t addr) {
                  : "memory");
     return v;
 }
-// two e4m3 codes (the lower bytes) as fp16 numbers
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two), __NV_E4M3);
-    return static_cast<uint32_t>(h.y) << 16 | h.x;
+// four e4m3 codes as fp16 numbers
+__device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t four) {
+    uint2 v;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(v.x), "=r"(v.y)
+        : "r"(four));
+    return v;
+}
+// 16 or 8 bytes of a row that is there, read once
+__device__ __forceinline__ uint4 ld_row(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_row8(const void* p) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 ld_shared8(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
 }
 // the upper halves of two floats
 __device__ __forceinline__ uint32_t cut_bf16x2(float lo, float hi) {
@@ -144,6 +168,10 @@ template <bool kSpan>
 __device__ __forceinline__ bool any_seen(const PagedView& c, int row, int n) {
     return !kSpan || row < c.sink || row + 7 >= n - c.window;
 }
+
+// CTAs per SM, by the registers that 128 and 64 dimensions need (see the launches below), and e4m3's tiles in
+// shared memory
+constexpr int occ_of(int dtype, int d) { return (dtype == SKV_F32 || dtype == SKV_E4M3 ? 2 : 3) + (d == 64 ? 1 : 0); }
 
 // ------------------------------------------------------------------ the split of the work
 
@@ -339,17 +367,19 @@ __device__ __forceinline__ float share_weight(float x, float l, float m) {
 struct HoldNone { __device__ __forceinline__ void operator()() const {} };     // a warp of few tiles
 
 // Page ids of a warp's coming tiles, and the scales of an 8-bit cache: lane j holds those of tile j of the
-// current 32, of its first and last eight rows.
+// current 32, of its first and last eight rows.  `all`: its 16 rows all take part, and lie in one page.
 struct PageIds { int a, b; };
+struct SpanIds : PageIds { int all; };
 struct Scales { float ka, kb, va, vb; };           // of keys; of values, in powers of two
-struct ScaledIds : PageIds { Scales s; };
-template <bool kScaled> struct IdsOf { using type = PageIds; };
-template <> struct IdsOf<true> { using type = ScaledIds; };
+struct ScaledIds : SpanIds { Scales s; };
+template <bool kSpan, bool kScaled> struct IdsOf { using type = PageIds; };
+template <> struct IdsOf<true, false> { using type = SpanIds; };
+template <> struct IdsOf<true, true> { using type = ScaledIds; };
 
 template <bool kSpan, bool kScaled>
-__device__ __forceinline__ typename IdsOf<kScaled>::type page_ids(const PagedAttnParams& p, int b, int h, int row, int end, int n) {
+__device__ __forceinline__ typename IdsOf<kSpan, kScaled>::type page_ids(const PagedAttnParams& p, int b, int h, int row, int end, int n) {
     const PagedView& c = p.c;
-    typename IdsOf<kScaled>::type id;
+    typename IdsOf<kSpan, kScaled>::type id;
     id.a = id.b = -1;
     const int real = real_row<kSpan>(c, row, n);
     if (row < end) {
@@ -358,6 +388,8 @@ __device__ __forceinline__ typename IdsOf<kScaled>::type page_ids(const PagedAtt
         else if (row + 8 < end && any_seen<kSpan>(c, real + 8, n))
             id.b = c.lg > 3 && id.a >= 0 ? id.a : page_of(c, b, real + 8, g_err, 712);
     }
+    if constexpr (kSpan)
+        id.all = c.lg > 3 && id.a >= 0 && id.b >= 0 && row + 16 <= end && (real + 15 < c.sink || real >= n - c.window);
     if constexpr (kScaled) {
         const int mask = (1 << c.lg) - 1, blocks = 1 << (c.lg - p.lgb);
         auto at = [&](int page, int r) { return (static_cast<int64_t>(page) * c.H + h) * blocks + ((r & mask) >> p.lgb); };
@@ -376,10 +408,18 @@ __device__ __forceinline__ typename IdsOf<kScaled>::type page_ids(const PagedAtt
 __device__ __forceinline__ PageIds of_tile(const PageIds& ids, int t) {
     return PageIds{__shfl_sync(0xffffffffu, ids.a, t), __shfl_sync(0xffffffffu, ids.b, t)};
 }
+__device__ __forceinline__ SpanIds of_tile(const SpanIds& ids, int t) {
+    SpanIds x;
+    x.a = __shfl_sync(0xffffffffu, ids.a, t);
+    x.b = __shfl_sync(0xffffffffu, ids.b, t);
+    x.all = __shfl_sync(0xffffffffu, ids.all, t);
+    return x;
+}
 __device__ __forceinline__ ScaledIds of_tile(const ScaledIds& ids, int t) {
     ScaledIds x;
     x.a = __shfl_sync(0xffffffffu, ids.a, t);
     x.b = __shfl_sync(0xffffffffu, ids.b, t);
+    x.all = __shfl_sync(0xffffffffu, ids.all, t);
     x.s.ka = __shfl_sync(0xffffffffu, ids.s.ka, t);
     x.s.kb = __shfl_sync(0xffffffffu, ids.s.kb, t);
     x.s.va = __shfl_sync(0xffffffffu, ids.s.va, t);
@@ -392,8 +432,8 @@ __device__ __forceinline__ ScaledIds of_tile(const ScaledIds& ids, int t) {
 template <bool kSpan, bool kScaled>
 struct PieceOf {
     int b, h, row, end, n;
-    typename IdsOf<kScaled>::type ids;
-    __device__ __forceinline__ typename IdsOf<kScaled>::type ask(const PagedAttnParams& p, int from) const {
+    typename IdsOf<kSpan, kScaled>::type ids;
+    __device__ __forceinline__ typename IdsOf<kSpan, kScaled>::type ask(const PagedAttnParams& p, int from) const {
         return page_ids<kSpan, kScaled>(p, b, h, from + (threadIdx.x & 31) * kPaTile, end, n);
     }
 };
@@ -480,14 +520,22 @@ struct KeepShared {
 // therefore one of its own: the largest product of a probability and a scale.
 enum class Holds { kBf16, kE5M2, kE4M3 };
 
+template <bool kCodes> struct ParamsOf { using type = PagedAttnParams; };
+template <> struct ParamsOf<true> { using type = PagedCodesParams; };
+
 template <int D, Holds kHolds, bool kSpanned = false>
 struct TileTC {
     static constexpr bool kSpan = kSpanned, kE5M2 = kHolds == Holds::kE5M2, kE4M3 = kHolds == Holds::kE4M3;
     using Piece = PieceOf<kSpan, kE4M3>;
-    using Ids = typename IdsOf<kE4M3>::type;
+    using Ids = typename IdsOf<kSpan, kE4M3>::type;
     static constexpr int kKV = kE4M3 ? D / 64 : D / 32;    // 16-byte words of a key row per lane
     static constexpr int kVV = kHolds != Holds::kBf16 ? 1 : D / 64;      // words of a value row per lane
     // fp16 probabilities: up to 2^15, the more of the small ones are normal (2^30 e5m2 values fit into a sum)
+    // e4m3: tiles on their way to shared memory.  Two are worked on together, side by side.
+    static constexpr int kRing = !kE4M3 ? 0 : D == 64 ? 6 : 4;
+    static constexpr int kSlotBytes = 32 * D, kWarpBytes = kE4M3 ? kRing * kSlotBytes + 1024 : 0;
+    using Params = typename ParamsOf<kE4M3>::type;
+    static constexpr int kOcc = occ_of(kE4M3 ? SKV_E4M3 : SKV_BF16, D);
     static constexpr float kBaseShift = kE5M2 ? 7.f : 0.f;
     static constexpr float kValueShift = 7.f;              // the same where values have a base of their own
     static constexpr bool kLow = !kE5M2;                   // whether p.down is in the sums of values
@@ -495,7 +543,7 @@ struct TileTC {
     float o[D / 16][4];
     float m0, m1, l0, l1;                                  // heads 2c and 2c + 1
     float v0, v1;                                          // e4m3: bases of the sums of values
-    float q0, q1;                                          // e4m3: powers of two of the queries
+    float q0, q1;                                          // e4m3: powers of two of the queries, times scale
     bool held;                                             // whether the unit has held sums
 
     __device__ __forceinline__ void load_q(const PagedAttnParams& p, int b, int h) {
@@ -534,8 +582,8 @@ struct TileTC {
                 }
                 q[j] = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            q0 = __shfl_sync(0xffffffffu, up, 8 * c);
-            q1 = __shfl_sync(0xffffffffu, up, 8 * c + 4);
+            q0 = __shfl_sync(0xffffffffu, up, 8 * c) * p.scale_log2;
+            q1 = __shfl_sync(0xffffffffu, up, 8 * c + 4) * p.scale_log2;
         }
     }
     __device__ __forceinline__ void reset() {
@@ -553,9 +601,23 @@ struct TileTC {
     __device__ __forceinline__ static bool takes_part(const PagedAttnParams& p, const Piece& at, int row, int i, int id) {
         return id >= 0 && row + i < at.end && seen<kSpan>(p.c, real_row<kSpan>(p.c, row, at.n) + i, at.n);
     }
+    static constexpr int kKeyBytes = kE4M3 ? 1 : 2, kValueBytes = kHolds != Holds::kBf16 ? 1 : 2;
     __device__ __forceinline__ void load_k(const PagedAttnParams& p, const Piece& at, int row, const Ids& id, Keys& k) {
         const int r = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3, mask = (1 << p.c.lg) - 1;
         const int real = real_row<kSpan>(p.c, row, at.n);
+        if constexpr (kSpan) {
+            if (id.all) {
+                const uint8_t* a = static_cast<const uint8_t*>(p.c.k) + c * 16 +
+                                   (at.h * p.c.k_head + id.a * p.c.k_page + ((real & mask) + r) * p.c.k_row) * kKeyBytes;
+                const uint8_t* b = a + 8 * kKeyBytes * p.c.k_row;
+#pragma unroll
+                for (int j = 0; j < kKV; ++j) {
+                    k.a[j] = ld_row(a + 64 * j);
+                    k.b[j] = ld_row(b + 64 * j);
+                }
+                return;
+            }
+        }
         const bool ia = takes_part(p, at, row, r, id.a), ib = takes_part(p, at, row, 8 + r, id.b);
         if constexpr (kE4M3) {
             const uint8_t* base = static_cast<const uint8_t*>(p.c.k) + at.h * p.c.k_head + c * 16;
@@ -580,6 +642,21 @@ struct TileTC {
     __device__ __forceinline__ void load_v(const PagedAttnParams& p, const Piece& at, int row, const Ids& ids, Values& v) {
         const int r = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3, mask = (1 << p.c.lg) - 1;
         const int real = real_row<kSpan>(p.c, row, at.n), h = at.h;
+        if constexpr (kSpan) {
+            if (ids.all) {
+                const int64_t step = p.c.v_row * kValueBytes;
+                const uint8_t* x = static_cast<const uint8_t*>(p.c.v) + r * (kHolds != Holds::kBf16 ? D / 8 : 16) +
+                                   (h * p.c.v_head + ids.a * p.c.v_page + ((real & mask) + 2 * c) * p.c.v_row) * kValueBytes;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint8_t* src = x + (i & 1) * step + (i >> 1) * 8 * step;
+#pragma unroll
+                    for (int j = 0; j < kVV; ++j)
+                        v.v[i][j] = kHolds != Holds::kBf16 && D == 64 ? ld_row8(src) : ld_row(src + 128 * j);
+                }
+                return;
+            }
+        }
         constexpr int es = kHolds != Holds::kBf16 ? 1 : 2, lane_bytes = kHolds != Holds::kBf16 ? D / 8 : 16;
         const uint8_t* base = static_cast<const uint8_t*>(p.c.v) + h * p.c.v_head * es + r * lane_bytes;
 #pragma unroll
@@ -598,23 +675,23 @@ struct TileTC {
             }
         }
     }
-    // scores of the tile's rows: s[0], s[1] row r, s[2], s[3] row r + 8, heads 2c and 2c + 1
+    // scores of the tile's rows: s[0], s[1] row r, s[2], s[3] row r + 8, heads 2c and 2c + 1 (e4m3: times scale)
     __device__ __forceinline__ void scores(const Keys& k, const Ids& id, float (&s)[4]) {
         s[0] = s[1] = s[2] = s[3] = 0.f;
         if constexpr (kE4M3) {
+            float u[4] = {0.f, 0.f, 0.f, 0.f};       // (every other product: half the chain)
 #pragma unroll
             for (int j = 0; j < kKV; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t a = word(k.a[j], i), b = word(k.b[j], i);
+                    const uint2 a = e4m3x4_to_f16x4(word(k.a[j], i)), b = e4m3x4_to_f16x4(word(k.b[j], i));
                     const uint4& x = q[2 * j + i / 2];
-                    mma_f16(s, e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(b), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(b >> 16),
-                            word(x, 2 * (i & 1)), word(x, 2 * (i & 1) + 1));
+                    mma_f16(i & 1 ? u : s, a.x, b.x, a.y, b.y, word(x, 2 * (i & 1)), word(x, 2 * (i & 1) + 1));
                 }
-            s[0] = s[0] * id.s.ka * q0;
-            s[1] = s[1] * id.s.ka * q1;
-            s[2] = s[2] * id.s.kb * q0;
-            s[3] = s[3] * id.s.kb * q1;
+            s[0] = (s[0] + u[0]) * id.s.ka * q0;
+            s[1] = (s[1] + u[1]) * id.s.ka * q1;
+            s[2] = (s[2] + u[2]) * id.s.kb * q0;
+            s[3] = (s[3] + u[3]) * id.s.kb * q1;
         } else {
 #pragma unroll
             for (int j = 0; j < kKV; ++j) {
@@ -636,27 +713,21 @@ struct TileTC {
             *reinterpret_cast<float2*>(z + (8 + r) * p.Gp + 2 * c) =
                 idb >= 0 ? make_float2(s[2], s[3]) : make_float2(none, none);
     }
-    // probabilities against the running base; returns P^T as the second product's operand, b, and what
-    // its rounding to bf16 left, r
-    __device__ __forceinline__ void softmax(const PagedAttnParams& p, const Piece& at, int row, const Ids& id, const float (&s)[4],
-                                            uint32_t& b0, uint32_t& b1, uint32_t& r0, uint32_t& r1) {
-        const int r = (threadIdx.x & 31) >> 2;
-        const float scale = p.scale_log2, down = p.down;
-        // scores in powers of two, -inf for an absent row (whatever the sign of the scale)
-        const bool ia = takes_part(p, at, row, r, id.a), ib = takes_part(p, at, row, 8 + r, id.b);
-        float x0 = ia ? s[0] * scale : -CUDART_INF_F, x1 = ia ? s[1] * scale : -CUDART_INF_F;
-        float x2 = ib ? s[2] * scale : -CUDART_INF_F, x3 = ib ? s[3] * scale : -CUDART_INF_F;
-        float t0 = fmaxf(x0, x2), t1 = fmaxf(x1, x3);
+    // e4m3, two tiles: x and z are scores in powers of two (-inf for an absent row); b probabilities times the scales of
+    // their values, against a base of their own
+    __device__ __forceinline__ void softmax_two(const Ids& id, const Ids& jd, const float (&x)[4], const float (&z)[4], uint32_t (&b)[4]) {
         if constexpr (kE4M3) {
-            // the same of a probability's product with its value's scale
-            float y0 = fmaxf(x0 + id.s.va, x2 + id.s.vb), y1 = fmaxf(x1 + id.s.va, x3 + id.s.vb);
+            const float xa = id.s.va, xb = id.s.vb, za = jd.s.va, zb = jd.s.vb;
+            float t0 = fmaxf(fmaxf(x[0], x[2]), fmaxf(z[0], z[2])), t1 = fmaxf(fmaxf(x[1], x[3]), fmaxf(z[1], z[3]));
+            float y0 = fmaxf(fmaxf(x[0] + xa, x[2] + xb), fmaxf(z[0] + za, z[2] + zb));
+            float y1 = fmaxf(fmaxf(x[1] + xa, x[3] + xb), fmaxf(z[1] + za, z[3] + zb));
             if (__any_sync(0xffffffffu, t0 > m0 + kPaSlack || t1 > m1 + kPaSlack || y0 > v0 + kPaSlack || y1 > v1 + kPaSlack)) {
 #pragma unroll
-                for (int x = 4; x < 32; x <<= 1) {
-                    t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
-                    t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
-                    y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, x));
-                    y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, x));
+                for (int d = 4; d < 32; d <<= 1) {
+                    t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, d));
+                    t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, d));
+                    y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, d));
+                    y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, d));
                 }
                 t0 = fmaxf(t0, m0);
                 t1 = fmaxf(t1, m1);
@@ -678,19 +749,42 @@ struct TileTC {
                     o[i][3] *= w1;
                 }
             }
+            // (a base of -infinity: nothing has scored above it, and what is there weighs nothing)
             const float n0 = m0 == -CUDART_INF_F ? 0.f : m0, n1 = m1 == -CUDART_INF_F ? 0.f : m1;
-            l0 += (ia ? exp2_fast(fmaf(s[0], scale, -n0)) : 0.f) + (ib ? exp2_fast(fmaf(s[2], scale, -n0)) : 0.f);
-            l1 += (ia ? exp2_fast(fmaf(s[1], scale, -n1)) : 0.f) + (ib ? exp2_fast(fmaf(s[3], scale, -n1)) : 0.f);
+            l0 += (exp2_fast(x[0] - n0) + exp2_fast(x[2] - n0)) + (exp2_fast(z[0] - n0) + exp2_fast(z[2] - n0));
+            l1 += (exp2_fast(x[1] - n1) + exp2_fast(x[3] - n1)) + (exp2_fast(z[1] - n1) + exp2_fast(z[3] - n1));
             const float u0 = v0 == -CUDART_INF_F ? 0.f : v0 - kValueShift, u1 = v1 == -CUDART_INF_F ? 0.f : v1 - kValueShift;
-            x0 = ia ? exp2_fast(fmaf(s[0], scale, id.s.va - u0)) : 0.f;
-            x1 = ia ? exp2_fast(fmaf(s[1], scale, id.s.va - u1)) : 0.f;
-            x2 = ib ? exp2_fast(fmaf(s[2], scale, id.s.vb - u0)) : 0.f;
-            x3 = ib ? exp2_fast(fmaf(s[3], scale, id.s.vb - u1)) : 0.f;
-            const __half2 lo = __floats2half2_rn(x0, x1), hi = __floats2half2_rn(x2, x3);
-            b0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&lo));
-            b1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi));
-            return;
+            auto two = [](float lo, float hi) {
+                const __half2 h = __floats2half2_rn(exp2_fast(lo), exp2_fast(hi));
+                return transpose8x8(*reinterpret_cast<const uint32_t*>(&h));
+            };
+            b[0] = two(x[0] + (xa - u0), x[1] + (xa - u1));
+            b[1] = two(x[2] + (xb - u0), x[3] + (xb - u1));
+            b[2] = two(z[0] + (za - u0), z[1] + (za - u1));
+            b[3] = two(z[2] + (zb - u0), z[3] + (zb - u1));
         }
+    }
+    // probabilities against the running base; returns P^T as the second product's operand, b, and what
+    // its rounding to bf16 left, r
+    __device__ __forceinline__ void softmax(const PagedAttnParams& p, const Piece& at, int row, const Ids& id, const float (&s)[4],
+                                            uint32_t& b0, uint32_t& b1, uint32_t& r0, uint32_t& r1) {
+        const int r = (threadIdx.x & 31) >> 2;
+        const float scale = p.scale_log2, down = p.down;
+        // scores in powers of two, -inf for an absent row (whatever the sign of the scale)
+        bool ia, ib;
+        if constexpr (kSpan) {
+            ia = ib = true;
+            if (!id.all) {
+                ia = takes_part(p, at, row, r, id.a);
+                ib = takes_part(p, at, row, 8 + r, id.b);
+            }
+        } else {
+            ia = takes_part(p, at, row, r, id.a);
+            ib = takes_part(p, at, row, 8 + r, id.b);
+        }
+        float x0 = ia ? s[0] * scale : -CUDART_INF_F, x1 = ia ? s[1] * scale : -CUDART_INF_F;
+        float x2 = ib ? s[2] * scale : -CUDART_INF_F, x3 = ib ? s[3] * scale : -CUDART_INF_F;
+        float t0 = fmaxf(x0, x2), t1 = fmaxf(x1, x3);
         if (__any_sync(0xffffffffu, t0 > m0 + kPaSlack || t1 > m1 + kPaSlack)) {
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) {
@@ -744,9 +838,9 @@ struct TileTC {
             if (kE4M3) {
                 // tile t: dimensions 2t and 2t + 1 of the lane's, of two rows each
                 const uint32_t sel = (t & 1) ? 0x7362 : 0x5140;
-                const uint32_t lo = __byte_perm(word(v.v[0][0], t >> 1), word(v.v[1][0], t >> 1), sel);
-                const uint32_t hi = __byte_perm(word(v.v[2][0], t >> 1), word(v.v[3][0], t >> 1), sel);
-                mma_f16(o[t], e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2(hi >> 16), b0, b1);
+                const uint2 lo = e4m3x4_to_f16x4(__byte_perm(word(v.v[0][0], t >> 1), word(v.v[1][0], t >> 1), sel));
+                const uint2 hi = e4m3x4_to_f16x4(__byte_perm(word(v.v[2][0], t >> 1), word(v.v[3][0], t >> 1), sel));
+                mma_f16(o[t], lo.x, lo.y, hi.x, hi.y, b0, b1);
             } else if (kE5M2) {
                 // tile t: dimensions 2t and 2t + 1 of the lane's; a byte becomes the upper half of an fp16
                 const uint32_t sel = (t & 1) ? 0x7362 : 0x5140;
@@ -884,12 +978,197 @@ struct TileTC {
             }
         }
     }
+    // Where 16 bytes of a row of a slot's keys or values are: the copies swizzle them, 128 bytes by eight rows, 64 by
+    // four pairs of rows.
+    __device__ __forceinline__ static uint32_t place(int row, int word) {
+        return D == 128 ? row * 128 + ((word ^ (row & 7)) << 4) : row * 64 + ((word ^ (row >> 1 & 3)) << 4);
+    }
+    __device__ __forceinline__ void take_k(uint32_t slot, Keys& k) const {
+        const int r = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
+#pragma unroll
+        for (int j = 0; j < kKV; ++j) {
+            k.a[j] = ld_shared16(slot + place(r, 4 * j + c));
+            k.b[j] = ld_shared16(slot + place(r + 8, 4 * j + c));
+        }
+    }
+    __device__ __forceinline__ void take_v(uint32_t slot, Values& v) const {
+        const int r = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 2 * c + (i & 1) + (i >> 1) * 8;
+            if (D == 64) {
+                const uint2 x = ld_shared8(slot + place(row, r >> 1) + (r & 1) * 8);
+                v.v[i][0] = make_uint4(x.x, x.y, 0, 0);
+            } else {
+                v.v[i][0] = ld_shared16(slot + place(row, r));
+            }
+        }
+    }
+    __device__ __forceinline__ static void clear(Values& v, int i) { v.v[i][0] = make_uint4(0, 0, 0, 0); }
+    // The same as stream() below, with kRing tiles in shared memory: the copies go through the pieces by themselves,
+    // ahead of the products, and leave a note of each tile beside its slot.  A copy brings whole tiles (zeros for a page
+    // that is not followed); rows that take no part are dropped on the way to the products.
+    struct Note { Piece at; int last, more; };         // a tile: its place, whether it ends its piece, whether one follows
+    struct Ring { Note note[kE4M3 ? kRing : 1]; uint64_t full[kE4M3 ? kRing : 1]; int dead; };
+    template <class Hold, class Next, class Done>
+    __device__ __forceinline__ void stream_ring(const Params& p, Piece ahead, void* memory, Hold put_by, Next next, Done done) {
+        static_assert(sizeof(Ring) <= 1024, "");
+        const uint32_t base = smem_u32(memory);
+        Ring& ring = *reinterpret_cast<Ring*>(static_cast<uint8_t*>(memory) + kRing * kSlotBytes);
+        const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3, mask = (1 << p.c.lg) - 1;
+        if (lane == 0) {
+            for (int i = 0; i < kRing; ++i) mbar_init(&ring.full[i], 1);
+            ring.dead = 0;
+            fence_mbar_init();
+            // rows that kernels before this one wrote, to be read by the copy engine
+            asm volatile("fence.proxy.async;" ::: "memory");
+        }
+        __syncwarp();
+        Piece then;
+        bool more = next(then), any = true;
+        Ids ids = ahead.ids, later = ids;
+        if (ahead.row + 32 * kPaTile < ahead.end) later = ahead.ask(p, ahead.row + 32 * kPaTile);
+        int t = 0, to = 0, asked = 0;
+        auto issue = [&] {
+            if (!any) return;
+            const Ids id = of_tile(ids, t);
+            const bool last = ahead.row + kPaTile >= ahead.end;
+            if (lane == 0) {
+                Note& note = ring.note[to];
+                note.at = ahead;
+                note.at.ids = id;
+                note.last = last;
+                note.more = more;
+                const uint32_t slot = base + to * kSlotBytes;
+                const int row = real_row<kSpan>(p.c, ahead.row, ahead.n) & mask, none = static_cast<int>(p.c.n_pages);
+                const int a = id.a < 0 ? none : id.a, b = id.b < 0 ? none : id.b;
+                mbar_arrive_expect_tx(&ring.full[to], kSlotBytes);
+                if (p.c.lg > 3) {          // (halves of a tile in one page: a's, where it is looked at)
+                    const int page = id.a < 0 ? b : a;
+                    tma_load_4d(slot, &p.mk, 0, row, ahead.h, page, &ring.full[to]);
+                    tma_load_4d(slot + 16 * D, &p.mv, 0, row, ahead.h, page, &ring.full[to]);
+                } else {
+                    tma_load_4d(slot, &p.mk, 0, 0, ahead.h, a, &ring.full[to]);
+                    tma_load_4d(slot + 8 * D, &p.mk, 0, 0, ahead.h, b, &ring.full[to]);
+                    tma_load_4d(slot + 16 * D, &p.mv, 0, 0, ahead.h, a, &ring.full[to]);
+                    tma_load_4d(slot + 24 * D, &p.mv, 0, 0, ahead.h, b, &ring.full[to]);
+                }
+            }
+            to = to + 1 == kRing ? 0 : to + 1;
+            ++asked;
+            if (!last) {
+                ahead.row += kPaTile;
+                if (++t == 32) {
+                    t = 0;
+                    ids = later;
+                    if (ahead.row + 32 * kPaTile < ahead.end) later = ahead.ask(p, ahead.row + 32 * kPaTile);
+                }
+            } else if (more) {
+                ahead = then;
+                ids = ahead.ids;
+                t = 0;
+                if (ahead.row + 32 * kPaTile < ahead.end) later = ahead.ask(p, ahead.row + 32 * kPaTile);
+                more = next(then);
+            } else {
+                any = false;
+            }
+        };
+        load_q(p, ahead.b, ahead.h);
+        reset();
+#pragma unroll 1
+        for (int i = 0; i < kRing; ++i) issue();
+        int at = 0, run = 0;
+        uint32_t turn = 0;                 // of the ring: what its slots' barriers are waited for with
+        bool good = true;
+        __syncwarp();
+        for (;;) {
+            good = wait_or_give_up(&ring.full[at], turn, &ring.dead) && good;
+            const Note& one = ring.note[at];
+            const bool two = !one.last;
+            const int at2 = at + 1 == kRing ? 0 : at + 1;
+            const uint32_t turn2 = at2 ? turn : turn ^ 1;
+            if (two) good = wait_or_give_up(&ring.full[at2], turn2, &ring.dead) && good;
+            // two tiles into registers, and the next copies into their slots
+            const Note& second = two ? ring.note[at2] : one;
+            const Ids id1 = one.at.ids, id2 = second.at.ids;
+            const bool last = second.last, more_behind = second.more;
+            const int b = one.at.b, h = one.at.h;
+            bool in[4] = {true, true, two, two};
+            Keys k1, k2;
+            Values x1, x2;
+            take_k(base + at * kSlotBytes, k1);
+            take_v(base + at * kSlotBytes + 16 * D, x1);
+            take_k(base + at2 * kSlotBytes, k2);
+            take_v(base + at2 * kSlotBytes + 16 * D, x2);
+            if (!id1.all) {
+                in[0] = takes_part(p, one.at, one.at.row, r, id1.a);
+                in[1] = takes_part(p, one.at, one.at.row, 8 + r, id1.b);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!takes_part(p, one.at, one.at.row, 2 * c + (i & 1) + (i >> 1) * 8, i < 2 ? id1.a : id1.b)) clear(x1, i);
+            }
+            if (!two || !id2.all) {
+                in[2] = two && takes_part(p, second.at, second.at.row, r, id2.a);
+                in[3] = two && takes_part(p, second.at, second.at.row, 8 + r, id2.b);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!two || !takes_part(p, second.at, second.at.row, 2 * c + (i & 1) + (i >> 1) * 8, i < 2 ? id2.a : id2.b))
+                        clear(x2, i);
+            }
+            at = two ? at2 : at;
+            turn = two ? turn2 : turn;
+            at = at + 1 == kRing ? 0 : at + 1;
+            turn = at ? turn : turn ^ 1;
+            const int b_next = ring.note[at].at.b, h_next = ring.note[at].at.h;
+            __syncwarp();                  // every lane has read
+            issue();
+            if (two) issue();
+            float s1[4], s2[4];
+            scores(k1, id1, s1);
+            scores(k2, id2, s2);
+            if (last && more_behind) load_q(p, b_next, h_next);
+            if (!in[0]) s1[0] = s1[1] = -CUDART_INF_F;
+            if (!in[1]) s1[2] = s1[3] = -CUDART_INF_F;
+            if (!in[2]) s2[0] = s2[1] = -CUDART_INF_F;
+            if (!in[3]) s2[2] = s2[3] = -CUDART_INF_F;
+            uint32_t w[4];
+            softmax_two(id1, id2, s1, s2, w);
+            values(x1, w[0], w[1], 0, 0);
+            values(x2, w[2], w[3], 0, 0);
+            __syncwarp();                  // the notes of the copies above
+            if (!last) {
+                if (++run == 16) {
+                    run = 0;
+                    put_by();
+                }
+                continue;
+            }
+            run = 0;
+            if (!good) l0 = l1 = CUDART_NAN_F;
+            Piece piece{};
+            piece.b = b;
+            piece.h = h;
+            done(piece, more_behind);
+            if (!more_behind) break;
+            reset();
+        }
+        if (!good && lane == 0) {
+            // given up: no copy may be on its way when the CTA ends
+            set_err(g_err, DEV_ERR_TIMEOUT, 713);
+            for (int i = max(0, asked - kRing); i < asked; ++i) mbar_wait(&ring.full[i % kRing], i / kRing & 1);
+        }
+        __syncwarp();
+    }
     // The pieces from `cur` on, as one stream of tiles: the first loads of the next piece are on their
     // way before this one is done with.  next(piece) gives the following one; done(piece, whether there is
     // another) hands over; put_by() holds the sums.
     template <class Keep, class Hold, class Next, class Done>
-    __device__ __forceinline__ void stream(const PagedAttnParams& p, Piece cur, float*, Keep z, Hold put_by, Next next,
+    __device__ __forceinline__ void stream(const Params& p, Piece cur, void* ring, Keep z, Hold put_by, Next next,
                                            Done done) {
+        if constexpr (kE4M3) {
+            stream_ring(p, cur, ring, put_by, next, done);
+            return;
+        }
         Piece then;
         bool more = next(then);
         Ids ids = cur.ids, later = ids;
@@ -949,6 +1228,9 @@ template <int D, int G, bool kSpanned = false>
 struct TileF32 {
     static constexpr bool kSpan = kSpanned;
     using Piece = PieceOf<kSpan, false>;
+    using Params = PagedAttnParams;
+    static constexpr int kRing = 0, kWarpBytes = G * (D + 4) * 4;      // of shared memory: the queries
+    static constexpr int kOcc = occ_of(SKV_F32, D);
     static constexpr int kV = D / 64;      // float4 of a row per lane
     static constexpr bool kLow = true;     // whether p.down is in the sums of values
     float o[G][4 * kV];
@@ -1075,8 +1357,9 @@ struct TileF32 {
         }
     }
     template <class Keep, class Hold, class Next, class Done>
-    __device__ __forceinline__ void stream(const PagedAttnParams& p, Piece cur, float* s_q, Keep z, Hold put_by, Next next,
+    __device__ __forceinline__ void stream(const PagedAttnParams& p, Piece cur, void* queries, Keep z, Hold put_by, Next next,
                                            Done done) {
+        float* s_q = static_cast<float*>(queries);
         for (bool more = true; more;) {
             load_q(p, cur.b, cur.h, s_q);
             reset();
@@ -1232,9 +1515,19 @@ __device__ __forceinline__ void join_shares(const PagedAttnParams& p, JoinSmem<D
     }
 }
 
+// A warp's part of the dynamic shared memory (tiles begin at 1024 bytes).
+template <class Tile>
+constexpr int own_bytes() { return kPaWarps * Tile::kWarpBytes + (Tile::kRing ? 1024 : 0); }
+template <class Tile>
+__device__ __forceinline__ void* own_memory(void* all, int warp) {
+    uint8_t* at = static_cast<uint8_t*>(all);
+    if (Tile::kRing) at += (1024 - (smem_u32(at) & 1023)) & 1023;
+    return at + warp * Tile::kWarpBytes;
+}
+
 template <class Tile, int D, bool kF32, int G, int kOcc, bool kKeep>
-__global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_constant__ PagedAttnParams p) {
-    extern __shared__ __align__(16) float s_q[];       // fp32: [warps][G][D + 4] their queries
+__global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_constant__ typename Tile::Params p) {
+    extern __shared__ __align__(16) uint8_t s_warps[];  // fp32: [warps][G][D + 4] their queries; e4m3: their tiles
     __shared__ PlanSmem<kPaWarps> s_plan;
     __shared__ __align__(16) JoinSmem<D, G> js;
     begin_call();
@@ -1258,7 +1551,7 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_attn(const __grid_co
             if (!(begins && ends) && lane == 0) js.of[slot] = ShareOf{q.b, q.h, begins, ends, first && w0 == pl.lo};
             first = false;
         };
-        float* queries = s_q + warp * G * (D + 4);
+        void* queries = own_memory<Tile>(s_warps, warp);
         if constexpr (kKeep) tile.stream(p, head, queries, KeepGlobal{p}, put_by, next, done);
         else tile.stream(p, head, queries, KeepNone{}, put_by, next, done);
     }
@@ -1297,8 +1590,8 @@ __host__ __device__ __forceinline__ int cluster_tiles(int cap, int ranks) {
     return ((cap + kPaTile - 1) / kPaTile + parts - 1) / parts;
 }
 template <class Tile, int D, bool kF32, int G, int kOcc, bool kKeep>
-__global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid_constant__ PagedAttnParams p, int ranks) {
-    extern __shared__ __align__(16) float s_z[];        // [warps][rows of a warp at most][Gp]
+__global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid_constant__ typename Tile::Params p, int ranks) {
+    extern __shared__ __align__(16) float s_z[];        // [warps][rows of a warp at most][Gp]; e4m3: the warps' tiles
     __shared__ __align__(16) JoinSmem<D, G> js;
     begin_call();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1316,7 +1609,7 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid
     Piece piece{b, h, piece_row, piece_end, n, {}};
     if (t0 < t1) {
         piece.ids = piece.ask(p, piece_row);
-        float* queries = js.o[2 * warp + 1][0];
+        void* queries = Tile::kRing ? own_memory<Tile>(s_z, warp) : js.o[2 * warp + 1][0];
         auto none = [](Piece&) { return false; };
         // (at most kOneWaveTiles tiles: none of them fills a row of page ids)
         if constexpr (kKeep) tile.stream(p, piece, queries, KeepShared{my_z, piece.row, p.Gp}, HoldNone{}, none, hand_over);
@@ -1623,7 +1916,6 @@ __global__ void __launch_bounds__(kPaThreads, kWeighOcc) k_paged_weigh(const __g
 // of 16K rows of four heads 51 with three, 57 with two, of eight 72 and 80; 128 dimensions and four heads
 // 105 and 87.)  Short sequences in fp32 take two all the same (three of 4099 rows of 2 x 8 heads, 64
 // dimensions, 14.6 us against 15.7).
-constexpr int occ_of(bool f32, int d) { return (f32 ? 2 : 3) + (d == 64 ? 1 : 0); }
 
 // Clusters of `ranks` CTAs that the device holds at once, asked for once per kernel: those of four and
 // more do not fill every GPC (of 152 SMs with three CTAs each 110 of four, 51 of eight, 21 of 16).
@@ -1634,7 +1926,8 @@ constexpr int z_bytes(int tiles, int Gp) { return kPaWarps * tiles * kPaTile * G
 template <class Kernel>
 static bool allow(Kernel kernel, int ranks, int smem) {
     return (ranks <= 8 || cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) &&
-           (!smem || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, z_bytes(kOneWaveTiles, 8)) == cudaSuccess);
+           (!smem || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          smem > z_bytes(kOneWaveTiles, 8) ? smem : z_bytes(kOneWaveTiles, 8)) == cudaSuccess);
 }
 // shared memory of an SM that holds kOcc CTAs of a cluster form's kernel, and the split to ask for
 template <int D, int G, int kOcc>
@@ -1649,7 +1942,7 @@ static int clusters_held(int ranks) {
     int n = known[ranks].load(std::memory_order_relaxed) - 1;
     if (n >= 0) return n;
     auto kernel = k_paged_cluster<Tile, D, kF32, G, kOcc, kKeep>;
-    const int smem = kKeep ? z_bytes(kClusterTiles, 8) : 0;
+    const int smem = kKeep ? z_bytes(kClusterTiles, 8) : Tile::kRing ? own_bytes<Tile>() : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ranks);
     cfg.blockDim = dim3(kPaThreads);
@@ -1704,9 +1997,9 @@ static int cluster_ranks(const PagedAttnParams& p, int ncta) {
 }
 
 template <class Tile, int D, bool kF32, int G, int kOcc, bool kKeep>
-static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
+static int launch_cluster(const typename Tile::Params& p, int ranks, cudaStream_t s) {
     auto kernel = k_paged_cluster<Tile, D, kF32, G, kOcc, kKeep>;
-    const int smem = kKeep ? z_bytes(cluster_tiles(p.span, ranks), p.Gp) : 0;
+    const int smem = kKeep ? z_bytes(cluster_tiles(p.span, ranks), p.Gp) : Tile::kRing ? own_bytes<Tile>() : 0;
     if (!allow(kernel, ranks, smem)) return -1;
     const int carve = carve_of(shared_bytes<D, G, kOcc>(smem));
     return launch_first(kernel, static_cast<unsigned>(p.c.batch) * p.c.H * ranks, kPaThreads, smem, ranks, carve, s, p, ranks) ==
@@ -1716,11 +2009,11 @@ static int launch_cluster(const PagedAttnParams& p, int ranks, cudaStream_t s) {
 }
 
 template <class Tile, int D, bool kF32, int G>
-static int launch_pa(PagedAttnParams p, int ncta, cudaStream_t s) {
+static int launch_pa(typename Tile::Params p, int ncta, cudaStream_t s) {
     int bits = static_cast<int>(kPaSlack);
     while (Tile::kLow && p.span > 1 << (bits - static_cast<int>(kPaSlack))) ++bits;
     p.down = Tile::kLow ? 1.f / static_cast<float>(int64_t(1) << bits) : 1.f;
-    constexpr int kOcc = occ_of(kF32, D), kOccShort = kF32 ? 2 : kOcc;
+    constexpr int kOcc = Tile::kOcc, kOccShort = kF32 ? 2 : kOcc;
     const int held = ncta / kOcc * kOccShort;
     constexpr bool kWeighs = !Tile::kSpan;      // weights go with whole caches
     if constexpr (kWeighs) {
@@ -1740,20 +2033,21 @@ static int launch_pa(PagedAttnParams p, int ncta, cudaStream_t s) {
     auto kernel = k_paged_attn<Tile, D, kF32, G, kOcc, false>;
     if constexpr (kWeighs)
         if (p.weight_out) kernel = k_paged_attn<Tile, D, kF32, G, kOcc, true>;
-    const int smem = kF32 ? kPaWarps * G * (D + 4) * 4 : 0;
-    // (eight heads of 128 dimensions take more than a kernel has without asking)
-    if (kF32 && G * D >= 1024 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    constexpr int smem = kF32 || Tile::kRing ? own_bytes<Tile>() : 0;
+    // (eight heads of 128 dimensions take more than a kernel has without asking, and so do tiles)
+    if ((Tile::kRing || (kF32 && G * D >= 1024)) && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return -1;
-    if (launch_first(kernel, n, kPaThreads, smem, 1, kCarve, s, p) != cudaSuccess) return -1;
+    constexpr int carve = Tile::kRing ? carve_of(shared_bytes<D, G, kOcc>(smem)) : kCarve;
+    if (launch_first(kernel, n, kPaThreads, smem, 1, carve, s, p) != cudaSuccess) return -1;
     // a CTA per head where units are few and so have many shares; one for all heads where they are many
     const int heads = p.c.batch * static_cast<int64_t>(p.c.H) * 4 >= n ? 1 : p.G;
-    if (launch_first(k_paged_merge<D, kF32>, dim3(n, heads), kPaThreads, 0, 1, kCarve, s, p) != cudaSuccess) return -1;
+    if (launch_first(k_paged_merge<D, kF32>, dim3(n, heads), kPaThreads, 0, 1, kCarve, s, static_cast<const PagedAttnParams&>(p)) != cudaSuccess) return -1;
     if (p.weight_out) {
         const int64_t blocks = static_cast<int64_t>(p.c.batch) * p.c.H * ((p.c.cap + kWeighRows - 1) / kWeighRows);
         const int64_t wide = static_cast<int64_t>(kWeighOcc) * (ncta / kOcc);
         const int nw = static_cast<int>(blocks < wide ? blocks : wide);
         auto weigh = p.Gp == 2 ? k_paged_weigh<2> : p.Gp == 4 ? k_paged_weigh<4> : p.Gp == 6 ? k_paged_weigh<6> : k_paged_weigh<8>;
-        if (launch_first(weigh, nw, kPaThreads, 0, 1, kCarve, s, p) != cudaSuccess) return -1;
+        if (launch_first(weigh, nw, kPaThreads, 0, 1, kCarve, s, static_cast<const PagedAttnParams&>(p)) != cudaSuccess) return -1;
     }
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

@@ -56,10 +56,14 @@ struct PagedAttnParams {
     int span;                 // rows that a sequence can show at most
     const float *ks, *vs; int lgb;      // e4m3: scales [n_pages][H][page_size >> lgb]
 };
+struct alignas(64) PagedCodesParams : PagedAttnParams {
+    CUtensorMap mk, mv;       // the pools, d by 16 rows (8 where a page has no more) to a box
+};
 constexpr int kPaWarps = 4;                  // warps of a CTA of the attention
 int paged_attn_ctas(int dtype, int d, int nsm);     // CTAs that fill nsm SMs
 int launch_paged_attn(int dtype, int d, const PagedAttnParams& p, int ncta, cudaStream_t s);
 int launch_paged_span(int dtype, int d, const PagedAttnParams& p, int ncta, cudaStream_t s);
+int launch_paged_codes(int d, const PagedCodesParams& p, int ncta, cudaStream_t s);
 
 struct QuantParams {
     PagedView c;
@@ -155,6 +159,40 @@ inline cudaError_t launch_first(void (*k)(KArgs...), dim3 grid, int block, size_
         ++cfg.numAttrs;
     }
     return cudaLaunchKernelEx(&cfg, k, static_cast<Args&&>(args)...);
+}
+// A wait for a barrier's phase that ends after about a second, or once *dead is set; false then, and *dead is.  One
+// statement: with a way out for some threads of a warp alone the compiler keeps what is the warp's in registers of
+// each thread behind it (a prompt of 32K tokens: 6.5 ms against 6.3).  The threads of a warp are told the same: a
+// phase that one of them saw end does not come again before all of them went on.
+__device__ __forceinline__ bool wait_or_give_up(uint64_t* bar, uint32_t parity, int* dead) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 now, end;\n\t.reg .b32 given_up;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "mov.u64 end, %%globaltimer;\n\tadd.u64 end, end, %4;\n\t"
+        "AGAIN:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+        "ld.volatile.shared::cta.u32 given_up, [%3];\n\tsetp.ne.u32 q, given_up, 0;\n\t@q bra DONE;\n\t"
+        "mov.u64 now, %%globaltimer;\n\tsetp.lt.u64 q, now, end;\n\t@q bra AGAIN;\n\t"
+        "st.volatile.shared::cta.u32 [%3], 1;\n\t"
+        "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(smem_u32(dead)), "n"(kWaitLimitNs)
+        : "memory");
+    return ok != 0;
+}
+// A box of a tensor of three or four dimensions to shared memory, counted on `bar`
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
 }
 // Its first lines: the kernels after it may be brought in once it knows that those before it are done.
 // So a kernel is on the device while those before it write, and reads what they wrote by coherent loads only:
