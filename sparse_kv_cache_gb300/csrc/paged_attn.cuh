@@ -1919,7 +1919,7 @@ __global__ void __launch_bounds__(kPaThreads, kWeighOcc) k_paged_weigh(const __g
 
 // Clusters of `ranks` CTAs that the device holds at once, asked for once per kernel: those of four and
 // more do not fill every GPC (of 152 SMs with three CTAs each 110 of four, 51 of eight, 21 of 16).
-constexpr int kClusterTiles = 8, kUnitTiles = 12, kOneWaveTiles = 16;
+constexpr int kClusterTiles = 8, kUnitTiles = 12, kOneWaveTiles = 16, kCodeTiles = 40;
 // shared memory of a cluster form's kernel: all of a kind are allowed the most, whatever one takes (calls of
 // several host threads would set each other's limit)
 constexpr int z_bytes(int tiles, int Gp) { return kPaWarps * tiles * kPaTile * Gp * 4; }
@@ -1975,6 +1975,9 @@ static int clusters_held(int ranks) {
 // 28.2, and 37.7 against 44.7 of 1000 each.  Units of one length lose where a few are left over: 460 of 750
 // rows 41.6 against 36.5, 912 57.4 against 59.8.  fp32, 600 ragged ones of 250 rows 27.0 against 33.5; 912
 // of exactly 250 54.4 against 44.7.)
+// Codes have half the bytes to a row and the same to do at the end of a unit, and units of their own pay for longer
+// (kCodeTiles: of 1000 rows each, 304 units 20.0 us against 27.4, 912 56.7 against 56.5, ragged 45.4 against 67.7; of
+// 2500 304 38.4 against 47.9, 456 72.3 against 71.6, 912 ragged 82.2 against 98.5; 912 of 300 each 32.3 against 28.2).
 // The products that are kept for the weights take shared memory, and with it an SM's L1 through which the
 // loads go: a unit has a CTA only where that leaves kLeastL1 of it.  (452 units with eight heads of 128
 // dimensions, weighed, in CTAs against the general form: of 600 rows, 181 KB an SM, 29.4 us against 43.3; of
@@ -1988,7 +1991,7 @@ static int cluster_ranks(const PagedAttnParams& p, int ncta) {
            U <= clusters_held<Tile, D, kF32, G, kOcc, kKeep>(2 * ranks))
         ranks *= 2;
     if (ranks == 1) {
-        const int tiles_most = U <= ncta && 4 * U >= 3 * static_cast<int64_t>(ncta) ? kOneWaveTiles : kUnitTiles;
+        const int tiles_most = Tile::kRing ? kCodeTiles : U <= ncta && 4 * U >= 3 * static_cast<int64_t>(ncta) ? kOneWaveTiles : kUnitTiles;
         const int mine = cluster_tiles(p.span, 1);
         if (U > (kF32 ? 2 : 3) * static_cast<int64_t>(ncta) || mine > tiles_most) return 0;
         return !kKeep || shared_bytes<D, G, kOcc>(z_bytes(mine, p.Gp)) <= kSmShared - kLeastL1 ? 1 : 0;
