@@ -38,12 +38,8 @@ static __device__ int g_err[2];
 
 constexpr int kPrTile = 128;                   // rows of a tile of keys
 constexpr int kPrHalf = 128;                   // query rows of an accumulator
-constexpr int kPrThreads = 384;
 constexpr float kPrSlack = 8.f;                // the base moves when a score passes it by 2^8
-constexpr int kPrStages = 2;                   // tiles of keys, and of values, on their way or in use
-// registers of a thread: 384 x 168 at launch; the eight warps with a row per thread take 208, the others 88
-constexpr int kPrRegsMore = 208, kPrRegsLess = 88;
-static_assert(256 * kPrRegsMore + 128 * kPrRegsLess <= kPrThreads * 168, "");
+constexpr int kPrStages = 2;                   // tiles of keys, and of values, on their way or in use, at most
 
 __device__ __forceinline__ float pr_exp2(float x) {
     float y;
@@ -174,7 +170,7 @@ __device__ __forceinline__ PrWhole whole(const PrSees& s) {
 
 // By one warp: which unit a block has; ntok 0 if none.
 __device__ __forceinline__ PrUnit find_unit(const PromptParams& p, int64_t block) {
-    const int t2 = 2 * p.tq;
+    const int t2 = p.halves * p.tq;
     PrUnit u{};
     u.split = static_cast<int>(block % p.nsplit);
     block /= p.nsplit;
@@ -206,11 +202,19 @@ __device__ __forceinline__ PrUnit find_unit(const PromptParams& p, int64_t block
     return u;
 }
 
-template <int D>
-struct PrSmem {
+// A CTA's form: two halves, one CTA to an SM; or where a unit's tokens are few one half, two CTAs to an SM, whose tiles
+// and softmax take turns (8 sequences of 5 tokens over 4099 rows: 40 us with two halves of which one is empty).
+template <int D, int kHalves_>
+struct PrForm {
+    static constexpr int kHalves = kHalves_, kSoft = 4 * kHalves, kThreads = 32 * (kSoft + 4), kCtas = 3 - kHalves;
+    static constexpr int kStages = kHalves == 2 || D == 64 ? 2 : 1;
+    // registers of a thread: what the launch gives, then those of a thread per row, and of the others
+    static constexpr int kRegs = kHalves == 2 ? 168 : 128, kRegsMore = kHalves == 2 ? 208 : 200, kRegsLess = kHalves == 2 ? 88 : 56;
+    static_assert(32 * kSoft * kRegsMore + 128 * kRegsLess <= kThreads * kRegs && kCtas * kThreads * kRegs <= 65536, "");
+    static constexpr int kColumns = 256 * kHalves;                   // of the tensor memory: S, then O
     static constexpr int kParts = D / 64;                            // 64 dimensions of 128 rows: 16 KB
     static constexpr int kTileBytes = kParts * 16384;
-    static constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kPrStages * kTileBytes, kBytes = kV + kPrStages * kTileBytes;
+    static constexpr int kQ = 0, kK = kHalves * kTileBytes, kV = kK + kStages * kTileBytes, kBytes = kV + kStages * kTileBytes;
 };
 struct PrShared {
     uint64_t q_full, k_full[kPrStages], k_empty[kPrStages], v_full[kPrStages], v_ok[kPrStages], v_empty[kPrStages];
@@ -230,10 +234,9 @@ struct PrShared {
 
 // ------------------------------------------------------------------ the roles
 
-template <int D>
+template <int D, class L>
 __device__ void pr_load(const PromptParams& p, const CUtensorMap* mq, const CUtensorMap* mk, const CUtensorMap* mv, PrShared& sh,
                         uint8_t* base) {
-    using L = PrSmem<D>;
     const PrUnit u = sh.unit;
     const PrSees both = sees(p, u, 2);
     const int lane = threadIdx.x & 31;
@@ -251,8 +254,8 @@ __device__ void pr_load(const PromptParams& p, const CUtensorMap* mq, const CUte
     }
     int keys = 0, vals = 0;                        // tiles that are on their way or there
     for (int pos = u.lo; pos < u.hi; ++pos) {
-        const int n = pos - u.lo, s = n % kPrStages, row = u.tile(pos) * kPrTile;
-        const uint32_t parity = (n / kPrStages + 1) & 1;
+        const int n = pos - u.lo, s = n % L::kStages, row = u.tile(pos) * kPrTile;
+        const uint32_t parity = (n / L::kStages + 1) & 1;
         int page = -1;
         if (lane < boxes && both.any(row + lane * box, row + lane * box + box - 1)) page = page_of(p.c, u.b, row + lane * box, g_err, 914);
         const uint32_t gone = __ballot_sync(0xffffffffu, page < 0);
@@ -279,14 +282,13 @@ __device__ void pr_load(const PromptParams& p, const CUtensorMap* mq, const CUte
     if (*const_cast<volatile int*>(&sh.dead)) {
         // given up: no copy may be on its way when the CTA ends
         mbar_wait(&sh.q_full, 0);
-        for (int n = max(0, keys - kPrStages); n < keys; ++n) mbar_wait(&sh.k_full[n % kPrStages], (n / kPrStages) & 1);
-        for (int n = max(0, vals - kPrStages); n < vals; ++n) mbar_wait(&sh.v_full[n % kPrStages], (n / kPrStages) & 1);
+        for (int n = max(0, keys - L::kStages); n < keys; ++n) mbar_wait(&sh.k_full[n % L::kStages], (n / L::kStages) & 1);
+        for (int n = max(0, vals - L::kStages); n < vals; ++n) mbar_wait(&sh.v_full[n % L::kStages], (n / L::kStages) & 1);
     }
 }
 
-template <int D>
+template <int D, class L>
 __device__ bool pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) {
-    using L = PrSmem<D>;
     const PrUnit u = sh.unit;
     const PrWhole calm = sh.whole[2];
     const uint32_t at = smem_u32(base), tmem = sh.tmem;
@@ -298,7 +300,7 @@ __device__ bool pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) 
     const bool mine = elect_one();
     const uint64_t q_desc = smem_desc_sw128(at + L::kQ), k_desc = smem_desc_sw128(at + L::kK), v_desc = smem_desc_mn(at + L::kV, 16384);
     auto scores = [&](int x, int n) {
-        const uint64_t q = q_desc + x * (L::kTileBytes >> 4), k = k_desc + (n % kPrStages) * (L::kTileBytes >> 4);
+        const uint64_t q = q_desc + x * (L::kTileBytes >> 4), k = k_desc + (n % L::kStages) * (L::kTileBytes >> 4);
         if (!mine) return;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -308,11 +310,11 @@ __device__ bool pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) 
         tc_commit(&sh.s_full[x]);
     };
     auto values = [&](int x, int n) {
-        const uint64_t v = v_desc + (n % kPrStages) * (L::kTileBytes >> 4);
+        const uint64_t v = v_desc + (n % L::kStages) * (L::kTileBytes >> 4);
         if (!mine) return;
 #pragma unroll
         for (int i = 0; i < kPrTile / 16; ++i)
-            tc_mma_bf16_ts(tmem + 256 + x * 128, tmem + x * 128 + i * 8, v + i * (2048 >> 4), pv, n > 0 || i > 0);
+            tc_mma_bf16_ts(tmem + 128 * L::kHalves + x * 128, tmem + x * 128 + i * 8, v + i * (2048 >> 4), pv, n > 0 || i > 0);
     };
     auto told = [&](uint64_t* bar, uint32_t parity) { return wait_or_give_up(bar, parity, &sh.dead); };
     auto commit = [&](uint64_t* bar) {
@@ -322,8 +324,8 @@ __device__ bool pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) 
     for (int x = 0; x < halves; ++x) scores(x, 0);
     commit(&sh.k_empty[0]);
     for (int n = 0; n < tiles; ++n) {
-        const int s = n % kPrStages, next = (n + 1) % kPrStages;
-        if (!told(&sh.v_ok[s], (n / kPrStages) & 1)) return false;
+        const int s = n % L::kStages, next = (n + 1) % L::kStages;
+        if (!told(&sh.v_ok[s], (n / L::kStages) & 1)) return false;
         const bool wild = !calm.has(u.tile(u.lo + n)) && sh.is_wild(s);
         for (int x = 0; x < halves; ++x) {
             if (!told(&sh.p_full[x], n & 1)) return false;
@@ -331,7 +333,7 @@ __device__ bool pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) 
             if (!wild) values(x, n);       // otherwise the row's threads have done it
             if (x == halves - 1) commit(&sh.v_empty[s]);
             if (n + 1 < tiles) {
-                if (x == 0 && !told(&sh.k_full[next], ((n + 1) / kPrStages) & 1)) return false;
+                if (x == 0 && !told(&sh.k_full[next], ((n + 1) / L::kStages) & 1)) return false;
                 scores(x, n + 1);
                 if (x == halves - 1) commit(&sh.k_empty[next]);
             } else {
@@ -342,16 +344,15 @@ __device__ bool pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) 
     return true;
 }
 
-template <int D>
+template <int D, class L>
 __device__ void pr_look(const PromptParams& p, PrShared& sh, uint8_t* base) {
-    using L = PrSmem<D>;
     const PrUnit u = sh.unit;
     const PrSees both = sees(p, u, 2);
     const PrWhole calm = sh.whole[2];
-    const int t = threadIdx.x - 320, warp = t >> 5;   // of 64
+    const int t = threadIdx.x - 32 * (L::kSoft + 2), warp = t >> 5;   // of 64
     for (int n = 0; n < u.hi - u.lo; ++n) {
-        const int s = n % kPrStages, tile = u.tile(u.lo + n);
-        if (!wait_or_give_up(&sh.v_full[s], (n / kPrStages) & 1, &sh.dead)) return;
+        const int s = n % L::kStages, tile = u.tile(u.lo + n);
+        if (!wait_or_give_up(&sh.v_full[s], (n / L::kStages) & 1, &sh.dead)) return;
         if (!calm.has(tile)) {
             uint32_t some = 0;
             uint8_t* v = base + L::kV + s * L::kTileBytes;
@@ -431,9 +432,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-template <int D>
+template <int D, class L>
 __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
-    using L = PrSmem<D>;
     const PrUnit& u = sh.unit;
     const int half = threadIdx.x >> 7, r = threadIdx.x & 127;
     const int lo = u.lo, tiles = u.hi - lo;
@@ -441,7 +441,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     if (half * p.tq >= u.ntok) return;
     const int row = u.row0 + min(token, u.ntok - 1);
     const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;      // 32 lanes of the tensor memory
-    const uint32_t s_at = sh.tmem + lanes + half * 128, o_at = s_at + 256;
+    const uint32_t s_at = sh.tmem + lanes + half * 128, o_at = s_at + 128 * L::kHalves;
     const float scale = p.scale_log2;
     const bool falls = scale < 0.f;
     const float none = falls ? CUDART_INF_F : -CUDART_INF_F;             // the product that scores -infinity
@@ -520,8 +520,8 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
         l = sum[0].x + sum[0].y;
         tmem_put_wait();
         if (!sh.whole[2].has(tile)) {
-            const int s = n % kPrStages;
-            good = wait_or_give_up(&sh.v_ok[s], (n / kPrStages) & 1, &sh.dead);
+            const int s = n % L::kStages;
+            good = wait_or_give_up(&sh.v_ok[s], (n / L::kStages) & 1, &sh.dead);
             if (!good) break;
             if (sh.is_wild(s)) pr_by_hand<D>(o_at, s_at, base + L::kV + s * L::kTileBytes, n == 0);
         }
@@ -538,7 +538,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     const int64_t head = static_cast<int64_t>(u.h) * p.G + g, tok = u.tok + token;
     const float base2 = m == -CUDART_INF_F ? m : m + p.down_bits;
     if (p.nsplit > 1) {
-        const int64_t rec = static_cast<int64_t>(blockIdx.x) * 2 * kPrHalf + threadIdx.x;
+        const int64_t rec = static_cast<int64_t>(blockIdx.x) * L::kHalves * kPrHalf + threadIdx.x;
         if (live) p.part_stat[rec] = good ? make_float2(base2, l) : make_float2(0.f, CUDART_NAN_F);
         if (!good || tiles <= 0) return;
 #pragma unroll 1
@@ -577,16 +577,17 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     if (live && p.lse) p.lse[tok * p.n_q + head] = !good ? CUDART_NAN_F : l == 0.f ? -CUDART_INF_F : (base2 + log2f(l)) * 0.693147180559945309f;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kPrThreads, 1) k_prompt_attn(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap mq,
-                                                               const __grid_constant__ CUtensorMap mk,
-                                                               const __grid_constant__ CUtensorMap mv) {
+template <int D, int kHalves>
+__global__ void __launch_bounds__(PrForm<D, kHalves>::kThreads, PrForm<D, kHalves>::kCtas)
+    k_prompt_attn(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                  const __grid_constant__ CUtensorMap mv) {
+    using L = PrForm<D, kHalves>;
     extern __shared__ uint8_t s_raw[];
     __shared__ PrShared sh;
     uint8_t* base = s_raw + ((1024 - (smem_u32(s_raw) & 1023)) & 1023);
     begin_call();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (warp == 8) {
+    if (warp == L::kSoft) {
         const PrUnit u = find_unit(p, blockIdx.x);
         if (lane == 0) {
             sh.unit = u;
@@ -614,33 +615,33 @@ __global__ void __launch_bounds__(kPrThreads, 1) k_prompt_attn(const __grid_cons
     }
     __syncthreads();
     if (sh.unit.ntok == 0) return;
-    if (warp == 9) {
-        tmem_alloc(&sh.tmem, 512);
+    if (warp == L::kSoft + 1) {
+        tmem_alloc(&sh.tmem, L::kColumns);
         tmem_relinquish();
         tc_fence_before();
     }
     __syncthreads();
     tc_fence_after();
-    if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrRegsMore));
-        pr_softmax<D>(p, sh, base);
+    if (warp < L::kSoft) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kRegsMore));
+        pr_softmax<D, L>(p, sh, base);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrRegsLess));
-        if (warp == 8) pr_load<D>(p, &mq, &mk, &mv, sh, base);
-        else if (warp == 9) {
-            if (!pr_multiply<D>(p, sh, base)) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegsLess));
+        if (warp == L::kSoft) pr_load<D, L>(p, &mq, &mk, &mv, sh, base);
+        else if (warp == L::kSoft + 1) {
+            if (!pr_multiply<D, L>(p, sh, base)) {
                 if (elect_one()) tc_commit(&sh.given_up);
                 mbar_wait(&sh.given_up, 0);
             }
-        } else pr_look<D>(p, sh, base);
+        } else pr_look<D, L>(p, sh, base);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && sh.dead) set_err(g_err, DEV_ERR_TIMEOUT, 911);
-    if (warp == 9) {
+    if (warp == L::kSoft + 1) {
         tc_fence_after();
-        tmem_dealloc(sh.tmem, 512);
+        tmem_dealloc(sh.tmem, L::kColumns);
     }
 }
 
@@ -660,15 +661,15 @@ __global__ void __launch_bounds__(256) k_prompt_merge(const __grid_constant__ Pr
     for (int k = threadIdx.x + blockIdx.y * 256; k < rows * (D / 4); k += 256 * gridDim.y) {
         const int i = k / (D / 4), dim = 4 * (k % (D / 4)), token = i / p.G, g = i % p.G;
         const int half = token / p.tq, r = (token - half * p.tq) * p.G + g;
-        const int64_t rec = static_cast<int64_t>(blockIdx.x) * p.nsplit * 2 * kPrHalf + half * kPrHalf + r;
+        const int64_t step = p.halves * kPrHalf, rec = static_cast<int64_t>(blockIdx.x) * p.nsplit * step + half * kPrHalf + r;
         float m = -CUDART_INF_F, l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < p.nsplit; ++s) m = fmaxf(m, __ldcg(p.part_stat + rec + s * 2 * kPrHalf).x);
+        for (int s = 0; s < p.nsplit; ++s) m = fmaxf(m, __ldcg(p.part_stat + rec + s * step).x);
         for (int s = 0; s < p.nsplit; ++s) {
-            const float2 st = __ldcg(p.part_stat + rec + s * 2 * kPrHalf);
+            const float2 st = __ldcg(p.part_stat + rec + s * step);
             if (st.y == 0.f) continue;             // this part sees nothing
             const float w = st.x == -CUDART_INF_F ? CUDART_NAN_F : pr_exp2(st.x - m);
             const float4 o = st.y != st.y ? make_float4(st.y, st.y, st.y, st.y)
-                                          : __ldcg(reinterpret_cast<const float4*>(p.part + (rec + s * 2 * kPrHalf) * D + dim));
+                                          : __ldcg(reinterpret_cast<const float4*>(p.part + (rec + s * step) * D + dim));
             l = fmaf(st.y, w, l);
             x[0] = fmaf(o.x, w, x[0]);
             x[1] = fmaf(o.y, w, x[1]);
@@ -685,27 +686,31 @@ __global__ void __launch_bounds__(256) k_prompt_merge(const __grid_constant__ Pr
 
 // ------------------------------------------------------------------ launches
 
-int64_t prompt_slots(int tokens, int batch, int G) { return tokens / (2 * (kPrHalf / G)) + static_cast<int64_t>(batch); }
-
-// Parts of a unit's tiles: as many as fill the SMs once, of two tiles at least.
-int prompt_splits(int64_t units, int64_t tiles, int nsm) {
-    const int64_t most = std::min<int64_t>((tiles + 1) / 2, nsm / std::max<int64_t>(units, 1));
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, 32)));
+PromptPlan prompt_plan(int tokens, int batch, int G, int H, int64_t tiles, int nsm) {
+    // one half where the sequences have no more tokens than that takes, on average (they are on the device)
+    const int tq = kPrHalf / G, halves = tokens <= static_cast<int64_t>(batch) * tq ? 1 : 2;
+    PromptPlan plan{halves, 1, tokens / (halves * tq) + static_cast<int64_t>(batch)};
+    // parts of a unit's tiles: as many as fill the SMs once, of two tiles at least
+    const int64_t units = plan.slots * H, most = std::min<int64_t>((tiles + 1) / 2, (3 - halves) * nsm / std::max<int64_t>(units, 1));
+    plan.nsplit = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, 32)));
+    return plan;
 }
 
-template <int D>
+template <int D, int kHalves>
 static int launch_prompt(const PromptParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
-    constexpr int smem = PrSmem<D>::kBytes + 1024;
-    if (cudaFuncSetAttribute(k_prompt_attn<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
+    using L = PrForm<D, kHalves>;
+    constexpr int smem = L::kBytes + 1024;
+    auto kernel = k_prompt_attn<D, kHalves>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
     const int64_t units = p.slots * p.c.H;
     if (units * p.nsplit > INT32_MAX) return -1;
-    if (launch_first(k_prompt_attn<D>, static_cast<unsigned>(units * p.nsplit), kPrThreads, smem, 1, 0, s, p, mq, mk, mv) != cudaSuccess)
-        return -1;
-    if (p.nsplit > 1 && launch_first(k_prompt_merge<D>, dim3(static_cast<unsigned>(units), 4), 256, 0, 1, 0, s, p) != cudaSuccess) return -1;
+    if (launch_first(kernel, static_cast<unsigned>(units * p.nsplit), L::kThreads, smem, 1, 100, s, p, mq, mk, mv) != cudaSuccess) return -1;
+    if (p.nsplit > 1 && launch_first(k_prompt_merge<D>, dim3(static_cast<unsigned>(units), 4), 256, 0, 1, 100, s, p) != cudaSuccess) return -1;
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 int launch_prompt_attn(int d, const PromptParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
-    return d == 64 ? launch_prompt<64>(p, mq, mk, mv, s) : launch_prompt<128>(p, mq, mk, mv, s);
+    if (p.halves == 1) return d == 64 ? launch_prompt<64, 1>(p, mq, mk, mv, s) : launch_prompt<128, 1>(p, mq, mk, mv, s);
+    return d == 64 ? launch_prompt<64, 2>(p, mq, mk, mv, s) : launch_prompt<128, 2>(p, mq, mk, mv, s);
 }
 
 cudaError_t prompt_err(int** e) { return cudaGetSymbolAddress(reinterpret_cast<void**>(e), g_err); }

@@ -253,7 +253,7 @@ int evict_space(const skv_paged_evict_args* a, EvictSpace* w) {
 
 // ------------------------------------------------------------------ attention of prompts
 
-struct PromptSpace { int64_t slots, tiles, stat, bytes; };
+struct PromptSpace { int64_t tiles, stat, bytes; };
 
 int prompt_space(const skv_paged_prompt_args* a, PromptSpace* w) {
     const skv_paged_cache& c = a->cache;
@@ -264,13 +264,11 @@ int prompt_space(const skv_paged_prompt_args* a, PromptSpace* w) {
     if (c.max_pages < 1 || c.page_size < 1 || static_cast<int64_t>(c.max_pages) * c.page_size > kMaxRows) return SKV_ERR_INVALID;
     if (static_cast<int64_t>(c.batch) * c.n_kv_heads > kMaxUnits) return SKV_ERR_INVALID;
     if (c.dtype != SKV_BF16) return SKV_ERR_UNSUPPORTED;
-    w->slots = prompt_slots(a->tokens, c.batch, G);
     // tiles of 128 rows that a unit of 256 / G tokens can see
     const int64_t all = (static_cast<int64_t>(c.max_pages) * c.page_size + 127) / 128;
     w->tiles = a->window ? std::min<int64_t>(all, (static_cast<int64_t>(a->sink) + 127) / 128 + (static_cast<int64_t>(a->window) + 256) / 128 + 2) : all;
-    const int64_t units = w->slots * c.n_kv_heads;
-    const int n = prompt_splits(units, w->tiles, kMaxSms);
-    const int64_t rows = n > 1 ? units * n * 256 : 0;
+    const PromptPlan plan = prompt_plan(a->tokens, c.batch, G, c.n_kv_heads, w->tiles, kMaxSms);
+    const int64_t rows = plan.nsplit > 1 ? plan.slots * c.n_kv_heads * plan.nsplit * plan.halves * 128 : 0;
     w->stat = rows * c.head_dim * 4;
     w->bytes = w->stat + rows * 8;
     return SKV_OK;
@@ -565,8 +563,8 @@ int shadowkv_paged_prompt_attention(const skv_paged_prompt_args* a, skv_stream s
     p.c.window = static_cast<int>(std::min<int64_t>(a->window, kMaxRows));
     p.c.sink = static_cast<int>(std::min<int64_t>(a->sink, kMaxRows));
     p.G = G; p.n_q = a->n_q_heads; p.tokens = a->tokens; p.tq = tq;
-    p.slots = w.slots;
-    p.nsplit = prompt_splits(w.slots * c.n_kv_heads, w.tiles, dev.nsm < kMaxSms ? dev.nsm : kMaxSms);
+    const PromptPlan plan = prompt_plan(a->tokens, c.batch, G, c.n_kv_heads, w.tiles, dev.nsm < kMaxSms ? dev.nsm : kMaxSms);
+    p.halves = plan.halves; p.nsplit = plan.nsplit; p.slots = plan.slots;
     p.scale_log2 = static_cast<float>((a->scale != 0.f ? static_cast<double>(a->scale) : 1.0 / std::sqrt(double(c.head_dim))) *
                                       1.4426950408889634074);
     p.down_bits = static_cast<float>(8 + log2_of(p.c.cap));

@@ -90,18 +90,19 @@ int launch_dequantise(int dtype, int d, const DequantParams& p, cudaStream_t s);
 struct PromptParams {
     PagedView c;              // window 0: none
     int G, n_q, tokens;
-    int tq;                   // tokens of half a unit: 128 / G
+    int tq;                   // tokens of 128 query rows: 128 / G
+    int halves;               // of a unit, of 128 query rows each
     int nsplit;               // parts of a unit's tiles
-    int64_t slots;            // places for units of 2 tq tokens of a sequence: prompt_slots()
+    int64_t slots;            // places for units of halves * tq tokens of a sequence
     float scale_log2, down_bits;
     int64_t o_tok, o_head;
     const int32_t* start;
     void* out; float* lse;
-    float* part;              // [slots * H * nsplit][256][d]: parts of sums, unnormalised
+    float* part;              // [slots * H * nsplit][halves * 128][d]: parts of sums, unnormalised
     float2* part_stat;        // their bases and sums of probabilities
 };
-int64_t prompt_slots(int tokens, int batch, int G);
-int prompt_splits(int64_t units, int64_t tiles, int nsm);
+struct PromptPlan { int halves, nsplit; int64_t slots; };
+PromptPlan prompt_plan(int tokens, int batch, int G, int H, int64_t tiles, int nsm);      // tiles that a unit can see
 int launch_prompt_attn(int d, const PromptParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s);
 
 struct EvictParams {
