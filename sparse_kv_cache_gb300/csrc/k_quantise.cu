@@ -80,8 +80,9 @@ __device__ __forceinline__ float block_scale(float m) {
 // one warp or several (block / 16).  Which blocks those are only the device knows: sequence b has
 // (start[b] >> lgb) + 2b slots before its own, which leaves every sequence room for the blocks that its
 // tokens can touch, and a slot without a block ends at once.  (32K tokens, blocks of 64: two slots of 514.)
+// A prompt of 32K tokens in bf16 36 us, 5.6 TB/s (three CTAs to an SM 40), in fp32 4.4 TB/s.
 template <typename T, int D>
-__global__ void __launch_bounds__(32 * kQzWarps, sizeof(T) == 4 ? 2 : 3) k_quantise(const __grid_constant__ QuantParams p) {
+__global__ void __launch_bounds__(32 * kQzWarps, sizeof(T) == 4 ? 3 : 4) k_quantise(const __grid_constant__ QuantParams p) {
     constexpr int kLanes = D / 8, kPer = 32 / kLanes, kSteps = kQzRows / kPer;
     __shared__ float s_most[kQzWarps];
     begin_call();
@@ -192,11 +193,13 @@ __global__ void __launch_bounds__(32 * kQzWarps, sizeof(T) == 4 ? 2 : 3) k_quant
 constexpr int kDqWarps = 8;
 constexpr int kDqTokens = 32;
 
-// A CTA takes 32 tokens, a warp of it all their rows of one head, of keys or of values, eight or four loads of 16
-// bytes per lane in flight together.
+// A CTA takes 32 tokens, a warp of it all their rows of one head, of keys or of values: 4 KB, all asked for before
+// any is converted.  Four 32K contexts in bf16 131 us, 6.2 TB/s (with 16 codes to a lane, whose result is two stores of
+// every other 16 bytes, 147; with several heads to a warp, the next one's loads during this one's stores, 180).
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kDqWarps) k_dequantise(const __grid_constant__ DequantParams p) {
-    constexpr int kLanes = D / 16, kPer = 32 / kLanes, kSteps = kDqTokens / kPer;
+    constexpr int kEach = 16 / sizeof(T);       // codes of a lane: 16 bytes of the result, side by side
+    constexpr int kLanes = D / kEach, kPer = 32 / kLanes, kSteps = kDqTokens / kPer;
     __shared__ int s_page[kDqTokens], s_at[kDqTokens];
     begin_call();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t0 = blockIdx.x * kDqTokens;
@@ -228,37 +231,43 @@ __global__ void __launch_bounds__(32 * kDqWarps) k_dequantise(const __grid_const
     if (what >= 2 * p.c.H) return;
     const int h = what >> 1;
     const bool values = what & 1;
-    const int sub = lane / kLanes, dim = 16 * (lane % kLanes);
+    const int sub = lane / kLanes, dim = kEach * (lane % kLanes);
     const uint8_t* pool = static_cast<const uint8_t*>(values ? p.c.v : p.c.k) + h * (values ? p.c.v_head : p.c.k_head) + dim;
     const int64_t pg = values ? p.c.v_page : p.c.k_page, pitch = values ? p.c.v_row : p.c.k_row;
     const float* scale = (values ? p.v_scale : p.k_scale) + static_cast<int64_t>(h) * (1 << (p.c.lg - p.lgb));
     T* out = static_cast<T*>(values ? p.v : p.k) + h * (values ? p.v_head : p.k_head) + dim;
     const int64_t o_tok = values ? p.v_tok : p.k_tok;
-    uint4 w[kSteps];
+    uint32_t w[kSteps][kEach / 4];
     float f[kSteps];
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
         const int i = s * kPer + sub;
         const int64_t page = s_page[i];
         if (page < 0) continue;
-        w[s] = *reinterpret_cast<const uint4*>(pool + page * pg + s_at[i] * pitch);
+        const uint8_t* src = pool + page * pg + s_at[i] * pitch;
+        if constexpr (kEach == 8) {
+            const uint2 x = *reinterpret_cast<const uint2*>(src);
+            w[s][0] = x.x;
+            w[s][1] = x.y;
+        } else {
+            w[s][0] = *reinterpret_cast<const uint32_t*>(src);
+        }
         f[s] = __ldcg(scale + page * p.c.H * (1 << (p.c.lg - p.lgb)) + (s_at[i] >> p.lgb));
     }
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
         const int i = s * kPer + sub;
         if (s_page[i] < 0) continue;
-        float v[2][8];
+        float v[kEach];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t four = e < 2 ? w[s].x : e < 4 ? w[s].y : e < 6 ? w[s].z : w[s].w;
-            const float2 x = from_e4m3x2(e & 1 ? four >> 16 : four & 0xFFFF);
-            v[e >> 2][2 * (e & 3)] = x.x * f[s];
-            v[e >> 2][2 * (e & 3) + 1] = x.y * f[s];
+        for (int e = 0; e < kEach; e += 2) {
+            const float2 x = from_e4m3x2(e & 2 ? w[s][e / 4] >> 16 : w[s][e / 4] & 0xFFFF);
+            v[e] = x.x * f[s];
+            v[e + 1] = x.y * f[s];
         }
         T* dst = out + (t0 + i) * o_tok;
-        store8(dst, v[0]);
-        store8(dst + 8, v[1]);
+        if constexpr (kEach == 8) store8(dst, v);
+        else *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
     }
 }
 
