@@ -613,16 +613,18 @@ int shadowkv_paged_evict(const skv_paged_evict_args* args, skv_stream stream);
  *
  * With window > 0 the token sees its sequence's last `window` rows and its first `sink` ones: row j < lens[b] with
  * j >= lens[b] - window or j < sink, by the place in the cache (a cache that has lost rows in an eviction has no
- * such order).  window 0: all rows, whatever sink is.  Groups of eight rows of which none is seen are not looked
- * at, neither the rows nor their page ids: a server may give the pages between back.
+ * such order).  window 0: all rows, whatever sink is.  Pages without a row that is seen are not looked
+ * at, nor are their ids: a server may give the pages between back.  What is in a row that is not seen has no part
+ * in the result, whatever it is.
  *
  * A cache of dtype SKV_E4M3 holds codes of four significant bits, keys and values alike, and their scales beside
  * the pools: a value is code * scale[page][head][row % page_size / block].  q and out are bf16.  The
- * scales are powers of two as shadowkv_paged_quantise writes them; any positive ones do here.  A code of NaN
- * in a row that is seen gives NaN.  Scores are formed from fp16 queries, a power of two per head apart (what is below
+ * scales are powers of two as shadowkv_paged_quantise writes them; any positive ones do here.  Strides of the pools are
+ * above zero where there is more than one to step through, and below 2^40 bytes; rows are read by tiles of 16, also
+ * those of a tile that are not seen or lie behind the last one.  A code of NaN in a row that is seen gives NaN.  Scores are formed from fp16 queries, a power of two per head apart (what is below
  * 2^-39 of a head's largest element is lost), probabilities take their value's scale and are rounded to fp16:
  * a row whose probability times scale is 2^-32 below the unit's heaviest may weigh nothing.  Everything else is
- * as above.
+ * as above.  Where a kernel's bounded wait ran out (shadowkv_paged_status: SKV_ERR_TIMEOUT) results are NaN.
  *
  * attn.weight and attn.weight_out go with whole caches of the other types (window 0), where this call is
  * shadowkv_paged_attention; anywhere else they are refused.
@@ -648,11 +650,13 @@ int shadowkv_paged_attention_ext(const skv_paged_attention_ext_args* args, skv_s
  * page's first) and head, of keys and of values:
  *   scale = 2^e, the smallest e >= -100 with |x| <= 448 * 2^e for the finite x among the block's new rows
  * and, where the block holds rows of the sequence already, the larger of that and the scale it has;
- * held codes are then rounded to the new one (between powers of two only what falls below 2^-9 of it is lost).
+ * held codes are then rounded to the new one (between powers of two, as this call leaves them, only what falls below
+ * 2^-9 of it is lost).
  *   code = x / scale, to the nearest, ties to even; NaN for a NaN and for an infinity
  * start does not fall, start[0] >= 0, start[batch] <= tokens; a sequence for which it does, or whose rows
  * would pass its table, sets the error word, and what is out of range is not written.  A bad page sets it too and
- * its rows are left out.  A sequence that is written to does not share its last page.
+ * its rows are left out.  A sequence that is written to does not share its last page, and no block of the
+ * call's is another's: no page is in two tables' places that are written.
  */
 typedef struct {
     skv_paged_cache cache;      /* dtype SKV_E4M3; lens: rows held before the call */
@@ -670,7 +674,7 @@ int shadowkv_paged_quantise(const skv_paged_quantise_args* args, skv_stream stre
  * Reads rows of a cache of dtype SKV_E4M3 back: tokens start[b] .. start[b+1] of k and v (bf16 or fp32) become
  * rows first[b] on of sequence b, code * scale in fp32, rounded once.  Rows from lens[b] on and tokens of no
  * sequence are left as they are, and so are the rows of a bad page, which sets the error word, and the
- * tokens of a sequence whose start or first is out of range, which does too.
+ * tokens of a sequence whose start or first is out of range, which does too.  k and v do not overlap.
  */
 typedef struct {
     skv_paged_cache cache;      /* dtype SKV_E4M3 */
@@ -690,7 +694,7 @@ int shadowkv_paged_dequantise(const skv_paged_dequantise_args* args, skv_stream 
  * start[b+1] of q are the last rows of sequence b, whose keys and values are in the cache already and counted in
  * lens[b]; token start[b+1] - 1 is row lens[b] - 1.  Token of row r sees row j <= r where window is 0, and
  * otherwise where j > r - window or j < sink besides.  out and lse as for one token; a token that sees nothing (there
- * are more tokens than rows, or its pages are bad) has out = 0 and lse = -inf.
+ * are more tokens than rows, or its pages are bad) has out = 0 and lse = -inf.  out overlaps nothing else.
  *
  * dtype SKV_BF16 (others: SKV_ERR_UNSUPPORTED; a cache of codes is read back by shadowkv_paged_dequantise into rows
  * that make pages).  Strides of q and of the pools are above zero where there is more than one

@@ -8,13 +8,14 @@
 // A CTA takes 256 query rows of one KV head -- 2 x tq tokens times its G query heads, two halves of 128 rows with an
 // accumulator each -- and walks the tiles of 128 rows that any of them sees.  Both halves use each tile of keys
 // and values: with one half the L2 would have to deliver 64 bytes per clock to every SM, more than it has.
-//   warp 8       page ids, TMA of queries, keys and values (pages are boxes of a tensor map)
-//   warp 9       S = Q.K^T (both operands in shared memory), O += P.V (P in tensor memory, V as it lies in the
+//   8 warps      a thread per query row: scores from tensor memory into registers, softmax, P back
+//   one          page ids, TMA of queries, keys and values (pages are boxes of a tensor map)
+//   one          S = Q.K^T (both operands in shared memory), O += P.V (P in tensor memory, V as it lies in the
 //                pages: its dimension is the one along the rows of a page, so the operand is MN-major)
-//   warps 0-7    a thread per query row: scores from tensor memory into registers, softmax, P back
-//   warps 10, 11 values of tiles at an edge: rows that no query sees become zeros, and whether an element that is
+//   two          values of tiles at an edge: rows that no query sees become zeros, and whether an element that is
 //                not finite is among the others, which must not meet a probability of zero
-// While one half's warps form its probabilities, the tensor cores have the other half's two products.
+// While one half's warps form its probabilities, the tensor cores have the other half's two products.  Few tokens take
+// one half and two CTAs to an SM; few units a part of their tiles each, joined by k_prompt_merge.
 //
 // The tensor memory holds S of both halves and O of both, 512 columns; P takes the place of its S.  A half's
 // products are issued in the order P(j).V, Q.K(j+1): they execute in that order, so what says that the second
@@ -24,6 +25,16 @@
 // (two terms would double the second product).  They are 2^-8 over the table's rows of a probability that is not
 // normalised, in the exponent, so that no sum of values passes the type's largest; O and the sums of
 // probabilities, in fp32, take the same factor, and it cancels.
+//
+// Measured (8 KV heads of 4 query heads, d = 128; cuBLAS reaches 1900 TFLOP/s in bursts, 1695 for seconds under the power
+// limit): a prompt of 32K tokens 6.26 ms, 1400 TFLOP/s; through a window of 4096 1.73 ms, 1190; 4 prompts of 4096 483
+// us, 1140; chunks of 13K tokens in all through a window of 1024 316 us, of 10.5 tiles a unit with three at an edge;
+// d = 64, 16K tokens 1.39 ms, 790, where the softmax takes as long as both products; 8 drafts of 5 tokens over up to
+// 4099 rows 31.6 us.  A half's tile takes its softmax about 1650 clocks (128 columns in 4 of them each at the
+// exponential unit, 32 a clock to an SM) and its products 1024, which the other half's overlap.
+// Tried: two threads to a row (7.1 ms for 32K: 20 warps to issue for), the first half of P handed over early (no
+// difference), six warps to look at values (505 us for the 4 prompts: they wait at the others' cost), CTAs that go through
+// many units (517 us: what a unit's start and end take is hidden, but the units fall unevenly).
 #include <math_constants.h>
 
 #include <algorithm>
@@ -703,7 +714,6 @@ static int launch_prompt(const PromptParams& p, const CUtensorMap& mq, const CUt
     auto kernel = k_prompt_attn<D, kHalves>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
     const int64_t units = p.slots * p.c.H;
-    if (units * p.nsplit > INT32_MAX) return -1;
     if (launch_first(kernel, static_cast<unsigned>(units * p.nsplit), L::kThreads, smem, 1, 100, s, p, mq, mk, mv) != cudaSuccess) return -1;
     if (p.nsplit > 1 && launch_first(k_prompt_merge<D>, dim3(static_cast<unsigned>(units), 4), 256, 0, 1, 100, s, p) != cudaSuccess) return -1;
     return cudaGetLastError() == cudaSuccess ? 0 : -1;

@@ -278,7 +278,6 @@ int64_t quantise_slots(int tokens, int batch, int lgb) { return (tokens >> lgb) 
 int launch_quantise(int dtype, int d, const QuantParams& p, cudaStream_t s) {
     const int W = p.lgb > 4 ? 1 << (p.lgb - 4) : 1;
     const int64_t units = p.slots * 2 * p.c.H, per = kQzWarps / W, grid = (units + per - 1) / per;
-    if (grid > INT32_MAX) return -1;
     auto kernel = dtype == SKV_F32 ? (d == 64 ? k_quantise<float, 64> : k_quantise<float, 128>)
                                    : (d == 64 ? k_quantise<__nv_bfloat16, 64> : k_quantise<__nv_bfloat16, 128>);
     return launch_first(kernel, static_cast<unsigned>(grid), 32 * kQzWarps, 0, 1, 0, s, p) == cudaSuccess ? 0 : -1;

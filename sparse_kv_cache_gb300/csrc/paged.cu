@@ -492,6 +492,7 @@ int shadowkv_paged_quantise(const skv_paged_quantise_args* a, skv_stream stream)
     p.lgb = log2_of(a->scales.block);
     p.tokens = a->tokens;
     p.slots = quantise_slots(a->tokens, c.batch, p.lgb);
+    if (p.slots * 2 * c.n_kv_heads > INT32_MAX) return SKV_ERR_INVALID;
     p.k_tok = a->k_tok; p.k_head = a->k_head; p.v_tok = a->v_tok; p.v_head = a->v_head;
     p.k = a->k; p.v = a->v; p.k_scale = a->scales.k; p.v_scale = a->scales.v; p.start = a->start;
     return done(launch_quantise(a->dtype, c.head_dim, p, stream));
@@ -564,6 +565,7 @@ int shadowkv_paged_prompt_attention(const skv_paged_prompt_args* a, skv_stream s
     p.c.sink = static_cast<int>(std::min<int64_t>(a->sink, kMaxRows));
     p.G = G; p.n_q = a->n_q_heads; p.tokens = a->tokens; p.tq = tq;
     const PromptPlan plan = prompt_plan(a->tokens, c.batch, G, c.n_kv_heads, w.tiles, dev.nsm < kMaxSms ? dev.nsm : kMaxSms);
+    if (plan.slots * c.n_kv_heads * plan.nsplit > INT32_MAX) return SKV_ERR_INVALID;
     p.halves = plan.halves; p.nsplit = plan.nsplit; p.slots = plan.slots;
     p.scale_log2 = static_cast<float>((a->scale != 0.f ? static_cast<double>(a->scale) : 1.0 / std::sqrt(double(c.head_dim))) *
                                       1.4426950408889634074);

@@ -556,3 +556,74 @@ def test_two_streams_and_host_threads_over_codes():
     assert not failed
     for i in range(2):
         assert len(got[i]) == 40 and all(torch.equal(o, want[i][0]) and torch.equal(s, want[i][1]) for o, s in got[i])
+
+
+@pytest.mark.parametrize("d,ps,block,layout,lens,window,sink", [
+    (128, 16, 8, "hnd", [1000, 33, 24, 7], 17, 20), (64, 8, 8, "nhd", [300, 31, 32, 33], 9, 1),
+    (128, 8, 8, "hnd", [900, 50], 40, 3), (64, 64, 16, "hnd", [2000, 65], 300, 5), (128, 1024, 128, "nhd", [3000], 1000, 130)])
+def test_codes_that_are_not_seen_may_be_anything(d, ps, block, layout, lens, window, sink):
+    """NaN codes in every row that is not seen, NaN scales in every block without a row that is."""
+    c = Codes(lens, 2, d, ps, block, layout, seed=d + ps)
+    for b, n in enumerate(lens):
+        live = ref.seen_rows(n - 1, window, sink)
+        hidden = torch.as_tensor(np.setdiff1d(np.arange(n), live))
+        page = c.table[b].cpu()[hidden // ps].long().cuda()
+        for pool in (c.k, c.v):
+            pool.view(torch.uint8)[page, :, (hidden % ps).cuda()] = 0x7F
+        blocks = torch.as_tensor(np.setdiff1d(np.arange(-(-n // block)), live // block))
+        page = c.table[b].cpu()[blocks * block // ps].long().cuda()
+        for scale in (c.ks, c.vs):
+            scale[page, :, (blocks * block % ps // block).cuda()] = math.nan
+    q = ask(c, 4)
+    for more in (0, 16384 // ps):
+        c.cache["table"] = torch.cat([c.table, torch.full((len(lens), more), -1, dtype=torch.int32, device="cuda")], 1)
+        check_codes(c, q, *attend(c, q, window=window, sink=sink), None, window, sink)
+    assert skv.paged_status() == 0
+
+
+def test_pools_of_codes_with_room_between_rows_and_pages():
+    """Pools that are part of a larger tensor, and strides of dimensions that are never stepped through."""
+    c = Codes([100, 37], 2, 64, 16, 16, seed=50)
+    wide = [torch.full((c.k.shape[0], 3, 20, 128), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for w, pool in zip(wide, (c.k, c.v)):
+        w[:, 1:, 2:18, 32:96] = pool.view(torch.uint8)
+    pools = [w[:, 1:, 2:18, 32:96].view(E4M3) for w in wide]
+    q = ask(c, 4)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    skv.paged_attention(q, *pools, c.table, c.lens, out, lse, k_scale=c.ks, v_scale=c.vs)
+    check_codes(c, q, out, lse)
+    x = torch.randn((5, 2, 64), device="cuda").to(torch.bfloat16)
+    before = [w.clone() for w in wide]
+    c.table = torch.cat([c.table, torch.full((2, 1), -1, dtype=torch.int32, device="cuda")], 1)
+    skv.paged_quantise(x, x, *pools, c.ks, c.vs, c.table, i32([100, 37]), i32([0, 5, 5]))
+    back = [torch.zeros_like(x) for _ in range(2)]
+    skv.paged_dequantise(*pools, c.ks, c.vs, c.table, i32([105, 37]), i32([100, 0]), i32([0, 5, 5]), *back)
+    for h in range(2):
+        want, size = quantised(c, 0, h, "k", 100, f64(x[:, h]))
+        assert np.array_equal(f64(back[0][:, h]), (want * size[:, None])[100:])
+    for w, b in zip(wide, before):
+        w[:, 1:, 2:18, 32:96] = b[:, 1:, 2:18, 32:96]
+        assert torch.equal(w, b)
+    assert skv.paged_status() == 0
+    # one page, one head: their strides may be anything
+    c = Codes([9], 1, 64, 16, 8, seed=51)
+    pools = [p[int(c.table[0, 0])][None].as_strided((1, 1, 16, 64), (77, 33, 64, 1)) for p in (c.k, c.v)]
+    scales = [s[int(c.table[0, 0])][None] for s in (c.ks, c.vs)]
+    q = ask(c, 2)
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    skv.paged_attention(q, *pools, torch.zeros((1, 1), dtype=torch.int32, device="cuda"), c.lens, out, lse, k_scale=scales[0],
+                        v_scale=scales[1])
+    check_codes(c, q, out, lse)
+
+
+def test_pools_of_codes_that_are_expanded_are_refused():
+    c = Codes([9], 1, 64, 16, 8, seed=52)
+    q = ask(c, 2)
+    for dim, shape in ((1, (-1, 2, -1, -1)), (0, (6, -1, -1, -1))):
+        pools = [p[:1].expand(*shape) if dim == 0 else p.expand(*shape) for p in (c.k, c.v)]
+        scales = [torch.ones((pools[0].shape[0], pools[0].shape[1], 2), device="cuda") for _ in range(2)]
+        heads = 2 * pools[0].shape[1]
+        with pytest.raises(skv.ShadowKVError) as e:
+            skv.paged_attention(q[:, :1].expand(-1, heads, -1).contiguous(), *pools, c.table, c.lens,
+                                torch.empty((1, heads, 64), dtype=torch.bfloat16, device="cuda"), k_scale=scales[0], v_scale=scales[1])
+        assert e.value.code == -1
