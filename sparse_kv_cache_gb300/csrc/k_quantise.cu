@@ -100,9 +100,10 @@ __global__ void __launch_bounds__(32 * kQzWarps, sizeof(T) == 4 ? 3 : 4) k_quant
         len = rows_of(p.c, b, g_err, 811);
         if (t0 < 0 || t1 > p.tokens || t1 < t0 || t1 - t0 > p.c.cap - len) set_err(g_err, DEV_ERR_BOUNDS, 812);
         if (t0 >= 0 && t1 <= p.tokens && t0 < t1) {
-            const int64_t blk = (len >> p.lgb) + slot - ((t0 >> p.lgb) + 2 * static_cast<int64_t>(b));
+            const int64_t skip = slot - ((t0 >> p.lgb) + 2 * static_cast<int64_t>(b)), blk = (len >> p.lgb) + skip;
             const int n = min(t1 - t0, p.c.cap - len);
-            if (blk << p.lgb < len + n) {
+            // (a place before the first sequence's has no block: tokens before start[0] are of no sequence)
+            if (skip >= 0 && blk << p.lgb < len + n) {
                 row0 = static_cast<int>(blk) << p.lgb;
                 from = max(row0, len);
                 to = min(row0 + (1 << p.lgb), len + n);

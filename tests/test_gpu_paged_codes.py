@@ -436,6 +436,36 @@ def test_what_is_out_of_range_is_not_written():
     assert skv.paged_status() == -5 and (out[0][:4] == 7.0).all() and not (out[0][4:8] == 7.0).all()
 
 
+def test_tokens_of_no_sequence_are_left_out():
+    """Tokens before start[0] and behind start[batch], more of them than the sequences have rows: places without a block,
+    which look at no table."""
+    for block, n in ((8, 300), (64, 1000)):
+        c = Codes([5, 0, 33], 2, 64, 64, block, seed=block, cap=128)
+        guard = torch.full((7, 2 + c.table.shape[1]), 1 << 29, dtype=torch.int32, device="cuda")    # bad ids around the table
+        guard[2:5, 1:-1] = c.table
+        table = guard[2:5, 1:-1]
+        start = np.array([n, n + 4, n + 4, n + 24])
+        x = torch.randn((n + 24 + 500, 2, 64), device="cuda").to(torch.bfloat16)
+        before = c.k.clone()
+        skv.paged_quantise(x, x, c.k, c.v, c.ks, c.vs, table, c.lens, i32(start))
+        assert skv.paged_status() == 0
+        back = [torch.full_like(x, 7.0) for _ in range(2)]
+        skv.paged_dequantise(c.k, c.v, c.ks, c.vs, table, i32([9, 0, 53]), c.lens, i32(start), *back)
+        assert skv.paged_status() == 0
+        for b, held in ((0, 5), (2, 33)):
+            for h in range(2):
+                want, size = quantised(c, b, h, "k", held, f64(x[start[b]:start[b + 1], h]))
+                got, gs = c.held("k", b, h, len(want))
+                assert np.array_equal(got, want) and np.array_equal(gs, size)
+                assert np.array_equal(f64(back[0][start[b]:start[b + 1], h]), (want * size[:, None])[held:])
+        assert (back[0][:n] == 7.0).all() and (back[0][n + 24:] == 7.0).all()
+        used = torch.zeros(c.k.shape[:3], dtype=torch.bool)
+        for b, rows in ((0, 9), (2, 53)):
+            at = torch.arange(rows)
+            used[c.table.cpu()[b, at // 64].long(), :, at % 64] = True
+        assert (c.k.view(torch.uint8).cpu() == before.view(torch.uint8).cpu())[~used].all()
+
+
 def test_codes_beyond_32_bit_offsets():
     """Pages 2^26 bytes apart: their offsets pass 2^32."""
     n, d, ps, step = 100, 128, 16, 1 << 26

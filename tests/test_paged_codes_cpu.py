@@ -132,6 +132,19 @@ def test_c_entries_of_the_further_calls_refuse(skv):  # noqa: F811
             assert call(**x) == -1, x
 
 
+def test_calls_of_no_tokens_and_no_sequences_do_nothing(skv):  # noqa: F811
+    for batch, tokens in ((2, 0), (0, 0), (0, 5)):
+        c = codes(batch=batch)
+        k, start, first = torch.zeros((tokens, 2, 128), dtype=torch.bfloat16), torch.zeros(batch + 1, dtype=torch.int32), torch.zeros(batch, dtype=torch.int32)
+        skv.paged_quantise(k, k, *(c[n] for n in ("k_cache", "v_cache", "k_scale", "v_scale", "table", "lens")), start, stream=0)
+        skv.paged_dequantise(*(c[n] for n in ("k_cache", "v_cache", "k_scale", "v_scale", "table", "lens")), first, start, k, k.clone(), stream=0)
+        q = torch.zeros((tokens, 4, 128), dtype=torch.bfloat16)
+        p = cache(batch=batch)
+        skv.paged_prompt_attention(q, p["k_cache"], p["v_cache"], p["table"], p["lens"], start, torch.empty_like(q), stream=0)
+    c, q = codes(batch=0), torch.zeros((0, 4, 128), dtype=torch.bfloat16)
+    skv.paged_attention(q, **c, out=torch.empty_like(q), window=3, sink=1, stream=0)
+
+
 # ------------------------------------------------------------------ the float64 forms
 
 def test_e4m3_pins():
