@@ -621,10 +621,11 @@ int shadowkv_paged_evict(const skv_paged_evict_args* args, skv_stream stream);
  * the pools: a value is code * scale[page][head][row % page_size / block].  q and out are bf16.  The
  * scales are powers of two as shadowkv_paged_quantise writes them; any positive ones do here.  Strides of the pools are
  * above zero where there is more than one to step through, and below 2^40 bytes; rows are read by tiles of 16, also
- * those of a tile that are not seen or lie behind the last one.  A code of NaN in a row that is seen gives NaN.  Scores are formed from fp16 queries, a power of two per head apart (what is below
- * 2^-39 of a head's largest element is lost), probabilities take their value's scale and are rounded to fp16:
- * a row whose probability times scale is 2^-32 below the unit's heaviest may weigh nothing.  Everything else is
- * as above.  Where a kernel's bounded wait ran out (shadowkv_paged_status: SKV_ERR_TIMEOUT) results are NaN.
+ * those of a tile that are not seen or lie behind the last one.  A code of NaN in a row that is seen gives NaN.
+ * Scores are formed from fp16 queries, a power of two per head apart (what is below 2^-39 of a head's largest
+ * element is lost), probabilities take their value's scale and are rounded to fp16: a row whose probability times
+ * scale is 2^-32 below the unit's heaviest may weigh nothing.  Everything else is as above.  Where a kernel's bounded
+ * wait ran out (shadowkv_paged_status: SKV_ERR_TIMEOUT) results are NaN.
  *
  * attn.weight and attn.weight_out go with whole caches of the other types (window 0), where this call is
  * shadowkv_paged_attention; anywhere else they are refused.

@@ -257,7 +257,7 @@ struct PromptSpace { int64_t tiles, stat, bytes; };
 
 int prompt_space(const skv_paged_prompt_args* a, PromptSpace* w) {
     const skv_paged_cache& c = a->cache;
-    if (!good_type(c) || c.batch < 0 || a->tokens < 0 || a->reserved || a->n_q_heads < 1 || a->n_q_heads % c.n_kv_heads)
+    if (!good_type(c, kAll) || c.batch < 0 || a->tokens < 0 || a->reserved || a->n_q_heads < 1 || a->n_q_heads % c.n_kv_heads)
         return SKV_ERR_INVALID;
     const int G = a->n_q_heads / c.n_kv_heads;
     if (G > 8 || !std::isfinite(a->scale) || a->window < 0 || a->sink < 0) return SKV_ERR_INVALID;

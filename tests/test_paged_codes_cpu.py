@@ -227,7 +227,7 @@ def test_prompt_entry_and_workspace(skv):  # noqa: F811
               dict(steps=(512, 128, 512, 120)), dict(steps=(512, 128, 128, 128)), dict(scale=float("inf")), dict(pools=long, nbytes=0),
               dict(pools=long, space=0), dict(pools=long, space=at + 8), dict(pools=(*pools[:17], 0)), dict(pools=(*pools[:3], 24, *pools[4:]))):
         assert call(**x) == -1, x
-    for kind in (0, 2):
+    for kind in (0, 2, 3):
         assert call(pools=(kind, *pools[1:])) == -8
     # parts take room, one unit per SM and more takes none; the most that there may be does not overflow
     size = lambda **kw: lib.shadowkv_paged_prompt_attention_workspace(args(**kw))  # noqa: E731
