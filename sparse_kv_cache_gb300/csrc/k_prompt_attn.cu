@@ -28,9 +28,9 @@
 //
 // Measured (8 KV heads of 4 query heads, d = 128; cuBLAS reaches 1900 TFLOP/s in bursts, 1695 for seconds under the power
 // limit): a prompt of 32K tokens 6.26 ms, 1400 TFLOP/s; through a window of 4096 1.73 ms, 1190; 4 prompts of 4096 483
-// us, 1140; chunks of 13K tokens in all through a window of 1024 316 us, of 10.5 tiles a unit with three at an edge;
+// us, 1140; chunks of 13K tokens in all through a window of 1024 313 us, of 10.5 tiles a unit with three at an edge;
 // d = 64, 16K tokens 1.39 ms, 790, where the softmax takes as long as both products; 8 drafts of 5 tokens over up to
-// 4099 rows 31.6 us.  A half's tile takes its softmax about 1650 clocks (128 columns in 4 of them each at the
+// 4099 rows 24.6 us.  A half's tile takes its softmax about 1650 clocks (128 columns in 4 of them each at the
 // exponential unit, 32 a clock to an SM) and its products 1024, which the other half's overlap.
 // Tried: two threads to a row (7.1 ms for 32K: 20 warps to issue for), the first half of P handed over early (no
 // difference), six warps to look at values (505 us for the 4 prompts: they wait at the others' cost), CTAs that go through
@@ -38,6 +38,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "skv_common.cuh"
 #include "skv_internal.h"
@@ -51,6 +52,8 @@ constexpr int kPrTile = 128;                   // rows of a tile of keys
 constexpr int kPrHalf = 128;                   // query rows of an accumulator
 constexpr float kPrSlack = 8.f;                // the base moves when a score passes it by 2^8
 constexpr int kPrStages = 2;                   // tiles of keys, and of values, on their way or in use, at most
+constexpr int kPrMaxSlots = 160;               // places for units that are taken in parts
+constexpr int kPrMaxParts = 64;                // of a unit
 
 __device__ __forceinline__ float pr_exp2(float x) {
     float y;
@@ -149,7 +152,7 @@ __device__ __forceinline__ void tmem_put_wait() { asm volatile("tcgen05.wait::st
 // The unit of a CTA: tokens `tok` .. of the call, at rows row0 .. of sequence b; its tiles are positions
 // lo .. hi of the list [0, ts), [tw, ..) of tiles.
 struct PrUnit {
-    int b, h, split, tok, ntok, row0, ts, tw, lo, hi;
+    int b, h, tok, ntok, row0, ts, tw, lo, hi;
     __device__ __forceinline__ int tile(int pos) const { return pos < ts ? pos : tw + (pos - ts); }
 };
 // Rows that the tokens first .. last of a sequence see.
@@ -179,26 +182,21 @@ __device__ __forceinline__ PrWhole whole(const PrSees& s) {
     return PrWhole{(s.first - (kPrTile - 1)) >> 7, s.window ? ((s.last - s.window) >> 7) + 1 : INT32_MIN, (s.sink - kPrTile) >> 7};
 }
 
-// By one warp: which unit a block has; ntok 0 if none.
-__device__ __forceinline__ PrUnit find_unit(const PromptParams& p, int64_t block) {
-    const int t2 = p.halves * p.tq;
+// The place of a sequence's first unit: from there on places are its, and have units as long as there are tokens.
+__device__ __forceinline__ int first_place(const PromptParams& p, int start, int b) { return start / p.unit_tokens + b; }
+// The unit `skip` places behind sequence b's first one, with all its tiles; ntok 0 if there is none.  The sequence has
+// tokens t0 .. t1 and `len` rows.
+__device__ __forceinline__ PrUnit unit_at(const PromptParams& p, int64_t skip, int b, int t0, int t1, int len) {
     PrUnit u{};
-    u.split = static_cast<int>(block % p.nsplit);
-    block /= p.nsplit;
-    u.h = static_cast<int>(block % p.c.H);
-    // the last tokens of a sequence see most: their units start first
-    const int64_t slot = p.slots - 1 - block / p.c.H;
-    u.b = find_sequence(p.start, p.c.batch, slot, [&](int s, int i) { return static_cast<int64_t>(s / t2) + i; });
-    const int t0 = __ldcg(p.start + u.b), t1 = __ldcg(p.start + u.b + 1);
-    const int len = rows_of(p.c, u.b, g_err, 912);
+    u.b = b;
     if (t0 < 0 || t1 < t0 || t1 > p.tokens) {
         set_err(g_err, DEV_ERR_BOUNDS, 913);
         return u;
     }
-    const int64_t skip = (slot - (static_cast<int64_t>(t0 / t2) + u.b)) * t2;
+    skip *= p.unit_tokens;
     if (skip < 0 || skip >= t1 - t0) return u;
     u.tok = t0 + static_cast<int>(skip);
-    u.ntok = min(t2, t1 - u.tok);
+    u.ntok = min(p.unit_tokens, t1 - u.tok);
     u.row0 = len - (t1 - u.tok);
     // tiles: those of the first rows, then from the first token's window to the last token
     const int last = u.row0 + u.ntok - 1;
@@ -206,10 +204,93 @@ __device__ __forceinline__ PrUnit find_unit(const PromptParams& p, int64_t block
         const int upto = last / kPrTile;
         u.tw = p.c.window ? max(0, u.row0 - p.c.window + 1) / kPrTile : 0;
         u.ts = p.c.window ? min(u.tw, (p.c.sink + kPrTile - 1) / kPrTile) : 0;
-        const int64_t n = u.ts + upto - u.tw + 1;
-        u.lo = static_cast<int>(n * u.split / p.nsplit);
-        u.hi = static_cast<int>(n * (u.split + 1) / p.nsplit);
+        u.hi = u.ts + upto - u.tw + 1;
     }
+    return u;
+}
+// By one warp: which unit a block has.
+__device__ __forceinline__ PrUnit find_unit(const PromptParams& p, int64_t block) {
+    // the last tokens of a sequence see most: their units start first
+    const int64_t place = p.slots - 1 - block / p.c.H;
+    const int b = find_sequence(p.start, p.c.batch, place, [&](int s, int i) { return static_cast<int64_t>(first_place(p, s, i)); });
+    const int t0 = __ldcg(p.start + b);
+    PrUnit u = unit_at(p, place - first_place(p, t0, b), b, t0, __ldcg(p.start + b + 1), rows_of(p.c, b, g_err, 912));
+    u.h = static_cast<int>(block % p.c.H);
+    return u;
+}
+
+// Few units: parts of a unit's tiles each, all of about as many tiles, whichever unit they are of -- which only the device
+// can tell.  (16 sequences of 5 tokens over 1 to 16000 rows: with as many parts for each unit 139 us.)
+struct PrParts {
+    int start[kPrMaxSlots + 1], len[kPrMaxSlots];
+    int place[kPrMaxSlots];        // a sequence's first
+    PrUnit unit[kPrMaxSlots];      // of a place
+    int first[kPrMaxSlots + 1];    // its first part
+};
+// the last of n numbers that do not fall which is at most x, 0 if there is none
+__device__ __forceinline__ int last_upto(const int* v, int n, int x) {
+    int lo = 0;
+    for (int hi = n; hi - lo > 1;) {
+        const int mid = (lo + hi) / 2;
+        if (v[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// By one warp: what a block has, its `part` of all parts.  (It is in the way of all else: a few hundred instructions, whose
+// fetching takes as long as what they do.)
+__device__ __forceinline__ PrUnit find_part(const PromptParams& p, PrParts& s, int part) {
+    const int lane = threadIdx.x & 31, slots = static_cast<int>(p.slots), batch = p.c.batch;
+#pragma unroll 1
+    for (int i = lane; i <= batch; i += 32) {
+        const int t = __ldcg(p.start + i), n = __ldcg(p.c.lens + min(i, batch - 1));
+        s.start[i] = t;
+        if (i < batch) {
+            s.len[i] = rows_in(p.c, n, g_err, 912);
+            s.place[i] = first_place(p, t, i);
+        }
+    }
+    __syncwarp();
+    unsigned total = 0, longest = 0, live = 0;
+#pragma unroll 1
+    for (int i = lane; i < slots; i += 32) {
+        const int b = last_upto(s.place, batch, i);
+        const PrUnit u = unit_at(p, i - s.place[b], b, s.start[b], s.start[b + 1], s.len[b]);
+        s.unit[i] = u;
+        total += u.hi;
+        longest = max(longest, static_cast<unsigned>(u.hi));
+        live += u.ntok > 0;
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    live = __reduce_add_sync(0xffffffffu, live);
+    // A unit of n tiles has 1 + (n - 1) / most parts (one where it sees nothing), so all have p.parts at most: each of
+    // `live` units one, and total / most further ones.
+    const float most = fmaxf(2.f, fmaxf(__fdividef(total, p.parts - live), longest * (1.f / kPrMaxParts))), inv = __fdividef(1.f, most);
+    int at = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 < slots; i0 += 32) {
+        const int i = i0 + lane;
+        const int mine = i >= slots || s.unit[i].ntok == 0 ? 0 : 1 + min(static_cast<int>(max(s.unit[i].hi - 1, 0) * inv), kPrMaxParts - 1);
+        int upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += x;
+        }
+        if (i < slots) s.first[i] = at + upto - mine;
+        at += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) s.first[slots] = at;
+    __syncwarp();
+    if (part >= at) return PrUnit{};
+    const int place = last_upto(s.first, slots, part);
+    PrUnit u = s.unit[place];
+    const int from = part - s.first[place], parts = s.first[place + 1] - s.first[place];
+    const float each = __fdividef(u.hi, parts);
+    u.lo = static_cast<int>(from * each);
+    if (from + 1 < parts) u.hi = static_cast<int>((from + 1) * each);
     return u;
 }
 
@@ -443,7 +524,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-template <int D, class L>
+template <int D, class L, bool kParts>
 __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     const PrUnit& u = sh.unit;
     const int half = threadIdx.x >> 7, r = threadIdx.x & 127;
@@ -548,8 +629,8 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     const int g = r % p.G;
     const int64_t head = static_cast<int64_t>(u.h) * p.G + g, tok = u.tok + token;
     const float base2 = m == -CUDART_INF_F ? m : m + p.down_bits;
-    if (p.nsplit > 1) {
-        const int64_t rec = static_cast<int64_t>(blockIdx.x) * L::kHalves * kPrHalf + threadIdx.x;
+    if constexpr (kParts) {
+        const int64_t rec = static_cast<int64_t>(blockIdx.y * p.c.H + blockIdx.x) * L::kHalves * kPrHalf + threadIdx.x;
         if (live) p.part_stat[rec] = good ? make_float2(base2, l) : make_float2(0.f, CUDART_NAN_F);
         if (!good || tiles <= 0) return;
 #pragma unroll 1
@@ -588,18 +669,25 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     if (live && p.lse) p.lse[tok * p.n_q + head] = !good ? CUDART_NAN_F : l == 0.f ? -CUDART_INF_F : (base2 + log2f(l)) * 0.693147180559945309f;
 }
 
-template <int D, int kHalves>
+template <int D, int kHalves, bool kParts>
 __global__ void __launch_bounds__(PrForm<D, kHalves>::kThreads, PrForm<D, kHalves>::kCtas)
     k_prompt_attn(const __grid_constant__ PromptParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv) {
     using L = PrForm<D, kHalves>;
     extern __shared__ uint8_t s_raw[];
     __shared__ PrShared sh;
+    __shared__ std::conditional_t<kParts, PrParts, int> all;
     uint8_t* base = s_raw + ((1024 - (smem_u32(s_raw) & 1023)) & 1023);
     begin_call();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == L::kSoft) {
-        const PrUnit u = find_unit(p, blockIdx.x);
+        PrUnit u;
+        if constexpr (kParts) {
+            u = find_part(p, all, blockIdx.y);
+            u.h = blockIdx.x;
+        } else {
+            u = find_unit(p, blockIdx.x);
+        }
         if (lane == 0) {
             sh.unit = u;
             for (int x = 0; x < 3; ++x) sh.whole[x] = whole(sees(p, u, x));
@@ -623,19 +711,26 @@ __global__ void __launch_bounds__(PrForm<D, kHalves>::kThreads, PrForm<D, kHalve
             prefetch_tensormap(&mk);
             prefetch_tensormap(&mv);
         }
-    }
-    __syncthreads();
-    if (sh.unit.ntok == 0) return;
-    if (warp == L::kSoft + 1) {
+    } else if (warp == L::kSoft + 1) {
         tmem_alloc(&sh.tmem, L::kColumns);
         tmem_relinquish();
         tc_fence_before();
     }
     __syncthreads();
     tc_fence_after();
+    // the merge's note of all places' parts
+    if constexpr (kParts) {
+        if (blockIdx.x + blockIdx.y == 0 && warp == L::kSoft + 2)
+            for (int i = lane; i < static_cast<int>(p.slots); i += 32)
+                p.note[i] = make_int4(all.first[i], all.first[i + 1] - all.first[i], all.unit[i].tok, all.unit[i].ntok);
+    }
+    if (sh.unit.ntok == 0) {
+        if (warp == L::kSoft + 1) tmem_dealloc(sh.tmem, L::kColumns);
+        return;
+    }
     if (warp < L::kSoft) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kRegsMore));
-        pr_softmax<D, L>(p, sh, base);
+        pr_softmax<D, L, kParts>(p, sh, base);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegsLess));
         if (warp == L::kSoft) pr_load<D, L>(p, &mq, &mk, &mv, sh, base);
@@ -656,42 +751,65 @@ __global__ void __launch_bounds__(PrForm<D, kHalves>::kThreads, PrForm<D, kHalve
     }
 }
 
-// Joins the parts of the units' rows in their order: a block per unit, a thread per row and four dimensions.
+// Joins the parts of the units' rows in their order: a warp per row, a lane per part for the weights, then per
+// dimensions.  (With a thread per row and four dimensions, which goes from part to part, 26 us for 37 parts.)
 template <int D>
 __global__ void __launch_bounds__(256) k_prompt_merge(const __grid_constant__ PromptParams p) {
-    __shared__ PrUnit s_unit;
+    constexpr int kEach = D / 32;
     pdl_wait();
     pdl_trigger();
-    if (threadIdx.x < 32) {
-        const PrUnit u = find_unit(p, static_cast<int64_t>(blockIdx.x) * p.nsplit);
-        if (threadIdx.x == 0) s_unit = u;
-    }
-    __syncthreads();
-    const PrUnit u = s_unit;
-    const int rows = u.ntok * p.G;
-    for (int k = threadIdx.x + blockIdx.y * 256; k < rows * (D / 4); k += 256 * gridDim.y) {
-        const int i = k / (D / 4), dim = 4 * (k % (D / 4)), token = i / p.G, g = i % p.G;
-        const int half = token / p.tq, r = (token - half * p.tq) * p.G + g;
-        const int64_t step = p.halves * kPrHalf, rec = static_cast<int64_t>(blockIdx.x) * p.nsplit * step + half * kPrHalf + r;
-        float m = -CUDART_INF_F, l = 0.f, x[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < p.nsplit; ++s) m = fmaxf(m, __ldcg(p.part_stat + rec + s * step).x);
-        for (int s = 0; s < p.nsplit; ++s) {
-            const float2 st = __ldcg(p.part_stat + rec + s * step);
-            if (st.y == 0.f) continue;             // this part sees nothing
-            const float w = st.x == -CUDART_INF_F ? CUDART_NAN_F : pr_exp2(st.x - m);
-            const float4 o = st.y != st.y ? make_float4(st.y, st.y, st.y, st.y)
-                                          : __ldcg(reinterpret_cast<const float4*>(p.part + (rec + s * step) * D + dim));
-            l = fmaf(st.y, w, l);
-            x[0] = fmaf(o.x, w, x[0]);
-            x[1] = fmaf(o.y, w, x[1]);
-            x[2] = fmaf(o.z, w, x[2]);
-            x[3] = fmaf(o.w, w, x[3]);
+    const int h = blockIdx.x % p.c.H, lane = threadIdx.x & 31;
+    const int4 note = __ldcg(p.note + blockIdx.x / p.c.H);
+    const int first = note.x, parts = note.y, tok0 = note.z, rows = note.w * p.G;
+    for (int i = blockIdx.y * 8 + (threadIdx.x >> 5); i < rows; i += 8 * gridDim.y) {
+        const int token = i / p.G, g = i - token * p.G, half = token / p.tq, r = (token - half * p.tq) * p.G + g;
+        const int64_t block = p.halves * kPrHalf, step = p.c.H * block, rec = first * step + h * block + half * kPrHalf + r;
+        float2 st[kPrMaxParts / 32];
+        float m = -CUDART_INF_F, l = 0.f, w[kPrMaxParts / 32], x[kEach] = {};
+#pragma unroll
+        for (int k = 0; k < kPrMaxParts / 32; ++k) {
+            const int s = 32 * k + lane;
+            st[k] = s < parts ? __ldcg(p.part_stat + rec + s * step) : make_float2(-CUDART_INF_F, 0.f);
+            m = fmaxf(m, st[k].x);
+        }
+        m = warp_max(m);
+#pragma unroll
+        for (int k = 0; k < kPrMaxParts / 32; ++k) {
+            // (a sum of zero: this part sees nothing; NaN is the row's, or that of a wait that ran out)
+            w[k] = st[k].y == 0.f ? 0.f : st[k].y != st[k].y ? CUDART_NAN_F : pr_exp2(st[k].x - m);
+            if (w[k] != 0.f) l = fmaf(st[k].y, w[k], l);
+        }
+        l = warp_sum(l);
+        auto add = [&](float weight, int s) {
+            const float* src = p.part + (rec + s * step) * D + kEach * lane;
+            if constexpr (kEach == 4) {
+                const float4 o = __ldcg(reinterpret_cast<const float4*>(src));
+                x[0] = fmaf(o.x, weight, x[0]);
+                x[1] = fmaf(o.y, weight, x[1]);
+                x[2] = fmaf(o.z, weight, x[2]);
+                x[3] = fmaf(o.w, weight, x[3]);
+            } else {
+                const float2 o = __ldcg(reinterpret_cast<const float2*>(src));
+                x[0] = fmaf(o.x, weight, x[0]);
+                x[1] = fmaf(o.y, weight, x[1]);
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < kPrMaxParts / 32; ++k) {
+            const int n = min(parts - 32 * k, 32);
+#pragma unroll 8
+            for (int s = 0; s < n; ++s) {
+                const float weight = __shfl_sync(0xffffffffu, w[k], s);
+                if (weight != 0.f) add(weight, 32 * k + s);        // (where it is, nothing may have been written)
+            }
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int64_t head = static_cast<int64_t>(u.h) * p.G + g, tok = u.tok + token;
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + tok * p.o_tok + head * p.o_head + dim) =
-            make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
-        if (dim == 0 && p.lse) p.lse[tok * p.n_q + head] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.693147180559945309f;
+        const int64_t head = static_cast<int64_t>(h) * p.G + g, tok = tok0 + token;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + tok * p.o_tok + head * p.o_head + kEach * lane;
+        const uint32_t lower = pack_bf16x2(x[0] * inv, x[1] * inv);
+        if constexpr (kEach == 4) *reinterpret_cast<uint2*>(out) = make_uint2(lower, pack_bf16x2(x[2] * inv, x[3] * inv));
+        else *reinterpret_cast<uint32_t*>(out) = lower;
+        if (lane == 0 && p.lse) p.lse[tok * p.n_q + head] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.693147180559945309f;
     }
 }
 
@@ -700,27 +818,34 @@ __global__ void __launch_bounds__(256) k_prompt_merge(const __grid_constant__ Pr
 PromptPlan prompt_plan(int tokens, int batch, int G, int H, int64_t tiles, int nsm) {
     // one half where the sequences have no more tokens than that takes, on average (they are on the device)
     const int tq = kPrHalf / G, halves = tokens <= static_cast<int64_t>(batch) * tq ? 1 : 2;
-    PromptPlan plan{halves, 1, tokens / (halves * tq) + static_cast<int64_t>(batch)};
-    // parts of a unit's tiles: as many as fill the SMs once, of two tiles at least
-    const int64_t units = plan.slots * H, most = std::min<int64_t>((tiles + 1) / 2, (3 - halves) * nsm / std::max<int64_t>(units, 1));
-    plan.nsplit = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(most, 32)));
+    PromptPlan plan{halves, 0, tokens / (halves * tq) + static_cast<int64_t>(batch)};
+    // parts of the units' tiles, two tiles at least: as many as fill the SMs once, where they can be two for each place
+    const int64_t room = (3 - halves) * nsm / H;
+    if (tiles > 2 && room >= 2 * plan.slots)
+        plan.parts = static_cast<int>(std::min<int64_t>({room, plan.slots * ((tiles + 1) / 2), plan.slots * kPrMaxParts}));
     return plan;
 }
 
-template <int D, int kHalves>
+template <int D, int kHalves, bool kParts>
 static int launch_prompt(const PromptParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
     using L = PrForm<D, kHalves>;
     constexpr int smem = L::kBytes + 1024;
-    auto kernel = k_prompt_attn<D, kHalves>;
+    auto kernel = k_prompt_attn<D, kHalves, kParts>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return -1;
-    const int64_t units = p.slots * p.c.H;
-    if (launch_first(kernel, static_cast<unsigned>(units * p.nsplit), L::kThreads, smem, 1, 100, s, p, mq, mk, mv) != cudaSuccess) return -1;
-    if (p.nsplit > 1 && launch_first(k_prompt_merge<D>, dim3(static_cast<unsigned>(units), 4), 256, 0, 1, 100, s, p) != cudaSuccess) return -1;
+    const unsigned units = static_cast<unsigned>(p.slots * p.c.H);
+    if (launch_first(kernel, kParts ? dim3(p.c.H, p.parts) : dim3(units), L::kThreads, smem, 1, 100, s, p, mq, mk, mv) != cudaSuccess) return -1;
+    // (a block of the merge takes eight rows at a time)
+    const unsigned rows = std::min(p.tokens, p.unit_tokens) * p.G;
+    if (kParts && launch_first(k_prompt_merge<D>, dim3(units, (rows + 7) / 8), 256, 0, 1, 100, s, p) != cudaSuccess) return -1;
     return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
+template <int D>
+static int launch_prompt_form(const PromptParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+    if (p.parts) return p.halves == 1 ? launch_prompt<D, 1, true>(p, mq, mk, mv, s) : launch_prompt<D, 2, true>(p, mq, mk, mv, s);
+    return p.halves == 1 ? launch_prompt<D, 1, false>(p, mq, mk, mv, s) : launch_prompt<D, 2, false>(p, mq, mk, mv, s);
+}
 int launch_prompt_attn(int d, const PromptParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
-    if (p.halves == 1) return d == 64 ? launch_prompt<64, 1>(p, mq, mk, mv, s) : launch_prompt<128, 1>(p, mq, mk, mv, s);
-    return d == 64 ? launch_prompt<64, 2>(p, mq, mk, mv, s) : launch_prompt<128, 2>(p, mq, mk, mv, s);
+    return d == 64 ? launch_prompt_form<64>(p, mq, mk, mv, s) : launch_prompt_form<128>(p, mq, mk, mv, s);
 }
 
 cudaError_t prompt_err(int** e) { return cudaGetSymbolAddress(reinterpret_cast<void**>(e), g_err); }

@@ -253,7 +253,7 @@ int evict_space(const skv_paged_evict_args* a, EvictSpace* w) {
 
 // ------------------------------------------------------------------ attention of prompts
 
-struct PromptSpace { int64_t tiles, stat, bytes; };
+struct PromptSpace { int64_t tiles, stat, note, bytes; };
 
 int prompt_space(const skv_paged_prompt_args* a, PromptSpace* w) {
     const skv_paged_cache& c = a->cache;
@@ -268,9 +268,10 @@ int prompt_space(const skv_paged_prompt_args* a, PromptSpace* w) {
     const int64_t all = (static_cast<int64_t>(c.max_pages) * c.page_size + 127) / 128;
     w->tiles = a->window ? std::min<int64_t>(all, (static_cast<int64_t>(a->sink) + 127) / 128 + (static_cast<int64_t>(a->window) + 256) / 128 + 2) : all;
     const PromptPlan plan = prompt_plan(a->tokens, c.batch, G, c.n_kv_heads, w->tiles, kMaxSms);
-    const int64_t rows = plan.nsplit > 1 ? plan.slots * c.n_kv_heads * plan.nsplit * plan.halves * 128 : 0;
+    const int64_t rows = static_cast<int64_t>(plan.parts) * c.n_kv_heads * plan.halves * 128;
     w->stat = rows * c.head_dim * 4;
-    w->bytes = w->stat + rows * 8;
+    w->note = w->stat + rows * 8;
+    w->bytes = w->note + (plan.parts ? plan.slots * 16 : 0);
     return SKV_OK;
 }
 
@@ -565,8 +566,8 @@ int shadowkv_paged_prompt_attention(const skv_paged_prompt_args* a, skv_stream s
     p.c.sink = static_cast<int>(std::min<int64_t>(a->sink, kMaxRows));
     p.G = G; p.n_q = a->n_q_heads; p.tokens = a->tokens; p.tq = tq;
     const PromptPlan plan = prompt_plan(a->tokens, c.batch, G, c.n_kv_heads, w.tiles, dev.nsm < kMaxSms ? dev.nsm : kMaxSms);
-    if (plan.slots * c.n_kv_heads * plan.nsplit > INT32_MAX) return SKV_ERR_INVALID;
-    p.halves = plan.halves; p.nsplit = plan.nsplit; p.slots = plan.slots;
+    if (plan.slots * c.n_kv_heads > INT32_MAX) return SKV_ERR_INVALID;
+    p.halves = plan.halves; p.unit_tokens = plan.halves * tq; p.parts = plan.parts; p.slots = plan.slots;
     p.scale_log2 = static_cast<float>((a->scale != 0.f ? static_cast<double>(a->scale) : 1.0 / std::sqrt(double(c.head_dim))) *
                                       1.4426950408889634074);
     p.down_bits = static_cast<float>(8 + log2_of(p.c.cap));
@@ -574,6 +575,7 @@ int shadowkv_paged_prompt_attention(const skv_paged_prompt_args* a, skv_stream s
     p.start = a->start; p.out = a->out; p.lse = a->lse;
     p.part = static_cast<float*>(a->workspace);
     p.part_stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(a->workspace) + w.stat);
+    p.note = reinterpret_cast<int4*>(static_cast<uint8_t*>(a->workspace) + w.note);
     return done(launch_prompt_attn(c.head_dim, p, mq, mk, mv, stream));
 }
 

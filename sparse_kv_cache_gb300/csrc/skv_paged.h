@@ -92,16 +92,18 @@ struct PromptParams {
     int G, n_q, tokens;
     int tq;                   // tokens of 128 query rows: 128 / G
     int halves;               // of a unit, of 128 query rows each
-    int nsplit;               // parts of a unit's tiles
+    int unit_tokens;          // halves * tq
+    int parts;                // of units' tiles, for each KV head at most; 0: units are not taken in parts
     int64_t slots;            // places for units of halves * tq tokens of a sequence
     float scale_log2, down_bits;
     int64_t o_tok, o_head;
     const int32_t* start;
     void* out; float* lse;
-    float* part;              // [slots * H * nsplit][halves * 128][d]: parts of sums, unnormalised
+    float* part;              // [parts][H][halves * 128][d]: parts of sums, unnormalised
     float2* part_stat;        // their bases and sums of probabilities
+    int4* note;               // [slots]: first part, parts, first token, tokens
 };
-struct PromptPlan { int halves, nsplit; int64_t slots; };
+struct PromptPlan { int halves, parts; int64_t slots; };
 PromptPlan prompt_plan(int tokens, int batch, int G, int H, int64_t tiles, int nsm);      // tiles that a unit can see
 int launch_prompt_attn(int d, const PromptParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s);
 

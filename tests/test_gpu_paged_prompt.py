@@ -98,6 +98,9 @@ CASES = [
     (4, 1, 128, 16, "hnd", [300, 20], [300, 20], 1 << 30, 7),
     (4, 1, 128, 16, "hnd", [300, 20], [300, 20], 5, (1 << 31) - 1),
     (2, 1, 64, 16, "hnd", [(i * 37) % 90 for i in range(300)], [min((i * 37) % 90, (i * 13) % 7) for i in range(300)], 0, 0),
+    (4, 1, 128, 16, "hnd", [(i * i * 211) % 3001 for i in range(60)], [min((i * i * 211) % 3001, (i * 13) % 7) for i in range(60)], 0, 0),   # parts of uneven units
+    (2, 2, 64, 32, "hnd", [20000, 0, 7, 129, 5000] + [i for i in range(20)], [5, 0, 7, 129, 66] + [i % 3 if i > 2 else 0 for i in range(20)], 0, 0),
+    (4, 1, 128, 64, "nhd", [9000, 300, 4000, 20, 2500], [40, 33, 3, 20, 31], 2000, 600),
 ]
 
 
