@@ -629,42 +629,66 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     const int g = r % p.G;
     const int64_t head = static_cast<int64_t>(u.h) * p.G + g, tok = u.tok + token;
     const float base2 = m == -CUDART_INF_F ? m : m + p.down_bits;
+    // Sums and results go through the place of the warp's 32 queries, which no product reads any more, and from there out by
+    // whole rows: a thread's row each would be 32 lines to a store (5800 clocks for a CTA's 256 rows, and 1800 this way).
+    constexpr int kWords = D / 8, kPer = 32 / kWords;          // words of 16 bytes of a row there; rows to a store
+    const int lane = r & 31, word = lane % kWords;
+    const uint32_t lives = __ballot_sync(0xffffffffu, live);
+    uint8_t* stage = base + L::kQ + half * L::kTileBytes + (r & ~31) * D * 2;
+    auto put = [&](int row, int w) { return stage + row * D * 2 + (w ^ (row & 7)) * 16; };
     if constexpr (kParts) {
-        const int64_t rec = static_cast<int64_t>(blockIdx.y * p.c.H + blockIdx.x) * L::kHalves * kPrHalf + threadIdx.x;
-        if (live) p.part_stat[rec] = good ? make_float2(base2, l) : make_float2(0.f, CUDART_NAN_F);
-        if (!good || tiles <= 0) return;
+        const int64_t rec = static_cast<int64_t>(blockIdx.y * p.c.H + blockIdx.x) * L::kHalves * kPrHalf + (threadIdx.x & ~31);
+        if (live) p.part_stat[rec + lane] = good ? make_float2(base2, l) : make_float2(0.f, CUDART_NAN_F);
+        if (!good || tiles <= 0 || !lives) return;
+#pragma unroll 1
+        for (int half_row = 0; half_row < D; half_row += D / 2) {
+#pragma unroll
+            for (int d0 = 0; d0 < D / 2; d0 += 32) {
+                uint32_t o[32];
+                tmem_get32(o_at + half_row + d0, o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    *reinterpret_cast<uint4*>(put(lane, d0 / 4 + i)) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int i = 0; i < 32; i += kPer) {
+                const int row = i + lane / kWords;
+                if (lives >> row & 1)
+                    *reinterpret_cast<uint4*>(p.part + (rec + row) * D + half_row + 4 * word) = *reinterpret_cast<const uint4*>(put(row, word));
+            }
+            __syncwarp();
+        }
+        return;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at = tok * p.o_tok + head * p.o_head;
+    if (good && tiles > 0) {
 #pragma unroll 1
         for (int d0 = 0; d0 < D; d0 += 32) {
             uint32_t o[32];
             tmem_get32(o_at + d0, o);
-            if (live) {
-                uint4* dst = reinterpret_cast<uint4*>(p.part + rec * D + d0);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            }
-        }
-        return;
-    }
-    const float inv = !good ? CUDART_NAN_F : l == 0.f ? 0.f : 1.f / l;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + tok * p.o_tok + head * p.o_head;
-#pragma unroll 1
-    for (int d0 = 0; d0 < D; d0 += 32) {
-        uint32_t o[32];
-        if (good && tiles > 0) {
-            tmem_get32(o_at + d0, o);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0;
-        }
-        if (live) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 float x[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = l == 0.f && good ? 0.f : __uint_as_float(o[8 * c + i]) * inv;
-                store8(out + d0 + 8 * c, x);
+                for (int i = 0; i < 8; ++i) x[i] = l == 0.f ? 0.f : __uint_as_float(o[8 * c + i]) * inv;
+                store8(reinterpret_cast<__nv_bfloat16*>(put(lane, d0 / 8 + c)), x);
             }
         }
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < 32; i += kPer) {
+            const int row = i + lane / kWords;
+            const int64_t to = __shfl_sync(0xffffffffu, at, row);
+            const uint4 x = *reinterpret_cast<const uint4*>(put(row, word));
+            if (lives >> row & 1) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + to + 8 * word) = x;
+        }
+    } else if (live) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = good ? 0.f : CUDART_NAN_F;
+        for (int c = 0; c < D / 8; ++c) store8(static_cast<__nv_bfloat16*>(p.out) + at + 8 * c, x);
     }
     if (live && p.lse) p.lse[tok * p.n_q + head] = !good ? CUDART_NAN_F : l == 0.f ? -CUDART_INF_F : (base2 + log2f(l)) * 0.693147180559945309f;
 }

@@ -100,7 +100,7 @@ struct PromptParams {
     const int32_t* start;
     void* out; float* lse;
     float* part;              // [parts][H][halves * 128][d]: parts of sums, unnormalised
-    float2* part_stat;        // their bases and sums of probabilities
+    float2* part_stat;        // [parts][H][halves * 128]: their bases and sums of probabilities
     int4* note;               // [slots]: first part, parts, first token, tokens
 };
 struct PromptPlan { int halves, parts; int64_t slots; };
