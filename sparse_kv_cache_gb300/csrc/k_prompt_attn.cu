@@ -326,24 +326,25 @@ struct PrShared {
 
 // ------------------------------------------------------------------ the roles
 
+// By one thread, of the warp that loads the rest.
 template <int D, class L>
-__device__ void pr_load(const PromptParams& p, const CUtensorMap* mq, const CUtensorMap* mk, const CUtensorMap* mv, PrShared& sh,
+__device__ __forceinline__ void pr_load_queries(const PromptParams& p, const CUtensorMap* mq, PrShared& sh, const PrUnit& u, uint8_t* base) {
+    const int halves = u.ntok > p.tq ? 2 : 1;
+    mbar_arrive_expect_tx(&sh.q_full, halves * L::kParts * p.tq * p.G * 128);
+    for (int x = 0; x < halves; ++x)
+        for (int i = 0; i < L::kParts; ++i)
+            tma_load_3d(smem_u32(base) + L::kQ + x * L::kTileBytes + i * 16384, mq, i * 64, u.h * p.G, u.tok + x * p.tq, &sh.q_full);
+}
+template <int D, class L>
+__device__ void pr_load(const PromptParams& p, const CUtensorMap* mk, const CUtensorMap* mv, PrShared& sh,
                         uint8_t* base) {
     const PrUnit u = sh.unit;
     const PrSees both = sees(p, u, 2);
     const int lane = threadIdx.x & 31;
     const int box = min(kPrTile, 1 << p.c.lg), boxes = kPrTile / box, mask = (1 << p.c.lg) - 1;
     const uint32_t at = smem_u32(base);
-    // rows that kernels before this one wrote, to be read by the copy engine
-    asm volatile("fence.proxy.async;" ::: "memory");
-    const int halves = u.ntok > p.tq ? 2 : 1, j = lane % boxes, part = lane / boxes;
+    const int j = lane % boxes, part = lane / boxes;
     if (u.lo >= u.hi) return;
-    if (lane == 0) {
-        mbar_arrive_expect_tx(&sh.q_full, halves * L::kParts * p.tq * p.G * 128);
-        for (int x = 0; x < halves; ++x)
-            for (int i = 0; i < L::kParts; ++i)
-                tma_load_3d(at + L::kQ + x * L::kTileBytes + i * 16384, mq, i * 64, u.h * p.G, u.tok + x * p.tq, &sh.q_full);
-    }
     int keys = 0, vals = 0;                        // tiles that are on their way or there
     for (int pos = u.lo; pos < u.hi; ++pos) {
         const int n = pos - u.lo, s = n % L::kStages, row = u.tile(pos) * kPrTile;
@@ -630,7 +631,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     const int64_t head = static_cast<int64_t>(u.h) * p.G + g, tok = u.tok + token;
     const float base2 = m == -CUDART_INF_F ? m : m + p.down_bits;
     // Sums and results go through the place of the warp's 32 queries, which no product reads any more, and from there out by
-    // whole rows: a thread's row each would be 32 lines to a store (5800 clocks for a CTA's 256 rows, and 1800 this way).
+    // whole rows: a thread's row each would be 32 lines to a store (4 prompts of 4096: 479 us; 468).
     constexpr int kWords = D / 8, kPer = 32 / kWords;          // words of 16 bytes of a row there; rows to a store
     const int lane = r & 31, word = lane % kWords;
     const uint32_t lives = __ballot_sync(0xffffffffu, live);
@@ -702,9 +703,34 @@ __global__ void __launch_bounds__(PrForm<D, kHalves>::kThreads, PrForm<D, kHalve
     __shared__ PrShared sh;
     __shared__ std::conditional_t<kParts, PrParts, int> all;
     uint8_t* base = s_raw + ((1024 - (smem_u32(s_raw) & 1023)) & 1023);
-    begin_call();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp == L::kSoft && lane == 0) {
+        sh.dead = 0;
+        mbar_init(&sh.q_full, 1);
+        for (int s = 0; s < kPrStages; ++s) {
+            mbar_init(&sh.k_full[s], 1);
+            mbar_init(&sh.k_empty[s], 1);
+            mbar_init(&sh.v_full[s], 1);
+            mbar_init(&sh.v_ok[s], 2);
+            mbar_init(&sh.v_empty[s], 1);
+        }
+        mbar_init(&sh.given_up, 1);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&sh.s_full[x], 1);
+            mbar_init(&sh.p_full[x], 4);
+            mbar_init(&sh.o_full[x], 1);
+        }
+        fence_mbar_init();
+        prefetch_tensormap(&mq);
+        prefetch_tensormap(&mk);
+        prefetch_tensormap(&mv);
+    }
+    __syncwarp();
+    begin_call();
     if (warp == L::kSoft) {
+        // rows that kernels before this one wrote, to be read by the copy engine (in all of memory, not shared memory's too:
+        // that takes 1000 clocks more)
+        asm volatile("fence.proxy.async.global;" ::: "memory");
         PrUnit u;
         if constexpr (kParts) {
             u = find_part(p, all, blockIdx.y);
@@ -713,27 +739,9 @@ __global__ void __launch_bounds__(PrForm<D, kHalves>::kThreads, PrForm<D, kHalve
             u = find_unit(p, blockIdx.x);
         }
         if (lane == 0) {
+            if (u.lo < u.hi) pr_load_queries<D, L>(p, &mq, sh, u, base);
             sh.unit = u;
             for (int x = 0; x < 3; ++x) sh.whole[x] = whole(sees(p, u, x));
-            sh.dead = 0;
-            mbar_init(&sh.q_full, 1);
-            for (int s = 0; s < kPrStages; ++s) {
-                mbar_init(&sh.k_full[s], 1);
-                mbar_init(&sh.k_empty[s], 1);
-                mbar_init(&sh.v_full[s], 1);
-                mbar_init(&sh.v_ok[s], 2);
-                mbar_init(&sh.v_empty[s], 1);
-            }
-            mbar_init(&sh.given_up, 1);
-            for (int x = 0; x < 2; ++x) {
-                mbar_init(&sh.s_full[x], 1);
-                mbar_init(&sh.p_full[x], 4);
-                mbar_init(&sh.o_full[x], 1);
-            }
-            fence_mbar_init();
-            prefetch_tensormap(&mq);
-            prefetch_tensormap(&mk);
-            prefetch_tensormap(&mv);
         }
     } else if (warp == L::kSoft + 1) {
         tmem_alloc(&sh.tmem, L::kColumns);
@@ -757,7 +765,7 @@ __global__ void __launch_bounds__(PrForm<D, kHalves>::kThreads, PrForm<D, kHalve
         pr_softmax<D, L, kParts>(p, sh, base);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegsLess));
-        if (warp == L::kSoft) pr_load<D, L>(p, &mq, &mk, &mv, sh, base);
+        if (warp == L::kSoft) pr_load<D, L>(p, &mk, &mv, sh, base);
         else if (warp == L::kSoft + 1) {
             if (!pr_multiply<D, L>(p, sh, base)) {
                 if (elect_one()) tc_commit(&sh.given_up);

@@ -1028,7 +1028,7 @@ struct TileTC {
             ring.dead = 0;
             fence_mbar_init();
             // rows that kernels before this one wrote, to be read by the copy engine
-            asm volatile("fence.proxy.async;" ::: "memory");
+            asm volatile("fence.proxy.async.global;" ::: "memory");
         }
         __syncwarp();
         Piece then;
