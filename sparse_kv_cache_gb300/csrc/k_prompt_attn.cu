@@ -27,14 +27,14 @@
 // probabilities, in fp32, take the same factor, and it cancels.
 //
 // Measured (8 KV heads of 4 query heads, d = 128; cuBLAS reaches 1900 TFLOP/s in bursts, 1695 for seconds under the power
-// limit): a prompt of 32K tokens 6.26 ms, 1400 TFLOP/s; through a window of 4096 1.73 ms, 1190; 4 prompts of 4096 483
-// us, 1140; chunks of 13K tokens in all through a window of 1024 313 us, of 10.5 tiles a unit with three at an edge;
-// d = 64, 16K tokens 1.39 ms, 790, where the softmax takes as long as both products; 8 drafts of 5 tokens over up to
-// 4099 rows 24.6 us.  A half's tile takes its softmax about 1650 clocks (128 columns in 4 of them each at the
+// limit): a prompt of 32K tokens 6.3 ms, 1395 TFLOP/s; through a window of 4096 1.69 ms, 1220; 4 prompts of 4096 464
+// us, 1185; chunks of 13K tokens in all through a window of 1024 302 us, of 10.5 tiles a unit with three at an edge;
+// d = 64, 16K tokens 1.37 ms, 805, where the softmax takes as long as both products; 8 drafts of 5 tokens over up to
+// 4099 rows 23.5 us.  A half's tile takes its softmax about 1650 clocks (128 columns in 4 of them each at the
 // exponential unit, 32 a clock to an SM) and its products 1024, which the other half's overlap.
 // Tried: two threads to a row (7.1 ms for 32K: 20 warps to issue for), the first half of P handed over early (no
-// difference), six warps to look at values (505 us for the 4 prompts: they wait at the others' cost), CTAs that go through
-// many units (517 us: what a unit's start and end take is hidden, but the units fall unevenly).
+// difference), six warps to look at values (505 us for the 4 prompts, 483 then: they wait at the others' cost), CTAs that go
+// through many units (517 us, 483 then: what a unit's start and end take is hidden, but the units fall unevenly).
 #include <math_constants.h>
 
 #include <algorithm>
@@ -238,8 +238,7 @@ __device__ __forceinline__ int last_upto(const int* v, int n, int x) {
     return lo;
 }
 
-// By one warp: what a block has, its `part` of all parts.  (It is in the way of all else: a few hundred instructions, whose
-// fetching takes as long as what they do.)
+// By one warp: what a block has, its `part` of all parts.  (All else waits for it: 4100 clocks, find_unit's 1900.)
 __device__ __forceinline__ PrUnit find_part(const PromptParams& p, PrParts& s, int part) {
     const int lane = threadIdx.x & 31, slots = static_cast<int>(p.slots), batch = p.c.batch;
 #pragma unroll 1
@@ -295,7 +294,8 @@ __device__ __forceinline__ PrUnit find_part(const PromptParams& p, PrParts& s, i
 }
 
 // A CTA's form: two halves, one CTA to an SM; or where a unit's tokens are few one half, two CTAs to an SM, whose tiles
-// and softmax take turns (8 sequences of 5 tokens over 4099 rows: 40 us with two halves of which one is empty).
+// and softmax take turns (8 sequences of 5 tokens over 4099 rows: 32 us, and 40 with two halves of which one is empty, both
+// with parts less even than now).
 template <int D, int kHalves_>
 struct PrForm {
     static constexpr int kHalves = kHalves_, kSoft = 4 * kHalves, kThreads = 32 * (kSoft + 4), kCtas = 3 - kHalves;
@@ -784,7 +784,8 @@ __global__ void __launch_bounds__(PrForm<D, kHalves>::kThreads, PrForm<D, kHalve
 }
 
 // Joins the parts of the units' rows in their order: a warp per row, a lane per part for the weights, then per
-// dimensions.  (37 parts of 20 rows for 8 heads 8 us, most of it the way there; a part at a time 22.)
+// dimensions.  (37 parts of 20 rows for 8 heads 8 us, most of it the way there; a part at a time 22; a thread per row
+// and four dimensions 11.)
 template <int D>
 __global__ void __launch_bounds__(256) k_prompt_merge(const __grid_constant__ PromptParams p) {
     constexpr int kEach = D / 32;
