@@ -335,6 +335,15 @@ __device__ __forceinline__ void pr_load_queries(const PromptParams& p, const CUt
         for (int i = 0; i < L::kParts; ++i)
             tma_load_3d(smem_u32(base) + L::kQ + x * L::kTileBytes + i * 16384, mq, i * 64, u.h * p.G, u.tok + x * p.tq, &sh.q_full);
 }
+// By one warp: the rows behind the last token's heads (G does not divide 128) are zeros.  Nothing is made of their scores, but
+// a warp's bases move together, so what lay there before would have a part in how other rows are rounded.
+template <int D, class L>
+__device__ __forceinline__ void pr_clear_queries(const PromptParams& p, uint8_t* base) {
+    const int from = p.tq * p.G, words = (kPrHalf - from) * 8;         // of 16 bytes, of 64 dimensions
+    for (int i = threadIdx.x & 31; i < L::kHalves * L::kParts * words; i += 32)
+        *reinterpret_cast<uint4*>(base + L::kQ + i / words * 16384 + from * 128 + i % words * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+}
 template <int D, class L>
 __device__ void pr_load(const PromptParams& p, const CUtensorMap* mk, const CUtensorMap* mv, PrShared& sh,
                         uint8_t* base) {
@@ -744,6 +753,7 @@ __global__ void __launch_bounds__(PrForm<D, kHalves>::kThreads, PrForm<D, kHalve
             for (int x = 0; x < 3; ++x) sh.whole[x] = whole(sees(p, u, x));
         }
     } else if (warp == L::kSoft + 1) {
+        if (p.tq * p.G < kPrHalf) pr_clear_queries<D, L>(p, base);
         tmem_alloc(&sh.tmem, L::kColumns);
         tmem_relinquish();
         tc_fence_before();

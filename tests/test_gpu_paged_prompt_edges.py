@@ -1,0 +1,29 @@
+"""Prompts' attention where its kernels' forms end: heads that do not fill a tile, and what a caller may do that
+test_gpu_paged_prompt.py does not.  (Sizes and tolerances as there.)"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_kv_cache_gb300 as skv
+from tests.paged_harness import Paged
+from tests.test_gpu_paged_prompt import ask, attend, check_all, i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("G", [3, 5, 6, 7])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("tokens", [[23, 14], [700, 90]])
+def test_the_same_bits_whatever_ran_before(G, d, tokens):
+    """128 query rows are not a whole number of tokens: the rows left over hold nothing of an earlier call."""
+    c = Paged("bf16", [800, 574], 2, d, 16, seed=G)
+    other = Paged("bf16", [800, 574], 2, d, 16, seed=G + 1)
+    q = ask(c, G, tokens)
+    want = attend(c, q, tokens, window=300, sink=4)
+    check_all(c, tokens, q, *want, 300, 4)
+    for i in range(6):
+        attend(other, ask(other, 8 - i % 2, tokens, i, 10.0 ** (i - 2)), tokens)      # queries of another size
+        got = attend(c, q, tokens, window=300, sink=4)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
