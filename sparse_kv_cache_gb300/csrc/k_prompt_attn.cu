@@ -365,7 +365,7 @@ __device__ void pr_load(const PromptParams& p, const CUtensorMap* mk, const CUte
         const int z = __shfl_sync(0xffffffffu, page < 0 ? static_cast<int>(p.c.n_pages) : page, j);
         const int in_page = (row + j * box) & mask;
         const uint32_t to = at + s * L::kTileBytes + part * 16384 + j * box * 128;
-        if (!wait_or_give_up(&sh.k_empty[s], parity, &sh.dead)) break;
+        if (!warp_wait_or_give_up(&sh.k_empty[s], parity, &sh.dead)) break;
         if (lane == 0) {
             int absent = 0;
             for (int i = 0; i < 16; ++i) absent |= (gone >> (i * 8 / box) & 1) << i;
@@ -375,7 +375,7 @@ __device__ void pr_load(const PromptParams& p, const CUtensorMap* mk, const CUte
         __syncwarp();
         if (part < L::kParts) tma_load_4d(to + L::kK, mk, part * 64, in_page, u.h, z, &sh.k_full[s]);
         keys = n + 1;
-        if (!wait_or_give_up(&sh.v_empty[s], parity, &sh.dead)) break;
+        if (!warp_wait_or_give_up(&sh.v_empty[s], parity, &sh.dead)) break;
         if (lane == 0) mbar_arrive_expect_tx(&sh.v_full[s], L::kTileBytes);
         __syncwarp();
         if (part < L::kParts) tma_load_4d(to + L::kV, mv, part * 64, in_page, u.h, z, &sh.v_full[s]);
@@ -418,7 +418,7 @@ __device__ bool pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) 
         for (int i = 0; i < kPrTile / 16; ++i)
             tc_mma_bf16_ts(tmem + 128 * L::kHalves + x * 128, tmem + x * 128 + i * 8, v + i * (2048 >> 4), pv, n > 0 || i > 0);
     };
-    auto told = [&](uint64_t* bar, uint32_t parity) { return wait_or_give_up(bar, parity, &sh.dead); };
+    auto told = [&](uint64_t* bar, uint32_t parity) { return warp_wait_or_give_up(bar, parity, &sh.dead); };
     auto commit = [&](uint64_t* bar) {
         if (mine) tc_commit(bar);
     };
@@ -454,7 +454,7 @@ __device__ void pr_look(const PromptParams& p, PrShared& sh, uint8_t* base) {
     const int t = threadIdx.x - 32 * (L::kSoft + 2), warp = t >> 5;   // of 64
     for (int n = 0; n < u.hi - u.lo; ++n) {
         const int s = n % L::kStages, tile = u.tile(u.lo + n);
-        if (!wait_or_give_up(&sh.v_full[s], (n / L::kStages) & 1, &sh.dead)) return;
+        if (!warp_wait_or_give_up(&sh.v_full[s], (n / L::kStages) & 1, &sh.dead)) return;
         if (!calm.has(tile)) {
             uint32_t some = 0;
             uint8_t* v = base + L::kV + s * L::kTileBytes;
@@ -551,7 +551,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     bool good = true;
     for (int n = 0; n < tiles; ++n) {
         const int tile = u.tile(lo + n);
-        good = wait_or_give_up(&sh.s_full[half], n & 1, &sh.dead);
+        good = warp_wait_or_give_up(&sh.s_full[half], n & 1, &sh.dead);
         if (!good) break;
         tc_fence_after();
         float x[4][32];
@@ -623,7 +623,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
         tmem_put_wait();
         if (!sh.whole[2].has(tile)) {
             const int s = n % L::kStages;
-            good = wait_or_give_up(&sh.v_ok[s], (n / L::kStages) & 1, &sh.dead);
+            good = warp_wait_or_give_up(&sh.v_ok[s], (n / L::kStages) & 1, &sh.dead);
             if (!good) break;
             if (sh.is_wild(s)) pr_by_hand<D>(o_at, s_at, base + L::kV + s * L::kTileBytes, n == 0);
         }
@@ -632,7 +632,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
         if ((r & 31) == 0) mbar_arrive(&sh.p_full[half]);
     }
     if (good && tiles > 0) {
-        good = wait_or_give_up(&sh.o_full[half], 0, &sh.dead);
+        good = warp_wait_or_give_up(&sh.o_full[half], 0, &sh.dead);
         tc_fence_after();
     }
     const bool live = r < p.tq * p.G && token < u.ntok;

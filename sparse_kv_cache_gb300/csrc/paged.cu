@@ -6,6 +6,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
+#include <cstring>
 #include <initializer_list>
 #include <mutex>
 
@@ -195,6 +197,13 @@ int tensor_map(CUtensorMap* m, const void* base, int bytes, int d, uint32_t widt
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? SKV_OK
                : SKV_ERR_INVALID;
+}
+
+// SHADOWKV_FAULT=wait:q, wait:k or wait:v (tests): copies of that tensor's tiles are half as high as the kernels count on, so that
+// their waits for them run out.
+bool falls_short(char tensor) {
+    const char* e = std::getenv("SHADOWKV_FAULT");
+    return e && std::strncmp(e, "wait:", 5) == 0 && e[5] == tensor;
 }
 
 // ------------------------------------------------------------------ attention
@@ -554,10 +563,13 @@ int shadowkv_paged_prompt_attention(const skv_paged_prompt_args* a, skv_stream s
         return rc;
     const uint32_t G = a->n_q_heads / c.n_kv_heads, tq = 128 / G, box = std::min(c.page_size, 128);
     CUtensorMap mq, mk, mv;
-    if (int rc = tensor_map(&mq, a->q, 2, c.head_dim, 64, {{a->n_q_heads, a->q_head}, {a->tokens, a->q_tok}}, {G, tq})) return rc;
-    if (int rc = tensor_map(&mk, c.k, 2, c.head_dim, 64, {{c.page_size, c.k_row}, {c.n_kv_heads, c.k_head}, {c.n_pages, c.k_page}}, {box, 1, 1}))
+    if (int rc = tensor_map(&mq, a->q, 2, c.head_dim, 64, {{a->n_q_heads, a->q_head}, {a->tokens, a->q_tok}}, {G, falls_short('q') ? tq / 2 : tq}))
         return rc;
-    if (int rc = tensor_map(&mv, c.v, 2, c.head_dim, 64, {{c.page_size, c.v_row}, {c.n_kv_heads, c.v_head}, {c.n_pages, c.v_page}}, {box, 1, 1}))
+    if (int rc = tensor_map(&mk, c.k, 2, c.head_dim, 64, {{c.page_size, c.k_row}, {c.n_kv_heads, c.k_head}, {c.n_pages, c.k_page}},
+                            {falls_short('k') ? box / 2 : box, 1, 1}))
+        return rc;
+    if (int rc = tensor_map(&mv, c.v, 2, c.head_dim, 64, {{c.page_size, c.v_row}, {c.n_kv_heads, c.v_head}, {c.n_pages, c.v_page}},
+                            {falls_short('v') ? box / 2 : box, 1, 1}))
         return rc;
     Range range("shadowkv_paged_prompt_attention");
     PromptParams p{};

@@ -1,8 +1,7 @@
 """Prompts' attention where its kernels' forms end: heads that do not fill a tile, and what a caller may do that
 test_gpu_paged_prompt.py does not.  (Sizes and tolerances as there.)"""
-import math
+import os
 
-import numpy as np
 import pytest
 import torch
 
@@ -27,3 +26,29 @@ def test_the_same_bits_whatever_ran_before(G, d, tokens):
         attend(other, ask(other, 8 - i % 2, tokens, i, 10.0 ** (i - 2)), tokens)      # queries of another size
         got = attend(c, q, tokens, window=300, sink=4)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("tensor", "qkv")
+@pytest.mark.parametrize("G,d,lens,tokens", [
+    (4, 128, [200], [20]),                    # a half to a CTA
+    (4, 128, [256, 130], [200, 100]),         # two halves
+    (2, 64, [3000, 140], [5, 3]),             # parts, of a half
+    (3, 128, [2500], [300]),                  # parts, of two halves
+])
+def test_waits_that_run_out(G, d, lens, tokens, tensor):
+    """Copies that bring less than a kernel waits for: after its limit the call ends, with NaN and its status, and the next one
+    is as if there had been none."""
+    c = Paged("bf16", lens, 2, d, 16, seed=31)
+    q = ask(c, G, tokens)
+    want = attend(c, q, tokens)
+    check_all(c, tokens, q, *want)
+    assert skv.paged_status() == 0
+    os.environ["SHADOWKV_FAULT"] = "wait:" + tensor
+    try:
+        out, lse = attend(c, q, tokens)
+    finally:
+        del os.environ["SHADOWKV_FAULT"]
+    assert skv.paged_status() == -6 and skv.paged_status() == 0
+    assert out.isnan().all() and lse.isnan().all()
+    got = attend(c, q, tokens)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and skv.paged_status() == 0
