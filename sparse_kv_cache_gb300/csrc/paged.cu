@@ -422,9 +422,11 @@ int attend(const skv_paged_attention_args* a, const Part* part, const char* name
     PagedCodesParams p{};
     if (codes) {
         const uint32_t d = c.head_dim, box = std::min(c.page_size, 16);
-        if (int rc = tensor_map(&p.mk, c.k, 1, d, d, {{c.page_size, c.k_row}, {c.n_kv_heads, c.k_head}, {c.n_pages, c.k_page}}, {box, 1, 1}))
+        if (int rc = tensor_map(&p.mk, c.k, 1, d, d, {{c.page_size, c.k_row}, {c.n_kv_heads, c.k_head}, {c.n_pages, c.k_page}},
+                                {falls_short('k') ? box / 2 : box, 1, 1}))
             return rc;
-        if (int rc = tensor_map(&p.mv, c.v, 1, d, d, {{c.page_size, c.v_row}, {c.n_kv_heads, c.v_head}, {c.n_pages, c.v_page}}, {box, 1, 1}))
+        if (int rc = tensor_map(&p.mv, c.v, 1, d, d, {{c.page_size, c.v_row}, {c.n_kv_heads, c.v_head}, {c.n_pages, c.v_page}},
+                                {falls_short('v') ? box / 2 : box, 1, 1}))
             return rc;
     }
     p.c = view(c);

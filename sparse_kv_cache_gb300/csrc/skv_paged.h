@@ -202,6 +202,11 @@ __device__ __forceinline__ bool warp_wait_or_give_up(uint64_t* bar, uint32_t par
         : "memory");
     return ok != 0;
 }
+// Waits for copies that nobody has use for any more, by one thread, before a CTA ends that gave up: for a barrier's phase, and until
+// kWaitLimitNs after `since` at most, whatever the number of barriers.
+__device__ __forceinline__ void wait_out(uint64_t* bar, uint32_t parity, unsigned long long since) {
+    while (!mbar_try_wait(bar, parity) && globaltimer() - since < kWaitLimitNs) {}
+}
 // A box of a tensor of three or four dimensions to shared memory, counted on `bar`
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
     asm volatile(
