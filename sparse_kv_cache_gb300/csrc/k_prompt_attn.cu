@@ -315,6 +315,7 @@ struct PrShared {
     PrWhole whole[3];          // of either half's tokens, and of all
     uint32_t tmem;
     int dead;
+    int2 begun;                // tiles whose keys (x) and values (y) were asked for
     int absent[4];             // per tile (mod 4): groups of eight rows whose page is out of range or not looked at
     int wild[kPrStages][2];    // a tile at an edge has values that are not finite (what each of the two warps found)
     uint64_t given_up;         // the products that were under way
@@ -353,8 +354,7 @@ __device__ void pr_load(const PromptParams& p, const CUtensorMap* mk, const CUte
     const int box = min(kPrTile, 1 << p.c.lg), boxes = kPrTile / box, mask = (1 << p.c.lg) - 1;
     const uint32_t at = smem_u32(base);
     const int j = lane % boxes, part = lane / boxes;
-    if (u.lo >= u.hi) return;
-    int keys = 0, vals = 0;                        // tiles that are on their way or there
+    int keys = 0, vals = 0;
     for (int pos = u.lo; pos < u.hi; ++pos) {
         const int n = pos - u.lo, s = n % L::kStages, row = u.tile(pos) * kPrTile;
         const uint32_t parity = (n / L::kStages + 1) & 1;
@@ -381,21 +381,16 @@ __device__ void pr_load(const PromptParams& p, const CUtensorMap* mk, const CUte
         if (part < L::kParts) tma_load_4d(to + L::kV, mv, part * 64, in_page, u.h, z, &sh.v_full[s]);
         vals = n + 1;
     }
-    if (*const_cast<volatile int*>(&sh.dead)) {
-        // given up: no copy may be on its way when the CTA ends
-        mbar_wait(&sh.q_full, 0);
-        for (int n = max(0, keys - L::kStages); n < keys; ++n) mbar_wait(&sh.k_full[n % L::kStages], (n / L::kStages) & 1);
-        for (int n = max(0, vals - L::kStages); n < vals; ++n) mbar_wait(&sh.v_full[n % L::kStages], (n / L::kStages) & 1);
-    }
+    if (lane == 0) sh.begun = make_int2(keys, vals);
 }
 
 template <int D, class L>
-__device__ bool pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) {
+__device__ void pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) {
     const PrUnit u = sh.unit;
     const PrWhole calm = sh.whole[2];
     const uint32_t at = smem_u32(base), tmem = sh.tmem;
     const int halves = u.ntok > p.tq ? 2 : 1, tiles = u.hi - u.lo;
-    if (tiles <= 0) return true;
+    if (tiles <= 0) return;
     constexpr uint32_t qk = idesc_bf16_f32(kPrHalf, kPrTile), pv = idesc_bf16_f32(kPrHalf, D) | kBIsMN;
     // The whole warp comes this way and one thread of it issues: operands that are the warp's stay in uniform
     // registers (with one thread alone on the path an instruction took 115 clocks to issue, twice its work).
@@ -422,20 +417,20 @@ __device__ bool pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) 
     auto commit = [&](uint64_t* bar) {
         if (mine) tc_commit(bar);
     };
-    if (!told(&sh.q_full, 0) || !told(&sh.k_full[0], 0)) return false;
+    if (!told(&sh.q_full, 0) || !told(&sh.k_full[0], 0)) return;
     for (int x = 0; x < halves; ++x) scores(x, 0);
     commit(&sh.k_empty[0]);
     for (int n = 0; n < tiles; ++n) {
         const int s = n % L::kStages, next = (n + 1) % L::kStages;
-        if (!told(&sh.v_ok[s], (n / L::kStages) & 1)) return false;
+        if (!told(&sh.v_ok[s], (n / L::kStages) & 1)) return;
         const bool wild = !calm.has(u.tile(u.lo + n)) && sh.is_wild(s);
         for (int x = 0; x < halves; ++x) {
-            if (!told(&sh.p_full[x], n & 1)) return false;
+            if (!told(&sh.p_full[x], n & 1)) return;
             tc_fence_after();
             if (!wild) values(x, n);       // otherwise the row's threads have done it
             if (x == halves - 1) commit(&sh.v_empty[s]);
             if (n + 1 < tiles) {
-                if (x == 0 && !told(&sh.k_full[next], ((n + 1) / L::kStages) & 1)) return false;
+                if (x == 0 && !told(&sh.k_full[next], ((n + 1) / L::kStages) & 1)) return;
                 scores(x, n + 1);
                 if (x == halves - 1) commit(&sh.k_empty[next]);
             } else {
@@ -443,7 +438,6 @@ __device__ bool pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) 
             }
         }
     }
-    return true;
 }
 
 template <int D, class L>
@@ -776,17 +770,26 @@ __global__ void __launch_bounds__(PrForm<D, kHalves>::kThreads, PrForm<D, kHalve
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRegsLess));
         if (warp == L::kSoft) pr_load<D, L>(p, &mk, &mv, sh, base);
-        else if (warp == L::kSoft + 1) {
-            if (!pr_multiply<D, L>(p, sh, base)) {
-                if (elect_one()) tc_commit(&sh.given_up);
-                mbar_wait(&sh.given_up, 0);
-            }
-        } else pr_look<D, L>(p, sh, base);
+        else if (warp == L::kSoft + 1) pr_multiply<D, L>(p, sh, base);
+        else pr_look<D, L>(p, sh, base);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && sh.dead) set_err(g_err, DEV_ERR_TIMEOUT, 911);
+    if (sh.dead) {
+        // A wait ran out, of whichever warp: no copy and no product may be under way when the CTA ends.
+        const unsigned long long since = globaltimer();
+        if (threadIdx.x == 0) set_err(g_err, DEV_ERR_TIMEOUT, 911);
+        if (warp == L::kSoft && lane == 0) {
+            wait_out(&sh.q_full, 0, since);
+            for (int n = max(0, sh.begun.x - L::kStages); n < sh.begun.x; ++n) wait_out(&sh.k_full[n % L::kStages], (n / L::kStages) & 1, since);
+            for (int n = max(0, sh.begun.y - L::kStages); n < sh.begun.y; ++n) wait_out(&sh.v_full[n % L::kStages], (n / L::kStages) & 1, since);
+        } else if (warp == L::kSoft + 1) {
+            if (elect_one()) tc_commit(&sh.given_up);
+            wait_out(&sh.given_up, 0, since);
+        }
+        __syncwarp();
+    }
     if (warp == L::kSoft + 1) {
         tc_fence_after();
         tmem_dealloc(sh.tmem, L::kColumns);

@@ -202,7 +202,7 @@ __device__ __forceinline__ bool warp_wait_or_give_up(uint64_t* bar, uint32_t par
         : "memory");
     return ok != 0;
 }
-// Waits for copies that nobody has use for any more, by one thread, before a CTA ends that gave up: for a barrier's phase, and until
+// Waits for copies or products that nobody has use for any more, before a CTA ends that gave up: for a barrier's phase, and until
 // kWaitLimitNs after `since` at most, whatever the number of barriers.
 __device__ __forceinline__ void wait_out(uint64_t* bar, uint32_t parity, unsigned long long since) {
     while (!mbar_try_wait(bar, parity) && globaltimer() - since < kWaitLimitNs) {}
