@@ -655,7 +655,8 @@ int shadowkv_paged_attention_ext(const skv_paged_attention_ext_args* args, skv_s
  * 2^-9 of it is lost).
  *   code = x / scale, to the nearest, ties to even; NaN for a NaN and for an infinity
  * start does not fall, start[0] >= 0, start[batch] <= tokens; a sequence for which it does, or whose rows
- * would pass its table, sets the error word, and what is out of range is not written.  A bad page sets it too and
+ * would pass its table, sets the error word, and what is out of range is not written.  Where start falls, rows of other
+ * sequences may be left out too.  A bad page sets it too and
  * its rows are left out.  A sequence that is written to does not share its last page, and no block of the
  * call's is another's: no page is in two tables' places that are written.
  */
@@ -675,7 +676,8 @@ int shadowkv_paged_quantise(const skv_paged_quantise_args* args, skv_stream stre
  * Reads rows of a cache of dtype SKV_E4M3 back: tokens start[b] .. start[b+1] of k and v (bf16 or fp32) become
  * rows first[b] on of sequence b, code * scale in fp32, rounded once.  Rows from lens[b] on and tokens of no
  * sequence are left as they are, and so are the rows of a bad page, which sets the error word, and the
- * tokens of a sequence whose start or first is out of range, which does too.  k and v do not overlap.
+ * tokens of a sequence whose start or first is out of range, which does too (where start falls, other sequences' may be left
+ * out with them).  k and v do not overlap.
  */
 typedef struct {
     skv_paged_cache cache;      /* dtype SKV_E4M3 */
@@ -702,7 +704,7 @@ int shadowkv_paged_dequantise(const skv_paged_dequantise_args* args, skv_stream 
  * to step through, and below 2^40 bytes.  Whole pages are read, also behind a sequence's last row; what is in
  * a row that a token does not see has no part in its result, whatever it is.  Pages of which no row is
  * seen are not looked at.  start does not fall, start[0] >= 0, start[batch] <= tokens: the tokens of a sequence
- * for which it does are left out and set the error word.  Tokens of no sequence are left as they are.
+ * for which it does are left out and set the error word, and with them others may be.  Tokens of no sequence are left as they are.
  *
  * Scores, sums and softmax statistics are fp32; probabilities are rounded to bf16 (2^-8 at most), and what is
  * 2^-88 below a row's heaviest may weigh nothing (an infinite value there gives NaN).  Sums of values

@@ -751,6 +751,10 @@ __global__ void __launch_bounds__(PrForm<D, kHalves>::kThreads, PrForm<D, kHalve
         tmem_alloc(&sh.tmem, L::kColumns);
         tmem_relinquish();
         tc_fence_before();
+    } else if (warp == L::kSoft + 2) {
+        const int64_t block = blockIdx.y * static_cast<int64_t>(gridDim.x) + blockIdx.x, blocks = static_cast<int64_t>(gridDim.x) * gridDim.y;
+        for (int64_t b = block * 32 + lane; b < p.c.batch; b += blocks * 32)
+            check_sequence(p.c, p.start, p.tokens, static_cast<int>(b), g_err, 915);
     }
     __syncthreads();
     tc_fence_after();

@@ -93,6 +93,9 @@ __global__ void __launch_bounds__(32 * kQzWarps, sizeof(T) == 4 ? 3 : 4) k_quant
     const int64_t slot = unit / per_slot;
     const int h = static_cast<int>(unit % per_slot) >> 1;
     const bool values = unit & 1;
+    // (there are more threads than sequences: 64 for each at least)
+    const int64_t thread = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (thread < p.c.batch) check_sequence(p.c, p.start, p.tokens, static_cast<int>(thread), g_err, 814);
     int row0 = 0, from = 0, to = 0, len = 0, tok = 0, page = -1;
     if (slot < p.slots) {
         const int b = find_sequence(p.start, p.c.batch, slot, [&](int s, int i) { return (s >> p.lgb) + 2 * static_cast<int64_t>(i); });
@@ -226,6 +229,11 @@ __global__ void __launch_bounds__(32 * kDqWarps) k_dequantise(const __grid_const
         }
         s_page[lane] = page;
         s_at[lane] = at & ((1 << p.c.lg) - 1);
+    } else if (warp == 1 && blockIdx.y == 0) {
+        for (int64_t b = t0 + lane; b < p.c.batch; b += static_cast<int64_t>(gridDim.x) * kDqTokens) {
+            check_sequence(p.c, p.start, p.tokens, static_cast<int>(b), g_err, 824);
+            if (__ldcg(p.first + b) < 0) set_err(g_err, DEV_ERR_BOUNDS, 824);
+        }
     }
     __syncthreads();
     const int what = blockIdx.y * kDqWarps + warp;

@@ -254,6 +254,13 @@ __device__ __forceinline__ int find_sequence(const int32_t* start, int batch, in
     }
     return lo;
 }
+// Sets the error word where sequence b's tokens are no part of the call's or its length is out of range.  Once for every
+// sequence of a call: the searches above pass over some where starts fall.
+__device__ __forceinline__ void check_sequence(const PagedView& c, const int32_t* start, int tokens, int b, int* err, int where) {
+    const int t0 = __ldcg(start + b), t1 = __ldcg(start + b + 1);
+    rows_of(c, b, err, where);
+    if (t0 < 0 || t1 < t0 || t1 > tokens) set_err(err, DEV_ERR_BOUNDS, where);
+}
 // page of row i of sequence b, or -1 (and the error word) if its id is out of range
 __device__ __forceinline__ int page_of(const PagedView& c, int b, int i, int* err, int where) {
     const int id = c.table[b * c.table_seq + (i >> c.lg)];

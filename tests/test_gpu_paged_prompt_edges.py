@@ -52,3 +52,30 @@ def test_waits_that_run_out(G, d, lens, tokens, tensor):
     assert out.isnan().all() and lse.isnan().all()
     got = attend(c, q, tokens)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and skv.paged_status() == 0
+
+
+@pytest.mark.parametrize("lens,tokens", [([16, 16, 16], 100),                # whole units
+                                         ([3000, 16, 16], 100),              # parts
+                                         ([400] * 40, 9000)])                # many units
+def test_starts_that_fall_behind_a_longer_sequence_are_reported(lens, tokens):
+    """A search among starts passes over a sequence that begins behind a later one: it is reported all the same, and what the
+    call leaves out is left as it was."""
+    c = Paged("bf16", lens, 1, 64, 16, seed=5)
+    q = ask(c, 2, [tokens])
+    start = [0, tokens, 4, 8] + [8] * (len(lens) - 3)
+    out = torch.full_like(q, 7.0)
+    skv.paged_prompt_attention(q, c.k, c.v, c.table, c.lens, i32(start), out)
+    assert skv.paged_status() == -5 and skv.paged_status() == 0
+    # a bad length of a sequence without tokens
+    start, bad = [0] + [tokens] * len(lens), i32(lens[:-1] + [-1])
+    skv.paged_prompt_attention(q, c.k, c.v, c.table, bad, i32(start), out)
+    assert skv.paged_status() == -5
+    # rejected sequences' tokens are not touched
+    for start in ([-3, tokens // 2, tokens + 1], [40, 0, 10], [0, tokens + 1, tokens + 2]):
+        out.fill_(7.0)
+        skv.paged_prompt_attention(q, c.k, c.v, c.table[:2], c.lens[:2], i32(start), out)
+        assert skv.paged_status() == -5
+        for t in range(tokens):
+            of = [b for b in range(2) if 0 <= start[b] <= t < start[b + 1] <= tokens]
+            if not of:
+                assert (out[t] == 7).all()
