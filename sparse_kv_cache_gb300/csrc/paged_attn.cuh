@@ -695,10 +695,11 @@ struct TileTC {
                     const uint4& x = q[2 * j + i / 2];
                     mma_f16(i & 1 ? u : s, a.x, b.x, a.y, b.y, word(x, 2 * (i & 1)), word(x, 2 * (i & 1) + 1));
                 }
-            s[0] = (s[0] + u[0]) * id.s.ka * q0;
-            s[1] = (s[1] + u[1]) * id.s.ka * q1;
-            s[2] = (s[2] + u[2]) * id.s.kb * q0;
-            s[3] = (s[3] + u[3]) * id.s.kb * q1;
+            // (the two factors first: a sum of 2^32 times a scale may pass fp32 where the score does not)
+            s[0] = (s[0] + u[0]) * (id.s.ka * q0);
+            s[1] = (s[1] + u[1]) * (id.s.ka * q1);
+            s[2] = (s[2] + u[2]) * (id.s.kb * q0);
+            s[3] = (s[3] + u[3]) * (id.s.kb * q1);
         } else {
 #pragma unroll
             for (int j = 0; j < kKV; ++j) {

@@ -62,3 +62,15 @@ def test_starts_that_fall_behind_a_longer_sequence_are_reported(start):
         if min(first) == 0:
             skv.paged_quantise(k, k, *pools, *scales, table, i32([0] + lens[1:]), i32([0, 100, 100, 100]))
             assert skv.paged_status() == -5
+
+
+@pytest.mark.parametrize("power,size", [(-96, 96), (-60, 60), (60, -60), (100, -100), (116, -100), (110, -90)])
+def test_keys_far_from_one_and_queries_that_make_up_for_it(power, size):
+    """Products of a code and a query, 2^32 at most, times a block's scale may be beyond fp32 where the score is not."""
+    c = Codes([700, 45, 3], 2, 128, 16, 8, seed=23)
+    c.ks.mul_(2.0 ** power)
+    c.scales["k"] = [s * 2.0 ** power for s in c.scales["k"]]
+    q = ask(c, 4, size=2.0 ** size)
+    out, lse = attend(c, q)
+    assert out.isfinite().all() and lse.isfinite().all()
+    check_codes(c, q, out, lse)
