@@ -52,6 +52,7 @@ constexpr int kPrTile = 128;                   // rows of a tile of keys
 constexpr int kPrHalf = 128;                   // query rows of an accumulator
 constexpr float kPrSlack = 8.f;                // the base moves when a score passes it by 2^8
 constexpr int kPrStages = 2;                   // tiles of keys, and of values, on their way or in use, at most
+static_assert((kPrHold & (kPrHold - 1)) == 0, "");
 constexpr int kPrMaxSlots = 160;               // places for units that are taken in parts
 constexpr int kPrMaxParts = 64;                // of a unit
 
@@ -411,7 +412,7 @@ __device__ void pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) 
         if (!mine) return;
 #pragma unroll
         for (int i = 0; i < kPrTile / 16; ++i)
-            tc_mma_bf16_ts(tmem + 128 * L::kHalves + x * 128, tmem + x * 128 + i * 8, v + i * (2048 >> 4), pv, n > 0 || i > 0);
+            tc_mma_bf16_ts(tmem + 128 * L::kHalves + x * 128, tmem + x * 128 + i * 8, v + i * (2048 >> 4), pv, n % kPrHold > 0 || i > 0);
     };
     auto told = [&](uint64_t* bar, uint32_t parity) { return warp_wait_or_give_up(bar, parity, &sh.dead); };
     auto commit = [&](uint64_t* bar) {
@@ -507,6 +508,32 @@ __device__ __noinline__ void pr_by_hand(uint32_t o_tmem, uint32_t p_tmem, const 
     tmem_put_wait();
 }
 
+// The tensor cores cut a sum off at every 16 rows it takes in, so what it loses grows with the rows.  Every kPrHold tiles O and the
+// sum of probabilities of this thread's row therefore go to the row's place in the workspace, with the base that they were formed
+// with, and begin again at zero.  (Equal values in 16M rows: off by 16 % without.)
+template <int D>
+__device__ __noinline__ void pr_hold(uint32_t o_tmem, float* place, float2* stat, float m, float l, bool first) {
+    const float2 was = first ? make_float2(m, 0.f) : *stat;
+    const float w = was.y == 0.f ? 0.f : pr_exp2(was.x - m);
+    for (int d0 = 0; d0 < D; d0 += 32) {
+        uint32_t raw[32];
+        tmem_get32(o_tmem + d0, raw);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float4* at = reinterpret_cast<float4*>(place + d0) + i;
+            float4 x = make_float4(__uint_as_float(raw[4 * i]), __uint_as_float(raw[4 * i + 1]), __uint_as_float(raw[4 * i + 2]),
+                                   __uint_as_float(raw[4 * i + 3]));
+            if (w != 0.f) {
+                const float4 y = *at;
+                x = make_float4(fmaf(y.x, w, x.x), fmaf(y.y, w, x.y), fmaf(y.z, w, x.z), fmaf(y.w, w, x.w));
+            }
+            *at = x;
+        }
+        __syncwarp();
+    }
+    *stat = make_float2(m, fmaf(was.y, w, l));
+}
+
 // O of this thread's row *= w
 template <int D>
 __device__ __forceinline__ void pr_rescale(uint32_t o_tmem, float w) {
@@ -543,11 +570,18 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     const float none = falls ? CUDART_INF_F : -CUDART_INF_F;             // the product that scores -infinity
     float m = -CUDART_INF_F, l = 0.f;
     bool good = true;
+    // this row's place in the workspace: a part's always, another unit's where there may be more tiles than kPrHold
+    auto place = [&] { return (kParts ? blockIdx.y * static_cast<int64_t>(p.c.H) + blockIdx.x : blockIdx.x) * (L::kHalves * kPrHalf) + threadIdx.x; };
+    auto put_by = [&](bool first) {
+        pr_hold<D>(o_at, p.part + place() * D, p.part_stat + place(), m, l, first);
+        l = 0.f;
+    };
     for (int n = 0; n < tiles; ++n) {
         const int tile = u.tile(lo + n);
         good = warp_wait_or_give_up(&sh.s_full[half], n & 1, &sh.dead);
         if (!good) break;
         tc_fence_after();
+        if (n > 0 && n % kPrHold == 0) put_by(n == kPrHold);
         float x[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ask32(s_at + 32 * c, x[c]);
@@ -592,7 +626,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
             if (n > 0) pr_rescale<D>(o_at, w);
         }
         const float minus = m == -CUDART_INF_F ? 0.f : -(m + p.down_bits);
-        float2 sum[4] = {make_float2(l, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float2 scale2 = make_float2(scale, scale), minus2 = make_float2(minus, minus);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -613,13 +647,13 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
             tmem_put16(s_at + 16 * c, two);
         }
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-        l = sum[0].x + sum[0].y;
+        l += sum[0].x + sum[0].y;
         tmem_put_wait();
         if (!sh.whole[2].has(tile)) {
             const int s = n % L::kStages;
             good = warp_wait_or_give_up(&sh.v_ok[s], (n / L::kStages) & 1, &sh.dead);
             if (!good) break;
-            if (sh.is_wild(s)) pr_by_hand<D>(o_at, s_at, base + L::kV + s * L::kTileBytes, n == 0);
+            if (sh.is_wild(s)) pr_by_hand<D>(o_at, s_at, base + L::kV + s * L::kTileBytes, n % kPrHold == 0);
         }
         tc_fence_before();
         __syncwarp();
@@ -628,6 +662,11 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     if (good && tiles > 0) {
         good = warp_wait_or_give_up(&sh.o_full[half], 0, &sh.dead);
         tc_fence_after();
+    }
+    const bool held = good && tiles > kPrHold;
+    if (held) {
+        put_by(false);
+        l = p.part_stat[place()].y;
     }
     const bool live = r < p.tq * p.G && token < u.ntok;
     const int g = r % p.G;
@@ -641,9 +680,9 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     uint8_t* stage = base + L::kQ + half * L::kTileBytes + (r & ~31) * D * 2;
     auto put = [&](int row, int w) { return stage + row * D * 2 + (w ^ (row & 7)) * 16; };
     if constexpr (kParts) {
-        const int64_t rec = static_cast<int64_t>(blockIdx.y * p.c.H + blockIdx.x) * L::kHalves * kPrHalf + (threadIdx.x & ~31);
+        const int64_t rec = place() - lane;
         if (live) p.part_stat[rec + lane] = good ? make_float2(base2, l) : make_float2(0.f, CUDART_NAN_F);
-        if (!good || tiles <= 0 || !lives) return;
+        if (!good || tiles <= 0 || !lives || held) return;
 #pragma unroll 1
         for (int half_row = 0; half_row < D; half_row += D / 2) {
 #pragma unroll
@@ -671,7 +710,19 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
 #pragma unroll 1
         for (int d0 = 0; d0 < D; d0 += 32) {
             uint32_t o[32];
-            tmem_get32(o_at + d0, o);
+            if (held) {
+                const uint4* src = reinterpret_cast<const uint4*>(p.part + place() * D + d0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint4 w = src[i];
+                    o[4 * i] = w.x;
+                    o[4 * i + 1] = w.y;
+                    o[4 * i + 2] = w.z;
+                    o[4 * i + 3] = w.w;
+                }
+            } else {
+                tmem_get32(o_at + d0, o);
+            }
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 float x[8];

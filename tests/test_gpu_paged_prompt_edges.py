@@ -1,5 +1,6 @@
 """Prompts' attention where its kernels' forms end: heads that do not fill a tile, and what a caller may do that
 test_gpu_paged_prompt.py does not.  (Sizes and tolerances as there.)"""
+import math
 import os
 
 import pytest
@@ -79,3 +80,49 @@ def test_starts_that_fall_behind_a_longer_sequence_are_reported(lens, tokens):
             of = [b for b in range(2) if 0 <= start[b] <= t < start[b + 1] <= tokens]
             if not of:
                 assert (out[t] == 7).all()
+
+
+@pytest.mark.parametrize("tokens", [3, 2500])
+def test_sums_over_very_long_contexts(tokens):
+    """16M rows, whole units of 2500 tokens and parts of units of 3.  What the tensor cores cut off of a sum, 2^-22 at every 16 rows, is that of
+    131072 rows at most, 2^-9, however many there are; besides, as in test_gpu_paged_prompt.py, 2^-16 of the sums of
+    probabilities (which are all alike, and exact) and 2^-8 of the result's rounding."""
+    n, ps, d = 1 << 24, 1024, 64
+    k = torch.zeros((n // ps, 1, ps, d), dtype=torch.bfloat16, device="cuda")
+    c = (1 + torch.arange(d, device="cuda") / 64).to(torch.bfloat16)      # exact
+    v = c.expand(n // ps, 1, ps, d).contiguous()
+    q = torch.ones((tokens, 8, d), dtype=torch.bfloat16, device="cuda")
+    table = torch.randperm(n // ps, generator=torch.Generator().manual_seed(1)).to(torch.int32)[None].cuda()
+    out, lse = torch.empty_like(q), torch.empty((tokens, 8), device="cuda")
+    skv.paged_prompt_attention(q, k, v, table, i32([n]), i32([0, tokens]), out, lse)
+    off = ((out.double() - c.double()) / c.double()).abs().max().item()
+    assert off <= 2.0 ** -9 + 2.0 ** -16 + 2.0 ** -8, off
+    want = torch.log(torch.arange(n - tokens + 1, n + 1, device="cuda").double())
+    assert (lse.double() - want[:, None]).abs().max() <= 2.0 ** -16 + 2.0 ** -22 * math.log(n)
+    assert skv.paged_status() == 0
+
+
+@pytest.mark.parametrize("G,d,n,tokens,window,sink", [(8, 64, 600000, 2500, 0, 0), (2, 128, 300000, 20000, 200000, 300), (4, 128, 500000, 700, 0, 0)])
+def test_long_contexts_match_float64(G, d, n, tokens, window, sink):
+    ps = 64
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k, v = (torch.randn((-(-n // ps), 1, ps, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    v += 0.5
+    q = torch.randn((tokens, G, d), generator=g, device="cuda").bfloat16()
+    table = torch.randperm(k.shape[0], generator=g, device="cuda").to(torch.int32)[None]
+    out, lse = torch.empty_like(q), torch.empty((tokens, G), device="cuda")
+    skv.paged_prompt_attention(q, k, v, table, i32([n]), i32([0, tokens]), out, lse, window=window, sink=sink)
+    rows = [x[table[0].long()].view(-1, d)[:n].double() for x in (k, v)]
+    for t in (0, tokens // 2, tokens - 1):
+        r, j = n - tokens + t, torch.arange(n, device="cuda")
+        seen = (j <= r) & ((j > r - window) | (j < sink) if window else j >= 0)
+        z = torch.where(seen, q[t].double() @ rows[0].T / math.sqrt(d), -math.inf)
+        top = z.max(1, keepdim=True).values
+        p = torch.exp(z - top)
+        total = p.sum(1, keepdim=True)
+        want, size = p / total @ rows[1], p / total @ rows[1].abs()
+        delta = d * 2.0 ** -24 / math.sqrt(d) * (q[t].double().abs() @ rows[0].abs().T).max(1, keepdim=True).values
+        tol = (2 * delta + 2.0 ** -8 + 2.0 ** -16 + min(n, 131072) * 2.0 ** -26) * size + 2.0 ** -8 * want.abs()
+        assert ((out[t].double() - want).abs() <= tol).all()
+        assert ((lse[t].double() - (top + torch.log(total))[:, 0]).abs() <= delta[:, 0] + 2.0 ** -16 + 2.0 ** -22 * 20).all()
+    assert skv.paged_status() == 0
