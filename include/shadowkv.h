@@ -708,8 +708,8 @@ int shadowkv_paged_dequantise(const skv_paged_dequantise_args* args, skv_stream 
  *
  * Scores, sums and softmax statistics are fp32; probabilities are rounded to bf16 (2^-8 at most), and what is
  * 2^-88 below a row's heaviest may weigh nothing (an infinite value there gives NaN or is passed over).  Sums of values
- * are cut off at every 16 rows, by 2^-22 of what is there, for 131072 rows at most: in tables for more the workspace has
- * 4 (d + 2) bytes for every token and query head besides, where sums are put by.  Keys that score -infinity count as absent.  Where a kernel's bounded wait ran
+ * are cut off at every 16 rows, by 2^-22 of what is there, for 131072 rows at most: then they are put by, in the workspace or in a
+ * fixed array of the library's (21 MB, a place for each CTA while it runs).  Keys that score -infinity count as absent.  Where a kernel's bounded wait ran
  * out (shadowkv_paged_status: SKV_ERR_TIMEOUT) results are NaN.
  */
 typedef struct {

@@ -52,7 +52,7 @@ constexpr int kPrTile = 128;                   // rows of a tile of keys
 constexpr int kPrHalf = 128;                   // query rows of an accumulator
 constexpr float kPrSlack = 8.f;                // the base moves when a score passes it by 2^8
 constexpr int kPrStages = 2;                   // tiles of keys, and of values, on their way or in use, at most
-static_assert((kPrHold & (kPrHold - 1)) == 0, "");
+constexpr int kPrHold = 1024;                  // tiles after which sums are put by, a power of two
 constexpr int kPrMaxSlots = 160;               // places for units that are taken in parts
 constexpr int kPrMaxParts = 64;                // of a unit
 
@@ -317,6 +317,8 @@ struct PrShared {
     uint32_t tmem;
     int dead;
     int2 begun;                // tiles whose keys (x) and values (y) were asked for
+    int again;                 // O begins again at tiles n with (n & again) == 0
+    int place[2];              // of g_put_by, for either half; -1: none
     int absent[4];             // per tile (mod 4): groups of eight rows whose page is out of range or not looked at
     int wild[kPrStages][2];    // a tile at an edge has values that are not finite (what each of the two warps found)
     uint64_t given_up;         // the products that were under way
@@ -326,8 +328,30 @@ struct PrShared {
     }
 };
 
+// Where sums of whole units are put by: two places for every SM, a CTA of two halves or two CTAs of one.
+constexpr int kPrPlaces = 2 * 160;
+static __device__ float g_put_by[kPrPlaces][kPrHalf * 128];
+static __device__ float2 g_put_by_stat[kPrPlaces][kPrHalf];
+static __device__ int g_in_use[kPrPlaces];
+
 // ------------------------------------------------------------------ the roles
 
+// By one thread: a place for each half.  Were there none within the limit, sums would run on.
+__device__ __noinline__ void pr_take_places(PrShared& sh, int halves) {
+    uint32_t sm;
+    asm volatile("mov.u32 %0, %%smid;" : "=r"(sm));
+    const unsigned long long since = globaltimer();
+    for (int x = 0; x < halves; ++x)
+        for (int i = 2 * sm; sh.place[x] < 0; ++i) {
+            if (atomicCAS(g_in_use + i % kPrPlaces, 0, 1) == 0) sh.place[x] = i % kPrPlaces;
+            else if (globaltimer() - since > kWaitLimitNs) {
+                set_err(g_err, DEV_ERR_TIMEOUT, 916);
+                sh.again = INT32_MAX;
+                return;
+            }
+        }
+    __threadfence();
+}
 // By one thread, of the warp that loads the rest.
 template <int D, class L>
 __device__ __forceinline__ void pr_load_queries(const PromptParams& p, const CUtensorMap* mq, PrShared& sh, const PrUnit& u, uint8_t* base) {
@@ -390,7 +414,7 @@ __device__ void pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) 
     const PrUnit u = sh.unit;
     const PrWhole calm = sh.whole[2];
     const uint32_t at = smem_u32(base), tmem = sh.tmem;
-    const int halves = u.ntok > p.tq ? 2 : 1, tiles = u.hi - u.lo;
+    const int halves = u.ntok > p.tq ? 2 : 1, tiles = u.hi - u.lo, again = sh.again;
     if (tiles <= 0) return;
     constexpr uint32_t qk = idesc_bf16_f32(kPrHalf, kPrTile), pv = idesc_bf16_f32(kPrHalf, D) | kBIsMN;
     // The whole warp comes this way and one thread of it issues: operands that are the warp's stay in uniform
@@ -412,7 +436,7 @@ __device__ void pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) 
         if (!mine) return;
 #pragma unroll
         for (int i = 0; i < kPrTile / 16; ++i)
-            tc_mma_bf16_ts(tmem + 128 * L::kHalves + x * 128, tmem + x * 128 + i * 8, v + i * (2048 >> 4), pv, n % kPrHold > 0 || i > 0);
+            tc_mma_bf16_ts(tmem + 128 * L::kHalves + x * 128, tmem + x * 128 + i * 8, v + i * (2048 >> 4), pv, (n & again) > 0 || i > 0);
     };
     auto told = [&](uint64_t* bar, uint32_t parity) { return warp_wait_or_give_up(bar, parity, &sh.dead); };
     auto commit = [&](uint64_t* bar) {
@@ -509,8 +533,9 @@ __device__ __noinline__ void pr_by_hand(uint32_t o_tmem, uint32_t p_tmem, const 
 }
 
 // The tensor cores cut a sum off at every 16 rows it takes in, so what it loses grows with the rows.  Every kPrHold tiles O and the
-// sum of probabilities of this thread's row therefore go to the row's place in the workspace, with the base that they were formed
-// with, and begin again at zero.  (Equal values in 16M rows: off by 16 % without.)
+// sum of probabilities of this thread's row are therefore put by, with the base that they were formed with, and begin again at
+// zero.  (Equal values in 16M rows: off by 16 % without.)  A part of a unit has its place in the workspace for that, and a whole
+// unit takes one of g_put_by while it runs: there are as many as CTAs of either form can be on the device.
 template <int D>
 __device__ __noinline__ void pr_hold(uint32_t o_tmem, float* place, float2* stat, float m, float l, bool first) {
     const float2 was = first ? make_float2(m, 0.f) : *stat;
@@ -570,10 +595,12 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     const float none = falls ? CUDART_INF_F : -CUDART_INF_F;             // the product that scores -infinity
     float m = -CUDART_INF_F, l = 0.f;
     bool good = true;
-    // this row's place in the workspace: a part's always, another unit's where there may be more tiles than kPrHold
-    auto place = [&] { return (kParts ? blockIdx.y * static_cast<int64_t>(p.c.H) + blockIdx.x : blockIdx.x) * (L::kHalves * kPrHalf) + threadIdx.x; };
+    // this row's place among the parts, and where its sums are put by
+    auto record = [&] { return static_cast<int64_t>(blockIdx.y * p.c.H + blockIdx.x) * (L::kHalves * kPrHalf) + threadIdx.x; };
+    auto sums = [&] { return kParts ? p.part + record() * D : g_put_by[sh.place[half]] + r * D; };
+    auto sums_stat = [&] { return kParts ? p.part_stat + record() : g_put_by_stat[sh.place[half]] + r; };
     auto put_by = [&](bool first) {
-        pr_hold<D>(o_at, p.part + place() * D, p.part_stat + place(), m, l, first);
+        pr_hold<D>(o_at, sums(), sums_stat(), m, l, first);
         l = 0.f;
     };
     for (int n = 0; n < tiles; ++n) {
@@ -581,7 +608,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
         good = warp_wait_or_give_up(&sh.s_full[half], n & 1, &sh.dead);
         if (!good) break;
         tc_fence_after();
-        if (n > 0 && n % kPrHold == 0) put_by(n == kPrHold);
+        if (n > 0 && (n & sh.again) == 0) put_by(n == kPrHold);
         float x[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ask32(s_at + 32 * c, x[c]);
@@ -653,7 +680,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
             const int s = n % L::kStages;
             good = warp_wait_or_give_up(&sh.v_ok[s], (n / L::kStages) & 1, &sh.dead);
             if (!good) break;
-            if (sh.is_wild(s)) pr_by_hand<D>(o_at, s_at, base + L::kV + s * L::kTileBytes, n % kPrHold == 0);
+            if (sh.is_wild(s)) pr_by_hand<D>(o_at, s_at, base + L::kV + s * L::kTileBytes, (n & sh.again) == 0);
         }
         tc_fence_before();
         __syncwarp();
@@ -663,10 +690,10 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
         good = warp_wait_or_give_up(&sh.o_full[half], 0, &sh.dead);
         tc_fence_after();
     }
-    const bool held = good && tiles > kPrHold;
+    const bool held = good && tiles > kPrHold && sh.again < tiles;
     if (held) {
         put_by(false);
-        l = p.part_stat[place()].y;
+        l = sums_stat()->y;
     }
     const bool live = r < p.tq * p.G && token < u.ntok;
     const int g = r % p.G;
@@ -680,7 +707,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     uint8_t* stage = base + L::kQ + half * L::kTileBytes + (r & ~31) * D * 2;
     auto put = [&](int row, int w) { return stage + row * D * 2 + (w ^ (row & 7)) * 16; };
     if constexpr (kParts) {
-        const int64_t rec = place() - lane;
+        const int64_t rec = record() - lane;
         if (live) p.part_stat[rec + lane] = good ? make_float2(base2, l) : make_float2(0.f, CUDART_NAN_F);
         if (!good || tiles <= 0 || !lives || held) return;
 #pragma unroll 1
@@ -711,7 +738,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
         for (int d0 = 0; d0 < D; d0 += 32) {
             uint32_t o[32];
             if (held) {
-                const uint4* src = reinterpret_cast<const uint4*>(p.part + place() * D + d0);
+                const uint4* src = reinterpret_cast<const uint4*>(sums() + d0);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint4 w = src[i];
@@ -794,6 +821,9 @@ __global__ void __launch_bounds__(PrForm<D, kHalves>::kThreads, PrForm<D, kHalve
         }
         if (lane == 0) {
             if (u.lo < u.hi) pr_load_queries<D, L>(p, &mq, sh, u, base);
+            sh.again = kPrHold - 1;
+            sh.place[0] = sh.place[1] = -1;
+            if (!kParts && u.hi - u.lo > kPrHold) pr_take_places(sh, u.ntok > p.tq ? 2 : 1);
             sh.unit = u;
             for (int x = 0; x < 3; ++x) sh.whole[x] = whole(sees(p, u, x));
         }
@@ -844,6 +874,10 @@ __global__ void __launch_bounds__(PrForm<D, kHalves>::kThreads, PrForm<D, kHalve
             wait_out(&sh.given_up, 0, since);
         }
         __syncwarp();
+    }
+    if (!kParts && threadIdx.x < 2 && sh.place[threadIdx.x] >= 0) {
+        __threadfence();
+        atomicExch(g_in_use + sh.place[threadIdx.x], 0);
     }
     if (warp == L::kSoft + 1) {
         tc_fence_after();

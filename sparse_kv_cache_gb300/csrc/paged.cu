@@ -277,9 +277,7 @@ int prompt_space(const skv_paged_prompt_args* a, PromptSpace* w) {
     const int64_t all = (static_cast<int64_t>(c.max_pages) * c.page_size + 127) / 128;
     w->tiles = a->window ? std::min<int64_t>(all, (static_cast<int64_t>(a->sink) + 127) / 128 + (static_cast<int64_t>(a->window) + 256) / 128 + 2) : all;
     const PromptPlan plan = prompt_plan(a->tokens, c.batch, G, c.n_kv_heads, w->tiles, kMaxSms);
-    if (plan.slots * c.n_kv_heads > INT32_MAX) return SKV_ERR_INVALID;
-    // records of parts, or of whole units that may have to put sums by (fewer SMs mean fewer parts, to none: at most as many records)
-    const int64_t rows = (plan.parts ? plan.parts : w->tiles > kPrHold ? plan.slots : 0) * c.n_kv_heads * plan.halves * 128;
+    const int64_t rows = static_cast<int64_t>(plan.parts) * c.n_kv_heads * plan.halves * 128;
     w->stat = rows * c.head_dim * 4;
     w->note = w->stat + rows * 8;
     w->bytes = w->note + (plan.parts ? plan.slots * 16 : 0);
@@ -582,6 +580,7 @@ int shadowkv_paged_prompt_attention(const skv_paged_prompt_args* a, skv_stream s
     p.c.sink = static_cast<int>(std::min<int64_t>(a->sink, kMaxRows));
     p.G = G; p.n_q = a->n_q_heads; p.tokens = a->tokens; p.tq = tq;
     const PromptPlan plan = prompt_plan(a->tokens, c.batch, G, c.n_kv_heads, w.tiles, dev.nsm < kMaxSms ? dev.nsm : kMaxSms);
+    if (plan.slots * c.n_kv_heads > INT32_MAX) return SKV_ERR_INVALID;
     p.halves = plan.halves; p.unit_tokens = plan.halves * tq; p.parts = plan.parts; p.slots = plan.slots;
     p.scale_log2 = static_cast<float>((a->scale != 0.f ? static_cast<double>(a->scale) : 1.0 / std::sqrt(double(c.head_dim))) *
                                       1.4426950408889634074);

@@ -99,12 +99,11 @@ struct PromptParams {
     int64_t o_tok, o_head;
     const int32_t* start;
     void* out; float* lse;
-    float* part;              // [parts or slots][H][halves * 128][d]: sums of parts, or those put by, unnormalised
-    float2* part_stat;        // [parts or slots][H][halves * 128]: their bases and sums of probabilities
+    float* part;              // [parts][H][halves * 128][d]: parts of sums, unnormalised
+    float2* part_stat;        // [parts][H][halves * 128]: their bases and sums of probabilities
     int4* note;               // [slots]: first part, parts, first token, tokens
 };
 struct PromptPlan { int halves, parts; int64_t slots; };
-constexpr int kPrHold = 1024;      // tiles of 128 rows after which sums are put by
 PromptPlan prompt_plan(int tokens, int batch, int G, int H, int64_t tiles, int nsm);      // tiles that a unit can see
 int launch_prompt_attn(int d, const PromptParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s);
 

@@ -126,3 +126,22 @@ def test_long_contexts_match_float64(G, d, n, tokens, window, sink):
         assert ((out[t].double() - want).abs() <= tol).all()
         assert ((lse[t].double() - (top + torch.log(total))[:, 0]).abs() <= delta[:, 0] + 2.0 ** -16 + 2.0 ** -22 * 20).all()
     assert skv.paged_status() == 0
+
+
+def test_very_long_contexts_on_two_streams_give_the_same_bits():
+    n, ps, d, tokens = 400000, 64, 64, [2500, 4000]
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k, v = (torch.randn((n // ps, 1, ps, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    table, lens = torch.arange(n // ps, dtype=torch.int32, device="cuda")[None], i32([n])
+    qs = [torch.randn((t, 8, d), generator=g, device="cuda").bfloat16() for t in tokens]
+    starts = [i32([0, t]) for t in tokens]
+    want = [skv.paged_prompt_attention(q, k, v, table, lens, s, torch.empty_like(q)) for q, s in zip(qs, starts)]
+    streams = [torch.cuda.Stream() for _ in tokens]
+    got = [[torch.empty_like(q) for _ in range(4)] for q in qs]
+    torch.cuda.synchronize()
+    for i in range(4):
+        for j, st in enumerate(streams):
+            skv.paged_prompt_attention(qs[j], k, v, table, lens, starts[j], got[j][i], stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, w) for x, w in zip(got[0] + got[1], [want[0]] * 4 + [want[1]] * 4))
+    assert skv.paged_status() == 0
