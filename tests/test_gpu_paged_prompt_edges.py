@@ -145,3 +145,24 @@ def test_very_long_contexts_on_two_streams_give_the_same_bits():
     torch.cuda.synchronize()
     assert all(torch.equal(x, w) for x, w in zip(got[0] + got[1], [want[0]] * 4 + [want[1]] * 4))
     assert skv.paged_status() == 0
+
+
+def test_handed_in_streams_give_the_same_bits():
+    """Calls on two streams that were handed in, side by side: parts have a workspace of their own on each."""
+    c = Paged("bf16", [5000, 500, 0, 3000], 2, 128, 16, seed=18)
+    tokens = [[3, 200, 0, 1], [1, 1, 0, 7]]
+    qs = [ask(c, 4, t, 19 + i) for i, t in enumerate(tokens)]
+    starts = [i32([0, *torch.tensor(t).cumsum(0).tolist()]) for t in tokens]
+    want = [attend(c, q, t) for q, t in zip(qs, tokens)]
+    for q, t, w in zip(qs, tokens, want):
+        check_all(c, t, q, *w)
+    got = [[(torch.full_like(q, math.nan), torch.full(q.shape[:2], math.nan, device="cuda")) for _ in range(6)] for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    for i in range(6):
+        for j, s in enumerate(streams):
+            skv.paged_prompt_attention(qs[j], c.k, c.v, c.table, c.lens, starts[j], *got[j][i], stream=s if i % 2 else s.cuda_stream)
+    torch.cuda.synchronize()
+    for j in range(2):
+        assert all(torch.equal(o, want[j][0]) and torch.equal(s, want[j][1]) for o, s in got[j])
+    assert skv.paged_status() == 0
