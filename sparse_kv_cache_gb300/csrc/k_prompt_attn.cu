@@ -56,11 +56,6 @@ constexpr int kPrHold = 1024;                  // tiles after which sums are put
 constexpr int kPrMaxSlots = 160;               // places for units that are taken in parts
 constexpr int kPrMaxParts = 64;                // of a unit
 
-__device__ __forceinline__ float pr_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // One thread of the warp, always the same.
 __device__ __forceinline__ bool elect_one() {
     uint32_t is;
@@ -539,7 +534,7 @@ __device__ __noinline__ void pr_by_hand(uint32_t o_tmem, uint32_t p_tmem, const 
 template <int D>
 __device__ __noinline__ void pr_hold(uint32_t o_tmem, float* place, float2* stat, float m, float l, bool first) {
     const float2 was = first ? make_float2(m, 0.f) : *stat;
-    const float w = was.y == 0.f ? 0.f : pr_exp2(was.x - m);
+    const float w = was.y == 0.f ? 0.f : exp2_fast(was.x - m);
     for (int d0 = 0; d0 < D; d0 += 32) {
         uint32_t raw[32];
         tmem_get32(o_tmem + d0, raw);
@@ -647,7 +642,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
         }
         if (__any_sync(0xffffffffu, top[0] > m + kPrSlack)) {
             const float now = fmaxf(m, top[0]);
-            const float w = m == -CUDART_INF_F ? 0.f : pr_exp2(m - now);
+            const float w = m == -CUDART_INF_F ? 0.f : exp2_fast(m - now);
             m = now;
             l *= w;
             if (n > 0) pr_rescale<D>(o_at, w);
@@ -664,7 +659,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
                 x[c][i + 1] = e.y;
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[c][i] = pr_exp2(x[c][i]);
+            for (int i = 0; i < 32; ++i) x[c][i] = exp2_fast(x[c][i]);
             uint32_t two[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -912,7 +907,7 @@ __global__ void __launch_bounds__(256) k_prompt_merge(const __grid_constant__ Pr
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             // (a sum of zero: this part sees nothing; NaN is the row's, or that of a wait that ran out)
-            w[k] = st[k].y == 0.f ? 0.f : st[k].y != st[k].y ? CUDART_NAN_F : pr_exp2(st[k].x - m);
+            w[k] = st[k].y == 0.f ? 0.f : st[k].y != st[k].y ? CUDART_NAN_F : exp2_fast(st[k].x - m);
             if (w[k] != 0.f) l = fmaf(st[k].y, w[k], l);
         }
         l = warp_sum(l);

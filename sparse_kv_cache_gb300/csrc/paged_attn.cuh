@@ -54,11 +54,6 @@ constexpr float kPaSlack = 8.f;                   // the base moves when a score
 // largest value, which may be the type's.  (Of a table for 128K rows, 2^-25: products of values below 2^-101
 // lose bits at fp32's smallest.  In the exponent it would cost all probabilities 2^-20 of themselves.)
 
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // 16 or 8 bytes read once (not kept in L1), zeros where `in` is false
 __device__ __forceinline__ uint4 ld_stream(const void* p, bool in) {
     uint4 v;
@@ -608,42 +603,31 @@ struct TileTC {
     __device__ __forceinline__ static bool takes_part(const PagedAttnParams& p, const Piece& at, int row, int i, int id) {
         return id >= 0 && row + i < at.end && seen<kSpan>(p.c, real_row<kSpan>(p.c, row, at.n) + i, at.n);
     }
-    static constexpr int kKeyBytes = kE4M3 ? 1 : 2, kValueBytes = kHolds != Holds::kBf16 ? 1 : 2;
+    static constexpr int kValueBytes = kE5M2 ? 1 : 2;      // as load_v() sees them
     __device__ __forceinline__ void load_k(const PagedAttnParams& p, const Piece& at, int row, const Ids& id, Keys& k) {
         const int r = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3, mask = (1 << p.c.lg) - 1;
         const int real = real_row<kSpan>(p.c, row, at.n);
         if constexpr (kSpan) {
             if (id.all) {
-                const uint8_t* a = static_cast<const uint8_t*>(p.c.k) + c * 16 +
-                                   (at.h * p.c.k_head + id.a * p.c.k_page + ((real & mask) + r) * p.c.k_row) * kKeyBytes;
-                const uint8_t* b = a + 8 * kKeyBytes * p.c.k_row;
+                const __nv_bfloat16* a = static_cast<const __nv_bfloat16*>(p.c.k) + c * 8 +
+                                         (at.h * p.c.k_head + id.a * p.c.k_page + ((real & mask) + r) * p.c.k_row);
+                const __nv_bfloat16* b = a + 8 * p.c.k_row;
 #pragma unroll
                 for (int j = 0; j < kKV; ++j) {
-                    k.a[j] = ld_row(a + 64 * j);
-                    k.b[j] = ld_row(b + 64 * j);
+                    k.a[j] = ld_row(a + 32 * j);
+                    k.b[j] = ld_row(b + 32 * j);
                 }
                 return;
             }
         }
         const bool ia = takes_part(p, at, row, r, id.a), ib = takes_part(p, at, row, 8 + r, id.b);
-        if constexpr (kE4M3) {
-            const uint8_t* base = static_cast<const uint8_t*>(p.c.k) + at.h * p.c.k_head + c * 16;
-            const uint8_t* pa = base + id.a * p.c.k_page + ((real + r) & mask) * p.c.k_row;
-            const uint8_t* pb = base + id.b * p.c.k_page + ((real + 8 + r) & mask) * p.c.k_row;
+        const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(p.c.k) + at.h * p.c.k_head + c * 8;
+        const __nv_bfloat16* pa = base + id.a * p.c.k_page + ((real + r) & mask) * p.c.k_row;
+        const __nv_bfloat16* pb = base + id.b * p.c.k_page + ((real + 8 + r) & mask) * p.c.k_row;
 #pragma unroll
-            for (int j = 0; j < kKV; ++j) {
-                k.a[j] = ld_stream(pa + 64 * j, ia);
-                k.b[j] = ld_stream(pb + 64 * j, ib);
-            }
-        } else {
-            const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(p.c.k) + at.h * p.c.k_head + c * 8;
-            const __nv_bfloat16* pa = base + id.a * p.c.k_page + ((real + r) & mask) * p.c.k_row;
-            const __nv_bfloat16* pb = base + id.b * p.c.k_page + ((real + 8 + r) & mask) * p.c.k_row;
-#pragma unroll
-            for (int j = 0; j < kKV; ++j) {
-                k.a[j] = ld_stream(pa + 32 * j, ia);
-                k.b[j] = ld_stream(pb + 32 * j, ib);
-            }
+        for (int j = 0; j < kKV; ++j) {
+            k.a[j] = ld_stream(pa + 32 * j, ia);
+            k.b[j] = ld_stream(pb + 32 * j, ib);
         }
     }
     __device__ __forceinline__ void load_v(const PagedAttnParams& p, const Piece& at, int row, const Ids& ids, Values& v) {
@@ -652,19 +636,19 @@ struct TileTC {
         if constexpr (kSpan) {
             if (ids.all) {
                 const int64_t step = p.c.v_row * kValueBytes;
-                const uint8_t* x = static_cast<const uint8_t*>(p.c.v) + r * (kHolds != Holds::kBf16 ? D / 8 : 16) +
+                const uint8_t* x = static_cast<const uint8_t*>(p.c.v) + r * (kE5M2 ? D / 8 : 16) +
                                    (h * p.c.v_head + ids.a * p.c.v_page + ((real & mask) + 2 * c) * p.c.v_row) * kValueBytes;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint8_t* src = x + (i & 1) * step + (i >> 1) * 8 * step;
 #pragma unroll
                     for (int j = 0; j < kVV; ++j)
-                        v.v[i][j] = kHolds != Holds::kBf16 && D == 64 ? ld_row8(src) : ld_row(src + 128 * j);
+                        v.v[i][j] = kE5M2 && D == 64 ? ld_row8(src) : ld_row(src + 128 * j);
                 }
                 return;
             }
         }
-        constexpr int es = kHolds != Holds::kBf16 ? 1 : 2, lane_bytes = kHolds != Holds::kBf16 ? D / 8 : 16;
+        constexpr int es = kE5M2 ? 1 : 2, lane_bytes = kE5M2 ? D / 8 : 16;
         const uint8_t* base = static_cast<const uint8_t*>(p.c.v) + h * p.c.v_head * es + r * lane_bytes;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -673,7 +657,7 @@ struct TileTC {
             const bool in = takes_part(p, at, row, t, id);
 #pragma unroll
             for (int j = 0; j < kVV; ++j) {
-                if (kHolds != Holds::kBf16 && D == 64) {
+                if (kE5M2 && D == 64) {
                     const uint2 x = ld_stream8(src, in);
                     v.v[i][j] = make_uint4(x.x, x.y, 0, 0);
                 } else {
@@ -1013,7 +997,7 @@ struct TileTC {
         }
     }
     __device__ __forceinline__ static void clear(Values& v, int i) { v.v[i][0] = make_uint4(0, 0, 0, 0); }
-    // The same as stream() below, with kRing tiles in shared memory: the copies go through the pieces by themselves,
+    // The same as stream_registers() below, with kRing tiles in shared memory: the copies go through the pieces by themselves,
     // ahead of the products, and leave a note of each tile beside its slot.  A copy brings whole tiles (zeros for a page
     // that is not followed); rows that take no part are dropped on the way to the products.
     struct Note { Piece at; int last, more; };         // a tile: its place, whether it ends its piece, whether one follows
@@ -1201,10 +1185,11 @@ struct TileTC {
     template <class Keep, class Hold, class Next, class Done>
     __device__ __forceinline__ void stream(const Params& p, Piece cur, void* ring, Keep z, Hold put_by, Next next,
                                            Done done) {
-        if constexpr (kE4M3) {
-            stream_ring(p, cur, ring, put_by, next, done);
-            return;
-        }
+        if constexpr (kE4M3) stream_ring(p, cur, ring, put_by, next, done);
+        else stream_registers(p, cur, z, put_by, next, done);
+    }
+    template <class Keep, class Hold, class Next, class Done>
+    __device__ __forceinline__ void stream_registers(const Params& p, Piece cur, Keep z, Hold put_by, Next next, Done done) {
         Piece then;
         bool more = next(then);
         Ids ids = cur.ids, later = ids;
@@ -1647,7 +1632,8 @@ __global__ void __launch_bounds__(kPaThreads, kOcc) k_paged_cluster(const __grid
         piece.ids = piece.ask(p, piece_row);
         void* queries = Tile::kRing ? own_memory<Tile>(s_z, warp) : js.o[2 * warp + 1][0];
         auto none = [](Piece&) { return false; };
-        // (at most kOneWaveTiles tiles: none of them fills a row of page ids)
+        // (At most kOneWaveTiles tiles, or kCodeTiles of codes.  Sums that are not held lose 2^-22 at every tile at most, so
+        // 2^-16.7 in 40, to a result that is rounded by 2^-9.)
         if constexpr (kKeep) tile.stream(p, piece, queries, KeepShared{my_z, piece.row, p.Gp}, HoldNone{}, none, hand_over);
         else tile.stream(p, piece, queries, KeepNone{}, HoldNone{}, none, hand_over);
     } else {

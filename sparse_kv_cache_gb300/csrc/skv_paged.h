@@ -163,6 +163,12 @@ inline cudaError_t launch_first(void (*k)(KArgs...), dim3 grid, int block, size_
     }
     return cudaLaunchKernelEx(&cfg, k, static_cast<Args&&>(args)...);
 }
+// 2^x, 0 for results below 2^-126
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // A wait for a barrier's phase that ends after about a second, or once *dead is set; false then, and *dead is.  One
 // statement: with a way out for some threads of a warp alone the compiler keeps what is the warp's in registers of
 // each thread behind it (a prompt of 32K tokens: 6.5 ms against 6.3).  The answer is the thread's: each
