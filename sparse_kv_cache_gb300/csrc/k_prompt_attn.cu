@@ -312,7 +312,6 @@ struct PrShared {
     uint32_t tmem;
     int dead;
     int2 begun;                // tiles whose keys (x) and values (y) were asked for
-    int again;                 // O begins again at tiles n with (n & again) == 0
     int place[2];              // of g_put_by, for either half; -1: none
     int absent[4];             // per tile (mod 4): groups of eight rows whose page is out of range or not looked at
     int wild[kPrStages][2];    // a tile at an edge has values that are not finite (what each of the two warps found)
@@ -325,13 +324,13 @@ struct PrShared {
 
 // Where sums of whole units are put by: two places for every SM, a CTA of two halves or two CTAs of one.
 constexpr int kPrPlaces = 2 * 160;
-static __device__ float g_put_by[kPrPlaces][kPrHalf * 128];
-static __device__ float2 g_put_by_stat[kPrPlaces][kPrHalf];
+static __device__ float g_put_by[kPrPlaces * kPrHalf * 128];
+static __device__ float2 g_put_by_stat[kPrPlaces * kPrHalf];
 static __device__ int g_in_use[kPrPlaces];
 
 // ------------------------------------------------------------------ the roles
 
-// By one thread: a place for each half.  Were there none within the limit, sums would run on.
+// By one thread: a place for each half, or -1 where there is none within the limit, and the unit's results are NaN.
 __device__ __noinline__ void pr_take_places(PrShared& sh, int halves) {
     uint32_t sm;
     asm volatile("mov.u32 %0, %%smid;" : "=r"(sm));
@@ -340,8 +339,6 @@ __device__ __noinline__ void pr_take_places(PrShared& sh, int halves) {
         for (int i = 2 * sm; sh.place[x] < 0; ++i) {
             if (atomicCAS(g_in_use + i % kPrPlaces, 0, 1) == 0) sh.place[x] = i % kPrPlaces;
             else if (globaltimer() - since > kWaitLimitNs) {
-                set_err(g_err, DEV_ERR_TIMEOUT, 916);
-                sh.again = INT32_MAX;
                 return;
             }
         }
@@ -409,7 +406,7 @@ __device__ void pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) 
     const PrUnit u = sh.unit;
     const PrWhole calm = sh.whole[2];
     const uint32_t at = smem_u32(base), tmem = sh.tmem;
-    const int halves = u.ntok > p.tq ? 2 : 1, tiles = u.hi - u.lo, again = sh.again;
+    const int halves = u.ntok > p.tq ? 2 : 1, tiles = u.hi - u.lo;
     if (tiles <= 0) return;
     constexpr uint32_t qk = idesc_bf16_f32(kPrHalf, kPrTile), pv = idesc_bf16_f32(kPrHalf, D) | kBIsMN;
     // The whole warp comes this way and one thread of it issues: operands that are the warp's stay in uniform
@@ -431,7 +428,7 @@ __device__ void pr_multiply(const PromptParams& p, PrShared& sh, uint8_t* base) 
         if (!mine) return;
 #pragma unroll
         for (int i = 0; i < kPrTile / 16; ++i)
-            tc_mma_bf16_ts(tmem + 128 * L::kHalves + x * 128, tmem + x * 128 + i * 8, v + i * (2048 >> 4), pv, (n & again) > 0 || i > 0);
+            tc_mma_bf16_ts(tmem + 128 * L::kHalves + x * 128, tmem + x * 128 + i * 8, v + i * (2048 >> 4), pv, n % kPrHold > 0 || i > 0);
     };
     auto told = [&](uint64_t* bar, uint32_t parity) { return warp_wait_or_give_up(bar, parity, &sh.dead); };
     auto commit = [&](uint64_t* bar) {
@@ -531,27 +528,38 @@ __device__ __noinline__ void pr_by_hand(uint32_t o_tmem, uint32_t p_tmem, const 
 // sum of probabilities of this thread's row are therefore put by, with the base that they were formed with, and begin again at
 // zero.  (Equal values in 16M rows: off by 16 % without.)  A part of a unit has its place in the workspace for that, and a whole
 // unit takes one of g_put_by while it runs: there are as many as CTAs of either form can be on the device.
+// The last time they go back to O instead.  Returns the sum of probabilities.
+enum class PrHold { kFirst, kNext, kLast };
 template <int D>
-__device__ __noinline__ void pr_hold(uint32_t o_tmem, float* place, float2* stat, float m, float l, bool first) {
-    const float2 was = first ? make_float2(m, 0.f) : *stat;
+__device__ __noinline__ float pr_hold(uint32_t o_tmem, float* place, float2* stat, float m, float l, PrHold time) {
+    const float2 was = time == PrHold::kFirst ? make_float2(m, 0.f) : *stat;
     const float w = was.y == 0.f ? 0.f : exp2_fast(was.x - m);
     for (int d0 = 0; d0 < D; d0 += 32) {
         uint32_t raw[32];
         tmem_get32(o_tmem + d0, raw);
+        if (w != 0.f) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float4* at = reinterpret_cast<float4*>(place + d0) + i;
-            float4 x = make_float4(__uint_as_float(raw[4 * i]), __uint_as_float(raw[4 * i + 1]), __uint_as_float(raw[4 * i + 2]),
-                                   __uint_as_float(raw[4 * i + 3]));
-            if (w != 0.f) {
-                const float4 y = *at;
-                x = make_float4(fmaf(y.x, w, x.x), fmaf(y.y, w, x.y), fmaf(y.z, w, x.z), fmaf(y.w, w, x.w));
+            for (int i = 0; i < 8; ++i) {
+                const float4 y = reinterpret_cast<const float4*>(place + d0)[i];
+                raw[4 * i] = __float_as_uint(fmaf(y.x, w, __uint_as_float(raw[4 * i])));
+                raw[4 * i + 1] = __float_as_uint(fmaf(y.y, w, __uint_as_float(raw[4 * i + 1])));
+                raw[4 * i + 2] = __float_as_uint(fmaf(y.z, w, __uint_as_float(raw[4 * i + 2])));
+                raw[4 * i + 3] = __float_as_uint(fmaf(y.w, w, __uint_as_float(raw[4 * i + 3])));
             }
-            *at = x;
         }
         __syncwarp();
+        if (time == PrHold::kLast) {
+            tmem_put32(o_tmem + d0, raw);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                reinterpret_cast<uint4*>(place + d0)[i] = make_uint4(raw[4 * i], raw[4 * i + 1], raw[4 * i + 2], raw[4 * i + 3]);
+        }
     }
-    *stat = make_float2(m, fmaf(was.y, w, l));
+    tmem_put_wait();
+    l = fmaf(was.y, w, l);
+    *stat = make_float2(m, l);
+    return l;
 }
 
 // O of this thread's row *= w
@@ -590,20 +598,26 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     const float none = falls ? CUDART_INF_F : -CUDART_INF_F;             // the product that scores -infinity
     float m = -CUDART_INF_F, l = 0.f;
     bool good = true;
-    // this row's place among the parts, and where its sums are put by
-    auto record = [&] { return static_cast<int64_t>(blockIdx.y * p.c.H + blockIdx.x) * (L::kHalves * kPrHalf) + threadIdx.x; };
-    auto sums = [&] { return kParts ? p.part + record() * D : g_put_by[sh.place[half]] + r * D; };
-    auto sums_stat = [&] { return kParts ? p.part_stat + record() : g_put_by_stat[sh.place[half]] + r; };
-    auto put_by = [&](bool first) {
-        pr_hold<D>(o_at, sums(), sums_stat(), m, l, first);
-        l = 0.f;
+    // this row's place where sums are put by
+    auto put_by = [&](PrHold time) {
+        const int64_t at = kParts ? static_cast<int64_t>(blockIdx.y * p.c.H + blockIdx.x) * (L::kHalves * kPrHalf) + threadIdx.x
+                                  : static_cast<int64_t>(sh.place[half]) * kPrHalf + r;
+        return pr_hold<D>(o_at, (kParts ? p.part : g_put_by) + at * D, (kParts ? p.part_stat : g_put_by_stat) + at, m, l, time);
     };
     for (int n = 0; n < tiles; ++n) {
         const int tile = u.tile(lo + n);
         good = warp_wait_or_give_up(&sh.s_full[half], n & 1, &sh.dead);
         if (!good) break;
         tc_fence_after();
-        if (n > 0 && (n & sh.again) == 0) put_by(n == kPrHold);
+        if (n > 0 && n % kPrHold == 0) {
+            if (!kParts && sh.place[half] < 0) {
+                *const_cast<volatile int*>(&sh.dead) = 1;
+                good = false;
+                break;
+            }
+            put_by(n == kPrHold ? PrHold::kFirst : PrHold::kNext);
+            l = 0.f;
+        }
         float x[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ask32(s_at + 32 * c, x[c]);
@@ -675,7 +689,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
             const int s = n % L::kStages;
             good = warp_wait_or_give_up(&sh.v_ok[s], (n / L::kStages) & 1, &sh.dead);
             if (!good) break;
-            if (sh.is_wild(s)) pr_by_hand<D>(o_at, s_at, base + L::kV + s * L::kTileBytes, (n & sh.again) == 0);
+            if (sh.is_wild(s)) pr_by_hand<D>(o_at, s_at, base + L::kV + s * L::kTileBytes, n % kPrHold == 0);
         }
         tc_fence_before();
         __syncwarp();
@@ -685,11 +699,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
         good = warp_wait_or_give_up(&sh.o_full[half], 0, &sh.dead);
         tc_fence_after();
     }
-    const bool held = good && tiles > kPrHold && sh.again < tiles;
-    if (held) {
-        put_by(false);
-        l = sums_stat()->y;
-    }
+    if (good && tiles > kPrHold) l = put_by(PrHold::kLast);
     const bool live = r < p.tq * p.G && token < u.ntok;
     const int g = r % p.G;
     const int64_t head = static_cast<int64_t>(u.h) * p.G + g, tok = u.tok + token;
@@ -702,9 +712,9 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
     uint8_t* stage = base + L::kQ + half * L::kTileBytes + (r & ~31) * D * 2;
     auto put = [&](int row, int w) { return stage + row * D * 2 + (w ^ (row & 7)) * 16; };
     if constexpr (kParts) {
-        const int64_t rec = record() - lane;
+        const int64_t rec = static_cast<int64_t>(blockIdx.y * p.c.H + blockIdx.x) * L::kHalves * kPrHalf + (threadIdx.x & ~31);
         if (live) p.part_stat[rec + lane] = good ? make_float2(base2, l) : make_float2(0.f, CUDART_NAN_F);
-        if (!good || tiles <= 0 || !lives || held) return;
+        if (!good || tiles <= 0 || !lives) return;
 #pragma unroll 1
         for (int half_row = 0; half_row < D; half_row += D / 2) {
 #pragma unroll
@@ -732,19 +742,7 @@ __device__ void pr_softmax(const PromptParams& p, PrShared& sh, uint8_t* base) {
 #pragma unroll 1
         for (int d0 = 0; d0 < D; d0 += 32) {
             uint32_t o[32];
-            if (held) {
-                const uint4* src = reinterpret_cast<const uint4*>(sums() + d0);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint4 w = src[i];
-                    o[4 * i] = w.x;
-                    o[4 * i + 1] = w.y;
-                    o[4 * i + 2] = w.z;
-                    o[4 * i + 3] = w.w;
-                }
-            } else {
-                tmem_get32(o_at + d0, o);
-            }
+            tmem_get32(o_at + d0, o);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 float x[8];
@@ -816,7 +814,6 @@ __global__ void __launch_bounds__(PrForm<D, kHalves>::kThreads, PrForm<D, kHalve
         }
         if (lane == 0) {
             if (u.lo < u.hi) pr_load_queries<D, L>(p, &mq, sh, u, base);
-            sh.again = kPrHold - 1;
             sh.place[0] = sh.place[1] = -1;
             if (!kParts && u.hi - u.lo > kPrHold) pr_take_places(sh, u.ntok > p.tq ? 2 : 1);
             sh.unit = u;
