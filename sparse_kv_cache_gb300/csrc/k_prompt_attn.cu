@@ -27,11 +27,12 @@
 // probabilities, in fp32, take the same factor, and it cancels.
 //
 // Measured (8 KV heads of 4 query heads, d = 128; cuBLAS reaches 1900 TFLOP/s in bursts, 1695 for seconds under the power
-// limit): a prompt of 32K tokens 6.3 ms, 1395 TFLOP/s; through a window of 4096 1.69 ms, 1220; 4 prompts of 4096 464
-// us, 1185; chunks of 13K tokens in all through a window of 1024 302 us, of 10.5 tiles a unit with three at an edge;
-// d = 64, 16K tokens 1.37 ms, 805, where the softmax takes as long as both products; 8 drafts of 5 tokens over up to
-// 4099 rows 23.5 us.  A half's tile takes its softmax about 1650 clocks (128 columns in 4 of them each at the
-// exponential unit, 32 a clock to an SM) and its products 1024, which the other half's overlap.
+// limit): a prompt of 32K tokens 6.3 to 6.4 ms by box, 1365 to 1397 TFLOP/s; through a window of 4096 1.70 ms, 1215; 4 prompts
+// of 4096 463 us, 1187; chunks of 13K tokens in all through a window of 1024 302 us, of 10.5 tiles a unit with three at an
+// edge; d = 64, 16K tokens 1.37 ms, 804; 8 drafts of 5 tokens over up to 4099 rows 23.5 us.  A half's tile takes its softmax
+// about 1690 clocks with 128 dimensions and 1700 with 64 (128 columns in 4 of them each at the exponential unit, 32 a clock to an
+// SM) and its products 1024 and 512, which the other half's overlap.  No unit is full (tensor cores 54 % and issue slots 35 %
+// of the cycles of 8192 tokens): the chain softmax, P.V, Q.K of each half bounds it.
 // Tried: two threads to a row (7.1 ms for 32K: 20 warps to issue for), the first half of P handed over early (no
 // difference), six warps to look at values (505 us for the 4 prompts, 483 then: they wait at the others' cost), CTAs that go
 // through many units (517 us, 483 then: what a unit's start and end take is hidden, but the units fall unevenly).

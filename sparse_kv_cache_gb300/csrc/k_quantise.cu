@@ -80,7 +80,7 @@ __device__ __forceinline__ float block_scale(float m) {
 // one warp or several (block / 16).  Which blocks those are only the device knows: sequence b has
 // (start[b] >> lgb) + 2b slots before its own, which leaves every sequence room for the blocks that its
 // tokens can touch, and a slot without a block ends at once.  (32K tokens, blocks of 64: two slots of 514.)
-// A prompt of 32K tokens in bf16 36 us, 5.6 TB/s (three CTAs to an SM 40), in fp32 4.4 TB/s.
+// A prompt of 32K tokens in bf16 36.4 us, 5.5 TB/s (three CTAs to an SM 40), in fp32 4.4 TB/s.
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kQzWarps, sizeof(T) == 4 ? 3 : 4) k_quantise(const __grid_constant__ QuantParams p) {
     constexpr int kLanes = D / 8, kPer = 32 / kLanes, kSteps = kQzRows / kPer;

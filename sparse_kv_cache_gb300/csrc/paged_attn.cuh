@@ -516,8 +516,8 @@ struct KeepShared {
 // block's scale and that power afterwards, in fp32.  A value's scale goes into its probability, whose base is
 // therefore one of its own: the largest product of a probability and a scale.
 //
-// Measured back to back (8 KV heads of 4 query heads, d = 128): 8 x 128K rows of codes 368 us, 5.8 TB/s; 4 x 32K rows 63
-// us; 768 units of which 1000 rows are seen 54 us; one sequence of 1013 rows 8.6 us.  With copies of 16 bytes a lane
+// Measured back to back (8 KV heads of 4 query heads, d = 128): 8 x 128K rows of codes 370 us, 5.8 TB/s; 4 x 32K rows 63
+// us; 768 units of which 1000 rows are seen 55.5 us; one sequence of 1013 rows 8.7 us.  With copies of 16 bytes a lane
 // (cp.async) instead of TMA the 128K rows took 460 us, 459 without any arithmetic; straight into registers, one tile
 // ahead, 511, bound by instructions (570 a tile of 16 rows, 390 now).
 enum class Holds { kBf16, kE5M2, kE4M3 };
