@@ -27,7 +27,7 @@
 // probabilities, in fp32, take the same factor, and it cancels.
 //
 // Measured (8 KV heads of 4 query heads, d = 128; cuBLAS reaches 1900 TFLOP/s in bursts, 1695 for seconds under the power
-// limit): a prompt of 32K tokens 6.3 to 6.4 ms by box, 1365 to 1397 TFLOP/s; through a window of 4096 1.70 ms, 1215; 4 prompts
+// limit): a prompt of 32K tokens 6.3 to 6.4 ms by machine, 1365 to 1397 TFLOP/s; through a window of 4096 1.70 ms, 1215; 4 prompts
 // of 4096 463 us, 1187; chunks of 13K tokens in all through a window of 1024 302 us, of 10.5 tiles a unit with three at an
 // edge; d = 64, 16K tokens 1.37 ms, 804; 8 drafts of 5 tokens over up to 4099 rows 23.5 us.  A half's tile takes its softmax
 // about 1690 clocks with 128 dimensions and 1700 with 64 (128 columns in 4 of them each at the exponential unit, 32 a clock to an

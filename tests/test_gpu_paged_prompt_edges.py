@@ -82,14 +82,15 @@ def test_starts_that_fall_behind_a_longer_sequence_are_reported(lens, tokens):
                 assert (out[t] == 7).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("tokens", [3, 2500])
-def test_sums_over_very_long_contexts(tokens):
+def test_sums_over_very_long_contexts(tokens, d):
     """16M rows, whole units of 2500 tokens and parts of units of 3.  What the tensor cores cut off of a sum, 2^-22 at every 16 rows, is that of
     131072 rows at most, 2^-9, however many there are; besides, as in test_gpu_paged_prompt.py, 2^-16 of the sums of
     probabilities (which are all alike, and exact) and 2^-8 of the result's rounding."""
-    n, ps, d = 1 << 24, 1024, 64
+    n, ps = 1 << 24, 1024
     k = torch.zeros((n // ps, 1, ps, d), dtype=torch.bfloat16, device="cuda")
-    c = (1 + torch.arange(d, device="cuda") / 64).to(torch.bfloat16)      # exact
+    c = (1 + torch.arange(d, device="cuda") / 128).to(torch.bfloat16)      # exact
     v = c.expand(n // ps, 1, ps, d).contiguous()
     q = torch.ones((tokens, 8, d), dtype=torch.bfloat16, device="cuda")
     table = torch.randperm(n // ps, generator=torch.Generator().manual_seed(1)).to(torch.int32)[None].cuda()
